@@ -83,9 +83,14 @@ typedef enum {
     LC_ERR_UNDECIDED = 17,      /* the destination could not be shown one-to-one:
                                    no stride split settles it and the modes left
                                    hold over 2^24 words to enumerate */
-    LC_ERR_NOT_MAPPED = 18      /* lc_layout_copy_mapped: a byte range is not
+    LC_ERR_NOT_MAPPED = 18,     /* lc_layout_copy_mapped: a byte range is not
                                    memory the device can address (pageable host
                                    memory, or a range leaving its mapping) */
+    LC_ERR_TYPE = 19,           /* an element type the operator does not take */
+    LC_ERR_CACHE_INDEX = 20,    /* device error word: a length outside the
+                                   sequence's capacity, or a page id outside
+                                   the pool */
+    LC_ERR_WORKSPACE = 21       /* a workspace is too small */
 } lc_status;
 
 /* Kernel classes (the planner picks one; lc_layout_copy_ex can force one). */

@@ -15,12 +15,14 @@ from typing import Sequence
 
 from . import _lib
 from ._lib import KERNELS, STATUS, STATUS_NAMES
+from .cache import PagedCache, cache_append, cache_attend, cache_attend_workspace, cache_evict
 
 __all__ = ["TileLayout", "LayoutCopyError", "layout_copy", "layout_copy_ptr", "layout_copy_host",
            "host_staging_bytes", "layout_copy_host_static", "window_sum", "plan",
            "choose_swizzle", "swizzle_conflicts", "gmem_smem_partition",
            "last_device_error", "debug_wait_timeout", "warp_unit_plan", "warp_unit_run",
            "loop_layout_default", "loop_layout_info", "loop_plan", "layout_copy_loop", "layout_copy_loop_ptr",
+           "PagedCache", "cache_append", "cache_attend", "cache_attend_workspace", "cache_evict",
            "KERNELS", "STATUS"]
 
 

@@ -26,6 +26,7 @@ STATUS_NAMES = {
     10: "LC_ERR_NO_SWIZZLE", 11: "LC_ERR_CUDA", 12: "LC_ERR_TIMEOUT",
     13: "LC_ERR_UNSUPPORTED", 14: "LC_ERR_OVERFLOW", 15: "LC_ERR_STAGING",
     16: "LC_ERR_LOOP_LAYOUT", 17: "LC_ERR_UNDECIDED", 18: "LC_ERR_NOT_MAPPED",
+    19: "LC_ERR_TYPE", 20: "LC_ERR_CACHE_INDEX", 21: "LC_ERR_WORKSPACE",
 }
 STATUS = {v: k for k, v in STATUS_NAMES.items()}
 KERNELS = {"auto": 0, "vec_copy": 1, "warp_permute": 2, "tile_transpose": 3, "smem_transpose": 4,
@@ -97,12 +98,41 @@ class CGmemSmem(ctypes.Structure):
                 ("div_m", ctypes.c_uint32 * MAX_RANK), ("div_s", ctypes.c_int32 * MAX_RANK)]
 
 
+class CPagedCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("n_pages", ctypes.c_int64),
+                ("type", ctypes.c_int32), ("n_seqs", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("pages_per_seq", ctypes.c_int32),
+                ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3),
+                ("k_scale_stride", ctypes.c_int64 * 3), ("v_scale_stride", ctypes.c_int64 * 3)]
+
+
+class CCacheQuery(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("type", ctypes.c_int32), ("n_q_heads", ctypes.c_int32),
+                ("q_stride", ctypes.c_int64 * 2), ("out_stride", ctypes.c_int64 * 2),
+                ("lengths", ctypes.c_void_p), ("mask", ctypes.c_void_p), ("mask_stride", ctypes.c_int64),
+                ("window", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("lse", ctypes.c_void_p), ("lse_stride", ctypes.c_int64),
+                ("scores", ctypes.c_void_p), ("scores_stride", ctypes.c_int64 * 2),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
+
+
+class CCacheEviction(ctypes.Structure):
+    _fields_ = [("lengths", ctypes.c_void_p), ("scores", ctypes.c_void_p), ("scores_stride", ctypes.c_int64 * 2),
+                ("budget", ctypes.c_int32), ("recent", ctypes.c_int32),
+                ("kept", ctypes.c_void_p), ("kept_stride", ctypes.c_int64 * 2),
+                ("new_scores", ctypes.c_void_p), ("new_scores_stride", ctypes.c_int64 * 2),
+                ("new_lengths", ctypes.c_void_p)]
+
+
 _P_LAYOUT = ctypes.POINTER(CTileLayout)
 _P_LOOP = ctypes.POINTER(CLoopLayout)
 _P_I32 = ctypes.POINTER(ctypes.c_int32)
 _P_I64 = ctypes.POINTER(ctypes.c_int64)
 
-# name -> (restype, argtypes); every symbol declared in include/layout_copy.h
+# name -> (restype, argtypes); every symbol declared in include/*.h
 PROTOTYPES = {
     "lc_layout_copy": (ctypes.c_int, [ctypes.c_void_p, _P_LAYOUT, ctypes.c_void_p, _P_LAYOUT,
                                       ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p]),
@@ -145,6 +175,13 @@ PROTOTYPES = {
                                              ctypes.c_int32, ctypes.c_int64, ctypes.c_int32,
                                              ctypes.POINTER(CSmemSwizzle), ctypes.c_void_p, ctypes.c_void_p,
                                              ctypes.c_void_p]),
+    "lc_cache_append": (ctypes.c_int, [ctypes.POINTER(CPagedCache), ctypes.c_void_p, ctypes.c_void_p,
+                                       ctypes.c_int32, _P_I64, _P_I64, ctypes.c_int32, ctypes.c_void_p,
+                                       ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "lc_cache_attend": (ctypes.c_int, [ctypes.POINTER(CPagedCache), ctypes.POINTER(CCacheQuery), ctypes.c_void_p]),
+    "lc_cache_attend_workspace": (ctypes.c_int64, [ctypes.POINTER(CPagedCache), ctypes.c_int32, ctypes.c_int32]),
+    "lc_cache_evict": (ctypes.c_int, [ctypes.POINTER(CPagedCache), ctypes.POINTER(CCacheEviction),
+                                      ctypes.c_void_p]),
     "lc_row_major_strides": (ctypes.c_int, [ctypes.c_int32, _P_I64, _P_I64]),
     "lc_layout_footprint": (ctypes.c_int64, [_P_LAYOUT, ctypes.c_int64]),
     "lc_status_string": (ctypes.c_char_p, [ctypes.c_int32]),

@@ -1,0 +1,267 @@
+"""Paged key-value cache: append, attention of one new token, eviction.
+
+A cache is a pool of pages seen as [page, kv_head, slot, dim] through its
+strides (a [page, slot, kv_head, dim] pool is passed as its ``transpose(1,
+2)``) and a page table naming each sequence's pages.  Everything runs in the
+C-ABI library (``include/layout_copy_cache.h``); this module marshals
+arguments and allocates outputs and workspaces through torch.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+from . import _lib
+
+__all__ = ["PagedCache", "cache_append", "cache_attend", "cache_attend_workspace", "cache_evict"]
+
+_TYPES = None  # torch dtype -> lc_cache_type
+
+
+def _types():
+    global _TYPES
+    if _TYPES is None:
+        import torch
+        _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
+    return _TYPES
+
+
+def _check(status: int, what: str) -> None:
+    if status != 0:
+        from . import LayoutCopyError
+        raise LayoutCopyError(status, what)
+
+
+class _on:
+    """Runs allocations on the stream the kernels will use, so that torch's
+    allocator hands the memory out in that stream's order."""
+
+    def __init__(self, stream):
+        import torch
+        if stream is None:
+            self.ctx, self.handle = None, torch.cuda.current_stream().cuda_stream
+        else:
+            s = stream
+            if isinstance(stream, int):
+                s = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+            self.ctx, self.handle = torch.cuda.stream(s), s.cuda_stream
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _tensor(t, name: str, dtype, shape, device):
+    """A tensor of that type and shape on the cache's device whose last mode's elements are adjacent."""
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if tuple(t.shape) != shape:
+        raise ValueError("%s must have shape %r, got %r" % (name, shape, tuple(t.shape)))
+    if t.device != device:
+        raise ValueError("%s is on %s, the cache on %s" % (name, t.device, device))
+    if shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError("%s: the elements of the last mode must be adjacent" % name)
+    return t
+
+
+class PagedCache:
+    """Pools of pages and a page table.
+
+    ``k``, ``v``: CUDA tensors [pages, kv_heads, page_size, head_dim] of
+    bfloat16, float16 or float8_e4m3fn, any strides with adjacent elements in
+    the last mode.  ``page_table``: int32 [seqs, pages_per_seq]; entries past a
+    sequence's pages are never read.  ``k_scale``, ``v_scale``: float32 [pages,
+    kv_heads, page_size] for float8_e4m3fn pools (value = code * scale).  The
+    tensors are kept by reference: what they hold may change between calls,
+    their memory may not.
+    """
+
+    def __init__(self, k, v, page_table, k_scale=None, v_scale=None):
+        import torch
+        if not k.is_cuda:
+            raise ValueError("a cache needs CUDA tensors (there is no CPU path)")
+        if k.dim() != 4 or page_table.dim() != 2:
+            raise ValueError("pools are [pages, kv_heads, page_size, head_dim], the table [seqs, pages_per_seq]")
+        if k.dtype not in _types():
+            raise ValueError("pools are bfloat16, float16 or float8_e4m3fn, got %s" % k.dtype)
+        _tensor(k, "k", k.dtype, tuple(k.shape), k.device)
+        _tensor(v, "v", k.dtype, tuple(k.shape), k.device)
+        _tensor(page_table, "page_table", torch.int32, tuple(page_table.shape), k.device)
+        q8 = k.dtype == torch.float8_e4m3fn
+        if q8 != (k_scale is not None) or q8 != (v_scale is not None):
+            raise ValueError("k_scale and v_scale belong to float8_e4m3fn pools, and only to them")
+        c = _lib.CPagedCache()
+        if q8:
+            for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
+                if s.dtype != torch.float32 or tuple(s.shape) != tuple(k.shape[:3]) or s.device != k.device:
+                    raise ValueError("%s must be float32 of shape %r on the pools' device" % (name, tuple(k.shape[:3])))
+            c.k_scale, c.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
+            c.k_scale_stride[:] = k_scale.stride()
+            c.v_scale_stride[:] = v_scale.stride()
+        c.k, c.v, c.page_table = k.data_ptr(), v.data_ptr(), page_table.data_ptr()
+        c.table_stride = page_table.stride(0)
+        c.n_pages, c.n_kv_heads, c.page_size, c.head_dim = k.shape
+        c.n_seqs, c.pages_per_seq = page_table.shape
+        c.type = _types()[k.dtype]
+        c.k_stride[:] = k.stride()[:3]
+        c.v_stride[:] = v.stride()[:3]
+        self._c, self._ref = c, ctypes.byref(c)
+        self._workspace_bytes = {}
+        self.k, self.v, self.page_table, self.k_scale, self.v_scale = k, v, page_table, k_scale, v_scale
+        self.device, self.dtype = k.device, k.dtype
+        self.n_seqs, self.pages_per_seq = page_table.shape
+        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
+        self.capacity = self.page_size * self.pages_per_seq
+        self.io_dtype = torch.bfloat16 if q8 else k.dtype
+
+    def workspace_bytes(self, n_q_heads: int, with_scores: bool) -> int:
+        key = (n_q_heads, with_scores)
+        n = self._workspace_bytes.get(key)
+        if n is None:
+            n = int(_lib.lib().lc_cache_attend_workspace(self._ref, n_q_heads, int(with_scores)))
+            if n < 0:
+                raise ValueError("a cache of %d key heads cannot take %d query heads (or is itself refused)"
+                                 % (self.n_kv_heads, n_q_heads))
+            self._workspace_bytes[key] = n
+        return n
+
+
+def cache_append(cache: PagedCache, k, v, lengths, counts=None, new_lengths=None, stream=None):
+    """Writes new tokens after each sequence's ``lengths``; returns the new lengths.
+
+    ``k``, ``v``: [seqs, tokens, kv_heads, head_dim] of the cache's type, or of
+    bfloat16 / float16 for a float8_e4m3fn cache (each row is quantised with a
+    scale of its own).  ``lengths``: int32 [seqs].  ``counts``: int32 [seqs],
+    how many of the tokens are a sequence's (default: all).  ``new_lengths``:
+    an int32 [seqs] tensor to receive lengths + counts, other than
+    ``lengths``.  Tokens past a sequence's capacity are dropped and set the device
+    error word (``last_device_error``).
+    """
+    import torch
+    if k.dim() != 4 or k.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("new keys and values are [seqs, tokens, kv_heads, head_dim] of bfloat16 or float16")
+    n_new = k.shape[1]
+    shape = (cache.n_seqs, n_new, cache.n_kv_heads, cache.head_dim)
+    _tensor(k, "k", k.dtype, shape, cache.device)
+    _tensor(v, "v", k.dtype, shape, cache.device)
+    _tensor(lengths, "lengths", torch.int32, (cache.n_seqs,), cache.device)
+    if counts is not None:
+        _tensor(counts, "counts", torch.int32, (cache.n_seqs,), cache.device)
+    with _on(stream) as handle:
+        if new_lengths is None:
+            new_lengths = torch.empty_like(lengths)
+        else:
+            _tensor(new_lengths, "new_lengths", torch.int32, (cache.n_seqs,), cache.device)
+        i64 = ctypes.c_int64 * 3
+        _check(_lib.lib().lc_cache_append(cache._ref, k.data_ptr(), v.data_ptr(), _types()[k.dtype],
+                                          i64(*k.stride()[:3]), i64(*v.stride()[:3]), n_new,
+                                          None if counts is None else counts.data_ptr(), lengths.data_ptr(),
+                                          new_lengths.data_ptr(), handle), "cache_append")
+    return new_lengths
+
+
+def cache_attend_workspace(cache: PagedCache, n_q_heads: int, with_scores: bool = False, stream=None):
+    """A workspace for ``cache_attend`` calls that do not overlap."""
+    import torch
+    with _on(stream):
+        return torch.empty(cache.workspace_bytes(n_q_heads, with_scores), dtype=torch.uint8, device=cache.device)
+
+
+def cache_attend(cache: PagedCache, q, lengths, out=None, scale=None, window: int = 0, mask=None, lse=None,
+                 scores=None, workspace=None, stream=None):
+    """Attention of one new token a sequence over its cached slots; returns ``out``.
+
+    ``q``: [seqs, q_heads, head_dim] of the cache's type (bfloat16 for a
+    float8_e4m3fn cache); query head i reads key head i // (q_heads //
+    kv_heads).  ``scale``: of the dot products, 1 / sqrt(head_dim) by default.
+    ``window``: only the newest so many slots are seen (0: all).  ``mask``:
+    bool or uint8 [seqs, capacity], slots of a zero are not seen.  ``lse``:
+    float32 [seqs, q_heads] to receive log sum exp.  ``scores``: float32
+    [seqs, kv_heads, capacity]; each slot's weight, summed over its query heads, is
+    added to it.  A row with no slot seen gives zeros (lse: -inf).
+    """
+    import torch
+    if q.dim() != 3:
+        raise ValueError("q is [seqs, q_heads, head_dim]")
+    n_q = q.shape[1]
+    _tensor(q, "q", cache.io_dtype, (cache.n_seqs, n_q, cache.head_dim), cache.device)
+    _tensor(lengths, "lengths", torch.int32, (cache.n_seqs,), cache.device)
+    a = _lib.CCacheQuery()
+    if mask is not None:
+        if mask.dtype not in (torch.bool, torch.uint8):
+            raise ValueError("mask must be bool or uint8, got %s" % mask.dtype)
+        _tensor(mask, "mask", mask.dtype, (cache.n_seqs, cache.capacity), cache.device)
+        a.mask, a.mask_stride = mask.data_ptr(), mask.stride(0)
+    if lse is not None:
+        _tensor(lse, "lse", torch.float32, (cache.n_seqs, n_q), cache.device)
+        a.lse, a.lse_stride = lse.data_ptr(), lse.stride(0)
+    if scores is not None:
+        _tensor(scores, "scores", torch.float32, (cache.n_seqs, cache.n_kv_heads, cache.capacity), cache.device)
+        a.scores = scores.data_ptr()
+        a.scores_stride[:] = scores.stride()[:2]
+    need = cache.workspace_bytes(n_q, scores is not None)
+    with _on(stream) as handle:
+        if out is None:
+            out = torch.empty((cache.n_seqs, n_q, cache.head_dim), dtype=q.dtype, device=q.device)
+        else:
+            _tensor(out, "out", q.dtype, tuple(q.shape), cache.device)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        elif workspace.device != cache.device or not workspace.is_contiguous():
+            raise ValueError("the workspace must be contiguous and on the cache's device")
+        a.q, a.out, a.lengths = q.data_ptr(), out.data_ptr(), lengths.data_ptr()
+        a.type, a.n_q_heads = _types()[q.dtype], n_q
+        a.q_stride[:] = q.stride()[:2]
+        a.out_stride[:] = out.stride()[:2]
+        a.window = window
+        a.scale = 1.0 / math.sqrt(cache.head_dim) if scale is None else scale
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        _check(_lib.lib().lc_cache_attend(cache._ref, ctypes.byref(a), handle), "cache_attend")
+    return out
+
+
+def cache_evict(cache: PagedCache, lengths, scores, budget: int, recent: int = 0, new_scores=None, kept=None,
+                new_lengths=None, stream=None):
+    """Cuts sequences of more than ``budget`` slots down to it; returns (kept, new_scores, new_lengths).
+
+    Per key head the ``recent`` newest slots stay, and of the others those of
+    the largest ``scores`` (float32 [seqs, kv_heads, capacity]; equal ones:
+    the lowest slots).  Their rows move to the front of the sequence's pages
+    in their order.  ``kept``: int32 [seqs, kv_heads, budget], the old slot of
+    each kept one, then -1.  ``new_scores``: the kept slots' scores, then
+    zeros, in a tensor other than ``scores``; ``new_lengths``: min(lengths,
+    budget), in a tensor other than ``lengths``.  The pages a sequence's table
+    names must be its own.
+    """
+    import torch
+    unit = (cache.n_seqs, cache.n_kv_heads)
+    _tensor(lengths, "lengths", torch.int32, (cache.n_seqs,), cache.device)
+    _tensor(scores, "scores", torch.float32, unit + (cache.capacity,), cache.device)
+    budget = int(budget)
+    a = _lib.CCacheEviction()
+    with _on(stream) as handle:
+        if kept is None:
+            kept = torch.empty(unit + (max(budget, 0),), dtype=torch.int32, device=cache.device)
+        else:
+            _tensor(kept, "kept", torch.int32, unit + (budget,), cache.device)
+        if new_scores is None:
+            new_scores = torch.empty(scores.shape, dtype=torch.float32, device=cache.device)
+        else:
+            _tensor(new_scores, "new_scores", torch.float32, tuple(scores.shape), cache.device)
+        if new_lengths is None:
+            new_lengths = torch.empty_like(lengths)
+        else:
+            _tensor(new_lengths, "new_lengths", torch.int32, (cache.n_seqs,), cache.device)
+        a.lengths, a.scores, a.kept = lengths.data_ptr(), scores.data_ptr(), kept.data_ptr()
+        a.new_scores, a.new_lengths = new_scores.data_ptr(), new_lengths.data_ptr()
+        a.scores_stride[:] = scores.stride()[:2]
+        a.kept_stride[:] = kept.stride()[:2]
+        a.new_scores_stride[:] = new_scores.stride()[:2]
+        a.budget, a.recent = budget, int(recent)
+        _check(_lib.lib().lc_cache_evict(cache._ref, ctypes.byref(a), handle), "cache_evict")
+    return kept, new_scores, new_lengths

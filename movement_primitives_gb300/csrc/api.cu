@@ -177,11 +177,13 @@ extern "C" int lc_layout_copy(const void *src, const lc_tile_layout *src_layout,
 
 extern "C" int lc_last_device_error(lc_stream_t stream, uint64_t *detail) {
     if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return LC_ERR_CUDA;
-    unsigned long long words[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    cudaError_t (*const take[8])(unsigned long long *) = {
-        lc::take_module_error, lc::take_error_tile, lc::take_error_tma_copy, lc::take_error_warp1,
-        lc::take_error_warp2,  lc::take_error_warp4, lc::take_error_warp8, lc::take_error_warp16};
-    for (int i = 0; i < 8; ++i)
+    constexpr int kWords = 11;
+    unsigned long long words[kWords] = {};
+    cudaError_t (*const take[kWords])(unsigned long long *) = {
+        lc::take_module_error, lc::take_error_tile,  lc::take_error_tma_copy,     lc::take_error_warp1,
+        lc::take_error_warp2,  lc::take_error_warp4, lc::take_error_warp8,        lc::take_error_warp16,
+        lc::take_error_append, lc::take_error_evict, lc::take_error_attend};
+    for (int i = 0; i < kWords; ++i)
         if (take[i](&words[i]) != cudaSuccess) return LC_ERR_CUDA;
     unsigned long long v = 0;
     for (unsigned long long w : words)
@@ -222,6 +224,9 @@ extern "C" const char *lc_status_string(int32_t status) {
             return "the destination could not be shown one-to-one (no stride split settles it, too many words to "
                    "enumerate)";
         case LC_ERR_NOT_MAPPED: return "a byte range is not memory the device can address";
+        case LC_ERR_TYPE: return "an element type the operator does not take";
+        case LC_ERR_CACHE_INDEX: return "a length outside the sequence's capacity or a page id outside the pool";
+        case LC_ERR_WORKSPACE: return "the workspace is too small";
     }
     return "unknown status";
 }

@@ -1,0 +1,190 @@
+// New tokens' rows into the pages of a key-value cache (lc_cache_append).
+//
+// Row (b, t, h) of the new keys and values goes to slot lengths[b] + t of
+// sequence b, as it is or quantised to E4M3:
+//     scale = max(max_e |x_e| / 448, 2^-126),  code_e = e4m3(x_e / scale)
+// in float32 (IEEE division, round to nearest even), NaN as the scale where
+// the largest magnitude is not finite.
+//
+// One warp moves one row of both pools: lanes 0-15 the keys', 16-31 the
+// values', each lane 16 bytes of new elements at a time.  Bound by memory:
+// every byte is read and written once.
+#include <cuda_fp8.h>
+
+#include "cache_common.cuh"
+
+namespace lc {
+
+constexpr int kApThreads = 256;
+
+struct AppendArgs {
+    CacheArgs c;
+    const uint16_t *k, *v;
+    int64_t kst[3], vst[3];  // elements: sequence, token, head
+    const int32_t *counts, *lengths;
+    int32_t *new_lengths;
+    int32_t n_new;
+    uint32_t rows;           // n_seqs * n_new * heads
+    FastDiv new_div, head_div;
+};
+
+// Q: 0 rows as they are, 1 bf16 -> E4M3, 2 fp16 -> E4M3.  VEC: every row on
+// both sides starts on the boundary of eight elements and holds whole eights.
+template <int Q, bool VEC>
+__global__ void __launch_bounds__(kApThreads) k_cache_append(const __grid_constant__ AppendArgs a) {
+    const CacheArgs &c = a.c;
+    const int64_t thread = int64_t(blockIdx.x) * kApThreads + threadIdx.x;
+    if (thread < c.n_seqs) {
+        const int at = static_cast<int>(thread);
+        const int n = cache_length(c, a.lengths, at, kClassAppend);
+        const int m = a.counts ? min(max(a.counts[at], 0), a.n_new) : a.n_new;
+        if ((a.counts && a.counts[at] != m) || m > c.cap - n) report_error(LC_ERR_CACHE_INDEX, kClassAppend);
+        a.new_lengths[at] = n + min(m, c.cap - n);
+    }
+    const uint32_t row_id = static_cast<uint32_t>(thread / 32);
+    if (row_id >= a.rows) return;
+    const uint32_t bt = fast_div(row_id, a.head_div);
+    const int h = static_cast<int>(row_id - bt * c.heads);
+    const int b = static_cast<int>(fast_div(bt, a.new_div));
+    const int t = static_cast<int>(bt - static_cast<uint32_t>(b) * a.n_new);
+    if (a.counts && t >= a.counts[b]) return;
+    const int n = min(max(a.lengths[b], 0), c.cap);
+    if (t >= c.cap - n) return;
+    int row;
+    const int page = cache_page(c, b, n + t, &row, kClassAppend);
+    if (page < 0) return;
+
+    const int lane = threadIdx.x & 15;
+    const bool is_v = threadIdx.x & 16;
+    const uint16_t *src = is_v ? a.v + b * a.vst[0] + t * a.vst[1] + h * a.vst[2]
+                               : a.k + b * a.kst[0] + t * a.kst[1] + h * a.kst[2];
+    const int64_t to = row_offset(is_v ? c.vst : c.kst, page, h, row);
+    uint8_t *dst = (is_v ? c.v : c.k) + (Q ? to : 2 * to);
+    if constexpr (Q == 0) {
+        if constexpr (VEC) {
+            for (int e = 8 * lane; e < c.dim; e += 128)
+                *reinterpret_cast<uint4 *>(dst + 2 * e) = *reinterpret_cast<const uint4 *>(src + e);
+        } else {
+            for (int e = lane; e < c.dim; e += 16) reinterpret_cast<uint16_t *>(dst)[e] = src[e];
+        }
+    } else {
+        // this lane's elements: eights 8 (lane + 16 i) (VEC), or lane + 16 j
+        float x[16];
+        float top = 0.f;
+        bool fine = true;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint16_t w[8];
+            if constexpr (VEC) {
+                uint4 q = make_uint4(0, 0, 0, 0);
+                if (8 * (lane + 16 * i) < c.dim) q = *reinterpret_cast<const uint4 *>(src + 8 * (lane + 16 * i));
+                *reinterpret_cast<uint4 *>(w) = q;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int e = lane + 16 * (8 * i + j);
+                    w[j] = e < c.dim ? src[e] : uint16_t(0);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float f = Q == 1 ? __uint_as_float(static_cast<uint32_t>(w[j]) << 16)
+                                       : __half2float(__ushort_as_half(w[j]));
+                x[8 * i + j] = f;
+                top = fmaxf(top, fabsf(f));
+                fine = fine && isfinite(f);
+            }
+        }
+#pragma unroll
+        for (int o = 8; o; o >>= 1) {
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            fine = __shfl_xor_sync(0xffffffffu, static_cast<int>(fine), o) && fine;
+        }
+        const float scale = fine ? fmaxf(__fdiv_rn(top, 448.f), 1.17549435e-38f) : __int_as_float(0x7fc00000);
+        if (lane == 0) (is_v ? c.vs : c.ks)[row_offset(is_v ? c.vss : c.kss, page, h, row)] = scale;
+        uint32_t code[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            code[j] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x[2 * j], scale), __fdiv_rn(x[2 * j + 1], scale)),
+                                               __NV_SATFINITE, __NV_E4M3);
+        if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (8 * (lane + 16 * i) < c.dim)
+                    *reinterpret_cast<uint2 *>(dst + 8 * (lane + 16 * i)) =
+                        make_uint2(code[4 * i] | code[4 * i + 1] << 16, code[4 * i + 2] | code[4 * i + 3] << 16);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (lane + 16 * j < c.dim) dst[lane + 16 * j] = static_cast<uint8_t>(code[j / 2] >> (8 * (j & 1)));
+        }
+    }
+}
+
+cudaError_t take_error_append(unsigned long long *v) { return take_module_error(v); }
+
+namespace {
+
+template <int Q>
+int launch_append(const AppendArgs &a, bool vec, cudaStream_t cs) {
+    const uint64_t threads = std::max<uint64_t>(uint64_t(a.rows) * 32, a.c.n_seqs);
+    const unsigned grid = static_cast<unsigned>((threads + kApThreads - 1) / kApThreads);
+    if (vec)
+        k_cache_append<Q, true><<<grid, kApThreads, 0, cs>>>(a);
+    else
+        k_cache_append<Q, false><<<grid, kApThreads, 0, cs>>>(a);
+    return finish_launch();
+}
+
+}  // namespace
+
+}  // namespace lc
+
+extern "C" int lc_cache_append(const lc_paged_cache *cache, const void *k_new, const void *v_new, int32_t type,
+                               const int64_t k_stride[3], const int64_t v_stride[3], int32_t n_new,
+                               const int32_t *counts, const int32_t *lengths, int32_t *new_lengths,
+                               lc_stream_t stream) {
+    using namespace lc;
+    AppendArgs a{};
+    int st = check_cache(cache, true, &a.c);
+    if (st) return st;
+    if (n_new < 0) return LC_ERR_SHAPE;
+    if (type != LC_CACHE_BF16 && type != LC_CACHE_F16) return LC_ERR_TYPE;
+    const bool q8 = cache->type == LC_CACHE_E4M3;
+    if (!q8 && type != cache->type) return LC_ERR_TYPE;
+    if (cache->n_seqs == 0) return LC_OK;
+    if (!lengths || !new_lengths || !k_stride || !v_stride || (n_new > 0 && (!k_new || !v_new))) return LC_ERR_NULL;
+    if (lengths == new_lengths && n_new > 0) return LC_ERR_OVERLAP;
+    if ((reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new)) % 2 ||
+        (reinterpret_cast<uintptr_t>(counts) | reinterpret_cast<uintptr_t>(lengths) |
+         reinterpret_cast<uintptr_t>(new_lengths)) % 4)
+        return LC_ERR_ALIGN;
+    const int64_t ext[3] = {cache->n_seqs, std::max(n_new, 1), cache->n_kv_heads};
+    st = check_reach(3, ext, k_stride, cache->head_dim);
+    if (!st) st = check_reach(3, ext, v_stride, cache->head_dim);
+    if (st) return st;
+    int64_t rows;
+    if (!mul_ok_ext(ext[0] * ext[2], n_new, &rows) || rows > (int64_t(1) << 31) - 1) return LC_ERR_OVERFLOW;
+    a.k = static_cast<const uint16_t *>(k_new);
+    a.v = static_cast<const uint16_t *>(v_new);
+    for (int i = 0; i < 3; ++i) {
+        a.kst[i] = k_stride[i];
+        a.vst[i] = v_stride[i];
+    }
+    a.counts = counts;
+    a.lengths = lengths;
+    a.new_lengths = new_lengths;
+    a.n_new = n_new;
+    a.rows = static_cast<uint32_t>(rows);
+    a.new_div = make_fastdiv(static_cast<uint32_t>(std::max(n_new, 1)));
+    a.head_div = make_fastdiv(static_cast<uint32_t>(cache->n_kv_heads));
+    const int64_t pool[3] = {cache->n_pages, cache->n_kv_heads, cache->page_size};
+    const int eb = cache_elem_bytes(cache->type);
+    const bool vec = cache->head_dim % 8 == 0 && rows_aligned(k_new, 3, ext, k_stride, 2, 16) &&
+                     rows_aligned(v_new, 3, ext, v_stride, 2, 16) &&
+                     rows_aligned(cache->k, 3, pool, cache->k_stride, eb, 8 * eb) &&
+                     rows_aligned(cache->v, 3, pool, cache->v_stride, eb, 8 * eb);
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    if (!q8) return launch_append<0>(a, vec, cs);
+    return type == LC_CACHE_BF16 ? launch_append<1>(a, vec, cs) : launch_append<2>(a, vec, cs);
+}

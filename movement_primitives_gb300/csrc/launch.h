@@ -46,5 +46,8 @@ cudaError_t take_error_warp2(unsigned long long *v);
 cudaError_t take_error_warp4(unsigned long long *v);
 cudaError_t take_error_warp8(unsigned long long *v);
 cudaError_t take_error_warp16(unsigned long long *v);
+cudaError_t take_error_append(unsigned long long *v);
+cudaError_t take_error_evict(unsigned long long *v);
+cudaError_t take_error_attend(unsigned long long *v);
 
 }  // namespace lc

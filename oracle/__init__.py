@@ -19,9 +19,11 @@ Contents
   banks        the shared-memory bank simulator and the XOR-bit choice
                (Apache TVM "permute_layout", "Algorithm" step 2)
   stencil      the window sum of MLC "Ep7", "Window Sum Example"
+  cache        the paged key-value cache operators (append with E4M3
+               rounding, attention of one token, eviction) in 64 bits
 
 Every function is pinned by at least one test; nothing here is "parity
 unpinned".
 """
-from . import banks, build, definition, index_maps, stencil  # noqa: F401
+from . import banks, build, cache, definition, index_maps, stencil  # noqa: F401
 from .definition import Layout, copy, offsets_of, paired_modes, cosize  # noqa: F401
