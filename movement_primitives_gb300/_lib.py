@@ -178,10 +178,9 @@ PROTOTYPES = {
     "lc_cache_append": (ctypes.c_int, [ctypes.POINTER(CPagedCache), ctypes.c_void_p, ctypes.c_void_p,
                                        ctypes.c_int32, _P_I64, _P_I64, ctypes.c_int32, ctypes.c_void_p,
                                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
-    "lc_cache_attend": (ctypes.c_int, [ctypes.POINTER(CPagedCache), ctypes.POINTER(CCacheQuery), ctypes.c_void_p]),
+    "lc_cache_attend": (ctypes.c_int, [ctypes.POINTER(CPagedCache), ctypes.c_void_p, ctypes.c_void_p]),
     "lc_cache_attend_workspace": (ctypes.c_int64, [ctypes.POINTER(CPagedCache), ctypes.c_int32, ctypes.c_int32]),
-    "lc_cache_evict": (ctypes.c_int, [ctypes.POINTER(CPagedCache), ctypes.POINTER(CCacheEviction),
-                                      ctypes.c_void_p]),
+    "lc_cache_evict": (ctypes.c_int, [ctypes.POINTER(CPagedCache), ctypes.c_void_p, ctypes.c_void_p]),
     "lc_row_major_strides": (ctypes.c_int, [ctypes.c_int32, _P_I64, _P_I64]),
     "lc_layout_footprint": (ctypes.c_int64, [_P_LAYOUT, ctypes.c_int64]),
     "lc_status_string": (ctypes.c_char_p, [ctypes.c_int32]),

@@ -10,11 +10,15 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 from . import _lib
 
 __all__ = ["PagedCache", "cache_append", "cache_attend", "cache_attend_workspace", "cache_evict"]
 
+_I64_3 = ctypes.c_int64 * 3
+_QUERY = struct.Struct("@PPiiqqqqPPqifPqPqqPq")     # lc_cache_query
+_EVICTION = struct.Struct("@PPqqiiPqqPqqP")          # lc_cache_eviction
 _TYPES = None  # torch dtype -> lc_cache_type
 
 
@@ -32,35 +36,35 @@ def _check(status: int, what: str) -> None:
         raise LayoutCopyError(status, what)
 
 
+def _current(device) -> int:
+    """Handle of the current stream (the raw query: torch.cuda.current_stream() builds an object, 3 us)."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
 class _on:
     """Runs allocations on the stream the kernels will use, so that torch's
     allocator hands the memory out in that stream's order."""
 
     def __init__(self, stream):
         import torch
-        if stream is None:
-            self.ctx, self.handle = None, torch.cuda.current_stream().cuda_stream
-        else:
-            s = stream
-            if isinstance(stream, int):
-                s = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
-            self.ctx, self.handle = torch.cuda.stream(s), s.cuda_stream
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+        self.ctx, self.handle = torch.cuda.stream(stream), stream.cuda_stream
 
     def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
+        self.ctx.__enter__()
         return self.handle
 
     def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+        self.ctx.__exit__(*exc)
 
 
 def _tensor(t, name: str, dtype, shape, device):
     """A tensor of that type and shape on the cache's device whose last mode's elements are adjacent."""
     if t.dtype != dtype:
         raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError("%s must have shape %r, got %r" % (name, shape, tuple(t.shape)))
     if t.device != device:
         raise ValueError("%s is on %s, the cache on %s" % (name, t.device, device))
@@ -117,6 +121,7 @@ class PagedCache:
         self.n_seqs, self.pages_per_seq = page_table.shape
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
         self.capacity = self.page_size * self.pages_per_seq
+        self.scale = 1.0 / math.sqrt(self.head_dim)
         self.io_dtype = torch.bfloat16 if q8 else k.dtype
 
     def workspace_bytes(self, n_q_heads: int, with_scores: bool) -> int:
@@ -152,24 +157,33 @@ def cache_append(cache: PagedCache, k, v, lengths, counts=None, new_lengths=None
     _tensor(lengths, "lengths", torch.int32, (cache.n_seqs,), cache.device)
     if counts is not None:
         _tensor(counts, "counts", torch.int32, (cache.n_seqs,), cache.device)
-    with _on(stream) as handle:
-        if new_lengths is None:
-            new_lengths = torch.empty_like(lengths)
-        else:
-            _tensor(new_lengths, "new_lengths", torch.int32, (cache.n_seqs,), cache.device)
-        i64 = ctypes.c_int64 * 3
-        _check(_lib.lib().lc_cache_append(cache._ref, k.data_ptr(), v.data_ptr(), _types()[k.dtype],
-                                          i64(*k.stride()[:3]), i64(*v.stride()[:3]), n_new,
-                                          None if counts is None else counts.data_ptr(), lengths.data_ptr(),
-                                          new_lengths.data_ptr(), handle), "cache_append")
+    if new_lengths is not None:
+        _tensor(new_lengths, "new_lengths", torch.int32, (cache.n_seqs,), cache.device)
+    if stream is not None:
+        with _on(stream) as handle:
+            return _append(cache, k, v, n_new, counts, lengths, new_lengths, handle)
+    return _append(cache, k, v, n_new, counts, lengths, new_lengths, _current(cache.device))
+
+
+def _append(cache, k, v, n_new, counts, lengths, new_lengths, handle):
+    if new_lengths is None:
+        import torch
+        new_lengths = torch.empty(lengths.shape, dtype=torch.int32, device=cache.device)
+    _check(_lib.lib().lc_cache_append(cache._ref, k.data_ptr(), v.data_ptr(), _types()[k.dtype],
+                                      _I64_3(*k.stride()[:3]), _I64_3(*v.stride()[:3]), n_new,
+                                      None if counts is None else counts.data_ptr(), lengths.data_ptr(),
+                                      new_lengths.data_ptr(), handle), "cache_append")
     return new_lengths
 
 
 def cache_attend_workspace(cache: PagedCache, n_q_heads: int, with_scores: bool = False, stream=None):
     """A workspace for ``cache_attend`` calls that do not overlap."""
     import torch
-    with _on(stream):
-        return torch.empty(cache.workspace_bytes(n_q_heads, with_scores), dtype=torch.uint8, device=cache.device)
+    n = cache.workspace_bytes(n_q_heads, with_scores)
+    if stream is not None:
+        with _on(stream):
+            return torch.empty(n, dtype=torch.uint8, device=cache.device)
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
 
 
 def cache_attend(cache: PagedCache, q, lengths, out=None, scale=None, window: int = 0, mask=None, lse=None,
@@ -191,37 +205,46 @@ def cache_attend(cache: PagedCache, q, lengths, out=None, scale=None, window: in
     n_q = q.shape[1]
     _tensor(q, "q", cache.io_dtype, (cache.n_seqs, n_q, cache.head_dim), cache.device)
     _tensor(lengths, "lengths", torch.int32, (cache.n_seqs,), cache.device)
-    a = _lib.CCacheQuery()
     if mask is not None:
         if mask.dtype not in (torch.bool, torch.uint8):
             raise ValueError("mask must be bool or uint8, got %s" % mask.dtype)
         _tensor(mask, "mask", mask.dtype, (cache.n_seqs, cache.capacity), cache.device)
-        a.mask, a.mask_stride = mask.data_ptr(), mask.stride(0)
     if lse is not None:
         _tensor(lse, "lse", torch.float32, (cache.n_seqs, n_q), cache.device)
-        a.lse, a.lse_stride = lse.data_ptr(), lse.stride(0)
     if scores is not None:
         _tensor(scores, "scores", torch.float32, (cache.n_seqs, cache.n_kv_heads, cache.capacity), cache.device)
-        a.scores = scores.data_ptr()
-        a.scores_stride[:] = scores.stride()[:2]
-    need = cache.workspace_bytes(n_q, scores is not None)
-    with _on(stream) as handle:
-        if out is None:
-            out = torch.empty((cache.n_seqs, n_q, cache.head_dim), dtype=q.dtype, device=q.device)
-        else:
-            _tensor(out, "out", q.dtype, tuple(q.shape), cache.device)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        elif workspace.device != cache.device or not workspace.is_contiguous():
-            raise ValueError("the workspace must be contiguous and on the cache's device")
-        a.q, a.out, a.lengths = q.data_ptr(), out.data_ptr(), lengths.data_ptr()
-        a.type, a.n_q_heads = _types()[q.dtype], n_q
-        a.q_stride[:] = q.stride()[:2]
-        a.out_stride[:] = out.stride()[:2]
-        a.window = window
-        a.scale = 1.0 / math.sqrt(cache.head_dim) if scale is None else scale
-        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        _check(_lib.lib().lc_cache_attend(cache._ref, ctypes.byref(a), handle), "cache_attend")
+    if out is not None:
+        _tensor(out, "out", q.dtype, q.shape, cache.device)
+    if workspace is not None and (workspace.device != cache.device or not workspace.is_contiguous()):
+        raise ValueError("the workspace must be contiguous and on the cache's device")
+    if stream is not None:
+        with _on(stream) as handle:
+            return _attend(cache, q, lengths, out, scale, window, mask, lse, scores, workspace, handle)
+    return _attend(cache, q, lengths, out, scale, window, mask, lse, scores, workspace, _current(cache.device))
+
+
+def _attend(cache, q, lengths, out, scale, window, mask, lse, scores, workspace, handle):
+    import torch
+    n_q = q.shape[1]
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    ws, ws_bytes = 0, 0
+    if workspace is not None:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    else:
+        ws_bytes = cache.workspace_bytes(n_q, scores is not None)
+        if ws_bytes:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+            ws = workspace.data_ptr()
+    qs, os = q.stride(), out.stride()
+    ss = (0, 0, 0) if scores is None else scores.stride()
+    # lc_cache_query, packed in one call (a ctypes structure's fields one by one cost several times that)
+    a = _QUERY.pack(q.data_ptr(), out.data_ptr(), _types()[q.dtype], n_q, qs[0], qs[1], os[0], os[1],
+                    lengths.data_ptr(), 0 if mask is None else mask.data_ptr(), 0 if mask is None else mask.stride(0),
+                    min(window, 0x7fffffff), cache.scale if scale is None else scale,
+                    0 if lse is None else lse.data_ptr(), 0 if lse is None else lse.stride(0),
+                    0 if scores is None else scores.data_ptr(), ss[0], ss[1], ws, ws_bytes)
+    _check(_lib.lib().lc_cache_attend(cache._ref, a, handle), "cache_attend")
     return out
 
 
@@ -242,26 +265,29 @@ def cache_evict(cache: PagedCache, lengths, scores, budget: int, recent: int = 0
     unit = (cache.n_seqs, cache.n_kv_heads)
     _tensor(lengths, "lengths", torch.int32, (cache.n_seqs,), cache.device)
     _tensor(scores, "scores", torch.float32, unit + (cache.capacity,), cache.device)
-    budget = int(budget)
-    a = _lib.CCacheEviction()
-    with _on(stream) as handle:
-        if kept is None:
-            kept = torch.empty(unit + (max(budget, 0),), dtype=torch.int32, device=cache.device)
-        else:
-            _tensor(kept, "kept", torch.int32, unit + (budget,), cache.device)
-        if new_scores is None:
-            new_scores = torch.empty(scores.shape, dtype=torch.float32, device=cache.device)
-        else:
-            _tensor(new_scores, "new_scores", torch.float32, tuple(scores.shape), cache.device)
-        if new_lengths is None:
-            new_lengths = torch.empty_like(lengths)
-        else:
-            _tensor(new_lengths, "new_lengths", torch.int32, (cache.n_seqs,), cache.device)
-        a.lengths, a.scores, a.kept = lengths.data_ptr(), scores.data_ptr(), kept.data_ptr()
-        a.new_scores, a.new_lengths = new_scores.data_ptr(), new_lengths.data_ptr()
-        a.scores_stride[:] = scores.stride()[:2]
-        a.kept_stride[:] = kept.stride()[:2]
-        a.new_scores_stride[:] = new_scores.stride()[:2]
-        a.budget, a.recent = budget, int(recent)
-        _check(_lib.lib().lc_cache_evict(cache._ref, ctypes.byref(a), handle), "cache_evict")
+    budget, recent = int(budget), int(recent)
+    if kept is not None:
+        _tensor(kept, "kept", torch.int32, unit + (budget,), cache.device)
+    if new_scores is not None:
+        _tensor(new_scores, "new_scores", torch.float32, scores.shape, cache.device)
+    if new_lengths is not None:
+        _tensor(new_lengths, "new_lengths", torch.int32, (cache.n_seqs,), cache.device)
+    if stream is not None:
+        with _on(stream) as handle:
+            return _evict(cache, lengths, scores, budget, recent, new_scores, kept, new_lengths, handle)
+    return _evict(cache, lengths, scores, budget, recent, new_scores, kept, new_lengths, _current(cache.device))
+
+
+def _evict(cache, lengths, scores, budget, recent, new_scores, kept, new_lengths, handle):
+    import torch
+    if kept is None:
+        kept = torch.empty((cache.n_seqs, cache.n_kv_heads, max(budget, 0)), dtype=torch.int32, device=cache.device)
+    if new_scores is None:
+        new_scores = torch.empty(scores.shape, dtype=torch.float32, device=cache.device)
+    if new_lengths is None:
+        new_lengths = torch.empty(lengths.shape, dtype=torch.int32, device=cache.device)
+    ss, ks, ns = scores.stride(), kept.stride(), new_scores.stride()
+    a = _EVICTION.pack(lengths.data_ptr(), scores.data_ptr(), ss[0], ss[1], budget, recent, kept.data_ptr(), ks[0],
+                       ks[1], new_scores.data_ptr(), ns[0], ns[1], new_lengths.data_ptr())
+    _check(_lib.lib().lc_cache_evict(cache._ref, a, handle), "cache_evict")
     return kept, new_scores, new_lengths

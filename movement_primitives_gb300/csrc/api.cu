@@ -177,12 +177,13 @@ extern "C" int lc_layout_copy(const void *src, const lc_tile_layout *src_layout,
 
 extern "C" int lc_last_device_error(lc_stream_t stream, uint64_t *detail) {
     if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return LC_ERR_CUDA;
-    constexpr int kWords = 11;
+    constexpr int kWords = 14;
     unsigned long long words[kWords] = {};
     cudaError_t (*const take[kWords])(unsigned long long *) = {
-        lc::take_module_error, lc::take_error_tile,  lc::take_error_tma_copy,     lc::take_error_warp1,
-        lc::take_error_warp2,  lc::take_error_warp4, lc::take_error_warp8,        lc::take_error_warp16,
-        lc::take_error_append, lc::take_error_evict, lc::take_error_attend};
+        lc::take_module_error,      lc::take_error_tile,       lc::take_error_tma_copy, lc::take_error_warp1,
+        lc::take_error_warp2,       lc::take_error_warp4,      lc::take_error_warp8,    lc::take_error_warp16,
+        lc::take_error_append,      lc::take_error_evict,      lc::take_error_attend,   lc::take_error_attend_bf16,
+        lc::take_error_attend_f16, lc::take_error_attend_e4m3};
     for (int i = 0; i < kWords; ++i)
         if (take[i](&words[i]) != cudaSuccess) return LC_ERR_CUDA;
     unsigned long long v = 0;

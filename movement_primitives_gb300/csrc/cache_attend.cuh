@@ -1,0 +1,798 @@
+// Attention of one new token a sequence over a paged key-value cache
+// (lc_cache_attend):
+//     x_j = scale * q . k_j,  w = softmax(x),  out = sum_j w_j v_j
+// over the slots j that are seen.
+//
+// Mathematics.  One pass over the keys and values: a warp keeps, for up to 16
+// query heads of one key head, the running maximum m of the logits (in base
+// 2: x_j log2 e), the sum l of 2^(x_j - m) and the output o of the slots it
+// has taken, all in float32, and rescales l and o when m grows.  Parts
+// (m, l, o) of one row join as sums weighted by 2^(m - max m).
+//
+// Both products are warp-level matrix instructions (mma.sync m16n8k16) with
+// the cache as the 16-row operand: 16 slots x 16 columns of the keys by 8 query heads,
+// and 16 columns x 16 slots of the values by 8 query heads, so that
+// up to 8 query heads a key head cost one instruction where heads as
+// rows would cost two.  The logits' fragment becomes the second product's operand by one
+// 8 x 8 transpose across lanes (movmatrix) a slot octet.  With G query
+// heads a key head the pass does G operations a byte of 16-bit cache, so memory
+// bounds it up to the 16 heads of a unit and the accumulators fit
+// registers.  The weights are rounded to the values' 16-bit type for the
+// second product (by at most 2^-9, or 2^-12 in float16, of each, no more
+// than the output's own rounding); the sum l takes them unrounded.
+//
+// Work.  Slots are taken in steps of TOK by one warp.  A (sequence, key head,
+// block of 16 query heads) is a unit; the steps of all units, laid end to end, are cut
+// into equal runs, one a warp, whatever the lengths: the warps find their
+// run from the lengths on the device.  A unit inside one run is finished there;
+// one that is cut leaves parts in the workspace, which k_attend_join joins
+// in their order, so results do not depend on timing.  Each warp streams its
+// run through a ring of its own in shared memory (cp.async, 16 bytes a lane,
+// rows swizzled for ldmatrix) that runs ahead across units, with no barrier
+// between warps.  Caches of few slots (kUnitSteps) take one block a unit instead,
+// joined in shared memory, with no second launch.
+#pragma once
+
+#include <cmath>
+#include <type_traits>
+
+#include "cache_common.cuh"
+
+namespace lc {
+
+constexpr int kAtWarps = 4;
+constexpr int kAtThreads = 32 * kAtWarps;
+constexpr int kAtRows = 16;        // query heads of a unit at most
+constexpr int kAtMaxBlocks = 608;  // of the main kernel; sizes the workspace
+constexpr int kAtMaxRuns = kAtMaxBlocks * kAtWarps;
+constexpr int kJoinThreads = 256;
+constexpr int kJoinWide = 1024;
+constexpr int kScorePer = 4;       // slots of a thread
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// A run takes at least this many steps: shorter ones leave more parts to join than
+// the further warps save.
+constexpr int kAtMinSteps = 2;
+// Capacity, in steps, up to which a unit is one block's.
+constexpr int kUnitSteps = 16;
+
+struct AttendArgs {
+    CacheArgs c;
+    const uint16_t *q;
+    uint16_t *out;
+    const int32_t *lengths;
+    const uint8_t *mask;
+    float *lse, *scores;
+    int64_t qst[2], ost[2], sst[2];
+    int64_t mask_stride, lse_stride;
+    int32_t q_heads, group, window;
+    int32_t row_blocks;   // units of one key head
+    float scale2;         // scale * log2 e
+    bool q_wide;          // rows of q on 8-byte boundaries
+    // workspace
+    float *part;          // [2 runs][part_rows][part_pitch]
+    float2 *part_ml;      // [2 runs][part_rows]
+    int2 *split;          // per unit: first and last run of a unit that is cut, first -1 when it is not
+    float *lse2;          // [sequence, query head], base 2, of units that are not cut (with scores)
+    float *logits;        // [sequence, query head, logit_stride], base 2, from the first slot seen (with scores)
+    int64_t logit_stride;
+    int32_t part_rows, part_pitch;
+    int32_t join_blocks, score_chunks;  // of k_attend_join
+};
+
+inline int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
+
+// Shapes of one instantiation.  DP: head_dim rounded up (64, 128, 256); KV: an
+// lc_cache_type; NG: query heads in eights (1, 2).  A step is 8 KiB where the shapes allow.
+template <int DP, int KV, int NG>
+struct AtShape {
+    static constexpr int EB = KV == LC_CACHE_E4M3 ? 1 : 2;
+    static constexpr int RB = DP * EB;                       // bytes of a row
+    static constexpr int CH = RB / 16;                       // its 16-byte chunks
+    static constexpr int TOK = 8192 / (2 * RB) >= 32 ? 32 : 16;
+    static constexpr int STEP = 2 * TOK * RB;                // keys, then values
+    static constexpr int ST = STEP <= 4096 ? 6 : 3;          // steps in the ring
+    static constexpr int SC = KV == LC_CACHE_E4M3 ? 2 * TOK * 4 : 0;  // scales of a step
+    static constexpr int WARP_BYTES = ST * (STEP + SC);
+    static constexpr int OP = DP + 4;                        // floats between the heads of a warp's output
+    static constexpr int SMEM = kAtWarps * WARP_BYTES;
+    static_assert(8 * NG * OP * 4 <= WARP_BYTES, "a warp's output is staged in its ring");
+};
+
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void *src, bool real) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4_zfill(uint32_t dst, const void *src, bool real) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         const uint32_t (&b)[2]) {
+    if constexpr (F16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b[0]), "r"(b[1]));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b[0]), "r"(b[1]));
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if constexpr (F16) {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    } else {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+}
+
+// Four E4M3 codes (bytes 0..3 of r) as two bfloat16 pairs: even = (0, 2), odd = (1,
+// 3).  Sign and magnitude move to bfloat16's places (the same exponent
+// layout, three of its seven fraction bits), and one exact product by 2^120
+// makes up for the biases, 7 and 127.
+__device__ __forceinline__ void e4m3_pairs(uint32_t r, uint32_t &even, uint32_t &odd) {
+    const uint32_t e = (r & 0x00800080u) << 8 | (r & 0x007f007fu) << 4;
+    const uint32_t o = (r & 0x80008000u) | (r >> 4 & 0x07f007f0u);
+    const uint32_t k = 0x7b807b80u;  // 2^120 twice
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(even) : "r"(e), "r"(k));
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(odd) : "r"(o), "r"(k));
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {  // 2 ulp, 0 for -infinity
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The slots [lo, n) that sequence b's query sees (before the mask).
+__device__ __forceinline__ int seen_from(const AttendArgs &a, int b, int *n) {
+    *n = cache_length(a.c, a.lengths, b, kClassAttend);
+    return a.window && a.window < *n ? *n - a.window : 0;
+}
+
+// A place in the steps of all units: step `t` of `steps` of unit `unit` of sequence b.
+struct Place {
+    int b, unit, t, steps, lo, n;
+};
+
+template <int TOK>
+__device__ __forceinline__ void enter_sequence(const AttendArgs &a, Place &p) {
+    p.lo = seen_from(a, p.b, &p.n);
+    p.steps = (p.n - p.lo + TOK - 1) / TOK;
+}
+
+// To the next step; there has to be one.
+template <int TOK>
+__device__ __forceinline__ void next_step(const AttendArgs &a, int units, Place &p) {
+    if (++p.t < p.steps) return;
+    p.t = 0;
+    if (++p.unit < units) return;
+    p.unit = 0;
+    do {
+        ++p.b;
+        enter_sequence<TOK>(a, p);
+    } while (p.steps == 0);
+}
+
+template <int DP, int KV, int NG, bool VEC>
+struct Attend {
+    using S = AtShape<DP, KV, NG>;
+    static constexpr bool F16 = KV == LC_CACHE_F16, Q8 = KV == LC_CACHE_E4M3;
+    static constexpr int KS = DP / 16;           // 16-wide pieces of a row
+    static constexpr int MT = S::TOK / 16;       // 16-slot pieces of a step
+
+    const AttendArgs &a;
+    const int lane;
+    uint8_t *ring;        // this warp's
+    uint32_t ring_s;
+    uint32_t *seen_bits;  // this warp's, one word a stage
+
+    // the unit: sequence, query heads, the first of them
+    int b, rows, q0;
+
+    uint32_t qb[KS][NG][2];
+    float o[KS][NG][4], m[NG][2], l[NG][2];
+
+    // the pages of a step's slots, one a lane, read one step ahead of its rows
+    int next_page, next_row, next_head;
+    bool next_seen;
+
+    __device__ __forceinline__ static uint32_t swz(int row, int chunk) {
+        return S::RB >= 128 ? (chunk ^ (row & 7)) * 16 : (chunk ^ (row >> 1 & 3)) * 16;
+    }
+
+    // The value column that row g (+ 8 i) of 16-wide piece c stands for: E4M3 columns come in adjacent pairs.
+    __device__ __forceinline__ static int col_of(int c, int g, int i) {
+        return Q8 ? 16 * c + 2 * g + i : 16 * c + g + 8 * i;
+    }
+
+    // Query heads as the 16 x 8 operand: head lane / 4, columns k = 2q, 2q + 1, 2q + 8, 2q + 9 of each 16-wide
+    // piece; for E4M3 keys, which come four adjacent columns a lane, 4q, 4q + 2, 4q + 1, 4q + 3.
+    __device__ __forceinline__ void load_q() {
+        const int q = lane & 3;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            const int head = 8 * g + (lane >> 2);
+            const uint16_t *p = a.q + b * a.qst[0] + (q0 + min(head, rows - 1)) * a.qst[1];
+            const bool on = head < rows;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                uint32_t x, y;
+                if (a.q_wide) {
+                    // whole fours of columns on 8-byte boundaries
+                    if (Q8) {
+                        const int c = 16 * ks + 4 * q;
+                        const uint2 v = on && c < a.c.dim ? *reinterpret_cast<const uint2 *>(p + c) : make_uint2(0, 0);
+                        x = __byte_perm(v.x, v.y, 0x5410);
+                        y = __byte_perm(v.x, v.y, 0x7632);
+                    } else {
+                        const int c = 16 * ks + 2 * q;
+                        x = on && c < a.c.dim ? *reinterpret_cast<const uint32_t *>(p + c) : 0;
+                        y = on && c + 8 < a.c.dim ? *reinterpret_cast<const uint32_t *>(p + c + 8) : 0;
+                    }
+                } else {
+                    const int c = 16 * ks + (Q8 ? 4 * q : 2 * q);
+                    const int d1 = Q8 ? 2 : 1, e0 = Q8 ? 1 : 8, e1 = Q8 ? 3 : 9;
+                    auto at = [&](int i) { return on && i < a.c.dim ? static_cast<uint32_t>(p[i]) : 0u; };
+                    x = at(c) | at(c + d1) << 16;
+                    y = at(c + e0) | at(c + e1) << 16;
+                }
+                qb[ks][g][0] = x;
+                qb[ks][g][1] = y;
+            }
+        }
+    }
+
+    // Reads the page of this lane's slot of the step that starts at slot j0 of sequence pb.
+    __device__ __forceinline__ void find_pages(int pb, int head, int j0, int n) {
+        const int j = j0 + lane;
+        next_page = -1;
+        next_row = 0;
+        next_head = head;
+        next_seen = false;
+        if (lane < S::TOK && j < n) {
+            const int i = static_cast<int>(fast_div(static_cast<uint32_t>(j), a.c.page_div));
+            next_row = j - i * a.c.page;
+            next_page = a.c.table[pb * a.c.table_stride + i];
+            next_seen = !a.mask || a.mask[pb * a.mask_stride + j];
+        }
+    }
+
+    // Starts the copies of the step whose pages find_pages read, into `stage`.
+    __device__ __forceinline__ void issue(int stage) {
+        const bool in_pool = next_page >= 0 && next_page < a.c.n_pages;
+        if (next_seen && !in_pool) report_error(LC_ERR_CACHE_INDEX, kClassAttend);
+        const bool seen = next_seen && in_pool;
+        const uint32_t bits = __ballot_sync(0xffffffffu, seen);
+        int64_t ko = 0, vo = 0;
+        if (seen) {
+            ko = row_offset(a.c.kst, next_page, next_head, next_row);
+            vo = row_offset(a.c.vst, next_page, next_head, next_row);
+        }
+        uint8_t *dst = ring + stage * (S::STEP + S::SC);
+        const uint32_t dst_s = ring_s + stage * (S::STEP + S::SC);
+        if (lane == 0) seen_bits[stage] = bits;
+        if constexpr (Q8)
+            if (lane < S::TOK) {
+                const float *ks = a.c.ks + (seen ? row_offset(a.c.kss, next_page, next_head, next_row) : 0);
+                const float *vs = a.c.vs + (seen ? row_offset(a.c.vss, next_page, next_head, next_row) : 0);
+                cp_async4_zfill(dst_s + S::STEP + 4 * lane, ks, seen);
+                cp_async4_zfill(dst_s + S::STEP + 4 * (S::TOK + lane), vs, seen);
+            }
+        if constexpr (VEC) {
+            const int chunks = a.c.dim * S::EB / 16;
+#pragma unroll
+            for (int side = 0; side < 2; ++side)
+#pragma unroll
+                for (int i = 0; i < S::TOK * S::CH / 32; ++i) {
+                    const int at = i * 32 + lane, row = at / S::CH, chunk = at % S::CH;
+                    const int64_t off = __shfl_sync(0xffffffffu, side ? vo : ko, row);
+                    const bool real = (bits >> row & 1) && chunk < chunks;
+                    cp_async16_zfill(dst_s + side * S::TOK * S::RB + row * S::RB + swz(row, chunk),
+                                     (side ? a.c.v : a.c.k) + off * S::EB + (real ? chunk * 16 : 0), real);
+                }
+        } else {
+#pragma unroll 1
+            for (int side = 0; side < 2; ++side)
+#pragma unroll 1
+                for (int row = 0; row < S::TOK; ++row) {
+                    const int64_t off = __shfl_sync(0xffffffffu, side ? vo : ko, row);
+                    const uint8_t *src = (side ? a.c.v : a.c.k) + off * S::EB;
+                    for (int e = lane; e < DP; e += 32) {
+                        const bool real = (bits >> row & 1) && e < a.c.dim;
+                        uint8_t *to = dst + side * S::TOK * S::RB + row * S::RB + swz(row, e * S::EB / 16) +
+                                      e * S::EB % 16;
+                        if constexpr (Q8)
+                            *to = real ? src[e] : uint8_t(0);
+                        else
+                            *reinterpret_cast<uint16_t *>(to) =
+                                real ? reinterpret_cast<const uint16_t *>(src)[e] : uint16_t(0);
+                    }
+                }
+        }
+    }
+
+    __device__ __forceinline__ void begin_unit(int seq, int unit) {
+        b = seq;
+        const int h = a.row_blocks == 1 ? unit : unit / a.row_blocks, rb = unit - h * a.row_blocks;
+        q0 = h * a.group + rb * kAtRows;
+        rows = min(a.group - rb * kAtRows, kAtRows);
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                m[g][i] = -INFINITY;
+                l[g][i] = 0.f;
+            }
+#pragma unroll
+        for (int c = 0; c < KS; ++c)
+#pragma unroll
+            for (int g = 0; g < NG; ++g) o[c][g][0] = o[c][g][1] = o[c][g][2] = o[c][g][3] = 0.f;
+        load_q();
+    }
+
+    // Takes the step in `stage`, the unit's slots from `at` on (counted from the first seen).
+    __device__ __forceinline__ void take(int stage, int at) {
+        const uint32_t bits = seen_bits[stage];
+        if (!a.logits && bits == 0) return;
+        const int slot = lane >> 2, q = lane & 3, mat = lane >> 3;
+        const uint32_t ks_s = ring_s + stage * (S::STEP + S::SC), vs_s = ks_s + S::TOK * S::RB;
+        const float *scales = reinterpret_cast<const float *>(ring + stage * (S::STEP + S::SC) + S::STEP);
+
+        // logits: x[t][g][0, 1] of slot 16 t + lane / 4, [2, 3] of the slot 8 on; query heads 8 g + 2 q, + 1
+        float x[MT][NG][4];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+#pragma unroll
+            for (int g = 0; g < NG; ++g) x[t][g][0] = x[t][g][1] = x[t][g][2] = x[t][g][3] = 0.f;
+            const int row = 16 * t + (lane & 7) + (mat & 1) * 8;
+            if constexpr (Q8) {
+#pragma unroll
+                for (int ks = 0; ks < KS; ks += 2) {
+                    uint32_t r[4], e0, d0, e1, d1;
+                    ldsm_x4(r, ks_s + row * S::RB + swz(row, ks + (mat >> 1)));
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        e4m3_pairs(r[2 * i], e0, d0);
+                        e4m3_pairs(r[2 * i + 1], e1, d1);
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) mma16816<false>(x[t][g], e0, e1, d0, d1, qb[ks + i][g]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    uint32_t r[4];
+                    ldsm_x4(r, ks_s + row * S::RB + swz(row, 2 * ks + (mat >> 1)));
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) mma16816<F16>(x[t][g], r[0], r[1], r[2], r[3], qb[ks][g]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int col = 16 * t + slot + 8 * i;
+                const float f = Q8 ? a.scale2 * scales[col] : a.scale2;
+                const bool on = bits >> col & 1;
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    x[t][g][2 * i] = on ? x[t][g][2 * i] * f : -INFINITY;
+                    x[t][g][2 * i + 1] = on ? x[t][g][2 * i + 1] * f : -INFINITY;
+                }
+            }
+        }
+        if (a.logits) {
+            float *to = a.logits + (int64_t(b) * a.q_heads + q0) * a.logit_stride + at;
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int head = 8 * g + 2 * q + u;
+                    if (head < rows)
+#pragma unroll
+                        for (int t = 0; t < MT; ++t)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                to[head * a.logit_stride + 16 * t + slot + 8 * i] = x[t][g][2 * i + u];
+                }
+            if (bits == 0) return;
+        }
+        // running maximum, sum and rescaling of the output
+        bool grown = false;
+        float keep[NG][2];
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                float top = fmaxf(x[0][g][u], x[0][g][2 + u]);
+#pragma unroll
+                for (int t = 1; t < MT; ++t) top = fmaxf(top, fmaxf(x[t][g][u], x[t][g][2 + u]));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                keep[g][u] = 1.f;
+                if (top > m[g][u]) {
+                    keep[g][u] = exp2_fast(m[g][u] - top);
+                    m[g][u] = top;
+                    grown = true;
+                }
+                const float safe = m[g][u] == -INFINITY ? 0.f : m[g][u];
+                float sum = 0.f;
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        x[t][g][2 * i + u] = exp2_fast(x[t][g][2 * i + u] - safe);
+                        sum += x[t][g][2 * i + u];
+                    }
+                l[g][u] = l[g][u] * keep[g][u] + sum;
+            }
+        if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+            for (int c = 0; c < KS; ++c)
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[c][g][i] *= keep[g][i & 1];
+        }
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            uint32_t p[NG][2];
+            const float s0 = Q8 ? scales[S::TOK + 16 * t + slot] : 1.f, s1 = Q8 ? scales[S::TOK + 16 * t + slot + 8] : 1.f;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                // slots lane / 4 of two heads -> head lane / 4 of two slots
+                p[g][0] = transpose8(pack2<F16>(x[t][g][0] * s0, x[t][g][1] * s0));
+                p[g][1] = transpose8(pack2<F16>(x[t][g][2] * s1, x[t][g][3] * s1));
+            }
+            const int row = 16 * t + (lane & 7) + (mat >> 1) * 8;
+            if constexpr (Q8) {
+                // slots 0-7 and 8-15 of two 16-wide pieces
+                const int vrow = 16 * t + (lane & 7) + (mat & 1) * 8;
+#pragma unroll
+                for (int c = 0; c < KS; c += 2) {
+                    uint32_t r[4], e0, d0, e1, d1;
+                    ldsm_x4_t(r, vs_s + vrow * S::RB + swz(vrow, c + (mat >> 1)));
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        e4m3_pairs(r[2 * i], e0, d0);
+                        e4m3_pairs(r[2 * i + 1], e1, d1);
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) mma16816<false>(o[c + i][g], e0, d0, e1, d1, p[g]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < KS; ++c) {
+                    uint32_t r[4];
+                    ldsm_x4_t(r, vs_s + row * S::RB + swz(row, 2 * c + (mat & 1)));
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) mma16816<F16>(o[c][g], r[0], r[1], r[2], r[3], p[g]);
+                }
+            }
+        }
+    }
+
+    // The lanes' sums become the warp's.
+    __device__ __forceinline__ void total() {
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l[g][u] += __shfl_xor_sync(0xffffffffu, l[g][u], d);
+    }
+
+    // Writes the finished unit (slot < 0), or its part.
+    __device__ __forceinline__ void write(int slot) {
+        const int row = lane >> 2, q = lane & 3;
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int head = 8 * g + 2 * q + u;
+                if (head >= rows) continue;
+                const float sum = l[g][u], top = m[g][u];
+                if (slot >= 0) {
+                    const int64_t at = int64_t(slot) * a.part_rows + head;
+                    float *to = a.part + at * a.part_pitch;
+#pragma unroll
+                    for (int c = 0; c < KS; ++c) {
+                        to[col_of(c, row, 0)] = o[c][g][u];
+                        to[col_of(c, row, 1)] = o[c][g][2 + u];
+                    }
+                    if (row == 0) a.part_ml[at] = make_float2(top, sum);
+                } else {
+                    const float f = sum == 0.f ? 0.f : 1.f / sum;
+                    uint16_t *to = a.out + b * a.ost[0] + (q0 + head) * a.ost[1];
+#pragma unroll
+                    for (int c = 0; c < KS; ++c)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int col = col_of(c, row, i);
+                            if (col < a.c.dim) to[col] = static_cast<uint16_t>(pack2<F16>(o[c][g][2 * i + u] * f, 0.f));
+                        }
+                    if (row == 0) write_lse(q0 + head, top, sum);
+                }
+            }
+    }
+
+    __device__ __forceinline__ float write_lse(int hq, float top, float sum) const {
+        const float lse = sum == 0.f ? -INFINITY : top + log2f(sum);
+        if (a.lse) a.lse[b * a.lse_stride + hq] = lse * kLn2;
+        if (a.logits) a.lse2[int64_t(b) * a.q_heads + hq] = lse;
+        return lse;
+    }
+};
+
+// One run a warp.
+template <int DP, int KV, int NG, bool VEC>
+__global__ void __launch_bounds__(kAtThreads) k_attend(const __grid_constant__ AttendArgs a) {
+    using A = Attend<DP, KV, NG, VEC>;
+    using S = typename A::S;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint32_t seen_bits[kAtWarps * S::ST];
+    __shared__ long long warp_sums[kAtWarps], upto[kAtThreads];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int units = a.c.heads * a.row_blocks;
+
+    // the steps up to the sequences of each thread: thread t stands for `per` of them
+    const int per = (a.c.n_seqs + kAtThreads - 1) / kAtThreads;
+    long long incl = 0;
+    for (int b = min(t * per, a.c.n_seqs); b < min(t * per + per, a.c.n_seqs); ++b) {
+        int n;
+        const int lo = seen_from(a, b, &n);
+        incl += (n - lo + S::TOK - 1) / S::TOK;
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += y;
+    }
+    if (lane == 31) warp_sums[warp] = incl;
+    __syncthreads();
+    long long total = 0;
+#pragma unroll
+    for (int w = 0; w < kAtWarps; ++w) {
+        if (w < warp) incl += warp_sums[w];
+        total += warp_sums[w];
+    }
+    upto[t] = incl * units;
+    total *= units;
+    __syncthreads();
+
+    // this warp's run [f0, f1) and the place it starts at
+    const long long runs =
+        min(static_cast<long long>(gridDim.x) * kAtWarps, (total + kAtMinSteps - 1) / kAtMinSteps);
+    const int run = blockIdx.x * kAtWarps + warp;
+    if (run >= runs) return;
+    const long long f0 = total * run / runs, f1 = total * (run + 1) / runs;
+    int owner = 0;  // the thread whose sequences hold f0
+#pragma unroll
+    for (int w = 0; w < kAtWarps; ++w) owner += __popc(__ballot_sync(0xffffffffu, upto[32 * w + lane] <= f0));
+    long long base = owner ? upto[owner - 1] : 0;
+    Place c{};
+    for (c.b = owner * per;; ++c.b) {
+        enter_sequence<S::TOK>(a, c);
+        const long long size = static_cast<long long>(c.steps) * units;
+        if (f0 < base + size) break;
+        base += size;
+    }
+    c.unit = static_cast<int>((f0 - base) / c.steps);
+    c.t = static_cast<int>(f0 - base - static_cast<long long>(c.unit) * c.steps);
+
+    A u{a, lane, smem + warp * S::WARP_BYTES, ptx::smem_addr(smem + warp * S::WARP_BYTES), seen_bits + warp * S::ST};
+    int left = static_cast<int>(f1 - f0), ahead = left;  // steps to take, and to find pages for
+    Place p = c;
+    bool found = false;  // a step's pages are at hand
+    auto find = [&] {
+        found = ahead > 0;
+        if (!found) return;
+        u.find_pages(p.b, a.row_blocks == 1 ? p.unit : p.unit / a.row_blocks, p.lo + p.t * S::TOK, p.n);
+        if (--ahead > 0) next_step<S::TOK>(a, units, p);
+    };
+    find();
+#pragma unroll 1
+    for (int i = 0; i < S::ST - 1; ++i) {
+        if (found) {
+            u.issue(i);
+            find();
+        }
+        ptx::cp_async_commit();
+    }
+    int stage = 0, fill = S::ST - 1;
+    while (left > 0) {
+        const int t0 = c.t, t1 = min(c.steps, t0 + left);
+        u.begin_unit(c.b, c.unit);
+#pragma unroll 1
+        for (int k = t0; k < t1; ++k) {
+            if (found) {
+                u.issue(fill);
+                find();
+            }
+            ptx::cp_async_commit();
+            ptx::cp_async_wait<S::ST - 1>();
+            __syncwarp();
+            u.take(stage, k * S::TOK);
+            __syncwarp();
+            stage = stage + 1 == S::ST ? 0 : stage + 1;
+            fill = fill + 1 == S::ST ? 0 : fill + 1;
+        }
+        u.total();
+        const bool first = t0 == 0, last = t1 == c.steps;
+        if (lane == 0) {
+            int2 *split = a.split + int64_t(c.b) * units + c.unit;
+            if (first) split->x = last ? -1 : run;
+            if (last) split->y = run;
+        }
+        u.write(first && last ? -1 : 2 * run + first);
+        left -= t1 - t0;
+        if (left > 0) {
+            c.t = t1 - 1;
+            next_step<S::TOK>(a, units, c);
+        }
+    }
+}
+
+// One unit a block, its steps dealt to the warps in turn and their results
+// joined in shared memory.
+template <int DP, int KV, int NG>
+__global__ void __launch_bounds__(kAtThreads) k_attend_unit(const __grid_constant__ AttendArgs a) {
+    using A = Attend<DP, KV, NG, true>;
+    using S = typename A::S;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint32_t seen_bits[kAtWarps * S::ST];
+    __shared__ float2 ml[kAtWarps][8 * NG];
+    __shared__ float lse_of[8 * NG];
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int units = a.c.heads * a.row_blocks;
+    Place c{};
+    c.b = blockIdx.x / units;
+    c.unit = blockIdx.x - c.b * units;
+    enter_sequence<S::TOK>(a, c);
+    A u{a, lane, smem + warp * S::WARP_BYTES, ptx::smem_addr(smem + warp * S::WARP_BYTES), seen_bits + warp * S::ST};
+    const int h = a.row_blocks == 1 ? c.unit : c.unit / a.row_blocks;
+    int ahead = warp;
+    auto issue = [&](int stage) {
+        if (ahead < c.steps) {
+            u.find_pages(c.b, h, c.lo + ahead * S::TOK, c.n);
+            u.issue(stage);
+        }
+        ahead += kAtWarps;
+        ptx::cp_async_commit();
+    };
+#pragma unroll 1
+    for (int i = 0; i < S::ST - 1; ++i) issue(i);
+    u.begin_unit(c.b, c.unit);
+    int stage = 0, fill = S::ST - 1;
+#pragma unroll 1
+    for (int k = warp; k < c.steps; k += kAtWarps) {
+        issue(fill);
+        ptx::cp_async_wait<S::ST - 1>();
+        __syncwarp();
+        u.take(stage, k * S::TOK);
+        __syncwarp();
+        stage = stage + 1 == S::ST ? 0 : stage + 1;
+        fill = fill + 1 == S::ST ? 0 : fill + 1;
+    }
+    u.total();
+    float *mine = reinterpret_cast<float *>(u.ring);
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int head = 8 * g + 2 * (lane & 3) + i, row = lane >> 2;
+            if (row == 0) ml[warp][head] = make_float2(u.m[g][i], u.l[g][i]);
+#pragma unroll
+            for (int k = 0; k < A::KS; ++k) {
+                mine[head * S::OP + A::col_of(k, row, 0)] = u.o[k][g][i];
+                mine[head * S::OP + A::col_of(k, row, 1)] = u.o[k][g][2 + i];
+            }
+        }
+    __syncthreads();
+    for (int at = t; at < u.rows * (DP / 4); at += kAtThreads) {
+        const int head = at / (DP / 4), col = at % (DP / 4) * 4;
+        float top = -INFINITY, sum = 0.f;
+        float y[4] = {};
+#pragma unroll
+        for (int w = 0; w < kAtWarps; ++w) top = fmaxf(top, ml[w][head].x);
+        const float safe = top == -INFINITY ? 0.f : top;
+#pragma unroll
+        for (int w = 0; w < kAtWarps; ++w) {
+            const float2 v = ml[w][head];
+            const float f = exp2_fast(v.x - safe);
+            const float4 z = *reinterpret_cast<const float4 *>(smem + w * S::WARP_BYTES + (head * S::OP + col) * 4);
+            sum += v.y * f;
+            y[0] += z.x * f;
+            y[1] += z.y * f;
+            y[2] += z.z * f;
+            y[3] += z.w * f;
+        }
+        const float f = sum == 0.f ? 0.f : 1.f / sum;
+        uint16_t *to = a.out + c.b * a.ost[0] + (u.q0 + head) * a.ost[1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (col + i < a.c.dim) to[col + i] = static_cast<uint16_t>(pack2<A::F16>(y[i] * f, 0.f));
+        if (col == 0) lse_of[head] = u.write_lse(u.q0 + head, top, sum);
+    }
+    if (a.logits) {
+        __syncthreads();
+        const float *x = a.logits + (int64_t(c.b) * a.q_heads + u.q0) * a.logit_stride;
+        for (int i = t; i < c.n - c.lo; i += kAtThreads) {
+            float w = 0.f;
+            for (int g = 0; g < u.rows; ++g) {
+                const float e = exp2_fast(x[g * a.logit_stride + i] - lse_of[g]);
+                w += lse_of[g] == -INFINITY ? 0.f : e;
+            }
+            a.scores[c.b * a.sst[0] + h * a.sst[1] + c.lo + i] += w;
+        }
+    }
+}
+
+// One warp instantiation's launches: one block a unit (VEC only), or one run a warp.
+template <int DP, int KV, int NG, bool VEC>
+int launch_attend(const AttendArgs &a, bool by_unit, int *runs, cudaStream_t cs) {
+    using S = AtShape<DP, KV, NG>;
+    const int64_t units = int64_t(a.c.n_seqs) * a.c.heads * a.row_blocks;
+    int sms, per;
+    if constexpr (VEC) {
+        if (by_unit) {
+            const void *fn = reinterpret_cast<const void *>(&k_attend_unit<DP, KV, NG>);
+            if (prepare(fn, kAtThreads, S::SMEM, S::SMEM, &sms, &per) != cudaSuccess) return LC_ERR_CUDA;
+            k_attend_unit<DP, KV, NG><<<static_cast<unsigned>(units), kAtThreads, S::SMEM, cs>>>(a);
+            return finish_launch();
+        }
+    }
+    const void *fn = reinterpret_cast<const void *>(&k_attend<DP, KV, NG, VEC>);
+    if (prepare(fn, kAtThreads, S::SMEM, S::SMEM, &sms, &per) != cudaSuccess) return LC_ERR_CUDA;
+    // no more blocks than are resident at once, nor than the steps of full sequences
+    const int64_t most = units * ((a.c.cap + S::TOK - 1) / S::TOK);
+    const int64_t grid = std::max<int64_t>(
+        1, std::min<int64_t>({int64_t(sms) * per, kAtMaxBlocks,
+                              (most + kAtMinSteps * kAtWarps - 1) / (kAtMinSteps * kAtWarps)}));
+    *runs = static_cast<int>(grid) * kAtWarps;
+    k_attend<DP, KV, NG, VEC><<<static_cast<unsigned>(grid), kAtThreads, S::SMEM, cs>>>(a);
+    return finish_launch();
+}
+
+// The main launch for one cache type; `runs` receives the runs of a launch by runs.
+template <int KV>
+int launch_attend_type(const AttendArgs &a, bool by_unit, bool vec, int *runs, cudaStream_t cs) {
+    auto heads = [&](auto dp) {
+        constexpr int DP = decltype(dp)::value;
+        if (a.group <= 8)
+            return vec ? launch_attend<DP, KV, 1, true>(a, by_unit, runs, cs)
+                       : launch_attend<DP, KV, 1, false>(a, by_unit, runs, cs);
+        return vec ? launch_attend<DP, KV, 2, true>(a, by_unit, runs, cs)
+                   : launch_attend<DP, KV, 2, false>(a, by_unit, runs, cs);
+    };
+    switch (padded_dim(a.c.dim)) {
+        case 64: return heads(std::integral_constant<int, 64>{});
+        case 128: return heads(std::integral_constant<int, 128>{});
+        default: return heads(std::integral_constant<int, 256>{});
+    }
+}
+
+}  // namespace lc

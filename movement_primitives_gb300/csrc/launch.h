@@ -49,5 +49,8 @@ cudaError_t take_error_warp16(unsigned long long *v);
 cudaError_t take_error_append(unsigned long long *v);
 cudaError_t take_error_evict(unsigned long long *v);
 cudaError_t take_error_attend(unsigned long long *v);
+cudaError_t take_error_attend_bf16(unsigned long long *v);
+cudaError_t take_error_attend_f16(unsigned long long *v);
+cudaError_t take_error_attend_e4m3(unsigned long long *v);
 
 }  // namespace lc
