@@ -75,7 +75,8 @@ typedef struct {
  *   *_stride  of sequence, token, head
  *   new_lengths  may be lengths' own buffer only where n_new is 0
  * Errors: LC_ERR_NULL, LC_ERR_SHAPE, LC_ERR_TYPE, LC_ERR_BAD_STRIDE,
- * LC_ERR_ALIGN, LC_ERR_OVERFLOW, LC_ERR_OVERLAP (new_lengths is lengths). */
+ * LC_ERR_ALIGN, LC_ERR_OVERFLOW, LC_ERR_NOT_INJECTIVE, LC_ERR_OVERLAP
+ * (new_lengths is lengths). */
 int lc_cache_append(const lc_paged_cache *cache, const void *k_new, const void *v_new, int32_t type,
                     const int64_t k_stride[3], const int64_t v_stride[3], int32_t n_new, const int32_t *counts,
                     const int32_t *lengths, int32_t *new_lengths, lc_stream_t stream);
@@ -119,7 +120,7 @@ int64_t lc_cache_attend_workspace(const lc_paged_cache *cache, int32_t n_q_heads
 
 /* Errors: LC_ERR_NULL, LC_ERR_SHAPE (n_q_heads no multiple of n_kv_heads,
  * negative window, sizes), LC_ERR_TYPE, LC_ERR_BAD_STRIDE, LC_ERR_ALIGN,
- * LC_ERR_OVERFLOW, LC_ERR_WORKSPACE. */
+ * LC_ERR_OVERFLOW, LC_ERR_NOT_INJECTIVE, LC_ERR_WORKSPACE. */
 int lc_cache_attend(const lc_paged_cache *cache, const lc_cache_query *query, lc_stream_t stream);
 
 /* One eviction.  A sequence of n = lengths[b] <= budget slots keeps them all.
@@ -132,7 +133,9 @@ int lc_cache_attend(const lc_paged_cache *cache, const lc_cache_query *query, lc
  *   kept        [n_seqs, n_kv_heads, budget] receives the old slot of every
  *               kept one, -1 past them
  *   new_scores  like scores, another buffer: the kept slots' scores, then zeros
- *   new_lengths [n_seqs], another buffer than lengths: min(n, budget) */
+ *   new_lengths [n_seqs], another buffer than lengths: min(n, budget)
+ *   workspace   at least lc_cache_evict_workspace(...) bytes, 256-byte
+ *               aligned, as lc_cache_attend's */
 typedef struct {
     const int32_t *lengths;
     const float *scores;
@@ -144,11 +147,18 @@ typedef struct {
     float *new_scores;
     int64_t new_scores_stride[2];
     int32_t *new_lengths;
+    void *workspace;
+    int64_t workspace_bytes;
 } lc_cache_eviction;
+
+/* Bytes of workspace of lc_cache_evict, or -1 for arguments that it refuses. */
+int64_t lc_cache_evict_workspace(const lc_paged_cache *cache, int32_t budget);
 
 /* Errors: LC_ERR_NULL, LC_ERR_SHAPE (budget < 1, recent outside 0 .. budget,
  * sizes), LC_ERR_TYPE, LC_ERR_BAD_STRIDE, LC_ERR_ALIGN, LC_ERR_OVERFLOW,
- * LC_ERR_OVERLAP (new_scores or new_lengths is the old buffer). */
+ * LC_ERR_NOT_INJECTIVE, LC_ERR_WORKSPACE, LC_ERR_OVERLAP (new_scores or
+ * new_lengths is the old buffer).  The move's waits for one another's reads
+ * are bounded (LC_ERR_TIMEOUT in the error word; rows are then left unmoved). */
 int lc_cache_evict(const lc_paged_cache *cache, const lc_cache_eviction *eviction, lc_stream_t stream);
 
 #ifdef __cplusplus

@@ -124,7 +124,8 @@ class CCacheEviction(ctypes.Structure):
                 ("budget", ctypes.c_int32), ("recent", ctypes.c_int32),
                 ("kept", ctypes.c_void_p), ("kept_stride", ctypes.c_int64 * 2),
                 ("new_scores", ctypes.c_void_p), ("new_scores_stride", ctypes.c_int64 * 2),
-                ("new_lengths", ctypes.c_void_p)]
+                ("new_lengths", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
 
 
 _P_LAYOUT = ctypes.POINTER(CTileLayout)
@@ -181,6 +182,7 @@ PROTOTYPES = {
     "lc_cache_attend": (ctypes.c_int, [ctypes.POINTER(CPagedCache), ctypes.c_void_p, ctypes.c_void_p]),
     "lc_cache_attend_workspace": (ctypes.c_int64, [ctypes.POINTER(CPagedCache), ctypes.c_int32, ctypes.c_int32]),
     "lc_cache_evict": (ctypes.c_int, [ctypes.POINTER(CPagedCache), ctypes.c_void_p, ctypes.c_void_p]),
+    "lc_cache_evict_workspace": (ctypes.c_int64, [ctypes.POINTER(CPagedCache), ctypes.c_int32]),
     "lc_row_major_strides": (ctypes.c_int, [ctypes.c_int32, _P_I64, _P_I64]),
     "lc_layout_footprint": (ctypes.c_int64, [_P_LAYOUT, ctypes.c_int64]),
     "lc_status_string": (ctypes.c_char_p, [ctypes.c_int32]),

@@ -18,7 +18,7 @@ __all__ = ["PagedCache", "cache_append", "cache_attend", "cache_attend_workspace
 
 _I64_3 = ctypes.c_int64 * 3
 _QUERY = struct.Struct("@PPiiqqqqPPqifPqPqqPq")     # lc_cache_query
-_EVICTION = struct.Struct("@PPqqiiPqqPqqP")          # lc_cache_eviction
+_EVICTION = struct.Struct("@PPqqiiPqqPqqPPq")        # lc_cache_eviction
 _TYPES = None  # torch dtype -> lc_cache_type
 
 
@@ -133,6 +133,13 @@ class PagedCache:
                 raise ValueError("a cache of %d key heads cannot take %d query heads (or is itself refused)"
                                  % (self.n_kv_heads, n_q_heads))
             self._workspace_bytes[key] = n
+        return n
+
+    def evict_workspace_bytes(self, budget: int) -> int:
+        n = self._workspace_bytes.get(budget)
+        if n is None:  # (0 for a refused budget: the call says why)
+            n = max(0, int(_lib.lib().lc_cache_evict_workspace(self._ref, budget)))
+            self._workspace_bytes[budget] = n
         return n
 
 
@@ -286,8 +293,10 @@ def _evict(cache, lengths, scores, budget, recent, new_scores, kept, new_lengths
         new_scores = torch.empty(scores.shape, dtype=torch.float32, device=cache.device)
     if new_lengths is None:
         new_lengths = torch.empty(lengths.shape, dtype=torch.int32, device=cache.device)
+    ws_bytes = cache.evict_workspace_bytes(budget)
+    workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=cache.device)
     ss, ks, ns = scores.stride(), kept.stride(), new_scores.stride()
     a = _EVICTION.pack(lengths.data_ptr(), scores.data_ptr(), ss[0], ss[1], budget, recent, kept.data_ptr(), ks[0],
-                       ks[1], new_scores.data_ptr(), ns[0], ns[1], new_lengths.data_ptr())
+                       ks[1], new_scores.data_ptr(), ns[0], ns[1], new_lengths.data_ptr(), workspace.data_ptr(), ws_bytes)
     _check(_lib.lib().lc_cache_evict(cache._ref, a, handle), "cache_evict")
     return kept, new_scores, new_lengths

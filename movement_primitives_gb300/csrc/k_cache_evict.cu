@@ -1,25 +1,43 @@
 // Eviction from a paged key-value cache by accumulated weight (lc_cache_evict).
 //
-// Per sequence and key head, of n > budget slots: the `recent` newest stay,
-// and of the others the budget - recent of largest score, equal scores in
-// slot order.  k_evict_select finds the score of the last one kept by radix
-// selection, 8 bits of an order-preserving 32-bit key at a time, and writes
-// the kept slots in ascending order (`kept`) with their scores;
-// k_evict_move moves the rows.
+// Per sequence and key head (a unit), of n > budget slots: the `recent`
+// newest stay, and of the others the budget - recent of largest score, equal
+// scores in slot order.
 //
-// Rows move in place: the r-th kept slot goes to slot r, and kept[r] >= r, so
-// a destination r never holds a row that a later rank j > r has yet to read
-// (kept[j] >= j > r).  Reading a run of ranks, a barrier, writing it, and
-// going on to the next run is therefore enough, and the columns of a row are
-// independent of one another: a row's words are split over several blocks.
+// k_evict_select, a block or a cluster of blocks a unit, finds the score of the last slot
+// kept by radix selection on an order-preserving 32-bit key (digits of 11,
+// 11 and 10 bits from the top: with the exponent and two fraction bits in
+// the first, weights fall in many bins and shared-memory atomics seldom collide), then writes the
+// kept slots in ascending order (`kept`) with their scores.  The keys are read from memory once and kept
+// in shared memory; the blocks of a cluster take a run of slots each and add
+// up their histograms through distributed shared memory.
+//
+// k_evict_move moves the rows, 32 ranks (a chunk) a block at a time.  Rows
+// move in place: the r-th kept slot goes to slot r, and kept[r] >= r, so slot
+// r may still hold a row that a rank j < r has yet to read, never one of a later
+// rank.  A chunk therefore reads its rows into shared memory without
+// waiting, publishes that it has, and before writing waits for the chunks that hold the
+// ranks of the slots it writes over (at most two, which the selection
+// leaves in `rank_at`).  Chunks are handed out in order by an atomic
+// counter, and waits go to lower chunks only, whose reads wait for nothing:
+// no wait can be circular, whichever blocks run.  Memory bounds it: every row that moves
+// is read and written once.
+#include <cooperative_groups.h>
+
 #include "cache_common.cuh"
 
 namespace lc {
 
+namespace cg = cooperative_groups;
+
 constexpr int kSelThreads = 1024;
-constexpr int kSelPer = 4;  // slots a thread looks at in one round of the ordered pass
-constexpr int kMvThreads = 256;
-constexpr int kMvPer = 8;   // words a thread holds at a time
+constexpr int kSelBins = 2048;
+constexpr int kSelPer = 4;          // slots a thread looks at in one round of the ordered pass
+constexpr int kSelKeys = 48 * 1024; // keys a block holds in shared memory
+constexpr int kSelCluster = 8;      // blocks of a unit at most
+constexpr int kSelLeast = 4096;     // slots a block of a cluster has at least
+constexpr int kMvThreads = 128;
+constexpr int kMvRows = 32;         // ranks of a chunk
 
 struct EvictArgs {
     CacheArgs c;
@@ -29,8 +47,13 @@ struct EvictArgs {
     int32_t *kept, *new_lengths;
     int64_t sst[2], nst[2], kst[2];  // sequence, head
     int32_t budget, recent;
-    int32_t slices;      // blocks that share a row of one pool
-    int32_t row_words;   // words of a row
+    int32_t chunks;          // of a unit: ceil(budget / kMvRows)
+    int32_t key_words;       // keys that fit the selection's shared memory
+    uint64_t wait_ns;
+    // workspace
+    uint32_t *ticket;        // the next chunk
+    uint32_t *done;          // [unit][chunk]: its rows have been read
+    int32_t *rank_at;        // [unit][chunk + 1]: kept slots below slot kMvRows * chunk
 };
 
 // Larger scores have larger keys; NaN counts as -infinity, -0 as 0.
@@ -64,66 +87,120 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t *warp_sums, 
 }
 
 __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_constant__ EvictArgs a) {
-    __shared__ uint32_t hist[256], warp_sums[32], chosen[2];
+    extern __shared__ uint32_t keys[];
+    __shared__ uint32_t hist[2][kSelBins], warp_sums[32], chosen[2], counts[2];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int parts = cluster.num_blocks(), part = cluster.block_rank();
     const int t = threadIdx.x;
-    const int b = blockIdx.x / a.c.heads, h = blockIdx.x - b * a.c.heads;
+    const int unit = blockIdx.x / parts;
+    const int b = unit / a.c.heads, h = unit - b * a.c.heads;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int n = cache_length(a.c, a.lengths, b, kClassEvict);
     const int m = min(n, a.budget);
     const float *scores = a.scores + b * a.sst[0] + h * a.sst[1];
     float *out = a.new_scores + b * a.nst[0] + h * a.nst[1];
     int32_t *kept = a.kept + b * a.kst[0] + h * a.kst[1];
-    if (h == 0 && t == 0) a.new_lengths[b] = m;
-    for (int i = m + t; i < a.budget; i += kSelThreads) kept[i] = -1;
-    for (int i = m + t; i < a.c.cap; i += kSelThreads) out[i] = 0.f;
-    if (n == m) {
-        for (int i = t; i < m; i += kSelThreads) {
+    int32_t *rank_at = a.rank_at + int64_t(unit) * (a.chunks + 1);
+    // what needs no selection, dealt to the cluster's threads
+    const int all = parts * kSelThreads, at = part * kSelThreads + t;
+    if (h == 0 && at == 0) a.new_lengths[b] = m;
+    if (unit == 0 && at == 0) *a.ticket = 0;
+    for (int i = at; i < a.chunks; i += all) a.done[int64_t(unit) * a.chunks + i] = 0;
+    for (int i = m + at; i < a.budget; i += all) kept[i] = -1;
+    for (int i = m + at; i < a.c.cap; i += all) out[i] = 0.f;
+    if (n == m) {  // the same for the whole cluster
+        for (int i = at; i < m; i += all) {
             kept[i] = i;
             out[i] = scores[i];
         }
         return;
     }
-    // the key of the last slot kept among the first `cand`, and how many of
-    // the slots with that key stay
-    const int cand = n - a.recent;
+    for (int i = (n - 1) / kMvRows + 1 + at; i <= a.chunks; i += all) rank_at[i] = m;
+
+    // this block's slots [s0, s1), whole rounds of the ordered pass but for the last
+    const int round = kSelThreads * kSelPer;
+    const int rounds = (n - 1) / round + 1, each = (rounds + parts - 1) / parts;
+    const int s0 = static_cast<int>(lmin(int64_t(part) * each * round, n));
+    const int s1 = static_cast<int>(lmin(s0 + int64_t(each) * round, n));
+    const int cand = n - a.recent;  // slots below it compete
+    const bool held = s1 - s0 <= a.key_words;
+    auto key_of = [&](int i) { return held ? keys[i - s0] : score_key(scores[i]); };
+    if (held)
+        for (int i = s0 + t; i < s1; i += kSelThreads) keys[i - s0] = score_key(scores[i]);
+
+    // the key of the last slot kept among the competing, and how many with that key stay
     uint32_t need = a.budget - a.recent, prefix = 0;
-    if (need) {
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            if (t < 256) hist[t] = 0;
+    const bool any = need > 0;
+    if (any) {
+#pragma unroll 1
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+            uint32_t *mine = hist[pass & 1];  // the cluster may still read the other one
+            for (int i = t; i < kSelBins; i += kSelThreads) mine[i] = 0;
             __syncthreads();
-            for (int i = t; i < cand; i += kSelThreads) {
-                const uint32_t key = score_key(scores[i]);
-                if (shift == 24 || key >> (shift + 8) == prefix) atomicAdd(&hist[key >> shift & 255], 1u);
+            for (int i = s0 + t; i < min(s1, cand); i += kSelThreads) {
+                const uint32_t key = key_of(i);
+                if (pass == 0 || key >> (shift + bits) == prefix)
+                    atomicAdd(&mine[key >> shift & ((1u << bits) - 1)], 1u);
             }
-            __syncthreads();
-            // digits from the largest down: thread t stands for digit 255 - t
-            const uint32_t mine = t < 256 ? hist[255 - t] : 0;
+            cluster.sync();
+            // digits from the largest down: thread t stands for the two of bins - 1 - 2t and below
+            uint32_t two[2] = {0, 0};
+            const int top = kSelBins - 1 - 2 * t;
+            for (int r = 0; r < parts; ++r) {
+                const uint32_t *other = cluster.map_shared_rank(mine, r);
+                two[0] += other[top];
+                two[1] += other[top - 1];
+            }
             uint32_t total;
-            const uint32_t before = block_scan(mine, warp_sums, &total);
-            if (t < 256 && before < need && before + mine >= need) {
-                chosen[0] = 255 - t;
-                chosen[1] = need - before;
+            const uint32_t before = block_scan(two[0] + two[1], warp_sums, &total);
+            if (before < need && before + two[0] + two[1] >= need) {
+                const bool second = before + two[0] < need;
+                chosen[0] = top - second;
+                chosen[1] = need - before - (second ? two[0] : 0);
             }
             __syncthreads();
-            prefix = prefix << 8 | chosen[0];
+            prefix = prefix << bits | chosen[0];
             need = chosen[1];
-            __syncthreads();
         }
     }
     // slots in order: `sure` are kept whatever else, of the `tied` ones the first `need`
     uint32_t sure = 0, tied = 0;
-    const bool any = a.budget > a.recent;
-    for (int base = 0; base < n; base += kSelThreads * kSelPer) {
-        float s[kSelPer];
+    if (parts > 1) {  // counts of the blocks before
+        uint32_t count = 0, total;
+        uint32_t ties = 0;
+        for (int i = s0 + t; i < s1; i += kSelThreads) {
+            if (i >= cand) {
+                ++count;
+            } else if (any) {
+                const uint32_t key = key_of(i);
+                count += key > prefix;
+                ties += key == prefix;
+            }
+        }
+        block_scan(count, warp_sums, &total);
+        if (t == 0) counts[0] = total;
+        block_scan(ties, warp_sums, &total);
+        if (t == 0) counts[1] = total;
+        cluster.sync();
+        for (int r = 0; r < part; ++r) {
+            const uint32_t *other = cluster.map_shared_rank(counts, r);
+            sure += other[0];
+            tied += other[1];
+        }
+        cluster.sync();  // no block leaves while another reads its shared memory
+    }
+    for (int64_t from = s0; from < s1; from += round) {
+        const int base = static_cast<int>(from);
         uint32_t is[kSelPer], count = 0;  // 1: sure, 1 << 16: tied
 #pragma unroll
         for (int j = 0; j < kSelPer; ++j) {
             const int i = base + t * kSelPer + j;
-            s[j] = i < n ? scores[i] : 0.f;
             is[j] = 0;
             if (i >= cand)
-                is[j] = i < n;
-            else if (any) {
-                const uint32_t key = score_key(s[j]);
+                is[j] = i < s1;
+            else if (any && i < s1) {
+                const uint32_t key = key_of(i);
                 is[j] = key > prefix ? 1u : key == prefix ? 1u << 16 : 0u;
             }
             count += is[j];
@@ -133,10 +210,12 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
         uint32_t g = sure + (before & 0xffff), e = tied + (before >> 16);
 #pragma unroll
         for (int j = 0; j < kSelPer; ++j) {
+            const int i = base + t * kSelPer + j;
+            const uint32_t r = g + min(e, need);
+            if (i < s1 && i % kMvRows == 0 && i / kMvRows <= a.chunks) rank_at[i / kMvRows] = r;
             if (is[j] == 1 || (is[j] && e < need)) {
-                const uint32_t r = g + min(e, need);
-                kept[r] = base + t * kSelPer + j;
-                out[r] = s[j];
+                kept[r] = i;
+                out[r] = scores[i];
             }
             g += is[j] & 0xffff;
             e += is[j] >> 16;
@@ -146,83 +225,195 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
     }
 }
 
-// Blocks (unit, pool, slice): the words [w0, w1) of every row of the unit's
-// keys or values, or (E4M3, the last two of a unit) its scales.
-template <typename T>
-__device__ __forceinline__ void move_rows(const EvictArgs &a, T *pool, const int64_t *st, int64_t word_elems, int b,
-                                          int h, int w0, int w1) {
-    const CacheArgs &c = a.c;
-    const int32_t *kept = a.kept + b * a.kst[0] + h * a.kst[1];
-    const int words = w1 - w0;
-    const int64_t items = int64_t(a.budget) * words;
-    for (int64_t base = 0; base < items; base += kMvThreads * kMvPer) {
-        T x[kMvPer];
-        T *to[kMvPer];
-#pragma unroll
-        for (int j = 0; j < kMvPer; ++j) {
-            const int64_t i = base + j * kMvThreads + threadIdx.x;
-            to[j] = nullptr;
-            if (i >= items) continue;
-            const int r = static_cast<int>(i / words), w = w0 + static_cast<int>(i - int64_t(r) * words);
-            const int from = kept[r];
-            if (from == r) continue;
-            int row_f, row_t;
-            const int pf = cache_page(c, b, from, &row_f, kClassEvict), pt = cache_page(c, b, r, &row_t, kClassEvict);
-            if (pf < 0 || pt < 0) continue;
-            x[j] = pool[row_offset(st, pf, h, row_f) / word_elems + w];
-            to[j] = pool + row_offset(st, pt, h, row_t) / word_elems + w;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < kMvPer; ++j)
-            if (to[j]) *to[j] = x[j];
-    }
+__device__ __forceinline__ uint32_t load_acquire(const uint32_t *p) {
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void store_release(uint32_t *p, uint32_t v) {
+    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
-template <typename T, bool Q8>
-__global__ void __launch_bounds__(kMvThreads) k_evict_move(const __grid_constant__ EvictArgs a) {
+// VEC: rows are whole 16-byte words on 16-byte boundaries; else they move an element at a time.
+template <int EB, bool VEC>
+__global__ void __launch_bounds__(kMvThreads, 12) k_evict_move(const __grid_constant__ EvictArgs a) {
+    extern __shared__ __align__(16) uint8_t rows[];  // [pool][row][pitch]
+    __shared__ float scales[2][kMvRows];
+    __shared__ uint32_t next;
+    __shared__ int late;
     const CacheArgs &c = a.c;
-    const int roles = 2 * a.slices + (Q8 ? 2 : 0);
-    const int unit = blockIdx.x / roles, role = blockIdx.x - unit * roles;
-    const int b = unit / c.heads, h = unit - b * c.heads;
-    if (min(max(a.lengths[b], 0), c.cap) <= a.budget) return;
-    if (Q8 && role >= 2 * a.slices) {
-        const bool v = role & 1;
-        move_rows<float>(a, v ? c.vs : c.ks, v ? c.vss : c.kss, 1, b, h, 0, 1);
-        return;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int row_bytes = c.dim * EB, pitch = (row_bytes + 15) / 16 * 16;
+    const int units = c.n_seqs * c.heads;
+    const int64_t tickets = int64_t(units) * a.chunks;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (t == 0) next = atomicAdd(a.ticket, 1u);
+    __syncthreads();
+    int64_t ticket = next;
+    while (ticket < tickets) {
+        uint32_t coming = 0;
+        if (t == 0) coming = atomicAdd(a.ticket, 1u);
+        // the units' chunks in turn: the chunks in flight are of many units
+        const int chunk = static_cast<int>(ticket / units), unit = static_cast<int>(ticket - int64_t(chunk) * units);
+        const int b = unit / c.heads, h = unit - b * c.heads;
+        const int n = min(max(a.lengths[b], 0), c.cap);
+        if (n > a.budget) {
+            // each lane finds one row's places
+            const int r = chunk * kMvRows + lane;
+            int64_t from[2] = {-1, -1}, to[2] = {0, 0};
+            if (r < a.budget) {
+                const int src = a.kept[b * a.kst[0] + h * a.kst[1] + r];
+                if (src != r) {
+                    int row_f, row_t;
+                    const int pf = cache_page(c, b, src, &row_f, kClassEvict);
+                    const int pt = cache_page(c, b, r, &row_t, kClassEvict);
+                    if (pf >= 0 && pt >= 0) {
+                        from[0] = row_offset(c.kst, pf, h, row_f);
+                        from[1] = row_offset(c.vst, pf, h, row_f);
+                        to[0] = row_offset(c.kst, pt, h, row_t);
+                        to[1] = row_offset(c.vst, pt, h, row_t);
+                        if (EB == 1 && warp < 2)
+                            scales[warp][lane] = (warp ? c.vs : c.ks)[row_offset(warp ? c.vss : c.kss, pf, h, row_f)];
+                    }
+                }
+            }
+            const uint32_t moves = __ballot_sync(0xffffffffu, from[0] >= 0);
+            // rows warp, warp + 4, ... of both pools, 16 bytes a lane
+            const int words = VEC ? row_bytes / 16 : c.dim;
+            const int per_row = min(words, 32), rows_at = 32 / per_row;
+            const int my_row = lane / per_row, my_word = lane - my_row * per_row;
+            auto each = [&](auto &&move) {
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+                    for (int i = warp * rows_at; i < kMvRows; i += kMvThreads / 32 * rows_at) {
+                        const int row = i + my_row;
+                        const int64_t f = __shfl_sync(0xffffffffu, from[p], row & 31);
+                        const int64_t o = __shfl_sync(0xffffffffu, to[p], row & 31);
+                        if (my_row < rows_at && row < kMvRows && (moves >> row & 1))
+                            for (int w = my_word; w < words; w += per_row)
+                                move((p ? c.v : c.k), f, o, rows + (p * kMvRows + row) * pitch, w);
+                    }
+            };
+            each([&](const uint8_t *pool, int64_t f, int64_t, uint8_t *at, int w) {
+                if constexpr (VEC)
+                    ptx::cp_async16(ptx::smem_addr(at + 16 * w), pool + f * EB + 16 * w);
+                else if constexpr (EB == 2)
+                    reinterpret_cast<uint16_t *>(at)[w] = reinterpret_cast<const uint16_t *>(pool)[f + w];
+                else
+                    at[w] = pool[f + w];
+            });
+            ptx::cp_async_commit();
+            ptx::cp_async_wait<0>();
+            __syncthreads();  // all rows have been read
+            uint32_t *done = a.done + int64_t(unit) * a.chunks;
+            if (t == 0) {
+                store_release(done + chunk, 1);
+                // the chunks whose rows sit in the slots written next
+                const int32_t *rank = a.rank_at + int64_t(unit) * (a.chunks + 1) + chunk;
+                const int first = rank[0] / kMvRows, last = min((rank[1] - 1) / kMvRows, chunk - 1);
+                bool ok = true;
+                for (int k = first; k <= last && ok; ++k) {
+                    if (load_acquire(done + k)) continue;
+                    const uint64_t t0 = ptx::global_timer_ns();
+                    uint32_t polls = 0;
+                    while (!load_acquire(done + k)) {
+                        if (++polls >= ptx::kMaxPolls || ptx::global_timer_ns() - t0 > a.wait_ns) {
+                            report_error(LC_ERR_TIMEOUT, kClassEvict);
+                            ok = false;
+                            break;
+                        }
+                    }
+                }
+                late = !ok;
+            }
+            __syncthreads();
+            if (!late) {
+                each([&](uint8_t *pool, int64_t, int64_t o, const uint8_t *at, int w) {
+                    if constexpr (VEC)
+                        *reinterpret_cast<uint4 *>(pool + o * EB + 16 * w) = reinterpret_cast<const uint4 *>(at)[w];
+                    else if constexpr (EB == 2)
+                        reinterpret_cast<uint16_t *>(pool)[o + w] = reinterpret_cast<const uint16_t *>(at)[w];
+                    else
+                        pool[o + w] = at[w];
+                });
+                if (EB == 1 && warp < 2 && from[0] >= 0) {
+                    int row_t;
+                    const int pt = cache_page(c, b, r, &row_t, kClassEvict);
+                    (warp ? c.vs : c.ks)[row_offset(warp ? c.vss : c.kss, pt, h, row_t)] = scales[warp][lane];
+                }
+            }
+        }
+        if (t == 0) next = coming;
+        __syncthreads();  // rows are free again
+        ticket = next;
+        __syncthreads();
     }
-    const bool v = role >= a.slices;
-    const int s = role - (v ? a.slices : 0);
-    const int w0 = static_cast<int>(int64_t(a.row_words) * s / a.slices);
-    const int w1 = static_cast<int>(int64_t(a.row_words) * (s + 1) / a.slices);
-    move_rows<T>(a, reinterpret_cast<T *>(v ? c.v : c.k), v ? c.vst : c.kst, sizeof(T) / (Q8 ? 1 : 2), b, h, w0, w1);
 }
 
 cudaError_t take_error_evict(unsigned long long *v) { return take_module_error(v); }
 
 namespace {
 
-template <typename T, bool Q8>
-int launch_evict(EvictArgs &a, int eb, cudaStream_t cs) {
-    a.row_words = a.c.dim * eb / static_cast<int>(sizeof(T));
-    const void *fn = reinterpret_cast<const void *>(&k_evict_move<T, Q8>);
-    int sms, per;
-    if (prepare(fn, kMvThreads, 0, 0, &sms, &per) != cudaSuccess) return LC_ERR_CUDA;
-    // rows are split until the GPU is full, into parts of 64 bytes or more
+struct EvictSpace {
+    int64_t done, rank_at, end;
+};
+
+EvictSpace evict_space(const CacheArgs &c, int budget) {
+    const int64_t units = int64_t(c.n_seqs) * c.heads, chunks = (int64_t(budget) + kMvRows - 1) / kMvRows;
+    EvictSpace s;
+    s.done = 256;  // behind the ticket
+    s.rank_at = s.done + round256(units * chunks * 4);
+    s.end = s.rank_at + round256(units * (chunks + 1) * 4);
+    return s;
+}
+
+template <int EB, bool VEC>
+int launch_evict(EvictArgs &a, cudaStream_t cs) {
     const int64_t units = int64_t(a.c.n_seqs) * a.c.heads;
-    a.slices = 1;
-    while (2 * units * a.slices < int64_t(sms) * per && a.row_words * static_cast<int>(sizeof(T)) >= 128 * a.slices)
-        a.slices *= 2;
-    const int64_t blocks = units * (2 * a.slices + (Q8 ? 2 : 0));
-    if (blocks > 0x7fffffff) return LC_ERR_OVERFLOW;
-    k_evict_select<<<static_cast<unsigned>(units), kSelThreads, 0, cs>>>(a);
-    k_evict_move<T, Q8><<<static_cast<unsigned>(blocks), kMvThreads, 0, cs>>>(a);
-    return finish_launch();
+    int sms, per;
+    // Selection: clusters where there are few units and many slots
+    const void *sel = reinterpret_cast<const void *>(&k_evict_select);
+    const int smem_max = kSelKeys * 4;
+    if (prepare(sel, kSelThreads, 0, smem_max, &sms, &per) != cudaSuccess) return LC_ERR_CUDA;
+    int parts = 1;
+    while (parts < kSelCluster && units * parts * 2 <= 2 * sms && a.c.cap / (2 * parts) >= kSelLeast) parts *= 2;
+    const int round = kSelThreads * kSelPer, rounds = a.c.cap ? (a.c.cap - 1) / round + 1 : 0;
+    const int64_t hold = int64_t(rounds + parts - 1) / parts * round;
+    a.key_words = hold <= kSelKeys ? static_cast<int>(hold) : 0;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = parts;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(units * parts));
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = a.key_words * 4;
+    cfg.stream = cs;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    void *args[] = {&a};
+    if (cudaLaunchKernelExC(&cfg, sel, args) != cudaSuccess) return LC_ERR_CUDA;
+
+    const void *fn = reinterpret_cast<const void *>(&k_evict_move<EB, VEC>);
+    const int smem = 2 * kMvRows * ((a.c.dim * EB + 15) / 16 * 16);
+    if (prepare(fn, kMvThreads, smem, smem, &sms, &per) != cudaSuccess) return LC_ERR_CUDA;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(units * a.chunks, int64_t(sms) * per)));
+    cfg.blockDim = dim3(kMvThreads);
+    cfg.dynamicSmemBytes = smem;
+    return cudaLaunchKernelExC(&cfg, fn, args) == cudaSuccess ? LC_OK : LC_ERR_CUDA;
 }
 
 }  // namespace
 
 }  // namespace lc
+
+extern "C" int64_t lc_cache_evict_workspace(const lc_paged_cache *cache, int32_t budget) {
+    lc::CacheArgs c;
+    if (lc::check_cache(cache, true, &c) || budget < 1) return -1;
+    return lc::evict_space(c, budget).end;
+}
 
 extern "C" int lc_cache_evict(const lc_paged_cache *cache, const lc_cache_eviction *e, lc_stream_t stream) {
     using namespace lc;
@@ -246,7 +437,13 @@ extern "C" int lc_cache_evict(const lc_paged_cache *cache, const lc_cache_evicti
     if (st) return st;
     if (!rows_apart(2, ext, e->new_scores_stride, std::max(a.c.cap, 1)) || !rows_apart(2, ext, e->kept_stride, e->budget))
         return LC_ERR_NOT_INJECTIVE;
-    if (ext[0] * ext[1] > 0x7fffffff) return LC_ERR_OVERFLOW;
+    const int64_t units = ext[0] * ext[1], chunks = (int64_t(e->budget) + kMvRows - 1) / kMvRows;
+    // the tickets that running blocks draw past the last one stay in 32 bits too
+    if (units > 0x0fffffff || units * chunks > 0xf0000000ll) return LC_ERR_OVERFLOW;
+    const EvictSpace space = evict_space(a.c, e->budget);
+    if (!e->workspace) return LC_ERR_NULL;
+    if (space.end > e->workspace_bytes) return LC_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(e->workspace) % 256) return LC_ERR_ALIGN;
     a.lengths = e->lengths;
     a.scores = e->scores;
     a.new_scores = e->new_scores;
@@ -259,12 +456,17 @@ extern "C" int lc_cache_evict(const lc_paged_cache *cache, const lc_cache_evicti
     }
     a.budget = e->budget;
     a.recent = e->recent;
+    a.chunks = static_cast<int32_t>(chunks);
+    a.wait_ns = wait_limit_ns();
+    uint8_t *ws = static_cast<uint8_t *>(e->workspace);
+    a.ticket = reinterpret_cast<uint32_t *>(ws);
+    a.done = reinterpret_cast<uint32_t *>(ws + space.done);
+    a.rank_at = reinterpret_cast<int32_t *>(ws + space.rank_at);
     const int eb = cache_elem_bytes(cache->type);
     const int64_t pool[3] = {cache->n_pages, cache->n_kv_heads, cache->page_size};
-    const bool wide = a.c.dim * eb % 16 == 0 && rows_aligned(cache->k, 3, pool, cache->k_stride, eb, 16) &&
-                      rows_aligned(cache->v, 3, pool, cache->v_stride, eb, 16);
+    const bool vec = a.c.dim * eb % 16 == 0 && rows_aligned(cache->k, 3, pool, cache->k_stride, eb, 16) &&
+                     rows_aligned(cache->v, 3, pool, cache->v_stride, eb, 16);
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    if (cache->type == LC_CACHE_E4M3)
-        return wide ? launch_evict<uint4, true>(a, eb, cs) : launch_evict<uint8_t, true>(a, eb, cs);
-    return wide ? launch_evict<uint4, false>(a, eb, cs) : launch_evict<uint16_t, false>(a, eb, cs);
+    if (cache->type == LC_CACHE_E4M3) return vec ? launch_evict<1, true>(a, cs) : launch_evict<1, false>(a, cs);
+    return vec ? launch_evict<2, true>(a, cs) : launch_evict<2, false>(a, cs);
 }

@@ -248,6 +248,7 @@ def test_evict_refusals(M):
         e.scores_stride[:] = e.new_scores_stride[:] = (4 * 48, 48)
         e.kept_stride[:] = (4 * 8, 8)
         e.budget, e.recent = 8, 2
+        e.workspace, e.workspace_bytes = 16 * BASE, lib.lc_cache_evict_workspace(ctypes.byref(_cache(M)), 8)
         for k, x in kw.items():
             if isinstance(x, tuple):
                 getattr(e, k)[:] = x
@@ -261,3 +262,7 @@ def test_evict_refusals(M):
     assert call(new_scores=2 * BASE) == call(new_lengths=BASE) == "LC_ERR_OVERLAP"
     assert call(kept_stride=(32, 7)) == call(new_scores_stride=(48, 47)) == "LC_ERR_NOT_INJECTIVE"
     assert call(scores_stride=(-1, 48)) == "LC_ERR_BAD_STRIDE"
+    need = lib.lc_cache_evict_workspace(ctypes.byref(_cache(M)), 8)
+    assert need > 0 and lib.lc_cache_evict_workspace(ctypes.byref(_cache(M)), 0) == -1
+    assert call(workspace=None) == "LC_ERR_NULL" and call(workspace=BASE + 64) == "LC_ERR_ALIGN"
+    assert call(workspace_bytes=need - 1) == "LC_ERR_WORKSPACE"
