@@ -40,9 +40,8 @@ typedef enum {
     LC_CACHE_BF16 = 0,
     LC_CACHE_F16 = 1,
     /* E4M3 codes with one float32 scale a slot and head: the value is
-     * code * scale.  The codes 0x7f and 0xff (NaN) are not given a meaning;
-     * lc_cache_append marks a row that holds an infinity or NaN by a scale
-     * of NaN instead. */
+     * code * scale.  lc_cache_append marks a row that holds an infinity or
+     * NaN by a scale of NaN. */
     LC_CACHE_E4M3 = 2
 } lc_cache_type;
 

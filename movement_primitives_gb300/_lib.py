@@ -177,8 +177,8 @@ PROTOTYPES = {
                                              ctypes.POINTER(CSmemSwizzle), ctypes.c_void_p, ctypes.c_void_p,
                                              ctypes.c_void_p]),
     "lc_cache_append": (ctypes.c_int, [ctypes.POINTER(CPagedCache), ctypes.c_void_p, ctypes.c_void_p,
-                                       ctypes.c_int32, _P_I64, _P_I64, ctypes.c_int32, ctypes.c_void_p,
-                                       ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+                                       ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+                                       ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
     "lc_cache_attend": (ctypes.c_int, [ctypes.POINTER(CPagedCache), ctypes.c_void_p, ctypes.c_void_p]),
     "lc_cache_attend_workspace": (ctypes.c_int64, [ctypes.POINTER(CPagedCache), ctypes.c_int32, ctypes.c_int32]),
     "lc_cache_evict": (ctypes.c_int, [ctypes.POINTER(CPagedCache), ctypes.c_void_p, ctypes.c_void_p]),

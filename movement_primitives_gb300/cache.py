@@ -16,16 +16,18 @@ from . import _lib
 
 __all__ = ["PagedCache", "cache_append", "cache_attend", "cache_attend_workspace", "cache_evict"]
 
-_I64_3 = ctypes.c_int64 * 3
+_STRIDES = struct.Struct("@3q")                      # int64_t[3]
 _QUERY = struct.Struct("@PPiiqqqqPPqifPqPqqPq")     # lc_cache_query
 _EVICTION = struct.Struct("@PPqqiiPqqPqqPPq")        # lc_cache_eviction
 _TYPES = None  # torch dtype -> lc_cache_type
+_BYTES = None  # torch.uint8
 
 
 def _types():
-    global _TYPES
+    global _TYPES, _BYTES
     if _TYPES is None:
         import torch
+        _BYTES = torch.uint8
         _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
     return _TYPES
 
@@ -40,6 +42,17 @@ def _current(device) -> int:
     """Handle of the current stream (the raw query: torch.cuda.current_stream() builds an object, 3 us)."""
     import torch
     return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _allocator():
+    """``empty(shape, strides, dtype)`` on the current device and stream.  torch's direct binding where it has it:
+    torch.empty takes 3.5 us more a call, as long as one of the library's launches."""
+    import torch
+    direct = getattr(getattr(torch._C._dynamo, "guards", None), "_empty_strided_cuda", None) \
+        if hasattr(torch._C, "_dynamo") else None
+    if direct is not None:
+        return direct
+    return lambda shape, strides, dtype: torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
 
 
 class _on:
@@ -121,6 +134,7 @@ class PagedCache:
         self.n_seqs, self.pages_per_seq = page_table.shape
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
         self.capacity = self.page_size * self.pages_per_seq
+        self._empty = _allocator()
         self.scale = 1.0 / math.sqrt(self.head_dim)
         self.io_dtype = torch.bfloat16 if q8 else k.dtype
 
@@ -174,10 +188,10 @@ def cache_append(cache: PagedCache, k, v, lengths, counts=None, new_lengths=None
 
 def _append(cache, k, v, n_new, counts, lengths, new_lengths, handle):
     if new_lengths is None:
-        import torch
-        new_lengths = torch.empty(lengths.shape, dtype=torch.int32, device=cache.device)
+        new_lengths = cache._empty((cache.n_seqs,), (1,), lengths.dtype)
+    ks, vs = k.stride(), v.stride()
     _check(_lib.lib().lc_cache_append(cache._ref, k.data_ptr(), v.data_ptr(), _types()[k.dtype],
-                                      _I64_3(*k.stride()[:3]), _I64_3(*v.stride()[:3]), n_new,
+                                      _STRIDES.pack(ks[0], ks[1], ks[2]), _STRIDES.pack(vs[0], vs[1], vs[2]), n_new,
                                       None if counts is None else counts.data_ptr(), lengths.data_ptr(),
                                       new_lengths.data_ptr(), handle), "cache_append")
     return new_lengths
@@ -231,17 +245,16 @@ def cache_attend(cache: PagedCache, q, lengths, out=None, scale=None, window: in
 
 
 def _attend(cache, q, lengths, out, scale, window, mask, lse, scores, workspace, handle):
-    import torch
-    n_q = q.shape[1]
+    n_q, d = q.shape[1], cache.head_dim
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = cache._empty((cache.n_seqs, n_q, d), (n_q * d, d, 1), q.dtype)
     ws, ws_bytes = 0, 0
     if workspace is not None:
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     else:
         ws_bytes = cache.workspace_bytes(n_q, scores is not None)
         if ws_bytes:
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+            workspace = cache._empty((ws_bytes,), (1,), _BYTES)
             ws = workspace.data_ptr()
     qs, os = q.stride(), out.stride()
     ss = (0, 0, 0) if scores is None else scores.stride()
@@ -286,15 +299,16 @@ def cache_evict(cache: PagedCache, lengths, scores, budget: int, recent: int = 0
 
 
 def _evict(cache, lengths, scores, budget, recent, new_scores, kept, new_lengths, handle):
-    import torch
+    b, h, cap = scores.shape
     if kept is None:
-        kept = torch.empty((cache.n_seqs, cache.n_kv_heads, max(budget, 0)), dtype=torch.int32, device=cache.device)
+        n = max(budget, 0)
+        kept = cache._empty((b, h, n), (h * n, n, 1), lengths.dtype)
     if new_scores is None:
-        new_scores = torch.empty(scores.shape, dtype=torch.float32, device=cache.device)
+        new_scores = cache._empty((b, h, cap), (h * cap, cap, 1), scores.dtype)
     if new_lengths is None:
-        new_lengths = torch.empty(lengths.shape, dtype=torch.int32, device=cache.device)
+        new_lengths = cache._empty((b,), (1,), lengths.dtype)
     ws_bytes = cache.evict_workspace_bytes(budget)
-    workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=cache.device)
+    workspace = cache._empty((ws_bytes,), (1,), _BYTES)
     ss, ks, ns = scores.stride(), kept.stride(), new_scores.stride()
     a = _EVICTION.pack(lengths.data_ptr(), scores.data_ptr(), ss[0], ss[1], budget, recent, kept.data_ptr(), ks[0],
                        ks[1], new_scores.data_ptr(), ns[0], ns[1], new_lengths.data_ptr(), workspace.data_ptr(), ws_bytes)

@@ -21,6 +21,12 @@
 // second product (by at most 2^-9, or 2^-12 in float16, of each, no more
 // than the output's own rounding); the sum l takes them unrounded.
 //
+// E4M3 codes are float16 numbers, converted exactly two at a time; their products run in
+// float16.  The keys' scales multiply the logits.  The values' scales s_j
+// join the weights as 2^(x_j + log2 |s_j| - mv), mv the running maximum of
+// that exponent: the largest weight is 1 whatever the scales, so float16
+// holds the others to 2^-12 of themselves, or to 2^-25 of the largest; o is kept relative to mv.
+//
 // Work.  Slots are taken in steps of TOK by one warp.  A (sequence, key head,
 // block of 16 query heads) is a unit; the steps of all units, laid end to end, are cut
 // into equal runs, one a warp, whatever the lengths: the warps find their
@@ -45,8 +51,7 @@ constexpr int kAtThreads = 32 * kAtWarps;
 constexpr int kAtRows = 16;        // query heads of a unit at most
 constexpr int kAtMaxBlocks = 608;  // of the main kernel; sizes the workspace
 constexpr int kAtMaxRuns = kAtMaxBlocks * kAtWarps;
-constexpr int kJoinThreads = 256;
-constexpr int kJoinWide = 1024;
+constexpr int kJoinLeast = 128, kJoinMost = 1024;  // threads of a joining block
 constexpr int kScorePer = 4;       // slots of a thread
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -82,6 +87,18 @@ struct AttendArgs {
 
 inline int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
+#ifndef LC_AT_STEP
+#define LC_AT_STEP 8192
+#endif
+#ifndef LC_AT_ST
+#define LC_AT_ST 3
+#endif
+#ifndef LC_AT_ST4
+#define LC_AT_ST4 6
+#endif
+#ifndef LC_AT_MINB
+#define LC_AT_MINB 1
+#endif
 // Shapes of one instantiation.  DP: head_dim rounded up (64, 128, 256); KV: an
 // lc_cache_type; NG: query heads in eights (1, 2).  A step is 8 KiB where the shapes allow.
 template <int DP, int KV, int NG>
@@ -89,9 +106,9 @@ struct AtShape {
     static constexpr int EB = KV == LC_CACHE_E4M3 ? 1 : 2;
     static constexpr int RB = DP * EB;                       // bytes of a row
     static constexpr int CH = RB / 16;                       // its 16-byte chunks
-    static constexpr int TOK = 8192 / (2 * RB) >= 32 ? 32 : 16;
+    static constexpr int TOK = LC_AT_STEP / (2 * RB) >= 32 ? 32 : 16;
     static constexpr int STEP = 2 * TOK * RB;                // keys, then values
-    static constexpr int ST = STEP <= 4096 ? 6 : 3;          // steps in the ring
+    static constexpr int ST = STEP <= 4096 ? LC_AT_ST4 : LC_AT_ST;          // steps in the ring
     static constexpr int SC = KV == LC_CACHE_E4M3 ? 2 * TOK * 4 : 0;  // scales of a step
     static constexpr int WARP_BYTES = ST * (STEP + SC);
     static constexpr int OP = DP + 4;                        // floats between the heads of a warp's output
@@ -148,21 +165,21 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     }
 }
 
-// Four E4M3 codes (bytes 0..3 of r) as two bfloat16 pairs: even = (0, 2), odd = (1,
-// 3).  Sign and magnitude move to bfloat16's places (the same exponent
-// layout, three of its seven fraction bits), and one exact product by 2^120
-// makes up for the biases, 7 and 127.
-__device__ __forceinline__ void e4m3_pairs(uint32_t r, uint32_t &even, uint32_t &odd) {
-    const uint32_t e = (r & 0x00800080u) << 8 | (r & 0x007f007fu) << 4;
-    const uint32_t o = (r & 0x80008000u) | (r >> 4 & 0x07f007f0u);
-    const uint32_t k = 0x7b807b80u;  // 2^120 twice
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(even) : "r"(e), "r"(k));
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(odd) : "r"(o), "r"(k));
+// Two E4M3 codes (the low 16 bits) as float16, exactly.
+__device__ __forceinline__ uint32_t e4m3_halves(uint32_t codes) {
+    uint32_t v;
+    asm("{.reg .b16 c; cvt.u16.u32 c, %1; cvt.rn.f16x2.e4m3x2 %0, c;}" : "=r"(v) : "r"(codes));
+    return v;
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {  // 2 ulp, 0 for -infinity
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float log2_fast(float x) {  // -infinity for 0
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
@@ -200,6 +217,7 @@ template <int DP, int KV, int NG, bool VEC>
 struct Attend {
     using S = AtShape<DP, KV, NG>;
     static constexpr bool F16 = KV == LC_CACHE_F16, Q8 = KV == LC_CACHE_E4M3;
+    static constexpr bool M16 = F16 || Q8;       // the matrix instructions' type is float16
     static constexpr int KS = DP / 16;           // 16-wide pieces of a row
     static constexpr int MT = S::TOK / 16;       // 16-slot pieces of a step
 
@@ -214,6 +232,8 @@ struct Attend {
 
     uint32_t qb[KS][NG][2];
     float o[KS][NG][4], m[NG][2], l[NG][2];
+    float q_scale[NG][2];  // E4M3: what the float16 queries are to be multiplied by, times scale2
+    float mv[NG][2];       // E4M3: the running maximum of logit + log2 |value scale|, which o is relative to
 
     // the pages of a step's slots, one a lane, read one step ahead of its rows
     int next_page, next_row, next_head;
@@ -229,7 +249,7 @@ struct Attend {
     }
 
     // Query heads as the 16 x 8 operand: head lane / 4, columns k = 2q, 2q + 1, 2q + 8, 2q + 9 of each 16-wide
-    // piece; for E4M3 keys, which come four adjacent columns a lane, 4q, 4q + 2, 4q + 1, 4q + 3.
+    // piece; for E4M3 keys, which come four adjacent columns a lane, 4q .. 4q + 3.
     __device__ __forceinline__ void load_q() {
         const int q = lane & 3;
 #pragma unroll
@@ -239,28 +259,51 @@ struct Attend {
             const bool on = head < rows;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
+                const int c0 = 16 * ks + (Q8 ? 4 * q : 2 * q), c1 = c0 + (Q8 ? 2 : 8);
                 uint32_t x, y;
-                if (a.q_wide) {
-                    // whole fours of columns on 8-byte boundaries
+                if (a.q_wide) {  // whole fours of columns on 8-byte boundaries
                     if (Q8) {
-                        const int c = 16 * ks + 4 * q;
-                        const uint2 v = on && c < a.c.dim ? *reinterpret_cast<const uint2 *>(p + c) : make_uint2(0, 0);
-                        x = __byte_perm(v.x, v.y, 0x5410);
-                        y = __byte_perm(v.x, v.y, 0x7632);
+                        const uint2 v = on && c0 < a.c.dim ? *reinterpret_cast<const uint2 *>(p + c0) : make_uint2(0, 0);
+                        x = v.x;
+                        y = v.y;
                     } else {
-                        const int c = 16 * ks + 2 * q;
-                        x = on && c < a.c.dim ? *reinterpret_cast<const uint32_t *>(p + c) : 0;
-                        y = on && c + 8 < a.c.dim ? *reinterpret_cast<const uint32_t *>(p + c + 8) : 0;
+                        x = on && c0 < a.c.dim ? *reinterpret_cast<const uint32_t *>(p + c0) : 0;
+                        y = on && c1 < a.c.dim ? *reinterpret_cast<const uint32_t *>(p + c1) : 0;
                     }
                 } else {
-                    const int c = 16 * ks + (Q8 ? 4 * q : 2 * q);
-                    const int d1 = Q8 ? 2 : 1, e0 = Q8 ? 1 : 8, e1 = Q8 ? 3 : 9;
                     auto at = [&](int i) { return on && i < a.c.dim ? static_cast<uint32_t>(p[i]) : 0u; };
-                    x = at(c) | at(c + d1) << 16;
-                    y = at(c + e0) | at(c + e1) << 16;
+                    x = at(c0) | at(c0 + 1) << 16;
+                    y = at(c1) | at(c1 + 1) << 16;
                 }
                 qb[ks][g][0] = x;
                 qb[ks][g][1] = y;
+            }
+        }
+        if constexpr (Q8) {
+            // bfloat16 to float16, each head divided by the power of two at or below its largest magnitude: exact but for
+            // elements below 2^-14 of it, which are off by at most 2^-25 of it
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                uint32_t top = 0;
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        top = max(top, max(qb[ks][g][i] & 0x7fffu, qb[ks][g][i] >> 16 & 0x7fffu));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const uint32_t e = min(max(top >> 7, 1u), 253u);  // 1 / 2^(e - 127) is a normal number too
+                const float down = __uint_as_float((254 - e) << 23), up = __uint_as_float(e << 23);
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t v = qb[ks][g][i];
+                        qb[ks][g][i] = pack2<true>(__uint_as_float(v << 16) * down, __uint_as_float(v & 0xffff0000u) * down);
+                    }
+                // logits come by columns: heads 2 q, 2 q + 1
+#pragma unroll
+                for (int u = 0; u < 2; ++u) q_scale[g][u] = a.scale2 * __shfl_sync(0xffffffffu, up, (2 * q + u) * 4);
             }
         }
     }
@@ -343,7 +386,7 @@ struct Attend {
         for (int g = 0; g < NG; ++g)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                m[g][i] = -INFINITY;
+                m[g][i] = mv[g][i] = -INFINITY;
                 l[g][i] = 0.f;
             }
 #pragma unroll
@@ -371,14 +414,14 @@ struct Attend {
             if constexpr (Q8) {
 #pragma unroll
                 for (int ks = 0; ks < KS; ks += 2) {
-                    uint32_t r[4], e0, d0, e1, d1;
+                    uint32_t r[4];
                     ldsm_x4(r, ks_s + row * S::RB + swz(row, ks + (mat >> 1)));
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        e4m3_pairs(r[2 * i], e0, d0);
-                        e4m3_pairs(r[2 * i + 1], e1, d1);
+                        const uint32_t a0 = e4m3_halves(r[2 * i]), a2 = e4m3_halves(r[2 * i] >> 16);
+                        const uint32_t a1 = e4m3_halves(r[2 * i + 1]), a3 = e4m3_halves(r[2 * i + 1] >> 16);
 #pragma unroll
-                        for (int g = 0; g < NG; ++g) mma16816<false>(x[t][g], e0, e1, d0, d1, qb[ks + i][g]);
+                        for (int g = 0; g < NG; ++g) mma16816<true>(x[t][g], a0, a1, a2, a3, qb[ks + i][g]);
                     }
                 }
             } else {
@@ -393,13 +436,13 @@ struct Attend {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int col = 16 * t + slot + 8 * i;
-                const float f = Q8 ? a.scale2 * scales[col] : a.scale2;
+                const float f = Q8 ? scales[col] : 1.f;
                 const bool on = bits >> col & 1;
 #pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    x[t][g][2 * i] = on ? x[t][g][2 * i] * f : -INFINITY;
-                    x[t][g][2 * i + 1] = on ? x[t][g][2 * i + 1] * f : -INFINITY;
-                }
+                for (int g = 0; g < NG; ++g)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        x[t][g][2 * i + u] = on ? x[t][g][2 * i + u] * (Q8 ? q_scale[g][u] * f : a.scale2) : -INFINITY;
             }
         }
         if (a.logits) {
@@ -419,6 +462,22 @@ struct Attend {
             if (bits == 0) return;
         }
         // running maximum, sum and rescaling of the output
+        auto warp_max = [](float v) {
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+            return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+        };
+        // E4M3: the values' scales, whose logarithms join the logits for the second product
+        float sv[MT][2], lv[MT][2];
+        if constexpr (Q8) {
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    sv[t][i] = scales[S::TOK + 16 * t + slot + 8 * i];
+                    lv[t][i] = log2_fast(fabsf(sv[t][i]));
+                }
+        }
         bool grown = false;
         float keep[NG][2];
 #pragma unroll
@@ -428,25 +487,51 @@ struct Attend {
                 float top = fmaxf(x[0][g][u], x[0][g][2 + u]);
 #pragma unroll
                 for (int t = 1; t < MT; ++t) top = fmaxf(top, fmaxf(x[t][g][u], x[t][g][2 + u]));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                top = warp_max(top);
                 keep[g][u] = 1.f;
                 if (top > m[g][u]) {
-                    keep[g][u] = exp2_fast(m[g][u] - top);
+                    const float k = exp2_fast(m[g][u] - top);
                     m[g][u] = top;
-                    grown = true;
+                    l[g][u] *= k;
+                    if (!Q8) {
+                        keep[g][u] = k;
+                        grown = true;
+                    }
                 }
                 const float safe = m[g][u] == -INFINITY ? 0.f : m[g][u];
                 float sum = 0.f;
+                if constexpr (Q8) {
+                    float topv = -INFINITY;
 #pragma unroll
-                for (int t = 0; t < MT; ++t)
+                    for (int t = 0; t < MT; ++t)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        x[t][g][2 * i + u] = exp2_fast(x[t][g][2 * i + u] - safe);
-                        sum += x[t][g][2 * i + u];
+                        for (int i = 0; i < 2; ++i) {
+                            sum += exp2_fast(x[t][g][2 * i + u] - safe);
+                            x[t][g][2 * i + u] += lv[t][i];
+                            topv = fmaxf(topv, x[t][g][2 * i + u]);
+                        }
+                    topv = warp_max(topv);
+                    if (topv > mv[g][u]) {
+                        keep[g][u] = exp2_fast(mv[g][u] - topv);
+                        mv[g][u] = topv;
+                        grown = true;
                     }
-                l[g][u] = l[g][u] * keep[g][u] + sum;
+                    const float safe_v = mv[g][u] == -INFINITY ? 0.f : mv[g][u];
+#pragma unroll
+                    for (int t = 0; t < MT; ++t)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            x[t][g][2 * i + u] = copysignf(exp2_fast(x[t][g][2 * i + u] - safe_v), sv[t][i]);
+                } else {
+#pragma unroll
+                    for (int t = 0; t < MT; ++t)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            x[t][g][2 * i + u] = exp2_fast(x[t][g][2 * i + u] - safe);
+                            sum += x[t][g][2 * i + u];
+                        }
+                }
+                l[g][u] += sum;
             }
         if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
@@ -459,30 +544,30 @@ struct Attend {
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
             uint32_t p[NG][2];
-            const float s0 = Q8 ? scales[S::TOK + 16 * t + slot] : 1.f, s1 = Q8 ? scales[S::TOK + 16 * t + slot + 8] : 1.f;
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 // slots lane / 4 of two heads -> head lane / 4 of two slots
-                p[g][0] = transpose8(pack2<F16>(x[t][g][0] * s0, x[t][g][1] * s0));
-                p[g][1] = transpose8(pack2<F16>(x[t][g][2] * s1, x[t][g][3] * s1));
+                p[g][0] = transpose8(pack2<M16>(x[t][g][0], x[t][g][1]));
+                p[g][1] = transpose8(pack2<M16>(x[t][g][2], x[t][g][3]));
             }
-            const int row = 16 * t + (lane & 7) + (mat >> 1) * 8;
             if constexpr (Q8) {
-                // slots 0-7 and 8-15 of two 16-wide pieces
-                const int vrow = 16 * t + (lane & 7) + (mat & 1) * 8;
+                // slots 0-7 and 8-15 of two 16-wide pieces; a register holds two adjacent columns of two slots
+                const int row = 16 * t + (lane & 7) + (mat & 1) * 8;
 #pragma unroll
                 for (int c = 0; c < KS; c += 2) {
-                    uint32_t r[4], e0, d0, e1, d1;
-                    ldsm_x4_t(r, vs_s + vrow * S::RB + swz(vrow, c + (mat >> 1)));
+                    uint32_t r[4];
+                    ldsm_x4_t(r, vs_s + row * S::RB + swz(row, c + (mat >> 1)));
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        e4m3_pairs(r[2 * i], e0, d0);
-                        e4m3_pairs(r[2 * i + 1], e1, d1);
+                        const uint32_t lo = __byte_perm(r[2 * i], 0, 0x3120), hi = __byte_perm(r[2 * i + 1], 0, 0x3120);
+                        const uint32_t a0 = e4m3_halves(lo), a1 = e4m3_halves(lo >> 16);
+                        const uint32_t a2 = e4m3_halves(hi), a3 = e4m3_halves(hi >> 16);
 #pragma unroll
-                        for (int g = 0; g < NG; ++g) mma16816<false>(o[c + i][g], e0, d0, e1, d1, p[g]);
+                        for (int g = 0; g < NG; ++g) mma16816<true>(o[c + i][g], a0, a1, a2, a3, p[g]);
                     }
                 }
             } else {
+                const int row = 16 * t + (lane & 7) + (mat >> 1) * 8;
 #pragma unroll
                 for (int c = 0; c < KS; ++c) {
                     uint32_t r[4];
@@ -494,14 +579,23 @@ struct Attend {
         }
     }
 
-    // The lanes' sums become the warp's.
+    // The lanes' sums become the warp's; the output relative to m.
     __device__ __forceinline__ void total() {
 #pragma unroll
         for (int g = 0; g < NG; ++g)
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < 2; ++u) {
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) l[g][u] += __shfl_xor_sync(0xffffffffu, l[g][u], d);
+                if constexpr (Q8) {
+                    const float f = mv[g][u] == -INFINITY ? 0.f : exp2f(mv[g][u] - m[g][u]);
+#pragma unroll
+                    for (int c = 0; c < KS; ++c) {
+                        o[c][g][u] *= f;
+                        o[c][g][2 + u] *= f;
+                    }
+                }
+            }
     }
 
     // Writes the finished unit (slot < 0), or its part.
@@ -548,7 +642,7 @@ struct Attend {
 
 // One run a warp.
 template <int DP, int KV, int NG, bool VEC>
-__global__ void __launch_bounds__(kAtThreads) k_attend(const __grid_constant__ AttendArgs a) {
+__global__ void __launch_bounds__(kAtThreads, DP <= 128 && NG == 1 ? LC_AT_MINB : 1) k_attend(const __grid_constant__ AttendArgs a) {
     using A = Attend<DP, KV, NG, VEC>;
     using S = typename A::S;
     extern __shared__ __align__(128) uint8_t smem[];

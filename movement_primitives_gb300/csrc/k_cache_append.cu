@@ -6,9 +6,10 @@
 // in float32 (IEEE division, round to nearest even), NaN as the scale where
 // the largest magnitude is not finite.
 //
-// One warp moves one row of both pools: lanes 0-15 the keys', 16-31 the
-// values', each lane 16 bytes of new elements at a time.  Bound by memory:
-// every byte is read and written once.
+// One warp moves a token's rows of U heads in both pools: lanes 0-15 the
+// keys', 16-31 the values', each lane 16 bytes of new elements at a time, the
+// loads of all U heads before the first store.  Bound by memory: every byte
+// is read and written once.
 #include <cuda_fp8.h>
 
 #include "cache_common.cuh"
@@ -16,6 +17,7 @@
 namespace lc {
 
 constexpr int kApThreads = 256;
+constexpr int64_t kApMany = 4 * 152 * 48;  // rows from which a warp takes four heads
 
 struct AppendArgs {
     CacheArgs c;
@@ -24,13 +26,72 @@ struct AppendArgs {
     const int32_t *counts, *lengths;
     int32_t *new_lengths;
     int32_t n_new;
-    uint32_t rows;           // n_seqs * n_new * heads
+    uint32_t items;          // n_seqs * n_new * head_div.d: a warp each
     FastDiv new_div, head_div;
 };
 
-// Q: 0 rows as they are, 1 bf16 -> E4M3, 2 fp16 -> E4M3.  VEC: every row on
-// both sides starts on the boundary of eight elements and holds whole eights.
-template <int Q, bool VEC>
+// One row's 16 elements a lane, as they were read, to the pool: Q 0 unchanged, 1 bfloat16 -> E4M3, 2 float16 -> E4M3.
+// NI: eights of elements a lane (rows of up to 128 NI).  VEC: lane l holds eights l and l + 16, else elements l + 16 j.
+template <int Q, bool VEC, int NI>
+__device__ __forceinline__ void put_row(const CacheArgs &c, bool is_v, int page, int h, int row, bool on,
+                                        const uint16_t (&w)[8 * NI]) {
+    const int lane = threadIdx.x & 15;
+    const int64_t to = row_offset(is_v ? c.vst : c.kst, page, h, row);
+    uint8_t *dst = (is_v ? c.v : c.k) + (Q ? to : 2 * to);
+    if constexpr (Q == 0) {
+        if (!on) return;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            if constexpr (VEC) {
+                if (8 * (lane + 16 * i) < c.dim)
+                    *reinterpret_cast<uint4 *>(dst + 16 * (lane + 16 * i)) = reinterpret_cast<const uint4 *>(w)[i];
+            } else {
+#pragma unroll
+                for (int j = 8 * i; j < 8 * i + 8; ++j)
+                    if (lane + 16 * j < c.dim) reinterpret_cast<uint16_t *>(dst)[lane + 16 * j] = w[j];
+            }
+        }
+    } else {
+        float x[8 * NI];
+        float top = 0.f;
+        bool fine = true;
+#pragma unroll
+        for (int j = 0; j < 8 * NI; ++j) {
+            x[j] = Q == 1 ? __uint_as_float(static_cast<uint32_t>(w[j]) << 16) : __half2float(__ushort_as_half(w[j]));
+            top = fmaxf(top, fabsf(x[j]));
+            fine = fine && isfinite(x[j]);
+        }
+#pragma unroll
+        for (int o = 8; o; o >>= 1) {
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            fine = __shfl_xor_sync(0xffffffffu, static_cast<int>(fine), o) && fine;
+        }
+        const float scale = fine ? fmaxf(__fdiv_rn(top, 448.f), 1.17549435e-38f) : __int_as_float(0x7fc00000);
+        if (!on) return;
+        if (lane == 0) (is_v ? c.vs : c.ks)[row_offset(is_v ? c.vss : c.kss, page, h, row)] = scale;
+        uint32_t code[4 * NI];
+#pragma unroll
+        for (int j = 0; j < 4 * NI; ++j)
+            code[j] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x[2 * j], scale), __fdiv_rn(x[2 * j + 1], scale)),
+                                               __NV_SATFINITE, __NV_E4M3);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            if constexpr (VEC) {
+                if (8 * (lane + 16 * i) < c.dim)
+                    *reinterpret_cast<uint2 *>(dst + 8 * (lane + 16 * i)) =
+                        make_uint2(code[4 * i] | code[4 * i + 1] << 16, code[4 * i + 2] | code[4 * i + 3] << 16);
+            } else {
+#pragma unroll
+                for (int j = 8 * i; j < 8 * i + 8; ++j)
+                    if (lane + 16 * j < c.dim) dst[lane + 16 * j] = static_cast<uint8_t>(code[j / 2] >> (8 * (j & 1)));
+            }
+        }
+    }
+}
+
+// U: heads of a warp.  VEC: every row on both sides starts on the boundary of
+// eight elements and holds whole eights.
+template <int Q, bool VEC, int NI, int U>
 __global__ void __launch_bounds__(kApThreads) k_cache_append(const __grid_constant__ AppendArgs a) {
     const CacheArgs &c = a.c;
     const int64_t thread = int64_t(blockIdx.x) * kApThreads + threadIdx.x;
@@ -41,99 +102,69 @@ __global__ void __launch_bounds__(kApThreads) k_cache_append(const __grid_consta
         if ((a.counts && a.counts[at] != m) || m > c.cap - n) report_error(LC_ERR_CACHE_INDEX, kClassAppend);
         a.new_lengths[at] = n + min(m, c.cap - n);
     }
-    const uint32_t row_id = static_cast<uint32_t>(thread / 32);
-    if (row_id >= a.rows) return;
-    const uint32_t bt = fast_div(row_id, a.head_div);
-    const int h = static_cast<int>(row_id - bt * c.heads);
+    const uint32_t item = static_cast<uint32_t>(thread / 32);
+    if (item >= a.items) return;
+    const uint32_t bt = fast_div(item, a.head_div);
+    const int h0 = static_cast<int>(item - bt * a.head_div.d) * U;
     const int b = static_cast<int>(fast_div(bt, a.new_div));
     const int t = static_cast<int>(bt - static_cast<uint32_t>(b) * a.n_new);
     if (a.counts && t >= a.counts[b]) return;
     const int n = min(max(a.lengths[b], 0), c.cap);
     if (t >= c.cap - n) return;
-    int row;
-    const int page = cache_page(c, b, n + t, &row, kClassAppend);
-    if (page < 0) return;
 
     const int lane = threadIdx.x & 15;
     const bool is_v = threadIdx.x & 16;
-    const uint16_t *src = is_v ? a.v + b * a.vst[0] + t * a.vst[1] + h * a.vst[2]
-                               : a.k + b * a.kst[0] + t * a.kst[1] + h * a.kst[2];
-    const int64_t to = row_offset(is_v ? c.vst : c.kst, page, h, row);
-    uint8_t *dst = (is_v ? c.v : c.k) + (Q ? to : 2 * to);
-    if constexpr (Q == 0) {
-        if constexpr (VEC) {
-            for (int e = 8 * lane; e < c.dim; e += 128)
-                *reinterpret_cast<uint4 *>(dst + 2 * e) = *reinterpret_cast<const uint4 *>(src + e);
-        } else {
-            for (int e = lane; e < c.dim; e += 16) reinterpret_cast<uint16_t *>(dst)[e] = src[e];
-        }
-    } else {
-        // this lane's elements: eights 8 (lane + 16 i) (VEC), or lane + 16 j
-        float x[16];
-        float top = 0.f;
-        bool fine = true;
+    const int64_t head_stride = (is_v ? a.vst : a.kst)[2];
+    const uint16_t *src = is_v ? a.v + b * a.vst[0] + t * a.vst[1] + h0 * head_stride
+                               : a.k + b * a.kst[0] + t * a.kst[1] + h0 * head_stride;
+    __align__(16) uint16_t w[U][8 * NI];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            uint16_t w[8];
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const bool on = h0 + u < c.heads;
             if constexpr (VEC) {
                 uint4 q = make_uint4(0, 0, 0, 0);
-                if (8 * (lane + 16 * i) < c.dim) q = *reinterpret_cast<const uint4 *>(src + 8 * (lane + 16 * i));
-                *reinterpret_cast<uint4 *>(w) = q;
+                if (on && 8 * (lane + 16 * i) < c.dim)
+                    q = *reinterpret_cast<const uint4 *>(src + u * head_stride + 8 * (lane + 16 * i));
+                reinterpret_cast<uint4 *>(w[u])[i] = q;
             } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int e = lane + 16 * (8 * i + j);
-                    w[j] = e < c.dim ? src[e] : uint16_t(0);
+                for (int j = 8 * i; j < 8 * i + 8; ++j) {
+                    const int e = lane + 16 * j;
+                    w[u][j] = on && e < c.dim ? src[u * head_stride + e] : uint16_t(0);
                 }
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float f = Q == 1 ? __uint_as_float(static_cast<uint32_t>(w[j]) << 16)
-                                       : __half2float(__ushort_as_half(w[j]));
-                x[8 * i + j] = f;
-                top = fmaxf(top, fabsf(f));
-                fine = fine && isfinite(f);
-            }
         }
+    int row;
+    const int page = cache_page(c, b, n + t, &row, kClassAppend);
+    if (page < 0) return;
 #pragma unroll
-        for (int o = 8; o; o >>= 1) {
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            fine = __shfl_xor_sync(0xffffffffu, static_cast<int>(fine), o) && fine;
-        }
-        const float scale = fine ? fmaxf(__fdiv_rn(top, 448.f), 1.17549435e-38f) : __int_as_float(0x7fc00000);
-        if (lane == 0) (is_v ? c.vs : c.ks)[row_offset(is_v ? c.vss : c.kss, page, h, row)] = scale;
-        uint32_t code[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            code[j] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x[2 * j], scale), __fdiv_rn(x[2 * j + 1], scale)),
-                                               __NV_SATFINITE, __NV_E4M3);
-        if constexpr (VEC) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (8 * (lane + 16 * i) < c.dim)
-                    *reinterpret_cast<uint2 *>(dst + 8 * (lane + 16 * i)) =
-                        make_uint2(code[4 * i] | code[4 * i + 1] << 16, code[4 * i + 2] | code[4 * i + 3] << 16);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                if (lane + 16 * j < c.dim) dst[lane + 16 * j] = static_cast<uint8_t>(code[j / 2] >> (8 * (j & 1)));
-        }
-    }
+    for (int u = 0; u < U; ++u) put_row<Q, VEC, NI>(c, is_v, page, h0 + u, row, h0 + u < c.heads, w[u]);
 }
 
 cudaError_t take_error_append(unsigned long long *v) { return take_module_error(v); }
 
 namespace {
 
-template <int Q>
-int launch_append(const AppendArgs &a, bool vec, cudaStream_t cs) {
-    const uint64_t threads = std::max<uint64_t>(uint64_t(a.rows) * 32, a.c.n_seqs);
-    const unsigned grid = static_cast<unsigned>((threads + kApThreads - 1) / kApThreads);
-    if (vec)
-        k_cache_append<Q, true><<<grid, kApThreads, 0, cs>>>(a);
-    else
-        k_cache_append<Q, false><<<grid, kApThreads, 0, cs>>>(a);
+template <int Q, bool VEC, int NI, int U>
+int launch_append(AppendArgs &a, int64_t tokens, cudaStream_t cs) {
+    const int per = (a.c.heads + U - 1) / U;
+    a.items = static_cast<uint32_t>(tokens * per);
+    a.head_div = make_fastdiv(static_cast<uint32_t>(per));
+    const uint64_t threads = std::max<uint64_t>(uint64_t(a.items) * 32, a.c.n_seqs);
+    k_cache_append<Q, VEC, NI, U><<<static_cast<unsigned>((threads + kApThreads - 1) / kApThreads), kApThreads, 0, cs>>>(a);
     return finish_launch();
+}
+
+template <int Q>
+int launch_append_as(AppendArgs &a, int64_t tokens, bool vec, cudaStream_t cs) {
+    if (!vec) return launch_append<Q, false, 2, 1>(a, tokens, cs);
+    // four heads a warp once there are warps enough to fill the GPU with them
+    const bool many = tokens * a.c.heads >= kApMany;
+    if (a.c.dim <= 128)
+        return many ? launch_append<Q, true, 1, 4>(a, tokens, cs) : launch_append<Q, true, 1, 1>(a, tokens, cs);
+    return many ? launch_append<Q, true, 2, 4>(a, tokens, cs) : launch_append<Q, true, 2, 1>(a, tokens, cs);
 }
 
 }  // namespace
@@ -175,9 +206,7 @@ extern "C" int lc_cache_append(const lc_paged_cache *cache, const void *k_new, c
     a.lengths = lengths;
     a.new_lengths = new_lengths;
     a.n_new = n_new;
-    a.rows = static_cast<uint32_t>(rows);
     a.new_div = make_fastdiv(static_cast<uint32_t>(std::max(n_new, 1)));
-    a.head_div = make_fastdiv(static_cast<uint32_t>(cache->n_kv_heads));
     const int64_t pool[3] = {cache->n_pages, cache->n_kv_heads, cache->page_size};
     const int eb = cache_elem_bytes(cache->type);
     const bool vec = cache->head_dim % 8 == 0 && rows_aligned(k_new, 3, ext, k_stride, 2, 16) &&
@@ -185,6 +214,7 @@ extern "C" int lc_cache_append(const lc_paged_cache *cache, const void *k_new, c
                      rows_aligned(cache->k, 3, pool, cache->k_stride, eb, 8 * eb) &&
                      rows_aligned(cache->v, 3, pool, cache->v_stride, eb, 8 * eb);
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    if (!q8) return launch_append<0>(a, vec, cs);
-    return type == LC_CACHE_BF16 ? launch_append<1>(a, vec, cs) : launch_append<2>(a, vec, cs);
+    const int64_t tokens = ext[0] * n_new;
+    if (!q8) return launch_append_as<0>(a, tokens, vec, cs);
+    return type == LC_CACHE_BF16 ? launch_append_as<1>(a, tokens, vec, cs) : launch_append_as<2>(a, tokens, vec, cs);
 }

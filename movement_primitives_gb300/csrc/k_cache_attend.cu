@@ -33,9 +33,8 @@ __device__ __forceinline__ float2 join_ml(const AttendArgs &a, const Parts &p, i
 // scores), one a (sequence, key head, chunk of slots): scores += sum over the
 // group's query heads of 2^(logit - lse).
 template <bool F16>
-__global__ void __launch_bounds__(kJoinWide) k_attend_join(const __grid_constant__ AttendArgs a) {
-    __shared__ float acc[kJoinWide * 4];
-    __shared__ float2 row_ml;
+__global__ void __launch_bounds__(kJoinMost) k_attend_join(const __grid_constant__ AttendArgs a) {
+    extern __shared__ float acc[];  // four floats a thread
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, threads = blockDim.x;
     const int units = a.c.heads * a.row_blocks;
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -48,9 +47,9 @@ __global__ void __launch_bounds__(kJoinWide) k_attend_join(const __grid_constant
         const int i0 = chunk * threads * kScorePer;
         if (i0 >= n - lo) return;
         float w[kScorePer] = {};
-        for (int g0 = 0; g0 < a.group; g0 += kJoinWide) {
+        for (int g0 = 0; g0 < a.group; g0 += 4 * threads) {
             // the rows' log sums, a warp each
-            const int gn = min(a.group - g0, kJoinWide);
+            const int gn = min(a.group - g0, 4 * threads);
             __syncthreads();
             for (int g = warp; g < gn; g += threads / 32) {
                 const int rb = (g0 + g) / kAtRows;
@@ -66,12 +65,16 @@ __global__ void __launch_bounds__(kJoinWide) k_attend_join(const __grid_constant
             }
             __syncthreads();
             const float *x = a.logits + (int64_t(b) * a.q_heads + h * a.group + g0) * a.logit_stride + i0 + t;
+#pragma unroll 2
             for (int g = 0; g < gn; ++g) {
                 const float z = acc[g];
-                if (z == -INFINITY) continue;
+                float y[kScorePer];
 #pragma unroll
                 for (int k = 0; k < kScorePer; ++k)
-                    if (i0 + t + k * threads < n - lo) w[k] += exp2_fast(x[g * a.logit_stride + k * threads] - z);
+                    y[k] = i0 + t + k * threads < n - lo ? x[g * a.logit_stride + k * threads] : -INFINITY;
+                if (z != -INFINITY)
+#pragma unroll
+                    for (int k = 0; k < kScorePer; ++k) w[k] += exp2_fast(y[k] - z);
             }
         }
         float *to = a.scores + b * a.sst[0] + h * a.sst[1] + lo + i0 + t;
@@ -83,23 +86,19 @@ __global__ void __launch_bounds__(kJoinWide) k_attend_join(const __grid_constant
     const int b = blockIdx.x / a.q_heads, hq = blockIdx.x - b * a.q_heads;
     const int h = hq / a.group, rb = (hq - h * a.group) / kAtRows, row = (hq - h * a.group) % kAtRows;
     uint16_t *out = a.out + b * a.ost[0] + hq * a.ost[1];
+    const int2 split = a.split[int64_t(b) * units + h * a.row_blocks + rb];  // of no meaning for an empty sequence
     const int lo = seen_from(a, b, &n);
     if (lo >= n) {
         for (int i = t; i < a.c.dim; i += threads) out[i] = 0;
         if (t == 0 && a.lse) a.lse[b * a.lse_stride + hq] = -INFINITY;
         return;
     }
-    const int2 split = a.split[int64_t(b) * units + h * a.row_blocks + rb];
     if (split.x < 0) return;
     const Parts p{split.x, split.y - split.x + 1};
-    if (warp == 0) {
-        const float2 v = join_ml(a, p, row);
-        if (lane == 0) row_ml = v;
-    }
-    __syncthreads();
-    const float top = row_ml.x, safe = top == -INFINITY ? 0.f : top, total = row_ml.y;
     const int quads = a.part_pitch / 4, lanes = threads / quads;  // parts read at a time
     const int col = t % quads * 4, first = t / quads;
+    const float2 whole = join_ml(a, p, row);  // by every warp for itself
+    const float top = whole.x, safe = top == -INFINITY ? 0.f : top, total = whole.y;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int i = first; i < p.count; i += lanes) {
@@ -131,7 +130,7 @@ int launch_attend_e4m3(const AttendArgs &a, bool by_unit, bool vec, int *runs, c
 namespace {
 
 // Slots of a step: AtShape's TOK.
-int step_slots(int dim, int type) { return 8192 / (2 * padded_dim(dim) * cache_elem_bytes(type)) >= 32 ? 32 : 16; }
+int step_slots(int dim, int type) { return LC_AT_STEP / (2 * padded_dim(dim) * cache_elem_bytes(type)) >= 32 ? 32 : 16; }
 
 // How a call of these sizes goes: one block a unit, or runs; with runs, or with
 // scores, it needs a workspace of these offsets and this end.
@@ -165,13 +164,14 @@ bool attend_space(const lc_paged_cache &cache, const CacheArgs &c, int q_heads, 
 }
 
 // Launches a kernel that may start before the one ahead of it has ended (and waits for it itself).
-cudaError_t launch_after(const void *fn, unsigned grid, unsigned threads, cudaStream_t cs, void **args) {
+cudaError_t launch_after(const void *fn, unsigned grid, unsigned threads, unsigned smem, cudaStream_t cs, void **args) {
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = cs;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
@@ -217,7 +217,7 @@ extern "C" int lc_cache_attend(const lc_paged_cache *cache, const lc_cache_query
         (q->scores && !rows_apart(2, kext, q->scores_stride, std::max(a.c.cap, 1))))
         return LC_ERR_NOT_INJECTIVE;
     AttendSpace space;
-    const int64_t chunks = (int64_t(a.c.cap) + kJoinThreads * kScorePer - 1) / (kJoinThreads * kScorePer);
+    const int64_t chunks = (int64_t(a.c.cap) + kJoinLeast * kScorePer - 1) / (kJoinLeast * kScorePer);
     if (!attend_space(*cache, a.c, q->n_q_heads, q->scores != nullptr, &space) ||
         qext[0] * qext[1] > 0x3fffffff || (q->scores && chunks && kext[0] * kext[1] > 0x3fffffff / chunks))
         return LC_ERR_OVERFLOW;
@@ -259,13 +259,14 @@ extern "C" int lc_cache_attend(const lc_paged_cache *cache, const lc_cache_query
                                                       : launch_attend_e4m3;
     st = launch(a, space.by_unit, space.vec, &runs, cs);
     if (st || space.by_unit) return st;
-    // few units: many parts a row, which a wider block reads more of at a time
-    const int threads = runs >= 32 * (kext[0] * kext[1] * a.row_blocks) ? kJoinWide : kJoinThreads;
+    // blocks as wide as lets all rows run at once: few rows have many parts each, which a wide block reads more of at a time
+    int threads = kJoinMost;
+    while (threads > kJoinLeast && qext[0] * qext[1] * threads > 152 * 1024) threads /= 2;
     a.join_blocks = static_cast<int32_t>(qext[0] * qext[1]);
     a.score_chunks = a.scores ? (a.c.cap + threads * kScorePer - 1) / (threads * kScorePer) : 0;
     const int64_t blocks = a.join_blocks + kext[0] * kext[1] * a.score_chunks;
     void *args[] = {&a};
     const void *join = cache->type == LC_CACHE_F16 ? reinterpret_cast<const void *>(&k_attend_join<true>)
                                                    : reinterpret_cast<const void *>(&k_attend_join<false>);
-    return launch_after(join, static_cast<unsigned>(blocks), threads, cs, args) == cudaSuccess ? LC_OK : LC_ERR_CUDA;
+    return launch_after(join, static_cast<unsigned>(blocks), threads, threads * 16, cs, args) == cudaSuccess ? LC_OK : LC_ERR_CUDA;
 }

@@ -32,8 +32,10 @@ namespace cg = cooperative_groups;
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelBins = 2048;
+constexpr int kSelCopies = 4;       // of the first digit's histogram: lanes l, l + 4, ... share one
+constexpr int kSelCopy = kSelBins + 8;  // words of a copy: equal bins of two copies are in different banks
 constexpr int kSelPer = 4;          // slots a thread looks at in one round of the ordered pass
-constexpr int kSelKeys = 48 * 1024; // keys a block holds in shared memory
+constexpr int kSelKeys = 44 * 1024; // keys a block holds in shared memory
 constexpr int kSelCluster = 8;      // blocks of a unit at most
 constexpr int kSelLeast = 4096;     // slots a block of a cluster has at least
 constexpr int kMvThreads = 128;
@@ -88,7 +90,7 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t *warp_sums, 
 
 __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_constant__ EvictArgs a) {
     extern __shared__ uint32_t keys[];
-    __shared__ uint32_t hist[2][kSelBins], warp_sums[32], chosen[2], counts[2];
+    __shared__ uint32_t hist0[kSelCopies * kSelCopy], hist1[kSelBins], warp_sums[32], chosen[2], counts[2];
     cg::cluster_group cluster = cg::this_cluster();
     const int parts = cluster.num_blocks(), part = cluster.block_rank();
     const int t = threadIdx.x;
@@ -135,13 +137,24 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
 #pragma unroll 1
         for (int pass = 0; pass < 3; ++pass) {
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-            uint32_t *mine = hist[pass & 1];  // the cluster may still read the other one
-            for (int i = t; i < kSelBins; i += kSelThreads) mine[i] = 0;
+            uint32_t *mine = pass & 1 ? hist1 : hist0;  // the cluster may still read the other one
+            const int copies = pass == 0 ? kSelCopies : 1;
+            for (int i = t; i < (pass == 0 ? kSelCopies * kSelCopy : kSelBins); i += kSelThreads) mine[i] = 0;
             __syncthreads();
+            uint32_t *copy = mine + (t & (copies - 1)) * kSelCopy;
             for (int i = s0 + t; i < min(s1, cand); i += kSelThreads) {
                 const uint32_t key = key_of(i);
                 if (pass == 0 || key >> (shift + bits) == prefix)
-                    atomicAdd(&mine[key >> shift & ((1u << bits) - 1)], 1u);
+                    atomicAdd(&copy[key >> shift & ((1u << bits) - 1)], 1u);
+            }
+            if (pass == 0) {
+                __syncthreads();
+                for (int i = t; i < kSelBins; i += kSelThreads) {
+                    uint32_t sum = mine[i];
+#pragma unroll
+                    for (int k = 1; k < kSelCopies; ++k) sum += mine[k * kSelCopy + i];
+                    mine[i] = sum;
+                }
             }
             cluster.sync();
             // digits from the largest down: thread t stands for the two of bins - 1 - 2t and below
