@@ -4,13 +4,13 @@
 // newest stay, and of the others the budget - recent of largest score, equal
 // scores in slot order.
 //
-// k_evict_select, a block or a cluster of blocks a unit, finds the score of the last slot
-// kept by radix selection on an order-preserving 32-bit key (digits of 11,
-// 11 and 10 bits from the top: with the exponent and two fraction bits in
-// the first, weights fall in many bins and shared-memory atomics seldom collide), then writes the
-// kept slots in ascending order (`kept`) with their scores.  The keys are read from memory once and kept
-// in shared memory; the blocks of a cluster take a run of slots each and add
-// up their histograms through distributed shared memory.
+// k_evict_select, a block or a cluster of blocks a unit, finds the score of
+// the last slot kept by radix selection on an order-preserving 32-bit key
+// (digits of 11, 11 and 10 bits from the top, the first one's histogram made
+// as the scores come in), then writes the kept slots in ascending order
+// (`kept`) with their scores.  The scores are read from memory once and their
+// keys kept in shared memory; the blocks of a cluster take a run of slots
+// each and add up their histograms through distributed shared memory.
 //
 // k_evict_move moves the rows, 32 ranks (a chunk) a block at a time.  Rows
 // move in place: the r-th kept slot goes to slot r, and kept[r] >= r, so slot
@@ -30,12 +30,10 @@ namespace lc {
 
 namespace cg = cooperative_groups;
 
-constexpr int kSelThreads = 1024;
-constexpr int kSelBins = 2048;
-constexpr int kSelCopies = 4;       // of the first digit's histogram: lanes l, l + 4, ... share one
-constexpr int kSelCopy = kSelBins + 8;  // words of a copy: equal bins of two copies are in different banks
-constexpr int kSelPer = 4;          // slots a thread looks at in one round of the ordered pass
-constexpr int kSelKeys = 44 * 1024; // keys a block holds in shared memory
+constexpr int kSelThreads = 512;
+constexpr int kSelBins = 2048;      // four a thread
+constexpr int kSelRound = 4 * kSelThreads;  // slots of a round of the ordered pass, four a thread
+constexpr int kSelKeys = 48 * 1024; // keys a block holds in shared memory
 constexpr int kSelCluster = 8;      // blocks of a unit at most
 constexpr int kSelLeast = 4096;     // slots a block of a cluster has at least
 constexpr int kMvThreads = 128;
@@ -66,7 +64,9 @@ __device__ __forceinline__ uint32_t score_key(float s) {
 }
 
 // Exclusive scan of one value a thread over the block; `total` is the sum.
-__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t *warp_sums, uint32_t *total) {
+// One barrier: successive calls use different `sums`.
+__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t *sums, uint32_t *total) {
+    constexpr int kWarps = kSelThreads / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t s = x;
 #pragma unroll
@@ -74,23 +74,23 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t *warp_sums, 
         const uint32_t y = __shfl_up_sync(0xffffffffu, s, o);
         if (lane >= o) s += y;
     }
-    if (lane == 31) warp_sums[warp] = s;
+    if (lane == 31) sums[warp] = s;
     __syncthreads();
-    uint32_t w = warp_sums[lane];
+    uint32_t w = lane < kWarps ? sums[lane] : 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
+    for (int o = 1; o < kWarps; o <<= 1) {
         const uint32_t y = __shfl_up_sync(0xffffffffu, w, o);
         if (lane >= o) w += y;
     }
-    *total = __shfl_sync(0xffffffffu, w, 31);
+    *total = __shfl_sync(0xffffffffu, w, kWarps - 1);
     const uint32_t before = __shfl_sync(0xffffffffu, w, warp ? warp - 1 : 0);
-    __syncthreads();  // warp_sums is free again
     return (warp ? before : 0) + s - x;
 }
 
-__global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_constant__ EvictArgs a) {
-    extern __shared__ uint32_t keys[];
-    __shared__ uint32_t hist0[kSelCopies * kSelCopy], hist1[kSelBins], warp_sums[32], chosen[2], counts[2];
+__global__ void __launch_bounds__(kSelThreads, 2) k_evict_select(const __grid_constant__ EvictArgs a) {
+    extern __shared__ __align__(16) uint32_t keys[];
+    __shared__ __align__(16) uint32_t hist[2][kSelBins];
+    __shared__ uint32_t sums[2][32], chosen[3][2], counts[2];
     cg::cluster_group cluster = cg::this_cluster();
     const int parts = cluster.num_blocks(), part = cluster.block_rank();
     const int t = threadIdx.x;
@@ -120,81 +120,86 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
     for (int i = (n - 1) / kMvRows + 1 + at; i <= a.chunks; i += all) rank_at[i] = m;
 
     // this block's slots [s0, s1), whole rounds of the ordered pass but for the last
-    const int round = kSelThreads * kSelPer;
-    const int rounds = (n - 1) / round + 1, each = (rounds + parts - 1) / parts;
-    const int s0 = static_cast<int>(lmin(int64_t(part) * each * round, n));
-    const int s1 = static_cast<int>(lmin(s0 + int64_t(each) * round, n));
-    const int cand = n - a.recent;  // slots below it compete
+    const int rounds = (n - 1) / kSelRound + 1, each = (rounds + parts - 1) / parts;
+    const int s0 = static_cast<int>(lmin(int64_t(part) * each * kSelRound, n));
+    const int s1 = static_cast<int>(lmin(s0 + int64_t(each) * kSelRound, n));
+    const int cand = n - a.recent;       // slots below it compete
+    const int c1 = max(min(s1, cand), s0);  // this block's competing ones end there
     const bool held = s1 - s0 <= a.key_words;
     auto key_of = [&](int i) { return held ? keys[i - s0] : score_key(scores[i]); };
-    if (held)
-        for (int i = s0 + t; i < s1; i += kSelThreads) keys[i - s0] = score_key(scores[i]);
 
     // the key of the last slot kept among the competing, and how many with that key stay
     uint32_t need = a.budget - a.recent, prefix = 0;
     const bool any = need > 0;
+    for (int i = t; i < kSelBins; i += kSelThreads) hist[0][i] = 0;
+    if (t < 2) counts[t] = 0;
+    __syncthreads();
+    // the first digit's histogram as the keys come in
+#pragma unroll 8
+    for (int i = s0 + t; i < s1; i += kSelThreads) {
+        const uint32_t key = score_key(scores[i]);
+        if (held) keys[i - s0] = key;
+        if (any && i < c1) atomicAdd(&hist[0][key >> 21], 1u);
+    }
     if (any) {
 #pragma unroll 1
         for (int pass = 0; pass < 3; ++pass) {
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-            uint32_t *mine = pass & 1 ? hist1 : hist0;  // the cluster may still read the other one
-            const int copies = pass == 0 ? kSelCopies : 1;
-            for (int i = t; i < (pass == 0 ? kSelCopies * kSelCopy : kSelBins); i += kSelThreads) mine[i] = 0;
-            __syncthreads();
-            uint32_t *copy = mine + (t & (copies - 1)) * kSelCopy;
-            for (int i = s0 + t; i < min(s1, cand); i += kSelThreads) {
-                const uint32_t key = key_of(i);
-                if (pass == 0 || key >> (shift + bits) == prefix)
-                    atomicAdd(&copy[key >> shift & ((1u << bits) - 1)], 1u);
-            }
-            if (pass == 0) {
+            uint32_t *mine = hist[pass & 1];  // the cluster may still read the other one
+            if (pass) {
+                for (int i = t; i < kSelBins; i += kSelThreads) mine[i] = 0;
                 __syncthreads();
-                for (int i = t; i < kSelBins; i += kSelThreads) {
-                    uint32_t sum = mine[i];
-#pragma unroll
-                    for (int k = 1; k < kSelCopies; ++k) sum += mine[k * kSelCopy + i];
-                    mine[i] = sum;
+#pragma unroll 4
+                for (int i = s0 + t; i < c1; i += kSelThreads) {
+                    const uint32_t key = key_of(i);
+                    if (key >> (shift + bits) == prefix) atomicAdd(&mine[key >> shift & ((1u << bits) - 1)], 1u);
                 }
             }
             cluster.sync();
-            // digits from the largest down: thread t stands for the two of bins - 1 - 2t and below
-            uint32_t two[2] = {0, 0};
-            const int top = kSelBins - 1 - 2 * t;
+            // digits from the largest down: thread t stands for bins four - 4 t .. - 1
+            const int low = kSelBins - 4 * (t + 1);
+            uint32_t bin[4] = {};
             for (int r = 0; r < parts; ++r) {
-                const uint32_t *other = cluster.map_shared_rank(mine, r);
-                two[0] += other[top];
-                two[1] += other[top - 1];
+                const uint4 v = *reinterpret_cast<const uint4 *>(cluster.map_shared_rank(mine, r) + low);
+                bin[0] += v.w;
+                bin[1] += v.z;
+                bin[2] += v.y;
+                bin[3] += v.x;
             }
             uint32_t total;
-            const uint32_t before = block_scan(two[0] + two[1], warp_sums, &total);
-            if (before < need && before + two[0] + two[1] >= need) {
-                const bool second = before + two[0] < need;
-                chosen[0] = top - second;
-                chosen[1] = need - before - (second ? two[0] : 0);
+            uint32_t before = block_scan(bin[0] + bin[1] + bin[2] + bin[3], sums[pass & 1], &total);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (before < need && before + bin[k] >= need) {
+                    chosen[pass][0] = low + 3 - k;
+                    chosen[pass][1] = need - before;
+                }
+                before += bin[k];
             }
             __syncthreads();
-            prefix = prefix << bits | chosen[0];
-            need = chosen[1];
+            prefix = prefix << bits | chosen[pass][0];
+            need = chosen[pass][1];
         }
     }
     // slots in order: `sure` are kept whatever else, of the `tied` ones the first `need`
     uint32_t sure = 0, tied = 0;
     if (parts > 1) {  // counts of the blocks before
-        uint32_t count = 0, total;
-        uint32_t ties = 0;
-        for (int i = s0 + t; i < s1; i += kSelThreads) {
-            if (i >= cand) {
-                ++count;
-            } else if (any) {
+        uint32_t count = 0, ties = 0;
+        if (any)
+#pragma unroll 4
+            for (int i = s0 + t; i < c1; i += kSelThreads) {
                 const uint32_t key = key_of(i);
                 count += key > prefix;
                 ties += key == prefix;
             }
+        count = __reduce_add_sync(0xffffffffu, count);
+        ties = __reduce_add_sync(0xffffffffu, ties);
+        if ((t & 31) == 0) {
+            atomicAdd(&counts[0], count);
+            atomicAdd(&counts[1], ties);
         }
-        block_scan(count, warp_sums, &total);
-        if (t == 0) counts[0] = total;
-        block_scan(ties, warp_sums, &total);
-        if (t == 0) counts[1] = total;
+        __syncthreads();
+        if (t == 0) counts[0] += s1 - c1;  // the newest
         cluster.sync();
         for (int r = 0; r < part; ++r) {
             const uint32_t *other = cluster.map_shared_rank(counts, r);
@@ -202,33 +207,42 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
             tied += other[1];
         }
         cluster.sync();  // no block leaves while another reads its shared memory
+    } else {
+        __syncthreads();
     }
-    for (int64_t from = s0; from < s1; from += round) {
-        const int base = static_cast<int>(from);
-        uint32_t is[kSelPer], count = 0;  // 1: sure, 1 << 16: tied
+    int buffer = 0;
+    for (int64_t from = s0; from < s1; from += kSelRound, buffer ^= 1) {
+        const int i0 = static_cast<int>(from) + 4 * t;
+        uint32_t key[4], is[4], count = 0;  // 1: sure, 1 << 16: tied
+        if (held) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(keys + (i0 - s0));
+            key[0] = v.x;
+            key[1] = v.y;
+            key[2] = v.z;
+            key[3] = v.w;
+        } else {
 #pragma unroll
-        for (int j = 0; j < kSelPer; ++j) {
-            const int i = base + t * kSelPer + j;
-            is[j] = 0;
-            if (i >= cand)
-                is[j] = i < s1;
-            else if (any && i < s1) {
-                const uint32_t key = key_of(i);
-                is[j] = key > prefix ? 1u : key == prefix ? 1u << 16 : 0u;
-            }
+            for (int j = 0; j < 4; ++j) key[j] = i0 + j < s1 ? score_key(scores[i0 + j]) : 0;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = i0 + j;
+            is[j] = i >= s1 ? 0u : i >= cand ? 1u : !any ? 0u : key[j] > prefix ? 1u : key[j] == prefix ? 1u << 16 : 0u;
             count += is[j];
         }
         uint32_t total;
-        const uint32_t before = block_scan(count, warp_sums, &total);
+        const uint32_t before = block_scan(count, sums[buffer], &total);
         uint32_t g = sure + (before & 0xffff), e = tied + (before >> 16);
 #pragma unroll
-        for (int j = 0; j < kSelPer; ++j) {
-            const int i = base + t * kSelPer + j;
+        for (int j = 0; j < 4; ++j) {
+            const int i = i0 + j;
             const uint32_t r = g + min(e, need);
             if (i < s1 && i % kMvRows == 0 && i / kMvRows <= a.chunks) rank_at[i / kMvRows] = r;
             if (is[j] == 1 || (is[j] && e < need)) {
                 kept[r] = i;
-                out[r] = scores[i];
+                // the score back from its key, but for those that share one with another
+                const uint32_t u = key[j] >> 31 ? key[j] ^ 0x80000000u : ~key[j];
+                out[r] = u == 0 || u == 0xff800000u ? scores[i] : __uint_as_float(u);
             }
             g += is[j] & 0xffff;
             e += is[j] >> 16;
@@ -389,9 +403,9 @@ int launch_evict(EvictArgs &a, cudaStream_t cs) {
     const int smem_max = kSelKeys * 4;
     if (prepare(sel, kSelThreads, 0, smem_max, &sms, &per) != cudaSuccess) return LC_ERR_CUDA;
     int parts = 1;
-    while (parts < kSelCluster && units * parts * 2 <= 2 * sms && a.c.cap / (2 * parts) >= kSelLeast) parts *= 2;
-    const int round = kSelThreads * kSelPer, rounds = a.c.cap ? (a.c.cap - 1) / round + 1 : 0;
-    const int64_t hold = int64_t(rounds + parts - 1) / parts * round;
+    while (parts < kSelCluster && units * parts <= sms && a.c.cap / (2 * parts) >= kSelLeast) parts *= 2;
+    const int rounds = a.c.cap ? (a.c.cap - 1) / kSelRound + 1 : 0;
+    const int64_t hold = int64_t(rounds + parts - 1) / parts * kSelRound;
     a.key_words = hold <= kSelKeys ? static_cast<int>(hold) : 0;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
