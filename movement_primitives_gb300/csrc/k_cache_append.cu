@@ -3,8 +3,12 @@
 // Row (b, t, h) of the new keys and values goes to slot lengths[b] + t of
 // sequence b, as it is or quantised to E4M3:
 //     scale = max(max_e |x_e| / 448, 2^-126),  code_e = e4m3(x_e / scale)
-// in float32 (IEEE division, round to nearest even), NaN as the scale where
-// the largest magnitude is not finite.
+// in float32 (division and conversion round to nearest even), NaN as the
+// scale where the largest magnitude is not finite.  A row's quotients share
+// their divisor: with its rounded reciprocal r, q = x r and q + (x - q scale) r
+// in fused operations is the rounded quotient (Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990), three
+// operations for a division's many; scales far out of range divide.
 //
 // One warp moves a token's rows of U heads in both pools: lanes 0-15 the
 // keys', 16-31 the values', each lane 16 bytes of new elements at a time, the
@@ -30,6 +34,12 @@ struct AppendArgs {
     FastDiv new_div, head_div;
 };
 
+// A bfloat16 (Q 1) or float16 (Q 2) element.
+template <int Q>
+__device__ __forceinline__ float value_of(uint32_t w) {
+    return Q == 1 ? __uint_as_float(w << 16) : __half2float(__ushort_as_half(static_cast<uint16_t>(w)));
+}
+
 // One row's 16 elements a lane, as they were read, to the pool: Q 0 unchanged, 1 bfloat16 -> E4M3, 2 float16 -> E4M3.
 // NI: eights of elements a lane (rows of up to 128 NI).  VEC: lane l holds eights l and l + 16, else elements l + 16 j.
 template <int Q, bool VEC, int NI>
@@ -52,27 +62,29 @@ __device__ __forceinline__ void put_row(const CacheArgs &c, bool is_v, int page,
             }
         }
     } else {
-        float x[8 * NI];
-        float top = 0.f;
-        bool fine = true;
+        // the largest magnitude, by its bits: infinities and NaN are above every number
+        uint32_t top = 0;
 #pragma unroll
-        for (int j = 0; j < 8 * NI; ++j) {
-            x[j] = Q == 1 ? __uint_as_float(static_cast<uint32_t>(w[j]) << 16) : __half2float(__ushort_as_half(w[j]));
-            top = fmaxf(top, fabsf(x[j]));
-            fine = fine && isfinite(x[j]);
-        }
+        for (int j = 0; j < 4 * NI; ++j)
+            top = __vmaxu2(top, reinterpret_cast<const uint32_t *>(w)[j] & 0x7fff7fffu);
+        top = max(top & 0xffffu, top >> 16);
 #pragma unroll
-        for (int o = 8; o; o >>= 1) {
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            fine = __shfl_xor_sync(0xffffffffu, static_cast<int>(fine), o) && fine;
-        }
-        const float scale = fine ? fmaxf(__fdiv_rn(top, 448.f), 1.17549435e-38f) : __int_as_float(0x7fc00000);
+        for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const bool fine = top < (Q == 1 ? 0x7f80u : 0x7c00u);
+        const float scale = fine ? fmaxf(__fdiv_rn(value_of<Q>(top), 448.f), 1.17549435e-38f) : __int_as_float(0x7fc00000);
         if (!on) return;
         if (lane == 0) (is_v ? c.vs : c.ks)[row_offset(is_v ? c.vss : c.kss, page, h, row)] = scale;
+        const bool near = scale > 0x1p-100f && scale < 0x1p100f;
+        const float inverse = __frcp_rn(scale);
+        auto quotient = [&](float x) {
+            if (!near) return __fdiv_rn(x, scale);
+            const float q = x * inverse;
+            return q == 0.f ? q : fmaf(fmaf(-q, scale, x), inverse, q);  // (a zero keeps its sign)
+        };
         uint32_t code[4 * NI];
 #pragma unroll
         for (int j = 0; j < 4 * NI; ++j)
-            code[j] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x[2 * j], scale), __fdiv_rn(x[2 * j + 1], scale)),
+            code[j] = __nv_cvt_float2_to_fp8x2(make_float2(quotient(value_of<Q>(w[2 * j])), quotient(value_of<Q>(w[2 * j + 1]))),
                                                __NV_SATFINITE, __NV_E4M3);
 #pragma unroll
         for (int i = 0; i < NI; ++i) {

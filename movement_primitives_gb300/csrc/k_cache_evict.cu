@@ -30,14 +30,14 @@ namespace lc {
 
 namespace cg = cooperative_groups;
 
-constexpr int kSelThreads = 512;
-constexpr int kSelBins = 2048;      // four a thread
-constexpr int kSelRound = 4 * kSelThreads;  // slots of a round of the ordered pass, four a thread
+constexpr int kSelBins = 2048;      // 64 groups of 32
+constexpr int kSelRound = 2048;     // slots are dealt to blocks in so many
 constexpr int kSelKeys = 48 * 1024; // keys a block holds in shared memory
+constexpr int kSelAhead = 4;        // keys a lane has at hand in the ordered pass
 constexpr int kSelCluster = 8;      // blocks of a unit at most
 constexpr int kSelLeast = 4096;     // slots a block of a cluster has at least
-constexpr int kMvThreads = 128;
-constexpr int kMvRows = 32;         // ranks of a chunk
+constexpr int kMvThreads = 64;
+constexpr int kMvRows = 32;         // ranks of a chunk (the selection writes rank_at once every 32 slots)
 
 struct EvictArgs {
     CacheArgs c;
@@ -48,7 +48,6 @@ struct EvictArgs {
     int64_t sst[2], nst[2], kst[2];  // sequence, head
     int32_t budget, recent;
     int32_t chunks;          // of a unit: ceil(budget / kMvRows)
-    int32_t key_words;       // keys that fit the selection's shared memory
     uint64_t wait_ns;
     // workspace
     uint32_t *ticket;        // the next chunk
@@ -63,37 +62,32 @@ __device__ __forceinline__ uint32_t score_key(float s) {
     return u >> 31 ? ~u : u | 0x80000000u;
 }
 
-// Exclusive scan of one value a thread over the block; `total` is the sum.
-// One barrier: successive calls use different `sums`.
-__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t *sums, uint32_t *total) {
-    constexpr int kWarps = kSelThreads / 32;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint32_t s = x;
+// From the largest down: the one of 32 lanes' counts that holds the need-th, and how many of it are needed.
+__device__ __forceinline__ int pick(uint32_t count, uint32_t *need) {
+    const int lane = threadIdx.x & 31;
+    uint32_t upto = count;  // lanes lane .. 31
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += y;
+        const uint32_t y = __shfl_down_sync(0xffffffffu, upto, o);
+        if (lane + o < 32) upto += y;
     }
-    if (lane == 31) sums[warp] = s;
-    __syncthreads();
-    uint32_t w = lane < kWarps ? sums[lane] : 0;
-#pragma unroll
-    for (int o = 1; o < kWarps; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, w, o);
-        if (lane >= o) w += y;
-    }
-    *total = __shfl_sync(0xffffffffu, w, kWarps - 1);
-    const uint32_t before = __shfl_sync(0xffffffffu, w, warp ? warp - 1 : 0);
-    return (warp ? before : 0) + s - x;
+    const uint32_t above = upto - count;
+    const int at = __ffs(__ballot_sync(0xffffffffu, above < *need && upto >= *need)) - 1;
+    *need -= __shfl_sync(0xffffffffu, above, at);
+    return at;
 }
 
-__global__ void __launch_bounds__(kSelThreads, 2) k_evict_select(const __grid_constant__ EvictArgs a) {
-    extern __shared__ __align__(16) uint32_t keys[];
-    __shared__ __align__(16) uint32_t hist[2][kSelBins];
-    __shared__ uint32_t sums[2][32], chosen[3][2], counts[2];
+// HELD: the keys of a block's slots fit its shared memory; else every pass reads the scores again.
+// THREADS: 512, two blocks an SM, or 1024.
+template <bool HELD, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_evict_select(const __grid_constant__ EvictArgs a) {
+    constexpr int kWarps = THREADS / 32;
+    extern __shared__ uint32_t keys[];
+    __shared__ uint32_t hist[2][kSelBins], groups[2][64], chosen[3][2], counts[2];
+    __shared__ uint2 warp_counts[kWarps];
     cg::cluster_group cluster = cg::this_cluster();
     const int parts = cluster.num_blocks(), part = cluster.block_rank();
-    const int t = threadIdx.x;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int unit = blockIdx.x / parts;
     const int b = unit / a.c.heads, h = unit - b * a.c.heads;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -103,8 +97,14 @@ __global__ void __launch_bounds__(kSelThreads, 2) k_evict_select(const __grid_co
     float *out = a.new_scores + b * a.nst[0] + h * a.nst[1];
     int32_t *kept = a.kept + b * a.kst[0] + h * a.kst[1];
     int32_t *rank_at = a.rank_at + int64_t(unit) * (a.chunks + 1);
+    auto sync_all = [&] {
+        if (parts > 1)
+            cluster.sync();
+        else
+            __syncthreads();
+    };
     // what needs no selection, dealt to the cluster's threads
-    const int all = parts * kSelThreads, at = part * kSelThreads + t;
+    const int all = parts * THREADS, at = part * THREADS + t;
     if (h == 0 && at == 0) a.new_lengths[b] = m;
     if (unit == 0 && at == 0) *a.ticket = 0;
     for (int i = at; i < a.chunks; i += all) a.done[int64_t(unit) * a.chunks + i] = 0;
@@ -119,137 +119,153 @@ __global__ void __launch_bounds__(kSelThreads, 2) k_evict_select(const __grid_co
     }
     for (int i = (n - 1) / kMvRows + 1 + at; i <= a.chunks; i += all) rank_at[i] = m;
 
-    // this block's slots [s0, s1), whole rounds of the ordered pass but for the last
-    const int rounds = (n - 1) / kSelRound + 1, each = (rounds + parts - 1) / parts;
+    // this block's slots [s0, s1), a run of `run` for each warp
+    const int rounds = (n - 1) / kSelRound + 1, each = (rounds + parts - 1) / parts, run = each * (kSelRound / kWarps);
     const int s0 = static_cast<int>(lmin(int64_t(part) * each * kSelRound, n));
     const int s1 = static_cast<int>(lmin(s0 + int64_t(each) * kSelRound, n));
-    const int cand = n - a.recent;       // slots below it compete
+    const int cand = n - a.recent;          // slots below it compete
     const int c1 = max(min(s1, cand), s0);  // this block's competing ones end there
-    const bool held = s1 - s0 <= a.key_words;
-    auto key_of = [&](int i) { return held ? keys[i - s0] : score_key(scores[i]); };
+    auto key_of = [&](int i) { return HELD ? keys[i - s0] : score_key(scores[i]); };
 
     // the key of the last slot kept among the competing, and how many with that key stay
     uint32_t need = a.budget - a.recent, prefix = 0;
     const bool any = need > 0;
-    for (int i = t; i < kSelBins; i += kSelThreads) hist[0][i] = 0;
-    if (t < 2) counts[t] = 0;
+    for (int i = t; i < kSelBins; i += THREADS) hist[0][i] = 0;
     __syncthreads();
     // the first digit's histogram as the keys come in
 #pragma unroll 8
-    for (int i = s0 + t; i < s1; i += kSelThreads) {
+    for (int i = s0 + t; i < s1; i += THREADS) {
         const uint32_t key = score_key(scores[i]);
-        if (held) keys[i - s0] = key;
+        if (HELD) keys[i - s0] = key;
         if (any && i < c1) atomicAdd(&hist[0][key >> 21], 1u);
     }
     if (any) {
-#pragma unroll 1
+#pragma unroll
         for (int pass = 0; pass < 3; ++pass) {
-            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+            constexpr int kShift[3] = {21, 10, 0}, kBits[3] = {11, 11, 10};
+            const int shift = kShift[pass], bits = kBits[pass];
             uint32_t *mine = hist[pass & 1];  // the cluster may still read the other one
             if (pass) {
-                for (int i = t; i < kSelBins; i += kSelThreads) mine[i] = 0;
+                for (int i = t; i < kSelBins; i += THREADS) mine[i] = 0;
                 __syncthreads();
-#pragma unroll 4
-                for (int i = s0 + t; i < c1; i += kSelThreads) {
+#pragma unroll 8
+                for (int i = s0 + t; i < c1; i += THREADS) {
                     const uint32_t key = key_of(i);
                     if (key >> (shift + bits) == prefix) atomicAdd(&mine[key >> shift & ((1u << bits) - 1)], 1u);
                 }
             }
-            cluster.sync();
-            // digits from the largest down: thread t stands for bins four - 4 t .. - 1
-            const int low = kSelBins - 4 * (t + 1);
-            uint32_t bin[4] = {};
-            for (int r = 0; r < parts; ++r) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(cluster.map_shared_rank(mine, r) + low);
-                bin[0] += v.w;
-                bin[1] += v.z;
-                bin[2] += v.y;
-                bin[3] += v.x;
+            __syncthreads();
+            // bins in 64 groups of 32: the cluster adds up the groups, then the bins of one
+            for (int g = warp; g < 64; g += kWarps) {
+                const uint32_t sum = __reduce_add_sync(0xffffffffu, mine[32 * g + lane]);
+                if (lane == 0) groups[pass & 1][g] = sum;
             }
-            uint32_t total;
-            uint32_t before = block_scan(bin[0] + bin[1] + bin[2] + bin[3], sums[pass & 1], &total);
+            sync_all();
+            if (warp == 0) {
+                uint32_t low = 0, high = 0, bin = 0, left = need;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (before < need && before + bin[k] >= need) {
-                    chosen[pass][0] = low + 3 - k;
-                    chosen[pass][1] = need - before;
+                for (int r = 0; r < kSelCluster; ++r)
+                    if (r < parts) {
+                        const uint32_t *other = parts > 1 ? cluster.map_shared_rank(groups[pass & 1], r) : groups[pass & 1];
+                        low += other[lane];
+                        high += other[32 + lane];
+                    }
+                const bool upper = __reduce_add_sync(0xffffffffu, high) >= left;
+                if (!upper) left -= __reduce_add_sync(0xffffffffu, high);
+                const int group = pick(upper ? high : low, &left) + (upper ? 32 : 0);
+#pragma unroll
+                for (int r = 0; r < kSelCluster; ++r)
+                    if (r < parts) bin += (parts > 1 ? cluster.map_shared_rank(mine, r) : mine)[32 * group + lane];
+                const int digit = 32 * group + pick(bin, &left);
+                if (lane == 0) {
+                    chosen[pass][0] = digit;
+                    chosen[pass][1] = left;
                 }
-                before += bin[k];
             }
             __syncthreads();
             prefix = prefix << bits | chosen[pass][0];
             need = chosen[pass][1];
         }
-    }
-    // slots in order: `sure` are kept whatever else, of the `tied` ones the first `need`
-    uint32_t sure = 0, tied = 0;
-    if (parts > 1) {  // counts of the blocks before
-        uint32_t count = 0, ties = 0;
-        if (any)
-#pragma unroll 4
-            for (int i = s0 + t; i < c1; i += kSelThreads) {
-                const uint32_t key = key_of(i);
-                count += key > prefix;
-                ties += key == prefix;
-            }
-        count = __reduce_add_sync(0xffffffffu, count);
-        ties = __reduce_add_sync(0xffffffffu, ties);
-        if ((t & 31) == 0) {
-            atomicAdd(&counts[0], count);
-            atomicAdd(&counts[1], ties);
-        }
-        __syncthreads();
-        if (t == 0) counts[0] += s1 - c1;  // the newest
-        cluster.sync();
-        for (int r = 0; r < part; ++r) {
-            const uint32_t *other = cluster.map_shared_rank(counts, r);
-            sure += other[0];
-            tied += other[1];
-        }
-        cluster.sync();  // no block leaves while another reads its shared memory
     } else {
         __syncthreads();
     }
-    int buffer = 0;
-    for (int64_t from = s0; from < s1; from += kSelRound, buffer ^= 1) {
-        const int i0 = static_cast<int>(from) + 4 * t;
-        uint32_t key[4], is[4], count = 0;  // 1: sure, 1 << 16: tied
-        if (held) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(keys + (i0 - s0));
-            key[0] = v.x;
-            key[1] = v.y;
-            key[2] = v.z;
-            key[3] = v.w;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) key[j] = i0 + j < s1 ? score_key(scores[i0 + j]) : 0;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int i = i0 + j;
-            is[j] = i >= s1 ? 0u : i >= cand ? 1u : !any ? 0u : key[j] > prefix ? 1u : key[j] == prefix ? 1u << 16 : 0u;
-            count += is[j];
-        }
-        uint32_t total;
-        const uint32_t before = block_scan(count, sums[buffer], &total);
-        uint32_t g = sure + (before & 0xffff), e = tied + (before >> 16);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int i = i0 + j;
-            const uint32_t r = g + min(e, need);
-            if (i < s1 && i % kMvRows == 0 && i / kMvRows <= a.chunks) rank_at[i / kMvRows] = r;
-            if (is[j] == 1 || (is[j] && e < need)) {
-                kept[r] = i;
-                // the score back from its key, but for those that share one with another
-                const uint32_t u = key[j] >> 31 ? key[j] ^ 0x80000000u : ~key[j];
-                out[r] = u == 0 || u == 0xff800000u ? scores[i] : __uint_as_float(u);
-            }
-            g += is[j] & 0xffff;
-            e += is[j] >> 16;
-        }
-        sure += total & 0xffff;
-        tied += total >> 16;
+    // Slots in order, 32 at a time: `sure` are kept whatever else, of the `tied` ones the first `need`.  Each warp counts
+    // its run's, then writes from the counts before it.
+    const int w0 = static_cast<int>(lmin(s0 + int64_t(warp) * run, s1)), w1 = static_cast<int>(lmin(w0 + int64_t(run), s1));
+    uint32_t sure = 0, tied = 0;
+#pragma unroll 4
+    for (int i = w0 + lane; i < w1; i += 32) {
+        const uint32_t key = key_of(i);
+        sure += i >= cand || (any && key > prefix);
+        tied += i < cand && any && key == prefix;
     }
+    sure = __reduce_add_sync(0xffffffffu, sure);
+    tied = __reduce_add_sync(0xffffffffu, tied);
+    if (lane == 0) warp_counts[warp] = make_uint2(sure, tied);
+    __syncthreads();
+    sure = tied = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        const uint2 v = warp_counts[w];
+        if (w < warp) {
+            sure += v.x;
+            tied += v.y;
+        }
+        if (t == 0 && parts > 1) {
+            counts[0] = (w ? counts[0] : 0) + v.x;
+            counts[1] = (w ? counts[1] : 0) + v.y;
+        }
+    }
+    if (parts > 1) {  // and the blocks before
+        cluster.sync();
+#pragma unroll
+        for (int r = 0; r < kSelCluster - 1; ++r)
+            if (r < part) {
+                const uint32_t *other = cluster.map_shared_rank(counts, r);
+                sure += other[0];
+                tied += other[1];
+            }
+    }
+    // whole steps of competing slots; where no key is tied and the kept ones are positive scores, whose
+    // keys stand for them, the ranks are those of the sure ones alone
+    const bool plain = any && prefix >= 0x80000000u;
+    for (int i0 = w0; i0 < w1; i0 += 32 * kSelAhead) {
+        uint32_t key[kSelAhead];
+#pragma unroll
+        for (int k = 0; k < kSelAhead; ++k) {
+            const int i = i0 + 32 * k + lane;
+            key[k] = i < w1 ? key_of(i) : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < kSelAhead; ++k) {
+            const int i = i0 + 32 * k + lane;
+            const uint32_t below = (1u << lane) - 1;
+            uint32_t is_tied = __ballot_sync(0xffffffffu, key[k] == prefix);
+            uint32_t r;
+            if (plain && is_tied == 0 && i0 + 32 * k + 32 <= c1) {
+                const bool stays = key[k] > prefix;
+                const uint32_t is_sure = __ballot_sync(0xffffffffu, stays);
+                r = sure + min(tied, need) + __popc(is_sure & below);
+                if (stays) kept[r] = i;
+                if (stays) out[r] = __uint_as_float(key[k] ^ 0x80000000u);
+                sure += __popc(is_sure);
+            } else {
+                const uint32_t is_sure = __ballot_sync(0xffffffffu, i < w1 && (i >= cand || (any && key[k] > prefix)));
+                is_tied = __ballot_sync(0xffffffffu, any && i < min(w1, cand) && key[k] == prefix);
+                const uint32_t e = tied + __popc(is_tied & below);
+                r = sure + __popc(is_sure & below) + min(e, need);
+                const bool stays = (is_sure >> lane & 1) || ((is_tied >> lane & 1) && e < need);
+                if (stays) {
+                    kept[r] = i;
+                    out[r] = scores[i];
+                }
+                sure += __popc(is_sure);
+                tied += __popc(is_tied);
+            }
+            if (lane == 0 && i < w1 && i / kMvRows <= a.chunks) rank_at[i / kMvRows] = r;
+        }
+    }
+    if (parts > 1) cluster.sync();  // no block leaves while another reads its shared memory
 }
 
 __device__ __forceinline__ uint32_t load_acquire(const uint32_t *p) {
@@ -263,7 +279,7 @@ __device__ __forceinline__ void store_release(uint32_t *p, uint32_t v) {
 
 // VEC: rows are whole 16-byte words on 16-byte boundaries; else they move an element at a time.
 template <int EB, bool VEC>
-__global__ void __launch_bounds__(kMvThreads, 12) k_evict_move(const __grid_constant__ EvictArgs a) {
+__global__ void __launch_bounds__(kMvThreads, 24) k_evict_move(const __grid_constant__ EvictArgs a) {
     extern __shared__ __align__(16) uint8_t rows[];  // [pool][row][pitch]
     __shared__ float scales[2][kMvRows];
     __shared__ uint32_t next;
@@ -305,7 +321,7 @@ __global__ void __launch_bounds__(kMvThreads, 12) k_evict_move(const __grid_cons
                 }
             }
             const uint32_t moves = __ballot_sync(0xffffffffu, from[0] >= 0);
-            // rows warp, warp + 4, ... of both pools, 16 bytes a lane
+            // the warps take the rows of both pools in turn, 16 bytes a lane
             const int words = VEC ? row_bytes / 16 : c.dim;
             const int per_row = min(words, 32), rows_at = 32 / per_row;
             const int my_row = lane / per_row, my_word = lane - my_row * per_row;
@@ -397,24 +413,31 @@ EvictSpace evict_space(const CacheArgs &c, int budget) {
 template <int EB, bool VEC>
 int launch_evict(EvictArgs &a, cudaStream_t cs) {
     const int64_t units = int64_t(a.c.n_seqs) * a.c.heads;
-    int sms, per;
+    const int smem = 2 * kMvRows * ((a.c.dim * EB + 15) / 16 * 16);
+    int sms, per, move_per;
     // Selection: clusters where there are few units and many slots
-    const void *sel = reinterpret_cast<const void *>(&k_evict_select);
-    const int smem_max = kSelKeys * 4;
-    if (prepare(sel, kSelThreads, 0, smem_max, &sms, &per) != cudaSuccess) return LC_ERR_CUDA;
     int parts = 1;
+    if (prepare(reinterpret_cast<const void *>(&k_evict_move<EB, VEC>), kMvThreads, smem, smem, &sms, &move_per) != cudaSuccess)
+        return LC_ERR_CUDA;
     while (parts < kSelCluster && units * parts <= sms && a.c.cap / (2 * parts) >= kSelLeast) parts *= 2;
     const int rounds = a.c.cap ? (a.c.cap - 1) / kSelRound + 1 : 0;
     const int64_t hold = int64_t(rounds + parts - 1) / parts * kSelRound;
-    a.key_words = hold <= kSelKeys ? static_cast<int>(hold) : 0;
+    const bool held = hold <= kSelKeys;
+    // a block an SM, with more than a few slots a thread: twice the warps
+    const int threads = units * parts <= sms && hold > 4096 ? 1024 : 512;
+    const void *sel = threads == 1024 ? (held ? reinterpret_cast<const void *>(&k_evict_select<true, 1024>)
+                                              : reinterpret_cast<const void *>(&k_evict_select<false, 1024>))
+                                      : (held ? reinterpret_cast<const void *>(&k_evict_select<true, 512>)
+                                              : reinterpret_cast<const void *>(&k_evict_select<false, 512>));
+    if (prepare(sel, threads, 0, kSelKeys * 4, &sms, &per) != cudaSuccess) return LC_ERR_CUDA;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = parts;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(units * parts));
-    cfg.blockDim = dim3(kSelThreads);
-    cfg.dynamicSmemBytes = a.key_words * 4;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = held ? static_cast<size_t>(hold) * 4 : 0;
     cfg.stream = cs;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
@@ -422,11 +445,9 @@ int launch_evict(EvictArgs &a, cudaStream_t cs) {
     if (cudaLaunchKernelExC(&cfg, sel, args) != cudaSuccess) return LC_ERR_CUDA;
 
     const void *fn = reinterpret_cast<const void *>(&k_evict_move<EB, VEC>);
-    const int smem = 2 * kMvRows * ((a.c.dim * EB + 15) / 16 * 16);
-    if (prepare(fn, kMvThreads, smem, smem, &sms, &per) != cudaSuccess) return LC_ERR_CUDA;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(units * a.chunks, int64_t(sms) * per)));
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(units * a.chunks, int64_t(sms) * move_per)));
     cfg.blockDim = dim3(kMvThreads);
     cfg.dynamicSmemBytes = smem;
     return cudaLaunchKernelExC(&cfg, fn, args) == cudaSuccess ? LC_OK : LC_ERR_CUDA;
