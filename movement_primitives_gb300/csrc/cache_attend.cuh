@@ -52,7 +52,9 @@ constexpr int kAtRows = 16;        // query heads of a unit at most
 constexpr int kAtMaxBlocks = 608;  // of the main kernel; sizes the workspace
 constexpr int kAtMaxRuns = kAtMaxBlocks * kAtWarps;
 constexpr int kJoinLeast = 128, kJoinMost = 1024;  // threads of a joining block
-constexpr int kScorePer = 4;       // slots of a thread
+constexpr int kJoinRows = kJoinLeast / 32;  // rows of a block of the least width
+constexpr int kJoinFew = 32;       // parts of a row that one warp joins
+constexpr int kScorePer = 8;       // slots of a thread
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // A run takes at least this many steps: shorter ones leave more parts to join than
@@ -82,7 +84,9 @@ struct AttendArgs {
     float *logits;        // [sequence, query head, logit_stride], base 2, from the first slot seen (with scores)
     int64_t logit_stride;
     int32_t part_rows, part_pitch;
-    int32_t join_blocks, score_chunks;  // of k_attend_join
+    // of k_attend_join
+    int32_t join_blocks, join_rows;
+    FastDiv chunk_div, head_div, q_div, group_div;
 };
 
 inline int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }

@@ -27,98 +27,149 @@ __device__ __forceinline__ float2 join_ml(const AttendArgs &a, const Parts &p, i
     return make_float2(top, sum);
 }
 
-// Blocks 0 .. join_blocks - 1, one a (sequence, query head): joins the parts of
-// a row whose unit was cut, in their order, several at a time, and writes
-// the zeros of sequences with nothing to see.  The blocks after them (with
-// scores), one a (sequence, key head, chunk of slots): scores += sum over the
-// group's query heads of 2^(logit - lse).
+// scores[b, h, j] += sum over the group's query heads of 2^(logit - lse), for one chunk of slots.
+__device__ __forceinline__ void add_scores(const AttendArgs &a, uint32_t at, float *lse) {
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, threads = blockDim.x;
+    const int units = a.c.heads * a.row_blocks;
+    const uint32_t unit = fast_div(at, a.chunk_div);
+    const int chunk = static_cast<int>(at - unit * a.chunk_div.d);
+    const int b = static_cast<int>(fast_div(unit, a.head_div)), h = static_cast<int>(unit) - b * a.c.heads;
+    int n;
+    const int lo = seen_from(a, b, &n);
+    const int i0 = chunk * threads * kScorePer;
+    if (i0 >= n - lo) return;
+    float w[kScorePer] = {};
+    for (int g0 = 0; g0 < a.group; g0 += threads) {
+        // the rows' log sums, a warp each
+        const int gn = min(a.group - g0, threads);
+        __syncthreads();
+        for (int g = warp; g < gn; g += threads / 32) {
+            const int rb = (g0 + g) / kAtRows;
+            const int2 split = a.split[int64_t(b) * units + h * a.row_blocks + rb];
+            float z;
+            if (split.x < 0) {
+                z = a.lse2[int64_t(b) * a.q_heads + h * a.group + g0 + g];
+            } else {
+                const float2 v = join_ml(a, Parts{split.x, split.y - split.x + 1}, g0 + g - rb * kAtRows);
+                z = v.y == 0.f ? -INFINITY : v.x + log2f(v.y);
+            }
+            if (lane == 0) lse[g] = z;
+        }
+        __syncthreads();
+        const float *x = a.logits + (int64_t(b) * a.q_heads + h * a.group + g0) * a.logit_stride + i0 + t;
+#pragma unroll 2
+        for (int g = 0; g < gn; ++g, x += a.logit_stride) {
+            const float z = lse[g];
+            float y[kScorePer];
+#pragma unroll
+            for (int k = 0; k < kScorePer; ++k) y[k] = i0 + t + k * threads < n - lo ? x[k * threads] : -INFINITY;
+            if (z != -INFINITY)
+#pragma unroll
+                for (int k = 0; k < kScorePer; ++k) w[k] += exp2_fast(y[k] - z);
+        }
+    }
+    float *to = a.scores + b * a.sst[0] + h * a.sst[1] + lo + i0 + t;
+#pragma unroll
+    for (int k = 0; k < kScorePer; ++k)
+        if (i0 + t + k * threads < n - lo) to[k * threads] += w[k];
+}
+
+// Blocks 0 .. join_blocks - 1 join the parts of the rows (sequence, query
+// head) whose units were cut, in their order, and write the zeros of
+// sequences with nothing to see.  Warp w takes row blockIdx + w join_blocks
+// (w < join_rows); a row of many parts is left for the whole block, several parts at
+// a time.  The blocks after them (with scores), one a (sequence, key head,
+// chunk of slots), add the weights.
 template <bool F16>
 __global__ void __launch_bounds__(kJoinMost) k_attend_join(const __grid_constant__ AttendArgs a) {
     extern __shared__ float acc[];  // four floats a thread
+    __shared__ int whole_block[kJoinRows];
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, threads = blockDim.x;
-    const int units = a.c.heads * a.row_blocks;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    int n;
     if (blockIdx.x >= a.join_blocks) {
-        const int at = blockIdx.x - a.join_blocks;
-        const int unit = at / a.score_chunks, chunk = at - unit * a.score_chunks;
-        const int b = unit / a.c.heads, h = unit - b * a.c.heads;
-        const int lo = seen_from(a, b, &n);
-        const int i0 = chunk * threads * kScorePer;
-        if (i0 >= n - lo) return;
-        float w[kScorePer] = {};
-        for (int g0 = 0; g0 < a.group; g0 += 4 * threads) {
-            // the rows' log sums, a warp each
-            const int gn = min(a.group - g0, 4 * threads);
-            __syncthreads();
-            for (int g = warp; g < gn; g += threads / 32) {
-                const int rb = (g0 + g) / kAtRows;
-                const int2 split = a.split[int64_t(b) * units + h * a.row_blocks + rb];
-                float z;
-                if (split.x < 0) {
-                    z = a.lse2[int64_t(b) * a.q_heads + h * a.group + g0 + g];
-                } else {
-                    const float2 v = join_ml(a, Parts{split.x, split.y - split.x + 1}, g0 + g - rb * kAtRows);
-                    z = v.y == 0.f ? -INFINITY : v.x + log2f(v.y);
-                }
-                if (lane == 0) acc[g] = z;
-            }
-            __syncthreads();
-            const float *x = a.logits + (int64_t(b) * a.q_heads + h * a.group + g0) * a.logit_stride + i0 + t;
-#pragma unroll 2
-            for (int g = 0; g < gn; ++g) {
-                const float z = acc[g];
-                float y[kScorePer];
-#pragma unroll
-                for (int k = 0; k < kScorePer; ++k)
-                    y[k] = i0 + t + k * threads < n - lo ? x[g * a.logit_stride + k * threads] : -INFINITY;
-                if (z != -INFINITY)
-#pragma unroll
-                    for (int k = 0; k < kScorePer; ++k) w[k] += exp2_fast(y[k] - z);
-            }
+        add_scores(a, blockIdx.x - a.join_blocks, acc);
+        return;
+    }
+    const int units = a.c.heads * a.row_blocks, quads = a.part_pitch / 4;
+    struct Row {
+        int b, hq, row;
+        Parts parts;  // count 0: nothing to join
+        int n, lo;
+    };
+    auto row_of = [&](int w) {
+        Row r{};
+        const uint32_t at = blockIdx.x + static_cast<uint32_t>(w) * a.join_blocks;
+        if (at >= static_cast<uint32_t>(a.c.n_seqs) * a.q_heads) {
+            r.n = 1;  // no such row
+            return r;
         }
-        float *to = a.scores + b * a.sst[0] + h * a.sst[1] + lo + i0 + t;
-#pragma unroll
-        for (int k = 0; k < kScorePer; ++k)
-            if (i0 + t + k * threads < n - lo) to[k * threads] += w[k];
-        return;
-    }
-    const int b = blockIdx.x / a.q_heads, hq = blockIdx.x - b * a.q_heads;
-    const int h = hq / a.group, rb = (hq - h * a.group) / kAtRows, row = (hq - h * a.group) % kAtRows;
-    uint16_t *out = a.out + b * a.ost[0] + hq * a.ost[1];
-    const int2 split = a.split[int64_t(b) * units + h * a.row_blocks + rb];  // of no meaning for an empty sequence
-    const int lo = seen_from(a, b, &n);
-    if (lo >= n) {
-        for (int i = t; i < a.c.dim; i += threads) out[i] = 0;
-        if (t == 0 && a.lse) a.lse[b * a.lse_stride + hq] = -INFINITY;
-        return;
-    }
-    if (split.x < 0) return;
-    const Parts p{split.x, split.y - split.x + 1};
-    const int quads = a.part_pitch / 4, lanes = threads / quads;  // parts read at a time
-    const int col = t % quads * 4, first = t / quads;
-    const float2 whole = join_ml(a, p, row);  // by every warp for itself
-    const float top = whole.x, safe = top == -INFINITY ? 0.f : top, total = whole.y;
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = first; i < p.count; i += lanes) {
-        const int64_t at = int64_t(p.slot(i)) * a.part_rows + row;
+        r.b = static_cast<int>(fast_div(at, a.q_div));
+        r.hq = static_cast<int>(at) - r.b * a.q_heads;
+        const int h = static_cast<int>(fast_div(r.hq, a.group_div)), g = r.hq - h * a.group;
+        r.row = g % kAtRows;
+        const int2 split = a.split[int64_t(r.b) * units + h * a.row_blocks + g / kAtRows];
+        r.lo = seen_from(a, r.b, &r.n);
+        if (r.lo < r.n && split.x >= 0) r.parts = Parts{split.x, split.y - split.x + 1};
+        return r;
+    };
+    auto part = [&](const Row &r, int i, int col, float safe, float4 &y) {
+        const int64_t at = int64_t(r.parts.slot(i)) * a.part_rows + r.row;
         const float f = exp2_fast(a.part_ml[at].x - safe);
         const float4 z = *reinterpret_cast<const float4 *>(a.part + at * a.part_pitch + col);
         y.x += z.x * f;
         y.y += z.y * f;
         y.z += z.z * f;
         y.w += z.w * f;
+    };
+    auto put = [&](const Row &r, int col, float x) {
+        if (col < a.c.dim) a.out[r.b * a.ost[0] + r.hq * a.ost[1] + col] = static_cast<uint16_t>(pack2<F16>(x, 0.f));
+    };
+    auto put_lse = [&](const Row &r, float2 v) {
+        if (a.lse) a.lse[r.b * a.lse_stride + r.hq] = v.y == 0.f ? -INFINITY : (v.x + log2f(v.y)) * kLn2;
+    };
+    if (warp < a.join_rows) {
+        const Row r = row_of(warp);
+        const bool many = r.parts.count > (a.join_rows > 1 ? kJoinFew : 0);
+        if (lane == 0) whole_block[warp] = many;
+        if (r.lo >= r.n) {
+            for (int i = lane; i < a.c.dim; i += 32) put(r, i, 0.f);
+            if (lane == 0) put_lse(r, make_float2(0.f, 0.f));
+        } else if (r.parts.count && !many) {
+            const float2 v = join_ml(a, r.parts, r.row);
+            const float safe = v.x == -INFINITY ? 0.f : v.x, f = v.y == 0.f ? 0.f : 1.f / v.y;
+            for (int col = 4 * lane; col < a.part_pitch; col += 128) {
+                float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                for (int i = 0; i < r.parts.count; ++i) part(r, i, col, safe, y);
+                put(r, col, y.x * f);
+                put(r, col + 1, y.y * f);
+                put(r, col + 2, y.z * f);
+                put(r, col + 3, y.w * f);
+            }
+            if (lane == 0) put_lse(r, v);
+        }
     }
-    *reinterpret_cast<float4 *>(acc + first * a.part_pitch + col) = y;
     __syncthreads();
-    const float f = total == 0.f ? 0.f : 1.f / total;
-    for (int i = t; i < a.c.dim; i += threads) {
-        float s = 0.f;
-        for (int k = 0; k < lanes; ++k) s += acc[k * a.part_pitch + i];
-        out[i] = static_cast<uint16_t>(pack2<F16>(s * f, 0.f));
+    const int lanes = threads / quads;  // parts read at a time
+    const int col = t % quads * 4, first = t / quads;
+    for (int w = 0; w < a.join_rows; ++w) {
+        if (!whole_block[w]) continue;
+        const Row r = row_of(w);
+        const float2 v = join_ml(a, r.parts, r.row);  // by every warp for itself
+        const float safe = v.x == -INFINITY ? 0.f : v.x, f = v.y == 0.f ? 0.f : 1.f / v.y;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int i = first; i < r.parts.count; i += lanes) part(r, i, col, safe, y);
+        __syncthreads();
+        *reinterpret_cast<float4 *>(acc + first * a.part_pitch + col) = y;
+        __syncthreads();
+        for (int i = t; i < a.c.dim; i += threads) {
+            float s = 0.f;
+            for (int k = 0; k < lanes; ++k) s += acc[k * a.part_pitch + i];
+            put(r, i, s * f);
+        }
+        if (t == 0) put_lse(r, v);
     }
-    if (t == 0 && a.lse) a.lse[b * a.lse_stride + hq] = total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
 }
 
 cudaError_t take_error_attend(unsigned long long *v) { return take_module_error(v); }
@@ -259,12 +310,19 @@ extern "C" int lc_cache_attend(const lc_paged_cache *cache, const lc_cache_query
                                                       : launch_attend_e4m3;
     st = launch(a, space.by_unit, space.vec, &runs, cs);
     if (st || space.by_unit) return st;
-    // blocks as wide as lets all rows run at once: few rows have many parts each, which a wide block reads more of at a time
+    // a row a block, as wide as lets all rows run at once: few rows have many parts each, which a wide block reads more
+    // of at a time; rows past that share blocks of the least width, a warp each
+    const int64_t rows = qext[0] * qext[1];
     int threads = kJoinMost;
-    while (threads > kJoinLeast && qext[0] * qext[1] * threads > 152 * 1024) threads /= 2;
-    a.join_blocks = static_cast<int32_t>(qext[0] * qext[1]);
-    a.score_chunks = a.scores ? (a.c.cap + threads * kScorePer - 1) / (threads * kScorePer) : 0;
-    const int64_t blocks = a.join_blocks + kext[0] * kext[1] * a.score_chunks;
+    while (threads > kJoinLeast && rows * threads > 152 * 1024) threads /= 2;
+    a.join_rows = rows * threads > 152 * 1024 ? kJoinRows : 1;
+    a.join_blocks = static_cast<int32_t>((rows + a.join_rows - 1) / a.join_rows);
+    const int chunks_of = a.scores ? (a.c.cap + threads * kScorePer - 1) / (threads * kScorePer) : 0;
+    a.chunk_div = make_fastdiv(static_cast<uint32_t>(std::max(chunks_of, 1)));
+    a.head_div = make_fastdiv(static_cast<uint32_t>(a.c.heads));
+    a.q_div = make_fastdiv(static_cast<uint32_t>(a.q_heads));
+    a.group_div = make_fastdiv(static_cast<uint32_t>(a.group));
+    const int64_t blocks = a.join_blocks + kext[0] * kext[1] * chunks_of;
     void *args[] = {&a};
     const void *join = cache->type == LC_CACHE_F16 ? reinterpret_cast<const void *>(&k_attend_join<true>)
                                                    : reinterpret_cast<const void *>(&k_attend_join<false>);
