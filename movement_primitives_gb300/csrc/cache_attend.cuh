@@ -48,6 +48,7 @@ namespace lc {
 
 constexpr int kAtWarps = 4;
 constexpr int kAtThreads = 32 * kAtWarps;
+constexpr int kAtBlocks = 2;       // of an SM
 constexpr int kAtRows = 16;        // query heads of a unit at most
 constexpr int kAtMaxBlocks = 608;  // of the main kernel; sizes the workspace
 constexpr int kAtMaxRuns = kAtMaxBlocks * kAtWarps;
@@ -86,22 +87,20 @@ struct AttendArgs {
     int32_t part_rows, part_pitch;
     // of k_attend_join
     int32_t join_blocks, join_rows;
+    uint32_t score_blocks;
     FastDiv chunk_div, head_div, q_div, group_div;
 };
 
 inline int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
-#ifndef LC_AT_STEP
-#define LC_AT_STEP 8192
+#ifndef LC_AT_ST8  // compile-time knobs so that variants can be measured
+#define LC_AT_ST8 2
 #endif
-#ifndef LC_AT_ST
-#define LC_AT_ST 3
+#ifndef LC_AT_ST16
+#define LC_AT_ST16 2
 #endif
 #ifndef LC_AT_ST4
-#define LC_AT_ST4 6
-#endif
-#ifndef LC_AT_MINB
-#define LC_AT_MINB 1
+#define LC_AT_ST4 3
 #endif
 // Shapes of one instantiation.  DP: head_dim rounded up (64, 128, 256); KV: an
 // lc_cache_type; NG: query heads in eights (1, 2).  A step is 8 KiB where the shapes allow.
@@ -110,9 +109,9 @@ struct AtShape {
     static constexpr int EB = KV == LC_CACHE_E4M3 ? 1 : 2;
     static constexpr int RB = DP * EB;                       // bytes of a row
     static constexpr int CH = RB / 16;                       // its 16-byte chunks
-    static constexpr int TOK = LC_AT_STEP / (2 * RB) >= 32 ? 32 : 16;
+    static constexpr int TOK = 8192 / (2 * RB) >= 32 ? 32 : 16;
     static constexpr int STEP = 2 * TOK * RB;                // keys, then values
-    static constexpr int ST = STEP <= 4096 ? LC_AT_ST4 : LC_AT_ST;          // steps in the ring
+    static constexpr int ST = STEP <= 4096 ? LC_AT_ST4 : STEP <= 8192 ? LC_AT_ST8 : LC_AT_ST16;  // steps in the ring
     static constexpr int SC = KV == LC_CACHE_E4M3 ? 2 * TOK * 4 : 0;  // scales of a step
     static constexpr int WARP_BYTES = ST * (STEP + SC);
     static constexpr int OP = DP + 4;                        // floats between the heads of a warp's output
@@ -646,15 +645,15 @@ struct Attend {
 
 // One run a warp.
 template <int DP, int KV, int NG, bool VEC>
-__global__ void __launch_bounds__(kAtThreads, DP <= 128 && NG == 1 ? LC_AT_MINB : 1) k_attend(const __grid_constant__ AttendArgs a) {
+__global__ void __launch_bounds__(kAtThreads, kAtBlocks) k_attend(const __grid_constant__ AttendArgs a) {
     using A = Attend<DP, KV, NG, VEC>;
     using S = typename A::S;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint32_t seen_bits[kAtWarps * S::ST];
     __shared__ long long warp_sums[kAtWarps], upto[kAtThreads];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int units = a.c.heads * a.row_blocks;
+    start_after_prior();
 
     // the steps up to the sequences of each thread: thread t stands for `per` of them
     const int per = (a.c.n_seqs + kAtThreads - 1) / kAtThreads;
@@ -766,6 +765,7 @@ __global__ void __launch_bounds__(kAtThreads) k_attend_unit(const __grid_constan
     __shared__ float lse_of[8 * NG];
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int units = a.c.heads * a.row_blocks;
+    start_after_prior();
     Place c{};
     c.b = blockIdx.x / units;
     c.unit = blockIdx.x - c.b * units;
@@ -859,8 +859,7 @@ int launch_attend(const AttendArgs &a, bool by_unit, int *runs, cudaStream_t cs)
         if (by_unit) {
             const void *fn = reinterpret_cast<const void *>(&k_attend_unit<DP, KV, NG>);
             if (prepare(fn, kAtThreads, S::SMEM, S::SMEM, &sms, &per) != cudaSuccess) return LC_ERR_CUDA;
-            k_attend_unit<DP, KV, NG><<<static_cast<unsigned>(units), kAtThreads, S::SMEM, cs>>>(a);
-            return finish_launch();
+            return launch_after(fn, static_cast<unsigned>(units), kAtThreads, S::SMEM, cs, &a);
         }
     }
     const void *fn = reinterpret_cast<const void *>(&k_attend<DP, KV, NG, VEC>);
@@ -871,8 +870,7 @@ int launch_attend(const AttendArgs &a, bool by_unit, int *runs, cudaStream_t cs)
         1, std::min<int64_t>({int64_t(sms) * per, kAtMaxBlocks,
                               (most + kAtMinSteps * kAtWarps - 1) / (kAtMinSteps * kAtWarps)}));
     *runs = static_cast<int>(grid) * kAtWarps;
-    k_attend<DP, KV, NG, VEC><<<static_cast<unsigned>(grid), kAtThreads, S::SMEM, cs>>>(a);
-    return finish_launch();
+    return launch_after(fn, static_cast<unsigned>(grid), kAtThreads, S::SMEM, cs, &a);
 }
 
 // The main launch for one cache type; `runs` receives the runs of a launch by runs.

@@ -17,6 +17,15 @@ namespace lc {
 // Kernel classes in the device error word.
 constexpr uint32_t kClassAppend = 0xf0, kClassAttend = 0xf1, kClassEvict = 0xf2;
 
+// Kernels are launched to overlap the end of what precedes them on the
+// stream (launch_after): the next one may be set up as soon as every block
+// has come here, and this one touches no memory until all before it has
+// ended and is visible.
+__device__ __forceinline__ void start_after_prior() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 struct CacheArgs {
     uint8_t *k, *v;
     float *ks, *vs;
@@ -51,6 +60,27 @@ __device__ __forceinline__ int64_t row_offset(const int64_t *st, int page, int h
 }
 
 // ---- host ----------------------------------------------------------------
+
+// Launches a kernel of one parameter struct that calls start_after_prior; in
+// clusters of `cluster` blocks.
+inline int launch_after(const void *fn, unsigned grid, unsigned threads, size_t smem, cudaStream_t cs, const void *arg,
+                        unsigned cluster = 1) {
+    cudaLaunchAttribute attr[2] = {};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = cs;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    void *args[] = {const_cast<void *>(arg)};
+    return cudaLaunchKernelExC(&cfg, fn, args) == cudaSuccess ? LC_OK : LC_ERR_CUDA;
+}
 
 inline int cache_elem_bytes(int type) { return type == LC_CACHE_E4M3 ? 1 : 2; }
 

@@ -106,6 +106,7 @@ __device__ __forceinline__ void put_row(const CacheArgs &c, bool is_v, int page,
 template <int Q, bool VEC, int NI, int U>
 __global__ void __launch_bounds__(kApThreads) k_cache_append(const __grid_constant__ AppendArgs a) {
     const CacheArgs &c = a.c;
+    start_after_prior();
     const int64_t thread = int64_t(blockIdx.x) * kApThreads + threadIdx.x;
     if (thread < c.n_seqs) {
         const int at = static_cast<int>(thread);
@@ -165,8 +166,8 @@ int launch_append(AppendArgs &a, int64_t tokens, cudaStream_t cs) {
     a.items = static_cast<uint32_t>(tokens * per);
     a.head_div = make_fastdiv(static_cast<uint32_t>(per));
     const uint64_t threads = std::max<uint64_t>(uint64_t(a.items) * 32, a.c.n_seqs);
-    k_cache_append<Q, VEC, NI, U><<<static_cast<unsigned>((threads + kApThreads - 1) / kApThreads), kApThreads, 0, cs>>>(a);
-    return finish_launch();
+    return launch_after(reinterpret_cast<const void *>(&k_cache_append<Q, VEC, NI, U>),
+                        static_cast<unsigned>((threads + kApThreads - 1) / kApThreads), kApThreads, 0, cs, &a);
 }
 
 template <int Q>

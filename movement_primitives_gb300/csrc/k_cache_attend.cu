@@ -12,19 +12,31 @@ struct Parts {
 };
 
 __device__ __forceinline__ float2 join_ml(const AttendArgs &a, const Parts &p, int row) {
+    constexpr int kAhead = 4;
     const int lane = threadIdx.x & 31;
     float top = -INFINITY, sum = 0.f;
-    for (int i = lane; i < p.count; i += 32) top = fmaxf(top, a.part_ml[int64_t(p.slot(i)) * a.part_rows + row].x);
+    for (int i = lane; i < p.count; i += 32 * kAhead) {
+        float2 v[kAhead];
+        float most = top;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    const float safe = top == -INFINITY ? 0.f : top;
-    for (int i = lane; i < p.count; i += 32) {
-        const float2 v = a.part_ml[int64_t(p.slot(i)) * a.part_rows + row];
-        sum += v.y * exp2_fast(v.x - safe);
+        for (int k = 0; k < kAhead; ++k) {
+            v[k] = i + 32 * k < p.count ? a.part_ml[int64_t(p.slot(i + 32 * k)) * a.part_rows + row]
+                                        : make_float2(-INFINITY, 0.f);
+            most = fmaxf(most, v[k].x);
+        }
+        const float safe = most == -INFINITY ? 0.f : most;
+        sum *= exp2_fast(top - safe);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) sum += v[k].y * exp2_fast(v[k].x - safe);
+        top = most;
     }
+    float most = top;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+    sum *= exp2_fast(top - (most == -INFINITY ? 0.f : most));
 #pragma unroll
     for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    return make_float2(top, sum);
+    return make_float2(most, sum);
 }
 
 // scores[b, h, j] += sum over the group's query heads of 2^(logit - lse), for one chunk of slots.
@@ -74,20 +86,20 @@ __device__ __forceinline__ void add_scores(const AttendArgs &a, uint32_t at, flo
         if (i0 + t + k * threads < n - lo) to[k * threads] += w[k];
 }
 
-// Blocks 0 .. join_blocks - 1 join the parts of the rows (sequence, query
-// head) whose units were cut, in their order, and write the zeros of
-// sequences with nothing to see.  Warp w takes row blockIdx + w join_blocks
-// (w < join_rows); a row of many parts is left for the whole block, several parts at
-// a time.  The blocks after them (with scores), one a (sequence, key head,
-// chunk of slots), add the weights.
+// The first score_blocks blocks (with scores), one a (sequence, key head,
+// chunk of slots), add the weights.  The join_blocks after them join the parts of the rows
+// (sequence, query head) whose units were cut, in their order, and write the
+// zeros of sequences with nothing to see: warp w of the i-th takes row i + w
+// join_blocks (w < join_rows); a row of many parts is left for the whole
+// block, several parts at a time.
 template <bool F16>
 __global__ void __launch_bounds__(kJoinMost) k_attend_join(const __grid_constant__ AttendArgs a) {
     extern __shared__ float acc[];  // four floats a thread
     __shared__ int whole_block[kJoinRows];
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, threads = blockDim.x;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (blockIdx.x >= a.join_blocks) {
-        add_scores(a, blockIdx.x - a.join_blocks, acc);
+    start_after_prior();
+    if (blockIdx.x < a.score_blocks) {
+        add_scores(a, blockIdx.x, acc);
         return;
     }
     const int units = a.c.heads * a.row_blocks, quads = a.part_pitch / 4;
@@ -98,7 +110,7 @@ __global__ void __launch_bounds__(kJoinMost) k_attend_join(const __grid_constant
     };
     auto row_of = [&](int w) {
         Row r{};
-        const uint32_t at = blockIdx.x + static_cast<uint32_t>(w) * a.join_blocks;
+        const uint32_t at = blockIdx.x - a.score_blocks + static_cast<uint32_t>(w) * a.join_blocks;
         if (at >= static_cast<uint32_t>(a.c.n_seqs) * a.q_heads) {
             r.n = 1;  // no such row
             return r;
@@ -181,7 +193,7 @@ int launch_attend_e4m3(const AttendArgs &a, bool by_unit, bool vec, int *runs, c
 namespace {
 
 // Slots of a step: AtShape's TOK.
-int step_slots(int dim, int type) { return LC_AT_STEP / (2 * padded_dim(dim) * cache_elem_bytes(type)) >= 32 ? 32 : 16; }
+int step_slots(int dim, int type) { return 8192 / (2 * padded_dim(dim) * cache_elem_bytes(type)) >= 32 ? 32 : 16; }
 
 // How a call of these sizes goes: one block a unit, or runs; with runs, or with
 // scores, it needs a workspace of these offsets and this end.
@@ -212,21 +224,6 @@ bool attend_space(const lc_paged_cache &cache, const CacheArgs &c, int q_heads, 
     int64_t logits;
     if (!mul_ok_ext(heads, s->logit_stride * 4, &logits)) return false;
     return add_ok_ext(s->logits, scores ? logits : 0, &s->end) && s->end < int64_t(1) << 60;
-}
-
-// Launches a kernel that may start before the one ahead of it has ended (and waits for it itself).
-cudaError_t launch_after(const void *fn, unsigned grid, unsigned threads, unsigned smem, cudaStream_t cs, void **args) {
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = cs;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
 }  // namespace
@@ -322,9 +319,9 @@ extern "C" int lc_cache_attend(const lc_paged_cache *cache, const lc_cache_query
     a.head_div = make_fastdiv(static_cast<uint32_t>(a.c.heads));
     a.q_div = make_fastdiv(static_cast<uint32_t>(a.q_heads));
     a.group_div = make_fastdiv(static_cast<uint32_t>(a.group));
-    const int64_t blocks = a.join_blocks + kext[0] * kext[1] * chunks_of;
-    void *args[] = {&a};
+    a.score_blocks = static_cast<uint32_t>(kext[0] * kext[1] * chunks_of);
+    const int64_t blocks = int64_t(a.score_blocks) + a.join_blocks;
     const void *join = cache->type == LC_CACHE_F16 ? reinterpret_cast<const void *>(&k_attend_join<true>)
                                                    : reinterpret_cast<const void *>(&k_attend_join<false>);
-    return launch_after(join, static_cast<unsigned>(blocks), threads, threads * 16, cs, args) == cudaSuccess ? LC_OK : LC_ERR_CUDA;
+    return launch_after(join, static_cast<unsigned>(blocks), threads, threads * 16, cs, &a);
 }

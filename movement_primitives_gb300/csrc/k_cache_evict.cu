@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_evict_select(const 
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int unit = blockIdx.x / parts;
     const int b = unit / a.c.heads, h = unit - b * a.c.heads;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    start_after_prior();
     const int n = cache_length(a.c, a.lengths, b, kClassEvict);
     const int m = min(n, a.budget);
     const float *scores = a.scores + b * a.sst[0] + h * a.sst[1];
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kMvThreads, 24) k_evict_move(const __grid_cons
     const int row_bytes = c.dim * EB, pitch = (row_bytes + 15) / 16 * 16;
     const int units = c.n_seqs * c.heads;
     const int64_t tickets = int64_t(units) * a.chunks;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    start_after_prior();
     if (t == 0) next = atomicAdd(a.ticket, 1u);
     __syncthreads();
     int64_t ticket = next;
@@ -430,27 +430,12 @@ int launch_evict(EvictArgs &a, cudaStream_t cs) {
                                       : (held ? reinterpret_cast<const void *>(&k_evict_select<true, 512>)
                                               : reinterpret_cast<const void *>(&k_evict_select<false, 512>));
     if (prepare(sel, threads, 0, kSelKeys * 4, &sms, &per) != cudaSuccess) return LC_ERR_CUDA;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = parts;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(units * parts));
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = held ? static_cast<size_t>(hold) * 4 : 0;
-    cfg.stream = cs;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    void *args[] = {&a};
-    if (cudaLaunchKernelExC(&cfg, sel, args) != cudaSuccess) return LC_ERR_CUDA;
-
-    const void *fn = reinterpret_cast<const void *>(&k_evict_move<EB, VEC>);
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(units * a.chunks, int64_t(sms) * move_per)));
-    cfg.blockDim = dim3(kMvThreads);
-    cfg.dynamicSmemBytes = smem;
-    return cudaLaunchKernelExC(&cfg, fn, args) == cudaSuccess ? LC_OK : LC_ERR_CUDA;
+    const int st = launch_after(sel, static_cast<unsigned>(units * parts), threads,
+                                held ? static_cast<size_t>(hold) * 4 : 0, cs, &a, parts);
+    if (st) return st;
+    return launch_after(reinterpret_cast<const void *>(&k_evict_move<EB, VEC>),
+                        static_cast<unsigned>(std::min<int64_t>(units * a.chunks, int64_t(sms) * move_per)), kMvThreads,
+                        smem, cs, &a);
 }
 
 }  // namespace
