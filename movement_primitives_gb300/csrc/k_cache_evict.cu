@@ -83,7 +83,7 @@ template <bool HELD, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_evict_select(const __grid_constant__ EvictArgs a) {
     constexpr int kWarps = THREADS / 32;
     extern __shared__ uint32_t keys[];
-    __shared__ uint32_t hist[2][kSelBins], groups[2][64], chosen[3][2], counts[2];
+    __shared__ uint32_t hist[2][kSelBins], groups[2][64], chosen[3][3], counts[2];
     __shared__ uint2 warp_counts[kWarps];
     cg::cluster_group cluster = cg::this_cluster();
     const int parts = cluster.num_blocks(), part = cluster.block_rank();
@@ -176,15 +176,21 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_evict_select(const 
 #pragma unroll
                 for (int r = 0; r < kSelCluster; ++r)
                     if (r < parts) bin += (parts > 1 ? cluster.map_shared_rank(mine, r) : mine)[32 * group + lane];
-                const int digit = 32 * group + pick(bin, &left);
-                if (lane == 0) {
-                    chosen[pass][0] = digit;
+                if (lane == pick(bin, &left)) {
+                    chosen[pass][0] = 32 * group + lane;
                     chosen[pass][1] = left;
+                    chosen[pass][2] = bin == left;  // all of that digit stay
                 }
             }
             __syncthreads();
             prefix = prefix << bits | chosen[pass][0];
             need = chosen[pass][1];
+            if (chosen[pass][2]) {
+                // every key from this prefix up stays (it is above 0: not all that compete stay), none of a tie
+                prefix = (prefix << shift) - 1;
+                need = 0;
+                break;
+            }
         }
     } else {
         __syncthreads();
