@@ -48,7 +48,12 @@ namespace lc {
 
 constexpr int kAtWarps = 4;
 constexpr int kAtThreads = 32 * kAtWarps;
-constexpr int kAtBlocks = 2;       // of an SM
+// Blocks of an SM (at least; registers) and steps in a warp's ring.  Measured
+// on 1.09 GB of bfloat16 (64 sequences of up to 8192 slots, dim 128) and on
+// 0.27 GB of dim 64: 2 blocks x 2 steps 168 and 51 us; x 3 steps 178 and 51;
+// 3 blocks x 2 steps 174 and 62.  More streams do not hide more latency, they
+// cost the memory its order.
+constexpr int kAtBlocks = 2, kAtStages = 2;
 constexpr int kAtRows = 16;        // query heads of a unit at most
 constexpr int kAtMaxBlocks = 608;  // of the main kernel; sizes the workspace
 constexpr int kAtMaxRuns = kAtMaxBlocks * kAtWarps;
@@ -93,15 +98,6 @@ struct AttendArgs {
 
 inline int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
-#ifndef LC_AT_ST8  // compile-time knobs so that variants can be measured
-#define LC_AT_ST8 2
-#endif
-#ifndef LC_AT_ST16
-#define LC_AT_ST16 2
-#endif
-#ifndef LC_AT_ST4
-#define LC_AT_ST4 3
-#endif
 // Shapes of one instantiation.  DP: head_dim rounded up (64, 128, 256); KV: an
 // lc_cache_type; NG: query heads in eights (1, 2).  A step is 8 KiB where the shapes allow.
 template <int DP, int KV, int NG>
@@ -111,7 +107,7 @@ struct AtShape {
     static constexpr int CH = RB / 16;                       // its 16-byte chunks
     static constexpr int TOK = 8192 / (2 * RB) >= 32 ? 32 : 16;
     static constexpr int STEP = 2 * TOK * RB;                // keys, then values
-    static constexpr int ST = STEP <= 4096 ? LC_AT_ST4 : STEP <= 8192 ? LC_AT_ST8 : LC_AT_ST16;  // steps in the ring
+    static constexpr int ST = kAtStages;                     // steps in the ring
     static constexpr int SC = KV == LC_CACHE_E4M3 ? 2 * TOK * 4 : 0;  // scales of a step
     static constexpr int WARP_BYTES = ST * (STEP + SC);
     static constexpr int OP = DP + 4;                        // floats between the heads of a warp's output
