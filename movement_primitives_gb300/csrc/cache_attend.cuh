@@ -35,9 +35,11 @@
 // in their order, so results do not depend on timing.  Each warp streams its
 // run through a ring of its own in shared memory (cp.async, 16 bytes a lane,
 // rows swizzled for ldmatrix) that runs ahead across units, with no barrier
-// between warps.  Caches of few slots (kUnitSteps) take one block a unit instead,
-// joined in shared memory, with no second launch.
+// between warps.  Where units are few and short (kUnitSteps) a block or a cluster
+// of blocks takes one instead, joined in shared memory, with no second launch.
 #pragma once
+
+#include <cooperative_groups.h>
 
 #include <cmath>
 #include <type_traits>
@@ -45,6 +47,8 @@
 #include "cache_common.cuh"
 
 namespace lc {
+
+namespace cg = cooperative_groups;
 
 constexpr int kAtWarps = 4;
 constexpr int kAtThreads = 32 * kAtWarps;
@@ -66,8 +70,14 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // A run takes at least this many steps: shorter ones leave more parts to join than
 // the further warps save.
 constexpr int kAtMinSteps = 2;
-// Capacity, in steps, up to which a unit is one block's.
-constexpr int kUnitSteps = 16;
+// A unit is one block's, or a cluster's of up to kUnitCluster blocks while
+// there are kUnitBlocks at most, where a warp then takes kUnitSteps steps or
+// fewer: one launch and no parts in memory, but units of unlike lengths are
+// not evened out.  GPU time against runs: 8 units of 64 steps of 16 KiB 13.5
+// and 19.9 us; 96 units of up to 50 steps of 5 KiB 12.1 and 12.1 (the host
+// saves 5 us of a launch); at 16 steps a warp, 84 units of up to 125 steps 24.5
+// and 14.9, 128 units of up to 128 steps of 8 KiB 25.9 and 21.5.
+constexpr int kUnitSteps = 8, kUnitBlocks = 304, kUnitCluster = 8;
 
 struct AttendArgs {
     CacheArgs c;
@@ -96,18 +106,23 @@ struct AttendArgs {
     FastDiv chunk_div, head_div, q_div, group_div;
 };
 
+// Steps in a warp's ring where a unit is a block's: few steps, whose latency counts.
+template <int DP, int KV>
+constexpr int kUnitStages = DP * (KV == LC_CACHE_E4M3 ? 1 : 2) > 256 ? 2 : 3;
+
 inline int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
 // Shapes of one instantiation.  DP: head_dim rounded up (64, 128, 256); KV: an
-// lc_cache_type; NG: query heads in eights (1, 2).  A step is 8 KiB where the shapes allow.
-template <int DP, int KV, int NG>
+// lc_cache_type; NG: query heads in eights (1, 2); STAGES: steps in a warp's
+// ring.  A step is 8 KiB where the shapes allow.
+template <int DP, int KV, int NG, int STAGES>
 struct AtShape {
     static constexpr int EB = KV == LC_CACHE_E4M3 ? 1 : 2;
     static constexpr int RB = DP * EB;                       // bytes of a row
     static constexpr int CH = RB / 16;                       // its 16-byte chunks
     static constexpr int TOK = 8192 / (2 * RB) >= 32 ? 32 : 16;
     static constexpr int STEP = 2 * TOK * RB;                // keys, then values
-    static constexpr int ST = kAtStages;                     // steps in the ring
+    static constexpr int ST = STAGES;
     static constexpr int SC = KV == LC_CACHE_E4M3 ? 2 * TOK * 4 : 0;  // scales of a step
     static constexpr int WARP_BYTES = ST * (STEP + SC);
     static constexpr int OP = DP + 4;                        // floats between the heads of a warp's output
@@ -212,9 +227,9 @@ __device__ __forceinline__ void next_step(const AttendArgs &a, int units, Place 
     } while (p.steps == 0);
 }
 
-template <int DP, int KV, int NG, bool VEC>
+template <int DP, int KV, int NG, bool VEC, int STAGES>
 struct Attend {
-    using S = AtShape<DP, KV, NG>;
+    using S = AtShape<DP, KV, NG, STAGES>;
     static constexpr bool F16 = KV == LC_CACHE_F16, Q8 = KV == LC_CACHE_E4M3;
     static constexpr bool M16 = F16 || Q8;       // the matrix instructions' type is float16
     static constexpr int KS = DP / 16;           // 16-wide pieces of a row
@@ -642,7 +657,7 @@ struct Attend {
 // One run a warp.
 template <int DP, int KV, int NG, bool VEC>
 __global__ void __launch_bounds__(kAtThreads, kAtBlocks) k_attend(const __grid_constant__ AttendArgs a) {
-    using A = Attend<DP, KV, NG, VEC>;
+    using A = Attend<DP, KV, NG, VEC, kAtStages>;
     using S = typename A::S;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint32_t seen_bits[kAtWarps * S::ST];
@@ -749,40 +764,49 @@ __global__ void __launch_bounds__(kAtThreads, kAtBlocks) k_attend(const __grid_c
     }
 }
 
-// One unit a block, its steps dealt to the warps in turn and their results
-// joined in shared memory.
+// One unit a block, or a cluster of blocks, its steps dealt to the warps in
+// turn; their results are joined in shared memory, the blocks' through
+// distributed shared memory, each block writing a share.
 template <int DP, int KV, int NG>
 __global__ void __launch_bounds__(kAtThreads) k_attend_unit(const __grid_constant__ AttendArgs a) {
-    using A = Attend<DP, KV, NG, true>;
+    using A = Attend<DP, KV, NG, true, kUnitStages<DP, KV>>;
     using S = typename A::S;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint32_t seen_bits[kAtWarps * S::ST];
-    __shared__ float2 ml[kAtWarps][8 * NG];
+    __shared__ float2 ml[kAtWarps][8 * NG], block_ml[8 * NG];
     __shared__ float lse_of[8 * NG];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int parts = cluster.num_blocks(), part = cluster.block_rank();
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int units = a.c.heads * a.row_blocks;
     start_after_prior();
     Place c{};
-    c.b = blockIdx.x / units;
-    c.unit = blockIdx.x - c.b * units;
+    const int at_unit = blockIdx.x / parts;
+    c.b = at_unit / units;
+    c.unit = at_unit - c.b * units;
     enter_sequence<S::TOK>(a, c);
     A u{a, lane, smem + warp * S::WARP_BYTES, ptx::smem_addr(smem + warp * S::WARP_BYTES), seen_bits + warp * S::ST};
     const int h = a.row_blocks == 1 ? c.unit : c.unit / a.row_blocks;
-    int ahead = warp;
+    const int first = part * kAtWarps + warp, stride = parts * kAtWarps;
+    int ahead = first;
+    auto find = [&] {
+        if (ahead < c.steps) u.find_pages(c.b, h, c.lo + ahead * S::TOK, c.n);
+    };
     auto issue = [&](int stage) {
         if (ahead < c.steps) {
-            u.find_pages(c.b, h, c.lo + ahead * S::TOK, c.n);
             u.issue(stage);
+            ahead += stride;
+            find();
         }
-        ahead += kAtWarps;
         ptx::cp_async_commit();
     };
+    find();
 #pragma unroll 1
     for (int i = 0; i < S::ST - 1; ++i) issue(i);
     u.begin_unit(c.b, c.unit);
     int stage = 0, fill = S::ST - 1;
 #pragma unroll 1
-    for (int k = warp; k < c.steps; k += kAtWarps) {
+    for (int k = first; k < c.steps; k += stride) {
         issue(fill);
         ptx::cp_async_wait<S::ST - 1>();
         __syncwarp();
@@ -806,35 +830,75 @@ __global__ void __launch_bounds__(kAtThreads) k_attend_unit(const __grid_constan
             }
         }
     __syncthreads();
-    for (int at = t; at < u.rows * (DP / 4); at += kAtThreads) {
-        const int head = at / (DP / 4), col = at % (DP / 4) * 4;
+    // (m, l, o) of one head and four columns from `n` parts
+    auto join = [&](int n, auto &&ml_of, auto &&o_of, float2 *v, float (&y)[4]) {
         float top = -INFINITY, sum = 0.f;
-        float y[4] = {};
-#pragma unroll
-        for (int w = 0; w < kAtWarps; ++w) top = fmaxf(top, ml[w][head].x);
+        y[0] = y[1] = y[2] = y[3] = 0.f;
+        for (int i = 0; i < n; ++i) top = fmaxf(top, ml_of(i).x);
         const float safe = top == -INFINITY ? 0.f : top;
-#pragma unroll
-        for (int w = 0; w < kAtWarps; ++w) {
-            const float2 v = ml[w][head];
-            const float f = exp2_fast(v.x - safe);
-            const float4 z = *reinterpret_cast<const float4 *>(smem + w * S::WARP_BYTES + (head * S::OP + col) * 4);
-            sum += v.y * f;
+        for (int i = 0; i < n; ++i) {
+            const float2 w = ml_of(i);
+            const float f = exp2_fast(w.x - safe);
+            const float4 z = o_of(i);
+            sum += w.y * f;
             y[0] += z.x * f;
             y[1] += z.y * f;
             y[2] += z.z * f;
             y[3] += z.w * f;
         }
-        const float f = sum == 0.f ? 0.f : 1.f / sum;
+        *v = make_float2(top, sum);
+    };
+    auto put = [&](int head, int col, float2 v, const float (&y)[4]) {
+        const float f = v.y == 0.f ? 0.f : 1.f / v.y;
         uint16_t *to = a.out + c.b * a.ost[0] + (u.q0 + head) * a.ost[1];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (col + i < a.c.dim) to[col + i] = static_cast<uint16_t>(pack2<A::F16>(y[i] * f, 0.f));
-        if (col == 0) lse_of[head] = u.write_lse(u.q0 + head, top, sum);
+        if (col == 0) lse_of[head] = u.write_lse(u.q0 + head, v.x, v.y);
+    };
+    for (int at = t; at < u.rows * (DP / 4); at += kAtThreads) {
+        const int head = at / (DP / 4), col = at % (DP / 4) * 4;
+        float2 v;
+        float y[4];
+        join(kAtWarps, [&](int w) { return ml[w][head]; },
+             [&](int w) {
+                 return *reinterpret_cast<const float4 *>(smem + w * S::WARP_BYTES + (head * S::OP + col) * 4);
+             },
+             &v, y);
+        if (parts == 1) {
+            put(head, col, v, y);
+        } else {  // in the place of the first warp's, which only this thread reads
+            *reinterpret_cast<float4 *>(smem + (head * S::OP + col) * 4) = make_float4(y[0], y[1], y[2], y[3]);
+            if (col == 0) block_ml[head] = v;
+        }
+    }
+    if (parts > 1) {
+        cluster.sync();
+        for (int at = part * kAtThreads + t; at < u.rows * (DP / 4); at += parts * kAtThreads) {
+            const int head = at / (DP / 4), col = at % (DP / 4) * 4;
+            float2 v;
+            float y[4];
+            join(parts, [&](int r) { return cluster.map_shared_rank(block_ml, r)[head]; },
+                 [&](int r) {
+                     return *reinterpret_cast<const float4 *>(cluster.map_shared_rank(smem, r) + (head * S::OP + col) * 4);
+                 },
+                 &v, y);
+            put(head, col, v, y);
+        }
     }
     if (a.logits) {
+        if (parts > 1 && t < u.rows) {  // every block needs every head's
+            float top = -INFINITY, sum = 0.f;
+            for (int r = 0; r < parts; ++r) top = fmaxf(top, cluster.map_shared_rank(block_ml, r)[t].x);
+            for (int r = 0; r < parts; ++r) {
+                const float2 v = cluster.map_shared_rank(block_ml, r)[t];
+                sum += v.y * exp2_fast(v.x - (top == -INFINITY ? 0.f : top));
+            }
+            lse_of[t] = sum == 0.f ? -INFINITY : top + log2f(sum);
+        }
         __syncthreads();
         const float *x = a.logits + (int64_t(c.b) * a.q_heads + u.q0) * a.logit_stride;
-        for (int i = t; i < c.n - c.lo; i += kAtThreads) {
+        for (int i = part * kAtThreads + t; i < c.n - c.lo; i += parts * kAtThreads) {
             float w = 0.f;
             for (int g = 0; g < u.rows; ++g) {
                 const float e = exp2_fast(x[g * a.logit_stride + i] - lse_of[g]);
@@ -843,19 +907,21 @@ __global__ void __launch_bounds__(kAtThreads) k_attend_unit(const __grid_constan
             a.scores[c.b * a.sst[0] + h * a.sst[1] + c.lo + i] += w;
         }
     }
+    if (parts > 1) cluster.sync();  // no block leaves while another reads its shared memory
 }
 
 // One warp instantiation's launches: one block a unit (VEC only), or one run a warp.
 template <int DP, int KV, int NG, bool VEC>
-int launch_attend(const AttendArgs &a, bool by_unit, int *runs, cudaStream_t cs) {
-    using S = AtShape<DP, KV, NG>;
+int launch_attend(const AttendArgs &a, int unit_blocks, int *runs, cudaStream_t cs) {
+    using S = AtShape<DP, KV, NG, kAtStages>;
     const int64_t units = int64_t(a.c.n_seqs) * a.c.heads * a.row_blocks;
     int sms, per;
     if constexpr (VEC) {
-        if (by_unit) {
+        if (unit_blocks) {
+            constexpr int kBytes = AtShape<DP, KV, NG, kUnitStages<DP, KV>>::SMEM;
             const void *fn = reinterpret_cast<const void *>(&k_attend_unit<DP, KV, NG>);
-            if (prepare(fn, kAtThreads, S::SMEM, S::SMEM, &sms, &per) != cudaSuccess) return LC_ERR_CUDA;
-            return launch_after(fn, static_cast<unsigned>(units), kAtThreads, S::SMEM, cs, &a);
+            if (prepare(fn, kAtThreads, kBytes, kBytes, &sms, &per) != cudaSuccess) return LC_ERR_CUDA;
+            return launch_after(fn, static_cast<unsigned>(units * unit_blocks), kAtThreads, kBytes, cs, &a, unit_blocks);
         }
     }
     const void *fn = reinterpret_cast<const void *>(&k_attend<DP, KV, NG, VEC>);
@@ -871,14 +937,14 @@ int launch_attend(const AttendArgs &a, bool by_unit, int *runs, cudaStream_t cs)
 
 // The main launch for one cache type; `runs` receives the runs of a launch by runs.
 template <int KV>
-int launch_attend_type(const AttendArgs &a, bool by_unit, bool vec, int *runs, cudaStream_t cs) {
+int launch_attend_type(const AttendArgs &a, int unit_blocks, bool vec, int *runs, cudaStream_t cs) {
     auto heads = [&](auto dp) {
         constexpr int DP = decltype(dp)::value;
         if (a.group <= 8)
-            return vec ? launch_attend<DP, KV, 1, true>(a, by_unit, runs, cs)
-                       : launch_attend<DP, KV, 1, false>(a, by_unit, runs, cs);
-        return vec ? launch_attend<DP, KV, 2, true>(a, by_unit, runs, cs)
-                   : launch_attend<DP, KV, 2, false>(a, by_unit, runs, cs);
+            return vec ? launch_attend<DP, KV, 1, true>(a, unit_blocks, runs, cs)
+                       : launch_attend<DP, KV, 1, false>(a, unit_blocks, runs, cs);
+        return vec ? launch_attend<DP, KV, 2, true>(a, unit_blocks, runs, cs)
+                   : launch_attend<DP, KV, 2, false>(a, unit_blocks, runs, cs);
     };
     switch (padded_dim(a.c.dim)) {
         case 64: return heads(std::integral_constant<int, 64>{});

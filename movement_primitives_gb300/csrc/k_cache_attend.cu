@@ -186,25 +186,26 @@ __global__ void __launch_bounds__(kJoinMost) k_attend_join(const __grid_constant
 
 cudaError_t take_error_attend(unsigned long long *v) { return take_module_error(v); }
 
-int launch_attend_bf16(const AttendArgs &a, bool by_unit, bool vec, int *runs, cudaStream_t cs);
-int launch_attend_f16(const AttendArgs &a, bool by_unit, bool vec, int *runs, cudaStream_t cs);
-int launch_attend_e4m3(const AttendArgs &a, bool by_unit, bool vec, int *runs, cudaStream_t cs);
+int launch_attend_bf16(const AttendArgs &a, int unit_blocks, bool vec, int *runs, cudaStream_t cs);
+int launch_attend_f16(const AttendArgs &a, int unit_blocks, bool vec, int *runs, cudaStream_t cs);
+int launch_attend_e4m3(const AttendArgs &a, int unit_blocks, bool vec, int *runs, cudaStream_t cs);
 
 namespace {
 
 // Slots of a step: AtShape's TOK.
 int step_slots(int dim, int type) { return 8192 / (2 * padded_dim(dim) * cache_elem_bytes(type)) >= 32 ? 32 : 16; }
 
-// How a call of these sizes goes: one block a unit, or runs; with runs, or with
-// scores, it needs a workspace of these offsets and this end.
+// How a call of these sizes goes: a block or a cluster a unit, or runs; with
+// runs, or with scores, it needs a workspace of these offsets and this end.
 struct AttendSpace {
     bool vec;      // rows of the pools are whole 16-byte words on 16-byte boundaries
-    bool by_unit;
+    int unit_blocks;  // 0: by runs
     int part_rows;
     int64_t part, ml, split, lse2, logits, end, logit_stride;
 };
 
-bool attend_space(const lc_paged_cache &cache, const CacheArgs &c, int q_heads, bool scores, AttendSpace *s) {
+bool attend_space(const lc_paged_cache &cache, const CacheArgs &c, int q_heads, int window, bool scores,
+                  AttendSpace *s) {
     const int eb = cache_elem_bytes(cache.type);
     const int64_t pool[3] = {cache.n_pages, cache.n_kv_heads, cache.page_size};
     s->vec = c.dim * eb % 16 == 0 && rows_aligned(cache.k, 3, pool, cache.k_stride, eb, 16) &&
@@ -212,13 +213,19 @@ bool attend_space(const lc_paged_cache &cache, const CacheArgs &c, int q_heads, 
     const int tok = step_slots(c.dim, cache.type), group = q_heads / c.heads;
     const int64_t units = c.heads * ((int64_t(group) + kAtRows - 1) / kAtRows), heads = int64_t(c.n_seqs) * q_heads;
     // scores of a key head whose query heads are several units' need the second launch
-    s->by_unit = s->vec && (int64_t(c.cap) + tok - 1) / tok <= kUnitSteps && !(scores && group > kAtRows);
+    s->unit_blocks = 0;
+    const int64_t steps = ((window ? std::min(window, c.cap) : c.cap) + int64_t(tok) - 1) / tok;
+    if (s->vec && !(scores && group > kAtRows)) {
+        int n = 1;
+        while (2 * n <= kUnitCluster && n * kAtWarps < steps && c.n_seqs * units * 2 * n <= kUnitBlocks) n *= 2;
+        if (steps <= int64_t(kUnitSteps) * kAtWarps * n) s->unit_blocks = n;
+    }
     s->part_rows = std::min(group, kAtRows);
-    const int64_t parts = s->by_unit ? 0 : int64_t(2) * kAtMaxRuns * s->part_rows;
+    const int64_t parts = s->unit_blocks ? 0 : int64_t(2) * kAtMaxRuns * s->part_rows;
     s->part = 0;
     s->ml = s->part + parts * padded_dim(c.dim) * 4;
     s->split = s->ml + round256(parts * 8);
-    s->lse2 = round256(s->split + (s->by_unit ? 0 : c.n_seqs * units * 8));
+    s->lse2 = round256(s->split + (s->unit_blocks ? 0 : c.n_seqs * units * 8));
     s->logits = round256(s->lse2 + (scores ? heads * 4 : 0));
     s->logit_stride = int64_t(c.cap) + tok;  // a unit's last step is written whole
     int64_t logits;
@@ -234,7 +241,7 @@ extern "C" int64_t lc_cache_attend_workspace(const lc_paged_cache *cache, int32_
     lc::CacheArgs c;
     lc::AttendSpace s;
     if (lc::check_cache(cache, false, &c) || n_q_heads < 1 || n_q_heads % c.heads ||
-        !lc::attend_space(*cache, c, n_q_heads, with_scores != 0, &s))
+        !lc::attend_space(*cache, c, n_q_heads, 0, with_scores != 0, &s))
         return -1;
     return s.end;
 }
@@ -266,7 +273,7 @@ extern "C" int lc_cache_attend(const lc_paged_cache *cache, const lc_cache_query
         return LC_ERR_NOT_INJECTIVE;
     AttendSpace space;
     const int64_t chunks = (int64_t(a.c.cap) + kJoinLeast * kScorePer - 1) / (kJoinLeast * kScorePer);
-    if (!attend_space(*cache, a.c, q->n_q_heads, q->scores != nullptr, &space) ||
+    if (!attend_space(*cache, a.c, q->n_q_heads, q->window, q->scores != nullptr, &space) ||
         qext[0] * qext[1] > 0x3fffffff || (q->scores && chunks && kext[0] * kext[1] > 0x3fffffff / chunks))
         return LC_ERR_OVERFLOW;
     if (space.end > 0 && !q->workspace) return LC_ERR_NULL;
@@ -305,8 +312,8 @@ extern "C" int lc_cache_attend(const lc_paged_cache *cache, const lc_cache_query
     const auto launch = cache->type == LC_CACHE_BF16  ? launch_attend_bf16
                         : cache->type == LC_CACHE_F16 ? launch_attend_f16
                                                       : launch_attend_e4m3;
-    st = launch(a, space.by_unit, space.vec, &runs, cs);
-    if (st || space.by_unit) return st;
+    st = launch(a, space.unit_blocks, space.vec, &runs, cs);
+    if (st || space.unit_blocks) return st;
     // a row a block, as wide as lets all rows run at once: few rows have many parts each, which a wide block reads more
     // of at a time; rows past that share blocks of the least width, a warp each
     const int64_t rows = qext[0] * qext[1];

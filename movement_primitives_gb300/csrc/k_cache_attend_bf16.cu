@@ -3,8 +3,8 @@
 
 namespace lc {
 
-int launch_attend_bf16(const AttendArgs &a, bool by_unit, bool vec, int *runs, cudaStream_t cs) {
-    return launch_attend_type<LC_CACHE_BF16>(a, by_unit, vec, runs, cs);
+int launch_attend_bf16(const AttendArgs &a, int unit_blocks, bool vec, int *runs, cudaStream_t cs) {
+    return launch_attend_type<LC_CACHE_BF16>(a, unit_blocks, vec, runs, cs);
 }
 cudaError_t take_error_attend_bf16(unsigned long long *v) { return take_module_error(v); }
 
