@@ -74,18 +74,23 @@ __device__ __forceinline__ void put_row(const CacheArgs &c, bool is_v, int page,
         const float scale = fine ? fmaxf(__fdiv_rn(value_of<Q>(top), 448.f), 1.17549435e-38f) : __int_as_float(0x7fc00000);
         if (!on) return;
         if (lane == 0) (is_v ? c.vs : c.ks)[row_offset(is_v ? c.vss : c.kss, page, h, row)] = scale;
-        const bool near = scale > 0x1p-100f && scale < 0x1p100f;
-        const float inverse = __frcp_rn(scale);
-        auto quotient = [&](float x) {
-            if (!near) return __fdiv_rn(x, scale);
-            const float q = x * inverse;
-            return q == 0.f ? q : fmaf(fmaf(-q, scale, x), inverse, q);  // (a zero keeps its sign)
-        };
         uint32_t code[4 * NI];
+        auto encode = [&](auto &&quotient) {
 #pragma unroll
-        for (int j = 0; j < 4 * NI; ++j)
-            code[j] = __nv_cvt_float2_to_fp8x2(make_float2(quotient(value_of<Q>(w[2 * j])), quotient(value_of<Q>(w[2 * j + 1]))),
-                                               __NV_SATFINITE, __NV_E4M3);
+            for (int j = 0; j < 4 * NI; ++j)
+                code[j] = __nv_cvt_float2_to_fp8x2(
+                    make_float2(quotient(value_of<Q>(w[2 * j])), quotient(value_of<Q>(w[2 * j + 1]))), __NV_SATFINITE,
+                    __NV_E4M3);
+        };
+        if (__all_sync(0xffffffffu, scale > 0x1p-100f && scale < 0x1p100f)) {
+            const float inverse = __frcp_rn(scale);
+            encode([&](float x) {
+                const float q = x * inverse, y = fmaf(fmaf(-q, scale, x), inverse, q);
+                return __uint_as_float(__float_as_uint(y) | (__float_as_uint(x) & 0x80000000u));  // a zero keeps its sign
+            });
+        } else {
+            encode([&](float x) { return __fdiv_rn(x, scale); });
+        }
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             if constexpr (VEC) {

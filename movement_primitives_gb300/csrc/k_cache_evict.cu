@@ -36,7 +36,7 @@ constexpr int kSelKeys = 48 * 1024; // keys a block holds in shared memory
 constexpr int kSelAhead = 4;        // keys a lane has at hand in the ordered pass
 constexpr int kSelCluster = 8;      // blocks of a unit at most
 constexpr int kSelLeast = 4096;     // slots a block of a cluster has at least
-constexpr int kMvThreads = 64;
+constexpr int kMvThreads = 64;        // a warp a pool where the rows' places are found
 constexpr int kMvRows = 32;         // ranks of a chunk (the selection writes rank_at once every 32 slots)
 
 struct EvictArgs {
@@ -48,6 +48,7 @@ struct EvictArgs {
     int64_t sst[2], nst[2], kst[2];  // sequence, head
     int32_t budget, recent;
     int32_t chunks;          // of a unit: ceil(budget / kMvRows)
+    FastDiv unit_div, head_div, word_div;  // units; key heads; words (VEC: of 16 bytes) of a row
     uint64_t wait_ns;
     // workspace
     uint32_t *ticket;        // the next chunk
@@ -285,15 +286,16 @@ __device__ __forceinline__ void store_release(uint32_t *p, uint32_t v) {
 
 // VEC: rows are whole 16-byte words on 16-byte boundaries; else they move an element at a time.
 template <int EB, bool VEC>
-__global__ void __launch_bounds__(kMvThreads, 24) k_evict_move(const __grid_constant__ EvictArgs a) {
+__global__ void __launch_bounds__(kMvThreads, 16) k_evict_move(const __grid_constant__ EvictArgs a) {
     extern __shared__ __align__(16) uint8_t rows[];  // [pool][row][pitch]
+    __shared__ int64_t from[2 * kMvRows], to[2 * kMvRows];  // bytes; from -1: the row stays, or has no place
     __shared__ float scales[2][kMvRows];
     __shared__ uint32_t next;
     __shared__ int late;
     const CacheArgs &c = a.c;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    const int row_bytes = c.dim * EB, pitch = (row_bytes + 15) / 16 * 16;
-    const int units = c.n_seqs * c.heads;
+    const int pitch = (c.dim * EB + 15) / 16 * 16;
+    const uint32_t units = static_cast<uint32_t>(c.n_seqs) * c.heads;
     const int64_t tickets = int64_t(units) * a.chunks;
     start_after_prior();
     if (t == 0) next = atomicAdd(a.ticket, 1u);
@@ -303,13 +305,15 @@ __global__ void __launch_bounds__(kMvThreads, 24) k_evict_move(const __grid_cons
         uint32_t coming = 0;
         if (t == 0) coming = atomicAdd(a.ticket, 1u);
         // the units' chunks in turn: the chunks in flight are of many units
-        const int chunk = static_cast<int>(ticket / units), unit = static_cast<int>(ticket - int64_t(chunk) * units);
-        const int b = unit / c.heads, h = unit - b * c.heads;
+        const uint32_t chunk = fast_div(static_cast<uint32_t>(ticket), a.unit_div);
+        const uint32_t unit = static_cast<uint32_t>(ticket) - chunk * units;
+        const int b = static_cast<int>(fast_div(unit, a.head_div)), h = static_cast<int>(unit) - b * c.heads;
         const int n = min(max(a.lengths[b], 0), c.cap);
         if (n > a.budget) {
-            // each lane finds one row's places
-            const int r = chunk * kMvRows + lane;
-            int64_t from[2] = {-1, -1}, to[2] = {0, 0};
+            // warp w finds the rows' places in pool w, a lane each
+            const int r = static_cast<int>(chunk) * kMvRows + lane;
+            const int64_t *st = warp ? c.vst : c.kst, *sst = warp ? c.vss : c.kss;
+            int64_t f = -1, o = 0, scale_to = 0;
             if (r < a.budget) {
                 const int src = a.kept[b * a.kst[0] + h * a.kst[1] + r];
                 if (src != r) {
@@ -317,40 +321,32 @@ __global__ void __launch_bounds__(kMvThreads, 24) k_evict_move(const __grid_cons
                     const int pf = cache_page(c, b, src, &row_f, kClassEvict);
                     const int pt = cache_page(c, b, r, &row_t, kClassEvict);
                     if (pf >= 0 && pt >= 0) {
-                        from[0] = row_offset(c.kst, pf, h, row_f);
-                        from[1] = row_offset(c.vst, pf, h, row_f);
-                        to[0] = row_offset(c.kst, pt, h, row_t);
-                        to[1] = row_offset(c.vst, pt, h, row_t);
-                        if (EB == 1 && warp < 2)
-                            scales[warp][lane] = (warp ? c.vs : c.ks)[row_offset(warp ? c.vss : c.kss, pf, h, row_f)];
+                        f = row_offset(st, pf, h, row_f) * EB;
+                        o = row_offset(st, pt, h, row_t) * EB;
+                        if (EB == 1) {
+                            scales[warp][lane] = (warp ? c.vs : c.ks)[row_offset(sst, pf, h, row_f)];
+                            scale_to = row_offset(sst, pt, h, row_t);
+                        }
                     }
                 }
             }
-            const uint32_t moves = __ballot_sync(0xffffffffu, from[0] >= 0);
-            // the warps take the rows of both pools in turn, 16 bytes a lane
-            const int words = VEC ? row_bytes / 16 : c.dim;
-            const int per_row = min(words, 32), rows_at = 32 / per_row;
-            const int my_row = lane / per_row, my_word = lane - my_row * per_row;
-            auto each = [&](auto &&move) {
-#pragma unroll
-                for (int p = 0; p < 2; ++p)
-                    for (int i = warp * rows_at; i < kMvRows; i += kMvThreads / 32 * rows_at) {
-                        const int row = i + my_row;
-                        const int64_t f = __shfl_sync(0xffffffffu, from[p], row & 31);
-                        const int64_t o = __shfl_sync(0xffffffffu, to[p], row & 31);
-                        if (my_row < rows_at && row < kMvRows && (moves >> row & 1))
-                            for (int w = my_word; w < words; w += per_row)
-                                move((p ? c.v : c.k), f, o, rows + (p * kMvRows + row) * pitch, w);
-                    }
-            };
-            each([&](const uint8_t *pool, int64_t f, int64_t, uint8_t *at, int w) {
+            from[warp * kMvRows + lane] = f;
+            to[warp * kMvRows + lane] = o;
+            __syncthreads();
+            const uint32_t words = a.word_div.d, items = 2 * kMvRows * words;
+#pragma unroll 4
+            for (uint32_t i = t; i < items; i += kMvThreads) {
+                const uint32_t row = fast_div(i, a.word_div), w = i - row * words;
+                if (from[row] < 0) continue;
+                const uint8_t *src = (row < kMvRows ? c.k : c.v) + from[row];
+                uint8_t *at = rows + row * pitch;
                 if constexpr (VEC)
-                    ptx::cp_async16(ptx::smem_addr(at + 16 * w), pool + f * EB + 16 * w);
+                    ptx::cp_async16(ptx::smem_addr(at + 16 * w), src + 16 * w);
                 else if constexpr (EB == 2)
-                    reinterpret_cast<uint16_t *>(at)[w] = reinterpret_cast<const uint16_t *>(pool)[f + w];
+                    reinterpret_cast<uint16_t *>(at)[w] = reinterpret_cast<const uint16_t *>(src)[w];
                 else
-                    at[w] = pool[f + w];
-            });
+                    at[w] = src[w];
+            }
             ptx::cp_async_commit();
             ptx::cp_async_wait<0>();
             __syncthreads();  // all rows have been read
@@ -359,7 +355,8 @@ __global__ void __launch_bounds__(kMvThreads, 24) k_evict_move(const __grid_cons
                 store_release(done + chunk, 1);
                 // the chunks whose rows sit in the slots written next
                 const int32_t *rank = a.rank_at + int64_t(unit) * (a.chunks + 1) + chunk;
-                const int first = rank[0] / kMvRows, last = min((rank[1] - 1) / kMvRows, chunk - 1);
+                const int first = rank[0] / kMvRows;
+                const int last = min((rank[1] - 1) / kMvRows, static_cast<int>(chunk) - 1);
                 bool ok = true;
                 for (int k = first; k <= last && ok; ++k) {
                     if (load_acquire(done + k)) continue;
@@ -377,23 +374,24 @@ __global__ void __launch_bounds__(kMvThreads, 24) k_evict_move(const __grid_cons
             }
             __syncthreads();
             if (!late) {
-                each([&](uint8_t *pool, int64_t, int64_t o, const uint8_t *at, int w) {
+#pragma unroll 4
+                for (uint32_t i = t; i < items; i += kMvThreads) {
+                    const uint32_t row = fast_div(i, a.word_div), w = i - row * words;
+                    if (from[row] < 0) continue;
+                    uint8_t *dst = (row < kMvRows ? c.k : c.v) + to[row];
+                    const uint8_t *at = rows + row * pitch;
                     if constexpr (VEC)
-                        *reinterpret_cast<uint4 *>(pool + o * EB + 16 * w) = reinterpret_cast<const uint4 *>(at)[w];
+                        *reinterpret_cast<uint4 *>(dst + 16 * w) = *reinterpret_cast<const uint4 *>(at + 16 * w);
                     else if constexpr (EB == 2)
-                        reinterpret_cast<uint16_t *>(pool)[o + w] = reinterpret_cast<const uint16_t *>(at)[w];
+                        reinterpret_cast<uint16_t *>(dst)[w] = reinterpret_cast<const uint16_t *>(at)[w];
                     else
-                        pool[o + w] = at[w];
-                });
-                if (EB == 1 && warp < 2 && from[0] >= 0) {
-                    int row_t;
-                    const int pt = cache_page(c, b, r, &row_t, kClassEvict);
-                    (warp ? c.vs : c.ks)[row_offset(warp ? c.vss : c.kss, pt, h, row_t)] = scales[warp][lane];
+                        dst[w] = at[w];
                 }
+                if (EB == 1 && f >= 0) (warp ? c.vs : c.ks)[scale_to] = scales[warp][lane];
             }
         }
         if (t == 0) next = coming;
-        __syncthreads();  // rows are free again
+        __syncthreads();  // rows, from and to are free again
         ticket = next;
         __syncthreads();
     }
@@ -420,6 +418,9 @@ template <int EB, bool VEC>
 int launch_evict(EvictArgs &a, cudaStream_t cs) {
     const int64_t units = int64_t(a.c.n_seqs) * a.c.heads;
     const int smem = 2 * kMvRows * ((a.c.dim * EB + 15) / 16 * 16);
+    a.unit_div = make_fastdiv(static_cast<uint32_t>(units));
+    a.head_div = make_fastdiv(static_cast<uint32_t>(a.c.heads));
+    a.word_div = make_fastdiv(static_cast<uint32_t>(VEC ? a.c.dim * EB / 16 : a.c.dim));
     int sms, per, move_per;
     // Selection: clusters where there are few units and many slots
     int parts = 1;
