@@ -20,7 +20,7 @@
 
 namespace lc {
 
-constexpr int kApThreads = 256;
+constexpr int kApThreads = 128;
 constexpr int64_t kApMany = 4 * 152 * 48;  // rows from which a warp takes four heads
 
 struct AppendArgs {
