@@ -40,25 +40,28 @@ __device__ __forceinline__ float value_of(uint32_t w) {
     return Q == 1 ? __uint_as_float(w << 16) : __half2float(__ushort_as_half(static_cast<uint16_t>(w)));
 }
 
+// x / d from d's rounded reciprocal (see above).
+__device__ __forceinline__ float rounded_quotient(float x, float d, float inverse) {
+    const float q = x * inverse;
+    return fmaf(fmaf(-q, d, x), inverse, q);
+}
+
 // One row's 16 elements a lane, as they were read, to the pool: Q 0 unchanged, 1 bfloat16 -> E4M3, 2 float16 -> E4M3.
 // NI: eights of elements a lane (rows of up to 128 NI).  VEC: lane l holds eights l and l + 16, else elements l + 16 j.
 template <int Q, bool VEC, int NI>
-__device__ __forceinline__ void put_row(const CacheArgs &c, bool is_v, int page, int h, int row, bool on,
-                                        const uint16_t (&w)[8 * NI]) {
+__device__ __forceinline__ void put_row(int dim, uint8_t *dst, float *scale_at, bool on, const uint16_t (&w)[8 * NI]) {
     const int lane = threadIdx.x & 15;
-    const int64_t to = row_offset(is_v ? c.vst : c.kst, page, h, row);
-    uint8_t *dst = (is_v ? c.v : c.k) + (Q ? to : 2 * to);
     if constexpr (Q == 0) {
         if (!on) return;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             if constexpr (VEC) {
-                if (8 * (lane + 16 * i) < c.dim)
+                if (8 * (lane + 16 * i) < dim)
                     *reinterpret_cast<uint4 *>(dst + 16 * (lane + 16 * i)) = reinterpret_cast<const uint4 *>(w)[i];
             } else {
 #pragma unroll
                 for (int j = 8 * i; j < 8 * i + 8; ++j)
-                    if (lane + 16 * j < c.dim) reinterpret_cast<uint16_t *>(dst)[lane + 16 * j] = w[j];
+                    if (lane + 16 * j < dim) reinterpret_cast<uint16_t *>(dst)[lane + 16 * j] = w[j];
             }
         }
     } else {
@@ -70,10 +73,8 @@ __device__ __forceinline__ void put_row(const CacheArgs &c, bool is_v, int page,
         top = max(top & 0xffffu, top >> 16);
 #pragma unroll
         for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const bool fine = top < (Q == 1 ? 0x7f80u : 0x7c00u);
-        const float scale = fine ? fmaxf(__fdiv_rn(value_of<Q>(top), 448.f), 1.17549435e-38f) : __int_as_float(0x7fc00000);
-        if (!on) return;
-        if (lane == 0) (is_v ? c.vs : c.ks)[row_offset(is_v ? c.vss : c.kss, page, h, row)] = scale;
+        const float most = value_of<Q>(top);
+        float scale;
         uint32_t code[4 * NI];
         auto encode = [&](auto &&quotient) {
 #pragma unroll
@@ -82,25 +83,30 @@ __device__ __forceinline__ void put_row(const CacheArgs &c, bool is_v, int page,
                     make_float2(quotient(value_of<Q>(w[2 * j])), quotient(value_of<Q>(w[2 * j + 1]))), __NV_SATFINITE,
                     __NV_E4M3);
         };
-        if (__all_sync(0xffffffffu, scale > 0x1p-100f && scale < 0x1p100f)) {
+        if (__all_sync(0xffffffffu, most > 0x1p-90f && most < 0x1p90f)) {
+            scale = rounded_quotient(most, 448.f, 1.f / 448.f);
             const float inverse = __frcp_rn(scale);
             encode([&](float x) {
-                const float q = x * inverse, y = fmaf(fmaf(-q, scale, x), inverse, q);
+                const float y = rounded_quotient(x, scale, inverse);
                 return __uint_as_float(__float_as_uint(y) | (__float_as_uint(x) & 0x80000000u));  // a zero keeps its sign
             });
         } else {
+            const bool fine = top < (Q == 1 ? 0x7f80u : 0x7c00u);
+            scale = fine ? fmaxf(__fdiv_rn(most, 448.f), 1.17549435e-38f) : __int_as_float(0x7fc00000);
             encode([&](float x) { return __fdiv_rn(x, scale); });
         }
+        if (!on) return;
+        if (lane == 0) *scale_at = scale;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             if constexpr (VEC) {
-                if (8 * (lane + 16 * i) < c.dim)
+                if (8 * (lane + 16 * i) < dim)
                     *reinterpret_cast<uint2 *>(dst + 8 * (lane + 16 * i)) =
                         make_uint2(code[4 * i] | code[4 * i + 1] << 16, code[4 * i + 2] | code[4 * i + 3] << 16);
             } else {
 #pragma unroll
                 for (int j = 8 * i; j < 8 * i + 8; ++j)
-                    if (lane + 16 * j < c.dim) dst[lane + 16 * j] = static_cast<uint8_t>(code[j / 2] >> (8 * (j & 1)));
+                    if (lane + 16 * j < dim) dst[lane + 16 * j] = static_cast<uint8_t>(code[j / 2] >> (8 * (j & 1)));
             }
         }
     }
@@ -157,8 +163,13 @@ __global__ void __launch_bounds__(kApThreads) k_cache_append(const __grid_consta
     int row;
     const int page = cache_page(c, b, n + t, &row, kClassAppend);
     if (page < 0) return;
+    const int64_t *st = is_v ? c.vst : c.kst, *sst = is_v ? c.vss : c.kss;
+    uint8_t *dst = (is_v ? c.v : c.k) + row_offset(st, page, h0, row) * (Q ? 1 : 2);
+    float *scale_at = Q ? (is_v ? c.vs : c.ks) + row_offset(sst, page, h0, row) : nullptr;
+    const int64_t dst_step = st[1] * (Q ? 1 : 2), scale_step = sst[1];
 #pragma unroll
-    for (int u = 0; u < U; ++u) put_row<Q, VEC, NI>(c, is_v, page, h0 + u, row, h0 + u < c.heads, w[u]);
+    for (int u = 0; u < U; ++u, dst += dst_step, scale_at += Q ? scale_step : 0)
+        put_row<Q, VEC, NI>(c.dim, dst, scale_at, h0 + u < c.heads, w[u]);
 }
 
 cudaError_t take_error_append(unsigned long long *v) { return take_module_error(v); }
