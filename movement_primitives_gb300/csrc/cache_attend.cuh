@@ -4,39 +4,41 @@
 // over the slots j that are seen.
 //
 // Mathematics.  One pass over the keys and values: a warp keeps, for up to 16
-// query heads of one key head, the running maximum m of the logits (in base
-// 2: x_j log2 e), the sum l of 2^(x_j - m) and the output o of the slots it
-// has taken, all in float32, and rescales l and o when m grows.  Parts
-// (m, l, o) of one row join as sums weighted by 2^(m - max m).
+// query heads of one key head, the running maximum m of the logits (in base 2:
+// x_j log2 e), the sum l of 2^(x_j - m) and the output o of the slots it has
+// taken, all in float32, and rescales l and o when m grows.  Parts (m, l, o)
+// of one row join as sums weighted by 2^(m - max m).
 //
 // Both products are warp-level matrix instructions (mma.sync m16n8k16) with
-// the cache as the 16-row operand: 16 slots x 16 columns of the keys by 8 query heads,
-// and 16 columns x 16 slots of the values by 8 query heads, so that
-// up to 8 query heads a key head cost one instruction where heads as
-// rows would cost two.  The logits' fragment becomes the second product's operand by one
-// 8 x 8 transpose across lanes (movmatrix) a slot octet.  With G query
-// heads a key head the pass does G operations a byte of 16-bit cache, so memory
-// bounds it up to the 16 heads of a unit and the accumulators fit
+// the cache as the 16-row operand: 16 slots x 16 columns of the keys by 8
+// query heads, and 16 columns x 16 slots of the values by 8 query heads, so
+// that up to 8 query heads a key head cost one instruction where heads as rows
+// would cost two.  The logits' fragment becomes the second product's operand
+// by one 8 x 8 transpose across lanes (movmatrix) a slot octet.  With G query
+// heads a key head the pass does G operations a byte of 16-bit cache, so
+// memory bounds it up to the 16 heads of a unit and the accumulators fit
 // registers.  The weights are rounded to the values' 16-bit type for the
-// second product (by at most 2^-9, or 2^-12 in float16, of each, no more
-// than the output's own rounding); the sum l takes them unrounded.
+// second product (by at most 2^-9, or 2^-12 in float16, of each, no more than
+// the output's own rounding); the sum l takes them unrounded.
 //
-// E4M3 codes are float16 numbers, converted exactly two at a time; their products run in
-// float16.  The keys' scales multiply the logits.  The values' scales s_j
-// join the weights as 2^(x_j + log2 |s_j| - mv), mv the running maximum of
-// that exponent: the largest weight is 1 whatever the scales, so float16
-// holds the others to 2^-12 of themselves, or to 2^-25 of the largest; o is kept relative to mv.
+// E4M3 codes are float16 numbers, converted exactly two at a time; their
+// products run in float16.  The keys' scales multiply the logits.  The values'
+// scales s_j join the weights as 2^(x_j + log2 |s_j| - mv), mv the running
+// maximum of that exponent: the largest weight is 1 whatever the scales, so
+// float16 holds the others to 2^-12 of themselves, or to 2^-25 of the largest;
+// o is kept relative to mv.
 //
 // Work.  Slots are taken in steps of TOK by one warp.  A (sequence, key head,
-// block of 16 query heads) is a unit; the steps of all units, laid end to end, are cut
-// into equal runs, one a warp, whatever the lengths: the warps find their
-// run from the lengths on the device.  A unit inside one run is finished there;
-// one that is cut leaves parts in the workspace, which k_attend_join joins
-// in their order, so results do not depend on timing.  Each warp streams its
-// run through a ring of its own in shared memory (cp.async, 16 bytes a lane,
-// rows swizzled for ldmatrix) that runs ahead across units, with no barrier
-// between warps.  Where units are few and short (kUnitSteps) a block or a cluster
-// of blocks takes one instead, joined in shared memory, with no second launch.
+// block of 16 query heads) is a unit; the steps of all units, laid end to end,
+// are cut into equal runs, one a warp, whatever the lengths: the warps find
+// their run from the lengths on the device.  A unit inside one run is finished
+// there; one that is cut leaves parts in the workspace, which k_attend_join
+// joins in their order, so results do not depend on timing.  Each warp streams
+// its run through a ring of its own in shared memory (cp.async, 16 bytes a
+// lane, rows swizzled for ldmatrix) that runs ahead across units, with no
+// barrier between warps.  Where units are few and short (kUnitSteps) a block
+// or a cluster of blocks takes one instead, joined in shared memory, with no
+// second launch.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -54,8 +56,8 @@ constexpr int kAtWarps = 4;
 constexpr int kAtThreads = 32 * kAtWarps;
 // Blocks of an SM (at least; registers) and steps in a warp's ring.  Measured
 // on 1.09 GB of bfloat16 (64 sequences of up to 8192 slots, dim 128) and on
-// 0.27 GB of dim 64: 2 blocks x 2 steps 168 and 51 us; x 3 steps 178 and 51;
-// 3 blocks x 2 steps 174 and 62.  More streams do not hide more latency, they
+// 0.27 GB of dim 64: 2 blocks x 2 steps 168 and 51 us; x 3 steps 178 and 51; 3
+// blocks x 2 steps 174 and 62.  More streams do not hide more latency, they
 // cost the memory its order.
 constexpr int kAtBlocks = 2, kAtStages = 2;
 constexpr int kAtRows = 16;        // query heads of a unit at most
@@ -64,19 +66,22 @@ constexpr int kAtMaxRuns = kAtMaxBlocks * kAtWarps;
 constexpr int kJoinLeast = 128, kJoinMost = 1024;  // threads of a joining block
 constexpr int kJoinRows = kJoinLeast / 32;  // rows of a block of the least width
 constexpr int kJoinFew = 32;       // parts of a row that one warp joins
-constexpr int kScorePer = 8;       // slots of a thread
+constexpr int kScorePer = 4;       // slots of a thread (4, 8, 16: 43.7, 45.4, 53 us
+                                   // of 32 E4M3 sequences with scores)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// A run takes at least this many steps: shorter ones leave more parts to join than
-// the further warps save.
-constexpr int kAtMinSteps = 2;
+// A run takes at least this many steps: shorter ones leave more parts to join
+// than the further warps save, longer ones leave warps idle.  Of 1, 2, 4, 6, 8
+// steps: one sequence of 32000 slots, 16 query heads on one key head 40, 36,
+// 25, 24, 24 us; of 8000 slots, 8 key heads 15.1, 15.1, 14.7, 16.9, 18.4.
+constexpr int kAtMinSteps = 4;
 // A unit is one block's, or a cluster's of up to kUnitCluster blocks while
 // there are kUnitBlocks at most, where a warp then takes kUnitSteps steps or
 // fewer: one launch and no parts in memory, but units of unlike lengths are
 // not evened out.  GPU time against runs: 8 units of 64 steps of 16 KiB 13.5
 // and 19.9 us; 96 units of up to 50 steps of 5 KiB 12.1 and 12.1 (the host
-// saves 5 us of a launch); at 16 steps a warp, 84 units of up to 125 steps 24.5
-// and 14.9, 128 units of up to 128 steps of 8 KiB 25.9 and 21.5.
+// saves 5 us of a launch); at 16 steps a warp, 84 units of up to 125 steps
+// 24.5 and 14.9, 128 units of up to 128 steps of 8 KiB 25.9 and 21.5.
 constexpr int kUnitSteps = 8, kUnitBlocks = 304, kUnitCluster = 8;
 
 struct AttendArgs {
@@ -106,7 +111,8 @@ struct AttendArgs {
     FastDiv chunk_div, head_div, q_div, group_div;
 };
 
-// Steps in a warp's ring where a unit is a block's: few steps, whose latency counts.
+// Steps in a warp's ring where a unit is a block's: few steps, whose latency
+// counts.
 template <int DP, int KV>
 constexpr int kUnitStages = DP * (KV == LC_CACHE_E4M3 ? 1 : 2) > 256 ? 2 : 3;
 
@@ -203,7 +209,8 @@ __device__ __forceinline__ int seen_from(const AttendArgs &a, int b, int *n) {
     return a.window && a.window < *n ? *n - a.window : 0;
 }
 
-// A place in the steps of all units: step `t` of `steps` of unit `unit` of sequence b.
+// A place in the steps of all units: step `t` of `steps` of unit `unit` of
+// sequence b.
 struct Place {
     int b, unit, t, steps, lo, n;
 };
@@ -257,13 +264,15 @@ struct Attend {
         return S::RB >= 128 ? (chunk ^ (row & 7)) * 16 : (chunk ^ (row >> 1 & 3)) * 16;
     }
 
-    // The value column that row g (+ 8 i) of 16-wide piece c stands for: E4M3 columns come in adjacent pairs.
+    // The value column that row g (+ 8 i) of 16-wide piece c stands for: E4M3
+    // columns come in adjacent pairs.
     __device__ __forceinline__ static int col_of(int c, int g, int i) {
         return Q8 ? 16 * c + 2 * g + i : 16 * c + g + 8 * i;
     }
 
-    // Query heads as the 16 x 8 operand: head lane / 4, columns k = 2q, 2q + 1, 2q + 8, 2q + 9 of each 16-wide
-    // piece; for E4M3 keys, which come four adjacent columns a lane, 4q .. 4q + 3.
+    // Query heads as the 16 x 8 operand: head lane / 4, columns k = 2q, 2q +
+    // 1, 2q + 8, 2q + 9 of each 16-wide piece; for E4M3 keys, which come four
+    // adjacent columns a lane, 4q .. 4q + 3.
     __device__ __forceinline__ void load_q() {
         const int q = lane & 3;
 #pragma unroll
@@ -294,8 +303,9 @@ struct Attend {
             }
         }
         if constexpr (Q8) {
-            // bfloat16 to float16, each head divided by the power of two at or below its largest magnitude: exact but for
-            // elements below 2^-14 of it, which are off by at most 2^-25 of it
+            // bfloat16 to float16, each head divided by the power of two at or below its largest
+            // magnitude: exact but for elements below 2^-14 of it, which are off by at most 2^-25
+            // of it
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 uint32_t top = 0;
@@ -322,7 +332,8 @@ struct Attend {
         }
     }
 
-    // Reads the page of this lane's slot of the step that starts at slot j0 of sequence pb.
+    // Reads the page of this lane's slot of the step that starts at slot j0 of
+    // sequence pb.
     __device__ __forceinline__ void find_pages(int pb, int head, int j0, int n) {
         const int j = j0 + lane;
         next_page = -1;
@@ -410,7 +421,8 @@ struct Attend {
         load_q();
     }
 
-    // Takes the step in `stage`, the unit's slots from `at` on (counted from the first seen).
+    // Takes the step in `stage`, the unit's slots from `at` on (counted from
+    // the first seen).
     __device__ __forceinline__ void take(int stage, int at) {
         const uint32_t bits = seen_bits[stage];
         if (!a.logits && bits == 0) return;
@@ -418,7 +430,8 @@ struct Attend {
         const uint32_t ks_s = ring_s + stage * (S::STEP + S::SC), vs_s = ks_s + S::TOK * S::RB;
         const float *scales = reinterpret_cast<const float *>(ring + stage * (S::STEP + S::SC) + S::STEP);
 
-        // logits: x[t][g][0, 1] of slot 16 t + lane / 4, [2, 3] of the slot 8 on; query heads 8 g + 2 q, + 1
+        // logits: x[t][g][0, 1] of slot 16 t + lane / 4, [2, 3] of the slot 8 on; query heads 8 g +
+        // 2 q, + 1
         float x[MT][NG][4];
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
@@ -565,7 +578,8 @@ struct Attend {
                 p[g][1] = transpose8(pack2<M16>(x[t][g][2], x[t][g][3]));
             }
             if constexpr (Q8) {
-                // slots 0-7 and 8-15 of two 16-wide pieces; a register holds two adjacent columns of two slots
+                // slots 0-7 and 8-15 of two 16-wide pieces; a register holds two adjacent columns
+                // of two slots
                 const int row = 16 * t + (lane & 7) + (mat & 1) * 8;
 #pragma unroll
                 for (int c = 0; c < KS; c += 2) {
@@ -666,7 +680,8 @@ __global__ void __launch_bounds__(kAtThreads, kAtBlocks) k_attend(const __grid_c
     const int units = a.c.heads * a.row_blocks;
     start_after_prior();
 
-    // the steps up to the sequences of each thread: thread t stands for `per` of them
+    // the steps up to the sequences of each thread: thread t stands for `per`
+    // of them
     const int per = (a.c.n_seqs + kAtThreads - 1) / kAtThreads;
     long long incl = 0;
     for (int b = min(t * per, a.c.n_seqs); b < min(t * per + per, a.c.n_seqs); ++b) {
@@ -910,7 +925,8 @@ __global__ void __launch_bounds__(kAtThreads) k_attend_unit(const __grid_constan
     if (parts > 1) cluster.sync();  // no block leaves while another reads its shared memory
 }
 
-// One warp instantiation's launches: one block a unit (VEC only), or one run a warp.
+// One warp instantiation's launches: one block a unit (VEC only), or one run a
+// warp.
 template <int DP, int KV, int NG, bool VEC>
 int launch_attend(const AttendArgs &a, int unit_blocks, int *runs, cudaStream_t cs) {
     using S = AtShape<DP, KV, NG, kAtStages>;
@@ -926,7 +942,8 @@ int launch_attend(const AttendArgs &a, int unit_blocks, int *runs, cudaStream_t 
     }
     const void *fn = reinterpret_cast<const void *>(&k_attend<DP, KV, NG, VEC>);
     if (prepare(fn, kAtThreads, S::SMEM, S::SMEM, &sms, &per) != cudaSuccess) return LC_ERR_CUDA;
-    // no more blocks than are resident at once, nor than the steps of full sequences
+    // no more blocks than are resident at once, nor than the steps of full
+    // sequences
     const int64_t most = units * ((a.c.cap + S::TOK - 1) / S::TOK);
     const int64_t grid = std::max<int64_t>(
         1, std::min<int64_t>({int64_t(sms) * per, kAtMaxBlocks,
@@ -935,7 +952,8 @@ int launch_attend(const AttendArgs &a, int unit_blocks, int *runs, cudaStream_t 
     return launch_after(fn, static_cast<unsigned>(grid), kAtThreads, S::SMEM, cs, &a);
 }
 
-// The main launch for one cache type; `runs` receives the runs of a launch by runs.
+// The main launch for one cache type; `runs` receives the runs of a launch by
+// runs.
 template <int KV>
 int launch_attend_type(const AttendArgs &a, int unit_blocks, bool vec, int *runs, cudaStream_t cs) {
     auto heads = [&](auto dp) {

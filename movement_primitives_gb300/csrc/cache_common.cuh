@@ -17,10 +17,10 @@ namespace lc {
 // Kernel classes in the device error word.
 constexpr uint32_t kClassAppend = 0xf0, kClassAttend = 0xf1, kClassEvict = 0xf2;
 
-// Kernels are launched to overlap the end of what precedes them on the
-// stream (launch_after): the next one may be set up as soon as every block
-// has come here, and this one touches no memory until all before it has
-// ended and is visible.
+// Kernels are launched to overlap the end of what precedes them on the stream
+// (launch_after): the next one may be set up as soon as every block has come
+// here, and this one touches no memory until all before it has ended and is
+// visible.
 __device__ __forceinline__ void start_after_prior() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -44,8 +44,8 @@ __device__ __forceinline__ int cache_length(const CacheArgs &c, const int32_t *l
     return m;
 }
 
-// Page of slot j (0 <= j < cap) of sequence b, -1 when the table names none
-// in the pool; `row` receives the slot's row in it.
+// Page of slot j (0 <= j < cap) of sequence b, -1 when the table names none in
+// the pool; `row` receives the slot's row in it.
 __device__ __forceinline__ int cache_page(const CacheArgs &c, int b, int j, int *row, uint32_t cls) {
     const int i = static_cast<int>(fast_div(static_cast<uint32_t>(j), c.page_div));
     *row = j - i * c.page;

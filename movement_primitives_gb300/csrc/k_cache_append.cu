@@ -3,17 +3,17 @@
 // Row (b, t, h) of the new keys and values goes to slot lengths[b] + t of
 // sequence b, as it is or quantised to E4M3:
 //     scale = max(max_e |x_e| / 448, 2^-126),  code_e = e4m3(x_e / scale)
-// in float32 (division and conversion round to nearest even), NaN as the
-// scale where the largest magnitude is not finite.  A row's quotients share
-// their divisor: with its rounded reciprocal r, q = x r and q + (x - q scale) r
-// in fused operations is the rounded quotient (Markstein, "Computation of
+// in float32 (division and conversion round to nearest even), NaN as the scale
+// where the largest magnitude is not finite.  A row's quotients share their
+// divisor: with its rounded reciprocal r, q = x r and q + (x - q scale) r in
+// fused operations is the rounded quotient (Markstein, "Computation of
 // elementary functions on the IBM RISC System/6000 processor", 1990), three
 // operations for a division's many; scales far out of range divide.
 //
 // One warp moves a token's rows of U heads in both pools: lanes 0-15 the
 // keys', 16-31 the values', each lane 16 bytes of new elements at a time, the
-// loads of all U heads before the first store.  Bound by memory: every byte
-// is read and written once.
+// loads of all U heads before the first store.  Bound by memory: every byte is
+// read and written once.
 #include <cuda_fp8.h>
 
 #include "cache_common.cuh"
@@ -46,8 +46,10 @@ __device__ __forceinline__ float rounded_quotient(float x, float d, float invers
     return fmaf(fmaf(-q, d, x), inverse, q);
 }
 
-// One row's 16 elements a lane, as they were read, to the pool: Q 0 unchanged, 1 bfloat16 -> E4M3, 2 float16 -> E4M3.
-// NI: eights of elements a lane (rows of up to 128 NI).  VEC: lane l holds eights l and l + 16, else elements l + 16 j.
+// One row's 16 elements a lane, as they were read, to the pool: Q 0 unchanged,
+// 1 bfloat16 -> E4M3, 2 float16 -> E4M3. NI: eights of elements a lane (rows
+// of up to 128 NI).  VEC: lane l holds eights l and l + 16, else elements l +
+// 16 j.
 template <int Q, bool VEC, int NI>
 __device__ __forceinline__ void put_row(int dim, uint8_t *dst, float *scale_at, bool on, const uint16_t (&w)[8 * NI]) {
     const int lane = threadIdx.x & 15;

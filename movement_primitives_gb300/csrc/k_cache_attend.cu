@@ -1,13 +1,15 @@
-// Cache attention: the joining of parts, the workspace and the C entry
-// points (lc_cache_attend; the main kernels are cache_attend.cuh).
+// Cache attention: the joining of parts, the workspace and the C entry points
+// (lc_cache_attend; the main kernels are cache_attend.cuh).
 #include "cache_attend.cuh"
 
 namespace lc {
 
-// The whole row's maximum and sum of exponentials of a unit that was cut, by one warp from its parts.
+// The whole row's maximum and sum of exponentials of a unit that was cut, by
+// one warp from its parts.
 struct Parts {
     int first, count;
-    // the unit's first part is its run's second (the unit starts there), the others their runs' first
+    // the unit's first part is its run's second (the unit starts there), the
+    // others their runs' first
     __device__ __forceinline__ int slot(int i) const { return 2 * (first + i) + (i == 0); }
 };
 
@@ -39,7 +41,8 @@ __device__ __forceinline__ float2 join_ml(const AttendArgs &a, const Parts &p, i
     return make_float2(most, sum);
 }
 
-// scores[b, h, j] += sum over the group's query heads of 2^(logit - lse), for one chunk of slots.
+// scores[b, h, j] += sum over the group's query heads of 2^(logit - lse), for
+// one chunk of slots.
 __device__ __forceinline__ void add_scores(const AttendArgs &a, uint32_t at, float *lse) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, threads = blockDim.x;
     const int units = a.c.heads * a.row_blocks;
@@ -87,11 +90,11 @@ __device__ __forceinline__ void add_scores(const AttendArgs &a, uint32_t at, flo
 }
 
 // The first score_blocks blocks (with scores), one a (sequence, key head,
-// chunk of slots), add the weights.  The join_blocks after them join the parts of the rows
-// (sequence, query head) whose units were cut, in their order, and write the
-// zeros of sequences with nothing to see: warp w of the i-th takes row i + w
-// join_blocks (w < join_rows); a row of many parts is left for the whole
-// block, several parts at a time.
+// chunk of slots), add the weights.  The join_blocks after them join the parts
+// of the rows (sequence, query head) whose units were cut, in their order, and
+// write the zeros of sequences with nothing to see: warp w of the i-th takes
+// row i + w join_blocks (w < join_rows); a row of many parts is left for the
+// whole block, several parts at a time.
 template <bool F16>
 __global__ void __launch_bounds__(kJoinMost) k_attend_join(const __grid_constant__ AttendArgs a) {
     extern __shared__ float acc[];  // four floats a thread
@@ -212,7 +215,8 @@ bool attend_space(const lc_paged_cache &cache, const CacheArgs &c, int q_heads, 
              rows_aligned(cache.v, 3, pool, cache.v_stride, eb, 16);
     const int tok = step_slots(c.dim, cache.type), group = q_heads / c.heads;
     const int64_t units = c.heads * ((int64_t(group) + kAtRows - 1) / kAtRows), heads = int64_t(c.n_seqs) * q_heads;
-    // scores of a key head whose query heads are several units' need the second launch
+    // scores of a key head whose query heads are several units' need the
+    // second launch
     s->unit_blocks = 0;
     const int64_t steps = ((window ? std::min(window, c.cap) : c.cap) + int64_t(tok) - 1) / tok;
     if (s->vec && !(scores && group > kAtRows)) {
@@ -314,8 +318,9 @@ extern "C" int lc_cache_attend(const lc_paged_cache *cache, const lc_cache_query
                                                       : launch_attend_e4m3;
     st = launch(a, space.unit_blocks, space.vec, &runs, cs);
     if (st || space.unit_blocks) return st;
-    // a row a block, as wide as lets all rows run at once: few rows have many parts each, which a wide block reads more
-    // of at a time; rows past that share blocks of the least width, a warp each
+    // a row a block, as wide as lets all rows run at once: few rows have many
+    // parts each, which a wide block reads more of at a time; rows past that
+    // share blocks of the least width, a warp each
     const int64_t rows = qext[0] * qext[1];
     int threads = kJoinMost;
     while (threads > kJoinLeast && rows * threads > 152 * 1024) threads /= 2;

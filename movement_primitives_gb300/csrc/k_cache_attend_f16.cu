@@ -1,4 +1,5 @@
-// Cache attention over float16 pages (one translation unit a cache type keeps the build parallel).
+// Cache attention over float16 pages (one translation unit a cache type keeps
+// the build parallel).
 #include "cache_attend.cuh"
 
 namespace lc {

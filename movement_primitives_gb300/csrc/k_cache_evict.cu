@@ -1,26 +1,27 @@
-// Eviction from a paged key-value cache by accumulated weight (lc_cache_evict).
+// Eviction from a paged key-value cache by accumulated weight
+// (lc_cache_evict).
 //
-// Per sequence and key head (a unit), of n > budget slots: the `recent`
-// newest stay, and of the others the budget - recent of largest score, equal
-// scores in slot order.
+// Per sequence and key head (a unit), of n > budget slots: the `recent` newest
+// stay, and of the others the budget - recent of largest score, equal scores
+// in slot order.
 //
 // k_evict_select, a block or a cluster of blocks a unit, finds the score of
 // the last slot kept by radix selection on an order-preserving 32-bit key
 // (digits of 11, 11 and 10 bits from the top, the first one's histogram made
 // as the scores come in), then writes the kept slots in ascending order
 // (`kept`) with their scores.  The scores are read from memory once and their
-// keys kept in shared memory; the blocks of a cluster take a run of slots
-// each and add up their histograms through distributed shared memory.
+// keys kept in shared memory; the blocks of a cluster take a run of slots each
+// and add up their histograms through distributed shared memory.
 //
 // k_evict_move moves the rows, 32 ranks (a chunk) a block at a time.  Rows
 // move in place: the r-th kept slot goes to slot r, and kept[r] >= r, so slot
-// r may still hold a row that a rank j < r has yet to read, never one of a later
-// rank.  A chunk therefore reads its rows into shared memory without
-// waiting, publishes that it has, and before writing waits for the chunks that hold the
-// ranks of the slots it writes over (at most two, which the selection
-// leaves in `rank_at`).  Chunks are handed out in order by an atomic
-// counter, and waits go to lower chunks only, whose reads wait for nothing:
-// no wait can be circular, whichever blocks run.  Memory bounds it: every row that moves
+// r may still hold a row that a rank j < r has yet to read, never one of a
+// later rank.  A chunk therefore reads its rows into shared memory without
+// waiting, publishes that it has, and before writing waits for the chunks that
+// hold the ranks of the slots it writes over (at most two, which the selection
+// leaves in `rank_at`).  Chunks are handed out in order by an atomic counter,
+// and waits go to lower chunks only, whose reads wait for nothing: no wait can
+// be circular, whichever blocks run.  Memory bounds it: every row that moves
 // is read and written once.
 #include <cooperative_groups.h>
 
@@ -63,7 +64,8 @@ __device__ __forceinline__ uint32_t score_key(float s) {
     return u >> 31 ? ~u : u | 0x80000000u;
 }
 
-// From the largest down: the one of 32 lanes' counts that holds the need-th, and how many of it are needed.
+// From the largest down: the one of 32 lanes' counts that holds the need-th,
+// and how many of it are needed.
 __device__ __forceinline__ int pick(uint32_t count, uint32_t *need) {
     const int lane = threadIdx.x & 31;
     uint32_t upto = count;  // lanes lane .. 31
@@ -78,8 +80,8 @@ __device__ __forceinline__ int pick(uint32_t count, uint32_t *need) {
     return at;
 }
 
-// HELD: the keys of a block's slots fit its shared memory; else every pass reads the scores again.
-// THREADS: 512, two blocks an SM, or 1024.
+// HELD: the keys of a block's slots fit its shared memory; else every pass
+// reads the scores again. THREADS: 512, two blocks an SM, or 1024.
 template <bool HELD, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_evict_select(const __grid_constant__ EvictArgs a) {
     constexpr int kWarps = THREADS / 32;
@@ -128,7 +130,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_evict_select(const 
     const int c1 = max(min(s1, cand), s0);  // this block's competing ones end there
     auto key_of = [&](int i) { return HELD ? keys[i - s0] : score_key(scores[i]); };
 
-    // the key of the last slot kept among the competing, and how many with that key stay
+    // the key of the last slot kept among the competing, and how many with
+    // that key stay
     uint32_t need = a.budget - a.recent, prefix = 0;
     const bool any = need > 0;
     for (int i = t; i < kSelBins; i += THREADS) hist[0][i] = 0;
@@ -187,7 +190,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_evict_select(const 
             prefix = prefix << bits | chosen[pass][0];
             need = chosen[pass][1];
             if (chosen[pass][2]) {
-                // every key from this prefix up stays (it is above 0: not all that compete stay), none of a tie
+                // every key from this prefix up stays (it is above 0: not all that compete stay),
+                // none of a tie
                 prefix = (prefix << shift) - 1;
                 need = 0;
                 break;
@@ -196,8 +200,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_evict_select(const 
     } else {
         __syncthreads();
     }
-    // Slots in order, 32 at a time: `sure` are kept whatever else, of the `tied` ones the first `need`.  Each warp counts
-    // its run's, then writes from the counts before it.
+    // Slots in order, 32 at a time: `sure` are kept whatever else, of the
+    // `tied` ones the first `need`.  Each warp counts its run's, then writes
+    // from the counts before it.
     const int w0 = static_cast<int>(lmin(s0 + int64_t(warp) * run, s1)), w1 = static_cast<int>(lmin(w0 + int64_t(run), s1));
     uint32_t sure = 0, tied = 0;
 #pragma unroll 4
@@ -233,8 +238,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_evict_select(const 
                 tied += other[1];
             }
     }
-    // whole steps of competing slots; where no key is tied and the kept ones are positive scores, whose
-    // keys stand for them, the ranks are those of the sure ones alone
+    // whole steps of competing slots; where no key is tied and the kept ones
+    // are positive scores, whose keys stand for them, the ranks are those of
+    // the sure ones alone
     const bool plain = any && prefix >= 0x80000000u;
     for (int i0 = w0; i0 < w1; i0 += 32 * kSelAhead) {
         uint32_t key[kSelAhead];
@@ -284,7 +290,8 @@ __device__ __forceinline__ void store_release(uint32_t *p, uint32_t v) {
     asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
-// VEC: rows are whole 16-byte words on 16-byte boundaries; else they move an element at a time.
+// VEC: rows are whole 16-byte words on 16-byte boundaries; else they move an
+// element at a time.
 template <int EB, bool VEC>
 __global__ void __launch_bounds__(kMvThreads, 16) k_evict_move(const __grid_constant__ EvictArgs a) {
     extern __shared__ __align__(16) uint8_t rows[];  // [pool][row][pitch]
@@ -478,7 +485,8 @@ extern "C" int lc_cache_evict(const lc_paged_cache *cache, const lc_cache_evicti
     if (!rows_apart(2, ext, e->new_scores_stride, std::max(a.c.cap, 1)) || !rows_apart(2, ext, e->kept_stride, e->budget))
         return LC_ERR_NOT_INJECTIVE;
     const int64_t units = ext[0] * ext[1], chunks = (int64_t(e->budget) + kMvRows - 1) / kMvRows;
-    // the tickets that running blocks draw past the last one stay in 32 bits too
+    // the tickets that running blocks draw past the last one stay in 32 bits
+    // too
     if (units > 0x0fffffff || units * chunks > 0xf0000000ll) return LC_ERR_OVERFLOW;
     const EvictSpace space = evict_space(a.c, e->budget);
     if (!e->workspace) return LC_ERR_NULL;
