@@ -50,7 +50,7 @@ typedef struct {
     float *k_scale, *v_scale;    /* E4M3 only, else NULL */
     const int32_t *page_table;   /* [n_seqs, pages_per_seq], rows table_stride apart */
     int64_t table_stride;
-    int64_t n_pages;             /* of the pools */
+    int64_t n_pages;             /* of the pools; at least 1 where sequences have slots */
     int32_t type;                /* lc_cache_type */
     int32_t n_seqs;
     int32_t n_kv_heads;

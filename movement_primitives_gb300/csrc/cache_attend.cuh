@@ -19,14 +19,16 @@
 // memory bounds it up to the 16 heads of a unit and the accumulators fit
 // registers.  The weights are rounded to the values' 16-bit type for the
 // second product (by at most 2^-9, or 2^-12 in float16, of each, no more than
-// the output's own rounding); the sum l takes them unrounded.
+// the output's own rounding); the sum l takes them unrounded.  Float16 has few
+// exponents, so its weights are lifted by 2^14: the largest is 2^14, and one of
+// 2^-38 of it is still held to a bit, so that a million slots together lose
+// nothing to an outlier above them.
 //
 // E4M3 codes are float16 numbers, converted exactly two at a time; their
 // products run in float16.  The keys' scales multiply the logits.  The values'
 // scales s_j join the weights as 2^(x_j + log2 |s_j| - mv), mv the running
-// maximum of that exponent: the largest weight is 1 whatever the scales, so
-// float16 holds the others to 2^-12 of themselves, or to 2^-25 of the largest;
-// o is kept relative to mv.
+// maximum of that exponent (lifted as above): the largest weight is the same
+// whatever the scales; o is kept relative to mv.
 //
 // Work.  Slots are taken in steps of TOK by one warp.  A (sequence, key head,
 // block of 16 query heads) is a unit; the steps of all units, laid end to end,
@@ -239,6 +241,7 @@ struct Attend {
     using S = AtShape<DP, KV, NG, STAGES>;
     static constexpr bool F16 = KV == LC_CACHE_F16, Q8 = KV == LC_CACHE_E4M3;
     static constexpr bool M16 = F16 || Q8;       // the matrix instructions' type is float16
+    static constexpr float kLift = M16 ? 14.f : 0.f;  // log2 of the largest weight of the second product
     static constexpr int KS = DP / 16;           // 16-wide pieces of a row
     static constexpr int MT = S::TOK / 16;       // 16-slot pieces of a step
 
@@ -525,7 +528,7 @@ struct Attend {
                         grown = true;
                     }
                 }
-                const float safe = m[g][u] == -INFINITY ? 0.f : m[g][u];
+                const float safe = m[g][u] == -INFINITY ? 0.f : m[g][u] - (Q8 ? 0.f : kLift);
                 float sum = 0.f;
                 if constexpr (Q8) {
                     float topv = -INFINITY;
@@ -543,7 +546,7 @@ struct Attend {
                         mv[g][u] = topv;
                         grown = true;
                     }
-                    const float safe_v = mv[g][u] == -INFINITY ? 0.f : mv[g][u];
+                    const float safe_v = mv[g][u] == -INFINITY ? 0.f : mv[g][u] - kLift;
 #pragma unroll
                     for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -615,8 +618,9 @@ struct Attend {
             for (int u = 0; u < 2; ++u) {
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) l[g][u] += __shfl_xor_sync(0xffffffffu, l[g][u], d);
+                if constexpr (F16) m[g][u] -= kLift;  // what l and o are relative to
                 if constexpr (Q8) {
-                    const float f = mv[g][u] == -INFINITY ? 0.f : exp2f(mv[g][u] - m[g][u]);
+                    const float f = mv[g][u] == -INFINITY ? 0.f : exp2f(mv[g][u] - kLift - m[g][u]);
 #pragma unroll
                     for (int c = 0; c < KS; ++c) {
                         o[c][g][u] *= f;

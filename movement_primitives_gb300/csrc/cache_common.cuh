@@ -119,6 +119,7 @@ inline int check_cache(const lc_paged_cache *c, bool write, CacheArgs *a) {
         c->head_dim > LC_CACHE_MAX_DIM || c->pages_per_seq < 0 || c->n_pages < 0 || c->n_pages > 0x7fffffff)
         return LC_ERR_SHAPE;
     if (int64_t(c->page_size) * c->pages_per_seq > 0x7fff0000) return LC_ERR_OVERFLOW;
+    if (c->n_seqs > 0 && c->pages_per_seq > 0 && c->n_pages < 1) return LC_ERR_SHAPE;
     if (c->n_pages > 0 && (!c->k || !c->v)) return LC_ERR_NULL;
     if (c->n_seqs > 0 && c->pages_per_seq > 0 && !c->page_table) return LC_ERR_NULL;
     const bool q8 = c->type == LC_CACHE_E4M3;

@@ -161,6 +161,7 @@ BAD_CACHES = [
     (dict(k_scale=BASE, v_scale=BASE), "LC_ERR_TYPE"), (dict(n_kv_heads=0), "LC_ERR_SHAPE"),
     (dict(page_size=0), "LC_ERR_SHAPE"), (dict(head_dim=0), "LC_ERR_SHAPE"), (dict(head_dim=257), "LC_ERR_SHAPE"),
     (dict(n_seqs=-1), "LC_ERR_SHAPE"), (dict(pages_per_seq=-1), "LC_ERR_SHAPE"), (dict(n_pages=-1), "LC_ERR_SHAPE"),
+    (dict(n_pages=0), "LC_ERR_SHAPE"),
     (dict(k=BASE + 1), "LC_ERR_ALIGN"), (dict(page_table=BASE + 2), "LC_ERR_ALIGN"),
     (dict(k_stride=(4096, -1, 64)), "LC_ERR_BAD_STRIDE"), (dict(table_stride=-1), "LC_ERR_BAD_STRIDE"),
     (dict(v_stride=(1 << 61, 1024, 64)), "LC_ERR_OVERFLOW"),

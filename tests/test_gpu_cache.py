@@ -274,6 +274,32 @@ def test_attend_growing_maximum():
     check_attend(s, q, out, lse, scale=1.0)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "e4m3"])
+def test_attend_many_small_weights_under_one_large(kind):
+    """One slot's logit 18 above all the others': each of those weighs 2^-26 of it, together half a
+    thousandth, which no 16-bit weight may lose."""
+    n = 40000
+    s = Setup([n], heads=1, dim=64, page=100, kind=kind, seed=15)
+    table = s.table[0].long()
+    if kind == "e4m3":
+        s.k.view(torch.uint8).zero_()
+        s.v.view(torch.uint8).copy_((torch.ones_like(s.v, dtype=torch.float32)).to(torch.float8_e4m3fn).view(torch.uint8))
+        s.scales[0].fill_(1.0)
+        s.scales[1].fill_(0.01)
+    else:
+        s.k.zero_()
+        s.v.fill_(0.01)
+    top = torch.full((64,), 2.25).to(s.k.dtype)
+    at = (int(table[3]), 0, 17)
+    (s.k.view(torch.uint8) if kind == "e4m3" else s.k)[at] = (top.view(torch.uint8) if kind == "e4m3" else top).cuda()
+    s.v.view(torch.uint8 if kind == "e4m3" else s.v.dtype)[at] = 0
+    q = torch.full((1, 2, 64), 1.0, dtype=IO[kind], device="cuda")
+    lse = torch.empty((1, 2), device="cuda")
+    out = lc().cache_attend(s.cache, q, s.lengths, scale=0.125, lse=lse)
+    check_attend(s, q, out, lse, scale=0.125)
+    assert torch.all(out > 0.01 * 5e-4)
+
+
 def test_attend_offsets_past_32_bits():
     """Pages more than 2^32 elements apart."""
     gap = 2_500_000_000
