@@ -12,8 +12,13 @@
 //
 // One warp moves a token's rows of U heads in both pools: lanes 0-15 the
 // keys', 16-31 the values', each lane 16 bytes of new elements at a time, the
-// loads of all U heads before the first store.  Bound by memory: every byte is
-// read and written once.
+// loads of all U heads before the first store.  Every byte is read and written
+// once.
+//
+// Measured on GB300: 64 tokens of 8 heads of 128 as they are 2.0 us, the
+// latency of three dependent reads; prompts of 8966 tokens into E4M3, 56 MB,
+// 16 us (3.4 TB/s), bound by the instructions of the quotients and the
+// rounding (issue slots 70 % busy), one head a warp 29 us, two 22, eight 21.
 #include <cuda_fp8.h>
 
 #include "cache_common.cuh"

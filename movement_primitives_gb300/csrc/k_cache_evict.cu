@@ -21,8 +21,15 @@
 // hold the ranks of the slots it writes over (at most two, which the selection
 // leaves in `rank_at`).  Chunks are handed out in order by an atomic counter,
 // and waits go to lower chunks only, whose reads wait for nothing: no wait can
-// be circular, whichever blocks run.  Memory bounds it: every row that moves
-// is read and written once.
+// be circular, whichever blocks run.  Every row that moves is read and written
+// once.
+//
+// Measured on GB300: 15 sequences of up to 16384 bfloat16 slots of 8 heads cut
+// to 4096, 403 MB moved, 93 us: the selection 21 us (bound by the latency of
+// its passes over the keys, each a barrier of the cluster), the move 72 us (5.6
+// TB/s).  One sequence of 131071 E4M3 slots cut to 32768, 138 MB, 62 us: 27 us
+// of selection on 64 blocks, 35 us of rows of 128 bytes.  Four sequences of
+// 1500 cut to 1024, 34 MB, 20 us.
 #include <cooperative_groups.h>
 
 #include "cache_common.cuh"
