@@ -440,7 +440,7 @@ int launch_evict(EvictArgs &a, cudaStream_t cs) {
     int parts = 1;
     if (prepare(reinterpret_cast<const void *>(&k_evict_move<EB, VEC>), kMvThreads, smem, smem, &sms, &move_per) != cudaSuccess)
         return LC_ERR_CUDA;
-    while (parts < kSelCluster && units * parts <= sms && a.c.cap / (2 * parts) >= kSelLeast) parts *= 2;
+    while (parts < kSelCluster && units * parts * 2 <= sms && a.c.cap / (2 * parts) >= kSelLeast) parts *= 2;
     const int rounds = a.c.cap ? (a.c.cap - 1) / kSelRound + 1 : 0;
     const int64_t hold = int64_t(rounds + parts - 1) / parts * kSelRound;
     const bool held = hold <= kSelKeys;
