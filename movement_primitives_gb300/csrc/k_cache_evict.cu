@@ -41,7 +41,6 @@ namespace cg = cooperative_groups;
 constexpr int kSelBins = 2048;      // 64 groups of 32
 constexpr int kSelRound = 2048;     // slots are dealt to blocks in so many
 constexpr int kSelKeys = 48 * 1024; // keys a block holds in shared memory
-constexpr int kSelAhead = 4;        // keys a lane has at hand in the ordered pass
 constexpr int kSelCluster = 8;      // blocks of a unit at most
 constexpr int kSelLeast = 4096;     // slots a block of a cluster has at least
 constexpr int kMvThreads = 64;        // a warp a pool where the rows' places are found
@@ -92,7 +91,7 @@ __device__ __forceinline__ int pick(uint32_t count, uint32_t *need) {
 template <bool HELD, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_evict_select(const __grid_constant__ EvictArgs a) {
     constexpr int kWarps = THREADS / 32;
-    extern __shared__ uint32_t keys[];
+    extern __shared__ __align__(16) uint32_t keys[];
     __shared__ uint32_t hist[2][kSelBins], groups[2][64], chosen[3][3], counts[2];
     __shared__ uint2 warp_counts[kWarps];
     cg::cluster_group cluster = cg::this_cluster();
@@ -207,9 +206,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_evict_select(const 
     } else {
         __syncthreads();
     }
-    // Slots in order, 32 at a time: `sure` are kept whatever else, of the
-    // `tied` ones the first `need`.  Each warp counts its run's, then writes
-    // from the counts before it.
+    // Slots in order: `sure` are kept whatever else, of the `tied` ones the
+    // first `need`.  Each warp counts its run's, then writes from the counts
+    // before it.
     const int w0 = static_cast<int>(lmin(s0 + int64_t(warp) * run, s1)), w1 = static_cast<int>(lmin(w0 + int64_t(run), s1));
     uint32_t sure = 0, tied = 0;
 #pragma unroll 4
@@ -245,45 +244,51 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_evict_select(const 
                 tied += other[1];
             }
     }
-    // whole steps of competing slots; where no key is tied and the kept ones
-    // are positive scores, whose keys stand for them, the ranks are those of
-    // the sure ones alone
-    const bool plain = any && prefix >= 0x80000000u;
-    for (int i0 = w0; i0 < w1; i0 += 32 * kSelAhead) {
-        uint32_t key[kSelAhead];
-#pragma unroll
-        for (int k = 0; k < kSelAhead; ++k) {
-            const int i = i0 + 32 * k + lane;
-            key[k] = i < w1 ? key_of(i) : 0;
-        }
-#pragma unroll
-        for (int k = 0; k < kSelAhead; ++k) {
-            const int i = i0 + 32 * k + lane;
-            const uint32_t below = (1u << lane) - 1;
-            uint32_t is_tied = __ballot_sync(0xffffffffu, key[k] == prefix);
-            uint32_t r;
-            if (plain && is_tied == 0 && i0 + 32 * k + 32 <= c1) {
-                const bool stays = key[k] > prefix;
-                const uint32_t is_sure = __ballot_sync(0xffffffffu, stays);
-                r = sure + min(tied, need) + __popc(is_sure & below);
-                if (stays) kept[r] = i;
-                if (stays) out[r] = __uint_as_float(key[k] ^ 0x80000000u);
-                sure += __popc(is_sure);
+    // 128 slots at a time, four adjacent ones a lane: the lanes' counts of sure
+    // and (from bit 16) tied ones, scanned, give each its rank
+    for (int i0 = w0; i0 < w1; i0 += 128) {
+        const int i = i0 + 4 * lane;
+        uint32_t key[4] = {}, count = 0;
+        if (i < w1) {
+            if constexpr (HELD) {
+                *reinterpret_cast<uint4 *>(key) = *reinterpret_cast<const uint4 *>(keys + (i - s0));
             } else {
-                const uint32_t is_sure = __ballot_sync(0xffffffffu, i < w1 && (i >= cand || (any && key[k] > prefix)));
-                is_tied = __ballot_sync(0xffffffffu, any && i < min(w1, cand) && key[k] == prefix);
-                const uint32_t e = tied + __popc(is_tied & below);
-                r = sure + __popc(is_sure & below) + min(e, need);
-                const bool stays = (is_sure >> lane & 1) || ((is_tied >> lane & 1) && e < need);
-                if (stays) {
-                    kept[r] = i;
-                    out[r] = scores[i];
-                }
-                sure += __popc(is_sure);
-                tied += __popc(is_tied);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (i + j < w1) key[j] = score_key(scores[i + j]);
             }
-            if (lane == 0 && i < w1 && i / kMvRows <= a.chunks) rank_at[i / kMvRows] = r;
         }
+        bool is_sure[4], is_tied[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const bool competes = i + j < c1;
+            is_sure[j] = competes ? any && key[j] > prefix : i + j < w1;
+            is_tied[j] = competes && any && key[j] == prefix;
+            count += (is_sure[j] ? 1u : 0u) + (is_tied[j] ? 1u << 16 : 0u);
+        }
+        uint32_t upto = count;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
+        }
+        uint32_t g = sure + (upto - count & 0xffff), e = tied + (upto - count >> 16);
+        // every eighth lane's first slot starts 32 of them
+        if ((lane & 7) == 0 && i < w1 && i / kMvRows <= a.chunks) rank_at[i / kMvRows] = g + min(e, need);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t r = g + min(e, need);
+            if (is_sure[j] || (is_tied[j] && e < need)) {
+                kept[r] = i + j;
+                // a positive score is its key but for the top bit; others are read again
+                out[r] = key[j] > 0x80000000u ? __uint_as_float(key[j] ^ 0x80000000u) : scores[i + j];
+            }
+            g += is_sure[j];
+            e += is_tied[j];
+        }
+        const uint32_t all_of = __shfl_sync(0xffffffffu, upto, 31);
+        sure += all_of & 0xffff;
+        tied += all_of >> 16;
     }
     if (parts > 1) cluster.sync();  // no block leaves while another reads its shared memory
 }
