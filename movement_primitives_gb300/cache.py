@@ -311,6 +311,7 @@ def _evict(cache, lengths, scores, budget, recent, new_scores, kept, new_lengths
     workspace = cache._empty((ws_bytes,), (1,), _BYTES)
     ss, ks, ns = scores.stride(), kept.stride(), new_scores.stride()
     a = _EVICTION.pack(lengths.data_ptr(), scores.data_ptr(), ss[0], ss[1], budget, recent, kept.data_ptr(), ks[0],
-                       ks[1], new_scores.data_ptr(), ns[0], ns[1], new_lengths.data_ptr(), workspace.data_ptr(), ws_bytes)
+                       ks[1], new_scores.data_ptr(), ns[0], ns[1], new_lengths.data_ptr(), workspace.data_ptr(),
+                       ws_bytes)
     _check(_lib.lib().lc_cache_evict(cache._ref, a, handle), "cache_evict")
     return kept, new_scores, new_lengths

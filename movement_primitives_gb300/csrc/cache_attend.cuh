@@ -300,7 +300,8 @@ struct Attend {
                 uint32_t x, y;
                 if (a.q_wide) {  // whole fours of columns on 8-byte boundaries
                     if (Q8) {
-                        const uint2 v = on && c0 < a.c.dim ? *reinterpret_cast<const uint2 *>(p + c0) : make_uint2(0, 0);
+                        uint2 v = make_uint2(0, 0);
+                        if (on && c0 < a.c.dim) v = *reinterpret_cast<const uint2 *>(p + c0);
                         x = v.x;
                         y = v.y;
                     } else {
@@ -337,7 +338,8 @@ struct Attend {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const uint32_t v = qb[ks][g][i];
-                        qb[ks][g][i] = pack2<true>(__uint_as_float(v << 16) * down, __uint_as_float(v & 0xffff0000u) * down);
+                        qb[ks][g][i] =
+                            pack2<true>(__uint_as_float(v << 16) * down, __uint_as_float(v & 0xffff0000u) * down);
                     }
                 // logits come by columns: heads 2 q, 2 q + 1
 #pragma unroll
@@ -910,7 +912,8 @@ __global__ void __launch_bounds__(kAtThreads) k_attend_unit(const __grid_constan
             float y[4];
             join(parts, [&](int r) { return cluster.map_shared_rank(block_ml, r)[head]; },
                  [&](int r) {
-                     return *reinterpret_cast<const float4 *>(cluster.map_shared_rank(smem, r) + (head * S::OP + col) * 4);
+                     const uint8_t *other = cluster.map_shared_rank(smem, r);
+                     return *reinterpret_cast<const float4 *>(other + (head * S::OP + col) * 4);
                  },
                  &v, y);
             put(head, col, v, y);
@@ -952,7 +955,8 @@ int launch_attend(const AttendArgs &a, int unit_blocks, int *runs, cudaStream_t 
             constexpr int kBytes = AtShape<DP, KV, NG, kUnitStages<DP, KV>>::SMEM;
             const void *fn = reinterpret_cast<const void *>(&k_attend_unit<DP, KV, NG>);
             if (prepare(fn, kAtThreads, kBytes, kBytes, &sms, &per) != cudaSuccess) return LC_ERR_CUDA;
-            return launch_after(fn, static_cast<unsigned>(units * unit_blocks), kAtThreads, kBytes, cs, &a, unit_blocks);
+            return launch_after(fn, static_cast<unsigned>(units * unit_blocks), kAtThreads, kBytes, cs, &a,
+                                unit_blocks);
         }
     }
     const void *fn = reinterpret_cast<const void *>(&k_attend<DP, KV, NG, VEC>);

@@ -95,7 +95,8 @@ __device__ __forceinline__ void put_row(int dim, uint8_t *dst, float *scale_at, 
             const float inverse = __frcp_rn(scale);
             encode([&](float x) {
                 const float y = rounded_quotient(x, scale, inverse);
-                return __uint_as_float(__float_as_uint(y) | (__float_as_uint(x) & 0x80000000u));  // a zero keeps its sign
+                // a zero keeps its sign
+                return __uint_as_float(__float_as_uint(y) | (__float_as_uint(x) & 0x80000000u));
             });
         } else {
             const bool fine = top < (Q == 1 ? 0x7f80u : 0x7c00u);

@@ -273,7 +273,7 @@ extern "C" int lc_cache_attend(const lc_paged_cache *cache, const lc_cache_query
     if (st) return st;
     if (!rows_apart(2, qext, q->out_stride, cache->head_dim) ||
         (q->lse && !rows_apart(1, qext, &q->lse_stride, q->n_q_heads)) ||
-        (q->scores && !rows_apart(2, kext, q->scores_stride, std::max(a.c.cap, 1))))
+        (q->scores && a.c.cap > 0 && !rows_apart(2, kext, q->scores_stride, a.c.cap)))
         return LC_ERR_NOT_INJECTIVE;
     AttendSpace space;
     const int64_t chunks = (int64_t(a.c.cap) + kJoinLeast * kScorePer - 1) / (kJoinLeast * kScorePer);

@@ -176,7 +176,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_evict_select(const 
 #pragma unroll
                 for (int r = 0; r < kSelCluster; ++r)
                     if (r < parts) {
-                        const uint32_t *other = parts > 1 ? cluster.map_shared_rank(groups[pass & 1], r) : groups[pass & 1];
+                        const uint32_t *own = groups[pass & 1];
+                        const uint32_t *other = parts > 1 ? cluster.map_shared_rank(own, r) : own;
                         low += other[lane];
                         high += other[32 + lane];
                     }
@@ -209,7 +210,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_evict_select(const 
     // Slots in order: `sure` are kept whatever else, of the `tied` ones the
     // first `need`.  Each warp counts its run's, then writes from the counts
     // before it.
-    const int w0 = static_cast<int>(lmin(s0 + int64_t(warp) * run, s1)), w1 = static_cast<int>(lmin(w0 + int64_t(run), s1));
+    const int w0 = static_cast<int>(lmin(s0 + int64_t(warp) * run, s1));
+    const int w1 = static_cast<int>(lmin(w0 + int64_t(run), s1));
     uint32_t sure = 0, tied = 0;
 #pragma unroll 4
     for (int i = w0 + lane; i < w1; i += 32) {
@@ -441,27 +443,29 @@ int launch_evict(EvictArgs &a, cudaStream_t cs) {
     a.head_div = make_fastdiv(static_cast<uint32_t>(a.c.heads));
     a.word_div = make_fastdiv(static_cast<uint32_t>(VEC ? a.c.dim * EB / 16 : a.c.dim));
     int sms, per, move_per;
-    // Selection: clusters where there are few units and many slots
+    const void *move = reinterpret_cast<const void *>(&k_evict_move<EB, VEC>);
+    if (prepare(move, kMvThreads, smem, smem, &sms, &move_per) != cudaSuccess) return LC_ERR_CUDA;
+    // Selection.  Clusters where there are few units and many slots, a block an
+    // SM at most (of 16 blocks, which are no longer portable, measured slower:
+    // 45 against 27 us for 8 units of 131071 slots); where blocks have an SM
+    // each and many slots a thread, 1024 threads (26 against 31 us).
     int parts = 1;
-    if (prepare(reinterpret_cast<const void *>(&k_evict_move<EB, VEC>), kMvThreads, smem, smem, &sms, &move_per) != cudaSuccess)
-        return LC_ERR_CUDA;
     while (parts < kSelCluster && units * parts * 2 <= sms && a.c.cap / (2 * parts) >= kSelLeast) parts *= 2;
     const int rounds = a.c.cap ? (a.c.cap - 1) / kSelRound + 1 : 0;
     const int64_t hold = int64_t(rounds + parts - 1) / parts * kSelRound;
     const bool held = hold <= kSelKeys;
-    // a block an SM, with more than a few slots a thread: twice the warps
     const int threads = units * parts <= sms && hold > 4096 ? 1024 : 512;
-    const void *sel = threads == 1024 ? (held ? reinterpret_cast<const void *>(&k_evict_select<true, 1024>)
-                                              : reinterpret_cast<const void *>(&k_evict_select<false, 1024>))
-                                      : (held ? reinterpret_cast<const void *>(&k_evict_select<true, 512>)
-                                              : reinterpret_cast<const void *>(&k_evict_select<false, 512>));
+    const void *forms[2][2] = {{reinterpret_cast<const void *>(&k_evict_select<false, 512>),
+                                reinterpret_cast<const void *>(&k_evict_select<false, 1024>)},
+                               {reinterpret_cast<const void *>(&k_evict_select<true, 512>),
+                                reinterpret_cast<const void *>(&k_evict_select<true, 1024>)}};
+    const void *sel = forms[held][threads == 1024];
     if (prepare(sel, threads, 0, kSelKeys * 4, &sms, &per) != cudaSuccess) return LC_ERR_CUDA;
     const int st = launch_after(sel, static_cast<unsigned>(units * parts), threads,
                                 held ? static_cast<size_t>(hold) * 4 : 0, cs, &a, parts);
     if (st) return st;
-    return launch_after(reinterpret_cast<const void *>(&k_evict_move<EB, VEC>),
-                        static_cast<unsigned>(std::min<int64_t>(units * a.chunks, int64_t(sms) * move_per)), kMvThreads,
-                        smem, cs, &a);
+    const int64_t blocks = std::min<int64_t>(units * a.chunks, int64_t(sms) * move_per);
+    return launch_after(move, static_cast<unsigned>(blocks), kMvThreads, smem, cs, &a);
 }
 
 }  // namespace
@@ -494,7 +498,8 @@ extern "C" int lc_cache_evict(const lc_paged_cache *cache, const lc_cache_evicti
     if (!st) st = check_reach(2, ext, e->new_scores_stride, a.c.cap);
     if (!st) st = check_reach(2, ext, e->kept_stride, e->budget);
     if (st) return st;
-    if (!rows_apart(2, ext, e->new_scores_stride, std::max(a.c.cap, 1)) || !rows_apart(2, ext, e->kept_stride, e->budget))
+    if ((a.c.cap > 0 && !rows_apart(2, ext, e->new_scores_stride, a.c.cap)) ||
+        !rows_apart(2, ext, e->kept_stride, e->budget))
         return LC_ERR_NOT_INJECTIVE;
     const int64_t units = ext[0] * ext[1], chunks = (int64_t(e->budget) + kMvRows - 1) / kMvRows;
     // the tickets that running blocks draw past the last one stay in 32 bits

@@ -73,7 +73,8 @@ class Setup:
         self.k, self.v = pools
         self.table = torch.randperm(n_pages, generator=g)[:n_seq * per].reshape(n_seq, per).to(torch.int32).cuda()
         self.lengths = torch.tensor(list(lengths), dtype=torch.int32, device="cuda")
-        self.kind, self.g, self.n_seq, self.heads, self.dim, self.page, self.cap = kind, g, n_seq, heads, dim, page, per * page
+        self.kind, self.g, self.n_seq, self.heads, self.dim, self.page = kind, g, n_seq, heads, dim, page
+        self.cap = per * page
         self.cache = lc().PagedCache(self.k, self.v, self.table, *self.scales)
 
     def values(self):
@@ -105,7 +106,8 @@ def check_attend(s, q, out, lse, scores=None, before=None, scale=None, window=0,
         got = lse.double().cpu().numpy()
         none = np.isneginf(want_lse)
         assert np.array_equal(none, np.isneginf(got))
-        assert np.all(np.abs(got - want_lse)[~none] <= (rel + 2.0 ** -22 * (1 + np.abs(want_lse)))[~none])
+        got, want_lse, slack = got[~none], want_lse[~none], rel[~none]
+        assert np.all(np.abs(got - want_lse) <= slack + 2.0 ** -22 * (1 + np.abs(want_lse)))
     if scores is not None:
         got, old = scores.double().cpu().numpy(), before.double().cpu().numpy()
         b = rel.reshape(s.n_seq, s.heads, -1).max(2) + 2.0 ** -22
@@ -251,6 +253,21 @@ def test_attend_long(kind, dim, n):
     """One sequence over the whole GPU, split and joined; logits large enough that a few slots dominate."""
     attend(Setup([n], heads=1, dim=dim, kind=kind, seed=n, page=64), 5, scores=True, scale=0.4)
     attend(Setup([n // 2, 3, n // 3], heads=2, dim=dim, kind=kind, seed=n), 4, scores=True)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "e4m3"])
+@pytest.mark.parametrize("dim,group", [(64, 3), (64, 12), (96, 8), (128, 9), (128, 20), (256, 2), (256, 16)])
+def test_attend_units_cut_into_runs(kind, dim, group):
+    """Units enough and long enough to be cut into runs, whole units among them, with windows and masks."""
+    wide = 2 * dim * (1 if kind == "e4m3" else 2) > 256  # steps of 16 slots, else of 32
+    n = 2100 if wide else 4200
+    s = Setup([n, 35, 0, n // 2 + 1], heads=12, dim=dim, kind=kind, page=30, order="token", seed=dim + group)
+    attend(s, 12 * group, scores=True)
+    if group < 10:
+        attend(s, 12 * group)
+        mask = (torch.rand((4, s.cap), generator=s.g) < 0.5).cuda()
+        mask[0, 100:1500] = False
+        attend(s, 12 * group, scores=True, mask=mask, window=n - 7)
 
 
 def test_attend_many_sequences():
@@ -551,6 +568,17 @@ def test_evict_long(n, budget, recent):
     check_evict(s, x.cuda(), budget, recent)
 
 
+def test_evict_more_slots_than_shared_memory_holds():
+    """Units too many for clusters, of more slots than a block holds keys of."""
+    n = [50001, 49500] + [30 + i for i in range(78)]
+    s = Setup(n, heads=1, dim=8, page=50, seed=4)
+    x = torch.exp(2 * torch.randn((80, 1, s.cap), generator=s.g))
+    x[1] = (x[1] * 4).round()
+    check_evict(s, x.cuda(), 4000, 50)
+    s = Setup(n[1:2] + n[2:], heads=1, dim=8, page=50, seed=5)
+    check_evict(s, (4 * x[1:]).round().cuda()[..., :s.cap].contiguous(), 40, 0)
+
+
 def test_evict_strided_arguments_and_streams():
     s = Setup([100, 60], heads=2, dim=64, seed=2)
     wide = torch.rand((2, 3, s.cap + 3), generator=s.g).cuda()
@@ -567,6 +595,30 @@ def test_evict_strided_arguments_and_streams():
 def test_evict_many_sequences():
     s = Setup([(37 * i) % 120 for i in range(200)], heads=3, dim=32, seed=3)
     check_evict(s, torch.rand((200, 3, s.cap), generator=s.g).cuda(), 50, 8)
+
+
+def test_no_sequences_and_no_capacity():
+    s = Setup([5, 9], heads=2, dim=64)
+    none = lc().PagedCache(s.k, s.v, s.table[:, :0])       # no slots: nothing fits, nothing is seen
+    zero = torch.zeros(2, dtype=torch.int32, device="cuda")
+    q = s.queries(4)
+    lse, scores = torch.zeros((2, 4), device="cuda"), torch.zeros((2, 2, 0), device="cuda")
+    out = lc().cache_attend(none, q, zero, lse=lse, scores=scores)
+    assert torch.all(out == 0) and torch.all(torch.isneginf(lse))
+    kept, new_scores, n = lc().cache_evict(none, zero, scores, 3)
+    assert torch.all(kept == -1) and new_scores.shape == (2, 2, 0) and torch.equal(n, zero)
+    empty = torch.zeros((2, 0, 2, 64), dtype=torch.bfloat16, device="cuda")
+    assert torch.equal(lc().cache_append(none, empty, empty, zero), zero)
+    no_device_error()
+    one = empty.new_zeros((2, 1, 2, 64))
+    assert torch.equal(lc().cache_append(none, one, one, zero), zero)
+    device_error_is("LC_ERR_CACHE_INDEX")
+    nobody = lc().PagedCache(s.k, s.v, s.table[:0])
+    no = zero[:0]
+    assert lc().cache_attend(nobody, q[:0], no).shape == (0, 4, 64)
+    assert lc().cache_append(nobody, empty[:0], empty[:0], no).shape == (0,)
+    assert lc().cache_evict(nobody, no, torch.zeros((0, 2, s.cap), device="cuda"), 3)[0].shape == (0, 2, 3)
+    no_device_error()
 
 
 # ---------------------------------------------------------------------------
