@@ -134,7 +134,7 @@ int lc_cache_attend(const lc_paged_cache *cache, const lc_cache_query *query, lc
  *   new_scores  like scores, another buffer: the kept slots' scores, then zeros
  *   new_lengths [n_seqs], another buffer than lengths: min(n, budget)
  *   workspace   at least lc_cache_evict_workspace(...) bytes, 256-byte
- *               aligned, as lc_cache_attend's */
+ *               aligned, as lc_cache_attend's; may be NULL where that is 0 */
 typedef struct {
     const int32_t *lengths;
     const float *scores;
@@ -150,7 +150,8 @@ typedef struct {
     int64_t workspace_bytes;
 } lc_cache_eviction;
 
-/* Bytes of workspace of lc_cache_evict, or -1 for arguments that it refuses. */
+/* Bytes of workspace of lc_cache_evict on this cache (0 where small sequences
+ * are selected and moved in one launch), or -1 for arguments that it refuses. */
 int64_t lc_cache_evict_workspace(const lc_paged_cache *cache, int32_t budget);
 
 /* Errors: LC_ERR_NULL, LC_ERR_SHAPE (budget < 1, recent outside 0 .. budget,

@@ -308,10 +308,10 @@ def _evict(cache, lengths, scores, budget, recent, new_scores, kept, new_lengths
     if new_lengths is None:
         new_lengths = cache._empty((b,), (1,), lengths.dtype)
     ws_bytes = cache.evict_workspace_bytes(budget)
-    workspace = cache._empty((ws_bytes,), (1,), _BYTES)
+    workspace = cache._empty((ws_bytes,), (1,), _BYTES) if ws_bytes else None
     ss, ks, ns = scores.stride(), kept.stride(), new_scores.stride()
     a = _EVICTION.pack(lengths.data_ptr(), scores.data_ptr(), ss[0], ss[1], budget, recent, kept.data_ptr(), ks[0],
-                       ks[1], new_scores.data_ptr(), ns[0], ns[1], new_lengths.data_ptr(), workspace.data_ptr(),
-                       ws_bytes)
+                       ks[1], new_scores.data_ptr(), ns[0], ns[1], new_lengths.data_ptr(),
+                       workspace.data_ptr() if ws_bytes else 0, ws_bytes)
     _check(_lib.lib().lc_cache_evict(cache._ref, a, handle), "cache_evict")
     return kept, new_scores, new_lengths

@@ -5,13 +5,16 @@
 // stay, and of the others the budget - recent of largest score, equal scores
 // in slot order.
 //
-// k_evict_select, a block or a cluster of blocks a unit, finds the score of
+// select_slots, by a block or a cluster of blocks a unit, finds the score of
 // the last slot kept by radix selection on an order-preserving 32-bit key
 // (digits of 11, 11 and 10 bits from the top, the first one's histogram made
 // as the scores come in), then writes the kept slots in ascending order
 // (`kept`) with their scores.  The scores are read from memory once and their
 // keys kept in shared memory; the blocks of a cluster take a run of slots each
 // and add up their histograms through distributed shared memory.
+//
+// Small units select and move in one launch (k_evict_small); others select
+// with k_evict_select and move with k_evict_move.
 //
 // k_evict_move moves the rows, 32 ranks (a chunk) a block at a time.  Rows
 // move in place: the r-th kept slot goes to slot r, and kept[r] >= r, so slot
@@ -29,7 +32,7 @@
 // its passes over the keys, each a barrier of the cluster), the move 72 us (5.6
 // TB/s).  One sequence of 131071 E4M3 slots cut to 32768, 138 MB, 62 us: 27 us
 // of selection on 64 blocks, 35 us of rows of 128 bytes.  Four sequences of
-// 1500 cut to 1024, 34 MB, 20 us.
+// 1500 cut to 1024, 34 MB, in one launch 15.5 us.
 #include <cooperative_groups.h>
 
 #include "cache_common.cuh"
@@ -43,7 +46,12 @@ constexpr int kSelRound = 2048;     // slots are dealt to blocks in so many
 constexpr int kSelKeys = 48 * 1024; // keys a block holds in shared memory
 constexpr int kSelCluster = 8;      // blocks of a unit at most
 constexpr int kSelLeast = 4096;     // slots a block of a cluster has at least
-constexpr int kMvThreads = 64;        // a warp a pool where the rows' places are found
+constexpr int kSmThreads = 512;     // of a block that selects and moves
+constexpr int kSmAhead = 4;         // words a thread reads at a time there
+constexpr int kSmBlocks = 304;      // two an SM
+constexpr int kSmSlots = 8192;      // of such a block's unit at most
+constexpr int kSmMoved = 128 * 1024; // bytes that such a block moves at most
+constexpr int kMvThreads = 64;      // a warp a pool where the rows' places are found
 constexpr int kMvRows = 32;         // ranks of a chunk (the selection writes rank_at once every 32 slots)
 
 struct EvictArgs {
@@ -56,6 +64,7 @@ struct EvictArgs {
     int32_t budget, recent;
     int32_t chunks;          // of a unit: ceil(budget / kMvRows)
     FastDiv unit_div, head_div, word_div;  // units; key heads; words (VEC: of 16 bytes) of a row
+    int32_t slices, held_keys;             // of k_evict_small; word_div is then of twice a slice's words
     uint64_t wait_ns;
     // workspace
     uint32_t *ticket;        // the next chunk
@@ -86,48 +95,28 @@ __device__ __forceinline__ int pick(uint32_t count, uint32_t *need) {
     return at;
 }
 
-// HELD: the keys of a block's slots fit its shared memory; else every pass
-// reads the scores again. THREADS: 512, two blocks an SM, or 1024.
-template <bool HELD, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_evict_select(const __grid_constant__ EvictArgs a) {
+// Finds the slots that stay of one unit's first n > budget ones: stay(rank,
+// slot, score) of each, and rank(k, r), the rank r of slot kMvRows k, for every
+// such slot.  By THREADS threads, or with CLUSTER by a cluster of `parts`
+// blocks, this one the `part`-th.  HELD: the keys of a block's slots fit its
+// shared memory (`keys`); else every pass reads the scores again.
+template <bool HELD, int THREADS, bool CLUSTER, typename Stay, typename Rank>
+__device__ __forceinline__ void select_slots(const EvictArgs &a, int parts, int part, int n, const float *scores,
+                                             uint32_t *keys, Stay &&stay, Rank &&rank) {
     constexpr int kWarps = THREADS / 32;
-    extern __shared__ __align__(16) uint32_t keys[];
     __shared__ uint32_t hist[2][kSelBins], groups[2][64], chosen[3][3], counts[2];
     __shared__ uint2 warp_counts[kWarps];
-    cg::cluster_group cluster = cg::this_cluster();
-    const int parts = cluster.num_blocks(), part = cluster.block_rank();
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    const int unit = blockIdx.x / parts;
-    const int b = unit / a.c.heads, h = unit - b * a.c.heads;
-    start_after_prior();
-    const int n = cache_length(a.c, a.lengths, b, kClassEvict);
-    const int m = min(n, a.budget);
-    const float *scores = a.scores + b * a.sst[0] + h * a.sst[1];
-    float *out = a.new_scores + b * a.nst[0] + h * a.nst[1];
-    int32_t *kept = a.kept + b * a.kst[0] + h * a.kst[1];
-    int32_t *rank_at = a.rank_at + int64_t(unit) * (a.chunks + 1);
-    auto sync_all = [&] {
-        if (parts > 1)
-            cluster.sync();
-        else
-            __syncthreads();
-    };
-    // what needs no selection, dealt to the cluster's threads
-    const int all = parts * THREADS, at = part * THREADS + t;
-    if (h == 0 && at == 0) a.new_lengths[b] = m;
-    if (unit == 0 && at == 0) *a.ticket = 0;
-    for (int i = at; i < a.chunks; i += all) a.done[int64_t(unit) * a.chunks + i] = 0;
-    for (int i = m + at; i < a.budget; i += all) kept[i] = -1;
-    for (int i = m + at; i < a.c.cap; i += all) out[i] = 0.f;
-    if (n == m) {  // the same for the whole cluster
-        for (int i = at; i < m; i += all) {
-            kept[i] = i;
-            out[i] = scores[i];
+    // f of each of the first `count` blocks' copies of a shared array
+    auto for_blocks = [&](int count, const uint32_t *own, auto &&f) {
+        if constexpr (CLUSTER) {
+#pragma unroll
+            for (int r = 0; r < kSelCluster; ++r)
+                if (r < count) f(static_cast<const uint32_t *>(cg::this_cluster().map_shared_rank(own, r)));
+        } else if (count) {
+            f(own);
         }
-        return;
-    }
-    for (int i = (n - 1) / kMvRows + 1 + at; i <= a.chunks; i += all) rank_at[i] = m;
-
+    };
     // this block's slots [s0, s1), a run of `run` for each warp
     const int rounds = (n - 1) / kSelRound + 1, each = (rounds + parts - 1) / parts, run = each * (kSelRound / kWarps);
     const int s0 = static_cast<int>(lmin(int64_t(part) * each * kSelRound, n));
@@ -170,23 +159,20 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_evict_select(const 
                 const uint32_t sum = __reduce_add_sync(0xffffffffu, mine[32 * g + lane]);
                 if (lane == 0) groups[pass & 1][g] = sum;
             }
-            sync_all();
+            if constexpr (CLUSTER)
+                cg::this_cluster().sync();
+            else
+                __syncthreads();
             if (warp == 0) {
                 uint32_t low = 0, high = 0, bin = 0, left = need;
-#pragma unroll
-                for (int r = 0; r < kSelCluster; ++r)
-                    if (r < parts) {
-                        const uint32_t *own = groups[pass & 1];
-                        const uint32_t *other = parts > 1 ? cluster.map_shared_rank(own, r) : own;
-                        low += other[lane];
-                        high += other[32 + lane];
-                    }
+                for_blocks(parts, groups[pass & 1], [&](const uint32_t *other) {
+                    low += other[lane];
+                    high += other[32 + lane];
+                });
                 const bool upper = __reduce_add_sync(0xffffffffu, high) >= left;
                 if (!upper) left -= __reduce_add_sync(0xffffffffu, high);
                 const int group = pick(upper ? high : low, &left) + (upper ? 32 : 0);
-#pragma unroll
-                for (int r = 0; r < kSelCluster; ++r)
-                    if (r < parts) bin += (parts > 1 ? cluster.map_shared_rank(mine, r) : mine)[32 * group + lane];
+                for_blocks(parts, mine, [&](const uint32_t *other) { bin += other[32 * group + lane]; });
                 if (lane == pick(bin, &left)) {
                     chosen[pass][0] = 32 * group + lane;
                     chosen[pass][1] = left;
@@ -231,20 +217,17 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_evict_select(const 
             sure += v.x;
             tied += v.y;
         }
-        if (t == 0 && parts > 1) {
+        if (CLUSTER && t == 0) {
             counts[0] = (w ? counts[0] : 0) + v.x;
             counts[1] = (w ? counts[1] : 0) + v.y;
         }
     }
-    if (parts > 1) {  // and the blocks before
-        cluster.sync();
-#pragma unroll
-        for (int r = 0; r < kSelCluster - 1; ++r)
-            if (r < part) {
-                const uint32_t *other = cluster.map_shared_rank(counts, r);
-                sure += other[0];
-                tied += other[1];
-            }
+    if constexpr (CLUSTER) {  // and the blocks before
+        cg::this_cluster().sync();
+        for_blocks(part, counts, [&](const uint32_t *other) {
+            sure += other[0];
+            tied += other[1];
+        });
     }
     // 128 slots at a time, four adjacent ones a lane: the lanes' counts of sure
     // and (from bit 16) tied ones, scanned, give each its rank
@@ -276,14 +259,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_evict_select(const 
         }
         uint32_t g = sure + (upto - count & 0xffff), e = tied + (upto - count >> 16);
         // every eighth lane's first slot starts 32 of them
-        if ((lane & 7) == 0 && i < w1 && i / kMvRows <= a.chunks) rank_at[i / kMvRows] = g + min(e, need);
+        if ((lane & 7) == 0 && i < w1) rank(i / kMvRows, g + min(e, need));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const uint32_t r = g + min(e, need);
             if (is_sure[j] || (is_tied[j] && e < need)) {
-                kept[r] = i + j;
                 // a positive score is its key but for the top bit; others are read again
-                out[r] = key[j] > 0x80000000u ? __uint_as_float(key[j] ^ 0x80000000u) : scores[i + j];
+                stay(r, i + j, key[j] > 0x80000000u ? __uint_as_float(key[j] ^ 0x80000000u) : scores[i + j]);
             }
             g += is_sure[j];
             e += is_tied[j];
@@ -292,7 +274,150 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_evict_select(const 
         sure += all_of & 0xffff;
         tied += all_of >> 16;
     }
-    if (parts > 1) cluster.sync();  // no block leaves while another reads its shared memory
+    if constexpr (CLUSTER) cg::this_cluster().sync();  // no block leaves while another reads its shared memory
+}
+
+// THREADS: 512, two blocks an SM, or 1024.
+template <bool HELD, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_evict_select(const __grid_constant__ EvictArgs a) {
+    extern __shared__ __align__(16) uint32_t keys[];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int parts = cluster.num_blocks(), part = cluster.block_rank();
+    const int t = threadIdx.x;
+    const int unit = blockIdx.x / parts;
+    const int b = unit / a.c.heads, h = unit - b * a.c.heads;
+    start_after_prior();
+    const int n = cache_length(a.c, a.lengths, b, kClassEvict);
+    const int m = min(n, a.budget);
+    const float *scores = a.scores + b * a.sst[0] + h * a.sst[1];
+    float *out = a.new_scores + b * a.nst[0] + h * a.nst[1];
+    int32_t *kept = a.kept + b * a.kst[0] + h * a.kst[1];
+    int32_t *rank_at = a.rank_at + int64_t(unit) * (a.chunks + 1);
+    // what needs no selection, dealt to the cluster's threads
+    const int all = parts * THREADS, at = part * THREADS + t;
+    if (h == 0 && at == 0) a.new_lengths[b] = m;
+    if (unit == 0 && at == 0) *a.ticket = 0;
+    for (int i = at; i < a.chunks; i += all) a.done[int64_t(unit) * a.chunks + i] = 0;
+    for (int i = m + at; i < a.budget; i += all) kept[i] = -1;
+    for (int i = m + at; i < a.c.cap; i += all) out[i] = 0.f;
+    if (n == m) {  // the same for the whole cluster
+        for (int i = at; i < m; i += all) {
+            kept[i] = i;
+            out[i] = scores[i];
+        }
+        return;
+    }
+    for (int i = (n - 1) / kMvRows + 1 + at; i <= a.chunks; i += all) rank_at[i] = m;
+    auto stay = [&](uint32_t r, int slot, float score) {
+        kept[r] = slot;
+        out[r] = score;
+    };
+    auto rank = [&](int k, uint32_t r) {
+        if (k <= a.chunks) rank_at[k] = r;
+    };
+    if (parts > 1)
+        select_slots<HELD, THREADS, true>(a, parts, part, n, scores, keys, stay, rank);
+    else
+        select_slots<HELD, THREADS, false>(a, 1, 0, n, scores, keys, stay, rank);
+}
+
+// Selection and move of small units in one launch, without a workspace.
+// `slices` blocks a unit each select for themselves (the first writes kept,
+// new_scores and new_lengths) and move a share of every row's words, of the key
+// and of the value: the columns of a row are independent, so the blocks need
+// nothing of one another.  A block moves runs of words in rank order, a run's
+// reads before its writes (a barrier between them); the next run's reads need
+// not wait for these: the source slot of rank j that moves is above j, and no
+// rank up to j writes there.  The barrier and one run in flight a block make
+// its rate 11 GB/s or so, which is why units of many bytes a block do not come here.
+template <int EB>
+__global__ void __launch_bounds__(kSmThreads, 2) k_evict_small(const __grid_constant__ EvictArgs a) {
+    extern __shared__ __align__(16) uint32_t keys[];
+    const CacheArgs &c = a.c;
+    int32_t *list = reinterpret_cast<int32_t *>(keys + a.held_keys);
+    const int t = threadIdx.x;
+    const int unit = blockIdx.x / a.slices, slice = blockIdx.x - unit * a.slices;
+    const int b = unit / c.heads, h = unit - b * c.heads;
+    start_after_prior();
+    const int n = cache_length(c, a.lengths, b, kClassEvict);
+    const int m = min(n, a.budget);
+    const float *scores = a.scores + b * a.sst[0] + h * a.sst[1];
+    float *out = a.new_scores + b * a.nst[0] + h * a.nst[1];
+    int32_t *kept = a.kept + b * a.kst[0] + h * a.kst[1];
+    if (slice == 0) {
+        if (h == 0 && t == 0) a.new_lengths[b] = m;
+        for (int i = m + t; i < a.budget; i += kSmThreads) kept[i] = -1;
+        for (int i = m + t; i < c.cap; i += kSmThreads) out[i] = 0.f;
+        if (n == m)
+            for (int i = t; i < m; i += kSmThreads) {
+                kept[i] = i;
+                out[i] = scores[i];
+            }
+    }
+    if (n == m) return;
+    select_slots<true, kSmThreads, false>(
+        a, 1, 0, n, scores, keys,
+        [&](uint32_t r, int slot, float score) {
+            list[r] = slot;
+            if (slice == 0) {
+                kept[r] = slot;
+                out[r] = score;
+            }
+        },
+        [](int, uint32_t) {});
+    __syncthreads();
+
+    // the slice's words of a rank: `words` of its key, then as many of its value
+    const int words = a.word_div.d / 2, items = a.budget * 2 * words;
+    for (int base = 0; base < items; base += kSmThreads * kSmAhead) {
+        uint4 x[kSmAhead];
+        uint8_t *to[kSmAhead];
+#pragma unroll
+        for (int k = 0; k < kSmAhead; ++k) {
+            const int at = base + k * kSmThreads + t;
+            to[k] = nullptr;
+            if (at >= items) continue;
+            const int r = static_cast<int>(fast_div(static_cast<uint32_t>(at), a.word_div));
+            const int from = list[r];
+            if (from == r) continue;
+            int row_f, row_t;
+            const int pf = cache_page(c, b, from, &row_f, kClassEvict), pt = cache_page(c, b, r, &row_t, kClassEvict);
+            if (pf < 0 || pt < 0) continue;
+            int w = at - r * 2 * words;
+            const bool v = w >= words;
+            w = w - (v ? words : 0) + slice * words;
+            uint8_t *pool = (v ? c.v : c.k) + 16 * w;
+            const int64_t *st = v ? c.vst : c.kst;
+            x[k] = *reinterpret_cast<const uint4 *>(pool + row_offset(st, pf, h, row_f) * EB);
+            to[k] = pool + row_offset(st, pt, h, row_t) * EB;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kSmAhead; ++k)
+            if (to[k]) *reinterpret_cast<uint4 *>(to[k]) = x[k];
+    }
+    if constexpr (EB == 1) {  // the scales: the keys' by the first slice, the values' by the last
+        for (int v = 0; v < 2; ++v) {
+            if (slice != (v ? a.slices - 1 : 0)) continue;
+            float *pool = v ? c.vs : c.ks;
+            const int64_t *st = v ? c.vss : c.kss;
+            for (int base = 0; base < a.budget; base += kSmThreads) {
+                const int r = base + t, from = r < a.budget ? list[r] : r;
+                float x = 0.f, *to = nullptr;
+                if (from != r) {
+                    int row_f, row_t;
+                    const int pf = cache_page(c, b, from, &row_f, kClassEvict);
+                    const int pt = cache_page(c, b, r, &row_t, kClassEvict);
+                    if (pf >= 0 && pt >= 0) {
+                        x = pool[row_offset(st, pf, h, row_f)];
+                        to = pool + row_offset(st, pt, h, row_t);
+                    }
+                }
+                __syncthreads();
+                if (to) *to = x;
+            }
+        }
+    }
 }
 
 __device__ __forceinline__ uint32_t load_acquire(const uint32_t *p) {
@@ -422,17 +547,54 @@ cudaError_t take_error_evict(unsigned long long *v) { return take_module_error(v
 
 namespace {
 
+// How a call of these sizes goes: in one launch of `slices` blocks a unit, or
+// (0) in two with a workspace of these offsets and this end.  One launch takes
+// units of at most kSmSlots slots, whose selections the blocks can afford to
+// repeat, and kSmMoved bytes a block.  Bfloat16 rows of 128, one launch against
+// two: 8 heads of 4 sequences of 2000 cut to 1000, 16.4 against 21.2 us; 8 of
+// 4000 to 1000, 26 against 32; 64 of 256 to 128, 23 against 30; 128 of 8000 to
+// 64, 52 against 61; at the bounds 4 of 8000 to 2000, 33 against 34.  Past them, 4
+// of up to 16384 to 4096, 59 against 40; 1 of 8000 to 4000, 32 against 25.
 struct EvictSpace {
+    bool vec;  // rows of the pools are whole 16-byte words on 16-byte boundaries
+    int slices, held_keys;
     int64_t done, rank_at, end;
 };
 
-EvictSpace evict_space(const CacheArgs &c, int budget) {
+EvictSpace evict_space(const lc_paged_cache &cache, const CacheArgs &c, int budget) {
     const int64_t units = int64_t(c.n_seqs) * c.heads, chunks = (int64_t(budget) + kMvRows - 1) / kMvRows;
-    EvictSpace s;
+    const int eb = cache_elem_bytes(cache.type);
+    const int64_t pool[3] = {cache.n_pages, cache.n_kv_heads, cache.page_size};
+    EvictSpace s{};
+    s.vec = c.dim * eb % 16 == 0 && rows_aligned(cache.k, 3, pool, cache.k_stride, eb, 16) &&
+            rows_aligned(cache.v, 3, pool, cache.v_stride, eb, 16);
+    const int64_t held = (int64_t(c.cap) + kSelRound - 1) / kSelRound * kSelRound;
+    const int words = c.dim * eb / 16;
+    if (s.vec && held <= kSmSlots) {
+        int slices = 1;  // as many as the row's words divide into, of 32 bytes or more
+        while (words % (2 * slices) == 0 && words / (2 * slices) >= 2 && units * 2 * slices <= kSmBlocks) slices *= 2;
+        if (int64_t(budget) * 2 * 16 * words / slices <= kSmMoved) {
+            s.slices = slices;
+            s.held_keys = static_cast<int>(held);
+            return s;
+        }
+    }
     s.done = 256;  // behind the ticket
     s.rank_at = s.done + round256(units * chunks * 4);
     s.end = s.rank_at + round256(units * (chunks + 1) * 4);
     return s;
+}
+
+template <int EB>
+int launch_evict_small(EvictArgs &a, cudaStream_t cs) {
+    a.word_div = make_fastdiv(static_cast<uint32_t>(2 * (a.c.dim * EB / 16 / a.slices)));
+    const void *fn = reinterpret_cast<const void *>(&k_evict_small<EB>);
+    int sms, per;
+    // 48 KB at most, and static memory besides: more than a block has unasked
+    constexpr int kMost = 4 * (kSmSlots + kSmMoved / 32);
+    if (prepare(fn, kSmThreads, 0, kMost + 1024, &sms, &per) != cudaSuccess) return LC_ERR_CUDA;
+    return launch_after(fn, static_cast<unsigned>(int64_t(a.c.n_seqs) * a.c.heads * a.slices), kSmThreads,
+                        4 * (size_t(a.held_keys) + a.budget), cs, &a);
 }
 
 template <int EB, bool VEC>
@@ -475,7 +637,7 @@ int launch_evict(EvictArgs &a, cudaStream_t cs) {
 extern "C" int64_t lc_cache_evict_workspace(const lc_paged_cache *cache, int32_t budget) {
     lc::CacheArgs c;
     if (lc::check_cache(cache, true, &c) || budget < 1) return -1;
-    return lc::evict_space(c, budget).end;
+    return lc::evict_space(*cache, c, budget).end;
 }
 
 extern "C" int lc_cache_evict(const lc_paged_cache *cache, const lc_cache_eviction *e, lc_stream_t stream) {
@@ -505,8 +667,8 @@ extern "C" int lc_cache_evict(const lc_paged_cache *cache, const lc_cache_evicti
     // the tickets that running blocks draw past the last one stay in 32 bits
     // too
     if (units > 0x0fffffff || units * chunks > 0xf0000000ll) return LC_ERR_OVERFLOW;
-    const EvictSpace space = evict_space(a.c, e->budget);
-    if (!e->workspace) return LC_ERR_NULL;
+    const EvictSpace space = evict_space(*cache, a.c, e->budget);
+    if (space.end > 0 && !e->workspace) return LC_ERR_NULL;
     if (space.end > e->workspace_bytes) return LC_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(e->workspace) % 256) return LC_ERR_ALIGN;
     a.lengths = e->lengths;
@@ -527,11 +689,13 @@ extern "C" int lc_cache_evict(const lc_paged_cache *cache, const lc_cache_evicti
     a.ticket = reinterpret_cast<uint32_t *>(ws);
     a.done = reinterpret_cast<uint32_t *>(ws + space.done);
     a.rank_at = reinterpret_cast<int32_t *>(ws + space.rank_at);
-    const int eb = cache_elem_bytes(cache->type);
-    const int64_t pool[3] = {cache->n_pages, cache->n_kv_heads, cache->page_size};
-    const bool vec = a.c.dim * eb % 16 == 0 && rows_aligned(cache->k, 3, pool, cache->k_stride, eb, 16) &&
-                     rows_aligned(cache->v, 3, pool, cache->v_stride, eb, 16);
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    if (cache->type == LC_CACHE_E4M3) return vec ? launch_evict<1, true>(a, cs) : launch_evict<1, false>(a, cs);
-    return vec ? launch_evict<2, true>(a, cs) : launch_evict<2, false>(a, cs);
+    const bool q8 = cache->type == LC_CACHE_E4M3;
+    if (space.slices) {
+        a.slices = space.slices;
+        a.held_keys = space.held_keys;
+        return q8 ? launch_evict_small<1>(a, cs) : launch_evict_small<2>(a, cs);
+    }
+    if (q8) return space.vec ? launch_evict<1, true>(a, cs) : launch_evict<1, false>(a, cs);
+    return space.vec ? launch_evict<2, true>(a, cs) : launch_evict<2, false>(a, cs);
 }

@@ -243,7 +243,7 @@ def test_append_refusals(M):
 def test_evict_refusals(M):
     lib, names = M._lib.lib(), M._lib.STATUS_NAMES
 
-    def call(**kw):
+    def call(cache=None, **kw):
         e = M._lib.CCacheEviction()
         e.lengths, e.scores, e.kept, e.new_scores, e.new_lengths = BASE, 2 * BASE, 3 * BASE, 4 * BASE, 5 * BASE
         e.scores_stride[:] = e.new_scores_stride[:] = (4 * 48, 48)
@@ -255,7 +255,7 @@ def test_evict_refusals(M):
                 getattr(e, k)[:] = x
             else:
                 setattr(e, k, x)
-        return names[lib.lc_cache_evict(ctypes.byref(_cache(M)), ctypes.byref(e), None)]
+        return names[lib.lc_cache_evict(ctypes.byref(_cache(M, **(cache or {}))), ctypes.byref(e), None)]
     for f in ("lengths", "scores", "kept", "new_scores", "new_lengths"):
         assert call(**{f: None}) == "LC_ERR_NULL"
         assert call(**{f: BASE * 9 + 2}) == "LC_ERR_ALIGN"
@@ -263,7 +263,10 @@ def test_evict_refusals(M):
     assert call(new_scores=2 * BASE) == call(new_lengths=BASE) == "LC_ERR_OVERLAP"
     assert call(kept_stride=(32, 7)) == call(new_scores_stride=(48, 47)) == "LC_ERR_NOT_INJECTIVE"
     assert call(scores_stride=(-1, 48)) == "LC_ERR_BAD_STRIDE"
-    need = lib.lc_cache_evict_workspace(ctypes.byref(_cache(M)), 8)
+    long = dict(pages_per_seq=2048, table_stride=2048)  # too long for the form that needs no workspace
+    wide = dict(scores_stride=(4 * 32768, 32768), new_scores_stride=(4 * 32768, 32768))
+    need = lib.lc_cache_evict_workspace(ctypes.byref(_cache(M, **long)), 8)
     assert need > 0 and lib.lc_cache_evict_workspace(ctypes.byref(_cache(M)), 0) == -1
-    assert call(workspace=None) == "LC_ERR_NULL" and call(workspace=BASE + 64) == "LC_ERR_ALIGN"
-    assert call(workspace_bytes=need - 1) == "LC_ERR_WORKSPACE"
+    assert call(long, workspace=None, **wide) == "LC_ERR_NULL"
+    assert call(long, workspace=BASE + 64, workspace_bytes=need, **wide) == "LC_ERR_ALIGN"
+    assert call(long, workspace_bytes=need - 1, **wide) == "LC_ERR_WORKSPACE"

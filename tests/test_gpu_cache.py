@@ -568,6 +568,18 @@ def test_evict_long(n, budget, recent):
     check_evict(s, x.cuda(), budget, recent)
 
 
+@pytest.mark.parametrize("kind,dim", [("bf16", 128), ("e4m3", 64), ("fp16", 32), ("e4m3", 16)])
+@pytest.mark.parametrize("cap", [8192, 8208])
+def test_evict_at_the_bound_of_one_launch(kind, dim, cap):
+    """Capacities and budgets on both sides of what one launch takes, with short sequences beside the long one."""
+    n = [cap, 1, 31, 32, 33, 64, 700, 2049]
+    for budget, recent in ((1, 1), (33, 0), (255, 60), (257, 0), (2048, 16), (cap - 1, 0)):
+        s = Setup(n, dim=dim, kind=kind, seed=budget + dim)
+        x = torch.rand((8, 2, s.cap), generator=s.g)
+        x[1:3] = (x[1:3] * 3).round()
+        check_evict(s, x.cuda(), budget, recent)
+
+
 def test_evict_more_slots_than_shared_memory_holds():
     """Units too many for clusters, of more slots than a block holds keys of."""
     n = [50001, 49500] + [30 + i for i in range(78)]
