@@ -50,7 +50,7 @@ constexpr int kSmThreads = 512;     // of a block that selects and moves
 constexpr int kSmAhead = 4;         // words a thread reads at a time there
 constexpr int kSmBlocks = 304;      // two an SM
 constexpr int kSmSlots = 8192;      // of such a block's unit at most
-constexpr int kSmMoved = 128 * 1024; // bytes that such a block moves at most
+constexpr int kSmMoved = 128 * 1024; // bytes that such a block moves at most, or twice that
 constexpr int kMvThreads = 64;      // a warp a pool where the rows' places are found
 constexpr int kMvRows = 32;         // ranks of a chunk (the selection writes rank_at once every 32 slots)
 
@@ -550,11 +550,13 @@ namespace {
 // How a call of these sizes goes: in one launch of `slices` blocks a unit, or
 // (0) in two with a workspace of these offsets and this end.  One launch takes
 // units of at most kSmSlots slots, whose selections the blocks can afford to
-// repeat, and kSmMoved bytes a block.  Bfloat16 rows of 128, one launch against
+// repeat, and kSmMoved bytes a block; twice the bytes where these are half the
+// slots or fewer and every SM has a block.  Bfloat16 rows of 128, one launch against
 // two: 8 heads of 4 sequences of 2000 cut to 1000, 16.4 against 21.2 us; 8 of
 // 4000 to 1000, 26 against 32; 64 of 256 to 128, 23 against 30; 128 of 8000 to
-// 64, 52 against 61; at the bounds 4 of 8000 to 2000, 33 against 34.  Past them, 4
-// of up to 16384 to 4096, 59 against 40; 1 of 8000 to 4000, 32 against 25.
+// 64, 52 against 61; 300 of 1000 to 500, 242 against 262; at the bounds 4 of 8000
+// to 2000, 33 against 34, and 8 of 4000 to 2000, 41 against 42.  Past them, 4 of up
+// to 16384 to 4096, 59 against 40; 4 of 8000 to 4000, 50 against 43.
 struct EvictSpace {
     bool vec;  // rows of the pools are whole 16-byte words on 16-byte boundaries
     int slices, held_keys;
@@ -573,7 +575,9 @@ EvictSpace evict_space(const lc_paged_cache &cache, const CacheArgs &c, int budg
     if (s.vec && held <= kSmSlots) {
         int slices = 1;  // as many as the row's words divide into, of 32 bytes or more
         while (words % (2 * slices) == 0 && words / (2 * slices) >= 2 && units * 2 * slices <= kSmBlocks) slices *= 2;
-        if (int64_t(budget) * 2 * 16 * words / slices <= kSmMoved) {
+        const bool filled = units * slices > kSmBlocks / 2;
+        const int most = held <= kSmSlots / 2 && filled ? 2 * kSmMoved : kSmMoved;
+        if (int64_t(budget) * 2 * 16 * words / slices <= most) {
             s.slices = slices;
             s.held_keys = static_cast<int>(held);
             return s;
@@ -591,7 +595,7 @@ int launch_evict_small(EvictArgs &a, cudaStream_t cs) {
     const void *fn = reinterpret_cast<const void *>(&k_evict_small<EB>);
     int sms, per;
     // 48 KB at most, and static memory besides: more than a block has unasked
-    constexpr int kMost = 4 * (kSmSlots + kSmMoved / 32);
+    constexpr int kMost = 4 * (kSmSlots + kSmMoved / 32);  // half the slots: twice the ranks
     if (prepare(fn, kSmThreads, 0, kMost + 1024, &sms, &per) != cudaSuccess) return LC_ERR_CUDA;
     return launch_after(fn, static_cast<unsigned>(int64_t(a.c.n_seqs) * a.c.heads * a.slices), kSmThreads,
                         4 * (size_t(a.held_keys) + a.budget), cs, &a);
