@@ -8,17 +8,17 @@
 // divisor: with its rounded reciprocal r, q = x r and q + (x - q scale) r in
 // fused operations is the rounded quotient (Markstein, "Computation of
 // elementary functions on the IBM RISC System/6000 processor", 1990), three
-// operations for a division's many; scales far out of range divide.
+// operations on pairs of elements for a division's many; scales far out of
+// range divide.
 //
-// One warp moves a token's rows of U heads in both pools: lanes 0-15 the
-// keys', 16-31 the values', each lane 16 bytes of new elements at a time, the
-// loads of all U heads before the first store.  Every byte is read and written
-// once.
+// One warp moves a token's rows of some heads in both pools: groups of 16, 8 or
+// 4 lanes take a row, each lane 16 bytes of new elements at a time, with all
+// loads before the first store.  Every byte is read and written once.
 //
-// Measured on GB300: 64 tokens of 8 heads of 128 as they are 2.0 us, the
+// Measured on GB300: 64 tokens of 8 heads of 128 as they are 1.9 us, the
 // latency of three dependent reads; prompts of 8966 tokens into E4M3, 56 MB,
-// 16 us (3.4 TB/s), bound by the instructions of the quotients and the
-// rounding (issue slots 70 % busy), one head a warp 29 us, two 22, eight 21.
+// 11.8 us (4.7 TB/s), 57 thousand tokens, 210 MB, 35 us (6.0 TB/s).  What is
+// left above the copy's rate is the start and the tail of the launch.
 #include <cuda_fp8.h>
 
 #include "cache_common.cuh"
@@ -26,7 +26,7 @@
 namespace lc {
 
 constexpr int kApThreads = 128;
-constexpr int64_t kApMany = 4 * 152 * 48;  // rows from which a warp takes four heads
+constexpr int64_t kApMany = 4 * 152 * 48;  // rows from which a warp takes several heads
 
 struct AppendArgs {
     CacheArgs c;
@@ -45,30 +45,52 @@ __device__ __forceinline__ float value_of(uint32_t w) {
     return Q == 1 ? __uint_as_float(w << 16) : __half2float(__ushort_as_half(static_cast<uint16_t>(w)));
 }
 
-// x / d from d's rounded reciprocal (see above).
+__device__ __forceinline__ uint64_t twice(float x) {
+    uint64_t y;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(y) : "f"(x));
+    return y;
+}
+
+// -x / d of two elements from d and minus its rounded reciprocal (see above).
+// With these signs a zero's comes out negated like every other: the remainder
+// of x = -0 and of x = +0 is +0, and the last sum adds two zeros of one sign.
+__device__ __forceinline__ float2 minus_quotients(float2 x, uint64_t d, uint64_t minus_inverse) {
+    float2 y;
+    asm("{\n\t"
+        ".reg .b64 x, q, rest;\n\t"
+        "mov.b64 x, {%2, %3};\n\t"
+        "mul.rn.f32x2 q, x, %5;\n\t"
+        "fma.rn.f32x2 rest, q, %4, x;\n\t"
+        "fma.rn.f32x2 q, rest, %5, q;\n\t"
+        "mov.b64 {%0, %1}, q;\n\t}"
+        : "=f"(y.x), "=f"(y.y)
+        : "f"(x.x), "f"(x.y), "l"(d), "l"(minus_inverse));
+    return y;
+}
+
+// x / d from d's rounded reciprocal.
 __device__ __forceinline__ float rounded_quotient(float x, float d, float inverse) {
     const float q = x * inverse;
     return fmaf(fmaf(-q, d, x), inverse, q);
 }
 
-// One row's 16 elements a lane, as they were read, to the pool: Q 0 unchanged,
-// 1 bfloat16 -> E4M3, 2 float16 -> E4M3. NI: eights of elements a lane (rows
-// of up to 128 NI).  VEC: lane l holds eights l and l + 16, else elements l +
-// 16 j.
-template <int Q, bool VEC, int NI>
+// One row's elements, as L lanes read them, to the pool: Q 0 unchanged, 1
+// bfloat16 -> E4M3, 2 float16 -> E4M3.  NI: eights of elements a lane (rows of
+// up to 8 L NI).  VEC: lane l holds eights l, l + L, .., else elements l + L j.
+template <int Q, bool VEC, int NI, int L>
 __device__ __forceinline__ void put_row(int dim, uint8_t *dst, float *scale_at, bool on, const uint16_t (&w)[8 * NI]) {
-    const int lane = threadIdx.x & 15;
+    const int lane = threadIdx.x & (L - 1);
     if constexpr (Q == 0) {
         if (!on) return;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             if constexpr (VEC) {
-                if (8 * (lane + 16 * i) < dim)
-                    *reinterpret_cast<uint4 *>(dst + 16 * (lane + 16 * i)) = reinterpret_cast<const uint4 *>(w)[i];
+                if (8 * (lane + L * i) < dim)
+                    *reinterpret_cast<uint4 *>(dst + 16 * (lane + L * i)) = reinterpret_cast<const uint4 *>(w)[i];
             } else {
 #pragma unroll
                 for (int j = 8 * i; j < 8 * i + 8; ++j)
-                    if (lane + 16 * j < dim) reinterpret_cast<uint16_t *>(dst)[lane + 16 * j] = w[j];
+                    if (lane + L * j < dim) reinterpret_cast<uint16_t *>(dst)[lane + L * j] = w[j];
             }
         }
     } else {
@@ -79,51 +101,52 @@ __device__ __forceinline__ void put_row(int dim, uint8_t *dst, float *scale_at, 
             top = __vmaxu2(top, reinterpret_cast<const uint32_t *>(w)[j] & 0x7fff7fffu);
         top = max(top & 0xffffu, top >> 16);
 #pragma unroll
-        for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        for (int o = L / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
         const float most = value_of<Q>(top);
         float scale;
         uint32_t code[4 * NI];
-        auto encode = [&](auto &&quotient) {
+        auto encode = [&](auto &&quotients) {
 #pragma unroll
             for (int j = 0; j < 4 * NI; ++j)
                 code[j] = __nv_cvt_float2_to_fp8x2(
-                    make_float2(quotient(value_of<Q>(w[2 * j])), quotient(value_of<Q>(w[2 * j + 1]))), __NV_SATFINITE,
+                    quotients(make_float2(value_of<Q>(w[2 * j]), value_of<Q>(w[2 * j + 1]))), __NV_SATFINITE,
                     __NV_E4M3);
         };
-        if (__all_sync(0xffffffffu, most > 0x1p-90f && most < 0x1p90f)) {
-            scale = rounded_quotient(most, 448.f, 1.f / 448.f);
-            const float inverse = __frcp_rn(scale);
-            encode([&](float x) {
-                const float y = rounded_quotient(x, scale, inverse);
-                // a zero keeps its sign
-                return __uint_as_float(__float_as_uint(y) | (__float_as_uint(x) & 0x80000000u));
-            });
+        // rows of zeros too, which heads past the last one look like
+        if (__all_sync(0xffffffffu, most == 0.f || (most > 0x1p-90f && most < 0x1p90f))) {
+            scale = fmaxf(rounded_quotient(most, 448.f, 1.f / 448.f), 0x1p-126f);
+            const uint64_t d = twice(scale), minus_inverse = twice(-__frcp_rn(scale));
+            encode([&](float2 x) { return minus_quotients(x, d, minus_inverse); });
+#pragma unroll
+            for (int j = 0; j < 4 * NI; ++j) code[j] ^= 0x8080u;
         } else {
             const bool fine = top < (Q == 1 ? 0x7f80u : 0x7c00u);
-            scale = fine ? fmaxf(__fdiv_rn(most, 448.f), 1.17549435e-38f) : __int_as_float(0x7fc00000);
-            encode([&](float x) { return __fdiv_rn(x, scale); });
+            scale = fine ? fmaxf(__fdiv_rn(most, 448.f), 0x1p-126f) : __int_as_float(0x7fc00000);
+            encode([&](float2 x) { return make_float2(__fdiv_rn(x.x, scale), __fdiv_rn(x.y, scale)); });
         }
         if (!on) return;
         if (lane == 0) *scale_at = scale;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             if constexpr (VEC) {
-                if (8 * (lane + 16 * i) < dim)
-                    *reinterpret_cast<uint2 *>(dst + 8 * (lane + 16 * i)) =
+                if (8 * (lane + L * i) < dim)
+                    *reinterpret_cast<uint2 *>(dst + 8 * (lane + L * i)) =
                         make_uint2(code[4 * i] | code[4 * i + 1] << 16, code[4 * i + 2] | code[4 * i + 3] << 16);
             } else {
 #pragma unroll
                 for (int j = 8 * i; j < 8 * i + 8; ++j)
-                    if (lane + 16 * j < dim) dst[lane + 16 * j] = static_cast<uint8_t>(code[j / 2] >> (8 * (j & 1)));
+                    if (lane + L * j < dim) dst[lane + L * j] = static_cast<uint8_t>(code[j / 2] >> (8 * (j & 1)));
             }
         }
     }
 }
 
-// U: heads of a warp.  VEC: every row on both sides starts on the boundary of
-// eight elements and holds whole eights.
-template <int Q, bool VEC, int NI, int U>
+// A row by L lanes, so 32 / L rows at a time: keys' and values' of 16 / L
+// heads, U times.  VEC: every row on both sides starts on the boundary of eight
+// elements and holds whole eights.
+template <int Q, bool VEC, int NI, int L, int U>
 __global__ void __launch_bounds__(kApThreads) k_cache_append(const __grid_constant__ AppendArgs a) {
+    constexpr int P = 16 / L;  // heads at a time
     const CacheArgs &c = a.c;
     start_after_prior();
     const int64_t thread = int64_t(blockIdx.x) * kApThreads + threadIdx.x;
@@ -137,15 +160,14 @@ __global__ void __launch_bounds__(kApThreads) k_cache_append(const __grid_consta
     const uint32_t item = static_cast<uint32_t>(thread / 32);
     if (item >= a.items) return;
     const uint32_t bt = fast_div(item, a.head_div);
-    const int h0 = static_cast<int>(item - bt * a.head_div.d) * U;
+    const int first = static_cast<int>(item - bt * a.head_div.d) * U * P, h0 = first + (threadIdx.x & 31) / (2 * L);
     const int b = static_cast<int>(fast_div(bt, a.new_div));
     const int t = static_cast<int>(bt - static_cast<uint32_t>(b) * a.n_new);
-    if (a.counts && t >= a.counts[b]) return;
-    const int n = min(max(a.lengths[b], 0), c.cap);
-    if (t >= c.cap - n) return;
+    const int count = a.counts ? a.counts[b] : a.n_new, n = min(max(a.lengths[b], 0), c.cap);
+    if (t >= min(count, c.cap - n)) return;
 
-    const int lane = threadIdx.x & 15;
-    const bool is_v = threadIdx.x & 16;
+    const int lane = threadIdx.x & (L - 1);
+    const bool is_v = threadIdx.x & L;
     const int64_t head_stride = (is_v ? a.vst : a.kst)[2];
     const uint16_t *src = is_v ? a.v + b * a.vst[0] + t * a.vst[1] + h0 * head_stride
                                : a.k + b * a.kst[0] + t * a.kst[1] + h0 * head_stride;
@@ -154,17 +176,17 @@ __global__ void __launch_bounds__(kApThreads) k_cache_append(const __grid_consta
     for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const bool on = h0 + u < c.heads;
+            const bool on = h0 + u * P < c.heads;
             if constexpr (VEC) {
                 uint4 q = make_uint4(0, 0, 0, 0);
-                if (on && 8 * (lane + 16 * i) < c.dim)
-                    q = *reinterpret_cast<const uint4 *>(src + u * head_stride + 8 * (lane + 16 * i));
+                if (on && 8 * (lane + L * i) < c.dim)
+                    q = *reinterpret_cast<const uint4 *>(src + u * P * head_stride + 8 * (lane + L * i));
                 reinterpret_cast<uint4 *>(w[u])[i] = q;
             } else {
 #pragma unroll
                 for (int j = 8 * i; j < 8 * i + 8; ++j) {
-                    const int e = lane + 16 * j;
-                    w[u][j] = on && e < c.dim ? src[u * head_stride + e] : uint16_t(0);
+                    const int e = lane + L * j;
+                    w[u][j] = on && e < c.dim ? src[u * P * head_stride + e] : uint16_t(0);
                 }
             }
         }
@@ -174,34 +196,52 @@ __global__ void __launch_bounds__(kApThreads) k_cache_append(const __grid_consta
     const int64_t *st = is_v ? c.vst : c.kst, *sst = is_v ? c.vss : c.kss;
     uint8_t *dst = (is_v ? c.v : c.k) + row_offset(st, page, h0, row) * (Q ? 1 : 2);
     float *scale_at = Q ? (is_v ? c.vs : c.ks) + row_offset(sst, page, h0, row) : nullptr;
-    const int64_t dst_step = st[1] * (Q ? 1 : 2), scale_step = sst[1];
+    const int64_t dst_step = P * st[1] * (Q ? 1 : 2), scale_step = P * sst[1];
 #pragma unroll
-    for (int u = 0; u < U; ++u, dst += dst_step, scale_at += Q ? scale_step : 0)
-        put_row<Q, VEC, NI>(c.dim, dst, scale_at, h0 + u < c.heads, w[u]);
+    for (int u = 0; u < U && first + u * P < c.heads; ++u, dst += dst_step, scale_at += Q ? scale_step : 0)
+        put_row<Q, VEC, NI, L>(c.dim, dst, scale_at, h0 + u * P < c.heads, w[u]);
 }
 
 cudaError_t take_error_append(unsigned long long *v) { return take_module_error(v); }
 
 namespace {
 
-template <int Q, bool VEC, int NI, int U>
+template <int Q, bool VEC, int NI, int L, int U>
 int launch_append(AppendArgs &a, int64_t tokens, cudaStream_t cs) {
-    const int per = (a.c.heads + U - 1) / U;
+    constexpr int kHeads = U * 16 / L;
+    const int per = (a.c.heads + kHeads - 1) / kHeads;
     a.items = static_cast<uint32_t>(tokens * per);
     a.head_div = make_fastdiv(static_cast<uint32_t>(per));
     const uint64_t threads = std::max<uint64_t>(uint64_t(a.items) * 32, a.c.n_seqs);
-    return launch_after(reinterpret_cast<const void *>(&k_cache_append<Q, VEC, NI, U>),
+    return launch_after(reinterpret_cast<const void *>(&k_cache_append<Q, VEC, NI, L, U>),
                         static_cast<unsigned>((threads + kApThreads - 1) / kApThreads), kApThreads, 0, cs, &a);
 }
 
 template <int Q>
 int launch_append_as(AppendArgs &a, int64_t tokens, bool vec, cudaStream_t cs) {
-    if (!vec) return launch_append<Q, false, 2, 1>(a, tokens, cs);
-    // four heads a warp once there are warps enough to fill the GPU with them
-    const bool many = tokens * a.c.heads >= kApMany;
-    if (a.c.dim <= 128)
-        return many ? launch_append<Q, true, 1, 4>(a, tokens, cs) : launch_append<Q, true, 1, 1>(a, tokens, cs);
-    return many ? launch_append<Q, true, 2, 4>(a, tokens, cs) : launch_append<Q, true, 2, 1>(a, tokens, cs);
+    if (!vec) return launch_append<Q, false, 2, 16, 1>(a, tokens, cs);
+    // A head a warp until there are warps enough to fill the GPU, then four, and
+    // of rows to quantise eight where there are as many heads and rows again.
+    // The fewer lanes a row, the fewer instructions go into its scale and
+    // addresses: prompts of 8966 tokens of 8 heads of 128 with 16 lanes a row
+    // 14.9 us, 8 lanes 13.2, 4 lanes 11.9, 4 lanes and eight heads 11.8 (57 thousand
+    // such tokens 43.8, 39.5 and 35.2, 4096 tokens 4.6, 4.4 and 4.8).
+    const int64_t rows = tokens * a.c.heads;
+    const bool many = rows >= kApMany;
+    if constexpr (Q != 0) {
+        if (many && a.c.heads >= 4) {
+            const bool eight = a.c.heads > 4 && rows >= 2 * kApMany;
+            if (a.c.dim > 128) return launch_append<Q, true, 4, 8, 2>(a, tokens, cs);
+            if (a.c.dim > 64)
+                return eight ? launch_append<Q, true, 4, 4, 2>(a, tokens, cs)
+                             : launch_append<Q, true, 4, 4, 1>(a, tokens, cs);
+            return eight ? launch_append<Q, true, 2, 4, 2>(a, tokens, cs) : launch_append<Q, true, 2, 4, 1>(a, tokens, cs);
+        }
+    }
+    const bool four = many && a.c.heads > 1;
+    if (a.c.dim > 128)
+        return four ? launch_append<Q, true, 2, 16, 4>(a, tokens, cs) : launch_append<Q, true, 2, 16, 1>(a, tokens, cs);
+    return four ? launch_append<Q, true, 1, 16, 4>(a, tokens, cs) : launch_append<Q, true, 1, 16, 1>(a, tokens, cs);
 }
 
 }  // namespace
