@@ -55,7 +55,8 @@ cudaError_t prepare(const void *fn, int threads, int smem, int attr_smem, int *s
     *sms = it->second;
     const auto akey = std::make_pair(fn, dev);
     if (g_attr.find(akey) == g_attr.end()) {
-        if (attr_smem > 48 * 1024 &&
+        // a block has 48 KB unasked, its static memory among them
+        if (attr_smem > 16 * 1024 &&
             (e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, attr_smem)) != cudaSuccess)
             return e;
         g_attr.emplace(akey, attr_smem);

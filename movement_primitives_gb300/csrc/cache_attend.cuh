@@ -96,6 +96,7 @@ constexpr int kAtMinSteps = 4;
 // saves 5 us of a launch); at 16 steps a warp, 84 units of up to 125 steps
 // 24.5 and 14.9, 128 units of up to 128 steps of 8 KiB 25.9 and 21.5.
 constexpr int kUnitSteps = 8, kUnitBlocks = 304, kUnitCluster = 8;
+constexpr int kWarpSteps = 16, kWarpUnits = 608;
 
 struct AttendArgs {
     CacheArgs c;
@@ -110,6 +111,7 @@ struct AttendArgs {
     int32_t row_blocks;   // units of one key head
     float scale2;         // scale * log2 e
     bool q_wide;          // rows of q on 8-byte boundaries
+    bool warp_units;      // k_attend_unit: a unit a warp
     // workspace
     float *part;          // [2 runs][part_rows][part_pitch]
     float2 *part_ml;      // [2 runs][part_rows]
@@ -129,9 +131,15 @@ struct AttendArgs {
 template <int DP, int KV>
 constexpr int kUnitStages = DP * (KV == LC_CACHE_E4M3 ? 1 : 2) > 256 ? 2 : 3;
 
-inline int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
+// head_dim as the kernels take it; rows that are read element by element have
+// fewer forms.
+inline int padded_dim(int dim, bool vec) {
+    if (vec && dim > 64 && dim <= 96) return 96;
+    if (vec && dim > 128 && dim <= 192) return 192;
+    return dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
+}
 
-// Shapes of one instantiation.  DP: head_dim rounded up (64, 128, 256); KV: an
+// Shapes of one instantiation.  DP: head_dim rounded up (padded_dim); KV: an
 // lc_cache_type; NG: query heads in eights (1, 2); STAGES: steps in a warp's
 // ring.  A step is 8 KiB where the shapes allow.
 template <int DP, int KV, int NG, int STAGES>
@@ -275,7 +283,9 @@ struct Attend {
     bool next_seen;
 
     __device__ __forceinline__ static uint32_t swz(int row, int chunk) {
-        return S::RB >= 128 ? (chunk ^ (row & 7)) * 16 : (chunk ^ (row >> 1 & 3)) * 16;
+        if constexpr (S::RB % 128 == 0) return (chunk ^ (row & 7)) * 16;
+        if constexpr (S::RB % 64 == 0) return (chunk ^ (row >> 1 & 3)) * 16;
+        return (chunk ^ (row >> 2 & 1)) * 16;  // rows of 96 bytes
     }
 
     // The value column that row g (+ 8 i) of 16-wide piece c stands for: E4M3
@@ -796,9 +806,26 @@ __global__ void __launch_bounds__(kAtThreads, kAtBlocks) k_attend(const __grid_c
     }
 }
 
+// Adds the weights of a unit's slots, seen from c.lo on, to the scores: the
+// share of the `t`-th of `threads`.
+template <typename Lse>
+__device__ __forceinline__ void add_weights(const AttendArgs &a, const Place &c, int h, int q0, int rows, int t,
+                                            int threads, Lse &&lse_of) {
+    const float *x = a.logits + (int64_t(c.b) * a.q_heads + q0) * a.logit_stride;
+    for (int i = t; i < c.n - c.lo; i += threads) {
+        float w = 0.f;
+        for (int g = 0; g < rows; ++g) {
+            const float e = exp2_fast(x[g * a.logit_stride + i] - lse_of(g));
+            w += lse_of(g) == -INFINITY ? 0.f : e;
+        }
+        a.scores[c.b * a.sst[0] + h * a.sst[1] + c.lo + i] += w;
+    }
+}
+
 // One unit a block, or a cluster of blocks, its steps dealt to the warps in
 // turn; their results are joined in shared memory, the blocks' through
-// distributed shared memory, each block writing a share.
+// distributed shared memory, each block writing a share.  Or (warp_units) one
+// unit a warp.
 template <int DP, int KV, int NG>
 __global__ void __launch_bounds__(kAtThreads) k_attend_unit(const __grid_constant__ AttendArgs a) {
     using A = Attend<DP, KV, NG, true, kUnitStages<DP, KV>>;
@@ -813,13 +840,14 @@ __global__ void __launch_bounds__(kAtThreads) k_attend_unit(const __grid_constan
     const int units = a.c.heads * a.row_blocks;
     start_after_prior();
     Place c{};
-    const int at_unit = blockIdx.x / parts;
+    const int at_unit = a.warp_units ? blockIdx.x * kAtWarps + warp : blockIdx.x / parts;
+    if (at_unit >= a.c.n_seqs * units) return;  // warps of no unit, past every barrier
     c.b = at_unit / units;
     c.unit = at_unit - c.b * units;
     enter_sequence<S::TOK>(a, c);
     A u{a, lane, smem + warp * S::WARP_BYTES, ptx::smem_addr(smem + warp * S::WARP_BYTES), seen_bits + warp * S::ST};
     const int h = a.row_blocks == 1 ? c.unit : c.unit / a.row_blocks;
-    const int first = part * kAtWarps + warp, stride = parts * kAtWarps;
+    const int first = a.warp_units ? 0 : part * kAtWarps + warp, stride = a.warp_units ? 1 : parts * kAtWarps;
     int ahead = first;
     auto find = [&] {
         if (ahead < c.steps) u.find_pages(c.b, h, c.lo + ahead * S::TOK, c.n);
@@ -848,6 +876,20 @@ __global__ void __launch_bounds__(kAtThreads) k_attend_unit(const __grid_constan
         fill = fill + 1 == S::ST ? 0 : fill + 1;
     }
     u.total();
+    if (a.warp_units) {
+        u.write(-1);
+        if (!a.logits) return;
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float sum = u.l[g][i], lse = sum == 0.f ? -INFINITY : u.m[g][i] + log2f(sum);
+                if (lane < 4) ml[warp][8 * g + 2 * lane + i].x = lse;
+            }
+        __syncwarp();
+        add_weights(a, c, h, u.q0, u.rows, lane, 32, [&](int g) { return ml[warp][g].x; });
+        return;
+    }
     float *mine = reinterpret_cast<float *>(u.ring);
 #pragma unroll
     for (int g = 0; g < NG; ++g)
@@ -930,15 +972,8 @@ __global__ void __launch_bounds__(kAtThreads) k_attend_unit(const __grid_constan
             lse_of[t] = sum == 0.f ? -INFINITY : top + log2f(sum);
         }
         __syncthreads();
-        const float *x = a.logits + (int64_t(c.b) * a.q_heads + u.q0) * a.logit_stride;
-        for (int i = part * kAtThreads + t; i < c.n - c.lo; i += parts * kAtThreads) {
-            float w = 0.f;
-            for (int g = 0; g < u.rows; ++g) {
-                const float e = exp2_fast(x[g * a.logit_stride + i] - lse_of[g]);
-                w += lse_of[g] == -INFINITY ? 0.f : e;
-            }
-            a.scores[c.b * a.sst[0] + h * a.sst[1] + c.lo + i] += w;
-        }
+        add_weights(a, c, h, u.q0, u.rows, part * kAtThreads + t, parts * kAtThreads,
+                    [&](int g) { return lse_of[g]; });
     }
     if (parts > 1) cluster.sync();  // no block leaves while another reads its shared memory
 }
@@ -955,6 +990,9 @@ int launch_attend(const AttendArgs &a, int unit_blocks, int *runs, cudaStream_t 
             constexpr int kBytes = AtShape<DP, KV, NG, kUnitStages<DP, KV>>::SMEM;
             const void *fn = reinterpret_cast<const void *>(&k_attend_unit<DP, KV, NG>);
             if (prepare(fn, kAtThreads, kBytes, kBytes, &sms, &per) != cudaSuccess) return LC_ERR_CUDA;
+            if (a.warp_units)
+                return launch_after(fn, static_cast<unsigned>((units + kAtWarps - 1) / kAtWarps), kAtThreads, kBytes,
+                                    cs, &a);
             return launch_after(fn, static_cast<unsigned>(units * unit_blocks), kAtThreads, kBytes, cs, &a,
                                 unit_blocks);
         }
@@ -983,9 +1021,16 @@ int launch_attend_type(const AttendArgs &a, int unit_blocks, bool vec, int *runs
         return vec ? launch_attend<DP, KV, 2, true>(a, unit_blocks, runs, cs)
                    : launch_attend<DP, KV, 2, false>(a, unit_blocks, runs, cs);
     };
-    switch (padded_dim(a.c.dim)) {
+    auto wide_heads = [&](auto dp) {
+        constexpr int DP = decltype(dp)::value;
+        return a.group <= 8 ? launch_attend<DP, KV, 1, true>(a, unit_blocks, runs, cs)
+                            : launch_attend<DP, KV, 2, true>(a, unit_blocks, runs, cs);
+    };
+    switch (padded_dim(a.c.dim, vec)) {
         case 64: return heads(std::integral_constant<int, 64>{});
+        case 96: return wide_heads(std::integral_constant<int, 96>{});
         case 128: return heads(std::integral_constant<int, 128>{});
+        case 192: return wide_heads(std::integral_constant<int, 192>{});
         default: return heads(std::integral_constant<int, 256>{});
     }
 }

@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kJoinMost) k_attend_join(const __grid_constant
         const float safe = v.x == -INFINITY ? 0.f : v.x, f = v.y == 0.f ? 0.f : 1.f / v.y;
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-        for (int i = first; i < r.parts.count; i += lanes) part(r, i, col, safe, y);
+        for (int i = first < lanes ? first : r.parts.count; i < r.parts.count; i += lanes) part(r, i, col, safe, y);
         __syncthreads();
         *reinterpret_cast<float4 *>(acc + first * a.part_pitch + col) = y;
         __syncthreads();
@@ -196,14 +196,15 @@ int launch_attend_e4m3(const AttendArgs &a, int unit_blocks, bool vec, int *runs
 namespace {
 
 // Slots of a step: AtShape's TOK.
-int step_slots(int dim, int type) { return 8192 / (2 * padded_dim(dim) * cache_elem_bytes(type)) >= 32 ? 32 : 16; }
+int step_slots(int padded, int type) { return 8192 / (2 * padded * cache_elem_bytes(type)) >= 32 ? 32 : 16; }
 
 // How a call of these sizes goes: a block or a cluster a unit, or runs; with
 // runs, or with scores, it needs a workspace of these offsets and this end.
 struct AttendSpace {
     bool vec;      // rows of the pools are whole 16-byte words on 16-byte boundaries
+    bool warp_units;  // a unit a warp
     int unit_blocks;  // 0: by runs
-    int part_rows;
+    int part_rows, dim;
     int64_t part, ml, split, lse2, logits, end, logit_stride;
 };
 
@@ -213,13 +214,16 @@ bool attend_space(const lc_paged_cache &cache, const CacheArgs &c, int q_heads, 
     const int64_t pool[3] = {cache.n_pages, cache.n_kv_heads, cache.page_size};
     s->vec = c.dim * eb % 16 == 0 && rows_aligned(cache.k, 3, pool, cache.k_stride, eb, 16) &&
              rows_aligned(cache.v, 3, pool, cache.v_stride, eb, 16);
-    const int tok = step_slots(c.dim, cache.type), group = q_heads / c.heads;
+    s->dim = padded_dim(c.dim, s->vec);
+    const int tok = step_slots(s->dim, cache.type), group = q_heads / c.heads;
     const int64_t units = c.heads * ((int64_t(group) + kAtRows - 1) / kAtRows), heads = int64_t(c.n_seqs) * q_heads;
     // scores of a key head whose query heads are several units' need the
     // second launch
     s->unit_blocks = 0;
+    s->warp_units = false;
     const int64_t steps = ((window ? std::min(window, c.cap) : c.cap) + int64_t(tok) - 1) / tok;
     if (s->vec && !(scores && group > kAtRows)) {
+        s->warp_units = steps <= kWarpSteps && c.n_seqs * units >= kWarpUnits;
         int n = 1;
         while (2 * n <= kUnitCluster && n * kAtWarps < steps && c.n_seqs * units * 2 * n <= kUnitBlocks) n *= 2;
         if (steps <= int64_t(kUnitSteps) * kAtWarps * n) s->unit_blocks = n;
@@ -227,7 +231,7 @@ bool attend_space(const lc_paged_cache &cache, const CacheArgs &c, int q_heads, 
     s->part_rows = std::min(group, kAtRows);
     const int64_t parts = s->unit_blocks ? 0 : int64_t(2) * kAtMaxRuns * s->part_rows;
     s->part = 0;
-    s->ml = s->part + parts * padded_dim(c.dim) * 4;
+    s->ml = s->part + parts * s->dim * 4;
     s->split = s->ml + round256(parts * 8);
     s->lse2 = round256(s->split + (s->unit_blocks ? 0 : c.n_seqs * units * 8));
     s->logits = round256(s->lse2 + (scores ? heads * 4 : 0));
@@ -310,7 +314,8 @@ extern "C" int lc_cache_attend(const lc_paged_cache *cache, const lc_cache_query
     a.logits = a.scores ? reinterpret_cast<float *>(ws + space.logits) : nullptr;
     a.logit_stride = space.logit_stride;
     a.part_rows = space.part_rows;
-    a.part_pitch = padded_dim(a.c.dim);
+    a.part_pitch = space.dim;
+    a.warp_units = space.warp_units;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     int runs = 0;
     const auto launch = cache->type == LC_CACHE_BF16  ? launch_attend_bf16

@@ -594,9 +594,8 @@ int launch_evict_small(EvictArgs &a, cudaStream_t cs) {
     a.word_div = make_fastdiv(static_cast<uint32_t>(2 * (a.c.dim * EB / 16 / a.slices)));
     const void *fn = reinterpret_cast<const void *>(&k_evict_small<EB>);
     int sms, per;
-    // 48 KB at most, and static memory besides: more than a block has unasked
     constexpr int kMost = 4 * (kSmSlots + kSmMoved / 32);  // half the slots: twice the ranks
-    if (prepare(fn, kSmThreads, 0, kMost + 1024, &sms, &per) != cudaSuccess) return LC_ERR_CUDA;
+    if (prepare(fn, kSmThreads, 0, kMost, &sms, &per) != cudaSuccess) return LC_ERR_CUDA;
     return launch_after(fn, static_cast<unsigned>(int64_t(a.c.n_seqs) * a.c.heads * a.slices), kSmThreads,
                         4 * (size_t(a.held_keys) + a.budget), cs, &a);
 }
