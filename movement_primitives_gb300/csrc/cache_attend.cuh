@@ -96,7 +96,14 @@ constexpr int kAtMinSteps = 4;
 // saves 5 us of a launch); at 16 steps a warp, 84 units of up to 125 steps
 // 24.5 and 14.9, 128 units of up to 128 steps of 8 KiB 25.9 and 21.5.
 constexpr int kUnitSteps = 8, kUnitBlocks = 304, kUnitCluster = 8;
-constexpr int kWarpSteps = 16, kWarpUnits = 608;
+// Where a unit would be one block's, it is one warp's instead if that is
+// sooner, counting kUnitCost steps for what a unit costs besides its own: the
+// blocks' rounds of kUnitBlocks units against the warps' of four times as many.
+// A warp against a block: 1000 sequences of up to 64 slots of 8 key heads 42
+// and 96 us, 600 of up to 500 (E4M3) 79 and 110, 100 of 200 14.0 and 15.1, but 40
+// of up to 250 19.2 and 9.4; at the boundary 100 of 200 (bfloat16) 18.6 and 17.6,
+// 76 of up to 100 10.0 and 10.0.
+constexpr int kUnitCost = 2;
 
 struct AttendArgs {
     CacheArgs c;
@@ -812,13 +819,27 @@ template <typename Lse>
 __device__ __forceinline__ void add_weights(const AttendArgs &a, const Place &c, int h, int q0, int rows, int t,
                                             int threads, Lse &&lse_of) {
     const float *x = a.logits + (int64_t(c.b) * a.q_heads + q0) * a.logit_stride;
-    for (int i = t; i < c.n - c.lo; i += threads) {
-        float w = 0.f;
-        for (int g = 0; g < rows; ++g) {
-            const float e = exp2_fast(x[g * a.logit_stride + i] - lse_of(g));
-            w += lse_of(g) == -INFINITY ? 0.f : e;
+    float *to = a.scores + c.b * a.sst[0] + h * a.sst[1] + c.lo;
+    const int n = c.n - c.lo;
+    for (int i0 = t; i0 < n; i0 += kScorePer * threads) {
+        float w[kScorePer], old[kScorePer];
+#pragma unroll
+        for (int k = 0; k < kScorePer; ++k) {
+            w[k] = 0.f;
+            old[k] = i0 + k * threads < n ? to[i0 + k * threads] : 0.f;
         }
-        a.scores[c.b * a.sst[0] + h * a.sst[1] + c.lo + i] += w;
+        for (int g = 0; g < rows; ++g, x += a.logit_stride) {
+            const float lse = lse_of(g);
+#pragma unroll
+            for (int k = 0; k < kScorePer; ++k) {
+                const float e = i0 + k * threads < n ? exp2_fast(x[i0 + k * threads] - lse) : 0.f;
+                w[k] += lse == -INFINITY ? 0.f : e;
+            }
+        }
+        x -= rows * a.logit_stride;
+#pragma unroll
+        for (int k = 0; k < kScorePer; ++k)
+            if (i0 + k * threads < n) to[i0 + k * threads] = old[k] + w[k];
     }
 }
 

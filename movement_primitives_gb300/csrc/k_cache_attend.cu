@@ -223,10 +223,15 @@ bool attend_space(const lc_paged_cache &cache, const CacheArgs &c, int q_heads, 
     s->warp_units = false;
     const int64_t steps = ((window ? std::min(window, c.cap) : c.cap) + int64_t(tok) - 1) / tok;
     if (s->vec && !(scores && group > kAtRows)) {
-        s->warp_units = steps <= kWarpSteps && c.n_seqs * units >= kWarpUnits;
+        const int64_t all = c.n_seqs * units;
         int n = 1;
-        while (2 * n <= kUnitCluster && n * kAtWarps < steps && c.n_seqs * units * 2 * n <= kUnitBlocks) n *= 2;
-        if (steps <= int64_t(kUnitSteps) * kAtWarps * n) s->unit_blocks = n;
+        while (2 * n <= kUnitCluster && n * kAtWarps < steps && all * 2 * n <= kUnitBlocks) n *= 2;
+        if (steps <= int64_t(kUnitSteps) * kAtWarps * n) {
+            s->unit_blocks = n;
+            const int64_t rounds = (all - 1) / kUnitBlocks + 1, deal = (steps + kAtWarps - 1) / kAtWarps;
+            s->warp_units = n == 1 && std::max<int64_t>(all, kAtWarps * kUnitBlocks) * (kUnitCost + steps) <
+                                          kAtWarps * kUnitBlocks * rounds * (kUnitCost + deal);
+        }
     }
     s->part_rows = std::min(group, kAtRows);
     const int64_t parts = s->unit_blocks ? 0 : int64_t(2) * kAtMaxRuns * s->part_rows;

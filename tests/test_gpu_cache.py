@@ -270,6 +270,28 @@ def test_attend_units_cut_into_runs(kind, dim, group):
         attend(s, 12 * group, scores=True, mask=mask, window=n - 7)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "e4m3"])
+@pytest.mark.parametrize("dim,group", [(80, 8), (80, 12), (160, 3), (192, 16), (144, 9)])
+def test_attend_between_padded_sizes_in_runs(kind, dim, group):
+    """Head sizes that are padded to less than a power of two, units cut into many parts."""
+    s = Setup([4300, 35, 0, 2051], heads=12, dim=dim, kind=kind, page=30, seed=dim + group)
+    attend(s, 12 * group, scores=True)
+    s = Setup([26001], heads=1, dim=dim, kind=kind, page=64, seed=dim)
+    attend(s, group, window=25000)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "e4m3"])
+@pytest.mark.parametrize("dim,group", [(64, 1), (64, 16), (80, 3), (128, 4), (128, 12), (192, 9), (256, 2), (256, 16)])
+def test_attend_a_unit_a_warp(kind, dim, group):
+    """Many units of few steps, of every length from none, their number no multiple of a block's."""
+    s = Setup([(5 * i) % 67 for i in range(211)], heads=3, dim=dim, kind=kind, page=16, order="token", seed=dim + group)
+    attend(s, 3 * group, scores=True)
+    mask = (torch.rand((211, s.cap), generator=s.g) < 0.5).cuda()
+    mask[::4] = False
+    attend(s, 3 * group, scores=True, mask=mask, window=40)
+    attend(s, 3 * group)
+
+
 def test_attend_many_sequences():
     attend(Setup([(7 * i) % 97 for i in range(700)], heads=1, dim=64, seed=8), 2, scores=True)
     attend(Setup([(131 * i) % 900 for i in range(150)], heads=4, dim=128, seed=9), 16, scores=True)
