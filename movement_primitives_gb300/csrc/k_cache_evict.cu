@@ -44,6 +44,7 @@ namespace cg = cooperative_groups;
 constexpr int kSelBins = 2048;      // 64 groups of 32
 constexpr int kSelRound = 2048;     // slots are dealt to blocks in so many
 constexpr int kSelKeys = 48 * 1024; // keys a block holds in shared memory
+constexpr int kSelEase = 16384;     // keys a block rather holds
 constexpr int kSelCluster = 8;      // blocks of a unit at most
 constexpr int kSelLeast = 4096;     // slots a block of a cluster has at least
 constexpr int kSmThreads = 512;     // of a block that selects and moves
@@ -612,12 +613,18 @@ int launch_evict(EvictArgs &a, cudaStream_t cs) {
     if (prepare(move, kMvThreads, smem, smem, &sms, &move_per) != cudaSuccess) return LC_ERR_CUDA;
     // Selection.  Clusters where there are few units and many slots, a block an
     // SM at most (of 16 blocks, which are no longer portable, measured slower:
-    // 45 against 27 us for 8 units of 131071 slots); where blocks have an SM
-    // each and many slots a thread, 1024 threads (26 against 31 us).
+    // 45 against 27 us for 8 units of 131071 slots), and where a block would hold
+    // more than kSelEase keys, twice that where it has an SM to itself: two
+    // blocks share an SM and hide each other's barriers (320 units of 20000 slots
+    // 48 against 57 us, 800 of them 92 against 111, 160 of 50000 77 against 122;
+    // but 32 of 98340 34.3 with 256 blocks and 32.5 with 128).  Where blocks have an
+    // SM each and many slots a thread, 1024 threads (26 against 31 us).
     int parts = 1;
     while (parts < kSelCluster && units * parts * 2 <= sms && a.c.cap / (2 * parts) >= kSelLeast) parts *= 2;
     const int rounds = a.c.cap ? (a.c.cap - 1) / kSelRound + 1 : 0;
-    const int64_t hold = int64_t(rounds + parts - 1) / parts * kSelRound;
+    auto keys_held = [&] { return int64_t(rounds + parts - 1) / parts * kSelRound; };
+    while (parts < kSelCluster && keys_held() > (units * parts <= sms ? 2 * kSelEase : kSelEase)) parts *= 2;
+    const int64_t hold = keys_held();
     const bool held = hold <= kSelKeys;
     const int threads = units * parts <= sms && hold > 4096 ? 1024 : 512;
     const void *forms[2][2] = {{reinterpret_cast<const void *>(&k_evict_select<false, 512>),

@@ -613,6 +613,15 @@ def test_evict_more_slots_than_shared_memory_holds():
     check_evict(s, (4 * x[1:]).round().cuda()[..., :s.cap].contiguous(), 40, 0)
 
 
+@pytest.mark.parametrize("lengths,heads", [([430001, 9], 1), ([20000, 16500, 40], 90), ([40000] * 3, 60)])
+def test_evict_clusters(lengths, heads):
+    """More slots than a cluster's blocks hold keys of, and clusters of units too many for an SM a block."""
+    s = Setup(lengths, heads=heads, dim=8, page=500, seed=heads)
+    x = torch.exp(2 * torch.randn((len(lengths), heads, s.cap), generator=s.g))
+    x[:, ::2] = (x[:, ::2] * 4).round()
+    check_evict(s, x.cuda(), 700, 50)
+
+
 def test_evict_strided_arguments_and_streams():
     s = Setup([100, 60], heads=2, dim=64, seed=2)
     wide = torch.rand((2, 3, s.cap + 3), generator=s.g).cuda()
