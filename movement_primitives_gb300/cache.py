@@ -19,15 +19,18 @@ __all__ = ["PagedCache", "cache_append", "cache_attend", "cache_attend_workspace
 _STRIDES = struct.Struct("@3q")                      # int64_t[3]
 _QUERY = struct.Struct("@PPiiqqqqPPqifPqPqqPq")     # lc_cache_query
 _EVICTION = struct.Struct("@PPqqiiPqqPqqPPq")        # lc_cache_eviction
-_TYPES = None  # torch dtype -> lc_cache_type
-_BYTES = None  # torch.uint8
+# of torch, known once a cache exists
+_TYPES = None  # dtype -> lc_cache_type
+_BYTES = _BOOL = _I32 = _F32 = None
+_CURRENT = None  # raw handle of a device's current stream (torch.cuda.current_stream() builds an object, 3 us)
 
 
 def _types():
-    global _TYPES, _BYTES
+    global _TYPES, _BYTES, _BOOL, _I32, _F32, _CURRENT
     if _TYPES is None:
         import torch
-        _BYTES = torch.uint8
+        _BYTES, _BOOL, _I32, _F32 = torch.uint8, torch.bool, torch.int32, torch.float32
+        _CURRENT = torch._C._cuda_getCurrentRawStream
         _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
     return _TYPES
 
@@ -36,12 +39,6 @@ def _check(status: int, what: str) -> None:
     if status != 0:
         from . import LayoutCopyError
         raise LayoutCopyError(status, what)
-
-
-def _current(device) -> int:
-    """Handle of the current stream (the raw query: torch.cuda.current_stream() builds an object, 3 us)."""
-    import torch
-    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _allocator():
@@ -75,15 +72,16 @@ class _on:
 
 def _tensor(t, name: str, dtype, shape, device):
     """A tensor of that type and shape on the cache's device whose last mode's elements are adjacent."""
+    if t.dtype is dtype and t.shape == shape and t.device == device and (
+            t.is_contiguous() or shape[-1] <= 1 or t.stride(-1) == 1):
+        return t
     if t.dtype != dtype:
         raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.shape != shape:
-        raise ValueError("%s must have shape %r, got %r" % (name, shape, tuple(t.shape)))
+        raise ValueError("%s must have shape %r, got %r" % (name, tuple(shape), tuple(t.shape)))
     if t.device != device:
         raise ValueError("%s is on %s, the cache on %s" % (name, t.device, device))
-    if shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError("%s: the elements of the last mode must be adjacent" % name)
-    return t
+    raise ValueError("%s: the elements of the last mode must be adjacent" % name)
 
 
 class PagedCache:
@@ -135,6 +133,7 @@ class PagedCache:
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
         self.capacity = self.page_size * self.pages_per_seq
         self._empty = _allocator()
+        self._index, self._seqs = k.device.index, (self.n_seqs,)
         self.scale = 1.0 / math.sqrt(self.head_dim)
         self.io_dtype = torch.bfloat16 if q8 else k.dtype
 
@@ -168,32 +167,32 @@ def cache_append(cache: PagedCache, k, v, lengths, counts=None, new_lengths=None
     ``lengths``.  Tokens past a sequence's capacity are dropped and set the device
     error word (``last_device_error``).
     """
-    import torch
-    if k.dim() != 4 or k.dtype not in (torch.bfloat16, torch.float16):
+    shape = k.shape
+    kind = _TYPES.get(k.dtype)
+    if len(shape) != 4 or kind is None or kind > 1:
         raise ValueError("new keys and values are [seqs, tokens, kv_heads, head_dim] of bfloat16 or float16")
-    n_new = k.shape[1]
-    shape = (cache.n_seqs, n_new, cache.n_kv_heads, cache.head_dim)
-    _tensor(k, "k", k.dtype, shape, cache.device)
-    _tensor(v, "v", k.dtype, shape, cache.device)
-    _tensor(lengths, "lengths", torch.int32, (cache.n_seqs,), cache.device)
+    device, seqs = cache.device, cache._seqs
+    _tensor(k, "k", k.dtype, (cache.n_seqs, shape[1], cache.n_kv_heads, cache.head_dim), device)
+    _tensor(v, "v", k.dtype, shape, device)
+    _tensor(lengths, "lengths", _I32, seqs, device)
     if counts is not None:
-        _tensor(counts, "counts", torch.int32, (cache.n_seqs,), cache.device)
+        _tensor(counts, "counts", _I32, seqs, device)
     if new_lengths is not None:
-        _tensor(new_lengths, "new_lengths", torch.int32, (cache.n_seqs,), cache.device)
+        _tensor(new_lengths, "new_lengths", _I32, seqs, device)
     if stream is not None:
         with _on(stream) as handle:
-            return _append(cache, k, v, n_new, counts, lengths, new_lengths, handle)
-    return _append(cache, k, v, n_new, counts, lengths, new_lengths, _current(cache.device))
+            return _append(cache, k, v, kind, shape[1], counts, lengths, new_lengths, handle)
+    return _append(cache, k, v, kind, shape[1], counts, lengths, new_lengths, _CURRENT(cache._index))
 
 
-def _append(cache, k, v, n_new, counts, lengths, new_lengths, handle):
+def _append(cache, k, v, kind, n_new, counts, lengths, new_lengths, handle):
     if new_lengths is None:
-        new_lengths = cache._empty((cache.n_seqs,), (1,), lengths.dtype)
-    ks, vs = k.stride(), v.stride()
-    _check(_lib.lib().lc_cache_append(cache._ref, k.data_ptr(), v.data_ptr(), _types()[k.dtype],
-                                      _STRIDES.pack(ks[0], ks[1], ks[2]), _STRIDES.pack(vs[0], vs[1], vs[2]), n_new,
-                                      None if counts is None else counts.data_ptr(), lengths.data_ptr(),
-                                      new_lengths.data_ptr(), handle), "cache_append")
+        new_lengths = cache._empty(cache._seqs, (1,), _I32)
+    status = _lib.lib().lc_cache_append(
+        cache._ref, k.data_ptr(), v.data_ptr(), kind, _STRIDES.pack(*k.stride()[:3]), _STRIDES.pack(*v.stride()[:3]),
+        n_new, None if counts is None else counts.data_ptr(), lengths.data_ptr(), new_lengths.data_ptr(), handle)
+    if status:
+        _check(status, "cache_append")
     return new_lengths
 
 
@@ -220,33 +219,34 @@ def cache_attend(cache: PagedCache, q, lengths, out=None, scale=None, window: in
     [seqs, kv_heads, capacity]; each slot's weight, summed over its query heads, is
     added to it.  A row with no slot seen gives zeros (lse: -inf).
     """
-    import torch
-    if q.dim() != 3:
+    shape = q.shape
+    if len(shape) != 3:
         raise ValueError("q is [seqs, q_heads, head_dim]")
-    n_q = q.shape[1]
-    _tensor(q, "q", cache.io_dtype, (cache.n_seqs, n_q, cache.head_dim), cache.device)
-    _tensor(lengths, "lengths", torch.int32, (cache.n_seqs,), cache.device)
+    n_q, n_seqs, device = shape[1], cache.n_seqs, cache.device
+    _tensor(q, "q", cache.io_dtype, (n_seqs, n_q, cache.head_dim), device)
+    _tensor(lengths, "lengths", _I32, cache._seqs, device)
     if mask is not None:
-        if mask.dtype not in (torch.bool, torch.uint8):
+        if mask.dtype is not _BOOL and mask.dtype is not _BYTES:
             raise ValueError("mask must be bool or uint8, got %s" % mask.dtype)
-        _tensor(mask, "mask", mask.dtype, (cache.n_seqs, cache.capacity), cache.device)
+        _tensor(mask, "mask", mask.dtype, (n_seqs, cache.capacity), device)
     if lse is not None:
-        _tensor(lse, "lse", torch.float32, (cache.n_seqs, n_q), cache.device)
+        _tensor(lse, "lse", _F32, (n_seqs, n_q), device)
     if scores is not None:
-        _tensor(scores, "scores", torch.float32, (cache.n_seqs, cache.n_kv_heads, cache.capacity), cache.device)
+        _tensor(scores, "scores", _F32, (n_seqs, cache.n_kv_heads, cache.capacity), device)
     if out is not None:
-        _tensor(out, "out", q.dtype, q.shape, cache.device)
-    if workspace is not None and (workspace.device != cache.device or not workspace.is_contiguous()):
+        _tensor(out, "out", q.dtype, shape, device)
+    if workspace is not None and (workspace.device != device or not workspace.is_contiguous()):
         raise ValueError("the workspace must be contiguous and on the cache's device")
     if stream is not None:
         with _on(stream) as handle:
-            return _attend(cache, q, lengths, out, scale, window, mask, lse, scores, workspace, handle)
-    return _attend(cache, q, lengths, out, scale, window, mask, lse, scores, workspace, _current(cache.device))
+            return _attend(cache, q, n_q, lengths, out, scale, window, mask, lse, scores, workspace, handle)
+    return _attend(cache, q, n_q, lengths, out, scale, window, mask, lse, scores, workspace, _CURRENT(cache._index))
 
 
-def _attend(cache, q, lengths, out, scale, window, mask, lse, scores, workspace, handle):
-    n_q, d = q.shape[1], cache.head_dim
+def _attend(cache, q, n_q, lengths, out, scale, window, mask, lse, scores, workspace, handle):
+    kind = _TYPES[q.dtype]
     if out is None:
+        d = cache.head_dim
         out = cache._empty((cache.n_seqs, n_q, d), (n_q * d, d, 1), q.dtype)
     ws, ws_bytes = 0, 0
     if workspace is not None:
@@ -256,15 +256,22 @@ def _attend(cache, q, lengths, out, scale, window, mask, lse, scores, workspace,
         if ws_bytes:
             workspace = cache._empty((ws_bytes,), (1,), _BYTES)
             ws = workspace.data_ptr()
-    qs, os = q.stride(), out.stride()
-    ss = (0, 0, 0) if scores is None else scores.stride()
+    q0, q1, _ = q.stride()
+    o0, o1, _ = out.stride()
     # lc_cache_query, packed in one call (a ctypes structure's fields one by one cost several times that)
-    a = _QUERY.pack(q.data_ptr(), out.data_ptr(), _types()[q.dtype], n_q, qs[0], qs[1], os[0], os[1],
-                    lengths.data_ptr(), 0 if mask is None else mask.data_ptr(), 0 if mask is None else mask.stride(0),
-                    min(window, 0x7fffffff), cache.scale if scale is None else scale,
-                    0 if lse is None else lse.data_ptr(), 0 if lse is None else lse.stride(0),
-                    0 if scores is None else scores.data_ptr(), ss[0], ss[1], ws, ws_bytes)
-    _check(_lib.lib().lc_cache_attend(cache._ref, a, handle), "cache_attend")
+    masked, mask_stride, logs, lse_stride, sums, s0, s1 = 0, 0, 0, 0, 0, 0, 0
+    if mask is not None:
+        masked, mask_stride = mask.data_ptr(), mask.stride(0)
+    if lse is not None:
+        logs, lse_stride = lse.data_ptr(), lse.stride(0)
+    if scores is not None:
+        sums, (s0, s1, _) = scores.data_ptr(), scores.stride()
+    a = _QUERY.pack(q.data_ptr(), out.data_ptr(), kind, n_q, q0, q1, o0, o1, lengths.data_ptr(), masked, mask_stride,
+                    window if window < 0x7fffffff else 0x7fffffff, cache.scale if scale is None else scale, logs,
+                    lse_stride, sums, s0, s1, ws, ws_bytes)
+    status = _lib.lib().lc_cache_attend(cache._ref, a, handle)
+    if status:
+        _check(status, "cache_attend")
     return out
 
 
@@ -281,37 +288,40 @@ def cache_evict(cache: PagedCache, lengths, scores, budget: int, recent: int = 0
     budget), in a tensor other than ``lengths``.  The pages a sequence's table
     names must be its own.
     """
-    import torch
-    unit = (cache.n_seqs, cache.n_kv_heads)
-    _tensor(lengths, "lengths", torch.int32, (cache.n_seqs,), cache.device)
-    _tensor(scores, "scores", torch.float32, unit + (cache.capacity,), cache.device)
+    n_seqs, heads, device = cache.n_seqs, cache.n_kv_heads, cache.device
+    _tensor(lengths, "lengths", _I32, cache._seqs, device)
+    _tensor(scores, "scores", _F32, (n_seqs, heads, cache.capacity), device)
     budget, recent = int(budget), int(recent)
     if kept is not None:
-        _tensor(kept, "kept", torch.int32, unit + (budget,), cache.device)
+        _tensor(kept, "kept", _I32, (n_seqs, heads, budget), device)
     if new_scores is not None:
-        _tensor(new_scores, "new_scores", torch.float32, scores.shape, cache.device)
+        _tensor(new_scores, "new_scores", _F32, scores.shape, device)
     if new_lengths is not None:
-        _tensor(new_lengths, "new_lengths", torch.int32, (cache.n_seqs,), cache.device)
+        _tensor(new_lengths, "new_lengths", _I32, cache._seqs, device)
     if stream is not None:
         with _on(stream) as handle:
             return _evict(cache, lengths, scores, budget, recent, new_scores, kept, new_lengths, handle)
-    return _evict(cache, lengths, scores, budget, recent, new_scores, kept, new_lengths, _current(cache.device))
+    return _evict(cache, lengths, scores, budget, recent, new_scores, kept, new_lengths, _CURRENT(cache._index))
 
 
 def _evict(cache, lengths, scores, budget, recent, new_scores, kept, new_lengths, handle):
-    b, h, cap = scores.shape
+    b, h, cap = cache.n_seqs, cache.n_kv_heads, cache.capacity
     if kept is None:
         n = max(budget, 0)
-        kept = cache._empty((b, h, n), (h * n, n, 1), lengths.dtype)
+        kept = cache._empty((b, h, n), (h * n, n, 1), _I32)
     if new_scores is None:
-        new_scores = cache._empty((b, h, cap), (h * cap, cap, 1), scores.dtype)
+        new_scores = cache._empty((b, h, cap), (h * cap, cap, 1), _F32)
     if new_lengths is None:
-        new_lengths = cache._empty((b,), (1,), lengths.dtype)
+        new_lengths = cache._empty((b,), (1,), _I32)
     ws_bytes = cache.evict_workspace_bytes(budget)
     workspace = cache._empty((ws_bytes,), (1,), _BYTES) if ws_bytes else None
-    ss, ks, ns = scores.stride(), kept.stride(), new_scores.stride()
-    a = _EVICTION.pack(lengths.data_ptr(), scores.data_ptr(), ss[0], ss[1], budget, recent, kept.data_ptr(), ks[0],
-                       ks[1], new_scores.data_ptr(), ns[0], ns[1], new_lengths.data_ptr(),
+    s0, s1, _ = scores.stride()
+    k0, k1, _ = kept.stride()
+    n0, n1, _ = new_scores.stride()
+    a = _EVICTION.pack(lengths.data_ptr(), scores.data_ptr(), s0, s1, budget, recent, kept.data_ptr(), k0, k1,
+                       new_scores.data_ptr(), n0, n1, new_lengths.data_ptr(),
                        workspace.data_ptr() if ws_bytes else 0, ws_bytes)
-    _check(_lib.lib().lc_cache_evict(cache._ref, a, handle), "cache_evict")
+    status = _lib.lib().lc_cache_evict(cache._ref, a, handle)
+    if status:
+        _check(status, "cache_evict")
     return kept, new_scores, new_lengths
