@@ -104,6 +104,8 @@ constexpr int kUnitSteps = 8, kUnitBlocks = 304, kUnitCluster = 8;
 // of up to 250 19.2 and 9.4; at the boundary 100 of 200 (bfloat16) 18.6 and 17.6,
 // 76 of up to 100 10.0 and 10.0.
 constexpr int kUnitCost = 2;
+// The largest shape's registers hold no second form of the end.
+constexpr __host__ __device__ bool unit_by_warp(int padded, int rows) { return padded < 256 || rows <= 8; }
 
 struct AttendArgs {
     CacheArgs c;
@@ -133,10 +135,17 @@ struct AttendArgs {
     FastDiv chunk_div, head_div, q_div, group_div;
 };
 
+// Slots of a step: of 8 KiB where the shapes allow, but 32 of E4M3 rows of 192
+// (12 KiB; 16 of them 89 us for 32 sequences of up to 8000 slots of 8 key heads,
+// 32 of them 77; of bfloat16 rows of 96, the same 192 bytes, 65 and 66).
+constexpr int step_slots(int padded, int elem_bytes) {
+    return padded * elem_bytes <= (elem_bytes == 1 ? 192 : 128) ? 32 : 16;
+}
+
 // Steps in a warp's ring where a unit is a block's: few steps, whose latency
 // counts.
 template <int DP, int KV>
-constexpr int kUnitStages = DP * (KV == LC_CACHE_E4M3 ? 1 : 2) > 256 ? 2 : 3;
+constexpr int kUnitStages = DP * (KV == LC_CACHE_E4M3 ? 1 : 2) > 256 || DP == 192 ? 2 : 3;
 
 // head_dim as the kernels take it; rows that are read element by element have
 // fewer forms.
@@ -148,13 +157,13 @@ inline int padded_dim(int dim, bool vec) {
 
 // Shapes of one instantiation.  DP: head_dim rounded up (padded_dim); KV: an
 // lc_cache_type; NG: query heads in eights (1, 2); STAGES: steps in a warp's
-// ring.  A step is 8 KiB where the shapes allow.
+// ring.
 template <int DP, int KV, int NG, int STAGES>
 struct AtShape {
     static constexpr int EB = KV == LC_CACHE_E4M3 ? 1 : 2;
     static constexpr int RB = DP * EB;                       // bytes of a row
     static constexpr int CH = RB / 16;                       // its 16-byte chunks
-    static constexpr int TOK = 8192 / (2 * RB) >= 32 ? 32 : 16;
+    static constexpr int TOK = step_slots(DP, EB);
     static constexpr int STEP = 2 * TOK * RB;                // keys, then values
     static constexpr int ST = STAGES;
     static constexpr int SC = KV == LC_CACHE_E4M3 ? 2 * TOK * 4 : 0;  // scales of a step
@@ -861,14 +870,15 @@ __global__ void __launch_bounds__(kAtThreads) k_attend_unit(const __grid_constan
     const int units = a.c.heads * a.row_blocks;
     start_after_prior();
     Place c{};
-    const int at_unit = a.warp_units ? blockIdx.x * kAtWarps + warp : blockIdx.x / parts;
+    const bool by_warp = unit_by_warp(DP, 8 * NG) && a.warp_units;
+    const int at_unit = by_warp ? blockIdx.x * kAtWarps + warp : blockIdx.x / parts;
     if (at_unit >= a.c.n_seqs * units) return;  // warps of no unit, past every barrier
     c.b = at_unit / units;
     c.unit = at_unit - c.b * units;
     enter_sequence<S::TOK>(a, c);
     A u{a, lane, smem + warp * S::WARP_BYTES, ptx::smem_addr(smem + warp * S::WARP_BYTES), seen_bits + warp * S::ST};
     const int h = a.row_blocks == 1 ? c.unit : c.unit / a.row_blocks;
-    const int first = a.warp_units ? 0 : part * kAtWarps + warp, stride = a.warp_units ? 1 : parts * kAtWarps;
+    const int first = by_warp ? 0 : part * kAtWarps + warp, stride = by_warp ? 1 : parts * kAtWarps;
     int ahead = first;
     auto find = [&] {
         if (ahead < c.steps) u.find_pages(c.b, h, c.lo + ahead * S::TOK, c.n);
@@ -897,7 +907,7 @@ __global__ void __launch_bounds__(kAtThreads) k_attend_unit(const __grid_constan
         fill = fill + 1 == S::ST ? 0 : fill + 1;
     }
     u.total();
-    if (a.warp_units) {
+    if (by_warp) {
         u.write(-1);
         if (!a.logits) return;
 #pragma unroll

@@ -195,9 +195,6 @@ int launch_attend_e4m3(const AttendArgs &a, int unit_blocks, bool vec, int *runs
 
 namespace {
 
-// Slots of a step: AtShape's TOK.
-int step_slots(int padded, int type) { return 8192 / (2 * padded * cache_elem_bytes(type)) >= 32 ? 32 : 16; }
-
 // How a call of these sizes goes: a block or a cluster a unit, or runs; with
 // runs, or with scores, it needs a workspace of these offsets and this end.
 struct AttendSpace {
@@ -215,7 +212,7 @@ bool attend_space(const lc_paged_cache &cache, const CacheArgs &c, int q_heads, 
     s->vec = c.dim * eb % 16 == 0 && rows_aligned(cache.k, 3, pool, cache.k_stride, eb, 16) &&
              rows_aligned(cache.v, 3, pool, cache.v_stride, eb, 16);
     s->dim = padded_dim(c.dim, s->vec);
-    const int tok = step_slots(s->dim, cache.type), group = q_heads / c.heads;
+    const int tok = step_slots(s->dim, cache_elem_bytes(cache.type)), group = q_heads / c.heads;
     const int64_t units = c.heads * ((int64_t(group) + kAtRows - 1) / kAtRows), heads = int64_t(c.n_seqs) * q_heads;
     // scores of a key head whose query heads are several units' need the
     // second launch
@@ -229,8 +226,9 @@ bool attend_space(const lc_paged_cache &cache, const CacheArgs &c, int q_heads, 
         if (steps <= int64_t(kUnitSteps) * kAtWarps * n) {
             s->unit_blocks = n;
             const int64_t rounds = (all - 1) / kUnitBlocks + 1, deal = (steps + kAtWarps - 1) / kAtWarps;
-            s->warp_units = n == 1 && std::max<int64_t>(all, kAtWarps * kUnitBlocks) * (kUnitCost + steps) <
-                                          kAtWarps * kUnitBlocks * rounds * (kUnitCost + deal);
+            const int64_t warps = kAtWarps * kUnitBlocks;
+            s->warp_units = n == 1 && unit_by_warp(s->dim, group) &&
+                            std::max(all, warps) * (kUnitCost + steps) < warps * rounds * (kUnitCost + deal);
         }
     }
     s->part_rows = std::min(group, kAtRows);
