@@ -38,9 +38,9 @@
 // joins in their order, so results do not depend on timing.  Each warp streams
 // its run through a ring of its own in shared memory (cp.async, 16 bytes a
 // lane, rows swizzled for ldmatrix) that runs ahead across units, with no
-// barrier between warps.  Where units are few and short (kUnitSteps) a block
-// or a cluster of blocks takes one instead, joined in shared memory, with no
-// second launch.
+// barrier between warps.  Where units are short (kUnitSteps) a block, a cluster
+// of blocks (few units) or a warp (many) takes one instead, joined in shared
+// memory, with no second launch.
 //
 // Measured on GB300 (device time a call; the copy peak is 6678 GB/s): 64
 // sequences of up to 8192 slots, 32 query on 8 key heads of 128 bfloat16, 1.09
@@ -147,8 +147,11 @@ constexpr int step_slots(int padded, int elem_bytes) {
 template <int DP, int KV>
 constexpr int kUnitStages = DP * (KV == LC_CACHE_E4M3 ? 1 : 2) > 256 || DP == 192 ? 2 : 3;
 
-// head_dim as the kernels take it; rows that are read element by element have
-// fewer forms.
+// head_dim as the kernels take it.  Columns past head_dim cost products and
+// registers, not bytes: 2 sequences of up to 99459 float16 slots, 16 query heads
+// a key head of 192, padded to 256 273 us, to 192 155; 7 sequences of up to 1999,
+// 12 heads of 80, to 128 15.0, to 96 14.0.  Rows that are read element by element
+// are slower than either and have fewer forms.
 inline int padded_dim(int dim, bool vec) {
     if (vec && dim > 64 && dim <= 96) return 96;
     if (vec && dim > 128 && dim <= 192) return 192;

@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kJoinMost) k_attend_join(const __grid_constant
         }
     }
     __syncthreads();
-    const int lanes = threads / quads;  // parts read at a time
+    const int lanes = threads / quads;  // parts read at a time; threads past them only write
     const int col = t % quads * 4, first = t / quads;
     for (int w = 0; w < a.join_rows; ++w) {
         if (!whole_block[w]) continue;

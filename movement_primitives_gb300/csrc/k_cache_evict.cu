@@ -28,10 +28,10 @@
 // once.
 //
 // Measured on GB300: 15 sequences of up to 16384 bfloat16 slots of 8 heads cut
-// to 4096, 403 MB moved, 93 us: the selection 21 us (bound by the latency of
+// to 4096, 403 MB moved, 92 us: the selection 20 us (bound by the latency of
 // its passes over the keys, each a barrier of the cluster), the move 72 us (5.6
-// TB/s).  One sequence of 131071 E4M3 slots cut to 32768, 138 MB, 62 us: 27 us
-// of selection on 64 blocks, 35 us of rows of 128 bytes.  Four sequences of
+// TB/s).  One sequence of 131071 E4M3 slots cut to 32768, 138 MB, 60 us: 26 us
+// of selection on 64 blocks, 34 us of rows of 128 bytes.  Four sequences of
 // 1500 cut to 1024, 34 MB, in one launch 15.5 us.
 #include <cooperative_groups.h>
 
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_evict_select(const 
 // reads before its writes (a barrier between them); the next run's reads need
 // not wait for these: the source slot of rank j that moves is above j, and no
 // rank up to j writes there.  The barrier and one run in flight a block make
-// its rate 11 GB/s or so, which is why units of many bytes a block do not come here.
+// it about 9 GB/s, which is why units of many bytes a block do not come here.
 template <int EB>
 __global__ void __launch_bounds__(kSmThreads, 2) k_evict_small(const __grid_constant__ EvictArgs a) {
     extern __shared__ __align__(16) uint32_t keys[];
