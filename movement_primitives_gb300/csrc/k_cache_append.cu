@@ -235,7 +235,8 @@ int launch_append_as(AppendArgs &a, int64_t tokens, bool vec, cudaStream_t cs) {
             if (a.c.dim > 64)
                 return eight ? launch_append<Q, true, 4, 4, 2>(a, tokens, cs)
                              : launch_append<Q, true, 4, 4, 1>(a, tokens, cs);
-            return eight ? launch_append<Q, true, 2, 4, 2>(a, tokens, cs) : launch_append<Q, true, 2, 4, 1>(a, tokens, cs);
+            return eight ? launch_append<Q, true, 2, 4, 2>(a, tokens, cs)
+                         : launch_append<Q, true, 2, 4, 1>(a, tokens, cs);
         }
     }
     const bool four = many && a.c.heads > 1;

@@ -329,8 +329,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_evict_select(const 
 // nothing of one another.  A block moves runs of words in rank order, a run's
 // reads before its writes (a barrier between them); the next run's reads need
 // not wait for these: the source slot of rank j that moves is above j, and no
-// rank up to j writes there.  The barrier and one run in flight a block make
-// it about 9 GB/s, which is why units of many bytes a block do not come here.
+// rank up to j writes there.  A block moves about 9 GB/s (one run in flight,
+// and its barrier), which is why units of many bytes a block do not come here.
 template <int EB>
 __global__ void __launch_bounds__(kSmThreads, 2) k_evict_small(const __grid_constant__ EvictArgs a) {
     extern __shared__ __align__(16) uint32_t keys[];
