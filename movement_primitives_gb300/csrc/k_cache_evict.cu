@@ -35,6 +35,8 @@
 // 1500 cut to 1024, 34 MB, in one launch 15.5 us.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "cache_common.cuh"
 
 namespace lc {
@@ -231,50 +233,59 @@ __device__ __forceinline__ void select_slots(const EvictArgs &a, int parts, int 
         });
     }
     // 128 slots at a time, four adjacent ones a lane: the lanes' counts of sure
-    // and (from bit 16) tied ones, scanned, give each its rank
-    for (int i0 = w0; i0 < w1; i0 += 128) {
-        const int i = i0 + 4 * lane;
-        uint32_t key[4] = {}, count = 0;
-        if (i < w1) {
-            if constexpr (HELD) {
-                *reinterpret_cast<uint4 *>(key) = *reinterpret_cast<const uint4 *>(keys + (i - s0));
-            } else {
+    // and (from bit 16) tied ones, scanned, give each its rank.  Most calls have
+    // no ties to tell apart, and half the instructions.
+    const uint32_t above = any ? prefix : 0xffffffffu;  // competing slots of larger keys are sure
+    auto place = [&](auto with_ties) {
+        constexpr bool TIES = decltype(with_ties)::value;
+        for (int i0 = w0; i0 < w1; i0 += 128) {
+            const int i = i0 + 4 * lane;
+            uint32_t key[4] = {}, count = 0;
+            if (i < w1) {
+                if constexpr (HELD) {
+                    *reinterpret_cast<uint4 *>(key) = *reinterpret_cast<const uint4 *>(keys + (i - s0));
+                } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (i + j < w1) key[j] = score_key(scores[i + j]);
+                    for (int j = 0; j < 4; ++j)
+                        if (i + j < w1) key[j] = score_key(scores[i + j]);
+                }
             }
-        }
-        bool is_sure[4], is_tied[4];
+            bool is_sure[4], is_tied[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const bool competes = i + j < c1;
-            is_sure[j] = competes ? any && key[j] > prefix : i + j < w1;
-            is_tied[j] = competes && any && key[j] == prefix;
-            count += (is_sure[j] ? 1u : 0u) + (is_tied[j] ? 1u << 16 : 0u);
-        }
-        uint32_t upto = count;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += y;
-        }
-        uint32_t g = sure + (upto - count & 0xffff), e = tied + (upto - count >> 16);
-        // every eighth lane's first slot starts 32 of them
-        if ((lane & 7) == 0 && i < w1) rank(i / kMvRows, g + min(e, need));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t r = g + min(e, need);
-            if (is_sure[j] || (is_tied[j] && e < need)) {
-                // a positive score is its key but for the top bit; others are read again
-                stay(r, i + j, key[j] > 0x80000000u ? __uint_as_float(key[j] ^ 0x80000000u) : scores[i + j]);
+            for (int j = 0; j < 4; ++j) {
+                // (every score's key is above 0)
+                is_sure[j] = key[j] > (i + j < c1 ? above : i + j < w1 ? 0u : 0xffffffffu);
+                is_tied[j] = TIES && i + j < c1 && key[j] == prefix;
+                count += (is_sure[j] ? 1u : 0u) + (is_tied[j] ? 1u << 16 : 0u);
             }
-            g += is_sure[j];
-            e += is_tied[j];
+            uint32_t upto = count;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += y;
+            }
+            uint32_t g = sure + (upto - count & 0xffff), e = tied + (upto - count >> 16);
+            // every eighth lane's first slot starts 32 of them
+            if ((lane & 7) == 0 && i < w1) rank(i / kMvRows, g + (TIES ? min(e, need) : 0));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (is_sure[j] || (is_tied[j] && e < need)) {
+                    // a positive score is its key but for the top bit; others are read again
+                    stay(g + (TIES ? min(e, need) : 0), i + j,
+                         key[j] > 0x80000000u ? __uint_as_float(key[j] ^ 0x80000000u) : scores[i + j]);
+                }
+                g += is_sure[j];
+                if (TIES) e += is_tied[j];
+            }
+            const uint32_t all_of = __shfl_sync(0xffffffffu, upto, 31);
+            sure += all_of & 0xffff;
+            tied += all_of >> 16;
         }
-        const uint32_t all_of = __shfl_sync(0xffffffffu, upto, 31);
-        sure += all_of & 0xffff;
-        tied += all_of >> 16;
-    }
+    };
+    if (any && need > 0)
+        place(std::true_type{});
+    else
+        place(std::false_type{});
     if constexpr (CLUSTER) cg::this_cluster().sync();  // no block leaves while another reads its shared memory
 }
 
