@@ -28,10 +28,10 @@
 // once.
 //
 // Measured on GB300: 15 sequences of up to 16384 bfloat16 slots of 8 heads cut
-// to 4096, 403 MB moved, 92 us: the selection 20 us (bound by the latency of
-// its passes over the keys, each a barrier of the cluster), the move 72 us (5.6
-// TB/s).  One sequence of 131071 E4M3 slots cut to 32768, 138 MB, 60 us: 26 us
-// of selection on 64 blocks, 34 us of rows of 128 bytes.  Four sequences of
+// to 4096, 403 MB moved, 90 us: the selection 18 us (bound by the latency of
+// its passes over the keys, each a barrier of the block or cluster), the move 72
+// us (5.6 TB/s).  One sequence of 131071 E4M3 slots cut to 32768, 138 MB, 59 us:
+// 25 us of selection on 64 blocks, 34 us of rows of 128 bytes.  Four sequences of
 // 1500 cut to 1024, 34 MB, in one launch 15.5 us.
 #include <cooperative_groups.h>
 
@@ -77,9 +77,8 @@ struct EvictArgs {
 
 // Larger scores have larger keys; NaN counts as -infinity, -0 as 0.
 __device__ __forceinline__ uint32_t score_key(float s) {
-    if (isnan(s)) s = __int_as_float(0xff800000);
-    const uint32_t u = __float_as_uint(s + 0.f);
-    return u >> 31 ? ~u : u | 0x80000000u;
+    const uint32_t u = __float_as_uint(fmaxf(s, -INFINITY) + 0.f);  // the maximum is not the NaN
+    return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
 }
 
 // From the largest down: the one of 32 lanes' counts that holds the need-th,
@@ -201,15 +200,17 @@ __device__ __forceinline__ void select_slots(const EvictArgs &a, int parts, int 
     // before it.
     const int w0 = static_cast<int>(lmin(s0 + int64_t(warp) * run, s1));
     const int w1 = static_cast<int>(lmin(w0 + int64_t(run), s1));
+    const uint32_t above = any ? prefix : 0xffffffffu;  // competing slots of larger keys are sure
+    const bool ties = any && need > 0;
     uint32_t sure = 0, tied = 0;
 #pragma unroll 4
     for (int i = w0 + lane; i < w1; i += 32) {
         const uint32_t key = key_of(i);
-        sure += i >= cand || (any && key > prefix);
-        tied += i < cand && any && key == prefix;
+        sure += key > (i < c1 ? above : 0);  // (every score's key is above 0)
+        if (ties) tied += i < c1 && key == prefix;
     }
     sure = __reduce_add_sync(0xffffffffu, sure);
-    tied = __reduce_add_sync(0xffffffffu, tied);
+    if (ties) tied = __reduce_add_sync(0xffffffffu, tied);
     if (lane == 0) warp_counts[warp] = make_uint2(sure, tied);
     __syncthreads();
     sure = tied = 0;
@@ -235,7 +236,6 @@ __device__ __forceinline__ void select_slots(const EvictArgs &a, int parts, int 
     // 128 slots at a time, four adjacent ones a lane: the lanes' counts of sure
     // and (from bit 16) tied ones, scanned, give each its rank.  Most calls have
     // no ties to tell apart, and half the instructions.
-    const uint32_t above = any ? prefix : 0xffffffffu;  // competing slots of larger keys are sure
     auto place = [&](auto with_ties) {
         constexpr bool TIES = decltype(with_ties)::value;
         for (int i0 = w0; i0 < w1; i0 += 128) {
@@ -253,7 +253,6 @@ __device__ __forceinline__ void select_slots(const EvictArgs &a, int parts, int 
             bool is_sure[4], is_tied[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                // (every score's key is above 0)
                 is_sure[j] = key[j] > (i + j < c1 ? above : i + j < w1 ? 0u : 0xffffffffu);
                 is_tied[j] = TIES && i + j < c1 && key[j] == prefix;
                 count += (is_sure[j] ? 1u : 0u) + (is_tied[j] ? 1u << 16 : 0u);
@@ -282,7 +281,7 @@ __device__ __forceinline__ void select_slots(const EvictArgs &a, int parts, int 
             tied += all_of >> 16;
         }
     };
-    if (any && need > 0)
+    if (ties)
         place(std::true_type{});
     else
         place(std::false_type{});
@@ -311,6 +310,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_evict_select(const 
     if (unit == 0 && at == 0) *a.ticket = 0;
     for (int i = at; i < a.chunks; i += all) a.done[int64_t(unit) * a.chunks + i] = 0;
     for (int i = m + at; i < a.budget; i += all) kept[i] = -1;
+#pragma unroll 4
     for (int i = m + at; i < a.c.cap; i += all) out[i] = 0.f;
     if (n == m) {  // the same for the whole cluster
         for (int i = at; i < m; i += all) {
