@@ -962,7 +962,10 @@ __global__ void __launch_bounds__(kAtThreads) k_attend_unit(const __grid_constan
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (col + i < a.c.dim) to[col + i] = static_cast<uint16_t>(pack2<A::F16>(y[i] * f, 0.f));
-        if (col == 0) lse_of[head] = u.write_lse(u.q0 + head, v.x, v.y);
+        if (col == 0) {
+            const float lse = u.write_lse(u.q0 + head, v.x, v.y);
+            if (parts == 1) lse_of[head] = lse;  // a cluster's blocks form all heads' below
+        }
     };
     for (int at = t; at < u.rows * (DP / 4); at += kAtThreads) {
         const int head = at / (DP / 4), col = at % (DP / 4) * 4;
