@@ -17,18 +17,22 @@
 // by one 8 x 8 transpose across lanes (movmatrix) a slot octet.  With G query
 // heads a key head the pass does G operations a byte of 16-bit cache, so
 // memory bounds it up to the 16 heads of a unit and the accumulators fit
-// registers.  The weights are rounded to the values' 16-bit type for the
-// second product (by at most 2^-9, or 2^-12 in float16, of each, no more than
-// the output's own rounding); the sum l takes them unrounded.  Float16 has few
-// exponents, so its weights are lifted by 2^14: the largest is 2^14, and one of
-// 2^-38 of it is still held to a bit, so that a million slots together lose
-// nothing to an outlier above them.
+// registers.  A weight enters the second product as two numbers of the values'
+// 16-bit type, its leading bits (8 in bfloat16, 11 in float16) and what they
+// leave, rounded: together within 2^-16 and 2^-22 of it, so that the output's own
+// rounding is the only one that shows (one rounded number a weight: errors against
+// 64 bits 7 to 20 % larger).  Neither is negative, and of a positive weight neither
+// is zero, so that an infinite value stays one.  The sum l takes the weights whole.  Float16 has few exponents, so its weights are
+// lifted by 2^14: the largest is 2^14, and one of 2^-38 of it is still held to a
+// bit, so that a million slots together lose nothing to an outlier above them.
 //
 // E4M3 codes are float16 numbers, converted exactly two at a time; their
 // products run in float16.  The keys' scales multiply the logits.  The values'
 // scales s_j join the weights as 2^(x_j + log2 |s_j| - mv), mv the running
 // maximum of that exponent (lifted as above): the largest weight is the same
-// whatever the scales; o is kept relative to mv.
+// whatever the scales; o is kept relative to mv.  These weights are one float16
+// number each: 2^-11 is an eighth of the bfloat16 output's rounding, and a second
+// number would go into the pass that instructions bound.
 //
 // Work.  Slots are taken in steps of TOK by one warp.  A (sequence, key head,
 // block of 16 query heads) is a unit; the steps of all units, laid end to end,
@@ -223,6 +227,22 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
         const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
         return *reinterpret_cast<const uint32_t *>(&v);
     }
+}
+
+// Two numbers >= 0 as the sums of two each: `lead`, their leading bits, and
+// `rest`, the remainders, rounded, but above 0 for a number above 0.
+template <bool F16>
+__device__ __forceinline__ void split2(float lo, float hi, uint32_t *lead, uint32_t *rest) {
+    constexpr float kLeast = F16 ? 0x1p-24f : 0x1p-133f;  // the type's smallest step
+    float2 v;
+    if constexpr (F16) {
+        asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(*lead) : "f"(hi), "f"(lo));
+        v = __half22float2(*reinterpret_cast<const __half2 *>(lead));
+    } else {
+        *lead = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+        v = make_float2(__uint_as_float(*lead << 16), __uint_as_float(*lead & 0xffff0000u));
+    }
+    *rest = pack2<F16>(fmaxf(lo - v.x, fminf(lo, kLeast)), fmaxf(hi - v.y, fminf(hi, kLeast)));
 }
 
 // Two E4M3 codes (the low 16 bits) as float16, exactly.
@@ -615,13 +635,20 @@ struct Attend {
         }
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-            uint32_t p[NG][2];
+            uint32_t p[NG][2], rest[NG][2];
 #pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                // slots lane / 4 of two heads -> head lane / 4 of two slots
-                p[g][0] = transpose8(pack2<M16>(x[t][g][0], x[t][g][1]));
-                p[g][1] = transpose8(pack2<M16>(x[t][g][2], x[t][g][3]));
-            }
+            for (int g = 0; g < NG; ++g)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    // slots lane / 4 of two heads -> head lane / 4 of two slots
+                    if constexpr (Q8) {
+                        p[g][i] = transpose8(pack2<true>(x[t][g][2 * i], x[t][g][2 * i + 1]));
+                    } else {
+                        split2<F16>(x[t][g][2 * i], x[t][g][2 * i + 1], &p[g][i], &rest[g][i]);
+                        p[g][i] = transpose8(p[g][i]);
+                        rest[g][i] = transpose8(rest[g][i]);
+                    }
+                }
             if constexpr (Q8) {
                 // slots 0-7 and 8-15 of two 16-wide pieces; a register holds two adjacent columns
                 // of two slots
@@ -647,6 +674,8 @@ struct Attend {
                     ldsm_x4_t(r, vs_s + row * S::RB + swz(row, 2 * c + (mat & 1)));
 #pragma unroll
                     for (int g = 0; g < NG; ++g) mma16816<F16>(o[c][g], r[0], r[1], r[2], r[3], p[g]);
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) mma16816<F16>(o[c][g], r[0], r[1], r[2], r[3], rest[g]);
                 }
             }
         }

@@ -41,3 +41,61 @@ def test_weights_of_a_unit_over_a_cluster_repeat(kind, group):
         again, logs = torch.zeros_like(first), torch.zeros_like(lse)
         assert torch.equal(lc().cache_attend(s.cache, q, s.lengths, scores=again, lse=logs), out)
         assert torch.equal(again, first) and torch.equal(logs, lse)
+
+
+# What a result may be off by (U_OUT: rounding to the output's type; U_WEIGHT: what a weight of the second product may
+# be off by, relatively).  16-bit caches: a weight is the sum of two numbers of the cache's type, its rounding (off by at
+# most u = 2^-8 in bfloat16, 2^-11 in float16) and the rounding of the rest, so u^2 (with the leading bits as the first
+# one: a rest below 2^-7 of the weight's power of two, rounded by half a step of at most 2^-15 of that, the same);
+# float16's smallest step, 2^-24 beside a largest weight of 2^14, adds half of it a slot.  E4M3 caches: one float16 number, 2^-11; the scale's logarithm
+# adds 2^-18 (2^-22 of at most 8, times ln 2 and a rounding), and the queries' conversion to float16 2^-25 of the
+# head's largest element an element.
+U_OUT = {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11, "e4m3": 2.0 ** -8}
+U_WEIGHT = {"bf16": 2.0 ** -16, "fp16": 2.0 ** -22, "e4m3": 2.0 ** -11 + 2.0 ** -18}
+
+
+def check_close(s, q, out, window=0, mask=None):
+    scale = 1 / math.sqrt(s.dim)
+    k, v = s.values()
+    qn, n = q.double().cpu().numpy(), s.lengths.cpu().numpy()
+    want, _, _, mag, reach = oc.attend(qn, k, v, s.table.cpu().numpy(), n, scale, window,
+                                       None if mask is None else mask.cpu().numpy())
+    err = (s.dim + 8) * 2.0 ** -24 * reach
+    if s.kind == "e4m3":
+        err = err + 2.0 ** -25 * scale * np.abs(qn).max(2) * np.abs(k).sum(3).max()
+    rel = 2 * err + (n.max() / 8 + 8) * 2.0 ** -23
+    off = mag * (U_WEIGHT[s.kind] + rel[..., None])
+    if s.kind == "fp16":
+        off = off + 2.0 ** -39 * n.max() * np.abs(v).max()
+    got = out.double().cpu().numpy()
+    tiny = {"fp16": 2.0 ** -25}.get(s.kind, 2.0 ** -134)  # half of the output's smallest step
+    worst = (np.abs(got - want) - (off + U_OUT[s.kind] * (np.abs(want) + off) + tiny)).max()
+    assert worst <= 0, worst
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "e4m3"])
+@pytest.mark.parametrize("dim,group", [(64, 1), (80, 5), (128, 4), (128, 16), (192, 12), (256, 8), (256, 16), (33, 3)])
+def test_attend_is_as_near_as_its_output_type_allows(kind, dim, group):
+    """Every form: a block, a cluster or a warp a unit, and runs that are joined; a few slots and many."""
+    for lens, heads in (([2, 3, 5, 17, 40, 0, 300], 3), ([(5 * i) % 67 for i in range(211)], 3),
+                        ([2100, 35, 0, 1051], 12)):
+        s = Setup(lens, heads=heads, dim=dim, kind=kind, page=16, seed=dim + group)
+        q = s.queries(heads * group)
+        check_close(s, q, lc().cache_attend(s.cache, q, s.lengths))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("lens,heads,dim", [([1, 2, 30], 2, 64), ([700, 1], 2, 128), ([4200, 35, 1], 12, 64), ([20, 1], 2, 33)])
+def test_an_infinite_value_in_a_seen_slot_stays_infinite(kind, lens, heads, dim):
+    """Weights that are whole in the cache's type (one slot's is 1) and weights that are not."""
+    s = Setup(lens, heads=heads, dim=dim, kind=kind, page=16, seed=dim)
+    for b in range(s.n_seq):
+        page = int(s.table[b, 0])
+        s.v[page, :, 0, 3], s.v[page, :, 0, 7] = math.inf, -math.inf
+    q = s.queries(2 * heads) * 0.25  # no weight below 2^-38 of the largest
+    q = q.to(IO[kind])
+    out = lc().cache_attend(s.cache, q, s.lengths).float()
+    assert torch.all(out[..., 3] == math.inf) and torch.all(out[..., 7] == -math.inf)
+    rest = [c for c in range(dim) if c not in (3, 7)]
+    assert torch.all(out[..., rest].isfinite())
+    no_device_error()
