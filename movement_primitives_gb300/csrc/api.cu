@@ -53,13 +53,14 @@ cudaError_t prepare(const void *fn, int threads, int smem, int attr_smem, int *s
         it = g_sms.emplace(dev, n).first;
     }
     *sms = it->second;
-    const auto akey = std::make_pair(fn, dev);
-    if (g_attr.find(akey) == g_attr.end()) {
-        // a block has 48 KB unasked, its static memory among them
+    // A block has 48 KB unasked, its static memory among them; a limit once set
+    // is raised by a later call of the same kernel that needs more.
+    int &limit = g_attr[std::make_pair(fn, dev)];
+    if (attr_smem > limit) {
         if (attr_smem > 16 * 1024 &&
             (e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, attr_smem)) != cudaSuccess)
             return e;
-        g_attr.emplace(akey, attr_smem);
+        limit = attr_smem;
     }
     const auto key = std::make_tuple(fn, dev, threads, smem);
     auto jt = g_occ.find(key);

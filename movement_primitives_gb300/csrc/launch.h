@@ -13,8 +13,8 @@ namespace lc {
 // Limit of every bounded device wait (LC_WAIT_TIMEOUT_NS overrides 2 s).
 uint64_t wait_limit_ns();
 
-// Opts `fn` into `attr_smem` bytes of dynamic shared memory on the current
-// device (once) and reports the SM count and resident blocks per SM.
+// Opts `fn` into at least `attr_smem` bytes of dynamic shared memory on the
+// current device and reports the SM count and resident blocks per SM.
 cudaError_t prepare(const void *fn, int threads, int smem, int attr_smem, int *sms, int *per_sm);
 
 inline int finish_launch() { return cudaGetLastError() == cudaSuccess ? LC_OK : LC_ERR_CUDA; }

@@ -99,3 +99,22 @@ def test_an_infinite_value_in_a_seen_slot_stays_infinite(kind, lens, heads, dim)
     rest = [c for c in range(dim) if c not in (3, 7)]
     assert torch.all(out[..., rest].isfinite())
     no_device_error()
+
+
+ASCENDING = """
+import sys
+sys.path[:0] = [%r, %r]
+import torch
+from test_gpu_cache import Setup, check_evict
+for dim in (130, 136, 192, 255, 256, 64):
+    s = Setup([8300, 40, 4099], heads=2, dim=dim, kind=%r, page=64, seed=dim)
+    check_evict(s, torch.rand((3, 2, s.cap), generator=s.g).cuda(), 150, 10)
+"""
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_evict_head_sizes_one_after_the_other(kind):
+    """Two-launch evictions of growing rows in a process of their own: a small one may not limit a later one."""
+    code = ASCENDING % (os.path.join(ROOT, "tests"), ROOT, kind)
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
