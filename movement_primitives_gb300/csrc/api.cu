@@ -44,12 +44,16 @@ std::map<int, int> g_sms;
 cudaError_t prepare(const void *fn, int threads, int smem, int attr_smem, int *sms, int *per_sm) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
+    auto failed = [&] {  // returned here: the next call's check does not see it
+        cudaGetLastError();
+        return e;
+    };
+    if (e != cudaSuccess) return failed();
     std::lock_guard<std::mutex> lk(g_mu);
     auto it = g_sms.find(dev);
     if (it == g_sms.end()) {
         int n = 0;
-        if ((e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+        if ((e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return failed();
         it = g_sms.emplace(dev, n).first;
     }
     *sms = it->second;
@@ -59,14 +63,14 @@ cudaError_t prepare(const void *fn, int threads, int smem, int attr_smem, int *s
     if (attr_smem > limit) {
         if (attr_smem > 16 * 1024 &&
             (e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, attr_smem)) != cudaSuccess)
-            return e;
+            return failed();
         limit = attr_smem;
     }
     const auto key = std::make_tuple(fn, dev, threads, smem);
     auto jt = g_occ.find(key);
     if (jt == g_occ.end()) {
         int nb = 0;
-        if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, fn, threads, smem)) != cudaSuccess) return e;
+        if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, fn, threads, smem)) != cudaSuccess) return failed();
         jt = g_occ.emplace(key, nb < 1 ? 1 : nb).first;
     }
     *per_sm = jt->second;

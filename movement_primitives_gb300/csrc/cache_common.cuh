@@ -79,7 +79,9 @@ inline int launch_after(const void *fn, unsigned grid, unsigned threads, size_t 
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
     void *args[] = {const_cast<void *>(arg)};
-    return cudaLaunchKernelExC(&cfg, fn, args) == cudaSuccess ? LC_OK : LC_ERR_CUDA;
+    if (cudaLaunchKernelExC(&cfg, fn, args) == cudaSuccess) return LC_OK;
+    cudaGetLastError();  // reported here: the next call's check does not see it
+    return LC_ERR_CUDA;
 }
 
 inline int cache_elem_bytes(int type) { return type == LC_CACHE_E4M3 ? 1 : 2; }
