@@ -854,6 +854,13 @@ __global__ void __launch_bounds__(kAtThreads, kAtBlocks) k_attend(const __grid_c
     }
 }
 
+// The weight of a slot from its logit and its row's log sum, both base 2.  A
+// slot that is not seen (logit -infinity) has none whatever the sum is: it is
+// NaN where a seen slot's logit is, -infinity where nothing is seen.
+__device__ __forceinline__ float weight_of(float logit, float lse) {
+    return logit == -INFINITY ? 0.f : exp2_fast(logit - lse);
+}
+
 // Adds the weights of a unit's slots, seen from c.lo on, to the scores: the
 // share of the `t`-th of `threads`.
 template <typename Lse>
@@ -873,8 +880,7 @@ __device__ __forceinline__ void add_weights(const AttendArgs &a, const Place &c,
             const float lse = lse_of(g);
 #pragma unroll
             for (int k = 0; k < kScorePer; ++k) {
-                const float e = i0 + k * threads < n ? exp2_fast(x[i0 + k * threads] - lse) : 0.f;
-                w[k] += lse == -INFINITY ? 0.f : e;
+                w[k] += i0 + k * threads < n ? weight_of(x[i0 + k * threads], lse) : 0.f;
             }
         }
         x -= rows * a.logit_stride;

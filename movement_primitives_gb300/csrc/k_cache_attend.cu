@@ -78,9 +78,8 @@ __device__ __forceinline__ void add_scores(const AttendArgs &a, uint32_t at, flo
             float y[kScorePer];
 #pragma unroll
             for (int k = 0; k < kScorePer; ++k) y[k] = i0 + t + k * threads < n - lo ? x[k * threads] : -INFINITY;
-            if (z != -INFINITY)
 #pragma unroll
-                for (int k = 0; k < kScorePer; ++k) w[k] += exp2_fast(y[k] - z);
+            for (int k = 0; k < kScorePer; ++k) w[k] += weight_of(y[k], z);
         }
     }
     float *to = a.scores + b * a.sst[0] + h * a.sst[1] + lo + i0 + t;

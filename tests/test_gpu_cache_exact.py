@@ -101,6 +101,32 @@ def test_an_infinite_value_in_a_seen_slot_stays_infinite(kind, lens, heads, dim)
     no_device_error()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "e4m3"])
+@pytest.mark.parametrize("lens,heads,group,dim", [([40, 25], 2, 4, 64),                        # a block or a warp a unit
+                                                  ([700, 90], 2, 4, 128),                      # a cluster a unit
+                                                  ([(5 * i) % 67 for i in range(211)], 3, 2, 64),  # a warp a unit
+                                                  ([4200, 35, 0, 2101], 12, 3, 64),            # runs
+                                                  ([150, 60], 2, 20, 64),                      # units that share scores
+                                                  ([90, 60], 2, 2, 33)])                       # rows by elements
+def test_a_nan_row_adds_nothing_to_slots_it_does_not_see(kind, lens, heads, group, dim):
+    """A query that is NaN makes its row and its seen slots' weights NaN, and no other slot's."""
+    s = Setup(lens, heads=heads, dim=dim, kind=kind, page=16, seed=dim)
+    q = s.queries(heads * group)
+    b = max(range(s.n_seq), key=lambda i: lens[i])
+    q[b, group, 1] = math.nan  # the first query head of key head 1
+    mask = (torch.rand((s.n_seq, s.cap), generator=s.g) < 0.5).cuda()
+    before = torch.rand((s.n_seq, heads, s.cap), generator=s.g).cuda()
+    scores = before.clone()
+    out = lc().cache_attend(s.cache, q, s.lengths, mask=mask, scores=scores)
+    seen = mask & (torch.arange(s.cap, device="cuda") < s.lengths[:, None])
+    assert torch.all(torch.isnan(out[b, group])) and int(torch.isnan(out).any(2).sum()) == 1
+    assert torch.equal(scores.isnan().any(2).nonzero(), torch.tensor([[b, 1]], device="cuda"))
+    assert torch.all(scores[b, 1].isnan() == seen[b])
+    unseen = ~seen[:, None].expand_as(scores)
+    assert torch.equal(scores[unseen], before[unseen])
+    no_device_error()
+
+
 ASCENDING = """
 import sys
 sys.path[:0] = [%r, %r]
