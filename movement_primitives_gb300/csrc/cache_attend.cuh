@@ -878,10 +878,11 @@ __device__ __forceinline__ void add_weights(const AttendArgs &a, const Place &c,
         }
         for (int g = 0; g < rows; ++g, x += a.logit_stride) {
             const float lse = lse_of(g);
+            float y[kScorePer];
 #pragma unroll
-            for (int k = 0; k < kScorePer; ++k) {
-                w[k] += i0 + k * threads < n ? weight_of(x[i0 + k * threads], lse) : 0.f;
-            }
+            for (int k = 0; k < kScorePer; ++k) y[k] = i0 + k * threads < n ? x[i0 + k * threads] : -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kScorePer; ++k) w[k] += weight_of(y[k], lse);
         }
         x -= rows * a.logit_stride;
 #pragma unroll
