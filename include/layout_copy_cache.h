@@ -72,10 +72,11 @@ typedef struct {
  *             rounded to nearest even; a row with an infinity or NaN gets the
  *             scale NaN
  *   *_stride  of sequence, token, head
- *   new_lengths  may be lengths' own buffer only where n_new is 0
+ *   new_lengths  shares no element with lengths or counts; where n_new is 0 it
+ *             may be either's own buffer
  * Errors: LC_ERR_NULL, LC_ERR_SHAPE, LC_ERR_TYPE, LC_ERR_BAD_STRIDE,
  * LC_ERR_ALIGN, LC_ERR_OVERFLOW, LC_ERR_NOT_INJECTIVE, LC_ERR_OVERLAP
- * (new_lengths is lengths). */
+ * (new_lengths meets lengths or counts). */
 int lc_cache_append(const lc_paged_cache *cache, const void *k_new, const void *v_new, int32_t type,
                     const int64_t k_stride[3], const int64_t v_stride[3], int32_t n_new, const int32_t *counts,
                     const int32_t *lengths, int32_t *new_lengths, lc_stream_t stream);
@@ -131,8 +132,9 @@ int lc_cache_attend(const lc_paged_cache *cache, const lc_cache_query *query, lc
  *   scores      [n_seqs, n_kv_heads, capacity], read only
  *   kept        [n_seqs, n_kv_heads, budget] receives the old slot of every
  *               kept one, -1 past them
- *   new_scores  like scores, another buffer: the kept slots' scores, then zeros
- *   new_lengths [n_seqs], another buffer than lengths: min(n, budget)
+ *   new_scores  like scores, sharing no element with them: the kept slots'
+ *               scores, then zeros
+ *   new_lengths [n_seqs], sharing no element with lengths: min(n, budget)
  *   workspace   at least lc_cache_evict_workspace(...) bytes, 256-byte
  *               aligned, as lc_cache_attend's; may be NULL where that is 0 */
 typedef struct {
@@ -157,7 +159,7 @@ int64_t lc_cache_evict_workspace(const lc_paged_cache *cache, int32_t budget);
 /* Errors: LC_ERR_NULL, LC_ERR_SHAPE (budget < 1, recent outside 0 .. budget,
  * sizes), LC_ERR_TYPE, LC_ERR_BAD_STRIDE, LC_ERR_ALIGN, LC_ERR_OVERFLOW,
  * LC_ERR_NOT_INJECTIVE, LC_ERR_WORKSPACE, LC_ERR_OVERLAP (new_scores or
- * new_lengths is the old buffer).  The move's waits for one another's reads
+ * new_lengths meets the old ones).  The move's waits for one another's reads
  * are bounded (LC_ERR_TIMEOUT in the error word; rows are then left unmoved). */
 int lc_cache_evict(const lc_paged_cache *cache, const lc_cache_eviction *eviction, lc_stream_t stream);
 

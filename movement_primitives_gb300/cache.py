@@ -163,8 +163,8 @@ def cache_append(cache: PagedCache, k, v, lengths, counts=None, new_lengths=None
     bfloat16 / float16 for a float8_e4m3fn cache (each row is quantised with a
     scale of its own).  ``lengths``: int32 [seqs].  ``counts``: int32 [seqs],
     how many of the tokens are a sequence's (default: all).  ``new_lengths``:
-    an int32 [seqs] tensor to receive lengths + counts, other than
-    ``lengths``.  Tokens past a sequence's capacity are dropped and set the device
+    an int32 [seqs] tensor to receive lengths + counts, apart from ``lengths``
+    and ``counts``.  Tokens past a sequence's capacity are dropped and set the device
     error word (``last_device_error``).
     """
     shape = k.shape
@@ -284,8 +284,8 @@ def cache_evict(cache: PagedCache, lengths, scores, budget: int, recent: int = 0
     the lowest slots).  Their rows move to the front of the sequence's pages
     in their order.  ``kept``: int32 [seqs, kv_heads, budget], the old slot of
     each kept one, then -1.  ``new_scores``: the kept slots' scores, then
-    zeros, in a tensor other than ``scores``; ``new_lengths``: min(lengths,
-    budget), in a tensor other than ``lengths``.  The pages a sequence's table
+    zeros, apart from ``scores``; ``new_lengths``: min(lengths, budget), apart
+    from ``lengths``.  The pages a sequence's table
     names must be its own.
     """
     n_seqs, heads, device = cache.n_seqs, cache.n_kv_heads, cache.device

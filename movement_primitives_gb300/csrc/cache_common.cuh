@@ -112,6 +112,39 @@ inline bool rows_apart(int n, const int64_t *e, const int64_t *st, int64_t run) 
     return true;
 }
 
+// Whether `n` 4-byte elements at p and at q share any.
+inline bool lists_meet(const void *p, const void *q, int64_t n) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return (a < b ? b - a : a - b) < static_cast<uint64_t>(n) * 4;
+}
+
+// Whether rows of `run` 4-byte elements at p (strides st) share any with those
+// at q (strides qst, rows apart), both of extents `e`.  Buffers whose ranges
+// meet may still be apart, as two interleaved halves of one are.
+inline bool rows_meet(const void *p, const int64_t *st, const void *q, const int64_t *qst, const int64_t *e,
+                      int64_t run) {
+    auto span = [&](const int64_t *s) { return (e[0] - 1) * s[0] + (e[1] - 1) * s[1] + run; };
+    const int64_t d = (static_cast<int64_t>(reinterpret_cast<uintptr_t>(p)) -
+                       static_cast<int64_t>(reinterpret_cast<uintptr_t>(q))) / 4;
+    if (d >= span(qst) || -d >= span(st)) return false;
+    // q's rows from their larger step to the smaller one; a step of one row is none
+    const int big = e[0] <= 1 ? 1 : e[1] <= 1 ? 0 : qst[0] < qst[1], small = 1 - big;
+    // the steps i of `x` that rows at `at` could meet: two at most, since a row is no longer than a step
+    auto meets = [&](int x, int64_t at, auto &&with) {
+        if (e[x] <= 1) return with(at);
+        const int64_t i0 = at >= 0 ? std::min(at / qst[x], e[x] - 1) : 0;
+        const int64_t i1 = at + run > 0 ? std::min((at + run - 1) / qst[x], e[x] - 1) : 0;
+        return with(at - i0 * qst[x]) || (i1 != i0 && with(at - i1 * qst[x]));
+    };
+    for (int64_t i = 0; i < e[0]; ++i)
+        for (int64_t j = 0; j < e[1]; ++j)
+            if (meets(big, d + i * st[0] + j * st[1], [&](int64_t at) {
+                    return meets(small, at, [&](int64_t off) { return (off < 0 ? -off : off) < run; });
+                }))
+                return true;
+    return false;
+}
+
 // Checks a cache descriptor and lays it out for the kernels.  `write`: the
 // operator writes rows, which then have to be apart.
 inline int check_cache(const lc_paged_cache *c, bool write, CacheArgs *a) {

@@ -263,7 +263,9 @@ extern "C" int lc_cache_append(const lc_paged_cache *cache, const void *k_new, c
     if (!q8 && type != cache->type) return LC_ERR_TYPE;
     if (cache->n_seqs == 0) return LC_OK;
     if (!lengths || !new_lengths || !k_stride || !v_stride || (n_new > 0 && (!k_new || !v_new))) return LC_ERR_NULL;
-    if (lengths == new_lengths && n_new > 0) return LC_ERR_OVERLAP;
+    // blocks read lengths and counts when others have written (no tokens: one thread a sequence does both)
+    for (const int32_t *in : {lengths, counts})
+        if (in && lists_meet(in, new_lengths, cache->n_seqs) && (n_new > 0 || in != new_lengths)) return LC_ERR_OVERLAP;
     if ((reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new)) % 2 ||
         (reinterpret_cast<uintptr_t>(counts) | reinterpret_cast<uintptr_t>(lengths) |
          reinterpret_cast<uintptr_t>(new_lengths)) % 4)

@@ -671,7 +671,7 @@ extern "C" int lc_cache_evict(const lc_paged_cache *cache, const lc_cache_evicti
     if (cache->n_seqs == 0) return LC_OK;
     if (!e->lengths || !e->kept || !e->new_lengths || (a.c.cap > 0 && (!e->scores || !e->new_scores)))
         return LC_ERR_NULL;
-    if (e->lengths == e->new_lengths || (a.c.cap > 0 && e->scores == e->new_scores)) return LC_ERR_OVERLAP;
+    if (lists_meet(e->lengths, e->new_lengths, cache->n_seqs)) return LC_ERR_OVERLAP;
     if ((reinterpret_cast<uintptr_t>(e->lengths) | reinterpret_cast<uintptr_t>(e->scores) |
          reinterpret_cast<uintptr_t>(e->kept) | reinterpret_cast<uintptr_t>(e->new_scores) |
          reinterpret_cast<uintptr_t>(e->new_lengths)) % 4)
@@ -684,6 +684,8 @@ extern "C" int lc_cache_evict(const lc_paged_cache *cache, const lc_cache_evicti
     if ((a.c.cap > 0 && !rows_apart(2, ext, e->new_scores_stride, a.c.cap)) ||
         !rows_apart(2, ext, e->kept_stride, e->budget))
         return LC_ERR_NOT_INJECTIVE;
+    if (a.c.cap > 0 && rows_meet(e->scores, e->scores_stride, e->new_scores, e->new_scores_stride, ext, a.c.cap))
+        return LC_ERR_OVERLAP;
     const int64_t units = ext[0] * ext[1], chunks = (int64_t(e->budget) + kMvRows - 1) / kMvRows;
     // the tickets that running blocks draw past the last one stay in 32 bits
     // too

@@ -16,7 +16,7 @@ from oracle import cache as oc
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from test_gpu_cache import IO, Setup, attend, check_attend, lc, no_device_error  # noqa: E402
+from test_gpu_cache import IO, Setup, attend, check_attend, check_evict, lc, no_device_error  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -144,3 +144,12 @@ def test_evict_head_sizes_one_after_the_other(kind):
     code = ASCENDING % (os.path.join(ROOT, "tests"), ROOT, kind)
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_evict_between_interleaved_halves_of_one_buffer():
+    """Scores and new scores whose ranges meet, but not their rows."""
+    for heads_first in (False, True):
+        s = Setup([100, 60], heads=3, dim=64, seed=2)
+        both = torch.rand((2, 2, 3, s.cap) if heads_first else (2, 3, 2, s.cap), generator=s.g).cuda()
+        old, new = (both[:, i] if heads_first else both[:, :, i] for i in range(2))
+        check_evict(s, old, 37, 6, new_scores=new)
