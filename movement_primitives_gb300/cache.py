@@ -23,14 +23,15 @@ _EVICTION = struct.Struct("@PPqqiiPqqPqqPPq")        # lc_cache_eviction
 _TYPES = None  # dtype -> lc_cache_type
 _BYTES = _BOOL = _I32 = _F32 = None
 _CURRENT = None  # raw handle of a device's current stream (torch.cuda.current_stream() builds an object, 3 us)
+_CUDA = None     # torch.cuda
 
 
 def _types():
-    global _TYPES, _BYTES, _BOOL, _I32, _F32, _CURRENT
+    global _TYPES, _BYTES, _BOOL, _I32, _F32, _CURRENT, _CUDA
     if _TYPES is None:
         import torch
         _BYTES, _BOOL, _I32, _F32 = torch.uint8, torch.bool, torch.int32, torch.float32
-        _CURRENT = torch._C._cuda_getCurrentRawStream
+        _CURRENT, _CUDA = torch._C._cuda_getCurrentRawStream, torch.cuda
         _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
     return _TYPES
 
@@ -50,6 +51,11 @@ def _allocator():
     if direct is not None:
         return direct
     return lambda shape, strides, dtype: torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
+
+
+def _elsewhere(cache):
+    raise ValueError("the cache is on %s, the current device is cuda:%d: outputs are made and kernels run there "
+                     "(torch.cuda.set_device, or a stream of the cache's device)" % (cache.device, _CUDA.current_device()))
 
 
 class _on:
@@ -93,7 +99,8 @@ class PagedCache:
     sequence's pages are never read.  ``k_scale``, ``v_scale``: float32 [pages,
     kv_heads, page_size] for float8_e4m3fn pools (value = code * scale).  The
     tensors are kept by reference: what they hold may change between calls,
-    their memory may not.
+    their memory may not.  The operators run on the current device, which has
+    to be theirs.
     """
 
     def __init__(self, k, v, page_table, k_scale=None, v_scale=None):
@@ -186,6 +193,8 @@ def cache_append(cache: PagedCache, k, v, lengths, counts=None, new_lengths=None
 
 
 def _append(cache, k, v, kind, n_new, counts, lengths, new_lengths, handle):
+    if _CUDA.current_device() != cache._index:
+        _elsewhere(cache)
     if new_lengths is None:
         new_lengths = cache._empty(cache._seqs, (1,), _I32)
     status = _lib.lib().lc_cache_append(
@@ -244,6 +253,8 @@ def cache_attend(cache: PagedCache, q, lengths, out=None, scale=None, window: in
 
 
 def _attend(cache, q, n_q, lengths, out, scale, window, mask, lse, scores, workspace, handle):
+    if _CUDA.current_device() != cache._index:
+        _elsewhere(cache)
     kind = _TYPES[q.dtype]
     if out is None:
         d = cache.head_dim
@@ -305,6 +316,8 @@ def cache_evict(cache: PagedCache, lengths, scores, budget: int, recent: int = 0
 
 
 def _evict(cache, lengths, scores, budget, recent, new_scores, kept, new_lengths, handle):
+    if _CUDA.current_device() != cache._index:
+        _elsewhere(cache)
     b, h, cap = cache.n_seqs, cache.n_kv_heads, cache.capacity
     if kept is None:
         n = max(budget, 0)

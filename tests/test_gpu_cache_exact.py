@@ -153,3 +153,30 @@ def test_evict_between_interleaved_halves_of_one_buffer():
         both = torch.rand((2, 2, 3, s.cap) if heads_first else (2, 3, 2, s.cap), generator=s.g).cuda()
         old, new = (both[:, i] if heads_first else both[:, :, i] for i in range(2))
         check_evict(s, old, 37, 6, new_scores=new)
+
+
+# ---------------------------------------------------------------------------
+# refusals
+# ---------------------------------------------------------------------------
+
+def calls(s):
+    """Every operator on this cache, by name."""
+    q = s.queries(2 * s.heads)
+    new = torch.zeros((s.n_seq, 1, s.heads, s.dim), dtype=IO[s.kind], device="cuda")
+    scores = torch.zeros((s.n_seq, s.heads, s.cap), device="cuda")
+    zero = torch.zeros_like(s.lengths)
+    return {"append": lambda **kw: lc().cache_append(s.cache, **{**dict(k=new, v=new, lengths=zero), **kw}),
+            "attend": lambda **kw: lc().cache_attend(s.cache, **{**dict(q=q, lengths=s.lengths), **kw}),
+            "evict": lambda **kw: lc().cache_evict(s.cache, **{**dict(lengths=s.lengths, scores=scores, budget=4), **kw})}
+
+
+def test_another_current_device_is_refused(monkeypatch):
+    """The library launches on the current device: a cache elsewhere is refused before anything is allocated."""
+    s = Setup([10, 20], heads=2, dim=64)
+    ops = calls(s)
+    for op in ops.values():
+        op()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: s.k.device.index + 1)
+    for name, op in ops.items():
+        with pytest.raises(ValueError, match="device"):
+            op()
