@@ -4,7 +4,8 @@ A cache is a pool of pages seen as [page, kv_head, slot, dim] through its
 strides (a [page, slot, kv_head, dim] pool is passed as its ``transpose(1,
 2)``) and a page table naming each sequence's pages.  Everything runs in the
 C-ABI library (``include/layout_copy_cache.h``); this module marshals
-arguments and allocates outputs and workspaces through torch.
+arguments and allocates outputs and workspaces through torch.  There is no
+backward pass: inputs that want a gradient are refused.
 """
 from __future__ import annotations
 
@@ -23,15 +24,17 @@ _EVICTION = struct.Struct("@PPqqiiPqqPqqPPq")        # lc_cache_eviction
 _TYPES = None  # dtype -> lc_cache_type
 _BYTES = _BOOL = _I32 = _F32 = None
 _CURRENT = None  # raw handle of a device's current stream (torch.cuda.current_stream() builds an object, 3 us)
-_CUDA = None     # torch.cuda
+_CUDA = _GRAD = None  # torch.cuda, torch.is_grad_enabled
 
 
 def _types():
-    global _TYPES, _BYTES, _BOOL, _I32, _F32, _CURRENT, _CUDA
+    global _TYPES, _BYTES, _BOOL, _I32, _F32, _CURRENT, _CUDA, _GRAD
     if _TYPES is None:
         import torch
         _BYTES, _BOOL, _I32, _F32 = torch.uint8, torch.bool, torch.int32, torch.float32
-        _CURRENT, _CUDA = torch._C._cuda_getCurrentRawStream, torch.cuda
+        _CURRENT = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _CUDA, _GRAD = torch.cuda, torch.is_grad_enabled
         _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
     return _TYPES
 
@@ -44,7 +47,9 @@ def _check(status: int, what: str) -> None:
 
 def _allocator():
     """``empty(shape, strides, dtype)`` on the current device and stream.  torch's direct binding where it has it:
-    torch.empty takes 3.5 us more a call, as long as one of the library's launches."""
+    torch.empty takes 3.5 us more a call, as long as one of the library's launches.  It comes from the same caching
+    allocator (streams, graphs and memory pools included) and passes by the dispatcher, whose modes see nothing of it
+    and fill nothing: every element of an output is written by the kernels."""
     import torch
     direct = getattr(getattr(torch._C._dynamo, "guards", None), "_empty_strided_cuda", None) \
         if hasattr(torch._C, "_dynamo") else None
@@ -74,6 +79,11 @@ class _on:
 
     def __exit__(self, *exc):
         self.ctx.__exit__(*exc)
+
+
+def _no_gradient():
+    if _GRAD():
+        raise ValueError("no operator of the cache has a gradient: detach its inputs or call it under torch.no_grad()")
 
 
 def _tensor(t, name: str, dtype, shape, device):
@@ -181,6 +191,8 @@ def cache_append(cache: PagedCache, k, v, lengths, counts=None, new_lengths=None
     device, seqs = cache.device, cache._seqs
     _tensor(k, "k", k.dtype, (cache.n_seqs, shape[1], cache.n_kv_heads, cache.head_dim), device)
     _tensor(v, "v", k.dtype, shape, device)
+    if k.requires_grad or v.requires_grad:
+        _no_gradient()
     _tensor(lengths, "lengths", _I32, seqs, device)
     if counts is not None:
         _tensor(counts, "counts", _I32, seqs, device)
@@ -233,6 +245,8 @@ def cache_attend(cache: PagedCache, q, lengths, out=None, scale=None, window: in
         raise ValueError("q is [seqs, q_heads, head_dim]")
     n_q, n_seqs, device = shape[1], cache.n_seqs, cache.device
     _tensor(q, "q", cache.io_dtype, (n_seqs, n_q, cache.head_dim), device)
+    if q.requires_grad:
+        _no_gradient()
     _tensor(lengths, "lengths", _I32, cache._seqs, device)
     if mask is not None:
         if mask.dtype is not _BOOL and mask.dtype is not _BYTES:

@@ -180,3 +180,35 @@ def test_another_current_device_is_refused(monkeypatch):
     for name, op in ops.items():
         with pytest.raises(ValueError, match="device"):
             op()
+
+
+def test_inputs_that_want_a_gradient_are_refused():
+    """No operator here has a backward pass: an output without a gradient would not say so."""
+    s = Setup([10, 20], heads=2, dim=64)
+    ops = calls(s)
+    q = s.queries(4).requires_grad_()
+    new = torch.zeros((2, 1, 2, 64), dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    for name, args in (("attend", dict(q=q)), ("append", dict(k=new)), ("append", dict(v=new))):
+        with pytest.raises(ValueError, match="gradient"):
+            ops[name](**args)
+        with torch.no_grad():
+            ops[name](**args)
+
+
+def test_streams_without_the_raw_binding(monkeypatch):
+    """Where torch has no raw stream handle, the stream object's is used."""
+    from movement_primitives_gb300 import cache as module
+    s = Setup([10, 20], heads=2, dim=64)
+    q = s.queries(4)
+    want = lc().cache_attend(s.cache, q, s.lengths)
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    for name in ("_TYPES", "_CURRENT"):
+        monkeypatch.setattr(module, name, None)
+    module._types()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = lc().cache_attend(s.cache, q, s.lengths)
+        assert module._CURRENT(s.cache._index) == side.cuda_stream
+    side.synchronize()
+    assert torch.equal(got, want)
