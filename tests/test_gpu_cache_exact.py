@@ -156,6 +156,91 @@ def test_evict_between_interleaved_halves_of_one_buffer():
 
 
 # ---------------------------------------------------------------------------
+# append: the forms that long prompts take
+# ---------------------------------------------------------------------------
+
+E4M3 = torch.tensor([oc.e4m3_value(c) if c & 127 != 127 else math.nan for c in range(256)], dtype=torch.float64)
+
+
+def quantised(x):
+    """(values as multiples of the scale, scale) of rows x [..., dim] in 16 bits: oracle.cache.quantise of many rows."""
+    x = x.double()
+    top = x.abs().amax(-1)
+    scale = torch.where(top.isfinite(), (top / 448).float().clamp(min=2.0 ** -126), math.nan).double()
+    y = (x / scale[..., None]).float().double()  # the float32 quotient: 53 bits are enough to round twice
+    e = torch.frexp(y.abs())[1].clamp(min=-5) - 1
+    step = (e.long() - 3 + 1023 << 52).view(torch.float64)  # 2^(e - 3)
+    return torch.copysign(((y.abs() / step).round() * step).clamp(max=448.0), y), scale
+
+
+@pytest.mark.parametrize("device", ["cpu", "cuda"])
+def test_the_vectorised_quantiser_is_the_oracle(device):
+    g = torch.Generator().manual_seed(0)
+    x = torch.randn((40, 24), generator=g) * torch.exp(4 * torch.randn((40, 1), generator=g))
+    x[3], x[4, 2], x[5, 7], x[6] = 0, math.inf, math.nan, x[6] * 1e-38
+    x = x.bfloat16()
+    values, scale = (y.cpu().numpy() for y in quantised(x.to(device)))
+    for row, v, sc in zip(x.float().numpy(), values, scale):
+        want, want_scale = oc.quantise(row)
+        assert np.array_equal(np.float32(sc), want_scale, equal_nan=True)
+        if not np.isnan(sc):
+            assert np.array_equal(v, want)
+
+
+FOUR = 4 * 152 * 48  # rows from which a warp takes several heads; from twice that of up to eight
+PROMPTS = [(1, 64, FOUR + 40), (2, 128, FOUR + 40), (3, 256, FOUR), (3, 72, FOUR + 9), (4, 64, 2 * FOUR),
+           (4, 128, 2 * FOUR + 8), (5, 72, 2 * FOUR + 35), (5, 64, 2 * FOUR + 5), (5, 128, FOUR - 5), (7, 136, FOUR + 49),
+           (7, 128, 2 * FOUR + 21), (8, 192, FOUR), (8, 64, 2 * FOUR), (8, 128, FOUR), (12, 256, 2 * FOUR),
+           (12, 72, 2 * FOUR + 48), (12, 64, FOUR + 24), (7, 8, FOUR + 49)]
+
+
+@pytest.mark.parametrize("kind,io,every", [("e4m3", "bf16", 1), ("e4m3", "fp16", 3), ("bf16", "bf16", 4), ("fp16", "fp16", 5)])
+def test_append_long_prompts(kind, io, every):
+    """Rows enough that a warp takes several heads: odd numbers of heads, lanes past a row's end, ragged counts,
+    rows that are not finite or whose magnitudes divide."""
+    for i, (heads, dim, rows) in enumerate(PROMPTS[::every]):
+        n_new = rows // heads // 2
+        s = Setup([3, 0], heads=heads, dim=dim, per=-(-(n_new + 3) // 64), page=64, kind=kind, seed=rows,
+                  order="token" if i % 2 else "head")
+        g = torch.Generator(device="cuda").manual_seed(rows)
+        new = [(3 * torch.randn((2, n_new, heads, dim), generator=g, device="cuda")).to(IO[io]) for _ in "kv"]
+        h = heads - 1
+        new[0][0, 1, h, dim - 1], new[1][0, 2, 0, 0], new[0][1, 3, h, 0] = math.inf, math.nan, -math.inf
+        new[0][0, 4, h] = 0
+        if io == "bf16":
+            for t, power in ((5, 100), (6, -91), (7, -126), (8, -133), (9, 126), (10, -90), (11, 90)):
+                new[t % 2][0, t, h] *= 2.0 ** power
+            new[1][1, 12, 0] = 2.0 ** -90  # the division's side of the bounds, and the other
+            new[1][1, 13, 0] = 2.0 ** 90
+        counts = torch.tensor([n_new, n_new - 37], dtype=torch.int32, device="cuda")
+        before = [x.clone() for x in (s.k.view(torch.uint8), s.v.view(torch.uint8))] if kind == "e4m3" else \
+                 [s.k.clone(), s.v.clone()]
+        old_scales = [None if x is None else x.clone() for x in s.scales]
+        got_n = lc().cache_append(s.cache, new[0], new[1], s.lengths, counts)
+        assert got_n.tolist() == [3 + n_new, n_new - 37]
+        t = torch.arange(n_new, device="cuda")
+        seq, tok = torch.nonzero(t[None] < counts[:, None], as_tuple=True)
+        at = s.lengths.long()[seq] + tok
+        page, row = s.table[seq, at // 64].long(), at % 64
+        for x, pool, old, scales, old_scale in zip(new, (s.k, s.v), before, s.scales, old_scales):
+            if kind != "e4m3":
+                old[page, :, row] = x[seq, tok]
+                assert torch.equal(pool.contiguous().view(torch.int16), old.contiguous().view(torch.int16)), (heads, dim, rows)
+                continue
+            values, scale = quantised(x[seq, tok])
+            codes = pool.view(torch.uint8)
+            got = E4M3.cuda()[codes[page, :, row].long()]
+            bad = scale.isnan()[..., None]
+            assert torch.equal(torch.where(bad, 0, got), torch.where(bad, 0, values)), (heads, dim, rows)
+            assert torch.equal(scales[page, :, row].nan_to_num(-1.0), scale.float().nan_to_num(-1.0))
+            # nothing else is written
+            old[page, :, row], old_scale[page, :, row] = codes[page, :, row], scales[page, :, row]
+            assert torch.equal(codes, old)
+            assert torch.equal(scales.nan_to_num(-1.0), old_scale.nan_to_num(-1.0))
+        no_device_error()
+
+
+# ---------------------------------------------------------------------------
 # refusals
 # ---------------------------------------------------------------------------
 
