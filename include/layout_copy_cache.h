@@ -160,7 +160,10 @@ int64_t lc_cache_evict_workspace(const lc_paged_cache *cache, int32_t budget);
  * sizes), LC_ERR_TYPE, LC_ERR_BAD_STRIDE, LC_ERR_ALIGN, LC_ERR_OVERFLOW,
  * LC_ERR_NOT_INJECTIVE, LC_ERR_WORKSPACE, LC_ERR_OVERLAP (new_scores or
  * new_lengths meets the old ones).  The move's waits for one another's reads
- * are bounded (LC_ERR_TIMEOUT in the error word; rows are then left unmoved). */
+ * are bounded (LC_WAIT_TIMEOUT_NS).  One that runs out sets LC_ERR_TIMEOUT in
+ * the error word and leaves the 32 slots that it was for as they were, in every
+ * pool; all others hold their kept rows, and kept, new_scores and new_lengths
+ * are written as ever.  That key head's rows are then to be given up. */
 int lc_cache_evict(const lc_paged_cache *cache, const lc_cache_eviction *eviction, lc_stream_t stream);
 
 #ifdef __cplusplus

@@ -297,3 +297,57 @@ def test_streams_without_the_raw_binding(monkeypatch):
         assert module._CURRENT(s.cache._index) == side.cuda_stream
     side.synchronize()
     assert torch.equal(got, want)
+
+
+LATE = """
+import os, sys
+os.environ["LC_WAIT_TIMEOUT_NS"] = "1"
+sys.path[:0] = [%r, %r]
+import torch
+from test_gpu_cache import Setup, lc, no_device_error
+n, cut, heads, dim = 20000, 40, 8, 64
+s = Setup([n] * 3, heads=heads, dim=dim, kind=%r, page=64, seed=1)
+other = Setup([700, 90], heads=2, dim=64, seed=2)
+q = other.queries(4)
+want = lc().cache_attend(other.cache, q, other.lengths)
+no_device_error()
+scores = torch.rand((3, heads, s.cap), generator=s.g).cuda()
+
+def rows(p):  # [sequence, head, slot, bytes]
+    p = p[s.table.long()].transpose(1, 2).flatten(2, 3).contiguous()
+    return (p[..., None] if p.dim() == 3 else p).view(torch.uint8)
+
+pools = [s.k, s.v] + [x for x in s.scales if x is not None]
+before = [rows(p) for p in pools]
+kept, new_scores, lengths = lc().cache_evict(s.cache, s.lengths, scores, n - cut)
+status, _ = lc().last_device_error()
+assert status == lc().STATUS["LC_ERR_TIMEOUT"], status
+assert lengths.tolist() == [n - cut] * 3
+chosen = scores[:, :, :n].topk(n - cut).indices.sort(-1).values
+assert torch.equal(kept.long(), chosen)
+assert torch.equal(new_scores[:, :, :n - cut], scores.gather(2, chosen))
+moved = stayed = None
+for pool, old in zip(pools, before):
+    now = rows(pool)
+    to = old.gather(2, kept.long()[..., None].expand(-1, -1, -1, old.shape[3]))
+    by32 = lambda x: x.flatten(2)[:, :, :(n - cut) // 32 * 32 * old.shape[3]].unflatten(2, (-1, 32 * old.shape[3])).all(3)
+    m, t = by32(now[:, :, :n - cut] == to), by32(now[:, :, :n - cut] == old[:, :, :n - cut])
+    assert torch.equal(now[:, :, n - cut:], old[:, :, n - cut:])
+    moved, stayed = (m, t) if moved is None else (moved & m, stayed & t)
+assert torch.all(moved | stayed)  # thirty-two slots as one, in every pool
+assert not torch.all(moved) and torch.any(moved & ~stayed)
+no_device_error()  # reading it cleared it
+assert torch.equal(lc().cache_attend(other.cache, q, other.lengths), want)
+lc().cache_evict(other.cache, other.lengths, torch.zeros((2, 2, other.cap), device="cuda"), 700)
+no_device_error()
+"""
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_evict_waits_that_run_out(kind):
+    """A limit of a nanosecond, in a process of its own: an ordinary eviction gives up where a lower chunk has not been
+    read yet (thousands of the 15 thousand chunks do here).  The error word says so, the slots of a chunk that gave up
+    are as they were, and what comes after runs as ever."""
+    code = LATE % (os.path.join(ROOT, "tests"), ROOT, kind)
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
