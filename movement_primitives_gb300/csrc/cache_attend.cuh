@@ -25,6 +25,8 @@
 // is zero, so that an infinite value stays one.  The sum l takes the weights whole.  Float16 has few exponents, so its weights are
 // lifted by 2^14: the largest is 2^14, and one of 2^-38 of it is still held to a
 // bit, so that a million slots together lose nothing to an outlier above them.
+// Others are lowered by 2^-31, so that sums of as many slots as there can be stay
+// in float32 whatever the values are; what is lost is below 2^-95 of the largest.
 //
 // E4M3 codes are float16 numbers, converted exactly two at a time; their
 // products run in float16.  The keys' scales multiply the logits.  The values'
@@ -263,6 +265,15 @@ __device__ __forceinline__ float log2_fast(float x) {  // -infinity for 0
     return y;
 }
 
+// log2 of the largest weight of a row's sum l (see above), and the logarithm,
+// base 2, of the whole sum from l and the maximum that it is relative to: the
+// factor is taken out first, whose digits would cost the logarithm some of its.
+constexpr __host__ __device__ float sum_lift(bool f16) { return f16 ? 14.f : -31.f; }
+template <bool F16>
+__device__ __forceinline__ float log_sum(float m, float l) {
+    return l == 0.f ? -INFINITY : m + sum_lift(F16) + log2f(l * (F16 ? 0x1p-14f : 0x1p31f));
+}
+
 // The slots [lo, n) that sequence b's query sees (before the mask).
 __device__ __forceinline__ int seen_from(const AttendArgs &a, int b, int *n) {
     *n = cache_length(a.c, a.lengths, b, kClassAttend);
@@ -299,7 +310,8 @@ struct Attend {
     using S = AtShape<DP, KV, NG, STAGES>;
     static constexpr bool F16 = KV == LC_CACHE_F16, Q8 = KV == LC_CACHE_E4M3;
     static constexpr bool M16 = F16 || Q8;       // the matrix instructions' type is float16
-    static constexpr float kLift = M16 ? 14.f : 0.f;  // log2 of the largest weight of the second product
+    // log2 of the largest weight: of the second product, and of the sum l
+    static constexpr float kLift = sum_lift(M16), kSumLift = sum_lift(F16);
     static constexpr int KS = DP / 16;           // 16-wide pieces of a row
     static constexpr int MT = S::TOK / 16;       // 16-slot pieces of a step
 
@@ -313,9 +325,10 @@ struct Attend {
     int b, rows, q0;
 
     uint32_t qb[KS][NG][2];
-    float o[KS][NG][4], m[NG][2], l[NG][2];
+    float o[KS][NG][4], l[NG][2];
+    float m[NG][2];        // the running maximum of the logits less kSumLift, which l and o are relative to
     float q_scale[NG][2];  // E4M3: what the float16 queries are to be multiplied by, times scale2
-    float mv[NG][2];       // E4M3: the running maximum of logit + log2 |value scale|, which o is relative to
+    float mv[NG][2];       // E4M3: that of logit + log2 |value scale|, less kLift, which o is relative to
 
     // the pages of a step's slots, one a lane, read one step ahead of its rows
     int next_page, next_row, next_head;
@@ -579,7 +592,7 @@ struct Attend {
                 float top = fmaxf(x[0][g][u], x[0][g][2 + u]);
 #pragma unroll
                 for (int t = 1; t < MT; ++t) top = fmaxf(top, fmaxf(x[t][g][u], x[t][g][2 + u]));
-                top = warp_max(top);
+                top = warp_max(top) - kSumLift;
                 keep[g][u] = 1.f;
                 if (top > m[g][u]) {
                     const float k = exp2_fast(m[g][u] - top);
@@ -590,7 +603,7 @@ struct Attend {
                         grown = true;
                     }
                 }
-                const float safe = m[g][u] == -INFINITY ? 0.f : m[g][u] - (Q8 ? 0.f : kLift);
+                const float safe = m[g][u] == -INFINITY ? 0.f : m[g][u];
                 float sum = 0.f;
                 if constexpr (Q8) {
                     float topv = -INFINITY;
@@ -602,13 +615,13 @@ struct Attend {
                             x[t][g][2 * i + u] += lv[t][i];
                             topv = fmaxf(topv, x[t][g][2 * i + u]);
                         }
-                    topv = warp_max(topv);
+                    topv = warp_max(topv) - kLift;
                     if (topv > mv[g][u]) {
                         keep[g][u] = exp2_fast(mv[g][u] - topv);
                         mv[g][u] = topv;
                         grown = true;
                     }
-                    const float safe_v = mv[g][u] == -INFINITY ? 0.f : mv[g][u] - kLift;
+                    const float safe_v = mv[g][u] == -INFINITY ? 0.f : mv[g][u];
 #pragma unroll
                     for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -689,9 +702,8 @@ struct Attend {
             for (int u = 0; u < 2; ++u) {
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) l[g][u] += __shfl_xor_sync(0xffffffffu, l[g][u], d);
-                if constexpr (F16) m[g][u] -= kLift;  // what l and o are relative to
                 if constexpr (Q8) {
-                    const float f = mv[g][u] == -INFINITY ? 0.f : exp2f(mv[g][u] - kLift - m[g][u]);
+                    const float f = mv[g][u] == -INFINITY ? 0.f : exp2f(mv[g][u] - m[g][u]);
 #pragma unroll
                     for (int c = 0; c < KS; ++c) {
                         o[c][g][u] *= f;
@@ -736,7 +748,7 @@ struct Attend {
     }
 
     __device__ __forceinline__ float write_lse(int hq, float top, float sum) const {
-        const float lse = sum == 0.f ? -INFINITY : top + log2f(sum);
+        const float lse = log_sum<F16>(top, sum);
         if (a.lse) a.lse[b * a.lse_stride + hq] = lse * kLn2;
         if (a.logits) a.lse2[int64_t(b) * a.q_heads + hq] = lse;
         return lse;
@@ -953,7 +965,7 @@ __global__ void __launch_bounds__(kAtThreads) k_attend_unit(const __grid_constan
         for (int g = 0; g < NG; ++g)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const float sum = u.l[g][i], lse = sum == 0.f ? -INFINITY : u.m[g][i] + log2f(sum);
+                const float lse = log_sum<A::F16>(u.m[g][i], u.l[g][i]);
                 if (lane < 4) ml[warp][8 * g + 2 * lane + i].x = lse;
             }
         __syncwarp();
@@ -1042,7 +1054,7 @@ __global__ void __launch_bounds__(kAtThreads) k_attend_unit(const __grid_constan
                 const float2 v = cluster.map_shared_rank(block_ml, r)[t];
                 sum += v.y * exp2_fast(v.x - (top == -INFINITY ? 0.f : top));
             }
-            lse_of[t] = sum == 0.f ? -INFINITY : top + log2f(sum);
+            lse_of[t] = log_sum<A::F16>(top, sum);
         }
         __syncthreads();
         add_weights(a, c, h, u.q0, u.rows, part * kAtThreads + t, parts * kAtThreads,

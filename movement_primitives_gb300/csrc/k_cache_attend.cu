@@ -43,6 +43,7 @@ __device__ __forceinline__ float2 join_ml(const AttendArgs &a, const Parts &p, i
 
 // scores[b, h, j] += sum over the group's query heads of 2^(logit - lse), for
 // one chunk of slots.
+template <bool F16>
 __device__ __forceinline__ void add_scores(const AttendArgs &a, uint32_t at, float *lse) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, threads = blockDim.x;
     const int units = a.c.heads * a.row_blocks;
@@ -66,7 +67,7 @@ __device__ __forceinline__ void add_scores(const AttendArgs &a, uint32_t at, flo
                 z = a.lse2[int64_t(b) * a.q_heads + h * a.group + g0 + g];
             } else {
                 const float2 v = join_ml(a, Parts{split.x, split.y - split.x + 1}, g0 + g - rb * kAtRows);
-                z = v.y == 0.f ? -INFINITY : v.x + log2f(v.y);
+                z = log_sum<F16>(v.x, v.y);
             }
             if (lane == 0) lse[g] = z;
         }
@@ -101,7 +102,7 @@ __global__ void __launch_bounds__(kJoinMost) k_attend_join(const __grid_constant
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, threads = blockDim.x;
     start_after_prior();
     if (blockIdx.x < a.score_blocks) {
-        add_scores(a, blockIdx.x, acc);
+        add_scores<F16>(a, blockIdx.x, acc);
         return;
     }
     const int units = a.c.heads * a.row_blocks, quads = a.part_pitch / 4;
@@ -139,7 +140,7 @@ __global__ void __launch_bounds__(kJoinMost) k_attend_join(const __grid_constant
         if (col < a.c.dim) a.out[r.b * a.ost[0] + r.hq * a.ost[1] + col] = static_cast<uint16_t>(pack2<F16>(x, 0.f));
     };
     auto put_lse = [&](const Row &r, float2 v) {
-        if (a.lse) a.lse[r.b * a.lse_stride + r.hq] = v.y == 0.f ? -INFINITY : (v.x + log2f(v.y)) * kLn2;
+        if (a.lse) a.lse[r.b * a.lse_stride + r.hq] = log_sum<F16>(v.x, v.y) * kLn2;
     };
     if (warp < a.join_rows) {
         const Row r = row_of(warp);

@@ -84,6 +84,45 @@ def test_attend_is_as_near_as_its_output_type_allows(kind, dim, group):
         check_close(s, q, lc().cache_attend(s.cache, q, s.lengths))
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "e4m3"])
+def test_log_sums_keep_their_digits(kind):
+    """One slot's log sum is its logit, that of n equal ones log n more: within a few of float32's steps there."""
+    for n in (1, 2, 33, 700, 20000):
+        s = Setup([n], heads=1, dim=64, kind=kind, page=64, seed=n)
+        q = s.queries(2)
+        k = s.k.view(torch.uint8) if kind == "e4m3" else s.k
+        k.copy_(k[int(s.table[0, 0]), 0, 0].clone().expand_as(k))
+        if kind == "e4m3":
+            s.scales[0].fill_(0.01)
+        lse = torch.empty((1, 2), device="cuda")
+        lc().cache_attend(s.cache, q, s.lengths, lse=lse)
+        _, want, _, _, reach = oc.attend(q.double().cpu().numpy(), *s.values(), s.table.cpu().numpy(), [n], 0.125)
+        # the logit's sum of 64 products, twice (as it is and base 2), the sum of n weights, three roundings of the result
+        bound = 2.0 ** -24 * (72 * reach + 2 * (n / 128 + 8) + 3 * np.abs(want) + 3 * math.log(n + 1))
+        if kind == "e4m3":
+            bound = bound + 2.0 ** -25 * 0.125 * np.abs(q.double().cpu().numpy()).max(2) * 448 * 64 * 0.01
+        assert np.all(np.abs(lse.double().cpu().numpy() - want) <= bound), (n, lse.tolist(), want, bound)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "e4m3"])
+@pytest.mark.parametrize("lens,heads,dim", [([1, 2, 30], 2, 64), ([700, 90], 2, 128), ([(5 * i) % 67 for i in range(211)], 3, 64),
+                                            ([4200, 35, 1], 12, 64), ([20, 90], 2, 33)])
+def test_values_near_the_largest_number(kind, lens, heads, dim):
+    """The average of many of the type's largest values is no larger than they are, their sum past float32."""
+    s = Setup(lens, heads=heads, dim=dim, kind=kind, page=16, seed=dim)
+    sign = torch.where(torch.arange(dim, device="cuda") % 3 == 0, -1.0, 1.0)
+    if kind == "e4m3":
+        s.v.view(torch.uint8).copy_((448 * sign).to(torch.float8_e4m3fn).view(torch.uint8).expand_as(s.v))
+        s.scales[1].fill_(2.0 ** 119)  # 448 * 2^119 = 0.875 * 2^128
+    else:
+        s.v.copy_((torch.finfo(IO[kind]).max * sign).to(IO[kind]).expand_as(s.v))
+    q = s.queries(2 * heads)
+    out = lc().cache_attend(s.cache, q, s.lengths)
+    assert torch.all(out.isfinite())
+    check_close(s, q, out)
+    no_device_error()
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp16"])
 @pytest.mark.parametrize("lens,heads,dim", [([1, 2, 30], 2, 64), ([700, 1], 2, 128), ([4200, 35, 1], 12, 64), ([20, 1], 2, 33)])
 def test_an_infinite_value_in_a_seen_slot_stays_infinite(kind, lens, heads, dim):
