@@ -24,17 +24,19 @@ _EVICTION = struct.Struct("@PPqqiiPqqPqqPPq")        # lc_cache_eviction
 _TYPES = None  # dtype -> lc_cache_type
 _BYTES = _BOOL = _I32 = _F32 = None
 _CURRENT = None  # raw handle of a device's current stream (torch.cuda.current_stream() builds an object, 3 us)
-_CUDA = _GRAD = None  # torch.cuda, torch.is_grad_enabled
+_DEVICE = None   # the current device's index (torch.cuda.current_device() takes twice as long)
+_GRAD = None     # whether gradients are recorded
 
 
 def _types():
-    global _TYPES, _BYTES, _BOOL, _I32, _F32, _CURRENT, _CUDA, _GRAD
+    global _TYPES, _BYTES, _BOOL, _I32, _F32, _CURRENT, _DEVICE, _GRAD
     if _TYPES is None:
         import torch
         _BYTES, _BOOL, _I32, _F32 = torch.uint8, torch.bool, torch.int32, torch.float32
         _CURRENT = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
             (lambda index: torch.cuda.current_stream(index).cuda_stream)
-        _CUDA, _GRAD = torch.cuda, torch.is_grad_enabled
+        _DEVICE = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        _GRAD = torch.is_grad_enabled
         _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
     return _TYPES
 
@@ -60,7 +62,7 @@ def _allocator():
 
 def _elsewhere(cache):
     raise ValueError("the cache is on %s, the current device is cuda:%d: outputs are made and kernels run there "
-                     "(torch.cuda.set_device, or a stream of the cache's device)" % (cache.device, _CUDA.current_device()))
+                     "(torch.cuda.set_device, or a stream of the cache's device)" % (cache.device, _DEVICE()))
 
 
 class _on:
@@ -205,7 +207,7 @@ def cache_append(cache: PagedCache, k, v, lengths, counts=None, new_lengths=None
 
 
 def _append(cache, k, v, kind, n_new, counts, lengths, new_lengths, handle):
-    if _CUDA.current_device() != cache._index:
+    if _DEVICE() != cache._index:
         _elsewhere(cache)
     if new_lengths is None:
         new_lengths = cache._empty(cache._seqs, (1,), _I32)
@@ -267,7 +269,7 @@ def cache_attend(cache: PagedCache, q, lengths, out=None, scale=None, window: in
 
 
 def _attend(cache, q, n_q, lengths, out, scale, window, mask, lse, scores, workspace, handle):
-    if _CUDA.current_device() != cache._index:
+    if _DEVICE() != cache._index:
         _elsewhere(cache)
     kind = _TYPES[q.dtype]
     if out is None:
@@ -330,7 +332,7 @@ def cache_evict(cache: PagedCache, lengths, scores, budget: int, recent: int = 0
 
 
 def _evict(cache, lengths, scores, budget, recent, new_scores, kept, new_lengths, handle):
-    if _CUDA.current_device() != cache._index:
+    if _DEVICE() != cache._index:
         _elsewhere(cache)
     b, h, cap = cache.n_seqs, cache.n_kv_heads, cache.capacity
     if kept is None:

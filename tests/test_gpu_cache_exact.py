@@ -300,7 +300,8 @@ def test_another_current_device_is_refused(monkeypatch):
     ops = calls(s)
     for op in ops.values():
         op()
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: s.k.device.index + 1)
+    from movement_primitives_gb300 import cache as module
+    monkeypatch.setattr(module, "_DEVICE", lambda: s.k.device.index + 1)
     for name, op in ops.items():
         with pytest.raises(ValueError, match="device"):
             op()
