@@ -75,9 +75,9 @@ constexpr int kAtWarps = 4;
 constexpr int kAtThreads = 32 * kAtWarps;
 // Blocks of an SM (at least; registers) and steps in a warp's ring.  Measured
 // on 1.09 GB of bfloat16 (64 sequences of up to 8192 slots, dim 128) and on
-// 0.27 GB of dim 64: 2 blocks x 2 steps 168 and 51 us; x 3 steps 178 and 51; 3
-// blocks x 2 steps 174 and 62.  More streams do not hide more latency, they
-// cost the memory its order.
+// 0.27 GB of dim 64: 2 blocks x 2 steps 167 and 51 us; x 3 steps 176 and 52; 3
+// blocks x 2 steps 208 (fewer registers) and 62.  More streams do not hide more
+// latency, they cost the memory its order.
 constexpr int kAtBlocks = 2, kAtStages = 2;
 constexpr int kAtRows = 16;        // query heads of a unit at most
 constexpr int kAtMaxBlocks = 608;  // of the main kernel; sizes the workspace
@@ -91,24 +91,24 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // A run takes at least this many steps: shorter ones leave more parts to join
 // than the further warps save, longer ones leave warps idle.  Of 1, 2, 4, 6, 8
-// steps: one sequence of 32000 slots, 16 query heads on one key head 40, 36,
-// 25, 24, 24 us; of 8000 slots, 8 key heads 15.1, 15.1, 14.7, 16.9, 18.4.
+// steps: one sequence of 32000 slots, 16 query heads on one key head 36, 32,
+// 23, 24, 24 us; of 8000 slots, 8 key heads 14.9, 14.8, 14.9, 17.2, 18.8.
 constexpr int kAtMinSteps = 4;
 // A unit is one block's, or a cluster's of up to kUnitCluster blocks while
 // there are kUnitBlocks at most, where a warp then takes kUnitSteps steps or
 // fewer: one launch and no parts in memory, but units of unlike lengths are
-// not evened out.  GPU time against runs: 8 units of 64 steps of 16 KiB 13.5
-// and 19.9 us; 96 units of up to 50 steps of 5 KiB 12.1 and 12.1 (the host
-// saves 5 us of a launch); at 16 steps a warp, 84 units of up to 125 steps
-// 24.5 and 14.9, 128 units of up to 128 steps of 8 KiB 25.9 and 21.5.
+// not evened out.  GPU time against runs: 8 units of 64 steps of 16 KiB, weights
+// collected, 15.2 and 23.1 us; 96 units of up to 50 steps of 5 KiB 11.4 and 13.2
+// (the host saves 5 us of a launch too); at 16 steps a warp, 84 units of up to 125
+// steps 21.8 and 14.1, 128 units of up to 128 steps of 8 KiB 27.4 and 21.7.
 constexpr int kUnitSteps = 8, kUnitBlocks = 304, kUnitCluster = 8;
 // Where a unit would be one block's, it is one warp's instead if that is
 // sooner, counting kUnitCost steps for what a unit costs besides its own: the
 // blocks' rounds of kUnitBlocks units against the warps' of four times as many.
-// A warp against a block: 1000 sequences of up to 64 slots of 8 key heads 42
-// and 96 us, 600 of up to 500 (E4M3) 79 and 110, 100 of 200 14.0 and 15.1, but 40
-// of up to 250 19.2 and 9.4; at the boundary 100 of 200 (bfloat16) 18.6 and 17.6,
-// 76 of up to 100 10.0 and 10.0.
+// A warp against a block: 1000 sequences of up to 64 slots of 8 key heads 43
+// and 97 us, 600 of up to 500 (E4M3) 79 and 110, 100 of 200 (E4M3) 13.9 and 15.2,
+// but 40 of up to 250 19.9 and 9.5; at the boundary 100 of 200 (bfloat16) 19.4 and
+// 18.0, 76 of up to 100 10.4 and 10.0.
 constexpr int kUnitCost = 2;
 // The largest shape's registers hold no second form of the end.
 constexpr __host__ __device__ bool unit_by_warp(int padded, int rows) { return padded < 256 || rows <= 8; }
@@ -142,8 +142,9 @@ struct AttendArgs {
 };
 
 // Slots of a step: of 8 KiB where the shapes allow, but 32 of E4M3 rows of 192
-// (12 KiB; 16 of them 89 us for 32 sequences of up to 8000 slots of 8 key heads,
-// 32 of them 77; of bfloat16 rows of 96, the same 192 bytes, 65 and 66).
+// (12 KiB; for 32 sequences of up to 8000 slots of 8 key heads in [head, slot]
+// order 16 of them take 90 us and 32 of them 77, in [slot, head] order 93 either
+// way; of bfloat16 rows of 96, the same 192 bytes, 65 and 66).
 constexpr int step_slots(int padded, int elem_bytes) {
     return padded * elem_bytes <= (elem_bytes == 1 ? 192 : 128) ? 32 : 16;
 }
@@ -155,8 +156,8 @@ constexpr int kUnitStages = DP * (KV == LC_CACHE_E4M3 ? 1 : 2) > 256 || DP == 19
 
 // head_dim as the kernels take it.  Columns past head_dim cost products and
 // registers, not bytes: 2 sequences of up to 99459 float16 slots, 16 query heads
-// a key head of 192, padded to 256 273 us, to 192 155; 7 sequences of up to 1999,
-// 12 heads of 80, to 128 15.0, to 96 14.0.  Rows that are read element by element
+// a key head of 192, padded to 256 299 us, to 192 157; 7 sequences of up to 1999,
+// 12 heads of 80, to 128 15.4, to 96 14.1.  Rows that are read element by element
 // are slower than either and have fewer forms.
 inline int padded_dim(int dim, bool vec) {
     if (vec && dim > 64 && dim <= 96) return 96;
