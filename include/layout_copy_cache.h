@@ -95,7 +95,19 @@ int lc_cache_append(const lc_paged_cache *cache, const void *k_new, const void *
  *              summed over the query heads of its key head, is added to it
  *   workspace  at least lc_cache_attend_workspace(...) bytes, 256-byte aligned;
  *              calls that may overlap need one each.  Nothing is kept in it
- *              between calls. */
+ *              between calls.
+ *
+ * Logits, maxima and sums are float32, and the output is rounded once.  The
+ * weights of a bfloat16 or float16 cache are multiplied with its values as sums
+ * of two numbers of that type (within 2^-16 or 2^-22 of the weight); those of an
+ * E4M3 cache as one float16 number (2^-11), and its queries as float16, scaled by
+ * a power of two a head (elements below 2^-14 of the largest are off by up to
+ * 2^-25 of it).  Exponentials and logarithms are the hardware's approximate ones.
+ *
+ * Workspace and kernels are chosen by the capacity, pages_per_seq * page_size,
+ * not by the lengths: with scores the workspace takes 4 bytes a query head and
+ * slot of it.  A descriptor of the table's first columns (and a mask and scores
+ * of as many slots) serves sequences that are known to be shorter. */
 typedef struct {
     const void *q;
     void *out;

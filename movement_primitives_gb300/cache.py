@@ -112,7 +112,10 @@ class PagedCache:
     kv_heads, page_size] for float8_e4m3fn pools (value = code * scale).  The
     tensors are kept by reference: what they hold may change between calls,
     their memory may not.  The operators run on the current device, which has
-    to be theirs.
+    to be theirs.  Kernels and workspaces are chosen by ``capacity``, the slots
+    that the table has columns for: where sequences are known to be far shorter, a
+    cache over ``page_table[:, :columns]`` (masks and scores of as many slots) is
+    faster and takes less memory.
     """
 
     def __init__(self, k, v, page_table, k_scale=None, v_scale=None):
@@ -240,7 +243,9 @@ def cache_attend(cache: PagedCache, q, lengths, out=None, scale=None, window: in
     bool or uint8 [seqs, capacity], slots of a zero are not seen.  ``lse``:
     float32 [seqs, q_heads] to receive log sum exp.  ``scores``: float32
     [seqs, kv_heads, capacity]; each slot's weight, summed over its query heads, is
-    added to it.  A row with no slot seen gives zeros (lse: -inf).
+    added to it.  A row with no slot seen gives zeros (lse: -inf).  Sums are
+    float32 and the output is rounded once; what is rounded on the way is in
+    ``include/layout_copy_cache.h``.
     """
     shape = q.shape
     if len(shape) != 3:

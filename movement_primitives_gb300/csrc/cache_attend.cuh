@@ -52,7 +52,7 @@
 // sequences of up to 8192 slots, 32 query on 8 key heads of 128 bfloat16, 1.09
 // GB, 167 us (6.5 TB/s, 98 %); one sequence of 131071 float16 slots, 537 MB, 89
 // us (6.0 TB/s; 9 us of it the launch and the joining of 152 parts a row); 16
-// sequences of up to 2048, 71 MB, 21 us, about half of it what a call costs
+// sequences of up to 2048, 71 MB, 21.5 us, about half of it what a call costs
 // whatever its size: the lengths, the pages, the first rows and the parts are
 // read one after the other, about a microsecond each.  E4M3 at 8 query heads a
 // key head, 148 MB, 44 us with weights collected: a step of 8 KiB takes 930

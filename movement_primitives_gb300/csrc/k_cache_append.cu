@@ -17,8 +17,9 @@
 //
 // Measured on GB300: 64 tokens of 8 heads of 128 as they are 1.9 us, the
 // latency of three dependent reads; prompts of 8966 tokens into E4M3, 56 MB,
-// 11.8 us (4.7 TB/s), 57 thousand tokens, 210 MB, 35 us (6.0 TB/s).  What is
-// left above the copy's rate is the start and the tail of the launch.
+// 11.8 us (4.7 TB/s), 34 thousand tokens, 210 MB, 35 us (6.0 TB/s); the same as
+// they are, 73 MB, 13.1 us (5.6 TB/s) and, 276 MB, 42 us (6.6 TB/s).  What is left
+// above the copy's rate is the start and the tail of the launch.
 #include <cuda_fp8.h>
 
 #include "cache_common.cuh"
@@ -224,7 +225,7 @@ int launch_append_as(AppendArgs &a, int64_t tokens, bool vec, cudaStream_t cs) {
     // of rows to quantise eight where there are as many heads and rows again.
     // The fewer lanes a row, the fewer instructions go into its scale and
     // addresses: prompts of 8966 tokens of 8 heads of 128 with 16 lanes a row
-    // 14.9 us, 8 lanes 13.2, 4 lanes 11.9, 4 lanes and eight heads 11.8 (57 thousand
+    // 14.9 us, 8 lanes 13.2, 4 lanes 11.9, 4 lanes and eight heads 11.8 (34 thousand
     // such tokens 43.8, 39.5 and 35.2, 4096 tokens 4.6, 4.4 and 4.8).
     const int64_t rows = tokens * a.c.heads;
     const bool many = rows >= kApMany;
