@@ -85,6 +85,8 @@ int lc_cache_append(const lc_paged_cache *cache, const void *k_new, const void *
  * head i reading key head i / (n_q_heads / n_kv_heads).
  *   type       of q and out: the cache's own; LC_CACHE_BF16 for an E4M3 cache
  *   *_stride   of sequence and head (lse: of sequence, heads adjacent)
+ *   out        may be q's own buffer with q's strides; else it shares no element
+ *              with q
  *   mask       NULL, or one byte a slot ([n_seqs, capacity], rows mask_stride
  *              apart): slots of a zero byte are not seen
  *   window     0, or the number of newest slots that are seen
@@ -132,7 +134,8 @@ int64_t lc_cache_attend_workspace(const lc_paged_cache *cache, int32_t n_q_heads
 
 /* Errors: LC_ERR_NULL, LC_ERR_SHAPE (n_q_heads no multiple of n_kv_heads,
  * negative window, sizes), LC_ERR_TYPE, LC_ERR_BAD_STRIDE, LC_ERR_ALIGN,
- * LC_ERR_OVERFLOW, LC_ERR_NOT_INJECTIVE, LC_ERR_WORKSPACE. */
+ * LC_ERR_OVERFLOW, LC_ERR_NOT_INJECTIVE, LC_ERR_OVERLAP (out meets q),
+ * LC_ERR_WORKSPACE. */
 int lc_cache_attend(const lc_paged_cache *cache, const lc_cache_query *query, lc_stream_t stream);
 
 /* One eviction.  A sequence of n = lengths[b] <= budget slots keeps them all.

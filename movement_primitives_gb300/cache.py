@@ -238,7 +238,8 @@ def cache_attend(cache: PagedCache, q, lengths, out=None, scale=None, window: in
 
     ``q``: [seqs, q_heads, head_dim] of the cache's type (bfloat16 for a
     float8_e4m3fn cache); query head i reads key head i // (q_heads //
-    kv_heads).  ``scale``: of the dot products, 1 / sqrt(head_dim) by default.
+    kv_heads).  ``out``: like ``q``, and either ``q`` itself or apart from it.
+    ``scale``: of the dot products, 1 / sqrt(head_dim) by default.
     ``window``: only the newest so many slots are seen (0: all).  ``mask``:
     bool or uint8 [seqs, capacity], slots of a zero are not seen.  ``lse``:
     float32 [seqs, q_heads] to receive log sum exp.  ``scores``: float32

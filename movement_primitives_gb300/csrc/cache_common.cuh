@@ -118,14 +118,14 @@ inline bool lists_meet(const void *p, const void *q, int64_t n) {
     return (a < b ? b - a : a - b) < static_cast<uint64_t>(n) * 4;
 }
 
-// Whether rows of `run` 4-byte elements at p (strides st) share any with those
+// Whether rows of `run` elements of eb bytes at p (strides st) share any with those
 // at q (strides qst, rows apart), both of extents `e`.  Buffers whose ranges
 // meet may still be apart, as two interleaved halves of one are.
 inline bool rows_meet(const void *p, const int64_t *st, const void *q, const int64_t *qst, const int64_t *e,
-                      int64_t run) {
+                      int64_t run, int64_t eb = 4) {
     auto span = [&](const int64_t *s) { return (e[0] - 1) * s[0] + (e[1] - 1) * s[1] + run; };
     const int64_t d = (static_cast<int64_t>(reinterpret_cast<uintptr_t>(p)) -
-                       static_cast<int64_t>(reinterpret_cast<uintptr_t>(q))) / 4;
+                       static_cast<int64_t>(reinterpret_cast<uintptr_t>(q))) / eb;
     if (d >= span(qst) || -d >= span(st)) return false;
     // q's rows from their larger step to the smaller one; a step of one row is none
     const int big = e[0] <= 1 ? 1 : e[1] <= 1 ? 0 : qst[0] < qst[1], small = 1 - big;

@@ -282,6 +282,11 @@ extern "C" int lc_cache_attend(const lc_paged_cache *cache, const lc_cache_query
         (q->lse && !rows_apart(1, qext, &q->lse_stride, q->n_q_heads)) ||
         (q->scores && a.c.cap > 0 && !rows_apart(2, kext, q->scores_stride, a.c.cap)))
         return LC_ERR_NOT_INJECTIVE;
+    // a row of the queries' own buffer is written when all that read it have
+    const bool in_place = q->out == q->q && (qext[0] == 1 || q->q_stride[0] == q->out_stride[0]) &&
+                          (qext[1] == 1 || q->q_stride[1] == q->out_stride[1]);
+    if (!in_place && rows_meet(q->q, q->q_stride, q->out, q->out_stride, qext, cache->head_dim, 2))
+        return LC_ERR_OVERLAP;
     AttendSpace space;
     const int64_t chunks = (int64_t(a.c.cap) + kJoinLeast * kScorePer - 1) / (kJoinLeast * kScorePer);
     if (!attend_space(*cache, a.c, q->n_q_heads, q->window, q->scores != nullptr, &space) ||

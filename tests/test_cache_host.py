@@ -159,3 +159,21 @@ def _cache(M):
     c.table_stride = 3
     c.k_stride[:] = c.v_stride[:] = (4 * 16 * 64, 16 * 64, 64)
     return c
+
+
+def test_attend_refuses_an_output_over_the_queries(M):
+    """Two sequences of eight heads of 64 16-bit elements: one element shared, or the same buffer in another order."""
+    c = _cache(M)
+
+    def call(out, stride=(8 * 64, 64), q_stride=(8 * 64, 64)):
+        q = M._lib.CCacheQuery()
+        q.q, q.out, q.lengths = 4 * BASE, out, 6 * BASE
+        q.type, q.n_q_heads, q.scale = 0, 8, 0.125
+        q.q_stride[:], q.out_stride[:] = q_stride, stride
+        q.workspace, q.workspace_bytes = 16 * BASE, 1 << 40
+        return M._lib.STATUS_NAMES[M._lib.lib().lc_cache_attend(ctypes.byref(c), ctypes.byref(q), None)]
+    size = 2 * 8 * 64 * 2
+    for at in (2 - size, -2, 2, 128, size - 2):
+        assert call(4 * BASE + at) == "LC_ERR_OVERLAP"
+    assert call(4 * BASE, stride=(64, 2 * 64)) == "LC_ERR_OVERLAP"
+    assert call(4 * BASE + 2 * (64 - 1), (16 * 64, 2 * 64), (16 * 64, 2 * 64)) == "LC_ERR_OVERLAP"

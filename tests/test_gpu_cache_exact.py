@@ -166,6 +166,22 @@ def test_a_nan_row_adds_nothing_to_slots_it_does_not_see(kind, lens, heads, grou
     no_device_error()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lens,heads,group,dim", [([40, 25], 2, 4, 64), ([700, 90], 2, 16, 128),
+                                                  ([(5 * i) % 67 for i in range(211)], 3, 2, 64),
+                                                  ([4200, 35, 0, 2101], 12, 3, 64), ([150, 60], 2, 20, 64), ([90, 60], 2, 2, 33)])
+def test_attend_into_the_queries_own_buffer_or_beside_it(kind, lens, heads, group, dim):
+    """Every form may write its rows where the queries were, or between them."""
+    s = Setup(lens, heads=heads, dim=dim, kind=kind, page=16, seed=dim)
+    q = s.queries(heads * group)
+    want = lc().cache_attend(s.cache, q, s.lengths)
+    both = torch.stack([q, torch.zeros_like(q)], 2)
+    got = lc().cache_attend(s.cache, both[:, :, 0], s.lengths, out=both[:, :, 1])
+    assert torch.equal(got, want) and torch.equal(both[:, :, 0], q)
+    assert torch.equal(lc().cache_attend(s.cache, q, s.lengths, out=q), want)
+    no_device_error()
+
+
 ASCENDING = """
 import sys
 sys.path[:0] = [%r, %r]
