@@ -128,6 +128,20 @@ class CCacheEviction(ctypes.Structure):
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
 
 
+class CPrompt(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("starts", ctypes.c_void_p), ("k_starts", ctypes.c_void_p),
+                ("n_tokens", ctypes.c_int64), ("n_keys", ctypes.c_int64),
+                ("type", ctypes.c_int32), ("n_seqs", ctypes.c_int32),
+                ("n_q_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("causal", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("q_stride", ctypes.c_int64 * 2), ("k_stride", ctypes.c_int64 * 2),
+                ("v_stride", ctypes.c_int64 * 2), ("out_stride", ctypes.c_int64 * 2),
+                ("lse_stride", ctypes.c_int64)]
+
+
 _P_LAYOUT = ctypes.POINTER(CTileLayout)
 _P_LOOP = ctypes.POINTER(CLoopLayout)
 _P_I32 = ctypes.POINTER(ctypes.c_int32)
@@ -183,6 +197,7 @@ PROTOTYPES = {
     "lc_cache_attend_workspace": (ctypes.c_int64, [ctypes.POINTER(CPagedCache), ctypes.c_int32, ctypes.c_int32]),
     "lc_cache_evict": (ctypes.c_int, [ctypes.POINTER(CPagedCache), ctypes.c_void_p, ctypes.c_void_p]),
     "lc_cache_evict_workspace": (ctypes.c_int64, [ctypes.POINTER(CPagedCache), ctypes.c_int32]),
+    "lc_prompt_attend": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
     "lc_row_major_strides": (ctypes.c_int, [ctypes.c_int32, _P_I64, _P_I64]),
     "lc_layout_footprint": (ctypes.c_int64, [_P_LAYOUT, ctypes.c_int64]),
     "lc_status_string": (ctypes.c_char_p, [ctypes.c_int32]),

@@ -25,9 +25,10 @@ SOURCES = ["plan.cpp", "api.cu", "host_copy.cu", "host_copy_static.cu", "k_vec.c
            "k_warp_w1.cu", "k_warp_w2.cu", "k_warp_w4.cu", "k_warp_w8.cu", "k_warp_w16.cu",
            "k_tile.cu", "k_smem.cu", "k_tma_copy.cu", "k_stencil.cu", "k_loop.cu",
            "k_cache_append.cu", "k_cache_evict.cu", "k_cache_attend.cu", "k_cache_attend_bf16.cu",
-           "k_cache_attend_f16.cu", "k_cache_attend_e4m3.cu"]
+           "k_cache_attend_f16.cu", "k_cache_attend_e4m3.cu",
+           "k_prompt_attend.cu", "k_prompt_attend_bf16.cu", "k_prompt_attend_f16.cu"]
 HEADERS = ["lc_internal.h", "ptx.cuh", "device_common.cuh", "launch.h", "k_warp.cuh", "tensor_map.h", "bulk_store.cuh",
-           "cache_common.cuh", "cache_attend.cuh"]
+           "cache_common.cuh", "cache_attend.cuh", "tensor_core.cuh", "prompt_attend.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O3",
           "-I", INCLUDE, "-I", CSRC]
@@ -42,7 +43,8 @@ def nvcc() -> str:
 
 def _inputs():
     files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS]
-    files += [os.path.join(INCLUDE, h) for h in ("layout_copy.h", "layout_copy_cache.h", "layout_copy_device.cuh")]
+    files += [os.path.join(INCLUDE, h) for h in ("layout_copy.h", "layout_copy_cache.h", "layout_copy_prompt.h",
+                                                  "layout_copy_device.cuh")]
     files.append(os.path.abspath(__file__))
     return files
 

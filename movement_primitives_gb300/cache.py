@@ -60,6 +60,17 @@ def _allocator():
     return lambda shape, strides, dtype: torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
 
 
+_EMPTY = None
+
+
+def _empty():
+    """The allocator, looked up once."""
+    global _EMPTY
+    if _EMPTY is None:
+        _EMPTY = _allocator()
+    return _EMPTY
+
+
 def _elsewhere(cache):
     raise ValueError("the cache is on %s, the current device is cuda:%d: outputs are made and kernels run there "
                      "(torch.cuda.set_device, or a stream of the cache's device)" % (cache.device, _DEVICE()))
@@ -154,7 +165,7 @@ class PagedCache:
         self.n_seqs, self.pages_per_seq = page_table.shape
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
         self.capacity = self.page_size * self.pages_per_seq
-        self._empty = _allocator()
+        self._empty = _empty()
         self._index, self._seqs = k.device.index, (self.n_seqs,)
         self.scale = 1.0 / math.sqrt(self.head_dim)
         self.io_dtype = torch.bfloat16 if q8 else k.dtype

@@ -52,5 +52,7 @@ cudaError_t take_error_attend(unsigned long long *v);
 cudaError_t take_error_attend_bf16(unsigned long long *v);
 cudaError_t take_error_attend_f16(unsigned long long *v);
 cudaError_t take_error_attend_e4m3(unsigned long long *v);
+cudaError_t take_error_prompt_bf16(unsigned long long *v);
+cudaError_t take_error_prompt_f16(unsigned long long *v);
 
 }  // namespace lc

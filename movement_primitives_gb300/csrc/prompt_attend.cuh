@@ -1,0 +1,730 @@
+// Attention over whole prompts (lc_prompt_attend):
+//     x_ij = scale * q_i . k_j,  w = softmax_j(x),  out_i = sum_j w_ij v_j
+// over the keys j of the query's own sequence that are seen.
+//
+// Mathematics.  A tile of 128 rows (query tokens x the query heads of one key
+// head) goes through its keys 128 at a time: S = Q K^T into tensor memory, one
+// thread a row turns S into weights 2^(x - m) relative to a running maximum m
+// and adds them up, P V is added to the output in tensor memory.  m follows the
+// maximum only when that has grown by 2^kRise (the output is then rescaled);
+// until then weights up to 2^kRise are as good as weights up to 1.
+//
+// Both products are fifth-generation tensor-core instructions: Q and K come
+// from shared memory, P from the tensor memory that held S, V from shared
+// memory in its own [key, dim] order.  Two row tiles take turns on the tensor
+// cores: while one tile's products run, the other's softmax does.  Past 128
+// elements a head the outputs of two tiles do not fit; one tile then has two S
+// and runs the next tile's first product during the softmax.
+//
+// A weight is rounded to the values' 16-bit type for the second product: with
+// independent roundings that adds as much as the output's own rounding does
+// (errors against 64 bits 1.4 times a 32-bit softmax's rounded once); a second
+// number a weight would make the tensor cores' work half as much again.
+#pragma once
+
+#include <cuda.h>
+
+#include "cache_common.cuh"
+#include "layout_copy_prompt.h"
+#include "tensor_core.cuh"
+
+namespace lc {
+
+constexpr uint32_t kClassPrompt = 0xf3;
+constexpr int kPrRows = 128;   // rows of a tile
+constexpr int kPrKeys = 128;   // keys of a step
+constexpr int kPrChunk = kPrKeys * 128;  // bytes of 64 columns of a tile
+constexpr int kPrItems = 4;    // items that the scheduling warp may be ahead
+constexpr int kPrMasked = 6;   // steps of an item whose values are looked through: three at either end of its keys at most
+constexpr int kPrTurns = 3;    // items whose unusual values are held: one tile may be two items ahead of the other
+
+struct PromptArgs {
+    const int32_t *starts, *k_starts;
+    uint16_t *out;
+    float *lse;
+    const uint16_t *v;
+    int64_t ost[2], vst[2];
+    int64_t lse_stride;
+    int32_t n_seqs, n_tokens, n_keys;
+    int32_t group, heads_tile, head_blocks, key_heads;  // query heads: a key head's, a tile's; tiles a key head's need
+    int32_t tokens_tile;                                // query tokens of a tile
+    int32_t dim, causal, window;
+    FastDiv heads_div;                                  // by heads_tile
+    FastDiv pair_div;                                   // by key_heads * head_blocks
+    float scale2;                                       // |scale| log2 e
+    int32_t negative;                                   // scale < 0
+    int32_t store;                                      // bytes of a store to out: 32, 16
+    uint64_t limit_ns;
+    CUtensorMap qm, km, vm;
+};
+
+// What one item is: up to two row tiles, the steps of keys that they see.
+struct PromptItem {
+    int32_t q0, nq;     // the sequence's first query row and its queries
+    int32_t k0, nk;
+    int32_t t0;         // first query token of the item
+    int32_t key_head, head0;  // first query head of the tile within its group
+    int32_t first, steps;     // steps of 128 keys, from the sequence's first key
+    int32_t end;        // not 0: there is no further item
+};
+
+template <int NC>
+struct PromptShape {
+    static constexpr int TILES = NC <= 2 ? 2 : 1;          // row tiles of an item
+    static constexpr int CPS = NC <= 2 ? NC : 1;           // 64-column chunks of a ring slot
+    static constexpr int SPT = NC / CPS;                   // slots of a tile of keys or values
+    static constexpr int SLOT = CPS * kPrChunk;
+    static constexpr int Q = TILES * NC * kPrChunk;
+    static constexpr int SLOTS = (232448 - 2048 - Q) / SLOT < 10 ? (232448 - 2048 - Q) / SLOT : 10;
+    static constexpr int SMEM = Q + SLOTS * SLOT + 2048;   // 1024 of them for alignment
+    static constexpr int SOFT = 4 * TILES;                 // softmax warps
+    static constexpr int THREADS = 32 * (SOFT + 4);        // products, loads, scheduling, one idle
+    static constexpr int O = 256;                          // first output column of tensor memory
+};
+
+struct PromptShared {
+    uint64_t ring_full[10], ring_empty[10];
+    uint64_t q_full[2], q_empty[2];
+    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t item_full[kPrItems], item_empty[kPrItems];
+    uint64_t drain;
+    PromptItem item[kPrItems];
+    uint32_t bad[kPrTurns][kPrMasked][4];   // [item's turn][masked step][rows of 32]: values that are not finite
+    int32_t bad_step[kPrTurns][kPrMasked];
+    uint32_t bad_any[kPrTurns][4];
+    uint32_t tmem;
+};
+static_assert(sizeof(PromptShared) <= 1024, "the shared block has 1024 bytes");
+
+__device__ __forceinline__ float pr_exp2(float x) {  // 2 ulp, 0 for -infinity
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t pr_pack(float lo, float hi) {
+    if constexpr (F16) {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    } else {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+}
+__device__ __forceinline__ float pr_max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// ---- scheduling ------------------------------------------------------------
+
+// Items are taken from the longest to the shortest.  A sequence's tiles are
+// counted from its last one down: the last one's level is the tiles of keys
+// that come before the sequence's end, the one before it has a level less.
+struct PromptSeq {
+    int level, tiles;
+};
+
+template <int TILES>
+__device__ __forceinline__ PromptSeq prompt_seq(const PromptArgs &a, int b, PromptItem *it) {
+    const int32_t *ks = a.k_starts ? a.k_starts : a.starts;
+    const int k_most = a.n_keys;
+    const int r0 = a.starts[b], r1 = a.starts[b + 1], s0 = ks[b], s1 = ks[b + 1];
+    const int q0 = min(max(r0, 0), a.n_tokens), q1 = min(max(r1, q0), a.n_tokens);
+    const int k0 = min(max(s0, 0), k_most), k1 = min(max(s1, k0), k_most);
+    if (q0 != r0 || q1 != r1 || k0 != s0 || k1 != s1) report_error(LC_ERR_CACHE_INDEX, kClassPrompt);
+    if (it) {
+        it->q0 = q0;
+        it->nq = q1 - q0;
+        it->k0 = k0;
+        it->nk = k1 - k0;
+    }
+    const int per = TILES * a.tokens_tile;
+    return PromptSeq{(max(k1 - k0, 1) - 1) / per, (q1 - q0 + per - 1) / per};
+}
+
+// Tiles of a sequence at level x or above.
+__device__ __forceinline__ int prompt_above(const PromptArgs &a, const PromptSeq &s, int x) {
+    if (x <= 0) return s.tiles;
+    if (!a.causal) return s.level >= x ? s.tiles : 0;
+    return min(max(s.level - x + 1, 0), s.tiles);
+}
+
+// Item `at` of all, by one warp.
+template <int TILES>
+__device__ __forceinline__ void prompt_item(const PromptArgs &a, uint32_t at, PromptItem *it) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t pair = fast_div(at, a.pair_div);
+    const int which = static_cast<int>(at - pair * a.pair_div.d);
+    PromptSeq mine{0, 0};
+    if (lane < a.n_seqs) mine = prompt_seq<TILES>(a, lane, nullptr);
+    auto total = [&](int x) {
+        uint32_t n = lane < a.n_seqs ? prompt_above(a, mine, x) : 0;
+        for (int b = 32 + lane; b < a.n_seqs; b += 32) n += prompt_above(a, prompt_seq<TILES>(a, b, nullptr), x);
+        return __reduce_add_sync(0xffffffffu, n);
+    };
+    it->end = 1;
+    if (pair >= total(0)) return;
+    it->end = 0;
+    // the highest level x with more than `pair` tiles at it or above
+    int lo = 0, hi = a.n_keys / (TILES * a.tokens_tile) + 1;
+    while (hi - lo > 1) {
+        const int mid = lo + (hi - lo) / 2;
+        if (total(mid) > pair) lo = mid;
+        else hi = mid;
+    }
+    uint32_t rest = pair - total(lo + 1);  // of the tiles at level `lo`, in the sequences' order
+    int tile = 0, seq = 0;
+    for (int b0 = 0; b0 < a.n_seqs; b0 += 32) {
+        const int b = b0 + lane;
+        PromptSeq s{0, 0};
+        if (b < a.n_seqs) s = b0 == 0 ? mine : prompt_seq<TILES>(a, b, nullptr);
+        const uint32_t n = b < a.n_seqs ? prompt_above(a, s, lo) - prompt_above(a, s, lo + 1) : 0;
+        uint32_t upto = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t o = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += o;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, upto > rest);
+        if (hit) {
+            const int src = __ffs(hit) - 1;
+            // tiles of the level begin where those above it, at the sequence's end, leave off
+            const int i = static_cast<int>(rest - (upto - n));
+            const int from = a.causal ? s.tiles - prompt_above(a, s, lo) : 0;
+            tile = __shfl_sync(0xffffffffu, from + i, src);
+            seq = b0 + src;
+            break;
+        }
+        rest -= __shfl_sync(0xffffffffu, upto, 31);
+    }
+    prompt_seq<TILES>(a, seq, it);
+    it->key_head = which / a.head_blocks;
+    it->head0 = which % a.head_blocks * a.heads_tile;
+    it->t0 = tile * TILES * a.tokens_tile;
+    // the keys that any of its rows sees
+    const int last = min(it->t0 + TILES * a.tokens_tile, it->nq) - 1, shift = it->nk - it->nq;
+    const int end = a.causal ? min(max(last + shift + 1, 0), it->nk) : it->nk;
+    const int begin = a.window ? max(it->t0 + shift - a.window + 1, 0) : 0;
+    it->first = begin / kPrKeys;
+    it->steps = max((end + kPrKeys - 1) / kPrKeys - it->first, 0);
+}
+
+// ---- the kernel ------------------------------------------------------------
+
+// Place in the ring, of an item's first slot, of step j's keys or values (in
+// slots of a tile): with two row tiles K0 V0 K1 V1 ..., with one K0 K1 V0 K2 V1 ...
+template <int TILES>
+__device__ __forceinline__ int key_place(int j) { return TILES == 2 ? 2 * j : j ? 2 * j - 1 : 0; }
+template <int TILES>
+__device__ __forceinline__ int value_place(int j, int steps) {
+    return TILES == 2 ? 2 * j + 1 : j + 1 < steps ? 2 * j + 2 : 2 * j + 1;
+}
+
+template <bool F16, int NC>
+__global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(const __grid_constant__ PromptArgs a) {
+    using S = PromptShape<NC>;
+    constexpr int TILES = S::TILES;
+    // weights are up to 2^(kLift + kRise): float16 has few exponents, so small ones are lifted into them; others are
+    // lowered so that sums of the type's largest values stay in float32
+    constexpr float kRise = F16 ? 4.f : 8.f, kLift = F16 ? 11.f : -40.f, kDrop = F16 ? 0x1p-11f : 0x1p40f;
+    extern __shared__ uint8_t raw[];
+    const uint32_t base = (ptx::smem_addr(raw) + 1023) & ~1023u;
+    const uint32_t q_s = base, ring_s = base + S::Q;
+    PromptShared &sh = *reinterpret_cast<PromptShared *>(raw + (base - ptx::smem_addr(raw)) + S::Q + S::SLOTS * S::SLOT);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto bar = [&](const uint64_t &b) { return ptx::smem_addr(&b); };
+
+    if (warp == S::SOFT) tc::alloc(ptx::smem_addr(&sh.tmem), 512);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::SLOTS; ++i) {
+            ptx::mbar_init(bar(sh.ring_full[i]), 1);
+            ptx::mbar_init(bar(sh.ring_empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(bar(sh.q_full[i]), 1);
+            ptx::mbar_init(bar(sh.q_empty[i]), 1);
+            ptx::mbar_init(bar(sh.s_full[i]), 1);
+            ptx::mbar_init(bar(sh.p_full[i]), 4);
+            ptx::mbar_init(bar(sh.o_full[i]), 1);
+        }
+        for (int i = 0; i < kPrItems; ++i) {
+            ptx::mbar_init(bar(sh.item_full[i]), 1);
+            ptx::mbar_init(bar(sh.item_empty[i]), S::SOFT + 2);
+        }
+        ptx::mbar_init(bar(sh.drain), 1);
+        ptx::fence_mbar_init();
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = sh.tmem;
+    start_after_prior();
+
+    bool ok = true;  // no wait of this thread has run out
+    auto wait = [&](const uint64_t &b, uint32_t n) {  // for phase n (counted from 0)
+        if (ok && !ptx::mbar_wait_bounded(bar(b), n & 1, a.limit_ns)) {
+            ok = false;
+            report_error(LC_ERR_TIMEOUT, kClassPrompt);
+        }
+        return ok;
+    };
+    auto arrive = [&](const uint64_t &b) {
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar(b)) : "memory");
+    };
+
+    // of a block's registers the softmax threads take the larger part (384 x 168 = 256 x 200 + 128 x 104)
+    auto few_registers = [] {
+        if constexpr (TILES == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    };
+    if (warp < S::SOFT) {
+        if constexpr (TILES == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        // softmax and outputs: row tile t, a thread a row
+        const int t = TILES == 2 ? warp >> 2 : 0, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21);
+        const int token = static_cast<int>(fast_div(row, a.heads_div)), head = row - token * a.heads_tile;
+        uint32_t n_s = 0, n_o = 0, pos = 0;
+        for (uint32_t i = 0; ok; ++i) {
+            if (!__all_sync(0xffffffffu, wait(sh.item_full[i % kPrItems], i / kPrItems))) break;
+            const PromptItem it = sh.item[i % kPrItems];
+            __syncwarp();
+            if (lane == 0) arrive(sh.item_empty[i % kPrItems]);
+            if (it.end) break;
+            const uint32_t p0 = pos;
+            pos += 2 * it.steps;
+            const int tile0 = it.t0 + t * a.tokens_tile;
+            if (tile0 >= it.nq) continue;
+            const int shift = it.nk - it.nq, mine = tile0 + token;
+            const bool real = token < a.tokens_tile && mine < it.nq && it.head0 + head < a.group;
+            auto keys_end = [&](int x) { return a.causal ? min(max(x + shift + 1, 0), it.nk) : it.nk; };
+            auto keys_begin = [&](int x) { return a.window ? max(x + shift - a.window + 1, 0) : 0; };
+            const int hi = keys_end(min(mine, it.nq - 1)), lo = keys_begin(min(mine, it.nq - 1));
+            // keys in [all_lo, all_hi) are seen by every row of the tile, and of the item
+            const int tile_last = min(tile0 + a.tokens_tile, it.nq) - 1;
+            const int all_hi = keys_end(tile0), all_lo = keys_begin(tile_last);
+            const int item_hi = keys_end(it.t0);
+            const int item_lo = keys_begin(min(it.t0 + TILES * a.tokens_tile, it.nq) - 1);
+            const int turn = i % kPrTurns;
+            float m = -INFINITY, less = -kLift, l = 0.f;
+            int n_bad = 0;
+            if (t == 0) {
+                if (lane == 0) sh.bad_any[turn][warp & 3] = 0;
+                __syncwarp();
+            }
+            for (int j = 0; j < it.steps; ++j) {
+                const int key0 = (it.first + j) * kPrKeys;
+                if (t == 0 && (key0 < item_lo || key0 + kPrKeys > item_hi)) {
+                    // values that some row does not see are multiplied by weights of 0 there: what is not finite
+                    // becomes 0, and is added at the end where it is seen
+                    const uint32_t p = p0 + value_place<TILES>(j, it.steps);
+                    bool found = false;
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        if (c % S::CPS == 0) {
+                            const uint32_t at = p * S::SPT + c / S::CPS;
+                            wait(sh.ring_full[at % S::SLOTS], at / S::SLOTS);
+                        }
+                        uint8_t *v = raw + (ring_s - ptx::smem_addr(raw)) +
+                                     (p * S::SPT + c / S::CPS) % S::SLOTS * S::SLOT + c % S::CPS * kPrChunk + row * 128;
+#pragma unroll
+                        for (int g = 0; g < 8; ++g) {
+                            uint4 *at = reinterpret_cast<uint4 *>(v + (g ^ (row & 7)) * 16);
+                            uint4 x = *at;
+                            constexpr uint32_t kExp = F16 ? 0x7c00u : 0x7f80u;
+                            uint32_t *w = reinterpret_cast<uint32_t *>(&x);
+                            bool here = false;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                here |= (w[e] & kExp) == kExp || (w[e] & kExp << 16) == kExp << 16;
+                            if (here) {
+                                found = true;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    if ((w[e] & kExp) == kExp) w[e] &= 0xffff0000u;
+                                    if ((w[e] & kExp << 16) == kExp << 16) w[e] &= 0xffffu;
+                                }
+                                *at = x;
+                            }
+                        }
+                    }
+                    const uint32_t rows = __ballot_sync(0xffffffffu, found);
+                    if (lane == 0) {
+                        sh.bad[turn][n_bad][warp & 3] = rows;
+                        sh.bad_step[turn][n_bad] = j;
+                        sh.bad_any[turn][warp & 3] |= rows ? 1u << n_bad : 0u;
+                    }
+                    n_bad = min(n_bad + 1, kPrMasked - 1);
+                    tc::fence_async_smem();
+                }
+                const int buf = TILES == 2 ? t : n_s & 1;
+                const uint32_t s_at = lanes + buf * 128;
+                if (!__all_sync(0xffffffffu, wait(sh.s_full[buf], TILES == 2 ? n_s : n_s >> 1))) break;
+                ++n_s;
+                tc::fence_after();
+                uint32_t x[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tc::ld32(x[c], s_at + c * 32);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tc::wait_ld(x[c]);
+                if (key0 < all_lo || key0 + kPrKeys > all_hi) {
+                    const int from = lo - key0, to = hi - key0;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (c * 32 + e < from || c * 32 + e >= to) x[c][e] = 0xff800000u;
+                }
+                float top = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2)
+                        top = pr_max3(top, __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
+                top *= a.scale2;
+                const bool rise = real && (top > m + kRise || (m == -INFINITY && top > m));
+                if (__any_sync(0xffffffffu, rise)) {
+                    const float f = rise ? pr_exp2(m - top) : 1.f;
+                    l *= f;
+                    if (rise) {
+                        m = top;
+                        less = top - kLift;
+                    }
+                    if (j > 0) {
+                        if (TILES == 1) {  // the product before this step's; with two tiles S came after it
+                            if (!__all_sync(0xffffffffu, wait(sh.o_full[0], n_s - 2))) break;
+                            tc::fence_after();
+                        }
+                        const uint32_t o_at = lanes + S::O + t * NC * 64;
+                        for (int c = 0; c < (a.dim + 31) / 32; ++c) {
+                            uint32_t o[32];
+                            tc::ld32(o, o_at + c * 32);
+                            tc::wait_ld(o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tc::st32(o_at + c * 32, o);
+                        }
+                    }
+                }
+                const float2 scale = make_float2(a.scale2, a.scale2), off = make_float2(-less, -less);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float2 y = tc::fma2(make_float2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])), scale, off);
+                        y.x = pr_exp2(y.x);
+                        y.y = pr_exp2(y.y);
+                        sum[e >> 1 & 1] = tc::add2(sum[e >> 1 & 1], y);
+                        p[e / 2] = pr_pack<F16>(y.x, y.y);
+                    }
+                    tc::st16(s_at + c * 16, p);
+                }
+                const float2 both = tc::add2(sum[0], sum[1]);
+                l += both.x + both.y;
+                tc::wait_st();
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) arrive(sh.p_full[buf]);
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            // output
+            if (it.steps) {
+                if (!__all_sync(0xffffffffu, wait(sh.o_full[t], TILES == 2 ? n_o++ : n_s - 1))) break;
+                tc::fence_after();
+            }
+            const int64_t at = it.q0 + mine;
+            const int hq = it.key_head * a.group + it.head0 + head;
+            uint16_t *out = a.out + at * a.ost[0] + hq * a.ost[1];
+            const float f = l == 0.f ? 0.f : 1.f / l;
+            uint32_t bad = 0;
+            if (it.steps)
+                for (int w = 0; w < 4; ++w) bad |= sh.bad_any[turn][w];
+            for (int c = 0; c < (a.dim + 31) / 32; ++c) {
+                uint32_t o[32];
+                __syncwarp();
+                if (it.steps) {
+                    tc::ld32(o, lanes + S::O + t * NC * 64 + c * 32);
+                    tc::wait_ld(o);
+                }
+                if (l == 0.f) {  // nothing to see
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0;
+                }
+                for (uint32_t left = bad; left; left &= left - 1) {
+                    const int n = __ffs(left) - 1, key0 = (it.first + sh.bad_step[turn][n]) * kPrKeys;
+                    for (int w = 0; w < 4; ++w)
+                        for (uint32_t keys = sh.bad[turn][n][w]; keys; keys &= keys - 1) {
+                            const int key = key0 + w * 32 + __ffs(keys) - 1;
+                            if (!real || key < lo || key >= hi) continue;
+                            const uint16_t *v = a.v + (it.k0 + key) * a.vst[0] + it.key_head * a.vst[1] + c * 32;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                if (c * 32 + e >= a.dim) break;
+                                const uint32_t bits = v[e];
+                                constexpr uint32_t kExp = F16 ? 0x7c00u : 0x7f80u;
+                                if ((bits & kExp) != kExp) continue;
+                                const float y = F16 ? __half2float(__ushort_as_half(bits)) : __uint_as_float(bits << 16);
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) + y);
+                            }
+                        }
+                }
+                if (real) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 16) {
+                    uint32_t y[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        y[k] = pr_pack<F16>(__uint_as_float(o[e + 2 * k]) * f, __uint_as_float(o[e + 2 * k + 1]) * f);
+                    uint16_t *to = out + c * 32 + e;
+                    if (a.store == 32 && c * 32 + e + 16 <= a.dim) {
+                        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(y[0]),
+                                     "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
+                                     : "memory");
+                    } else if (a.store >= 16) {
+                        if (c * 32 + e + 8 <= a.dim) *reinterpret_cast<uint4 *>(to) = make_uint4(y[0], y[1], y[2], y[3]);
+                        if (c * 32 + e + 16 <= a.dim)
+                            *reinterpret_cast<uint4 *>(to + 8) = make_uint4(y[4], y[5], y[6], y[7]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            if (c * 32 + e + k < a.dim) to[k] = static_cast<uint16_t>(y[k / 2] >> (k & 1) * 16);
+                    }
+                }
+                }
+            }
+            if (a.lse && real)
+                a.lse[at * a.lse_stride + hq] = l == 0.f ? -INFINITY : (less + kLift + log2f(l * kDrop)) * 0.6931471805599453f;
+        }
+    } else if (warp == S::SOFT + 2) {
+        few_registers();
+        // scheduling: items dealt in turn, every other round backwards, so that none gets the longest of each
+        for (uint32_t i = 0; ok; ++i) {
+            const uint32_t at = i * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            PromptItem it{};
+            prompt_item<TILES>(a, at, &it);
+            const int s = i % kPrItems;
+            if (i >= kPrItems) wait(sh.item_empty[s], i / kPrItems - 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (lane == 0) {
+                sh.item[s] = it;
+                arrive(sh.item_full[s]);
+            }
+            __syncwarp();
+            if (it.end) break;
+        }
+    } else if (warp == S::SOFT + 1) {
+        few_registers();
+        // loads
+        if (lane == 0) {
+            uint32_t pos = 0, tiles_q[2] = {0, 0};
+            for (uint32_t i = 0;; ++i) {
+                if (!wait(sh.item_full[i % kPrItems], i / kPrItems)) break;
+                const PromptItem it = sh.item[i % kPrItems];
+                arrive(sh.item_empty[i % kPrItems]);
+                if (it.end) break;
+                if (!it.steps) continue;
+                auto load_q = [&](int t) {
+                    if (it.t0 + t * a.tokens_tile >= it.nq) return;
+                    if (tiles_q[t] && !wait(sh.q_empty[t], tiles_q[t] - 1)) return;
+                    ++tiles_q[t];
+                    ptx::mbar_arrive_expect_tx(bar(sh.q_full[t]), NC * 128 * a.heads_tile * a.tokens_tile);
+#pragma unroll
+                    for (int c = 0; c < NC; ++c)
+                        ptx::tma_load_3d(q_s + (t * NC + c) * kPrChunk, &a.qm, c * 64, it.key_head * a.group + it.head0,
+                                         it.q0 + it.t0 + t * a.tokens_tile, bar(sh.q_full[t]));
+                };
+                auto load_tile = [&](const CUtensorMap &m, int j) {
+#pragma unroll
+                    for (int p = 0; p < S::SPT; ++p, ++pos) {
+                        const uint32_t s = pos % S::SLOTS, n = pos / S::SLOTS;
+                        if (n && !wait(sh.ring_empty[s], n - 1)) return;
+                        if (!ok) return;
+                        ptx::mbar_arrive_expect_tx(bar(sh.ring_full[s]), S::SLOT);
+#pragma unroll
+                        for (int c = 0; c < S::CPS; ++c)
+                            ptx::tma_load_3d(ring_s + s * S::SLOT + c * kPrChunk, &m, (p * S::CPS + c) * 64, it.key_head,
+                                             it.k0 + (it.first + j) * kPrKeys, bar(sh.ring_full[s]));
+                    }
+                };
+                load_q(0);
+                load_tile(a.km, 0);
+                if constexpr (TILES == 2) {
+                    load_q(1);
+                    load_tile(a.vm, 0);
+                    for (int j = 1; j < it.steps && ok; ++j) {
+                        load_tile(a.km, j);
+                        load_tile(a.vm, j);
+                    }
+                } else {
+                    for (int j = 1; j < it.steps && ok; ++j) {
+                        load_tile(a.km, j);
+                        load_tile(a.vm, j - 1);
+                    }
+                    load_tile(a.vm, it.steps - 1);
+                }
+                if (!ok) break;
+            }
+            if (!ok) {  // copies in flight end before the block does
+                ok = true;
+                for (uint32_t p = pos > S::SLOTS ? pos - S::SLOTS : 0; p < pos; ++p)
+                    wait(sh.ring_full[p % S::SLOTS], p / S::SLOTS);
+                for (int t = 0; t < TILES; ++t)
+                    if (tiles_q[t]) wait(sh.q_full[t], tiles_q[t] - 1);
+            }
+        }
+    } else if (warp == S::SOFT) {
+        few_registers();
+        // products
+        if (lane == 0) {
+            const uint32_t qk = tc::instr_desc(F16, kPrKeys, false, a.negative);
+            const int k_steps = (a.dim + 15) / 16;
+            uint32_t pos = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
+            for (uint32_t i = 0;; ++i) {
+                if (!wait(sh.item_full[i % kPrItems], i / kPrItems)) break;
+                const PromptItem it = sh.item[i % kPrItems];
+                arrive(sh.item_empty[i % kPrItems]);
+                if (it.end) break;
+                if (!it.steps) continue;
+                const int tiles = TILES == 2 && it.t0 + a.tokens_tile < it.nq ? 2 : 1;
+                auto wait_tile = [&](uint32_t p) {
+#pragma unroll
+                    for (int c = 0; c < S::SPT; ++c)
+                        wait(sh.ring_full[(p * S::SPT + c) % S::SLOTS], (p * S::SPT + c) / S::SLOTS);
+                    tc::fence_after();
+                };
+                auto free_tile = [&](uint32_t p) {
+#pragma unroll
+                    for (int c = 0; c < S::SPT; ++c) tc::commit(bar(sh.ring_empty[(p * S::SPT + c) % S::SLOTS]));
+                };
+                auto chunk_at = [&](uint32_t p, int c) {  // chunk c of the tile at place p
+                    return ring_s + (p * S::SPT + c / S::CPS) % S::SLOTS * S::SLOT + c % S::CPS * kPrChunk;
+                };
+                // S = Q K^T of row tile t into S buffer `to`
+                auto first_product = [&](int t, int to, uint32_t p) {
+                    for (int k = 0; k < k_steps; ++k) {
+                        const uint32_t at = (k & 3) * 32;
+                        tc::mma_ss(tmem + to * 128, tc::smem_desc(q_s + (t * NC + k / 4) * kPrChunk + at, 16),
+                                   tc::smem_desc(chunk_at(p, k / 4) + at, 16), qk, k > 0);
+                    }
+                    tc::commit(bar(sh.s_full[to]));
+                };
+                // O += P V
+                auto second_product = [&](int t, int from, uint32_t p, bool add) {
+#pragma unroll
+                    for (int c = 0; c < NC; c += S::CPS) {
+                        const int cols = min(a.dim - c * 64, S::CPS * 64);
+                        const uint32_t pv = tc::instr_desc(F16, (cols + 15) / 16 * 16, true, false);
+                        const uint32_t d = tmem + S::O + t * NC * 64 + c * 64;
+#pragma unroll
+                        for (int k = 0; k < kPrKeys / 16; ++k)
+                            tc::mma_ts(d, tmem + from * 128 + k * 8,
+                                       tc::smem_desc(chunk_at(p, c) + k * 2048, kPrChunk), pv, add || k > 0);
+                    }
+                };
+                const uint32_t p0 = pos;
+                pos += 2 * it.steps;
+                if constexpr (TILES == 2) {
+                    wait_tile(p0);
+                    for (int t = 0; t < tiles; ++t) {
+                        wait(sh.q_full[t], n_q[t]++);
+                        tc::fence_after();
+                        if (!ok) break;
+                        first_product(t, t, p0);
+                        if (it.steps == 1) tc::commit(bar(sh.q_empty[t]));
+                    }
+                    free_tile(p0);
+                    for (int j = 0; j < it.steps && ok; ++j) {
+                        const uint32_t pv = p0 + value_place<2>(j, it.steps), pk = p0 + key_place<2>(j + 1);
+                        const bool more = j + 1 < it.steps;
+                        wait_tile(pv);
+                        for (int t = 0; t < tiles; ++t) {
+                            wait(sh.p_full[t], n_p[t]++);
+                            tc::fence_after();
+                            if (!ok) break;
+                            second_product(t, t, pv, j > 0);
+                            if (t == tiles - 1) free_tile(pv);
+                            if (more) {
+                                if (t == 0) wait_tile(pk);
+                                if (!ok) break;
+                                first_product(t, t, pk);
+                                if (t == tiles - 1) free_tile(pk);
+                                if (j + 2 == it.steps) tc::commit(bar(sh.q_empty[t]));
+                            } else {
+                                tc::commit(bar(sh.o_full[t]));
+                            }
+                        }
+                    }
+                } else {
+                    wait(sh.q_full[0], n_q[0]++);
+                    tc::fence_after();
+                    const uint32_t t0 = n_p[0];  // steps before this item: the S buffers go on in turn
+                    for (int j = 0; j < 2 && j < it.steps && ok; ++j) {
+                        wait_tile(p0 + key_place<1>(j));
+                        if (!ok) break;
+                        first_product(0, (t0 + j) & 1, p0 + key_place<1>(j));
+                        free_tile(p0 + key_place<1>(j));
+                        if (j + 1 == it.steps) tc::commit(bar(sh.q_empty[0]));
+                    }
+                    for (int j = 0; j < it.steps && ok; ++j) {
+                        const int buf = n_p[0] & 1;
+                        const uint32_t pv = p0 + value_place<1>(j, it.steps);
+                        wait_tile(pv);
+                        wait(sh.p_full[buf], n_p[0]++ >> 1);
+                        tc::fence_after();
+                        if (!ok) break;
+                        second_product(0, buf, pv, j > 0);
+                        free_tile(pv);
+                        tc::commit(bar(sh.o_full[0]));
+                        if (j + 2 < it.steps) {
+                            const uint32_t pk = p0 + key_place<1>(j + 2);
+                            wait_tile(pk);
+                            if (!ok) break;
+                            first_product(0, buf, pk);
+                            free_tile(pk);
+                            if (j + 3 == it.steps) tc::commit(bar(sh.q_empty[0]));
+                        }
+                    }
+                }
+                if (!ok) break;
+            }
+            // products in flight end before the tensor memory is given back
+            ok = true;
+            tc::commit(bar(sh.drain));
+            wait(sh.drain, 0);
+        }
+    } else {
+        few_registers();
+    }
+    __syncwarp();
+    tc::fence_before();
+    __syncthreads();
+    if (warp == S::SOFT) {
+        tc::fence_after();
+        tc::dealloc(tmem, 512);
+    }
+}
+
+template <bool F16, int NC>
+int launch_prompt_shape(const PromptArgs &a, int64_t items, cudaStream_t cs) {
+    using S = PromptShape<NC>;
+    const void *fn = reinterpret_cast<const void *>(&k_prompt_attend<F16, NC>);
+    int sms = 0, per_sm = 0;
+    if (prepare(fn, S::THREADS, S::SMEM, S::SMEM, &sms, &per_sm) != cudaSuccess) return LC_ERR_CUDA;
+    return launch_after(fn, static_cast<unsigned>(std::min<int64_t>(items, sms)), S::THREADS, S::SMEM, cs, &a);
+}
+
+template <bool F16>
+int launch_prompt_type(const PromptArgs &a, int64_t items, cudaStream_t cs) {
+    switch ((a.dim + 63) / 64) {
+        case 1: return launch_prompt_shape<F16, 1>(a, items, cs);
+        case 2: return launch_prompt_shape<F16, 2>(a, items, cs);
+        case 3: return launch_prompt_shape<F16, 3>(a, items, cs);
+        default: return launch_prompt_shape<F16, 4>(a, items, cs);
+    }
+}
+
+}  // namespace lc
