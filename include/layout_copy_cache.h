@@ -11,8 +11,14 @@
  *
  *   lc_cache_append   writes new tokens' rows into their slots
  *   lc_cache_attend   attention of one new token a sequence over its slots
+ *   lc_cache_attend_tree  attention of a tree of drafted tokens a sequence
+ *   lc_cache_accept   keeps the accepted path of the drafts, moved together
+ *                     behind the tokens before them
  *   lc_cache_evict    keeps the slots of the largest accumulated weight and
  *                     the newest ones, moved together at the front
+ *   lc_cache_reserve  page tables from lengths and a stack of free pages, and
+ *                     the slots of packed tokens
+ *   lc_cache_append_packed  writes packed tokens' rows into such slots
  *
  * Conventions are those of layout_copy.h: strides count elements, structs
  * are read during the call and not retained, pointers are device addresses
@@ -137,6 +143,122 @@ int64_t lc_cache_attend_workspace(const lc_paged_cache *cache, int32_t n_q_heads
  * LC_ERR_OVERFLOW, LC_ERR_NOT_INJECTIVE, LC_ERR_OVERLAP (out meets q),
  * LC_ERR_WORKSPACE. */
 int lc_cache_attend(const lc_paged_cache *cache, const lc_cache_query *query, lc_stream_t stream);
+
+/* Most drafted tokens of a sequence in one call. */
+#define LC_CACHE_MAX_DRAFTS 64
+
+/* Attention of a tree of drafted tokens a sequence.  The drafts' rows are in the
+ * cache already, as lc_cache_append leaves them: draft t of counts[b] sits in slot
+ * lengths[b] - counts[b] + t.  It sees the slots before the drafts, its ancestors'
+ * and its own.  (A chain, parents[t] = t - 1, is causal attention of several new
+ * tokens.)
+ *   parents    [n_seqs, n_drafts], rows parents_stride apart: a draft's parent, an
+ *              earlier draft, or -1 where it follows the token before the drafts; any
+ *              other value counts as -1 and records LC_ERR_CACHE_INDEX
+ *   counts     [n_seqs], or NULL: n_drafts each, as far as the length goes; one outside 0 .. min(n_drafts,
+ *              length) is clamped, with LC_ERR_CACHE_INDEX
+ *   type       of q and out: the cache's own; LC_CACHE_BF16 for an E4M3 cache
+ *   *_stride   of sequence, draft, head (lse: of sequence, draft, heads adjacent)
+ *   out        shares no address range with q
+ *   window     0, or how many tokens are seen, a draft's own and its nearest ancestors
+ *              first, then the newest before the drafts
+ *   scale      of the dot products, finite
+ *   lse        NULL, or receives log(sum_j exp(scale q . k_j))
+ *   workspace  at least lc_cache_attend_tree_workspace(...) bytes, as lc_cache_attend's
+ *
+ * Rows of out and lse of drafts past a sequence's count are left as they were.
+ * Roundings are lc_cache_attend's: float32 sums, weights of a bfloat16 or float16
+ * cache as two numbers of its type, those of an E4M3 cache as one float16
+ * number, its queries as float16 scaled by a power of two a row.  A row that
+ * sees a value that is infinite or NaN has no finite number in that column. */
+typedef struct {
+    const void *q;
+    void *out;
+    int32_t type;
+    int32_t n_q_heads;
+    int32_t n_drafts;
+    int32_t window;
+    int64_t q_stride[3], out_stride[3];
+    const int32_t *lengths, *counts, *parents;
+    int64_t parents_stride;
+    float scale;
+    float *lse;
+    int64_t lse_stride[2];
+    void *workspace;
+    int64_t workspace_bytes;
+} lc_cache_tree;
+
+/* Bytes of workspace of lc_cache_attend_tree, or -1 for a cache that it refuses. */
+int64_t lc_cache_attend_tree_workspace(const lc_paged_cache *cache);
+
+/* Errors: as lc_cache_attend; LC_ERR_SHAPE also for n_drafts outside 0 ..
+ * LC_CACHE_MAX_DRAFTS.  Waits inside the kernel are bounded (LC_WAIT_TIMEOUT_NS);
+ * one that runs out sets LC_ERR_TIMEOUT in the error word. */
+int lc_cache_attend_tree(const lc_paged_cache *cache, const lc_cache_tree *tree, lc_stream_t stream);
+
+/* Keeps the drafts of a path and lets the others go: the i-th draft of the path
+ * moves from slot before + path[b, i] to slot before + i of its sequence, before =
+ * lengths[b] - counts[b], in both pools and their scales, and new_lengths[b] = before
+ * + the path's length.  Slots past that hold what they held or what moved.
+ *   path       [n_seqs, n_path], rows path_stride apart, n_path <= LC_CACHE_MAX_DRAFTS: drafts in rising
+ *              order, ended by -1; one that does not rise or is no draft of the
+ *              sequence ends the path too, and records LC_ERR_CACHE_INDEX
+ *   counts     [n_seqs], the drafts a sequence has, or NULL: n_path each, as far as
+ *              the length goes; clamped as in lc_cache_attend_tree
+ *   new_lengths  [n_seqs], sharing no element with lengths, counts or path
+ * The pages that hold the drafts must not be shared with another sequence.
+ * Errors: as lc_cache_append. */
+int lc_cache_accept(const lc_paged_cache *cache, const int32_t *lengths, const int32_t *counts, const int32_t *path,
+                    int64_t path_stride, int32_t n_path, int32_t *new_lengths, lc_stream_t stream);
+
+/* Writes packed tokens: row t of k_new and v_new, [n_tokens, n_kv_heads,
+ * head_dim], goes to slot slots[t] of the pool, page * page_size + row, whose pages lc_cache_reserve
+ * gives; -1 drops it, any other slot outside the pool does too, with LC_ERR_CACHE_INDEX. No two
+ * tokens have one slot.  *_stride: of token and head.  The cache's page table
+ * is not read.  Else as lc_cache_append. */
+int lc_cache_append_packed(const lc_paged_cache *cache, const void *k_new, const void *v_new, int32_t type,
+                           const int64_t k_stride[2], const int64_t v_stride[2], int32_t n_tokens, const int64_t *slots,
+                           lc_stream_t stream);
+
+/* Most sequences of one lc_cache_reserve. */
+#define LC_CACHE_MAX_RESERVED 4096
+
+/* Makes a page table hold the pages of lengths[b] + counts[b] tokens a sequence, and
+ * tells where each of the new tokens goes.
+ *   page_table   [n_seqs, pages_per_seq]: a sequence's pages, then -1
+ *   new_table    the same afterwards; may be page_table itself (with its stride)
+ *   free, n_free a stack of free pages of free_size entries and how many it has.  Pages past
+ *                those that a sequence wants (one that has ended: length 0, count 0) go on
+ *                top first, in the sequences' order; what is missing then comes off the top, in the
+ *                same order
+ *   new_n_free   how many the stack has afterwards
+ *   new_lengths  lengths + counts of the sequences that are served, lengths of the others
+ *   starts       [n_seqs + 1]: where each sequence's tokens begin among the packed ones
+ *   slots, positions, seqs   [max_tokens], of every packed token: page * page_size +
+ *                row, place in its sequence, sequence; -1 past the last
+ * A sequence is not served, keeps the pages that it has and gets no tokens where its
+ * pages do not last (those behind it that need pages are not served either), its
+ * tokens pass pages_per_seq, or max_tokens ends; that records LC_ERR_CACHE_INDEX,
+ * as a negative length or count (taken as 0) does.  All outputs and the stack lie
+ * apart from one another and from what is read.
+ * The stack's entries past its top and below free_size may change. */
+typedef struct {
+    const int32_t *page_table;
+    int32_t *new_table;
+    int64_t table_stride, new_table_stride;
+    const int32_t *lengths, *counts;
+    int32_t *free;
+    const int32_t *n_free;
+    int32_t *new_n_free, *new_lengths, *starts;
+    int64_t *slots;
+    int32_t *positions, *seqs;
+    int64_t free_size;
+    int32_t n_seqs, pages_per_seq, page_size, max_tokens;
+} lc_cache_reservation;
+
+/* Errors: LC_ERR_NULL, LC_ERR_SHAPE (sizes; more than LC_CACHE_MAX_RESERVED sequences),
+ * LC_ERR_BAD_STRIDE, LC_ERR_ALIGN, LC_ERR_OVERFLOW, LC_ERR_NOT_INJECTIVE, LC_ERR_OVERLAP, LC_ERR_CUDA. */
+int lc_cache_reserve(const lc_cache_reservation *reservation, lc_stream_t stream);
 
 /* One eviction.  A sequence of n = lengths[b] <= budget slots keeps them all.
  * A longer one keeps, per key head, its `recent` newest slots and, of the

@@ -15,7 +15,8 @@ from typing import Sequence
 
 from . import _lib
 from ._lib import KERNELS, STATUS, STATUS_NAMES
-from .cache import PagedCache, cache_append, cache_attend, cache_attend_workspace, cache_evict
+from .cache import (PagedCache, Reservation, cache_accept, cache_append, cache_append_packed, cache_attend,
+                    cache_attend_tree, cache_attend_workspace, cache_evict, cache_reserve)
 from .prompt import prompt_attend
 
 __all__ = ["TileLayout", "LayoutCopyError", "layout_copy", "layout_copy_ptr", "layout_copy_host",
@@ -24,6 +25,7 @@ __all__ = ["TileLayout", "LayoutCopyError", "layout_copy", "layout_copy_ptr", "l
            "last_device_error", "debug_wait_timeout", "warp_unit_plan", "warp_unit_run",
            "loop_layout_default", "loop_layout_info", "loop_plan", "layout_copy_loop", "layout_copy_loop_ptr",
            "PagedCache", "cache_append", "cache_attend", "cache_attend_workspace", "cache_evict",
+           "Reservation", "cache_accept", "cache_append_packed", "cache_attend_tree", "cache_reserve",
            "prompt_attend",
            "KERNELS", "STATUS"]
 

@@ -128,6 +128,28 @@ class CCacheEviction(ctypes.Structure):
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
 
 
+class CCacheTree(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("type", ctypes.c_int32), ("n_q_heads", ctypes.c_int32),
+                ("n_drafts", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("q_stride", ctypes.c_int64 * 3), ("out_stride", ctypes.c_int64 * 3),
+                ("lengths", ctypes.c_void_p), ("counts", ctypes.c_void_p), ("parents", ctypes.c_void_p),
+                ("parents_stride", ctypes.c_int64), ("scale", ctypes.c_float),
+                ("lse", ctypes.c_void_p), ("lse_stride", ctypes.c_int64 * 2),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
+
+
+class CCacheReservation(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("new_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("new_table_stride", ctypes.c_int64),
+                ("lengths", ctypes.c_void_p), ("counts", ctypes.c_void_p),
+                ("free", ctypes.c_void_p), ("n_free", ctypes.c_void_p),
+                ("new_n_free", ctypes.c_void_p), ("new_lengths", ctypes.c_void_p), ("starts", ctypes.c_void_p),
+                ("slots", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("seqs", ctypes.c_void_p),
+                ("free_size", ctypes.c_int64), ("n_seqs", ctypes.c_int32), ("pages_per_seq", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("max_tokens", ctypes.c_int32)]
+
+
 class CPrompt(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
                 ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
@@ -197,6 +219,14 @@ PROTOTYPES = {
     "lc_cache_attend_workspace": (ctypes.c_int64, [ctypes.POINTER(CPagedCache), ctypes.c_int32, ctypes.c_int32]),
     "lc_cache_evict": (ctypes.c_int, [ctypes.POINTER(CPagedCache), ctypes.c_void_p, ctypes.c_void_p]),
     "lc_cache_evict_workspace": (ctypes.c_int64, [ctypes.POINTER(CPagedCache), ctypes.c_int32]),
+    "lc_cache_append_packed": (ctypes.c_int, [ctypes.POINTER(CPagedCache), ctypes.c_void_p, ctypes.c_void_p,
+                                              ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+                                              ctypes.c_void_p, ctypes.c_void_p]),
+    "lc_cache_attend_tree": (ctypes.c_int, [ctypes.POINTER(CPagedCache), ctypes.c_void_p, ctypes.c_void_p]),
+    "lc_cache_attend_tree_workspace": (ctypes.c_int64, [ctypes.POINTER(CPagedCache)]),
+    "lc_cache_accept": (ctypes.c_int, [ctypes.POINTER(CPagedCache), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                       ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p]),
+    "lc_cache_reserve": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
     "lc_prompt_attend": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
     "lc_row_major_strides": (ctypes.c_int, [ctypes.c_int32, _P_I64, _P_I64]),
     "lc_layout_footprint": (ctypes.c_int64, [_P_LAYOUT, ctypes.c_int64]),

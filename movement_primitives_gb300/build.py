@@ -26,9 +26,11 @@ SOURCES = ["plan.cpp", "api.cu", "host_copy.cu", "host_copy_static.cu", "k_vec.c
            "k_tile.cu", "k_smem.cu", "k_tma_copy.cu", "k_stencil.cu", "k_loop.cu",
            "k_cache_append.cu", "k_cache_evict.cu", "k_cache_attend.cu", "k_cache_attend_bf16.cu",
            "k_cache_attend_f16.cu", "k_cache_attend_e4m3.cu",
-           "k_prompt_attend.cu", "k_prompt_attend_bf16.cu", "k_prompt_attend_f16.cu"]
+           "k_prompt_attend.cu", "k_prompt_attend_bf16.cu", "k_prompt_attend_f16.cu",
+           "k_tree_attend.cu", "k_tree_attend_bf16.cu", "k_tree_attend_f16.cu", "k_tree_attend_e4m3.cu",
+           "k_cache_accept.cu", "k_cache_reserve.cu"]
 HEADERS = ["lc_internal.h", "ptx.cuh", "device_common.cuh", "launch.h", "k_warp.cuh", "tensor_map.h", "bulk_store.cuh",
-           "cache_common.cuh", "cache_attend.cuh", "tensor_core.cuh", "prompt_attend.cuh"]
+           "cache_common.cuh", "cache_attend.cuh", "tensor_core.cuh", "prompt_attend.cuh", "tree_attend.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O3",
           "-I", INCLUDE, "-I", CSRC]

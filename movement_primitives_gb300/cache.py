@@ -1,4 +1,5 @@
-"""Paged key-value cache: append, attention of one new token, eviction.
+"""Paged key-value cache: append, attention of one new token or of a tree of
+drafted ones, acceptance of drafts, eviction, page tables.
 
 A cache is a pool of pages seen as [page, kv_head, slot, dim] through its
 strides (a [page, slot, kv_head, dim] pool is passed as its ``transpose(1,
@@ -12,27 +13,32 @@ from __future__ import annotations
 import ctypes
 import math
 import struct
+from typing import NamedTuple
 
 from . import _lib
 
-__all__ = ["PagedCache", "cache_append", "cache_attend", "cache_attend_workspace", "cache_evict"]
+__all__ = ["PagedCache", "Reservation", "cache_accept", "cache_append", "cache_append_packed", "cache_attend",
+           "cache_attend_tree", "cache_attend_workspace", "cache_evict", "cache_reserve"]
 
 _STRIDES = struct.Struct("@3q")                      # int64_t[3]
+_PAIR = struct.Struct("@2q")
 _QUERY = struct.Struct("@PPiiqqqqPPqifPqPqqPq")     # lc_cache_query
+_TREE = struct.Struct("@PP4i6q3PqfP2qPq")            # lc_cache_tree
+_RESERVATION = struct.Struct("@PP2q10Pq4i")          # lc_cache_reservation
 _EVICTION = struct.Struct("@PPqqiiPqqPqqPPq")        # lc_cache_eviction
 # of torch, known once a cache exists
 _TYPES = None  # dtype -> lc_cache_type
-_BYTES = _BOOL = _I32 = _F32 = None
+_BYTES = _BOOL = _I32 = _I64 = _F32 = None
 _CURRENT = None  # raw handle of a device's current stream (torch.cuda.current_stream() builds an object, 3 us)
 _DEVICE = None   # the current device's index (torch.cuda.current_device() takes twice as long)
 _GRAD = None     # whether gradients are recorded
 
 
 def _types():
-    global _TYPES, _BYTES, _BOOL, _I32, _F32, _CURRENT, _DEVICE, _GRAD
+    global _TYPES, _BYTES, _BOOL, _I32, _I64, _F32, _CURRENT, _DEVICE, _GRAD
     if _TYPES is None:
         import torch
-        _BYTES, _BOOL, _I32, _F32 = torch.uint8, torch.bool, torch.int32, torch.float32
+        _BYTES, _BOOL, _I32, _I64, _F32 = torch.uint8, torch.bool, torch.int32, torch.int64, torch.float32
         _CURRENT = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
             (lambda index: torch.cuda.current_stream(index).cuda_stream)
         _DEVICE = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
@@ -181,6 +187,13 @@ class PagedCache:
             self._workspace_bytes[key] = n
         return n
 
+    def tree_workspace_bytes(self) -> int:
+        n = self._workspace_bytes.get("tree")
+        if n is None:  # (0 for a refused cache: the call says why)
+            n = max(0, int(_lib.lib().lc_cache_attend_tree_workspace(self._ref)))
+            self._workspace_bytes["tree"] = n
+        return n
+
     def evict_workspace_bytes(self, budget: int) -> int:
         n = self._workspace_bytes.get(budget)
         if n is None:  # (0 for a refused budget: the call says why)
@@ -317,6 +330,204 @@ def _attend(cache, q, n_q, lengths, out, scale, window, mask, lse, scores, works
     if status:
         _check(status, "cache_attend")
     return out
+
+
+def cache_append_packed(cache: PagedCache, k, v, slots, stream=None):
+    """Writes packed tokens into the slots that ``cache_reserve`` gave them.
+
+    ``k``, ``v``: [tokens, kv_heads, head_dim], of the types that ``cache_append``
+    takes.  ``slots``: int64 [tokens], page * page_size + row, no two alike; a
+    token of -1 is dropped, and so is one outside the pool, which sets the device error word.
+    """
+    shape = k.shape
+    kind = _TYPES.get(k.dtype)
+    if len(shape) != 3 or kind is None or kind > 1:
+        raise ValueError("new keys and values are [tokens, kv_heads, head_dim] of bfloat16 or float16")
+    _tensor(k, "k", k.dtype, (shape[0], cache.n_kv_heads, cache.head_dim), cache.device)
+    _tensor(v, "v", k.dtype, shape, cache.device)
+    if k.requires_grad or v.requires_grad:
+        _no_gradient()
+    _tensor(slots, "slots", _I64, (shape[0],), cache.device)
+    if stream is not None:
+        with _on(stream) as handle:
+            return _append_packed(cache, k, v, kind, slots, handle)
+    return _append_packed(cache, k, v, kind, slots, _CURRENT(cache._index))
+
+
+def _append_packed(cache, k, v, kind, slots, handle):
+    if _DEVICE() != cache._index:
+        _elsewhere(cache)
+    status = _lib.lib().lc_cache_append_packed(
+        cache._ref, k.data_ptr(), v.data_ptr(), kind, _PAIR.pack(*k.stride()[:2]), _PAIR.pack(*v.stride()[:2]),
+        k.shape[0], slots.data_ptr(), handle)
+    if status:
+        _check(status, "cache_append_packed")
+
+
+def cache_attend_tree(cache: PagedCache, q, lengths, parents, counts=None, out=None, scale=None, window: int = 0,
+                      lse=None, workspace=None, stream=None):
+    """Attention of a tree of drafted tokens a sequence over its cached slots; returns ``out``.
+
+    The drafts' keys and values are in the cache already (``cache_append``):
+    draft t sits in slot lengths[b] - counts[b] + t.  It sees the slots before the drafts, its
+    ancestors' and its own.  ``q``: [seqs, drafts, q_heads, head_dim] of the cache's
+    type (bfloat16 for a float8_e4m3fn cache), at most 64 drafts; query head i reads key head
+    i // (q_heads // kv_heads).  ``parents``: int32 [seqs, drafts], an earlier draft
+    or -1 for those that follow the token before the drafts (a chain: t - 1).
+    ``counts``: int32 [seqs], how many drafts a sequence has (default: all); rows past them are left as they
+    were (in an ``out`` that is made here: undefined).  ``out``: like ``q``, apart from it.  ``scale``: of the dot
+    products, 1 / sqrt(head_dim) by default.  ``window``: how many tokens a draft sees,
+    itself, its nearest ancestors and then the newest before the drafts (0: all).
+    ``lse``: float32 [seqs, drafts, q_heads] to receive log sum exp.
+    ``workspace``: at least ``cache.tree_workspace_bytes()`` bytes; calls that may overlap need one each.
+    """
+    shape = q.shape
+    if len(shape) != 4:
+        raise ValueError("q is [seqs, drafts, q_heads, head_dim]")
+    device, (n_seqs, drafts, n_q, _) = cache.device, shape
+    _tensor(q, "q", cache.io_dtype, (cache.n_seqs, drafts, n_q, cache.head_dim), device)
+    if q.requires_grad:
+        _no_gradient()
+    _tensor(lengths, "lengths", _I32, cache._seqs, device)
+    _tensor(parents, "parents", _I32, (n_seqs, drafts), device)
+    if counts is not None:
+        _tensor(counts, "counts", _I32, cache._seqs, device)
+    if lse is not None:
+        _tensor(lse, "lse", _F32, (n_seqs, drafts, n_q), device)
+    if out is not None:
+        _tensor(out, "out", q.dtype, shape, device)
+    if workspace is not None and (workspace.device != device or not workspace.is_contiguous()):
+        raise ValueError("the workspace must be contiguous and on the cache's device")
+    if stream is not None:
+        with _on(stream) as handle:
+            return _attend_tree(cache, q, lengths, parents, counts, out, scale, window, lse, workspace, handle)
+    return _attend_tree(cache, q, lengths, parents, counts, out, scale, window, lse, workspace, _CURRENT(cache._index))
+
+
+def _attend_tree(cache, q, lengths, parents, counts, out, scale, window, lse, workspace, handle):
+    if _DEVICE() != cache._index:
+        _elsewhere(cache)
+    n, t, h, d = q.shape
+    if out is None:
+        out = cache._empty((n, t, h, d), (t * h * d, h * d, d, 1), q.dtype)
+    if workspace is None:
+        workspace = cache._empty((cache.tree_workspace_bytes(),), (1,), _BYTES)
+    l0 = l1 = logs = 0
+    if lse is not None:
+        logs, (l0, l1, _) = lse.data_ptr(), lse.stride()
+    a = _TREE.pack(q.data_ptr(), out.data_ptr(), _TYPES[q.dtype], h, t, window if window < 0x7fffffff else 0x7fffffff,
+                   *q.stride()[:3], *out.stride()[:3], lengths.data_ptr(), 0 if counts is None else counts.data_ptr(),
+                   parents.data_ptr(), parents.stride(0), cache.scale if scale is None else scale, logs, l0, l1,
+                   workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    status = _lib.lib().lc_cache_attend_tree(cache._ref, a, handle)
+    if status:
+        _check(status, "cache_attend_tree")
+    return out
+
+
+def cache_accept(cache: PagedCache, lengths, counts, path, new_lengths=None, stream=None):
+    """Keeps the accepted drafts of each sequence; returns the new lengths.
+
+    ``path``: int32 [seqs, most], at most 64 columns: a sequence's accepted drafts in rising order, ended by -1.
+    The i-th of them moves from slot lengths[b] - counts[b] + path[b, i] to slot
+    lengths[b] - counts[b] + i.  ``counts``: int32 [seqs], how many drafts a sequence
+    has (None: as many as ``path`` has columns).  ``new_lengths``: an int32 [seqs] tensor to receive lengths -
+    counts + the accepted ones, apart from the inputs.  A path that does not rise, or
+    leaves the drafts, ends there and sets the device error word.  The pages that hold
+    the drafts must not be shared with another sequence.
+    """
+    device, seqs = cache.device, cache._seqs
+    _tensor(lengths, "lengths", _I32, seqs, device)
+    if counts is not None:
+        _tensor(counts, "counts", _I32, seqs, device)
+    if path.dim() != 2:
+        raise ValueError("path is [seqs, most]")
+    _tensor(path, "path", _I32, (cache.n_seqs, path.shape[1]), device)
+    if new_lengths is not None:
+        _tensor(new_lengths, "new_lengths", _I32, seqs, device)
+    if stream is not None:
+        with _on(stream) as handle:
+            return _accept(cache, lengths, counts, path, new_lengths, handle)
+    return _accept(cache, lengths, counts, path, new_lengths, _CURRENT(cache._index))
+
+
+def _accept(cache, lengths, counts, path, new_lengths, handle):
+    if _DEVICE() != cache._index:
+        _elsewhere(cache)
+    if new_lengths is None:
+        new_lengths = cache._empty(cache._seqs, (1,), _I32)
+    status = _lib.lib().lc_cache_accept(cache._ref, lengths.data_ptr(), None if counts is None else counts.data_ptr(),
+                                        path.data_ptr(), path.stride(0), path.shape[1], new_lengths.data_ptr(), handle)
+    if status:
+        _check(status, "cache_accept")
+    return new_lengths
+
+
+class Reservation(NamedTuple):
+    """What ``cache_reserve`` returns."""
+    table: object      # int32 [seqs, pages_per_seq]
+    lengths: object    # int32 [seqs]: lengths with the new tokens of the sequences that are served
+    starts: object     # int32 [seqs + 1]: where each sequence's tokens begin among the packed ones
+    slots: object      # int64 [max_tokens]: page * page_size + row of every packed token, -1 past the last
+    positions: object  # int32 [max_tokens]: its place in its sequence
+    seqs: object       # int32 [max_tokens]: its sequence
+    n_free: object     # int32 [1]: pages left on the stack
+
+
+def cache_reserve(page_table, lengths, counts, free, n_free, page_size: int, max_tokens: int, new_table=None,
+                  stream=None):
+    """Makes a page table hold the pages of lengths + counts tokens a sequence; returns a ``Reservation``.
+
+    ``page_table``: int32 [seqs, pages_per_seq], each row a sequence's pages and then
+    -1; changed in place, or written to ``new_table`` where that is given.
+    ``lengths``, ``counts``: int32 [seqs], tokens that a sequence has, and new
+    ones.  ``free``, ``n_free``: int32 [any] and [1], a stack of free pages and how many it has;
+    the stack is changed in place, its new height returned.  Pages past those that a sequence wants (one that
+    has ended has length and count 0) go on the stack, then what is missing comes off
+    its top, in the sequences' order.  ``max_tokens``: the size of the packed lists.  A
+    sequence whose pages do not last, whose tokens pass the table's columns or the
+    lists gets none, keeps its pages, and the device error word is set; those behind it
+    that need no pages are served all the same.  At most 4096 sequences.
+    """
+    _types()
+    device, shape = page_table.device, page_table.shape
+    if page_table.dim() != 2 or not page_table.is_cuda:
+        raise ValueError("the page table is int32 [seqs, pages_per_seq] on a CUDA device (there is no CPU path)")
+    _tensor(page_table, "page_table", _I32, shape, device)
+    _tensor(lengths, "lengths", _I32, shape[:1], device)
+    _tensor(counts, "counts", _I32, shape[:1], device)
+    if free.dim() != 1:
+        raise ValueError("free is int32 [any]")
+    _tensor(free, "free", _I32, free.shape, device)
+    _tensor(n_free, "n_free", _I32, (1,), device)
+    if new_table is not None:
+        _tensor(new_table, "new_table", _I32, shape, device)
+    page_size, max_tokens = int(page_size), int(max_tokens)
+    if _DEVICE() != device.index:
+        raise ValueError("the page table is on %s, the current device is cuda:%d" % (device, _DEVICE()))
+    if stream is not None:
+        with _on(stream) as handle:
+            return _reserve(page_table, lengths, counts, free, n_free, page_size, max_tokens, new_table, handle)
+    return _reserve(page_table, lengths, counts, free, n_free, page_size, max_tokens, new_table, _CURRENT(device.index))
+
+
+def _reserve(page_table, lengths, counts, free, n_free, page_size, max_tokens, new_table, handle):
+    n, per = page_table.shape
+    tokens = max(max_tokens, 0)
+    empty = _empty()
+    if new_table is None:
+        new_table = page_table
+    new_lengths, starts = empty((n,), (1,), _I32), empty((n + 1,), (1,), _I32)
+    slots, positions, seqs = empty((tokens,), (1,), _I64), empty((tokens,), (1,), _I32), empty((tokens,), (1,), _I32)
+    new_n_free = empty((1,), (1,), _I32)
+    a = _RESERVATION.pack(page_table.data_ptr(), new_table.data_ptr(), page_table.stride(0), new_table.stride(0),
+                          lengths.data_ptr(), counts.data_ptr(), free.data_ptr(), n_free.data_ptr(),
+                          new_n_free.data_ptr(), new_lengths.data_ptr(), starts.data_ptr(), slots.data_ptr(),
+                          positions.data_ptr(), seqs.data_ptr(), free.shape[0], n, per, page_size, max_tokens)
+    status = _lib.lib().lc_cache_reserve(a, handle)
+    if status:
+        _check(status, "cache_reserve")
+    return Reservation(new_table, new_lengths, starts, slots, positions, seqs, new_n_free)
 
 
 def cache_evict(cache: PagedCache, lengths, scores, budget: int, recent: int = 0, new_scores=None, kept=None,

@@ -188,7 +188,8 @@ extern "C" int lc_last_device_error(lc_stream_t stream, uint64_t *detail) {
         lc::take_error_warp2,       lc::take_error_warp4,      lc::take_error_warp8,    lc::take_error_warp16,
         lc::take_error_append,      lc::take_error_evict,      lc::take_error_attend,   lc::take_error_attend_bf16,
         lc::take_error_attend_f16,  lc::take_error_attend_e4m3, lc::take_error_prompt_bf16,
-        lc::take_error_prompt_f16};
+        lc::take_error_prompt_f16,  lc::take_error_tree_bf16,  lc::take_error_tree_f16, lc::take_error_tree_e4m3,
+        lc::take_error_accept,      lc::take_error_reserve};
     constexpr int kWords = sizeof(take) / sizeof(take[0]);
     unsigned long long words[kWords] = {};
     for (int i = 0; i < kWords; ++i)

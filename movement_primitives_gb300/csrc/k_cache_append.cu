@@ -35,6 +35,7 @@ struct AppendArgs {
     int64_t kst[3], vst[3];  // elements: sequence, token, head
     const int32_t *counts, *lengths;
     int32_t *new_lengths;
+    const int64_t *slots;    // packed tokens: where they go (one "sequence" of n_new tokens)
     int32_t n_new;
     uint32_t items;          // n_seqs * n_new * head_div.d: a warp each
     FastDiv new_div, head_div;
@@ -142,6 +143,14 @@ __device__ __forceinline__ void put_row(int dim, uint8_t *dst, float *scale_at, 
     }
 }
 
+// Page of a slot of the pool, -1 when there is none.
+__device__ __forceinline__ int slot_page(const CacheArgs &c, int64_t slot, int *row) {
+    const int64_t page = slot < 0 ? -1 : slot / c.page;
+    *row = static_cast<int>(slot - page * c.page);
+    if (slot != -1 && (page < 0 || page >= c.n_pages)) report_error(LC_ERR_CACHE_INDEX, kClassAppend);
+    return page < c.n_pages ? static_cast<int>(page) : -1;
+}
+
 // A row by L lanes, so 32 / L rows at a time: keys' and values' of 16 / L
 // heads, U times.  VEC: every row on both sides starts on the boundary of eight
 // elements and holds whole eights.
@@ -151,7 +160,7 @@ __global__ void __launch_bounds__(kApThreads) k_cache_append(const __grid_consta
     const CacheArgs &c = a.c;
     start_after_prior();
     const int64_t thread = int64_t(blockIdx.x) * kApThreads + threadIdx.x;
-    if (thread < c.n_seqs) {
+    if (!a.slots && thread < c.n_seqs) {
         const int at = static_cast<int>(thread);
         const int n = cache_length(c, a.lengths, at, kClassAppend);
         const int m = a.counts ? min(max(a.counts[at], 0), a.n_new) : a.n_new;
@@ -164,8 +173,12 @@ __global__ void __launch_bounds__(kApThreads) k_cache_append(const __grid_consta
     const int first = static_cast<int>(item - bt * a.head_div.d) * U * P, h0 = first + (threadIdx.x & 31) / (2 * L);
     const int b = static_cast<int>(fast_div(bt, a.new_div));
     const int t = static_cast<int>(bt - static_cast<uint32_t>(b) * a.n_new);
-    const int count = a.counts ? a.counts[b] : a.n_new, n = min(max(a.lengths[b], 0), c.cap);
-    if (t >= min(count, c.cap - n)) return;
+    int n = 0;
+    if (!a.slots) {
+        const int count = a.counts ? a.counts[b] : a.n_new;
+        n = min(max(a.lengths[b], 0), c.cap);
+        if (t >= min(count, c.cap - n)) return;
+    }
 
     const int lane = threadIdx.x & (L - 1);
     const bool is_v = threadIdx.x & L;
@@ -192,7 +205,7 @@ __global__ void __launch_bounds__(kApThreads) k_cache_append(const __grid_consta
             }
         }
     int row;
-    const int page = cache_page(c, b, n + t, &row, kClassAppend);
+    const int page = a.slots ? slot_page(c, a.slots[t], &row) : cache_page(c, b, n + t, &row, kClassAppend);
     if (page < 0) return;
     const int64_t *st = is_v ? c.vst : c.kst, *sst = is_v ? c.vss : c.kss;
     uint8_t *dst = (is_v ? c.v : c.k) + row_offset(st, page, h0, row) * (Q ? 1 : 2);
@@ -298,4 +311,45 @@ extern "C" int lc_cache_append(const lc_paged_cache *cache, const void *k_new, c
     const int64_t tokens = ext[0] * n_new;
     if (!q8) return launch_append_as<0>(a, tokens, vec, cs);
     return type == LC_CACHE_BF16 ? launch_append_as<1>(a, tokens, vec, cs) : launch_append_as<2>(a, tokens, vec, cs);
+}
+
+extern "C" int lc_cache_append_packed(const lc_paged_cache *cache, const void *k_new, const void *v_new, int32_t type,
+                                      const int64_t k_stride[2], const int64_t v_stride[2], int32_t n_tokens,
+                                      const int64_t *slots, lc_stream_t stream) {
+    using namespace lc;
+    AppendArgs a{};
+    int st = check_cache(cache, true, &a.c);
+    if (st) return st;
+    if (n_tokens < 0) return LC_ERR_SHAPE;
+    if (type != LC_CACHE_BF16 && type != LC_CACHE_F16) return LC_ERR_TYPE;
+    const bool q8 = cache->type == LC_CACHE_E4M3;
+    if (!q8 && type != cache->type) return LC_ERR_TYPE;
+    if (n_tokens == 0 || cache->n_pages == 0) return LC_OK;
+    if (!k_new || !v_new || !k_stride || !v_stride || !slots) return LC_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new)) % 2 ||
+        reinterpret_cast<uintptr_t>(slots) % 8)
+        return LC_ERR_ALIGN;
+    const int64_t ext[2] = {n_tokens, cache->n_kv_heads};
+    st = check_reach(2, ext, k_stride, cache->head_dim);
+    if (!st) st = check_reach(2, ext, v_stride, cache->head_dim);
+    if (st) return st;
+    if (ext[0] * ext[1] > (int64_t(1) << 31) - 1) return LC_ERR_OVERFLOW;
+    a.k = static_cast<const uint16_t *>(k_new);
+    a.v = static_cast<const uint16_t *>(v_new);
+    for (int i = 0; i < 2; ++i) {
+        a.kst[i + 1] = k_stride[i];
+        a.vst[i + 1] = v_stride[i];
+    }
+    a.slots = slots;
+    a.n_new = n_tokens;
+    a.new_div = make_fastdiv(static_cast<uint32_t>(n_tokens));
+    const int64_t pool[3] = {cache->n_pages, cache->n_kv_heads, cache->page_size};
+    const int eb = cache_elem_bytes(cache->type);
+    const bool vec = cache->head_dim % 8 == 0 && rows_aligned(k_new, 2, ext, k_stride, 2, 16) &&
+                     rows_aligned(v_new, 2, ext, v_stride, 2, 16) &&
+                     rows_aligned(cache->k, 3, pool, cache->k_stride, eb, 8 * eb) &&
+                     rows_aligned(cache->v, 3, pool, cache->v_stride, eb, 8 * eb);
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    if (!q8) return launch_append_as<0>(a, n_tokens, vec, cs);
+    return type == LC_CACHE_BF16 ? launch_append_as<1>(a, n_tokens, vec, cs) : launch_append_as<2>(a, n_tokens, vec, cs);
 }

@@ -1,0 +1,101 @@
+// Attention of drafted trees over the cache: the checks, the workspace and the C
+// entry points (lc_cache_attend_tree; the kernels are tree_attend.cuh).
+#include <cmath>
+
+#include "tree_attend.cuh"
+
+namespace lc {
+
+int launch_tree_bf16(const TreeArgs &a, cudaStream_t cs);
+int launch_tree_f16(const TreeArgs &a, cudaStream_t cs);
+int launch_tree_e4m3(const TreeArgs &a, cudaStream_t cs);
+
+namespace {
+
+int64_t tree_workspace(const CacheArgs &c) {
+    const int64_t rows = int64_t(2) * kTrMostRuns * kTrRows;
+    return rows * ((c.dim + 63) / 64 * 64 * 4 + 8);
+}
+
+}  // namespace
+
+}  // namespace lc
+
+extern "C" int64_t lc_cache_attend_tree_workspace(const lc_paged_cache *cache) {
+    lc::CacheArgs c;
+    return lc::check_cache(cache, false, &c) ? -1 : lc::tree_workspace(c);
+}
+
+extern "C" int lc_cache_attend_tree(const lc_paged_cache *cache, const lc_cache_tree *q, lc_stream_t stream) {
+    using namespace lc;
+    TreeArgs a{};
+    int st = check_cache(cache, false, &a.c);
+    if (st) return st;
+    if (!q) return LC_ERR_NULL;
+    if (q->n_q_heads < 1 || q->n_q_heads % cache->n_kv_heads || q->window < 0 || q->n_drafts < 0 ||
+        q->n_drafts > LC_CACHE_MAX_DRAFTS || !std::isfinite(q->scale))
+        return LC_ERR_SHAPE;
+    if (q->type != (cache->type == LC_CACHE_E4M3 ? LC_CACHE_BF16 : cache->type)) return LC_ERR_TYPE;
+    if (cache->n_seqs == 0 || q->n_drafts == 0) return LC_OK;
+    if (!q->q || !q->out || !q->lengths || !q->parents) return LC_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(q->q) | reinterpret_cast<uintptr_t>(q->out)) % 2 ||
+        (reinterpret_cast<uintptr_t>(q->lengths) | reinterpret_cast<uintptr_t>(q->counts) |
+         reinterpret_cast<uintptr_t>(q->parents) | reinterpret_cast<uintptr_t>(q->lse)) % 4)
+        return LC_ERR_ALIGN;
+    const int64_t ext[3] = {cache->n_seqs, q->n_drafts, q->n_q_heads};
+    st = check_reach(3, ext, q->q_stride, cache->head_dim);
+    if (!st) st = check_reach(3, ext, q->out_stride, cache->head_dim);
+    if (!st) st = check_reach(1, ext, &q->parents_stride, q->n_drafts);
+    if (!st && q->lse) st = check_reach(2, ext, q->lse_stride, q->n_q_heads);
+    if (st) return st;
+    if (!rows_apart(3, ext, q->out_stride, cache->head_dim) || (q->lse && !rows_apart(2, ext, q->lse_stride, q->n_q_heads)))
+        return LC_ERR_NOT_INJECTIVE;
+    // parts of q's rows are read while others' output is written: out lies apart from them, range from range
+    int64_t q_top = 0, o_top = 0;
+    for (int i = 0; i < 3; ++i) {
+        q_top += (ext[i] - 1) * q->q_stride[i];
+        o_top += (ext[i] - 1) * q->out_stride[i];
+    }
+    const uintptr_t q0 = reinterpret_cast<uintptr_t>(q->q), o0 = reinterpret_cast<uintptr_t>(q->out);
+    if (q0 < o0 + 2 * (o_top + cache->head_dim) && o0 < q0 + 2 * (q_top + cache->head_dim)) return LC_ERR_OVERLAP;
+    a.group = q->n_q_heads / cache->n_kv_heads;
+    if (int64_t(q->n_drafts) * a.group > 1 << 24) return LC_ERR_OVERFLOW;
+    a.most_blocks = static_cast<int32_t>((int64_t(q->n_drafts) * a.group + kTrRows - 1) / kTrRows);
+    if (int64_t(cache->n_seqs) * cache->n_kv_heads > 0x1fffffff / a.most_blocks) return LC_ERR_OVERFLOW;
+    const int64_t need = tree_workspace(a.c);
+    if (!q->workspace) return LC_ERR_NULL;
+    if (need > q->workspace_bytes) return LC_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(q->workspace) % 256) return LC_ERR_ALIGN;
+    if (a.c.cap == 0) return LC_OK;  // no slots: no drafts
+    a.q = static_cast<const uint16_t *>(q->q);
+    a.out = static_cast<uint16_t *>(q->out);
+    a.lengths = q->lengths;
+    a.counts = q->counts;
+    a.parents = q->parents;
+    a.lse = q->lse;
+    for (int i = 0; i < 3; ++i) {
+        a.qst[i] = q->q_stride[i];
+        a.ost[i] = q->out_stride[i];
+    }
+    for (int i = 0; i < 2; ++i) a.lst[i] = q->lse_stride[i];
+    a.parents_stride = q->parents_stride;
+    a.drafts = q->n_drafts;
+    a.q_heads = q->n_q_heads;
+    a.group_div = make_fastdiv(static_cast<uint32_t>(a.group));
+    a.window = q->window;
+    // a scale of 0 is one too small to tell, so that unseen slots' -infinity stays what it is
+    a.scale2 = std::max(std::fabs(q->scale) * 1.4426950408889634f, 0x1p-100f);
+    a.negative = q->scale < 0.f;
+    const int eb = cache_elem_bytes(cache->type);
+    const int64_t pool[3] = {cache->n_pages, cache->n_kv_heads, cache->page_size};
+    a.vec = a.c.dim * eb % 16 == 0 && rows_aligned(cache->k, 3, pool, cache->k_stride, eb, 16) &&
+            rows_aligned(cache->v, 3, pool, cache->v_stride, eb, 16);
+    a.q_vec = a.c.dim % 8 == 0 && rows_aligned(q->q, 3, ext, q->q_stride, 2, 16);
+    a.out_vec = rows_aligned(q->out, 3, ext, q->out_stride, 2, 16);
+    a.part = static_cast<float *>(q->workspace);
+    a.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(q->workspace) +
+                                           int64_t(2) * kTrMostRuns * kTrRows * ((a.c.dim + 63) / 64 * 64 * 4));
+    a.limit_ns = wait_limit_ns();
+    const auto launch = cache->type == LC_CACHE_BF16 ? launch_tree_bf16 : cache->type == LC_CACHE_F16 ? launch_tree_f16 : launch_tree_e4m3;
+    return launch(a, reinterpret_cast<cudaStream_t>(stream));
+}

@@ -54,5 +54,10 @@ cudaError_t take_error_attend_f16(unsigned long long *v);
 cudaError_t take_error_attend_e4m3(unsigned long long *v);
 cudaError_t take_error_prompt_bf16(unsigned long long *v);
 cudaError_t take_error_prompt_f16(unsigned long long *v);
+cudaError_t take_error_tree_bf16(unsigned long long *v);
+cudaError_t take_error_tree_f16(unsigned long long *v);
+cudaError_t take_error_tree_e4m3(unsigned long long *v);
+cudaError_t take_error_accept(unsigned long long *v);
+cudaError_t take_error_reserve(unsigned long long *v);
 
 }  // namespace lc
