@@ -85,7 +85,8 @@ struct PromptShape {
 struct PromptShared {
     uint64_t ring_full[10], ring_empty[10];
     uint64_t q_full[2], q_empty[2];
-    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t s_full[2], p_full[2];
+    uint64_t o_full[2];              // of a tile's item; with one tile of every other step
     uint64_t item_full[kPrItems], item_empty[kPrItems];
     uint64_t drain;
     PromptItem item[kPrItems];
@@ -312,19 +313,25 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
                 if (lane == 0) sh.bad_any[turn][warp & 3] = 0;
                 __syncwarp();
             }
+            auto wait_values = [&](int j) {
+                for (int c = 0; c < S::SPT; ++c) {
+                    const uint32_t at = (p0 + value_place<TILES>(j, it.steps)) * S::SPT + c;
+                    wait(sh.ring_full[at % S::SLOTS], at / S::SLOTS);
+                }
+            };
             for (int j = 0; j < it.steps; ++j) {
                 const int key0 = (it.first + j) * kPrKeys;
+                // a barrier must not be two phases behind what is waited for: with two tiles what a slot held before was
+                // keys whose product this thread has seen, with one it may be the values before these, so all are waited for
+                if (TILES == 1) wait_values(j);
                 if (t == 0 && (key0 < item_lo || key0 + kPrKeys > item_hi)) {
                     // values that some row does not see are multiplied by weights of 0 there: what is not finite
                     // becomes 0, and is added at the end where it is seen
                     const uint32_t p = p0 + value_place<TILES>(j, it.steps);
+                    if (TILES == 2) wait_values(j);
                     bool found = false;
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
-                        if (c % S::CPS == 0) {
-                            const uint32_t at = p * S::SPT + c / S::CPS;
-                            wait(sh.ring_full[at % S::SLOTS], at / S::SLOTS);
-                        }
                         uint8_t *v = raw + (ring_s - ptx::smem_addr(raw)) +
                                      (p * S::SPT + c / S::CPS) % S::SLOTS * S::SLOT + c % S::CPS * kPrChunk + row * 128;
 #pragma unroll
@@ -392,7 +399,7 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
                     }
                     if (j > 0) {
                         if (TILES == 1) {  // the product before this step's; with two tiles S came after it
-                            if (!__all_sync(0xffffffffu, wait(sh.o_full[0], n_s - 2))) break;
+                            if (!__all_sync(0xffffffffu, wait(sh.o_full[n_s & 1], n_s - 2 >> 1))) break;
                             tc::fence_after();
                         }
                         const uint32_t o_at = lanes + S::O + t * NC * 64;
@@ -432,7 +439,8 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
             if (!ok) break;
             // output
             if (it.steps) {
-                if (!__all_sync(0xffffffffu, wait(sh.o_full[t], TILES == 2 ? n_o++ : n_s - 1))) break;
+                if (!__all_sync(0xffffffffu, TILES == 2 ? wait(sh.o_full[t], n_o++) : wait(sh.o_full[n_s - 1 & 1], n_s - 1 >> 1)))
+                    break;
                 tc::fence_after();
             }
             const int64_t at = it.q0 + mine;
@@ -678,7 +686,7 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
                         if (!ok) break;
                         second_product(0, buf, pv, j > 0);
                         free_tile(pv);
-                        tc::commit(bar(sh.o_full[0]));
+                        tc::commit(bar(sh.o_full[buf]));
                         if (j + 2 < it.steps) {
                             const uint32_t pk = p0 + key_place<1>(j + 2);
                             wait_tile(pk);

@@ -150,7 +150,7 @@ struct TreeShape {
 struct TreeShared {
     uint64_t ring_full[12], ring_empty[12];
     uint64_t q_full, q_empty;
-    uint64_t s_full[2], p_full[2], o_full;
+    uint64_t s_full[2], p_full[2], o_full[2];  // of every other step
     uint64_t item_full[kTrItems], item_empty[kTrItems];
     uint64_t drain;
     uint32_t tmem;
@@ -293,8 +293,8 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(bar(sh.s_full[i]), 1);
             ptx::mbar_init(bar(sh.p_full[i]), 4);
+            ptx::mbar_init(bar(sh.o_full[i]), 1);
         }
-        ptx::mbar_init(bar(sh.o_full), 1);
         for (int i = 0; i < kTrItems; ++i) {
             ptx::mbar_init(bar(sh.item_full[i]), 1);
             ptx::mbar_init(bar(sh.item_empty[i]), 4 + kTrLoaders + 1);
@@ -699,7 +699,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                             tc::mma_ts(tmem + S::O, tmem + buf * 128 + k / 2 * 32 + half * 16 + (k & 1) * 8,
                                        tc::smem_desc(tile + k * 2048, S::CHUNK), pv, j > 0 || half > 0 || k > 0);
                     tc::commit(bar(sh.ring_empty[p % S::SLOTS]));
-                    tc::commit(bar(sh.o_full));
+                    tc::commit(bar(sh.o_full[buf]));
                     if (j + 2 < steps) first_product(j + 2);
                 }
                 if (!ok) break;
@@ -817,7 +817,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                             }
                         }
                         if (j > 0) {
-                            if (!wait_warp(sh.o_full, n_s - 2)) break;
+                            if (!wait_warp(sh.o_full[n_s & 1], n_s - 2 >> 1)) break;
                             tc::fence_after();
                             for (int c = 0; c < (a.c.dim + 31) / 32; ++c) {
                                 uint32_t o[32];
@@ -867,7 +867,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
             }
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            if (!wait_warp(sh.o_full, n_s - 1)) break;
+            if (!wait_warp(sh.o_full[n_s - 1 & 1], n_s - 1 >> 1)) break;
             if (some) {
                 tc::fence_after();
                 const int hq = it.head * a.group + g;
