@@ -23,6 +23,11 @@ __device__ __forceinline__ void report_error(uint32_t status, uint32_t kernel_cl
     atomicCAS(&g_error_word, 0ull, v);
 }
 
+// The same out of line, for kernels whose instructions are to be few.
+static __device__ __noinline__ void note_error(uint32_t status, uint32_t kernel_class) {
+    report_error(status, kernel_class);
+}
+
 // Host side: read this module's error word, clearing it when set.
 static inline cudaError_t take_module_error(unsigned long long *v) {
     cudaError_t e = cudaMemcpyFromSymbol(v, g_error_word, sizeof(*v));

@@ -271,6 +271,12 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
         }
         return ok;
     };
+    // a warp's wait: one lane polls, for the others' polls take turns with what else the shared memory does
+    auto wait_warp = [&](const uint64_t &b, uint32_t n) {
+        if (lane == 0) wait(b, n);
+        ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0);
+        return ok;
+    };
     auto arrive = [&](const uint64_t &b) {
         asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar(b)) : "memory");
     };
@@ -287,7 +293,7 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
         const int token = static_cast<int>(fast_div(row, a.heads_div)), head = row - token * a.heads_tile;
         uint32_t n_s = 0, n_o = 0, pos = 0;
         for (uint32_t i = 0; ok; ++i) {
-            if (!__all_sync(0xffffffffu, wait(sh.item_full[i % kPrItems], i / kPrItems))) break;
+            if (!wait_warp(sh.item_full[i % kPrItems], i / kPrItems)) break;
             const PromptItem it = sh.item[i % kPrItems];
             __syncwarp();
             if (lane == 0) arrive(sh.item_empty[i % kPrItems]);
@@ -316,7 +322,7 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
             auto wait_values = [&](int j) {
                 for (int c = 0; c < S::SPT; ++c) {
                     const uint32_t at = (p0 + value_place<TILES>(j, it.steps)) * S::SPT + c;
-                    wait(sh.ring_full[at % S::SLOTS], at / S::SLOTS);
+                    wait_warp(sh.ring_full[at % S::SLOTS], at / S::SLOTS);
                 }
             };
             for (int j = 0; j < it.steps; ++j) {
@@ -366,7 +372,7 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
                 }
                 const int buf = TILES == 2 ? t : n_s & 1;
                 const uint32_t s_at = lanes + buf * 128;
-                if (!__all_sync(0xffffffffu, wait(sh.s_full[buf], TILES == 2 ? n_s : n_s >> 1))) break;
+                if (!wait_warp(sh.s_full[buf], TILES == 2 ? n_s : n_s >> 1)) break;
                 ++n_s;
                 tc::fence_after();
                 uint32_t x[4][32];
@@ -399,7 +405,7 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
                     }
                     if (j > 0) {
                         if (TILES == 1) {  // the product before this step's; with two tiles S came after it
-                            if (!__all_sync(0xffffffffu, wait(sh.o_full[n_s & 1], n_s - 2 >> 1))) break;
+                            if (!wait_warp(sh.o_full[n_s & 1], n_s - 2 >> 1)) break;
                             tc::fence_after();
                         }
                         const uint32_t o_at = lanes + S::O + t * NC * 64;
@@ -439,8 +445,7 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
             if (!ok) break;
             // output
             if (it.steps) {
-                if (!__all_sync(0xffffffffu, TILES == 2 ? wait(sh.o_full[t], n_o++) : wait(sh.o_full[n_s - 1 & 1], n_s - 1 >> 1)))
-                    break;
+                if (!(TILES == 2 ? wait_warp(sh.o_full[t], n_o++) : wait_warp(sh.o_full[n_s - 1 & 1], n_s - 1 >> 1))) break;
                 tc::fence_after();
             }
             const int64_t at = it.q0 + mine;
@@ -514,9 +519,7 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
             PromptItem it{};
             prompt_item<TILES>(a, at, &it);
             const int s = i % kPrItems;
-            if (i >= kPrItems) wait(sh.item_empty[s], i / kPrItems - 1);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
+            if (i >= kPrItems && !wait_warp(sh.item_empty[s], i / kPrItems - 1)) break;
             if (lane == 0) {
                 sh.item[s] = it;
                 arrive(sh.item_full[s]);

@@ -76,10 +76,12 @@ struct TreeSeq {
 template <int KEYS>
 __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs &a, int b) {
     TreeSeq s;
-    s.n = cache_length(a.c, a.lengths, b, kClassTree);
+    const int length = a.lengths[b];
+    s.n = min(max(length, 0), a.c.cap);
+    if (s.n != length) note_error(LC_ERR_CACHE_INDEX, kClassTree);
     const int want = a.counts ? a.counts[b] : min(a.drafts, s.n);
     s.count = min(max(want, 0), min(a.drafts, s.n));
-    if (s.count != want) report_error(LC_ERR_CACHE_INDEX, kClassTree);
+    if (s.count != want) note_error(LC_ERR_CACHE_INDEX, kClassTree);
     s.begin = a.window ? max(s.n - s.count + 1 - a.window, 0) : 0;
     s.blocks = (s.count * a.group + kTrRows - 1) / kTrRows;
     s.steps = s.count ? (s.n - s.begin + KEYS - 1) / KEYS : 0;
@@ -91,6 +93,7 @@ template <int KEYS>
 __device__ __forceinline__ int64_t tree_steps(const TreeArgs &a, int upto, int64_t *before) {
     const int lane = threadIdx.x & 31;
     int64_t all = 0, some = 0;
+#pragma unroll 1
     for (int b = lane; b < a.c.n_seqs; b += 32) {
         const TreeSeq s = tree_seq<KEYS>(a, b);
         const int64_t w = int64_t(s.steps) * s.blocks * a.c.heads;
@@ -139,7 +142,8 @@ struct TreeShape {
     static constexpr int RAW_TILE = TILE / 2;
     static constexpr int SHARED = 9216 + (Q8 ? kTrAux * KEYS * 8 : 0);  // the block of barriers and items, and 1024 for alignment
     static constexpr int FIT = (232448 - SHARED - Q - RAW * RAW_TILE) / TILE;
-    static constexpr int SLOTS = FIT < 12 ? FIT : 12;
+    // (what kTrAux holds is read before tiles this far on are started)
+    static constexpr int SLOTS = Q8 ? (FIT < 6 ? FIT : 6) : (FIT < 12 ? FIT : 12);
     static constexpr int LAG = Q8 ? RAW - 1 : SLOTS / 2;   // tiles under way
     static constexpr int SMEM = Q + RAW * RAW_TILE + SLOTS * TILE + SHARED;
     static constexpr int THREADS = 32 * (4 + kTrLoaders + 2);
@@ -205,17 +209,23 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t src) {
     return v;
 }
 
+// The kernel's warps go through different code at the same time: what is rare, or
+// may be a loop, is kept out of line or rolled, since instructions that do not fit the
+// cache bounded the first form (195 KB of them, 20 cycles an instruction).
+
 // 16 bytes of a row, element by element where they may not be read at once.
 template <int EB>
-__device__ __forceinline__ uint4 tree_piece(const uint8_t *row, int col, int dim, bool vec) {
-    if (vec) return *reinterpret_cast<const uint4 *>(row + col * EB);
-    uint32_t w[4] = {0, 0, 0, 0};
+__device__ __noinline__ uint4 tree_piece(const uint8_t *row, int col, int dim) {
+    uint64_t w[2] = {0, 0};
+#pragma unroll 1
     for (int i = 0; i < 16 / EB; ++i)
         if (col + i < dim) {
-            const uint32_t v = EB == 2 ? *reinterpret_cast<const uint16_t *>(row + (col + i) * 2) : row[col + i];
-            w[i * EB / 4] |= v << (i * EB % 4 * 8);
+            const uint64_t v = EB == 2 ? *reinterpret_cast<const uint16_t *>(row + (col + i) * 2) : row[col + i];
+            if (i * EB < 8) w[0] |= v << i * EB * 8;
+            else w[1] |= v << (i * EB - 8) * 8;
         }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    return make_uint4(static_cast<uint32_t>(w[0]), static_cast<uint32_t>(w[0] >> 32), static_cast<uint32_t>(w[1]),
+                      static_cast<uint32_t>(w[1] >> 32));
 }
 
 // The drafts that each draft of a sequence sees, and from where on it sees what was before them; by a warp, two drafts a lane.
@@ -232,10 +242,10 @@ __device__ __forceinline__ void tree_kin(const TreeArgs &a, TreeItem &it) {
         if (t < it.count) {
             const int p = parents[t];
             if (p >= -1 && p < t) up[i] = p;
-            else report_error(LC_ERR_CACHE_INDEX, kClassTree);
+            else note_error(LC_ERR_CACHE_INDEX, kClassTree);
         }
     }
-#pragma unroll
+#pragma unroll 1
     for (int round = 0; round < 6; ++round) {
         uint64_t k[2];
         int u[2];
@@ -261,6 +271,25 @@ __device__ __forceinline__ void tree_kin(const TreeArgs &a, TreeItem &it) {
             for (int d = depth; d > a.window; --d) kin[i] &= kin[i] - 1;
         it.kin[t] = kin[i];
         it.from[t] = a.window ? min(max(before + depth - a.window, 0), before) : 0;
+    }
+}
+
+// The values of a slot, and of an element 0 or what is not finite.
+template <int EB>
+__device__ __noinline__ const uint8_t *tree_value(const TreeArgs &a, int b, int head, int slot) {
+    int r = 0;
+    const int page = cache_page(a.c, b, slot, &r, kClassTree);
+    return page < 0 ? nullptr : a.c.v + row_offset(a.c.vst, page, head, r) * EB;
+}
+template <int KV>
+__device__ __noinline__ float tree_unusual(const uint8_t *v, int e) {
+    if constexpr (KV == LC_CACHE_E4M3) {
+        return (v[e] & 0x7f) == 0x7f ? NAN : 0.f;
+    } else {
+        const uint32_t u = reinterpret_cast<const uint16_t *>(v)[e];
+        constexpr uint32_t kExp = KV == LC_CACHE_F16 ? 0x7c00u : 0x7f80u;
+        if ((u & kExp) != kExp) return 0.f;
+        return KV == LC_CACHE_F16 ? __half2float(__ushort_as_half(u)) : __uint_as_float(u << 16);
     }
 }
 
@@ -310,15 +339,22 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
 
     bool ok = true;  // no wait of this thread has run out
     auto wait = [&](const uint64_t &b, uint32_t n) {  // for phase n (counted from 0)
-        if (ok && !ptx::mbar_wait_bounded(bar(b), n & 1, a.limit_ns)) {
+        if (ok && !ptx::mbar_wait_step(bar(b), n & 1, a.limit_ns)) {
             ok = false;
-            report_error(LC_ERR_TIMEOUT, kClassTree);
+            note_error(LC_ERR_TIMEOUT, kClassTree);
         }
         return ok;
     };
+    // a warp's wait: one lane polls, for the others' polls take turns with what else the shared memory does
     auto wait_warp = [&](const uint64_t &b, uint32_t n) {
-        ok = __all_sync(0xffffffffu, wait(b, n));
+        if (lane == 0) wait(b, n);
+        ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0);
         return ok;
+    };
+    auto done_warp = [&](const uint64_t &b, uint32_t n) {
+        int d = 0;
+        if (lane == 0) d = ptx::mbar_try_wait(bar(b), n & 1);
+        return __shfl_sync(0xffffffffu, d, 0) != 0;
     };
     auto arrive = [&](const uint64_t &b) {
         asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar(b)) : "memory");
@@ -350,6 +386,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
             arrive_warp(sh.item_full[s]);
             ++i;
         };
+#pragma unroll 1
         for (int b0 = 0; b0 < a.c.n_seqs && from < to && ok; b0 += 32) {
             TreeSeq s{};
             if (b0 + lane < a.c.n_seqs) s = tree_seq<KEYS>(a, b0 + lane);
@@ -457,7 +494,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
             }
             if constexpr (Q8) {
                 if (given >= S::SLOTS && !wait_warp(sh.ring_empty[slot], given / S::SLOTS - 1)) return;
-#pragma unroll
+#pragma unroll 2
                 for (int i = 0; i < ITER; ++i) {
                     int row, col;
                     piece_of(i, &row, &col);
@@ -495,10 +532,15 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                 ++back;
             }
         };
-        auto flush = [&]() {
-            ptx::cp_async_wait<0>();
-            while (given < issued && ok) give();
+        // gives the tiles that have landed, or waits for all of them
+        auto settle = [&](bool all) {
+            if (all) ptx::cp_async_wait<0>();
+            else ptx::cp_async_wait<S::LAG>();
+            const uint32_t to = all ? issued : issued - S::LAG;
+#pragma unroll 1
+            while (given < to && ok) give();
         };
+        auto flush = [&] { settle(true); };
         // starts a tile of pool w from the rows at `from`
         auto start = [&](int w, int64_t from, int32_t where, uint32_t signs) {
             const uint32_t slot = issued % S::SLOTS;
@@ -514,7 +556,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                 const bool real = r >= 0 && col < dim;
                 const uint8_t *src = pool[w] + (real ? r * EB : 0);
                 if (a.vec) tr_copy16(dst, src + (real ? col * EB : 0), real);
-                else st_shared16(dst, real ? tree_piece<EB>(src, col, dim, false) : make_uint4(0, 0, 0, 0));
+                else st_shared16(dst, real ? tree_piece<EB>(src, col, dim) : make_uint4(0, 0, 0, 0));
             }
             ptx::cp_async_commit();
 #pragma unroll
@@ -524,14 +566,11 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                     flip[i] = signs;
                 }
             ++issued;
-            if (issued - given > S::LAG) {
-                ptx::cp_async_wait<S::LAG>();
-                give();
-            }
+            if (issued - given > S::LAG) settle(false);
         };
         uint32_t step_no = 0;  // steps of all pieces
         for (uint32_t i = 0; ok; ++i) {
-            if (!__all_sync(0xffffffffu, ptx::mbar_try_wait(bar(sh.item_full[i % kTrItems]), i / kTrItems & 1))) flush();
+            if (!done_warp(sh.item_full[i % kTrItems], i / kTrItems)) flush();
             if (!wait_warp(sh.item_full[i % kTrItems], i / kTrItems)) break;
             TreeItem &it = sh.item[i % kTrItems];
             if (it.end) break;
@@ -544,61 +583,22 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                 const int slot = slot_first + j * KEYS + lw * RW + lane;
                 *row = 0;
                 if (lane >= RW || j >= steps || slot >= n) return -1;
-                return cache_page(a.c, b, slot, row, kClassTree);
+                const int at = static_cast<int>(fast_div(slot, a.c.page_div));
+                *row = slot - at * a.c.page;
+                const int id = a.c.table[b * a.c.table_stride + at];
+                if (id >= 0 && id < a.c.n_pages) return id;
+                note_error(LC_ERR_CACHE_INDEX, kClassTree);
+                return -1;
             };
             int row = 0, page = page_id(0, &row);
-            auto keys = [&](int j) {
-                const int64_t k_off = page >= 0 ? row_offset(a.c.kst, page, head, row) : -1;
-                v_off = v_next;
-                signs = signs_next;
-                v_next = page >= 0 ? row_offset(a.c.vst, page, head, row) : -1;
-                const int x = step_no % kTrAux;
-                const uint32_t there = __ballot_sync(0xffffffffu, page >= 0) & ((1u << RW) - 1);
-                if constexpr (RW == 16) {
-                    if (lane == 0) reinterpret_cast<uint16_t *>(sh.there[x])[lw] = static_cast<uint16_t>(there);
-                } else {
-                    if (lane == 0) reinterpret_cast<uint8_t *>(sh.there[x])[lw] = static_cast<uint8_t>(there);
+            auto load_q = [&] {
+                if (n_q && !done_warp(sh.q_empty, n_q - 1)) {
+                    flush();  // its last keys among them
+                    if (!wait_warp(sh.q_empty, n_q - 1)) return;
                 }
-                if constexpr (Q8) {
-                    float ks = 0.f, vs = 0.f;
-                    if (page >= 0) {
-                        ks = a.c.ks[row_offset(a.c.kss, page, head, row)];
-                        vs = a.c.vs[row_offset(a.c.vss, page, head, row)];
-                    }
-                    signs_next = __ballot_sync(0xffffffffu, vs < 0.f);
-                    if (lane < RW) {
-                        float lv;
-                        asm("lg2.approx.f32 %0, %1;" : "=f"(lv) : "f"(fabsf(vs)));
-                        aux[(x * 2) * KEYS + lw * RW + lane] = ks;
-                        aux[(x * 2 + 1) * KEYS + lw * RW + lane] = lv;
-                    }
-                }
-                int row2 = 0;
-                const int page2 = page_id(j + 1, &row2);
-                start(0, k_off, -1, 0);
-                page = page2;
-                row = row2;
-                ++step_no;
-            };
-            auto values = [&](int j, int64_t from, uint32_t sign) {
-                int32_t where = -1;
-                const int slot0 = slot_first + j * KEYS;
-                if (masked(it, slot0) && entry < kTrMasked) {
-                    where = static_cast<int>(i % kTrItems) * kTrMasked + entry;
-                    if (lw == 0 && lane == 0) it.bad_step[entry] = slot0;
-                    ++entry;
-                    if (lw == 0 && lane == 0) it.bad_steps = entry;
-                }
-                start(1, from, where, sign);
-            };
-            keys(0);
-            // the rows of q: a row a warp at a time, eight on the way
-            if (n_q && !__all_sync(0xffffffffu, ptx::mbar_try_wait(bar(sh.q_empty), (n_q - 1) & 1))) {
-                flush();  // its last keys among them
-                if (!wait_warp(sh.q_empty, n_q - 1)) break;
-            }
-            {
+                // the rows of q: a row a warp at a time, eight on the way
                 constexpr int PQ = NC * 8;
+#pragma unroll 1
                 for (int r0 = 0; r0 < kTrRows / kTrLoaders; r0 += 8) {
                     uint4 x[8];
 #pragma unroll
@@ -606,10 +606,11 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                         const int at = it.row0 + lw * (kTrRows / kTrLoaders) + r0 + r;
                         const int t = static_cast<int>(fast_div(at, a.group_div)), g = at - t * a.group;
                         x[r] = make_uint4(0, 0, 0, 0);
-                        if (t < it.count && lane * 8 < dim)
-                            x[r] = tree_piece<2>(reinterpret_cast<const uint8_t *>(a.q + b * a.qst[0] + t * a.qst[1] +
-                                                                                   (int64_t(head) * a.group + g) * a.qst[2]),
-                                                 lane * 8, dim, a.q_vec);
+                        if (t < it.count && lane * 8 < dim) {
+                            const uint16_t *from = a.q + b * a.qst[0] + t * a.qst[1] + (int64_t(head) * a.group + g) * a.qst[2];
+                            if (a.q_vec) x[r] = *reinterpret_cast<const uint4 *>(from + lane * 8);
+                            else x[r] = tree_piece<2>(reinterpret_cast<const uint8_t *>(from), lane * 8, dim);
+                        }
                     }
 #pragma unroll
                     for (int r = 0; r < 8; ++r) {
@@ -639,16 +640,62 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                 tc::fence_async_smem();
                 arrive_warp(sh.q_full);
                 ++n_q;
+            };
+            // tiles in their order: K0 K1 V0 K2 V1 ...
+#pragma unroll 1
+            for (int p = 0; p < 2 * steps && ok; ++p) {
+                const bool is_k = p == 0 || (p & 1 && p < 2 * steps - 1);
+                const int j = is_k ? (p + 1) / 2 : p == 2 * steps - 1 ? steps - 1 : p / 2 - 1;
+                int64_t from;
+                int32_t where = -1;
+                uint32_t sign = 0;
+                if (is_k) {
+                    from = page >= 0 ? row_offset(a.c.kst, page, head, row) : -1;
+                    v_off = v_next;
+                    signs = signs_next;
+                    v_next = page >= 0 ? row_offset(a.c.vst, page, head, row) : -1;
+                    const int x = step_no % kTrAux;
+                    const uint32_t there = __ballot_sync(0xffffffffu, page >= 0) & ((1u << RW) - 1);
+                    if (lane == 0) {
+                        if constexpr (RW == 16) reinterpret_cast<uint16_t *>(sh.there[x])[lw] = static_cast<uint16_t>(there);
+                        else reinterpret_cast<uint8_t *>(sh.there[x])[lw] = static_cast<uint8_t>(there);
+                    }
+                    if constexpr (Q8) {
+                        float ks = 0.f, vs = 0.f;
+                        if (page >= 0) {
+                            ks = a.c.ks[row_offset(a.c.kss, page, head, row)];
+                            vs = a.c.vs[row_offset(a.c.vss, page, head, row)];
+                        }
+                        signs_next = __ballot_sync(0xffffffffu, vs < 0.f);
+                        if (lane < RW) {
+                            float lv;
+                            asm("lg2.approx.f32 %0, %1;" : "=f"(lv) : "f"(fabsf(vs)));
+                            aux[(x * 2) * KEYS + lw * RW + lane] = ks;
+                            aux[(x * 2 + 1) * KEYS + lw * RW + lane] = lv;
+                        }
+                    }
+                    page = page_id(j + 1, &row);
+                    ++step_no;
+                } else {
+                    const bool last = j + 1 == steps;
+                    from = last ? v_next : v_off;
+                    sign = last ? signs_next : signs;
+                    const int slot0 = slot_first + j * KEYS;
+                    if (masked(it, slot0) && entry < kTrMasked) {
+                        where = static_cast<int>(i % kTrItems) * kTrMasked + entry;
+                        if (lw == 0 && lane == 0) it.bad_step[entry] = slot0;
+                        ++entry;
+                        if (lw == 0 && lane == 0) it.bad_steps = entry;
+                    }
+                    if (last) {  // before it is started: that may give the item back
+                        if (lane == 0) it.last_tile = issued + 1;  // (every warp the same)
+                        __syncwarp();
+                        ++done;
+                    }
+                }
+                start(is_k ? 0 : 1, from, where, sign);
+                if (p == 0 && ok) load_q();
             }
-            for (int j = 1; j < steps && ok; ++j) {
-                keys(j);
-                values(j - 1, v_off, signs);
-            }
-            // before its last tile is started: that may give it back
-            if (lane == 0) it.last_tile = issued + 1;  // (every warp the same)
-            __syncwarp();
-            ++done;
-            if (ok) values(steps - 1, v_next, signs_next);
         }
         if (ok) flush();
         ptx::cp_async_wait<0>();
@@ -675,6 +722,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                     wait(sh.ring_full[p % S::SLOTS], p / S::SLOTS);
                     if (!ok) return;
                     tc::fence_after();
+#pragma unroll 1
                     for (int k = 0; k < k_steps; ++k)
                         tc::mma_ss(tmem + to * 128, tc::smem_desc(q_s + k / 4 * S::QCHUNK + (k & 3) * 32, 16),
                                    tc::smem_desc(tile + k / 4 * S::CHUNK + (k & 3) * 32, 16), qk, k > 0);
@@ -693,6 +741,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                     wait(sh.p_full[buf], n_p++ >> 1);
                     if (!ok) break;
                     tc::fence_after();
+#pragma unroll 1
                     for (int half = 0; half < (Q8 ? 1 : 2); ++half)
 #pragma unroll
                         for (int k = 0; k < KEYS / 16; ++k)
@@ -743,22 +792,17 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                 if (Q8 && j == 0) scale2 = a.scale2 * sh.q_scale[i & 1][row];
                 if (some) {
                     tc::fence_after();
-                    uint32_t bits[KEYS / 32];
-                    bool part = masked(it, slot0);
+                    const bool cut = masked(it, slot0);
+                    bool part = cut;
 #pragma unroll
-                    for (int c = 0; c < KEYS / 32; ++c) {
-                        bits[c] = sh.there[x_at][c];
-                        part |= bits[c] != 0xffffffffu;
-                    }
-                    if (masked(it, slot0)) {
-#pragma unroll
-                        for (int c = 0; c < KEYS / 32; ++c) bits[c] &= seen(slot0 + 32 * c);
-                    }
+                    for (int c = 0; c < KEYS / 32; ++c) part |= sh.there[x_at][c] != 0xffffffffu;
                     const float *ks = aux + (x_at * 2) * KEYS, *lv = ks + KEYS;
                     (void)ks;
                     (void)lv;
                     // the largest logits
-                    float top = -INFINITY, top_v = -INFINITY;
+                    float tops[4], tops_v[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) tops[k] = tops_v[k] = -INFINITY;
                     auto load = [&](uint32_t (&x)[32], int c) {
                         tc::ld32(x, s_at + c * 32);
                         tc::wait_ld(x);
@@ -773,28 +817,36 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                             }
                         }
                         if (part) {
+                            const uint32_t bits = sh.there[x_at][c] & (cut ? seen(slot0 + 32 * c) : 0xffffffffu);
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
-                                if (!(bits[c] >> e & 1)) x[e] = 0xff800000u;
+                                if (!(bits & 1u << e)) x[e] = 0xff800000u;
                         }
                     };
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < KEYS / 32; ++c) {
                         uint32_t x[32];
                         load(x, c);
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
-                            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-                            if constexpr (Q8) s = *reinterpret_cast<const float4 *>(lv + c * 32 + e);
-                            const float sv[4] = {s.x, s.y, s.z, s.w};
+                            if constexpr (Q8) {
+                                const float4 s = *reinterpret_cast<const float4 *>(lv + c * 32 + e);
+                                const float sv[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                top = fmaxf(top, __uint_as_float(x[e + k]));
-                                if constexpr (Q8)
-                                    if (x[e + k] != 0xff800000u) top_v = fmaxf(top_v, __uint_as_float(x[e + k]) + sv[k]);
+                                for (int k = 0; k < 4; ++k) {
+                                    tops[k] = fmaxf(tops[k], __uint_as_float(x[e + k]));
+                                    // (a slot that is not seen may have any scale)
+                                    const float y = __uint_as_float(x[e + k]) + sv[k];
+                                    tops_v[k] = fmaxf(tops_v[k], part && x[e + k] == 0xff800000u ? -INFINITY : y);
+                                }
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) tops[k] = fmaxf(tops[k], __uint_as_float(x[e + k]));
                             }
                         }
                     }
+                    float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+                    float top_v = fmaxf(fmaxf(tops_v[0], tops_v[1]), fmaxf(tops_v[2], tops_v[3]));
                     if constexpr (!Q8) {
                         top *= scale2;
                         top_v = top;
@@ -819,6 +871,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                         if (j > 0) {
                             if (!wait_warp(sh.o_full[n_s & 1], n_s - 2 >> 1)) break;
                             tc::fence_after();
+#pragma unroll 1
                             for (int c = 0; c < (a.c.dim + 31) / 32; ++c) {
                                 uint32_t o[32];
                                 tc::ld32(o, lanes + S::O + c * 32);
@@ -832,7 +885,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                     const float2 scale = make_float2(scale2, scale2), off2 = make_float2(-less, -less);
                     // the weights of 32 slots take the columns of their logits: 16 of leading numbers, 16 of the rests
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < KEYS / 32; ++c) {
                         uint32_t x[32], p[16], rest[16];
                         load(x, c);
@@ -876,6 +929,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                 if (it.part >= 0) f = 1.f;
                 if (Q8) f *= mv == -INFINITY ? 0.f : exp2f(less_v - less);  // the output was relative to mv
                 uint16_t *out = a.out + it.b * a.ost[0] + t * a.ost[1] + hq * a.ost[2];
+#pragma unroll 1
                 for (int c = 0; c < (a.c.dim + 31) / 32; ++c) {
                     uint32_t o[32];
                     __syncwarp();
@@ -884,28 +938,18 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = none ? 0u : __float_as_uint(__uint_as_float(o[e]) * f);
                     for (int n = 0; n < it.bad_steps; ++n)
+#pragma unroll 1
                         for (int w = 0; w < 4; ++w)
+#pragma unroll 1
                             for (uint32_t left = it.bad[n][w]; left; left &= left - 1) {
                                 const int slot = it.bad_step[n] + w * 32 + __ffs(left) - 1;
                                 if (!real || !(seen(slot) & 1)) continue;
-                                int r = 0;
-                                const int page = cache_page(a.c, it.b, slot, &r, kClassTree);
-                                if (page < 0) continue;
-                                const uint8_t *v = a.c.v + row_offset(a.c.vst, page, it.head, r) * EB;
+                                const uint8_t *v = tree_value<EB>(a, it.b, it.head, slot);
+                                if (!v) continue;
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) {
-                                    if (c * 32 + e >= a.c.dim) break;
-                                    float y = 0.f;
-                                    if constexpr (Q8) {
-                                        if ((v[c * 32 + e] & 0x7f) == 0x7f) y = NAN;
-                                    } else {
-                                        const uint32_t u = reinterpret_cast<const uint16_t *>(v)[c * 32 + e];
-                                        constexpr uint32_t kExp = M16 ? 0x7c00u : 0x7f80u;
-                                        if ((u & kExp) == kExp)
-                                            y = M16 ? __half2float(__ushort_as_half(u)) : __uint_as_float(u << 16);
-                                    }
-                                    o[e] = __float_as_uint(__uint_as_float(o[e]) + y);
-                                }
+                                for (int e = 0; e < 32; ++e)
+                                    if (c * 32 + e < a.c.dim)
+                                        o[e] = __float_as_uint(__uint_as_float(o[e]) + tree_unusual<KV>(v, c * 32 + e));
                             }
                     if (!real) {
                     } else if (it.part >= 0) {
