@@ -188,8 +188,8 @@ typedef struct {
     int64_t workspace_bytes;
 } lc_cache_tree;
 
-/* Bytes of workspace of lc_cache_attend_tree, or -1 for a cache that it refuses. */
-int64_t lc_cache_attend_tree_workspace(const lc_paged_cache *cache);
+/* Bytes of workspace of lc_cache_attend_tree, or -1 for arguments that it refuses. */
+int64_t lc_cache_attend_tree_workspace(const lc_paged_cache *cache, int32_t n_q_heads, int32_t n_drafts);
 
 /* Errors: as lc_cache_attend; LC_ERR_SHAPE also for n_drafts outside 0 ..
  * LC_CACHE_MAX_DRAFTS.  Waits inside the kernel are bounded (LC_WAIT_TIMEOUT_NS);

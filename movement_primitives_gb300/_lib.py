@@ -223,7 +223,8 @@ PROTOTYPES = {
                                               ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
                                               ctypes.c_void_p, ctypes.c_void_p]),
     "lc_cache_attend_tree": (ctypes.c_int, [ctypes.POINTER(CPagedCache), ctypes.c_void_p, ctypes.c_void_p]),
-    "lc_cache_attend_tree_workspace": (ctypes.c_int64, [ctypes.POINTER(CPagedCache)]),
+    "lc_cache_attend_tree_workspace": (ctypes.c_int64, [ctypes.POINTER(CPagedCache), ctypes.c_int32,
+                                                        ctypes.c_int32]),
     "lc_cache_accept": (ctypes.c_int, [ctypes.POINTER(CPagedCache), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                        ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p]),
     "lc_cache_reserve": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),

@@ -187,11 +187,12 @@ class PagedCache:
             self._workspace_bytes[key] = n
         return n
 
-    def tree_workspace_bytes(self) -> int:
-        n = self._workspace_bytes.get("tree")
-        if n is None:  # (0 for a refused cache: the call says why)
-            n = max(0, int(_lib.lib().lc_cache_attend_tree_workspace(self._ref)))
-            self._workspace_bytes["tree"] = n
+    def tree_workspace_bytes(self, n_q_heads: int, drafts: int) -> int:
+        key = ("tree", n_q_heads, drafts)
+        n = self._workspace_bytes.get(key)
+        if n is None:  # (0 for refused arguments: the call says why)
+            n = max(0, int(_lib.lib().lc_cache_attend_tree_workspace(self._ref, n_q_heads, drafts)))
+            self._workspace_bytes[key] = n
         return n
 
     def evict_workspace_bytes(self, budget: int) -> int:
@@ -379,7 +380,7 @@ def cache_attend_tree(cache: PagedCache, q, lengths, parents, counts=None, out=N
     products, 1 / sqrt(head_dim) by default.  ``window``: how many tokens a draft sees,
     itself, its nearest ancestors and then the newest before the drafts (0: all).
     ``lse``: float32 [seqs, drafts, q_heads] to receive log sum exp.
-    ``workspace``: at least ``cache.tree_workspace_bytes()`` bytes; calls that may overlap need one each.
+    ``workspace``: at least ``cache.tree_workspace_bytes(q_heads, drafts)`` bytes; calls that may overlap need one each.
     """
     shape = q.shape
     if len(shape) != 4:
@@ -411,7 +412,7 @@ def _attend_tree(cache, q, lengths, parents, counts, out, scale, window, lse, wo
     if out is None:
         out = cache._empty((n, t, h, d), (t * h * d, h * d, d, 1), q.dtype)
     if workspace is None:
-        workspace = cache._empty((cache.tree_workspace_bytes(),), (1,), _BYTES)
+        workspace = cache._empty((cache.tree_workspace_bytes(h, t),), (1,), _BYTES)
     l0 = l1 = logs = 0
     if lse is not None:
         logs, (l0, l1, _) = lse.data_ptr(), lse.stride()

@@ -12,18 +12,30 @@ int launch_tree_e4m3(const TreeArgs &a, cudaStream_t cs);
 
 namespace {
 
-int64_t tree_workspace(const CacheArgs &c) {
-    const int64_t rows = int64_t(2) * kTrMostRuns * kTrRows;
-    return rows * ((c.dim + 63) / 64 * 64 * 4 + 8);
-}
+// Offsets of the parts' maxima and sums, of the units' runs, and the end.
+struct TreeSpace {
+    int64_t ml, split, end;
+    TreeSpace(const CacheArgs &c, int64_t units) {
+        const int64_t rows = int64_t(2) * kTrMostRuns * kTrRows;
+        ml = rows * ((c.dim + 63) / 64 * 64 * 4);
+        split = ml + rows * 8;
+        end = split + units * 8;
+    }
+};
+
+int most_blocks(int64_t n_drafts, int group) { return static_cast<int>((n_drafts * group + kTrRows - 1) / kTrRows); }
 
 }  // namespace
 
 }  // namespace lc
 
-extern "C" int64_t lc_cache_attend_tree_workspace(const lc_paged_cache *cache) {
-    lc::CacheArgs c;
-    return lc::check_cache(cache, false, &c) ? -1 : lc::tree_workspace(c);
+extern "C" int64_t lc_cache_attend_tree_workspace(const lc_paged_cache *cache, int32_t n_q_heads, int32_t n_drafts) {
+    using namespace lc;
+    CacheArgs c;
+    if (check_cache(cache, false, &c) || n_q_heads < 1 || n_q_heads % c.heads || n_drafts < 0 ||
+        n_drafts > LC_CACHE_MAX_DRAFTS)
+        return -1;
+    return TreeSpace(c, int64_t(c.n_seqs) * c.heads * most_blocks(n_drafts, n_q_heads / c.heads)).end;
 }
 
 extern "C" int lc_cache_attend_tree(const lc_paged_cache *cache, const lc_cache_tree *q, lc_stream_t stream) {
@@ -60,11 +72,12 @@ extern "C" int lc_cache_attend_tree(const lc_paged_cache *cache, const lc_cache_
     if (q0 < o0 + 2 * (o_top + cache->head_dim) && o0 < q0 + 2 * (q_top + cache->head_dim)) return LC_ERR_OVERLAP;
     a.group = q->n_q_heads / cache->n_kv_heads;
     if (int64_t(q->n_drafts) * a.group > 1 << 24) return LC_ERR_OVERFLOW;
-    a.most_blocks = static_cast<int32_t>((int64_t(q->n_drafts) * a.group + kTrRows - 1) / kTrRows);
-    if (int64_t(cache->n_seqs) * cache->n_kv_heads > 0x1fffffff / a.most_blocks) return LC_ERR_OVERFLOW;
-    const int64_t need = tree_workspace(a.c);
+    a.most_blocks = most_blocks(q->n_drafts, a.group);
+    const int64_t heads = int64_t(cache->n_seqs) * cache->n_kv_heads;
+    if (heads > 0x3ffffff / a.most_blocks) return LC_ERR_OVERFLOW;  // (32 blocks a unit in the second launch)
+    const TreeSpace space(a.c, heads * a.most_blocks);
     if (!q->workspace) return LC_ERR_NULL;
-    if (need > q->workspace_bytes) return LC_ERR_WORKSPACE;
+    if (space.end > q->workspace_bytes) return LC_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(q->workspace) % 256) return LC_ERR_ALIGN;
     if (a.c.cap == 0) return LC_OK;  // no slots: no drafts
     a.q = static_cast<const uint16_t *>(q->q);
@@ -93,8 +106,8 @@ extern "C" int lc_cache_attend_tree(const lc_paged_cache *cache, const lc_cache_
     a.q_vec = a.c.dim % 8 == 0 && rows_aligned(q->q, 3, ext, q->q_stride, 2, 16);
     a.out_vec = rows_aligned(q->out, 3, ext, q->out_stride, 2, 16);
     a.part = static_cast<float *>(q->workspace);
-    a.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(q->workspace) +
-                                           int64_t(2) * kTrMostRuns * kTrRows * ((a.c.dim + 63) / 64 * 64 * 4));
+    a.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(q->workspace) + space.ml);
+    a.split = reinterpret_cast<int2 *>(static_cast<uint8_t *>(q->workspace) + space.split);
     a.limit_ns = wait_limit_ns();
     const auto launch = cache->type == LC_CACHE_BF16 ? launch_tree_bf16 : cache->type == LC_CACHE_F16 ? launch_tree_f16 : launch_tree_e4m3;
     return launch(a, reinterpret_cast<cudaStream_t>(stream));

@@ -62,22 +62,18 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
 
 // The same for waits that one step of a pipeline after another goes through: the
 // timer, whose reading takes longer than most of them, is asked every 64 polls, and
-// the polling is out of line, where it takes no room among the step's instructions.
-static __device__ __noinline__ bool mbar_poll(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+// the loop is short, as every such wait has a copy of it.
+__device__ __forceinline__ bool mbar_wait_step(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
     uint64_t t0 = 0;
 #pragma unroll 1
-    for (uint32_t polls = 0; polls < kMaxPolls; ++polls) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if (polls % 64 == 63) {
+    for (uint32_t polls = 1; !mbar_try_wait(bar, parity); ++polls) {
+        if (polls % 64 == 0) {
             const uint64_t t = global_timer_ns();
-            if (t0 && t - t0 > limit_ns) return false;
+            if ((t0 && t - t0 > limit_ns) || polls > kMaxPolls) return false;
             if (!t0) t0 = t;
         }
     }
-    return false;
-}
-__device__ __forceinline__ bool mbar_wait_step(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
-    return mbar_try_wait(bar, parity) || mbar_poll(bar, parity, limit_ns);
+    return true;
 }
 
 __device__ __forceinline__ void prefetch_tensormap(const void *tmap) {

@@ -26,10 +26,10 @@
 // end to end, are cut into equal runs, one a block, found from the lengths on
 // the device.  A unit inside one run is finished there; a cut one leaves
 // parts in the workspace, which k_tree_join joins in their order, so results do not
-// depend on timing.  Eight warps of a block bring the rows of keys and values in
-// by asynchronous 16-byte copies (a row's place comes from the page table, which
-// tensor copies could not follow), several tiles ahead; one thread issues the
-// products; four warps do the softmax.
+// depend on timing.  Four warps of a block bring the rows of keys and values in
+// by asynchronous 16-byte copies (a row's place comes from the page table), several
+// tiles ahead; one thread issues the products; eight warps do the softmax, two of
+// them a row's (each half of the slots; they exchange their maxima).
 #pragma once
 
 #include "cache_common.cuh"
@@ -43,7 +43,8 @@ constexpr int kTrDrafts = LC_CACHE_MAX_DRAFTS;
 constexpr int kTrItems = 4;      // pieces that the scheduling warp may be ahead
 constexpr int kTrMasked = 4;     // steps of a piece that some row sees in part: two at either end at most
 constexpr int kTrAux = 8;        // steps whose slots' scales and presence are held
-constexpr int kTrLoaders = 8;
+constexpr int kTrLoaders = 4;    // warps
+constexpr int kTrSoft = 8;       // warps: two a 32 rows, each half of a step's slots
 constexpr int kTrMostRuns = 160;
 constexpr int kTrLeast = 2;      // steps of a run
 
@@ -62,6 +63,7 @@ struct TreeArgs {
     int32_t vec, q_vec, out_vec;  // rows of the pools, of q and of out are whole 16-byte words on 16-byte boundaries
     int32_t runs;           // blocks of the main kernel
     int32_t most_blocks;    // tiles of rows a key head at most
+    int2 *split;            // of a unit: its first and its last run
     float *part;            // [2 runs][dim / 4 rounded up to 16][128 rows][4]
     float2 *part_ml;        // [2 runs][128]
     uint64_t limit_ns;
@@ -88,33 +90,30 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs &a, int b) {
     return s;
 }
 
-// Steps of all units, and of those of the sequences before `upto`, by a warp.
+// Steps of all units, by a warp.
 template <int KEYS>
-__device__ __forceinline__ int64_t tree_steps(const TreeArgs &a, int upto, int64_t *before) {
+__device__ __forceinline__ int tree_steps(const TreeArgs &a) {
     const int lane = threadIdx.x & 31;
-    int64_t all = 0, some = 0;
+    int all = 0;
 #pragma unroll 1
     for (int b = lane; b < a.c.n_seqs; b += 32) {
         const TreeSeq s = tree_seq<KEYS>(a, b);
-        const int64_t w = int64_t(s.steps) * s.blocks * a.c.heads;
-        all += w;
-        if (b < upto) some += w;
+        all += s.steps * s.blocks * a.c.heads;
     }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) {
-        all += __shfl_xor_sync(0xffffffffu, all, d);
-        some += __shfl_xor_sync(0xffffffffu, some, d);
-    }
-    if (before) *before = some;
-    return all;
+    return __reduce_add_sync(0xffffffffu, all);
 }
 
-// Runs that `all` steps are cut into, and where run r begins.
-__device__ __forceinline__ int tree_runs(const TreeArgs &a, int64_t all) {
-    const int64_t most = (all + kTrLeast - 1) / kTrLeast;
-    return most < a.runs ? static_cast<int>(most) : a.runs;
-}
-__device__ __forceinline__ int64_t run_begin(int64_t all, int runs, int r) { return all * r / runs; }
+// The runs that `all` steps are cut into: run r begins at r * each + min(r, more).
+struct TreeRuns {
+    int runs, each, more;
+    __device__ __forceinline__ TreeRuns(const TreeArgs &a, int all)
+        : runs(min((all + kTrLeast - 1) / kTrLeast, a.runs)), each(all / max(runs, 1)), more(all - each * max(runs, 1)) {}
+    __device__ __forceinline__ int begin(int r) const { return r * each + min(r, more); }
+    __device__ __forceinline__ int of(int step) const {
+        const int wide = more * (each + 1);
+        return step < wide ? step / (each + 1) : more + (step - wide) / each;
+    }
+};
 
 // A piece of a run: steps first .. first + steps - 1 of a unit.
 struct TreeItem {
@@ -140,13 +139,13 @@ struct TreeShape {
     static constexpr int Q = NC * QCHUNK;
     static constexpr int RAW = !Q8 ? 0 : NC == 4 ? 3 : 4;     // E4M3 tiles under way
     static constexpr int RAW_TILE = TILE / 2;
-    static constexpr int SHARED = 9216 + (Q8 ? kTrAux * KEYS * 8 : 0);  // the block of barriers and items, and 1024 for alignment
+    static constexpr int SHARED = 12288 + (Q8 ? kTrAux * KEYS * 12 : 0);  // the block of barriers and items, and 1024 for alignment
     static constexpr int FIT = (232448 - SHARED - Q - RAW * RAW_TILE) / TILE;
     // (what kTrAux holds is read before tiles this far on are started)
     static constexpr int SLOTS = Q8 ? (FIT < 6 ? FIT : 6) : (FIT < 12 ? FIT : 12);
     static constexpr int LAG = Q8 ? RAW - 1 : SLOTS / 2;   // tiles under way
     static constexpr int SMEM = Q + RAW * RAW_TILE + SLOTS * TILE + SHARED;
-    static constexpr int THREADS = 32 * (4 + kTrLoaders + 2);
+    static constexpr int THREADS = 32 * (kTrSoft + kTrLoaders + 4);  // products, scheduling, two idle
     static constexpr int O = 256;                          // first output column of tensor memory
     static_assert(SLOTS >= 3 && LAG < SLOTS + (Q8 ? RAW : 0), "keys of two steps and values of one");
 };
@@ -155,18 +154,32 @@ struct TreeShared {
     uint64_t ring_full[12], ring_empty[12];
     uint64_t q_full, q_empty;
     uint64_t s_full[2], p_full[2], o_full[2];  // of every other step
-    uint64_t item_full[kTrItems], item_empty[kTrItems];
+    uint64_t item_full[kTrItems], item_empty[kTrItems], kin_full[kTrItems];
+    uint64_t pair[4];               // of the two warps of 32 rows
     uint64_t drain;
     uint32_t tmem;
+    float top[2][2][kTrRows], top_v[2][2][kTrRows];  // [step parity][half of the slots][row]
+    float sum[2][kTrRows];
     uint32_t there[kTrAux][4];      // the slots of a step that exist and whose pages do
     float q_scale[2][kTrRows];      // E4M3: what a row of q was divided by
     TreeItem item[kTrItems];
 };
-static_assert(sizeof(TreeShared) <= 8192, "the shared block has 8192 bytes");
+static_assert(sizeof(TreeShared) <= 11264, "the shared block has 11264 bytes");
 
 __device__ __forceinline__ float tr_exp2(float x) {  // 2 ulp, 0 for -infinity
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float tr_max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// Infinities as the largest number, NaN as it is.
+__device__ __forceinline__ float tr_finite(float x) {
+    float y;
+    asm("min.NaN.f32 %0, %1, 0f7F7FFFFF;" : "=f"(y) : "f"(x));
     return y;
 }
 template <bool F16>
@@ -301,17 +314,17 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
     constexpr int KEYS = S::KEYS, EB = Q8 ? 1 : 2;
     // weights are up to 2^(kLift + kRise): float16 has few exponents, so small ones are lifted into them; others are
     // lowered, as sums are, so that those of the type's largest values stay in float32
-    constexpr float kRise = M16 ? 2.f : 8.f, kLift = M16 ? 12.f : -40.f, kSumLift = Q8 ? -40.f : kLift;
+    constexpr float kRise = M16 ? 6.f : 8.f, kLift = M16 ? 8.f : -40.f, kSumLift = Q8 ? 0.f : kLift;
     extern __shared__ uint8_t raw_smem[];
     const uint32_t base = (ptx::smem_addr(raw_smem) + 1023) & ~1023u;
     const uint32_t q_s = base, ring_s = q_s + S::Q, raw_s = ring_s + S::SLOTS * S::TILE;
     uint8_t *const after = raw_smem + (base - ptx::smem_addr(raw_smem)) + S::Q + S::SLOTS * S::TILE + S::RAW * S::RAW_TILE;
     TreeShared &sh = *reinterpret_cast<TreeShared *>(after);
-    float *const aux = reinterpret_cast<float *>(after + 8192);  // E4M3: [kTrAux][keys' scales, log2 of values'][KEYS]
+    float *const aux = reinterpret_cast<float *>(after + 11264);  // E4M3: [kTrAux][keys' scales, values', log2 of those][KEYS]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     auto bar = [&](const uint64_t &b) { return ptx::smem_addr(&b); };
 
-    if (warp == 4 + kTrLoaders) tc::alloc(ptx::smem_addr(&sh.tmem), 512);
+    if (warp == kTrSoft + kTrLoaders) tc::alloc(ptx::smem_addr(&sh.tmem), 512);
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::SLOTS; ++i) {
             ptx::mbar_init(bar(sh.ring_full[i]), kTrLoaders);
@@ -321,12 +334,14 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
         ptx::mbar_init(bar(sh.q_empty), 1);
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(bar(sh.s_full[i]), 1);
-            ptx::mbar_init(bar(sh.p_full[i]), 4);
+            ptx::mbar_init(bar(sh.p_full[i]), kTrSoft);
             ptx::mbar_init(bar(sh.o_full[i]), 1);
         }
         for (int i = 0; i < kTrItems; ++i) {
             ptx::mbar_init(bar(sh.item_full[i]), 1);
-            ptx::mbar_init(bar(sh.item_empty[i]), 4 + kTrLoaders + 1);
+            ptx::mbar_init(bar(sh.item_empty[i]), kTrSoft + kTrLoaders + 1);
+            ptx::mbar_init(bar(sh.kin_full[i]), 1);
+            ptx::mbar_init(bar(sh.pair[i]), 2);
         }
         ptx::mbar_init(bar(sh.drain), 1);
         ptx::fence_mbar_init();
@@ -368,33 +383,39 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
         return slot0 + KEYS > it.n - it.count || (a.window && slot0 < it.n - it.count + kTrDrafts - a.window);
     };
 
-    if (warp == 4 + kTrLoaders + 1) {
+    // of a block's registers the softmax threads take the larger part (512 x 128 = 256 x 152 + 256 x 104)
+    auto few_registers = [] { asm volatile("setmaxnreg.dec.sync.aligned.u32 104;"); };
+    if (warp == kTrSoft + kTrLoaders + 1) {
+        few_registers();
         // scheduling: the pieces of this block's run
-        int64_t at = 0;
-        const int64_t all = tree_steps<KEYS>(a, 0, nullptr);
-        const int runs = tree_runs(a, all);
-        int64_t from = 0, to = 0;
-        if (static_cast<int>(blockIdx.x) < runs) {
-            from = run_begin(all, runs, blockIdx.x);
-            to = run_begin(all, runs, blockIdx.x + 1);
+        int at = 0, from = 0, to = 0;
+        const TreeRuns runs(a, tree_steps<KEYS>(a));
+        if (static_cast<int>(blockIdx.x) < runs.runs) {
+            from = runs.begin(blockIdx.x);
+            to = runs.begin(blockIdx.x + 1);
         }
         uint32_t i = 0;
         auto post = [&](auto &&fill) {
             const int s = i % kTrItems;
             if (i >= kTrItems && !wait_warp(sh.item_empty[s], i / kTrItems - 1)) return;
-            fill(sh.item[s]);
+            TreeItem &it = sh.item[s];
+            fill(it);
             arrive_warp(sh.item_full[s]);
+            if (!it.end) {  // only the softmax waits for this
+                tree_kin(a, it);
+                arrive_warp(sh.kin_full[s]);
+            }
             ++i;
         };
 #pragma unroll 1
         for (int b0 = 0; b0 < a.c.n_seqs && from < to && ok; b0 += 32) {
             TreeSeq s{};
             if (b0 + lane < a.c.n_seqs) s = tree_seq<KEYS>(a, b0 + lane);
-            const int64_t w = int64_t(s.steps) * s.blocks * a.c.heads;
-            int64_t upto = w;
+            const int w = s.steps * s.blocks * a.c.heads;
+            int upto = w;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
-                const int64_t o = __shfl_up_sync(0xffffffffu, upto, d);
+                const int o = __shfl_up_sync(0xffffffffu, upto, d);
                 if (lane >= d) upto += o;
             }
             while (from < to && ok) {
@@ -404,9 +425,12 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                 const int steps = __shfl_sync(0xffffffffu, s.steps, l), blocks = __shfl_sync(0xffffffffu, s.blocks, l);
                 const int n = __shfl_sync(0xffffffffu, s.n, l), count = __shfl_sync(0xffffffffu, s.count, l);
                 const int begin = __shfl_sync(0xffffffffu, s.begin, l);
-                const int64_t in = from - at - __shfl_sync(0xffffffffu, upto - w, l);
-                const int unit = static_cast<int>(in / steps), first = static_cast<int>(in - int64_t(unit) * steps);
-                const int take = static_cast<int>(min(to - from, int64_t(steps - first)));
+                const int in = from - at - __shfl_sync(0xffffffffu, upto - w, l);
+                const int unit = in / steps, first = in - unit * steps, take = min(to - from, steps - first);
+                // for the joining: the runs of a unit, from the one that holds its first step
+                if (first == 0 && lane == 0)
+                    a.split[(int64_t(b0 + l) * a.c.heads + unit / blocks) * a.most_blocks + unit % blocks] =
+                        make_int2(blockIdx.x, runs.of(from + steps - 1));
                 post([&](TreeItem &it) {
                     if (lane == 0) {
                         it.b = b0 + l;
@@ -423,18 +447,18 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                     }
                     if (lane < 4 * kTrMasked) it.bad[lane / 4][lane % 4] = 0;
                     __syncwarp();
-                    tree_kin(a, it);
                 });
                 from += take;
             }
             at += __shfl_sync(0xffffffffu, upto, 31);
         }
         if (ok) post([&](TreeItem &it) { if (lane == 0) it.end = 1; });
-    } else if (warp >= 4 && warp < 4 + kTrLoaders) {
+    } else if (warp >= kTrSoft && warp < kTrSoft + kTrLoaders) {
+        few_registers();
         // loads
         constexpr int RW = KEYS / kTrLoaders, PR = S::TILE / KEYS / 16 * EB / 2;  // rows of a warp, 16-byte pieces of a row
         constexpr int ITER = RW * PR / 32;
-        const int lw = warp - 4, dim = a.c.dim, dim16 = (dim + 15) / 16 * 16;
+        const int lw = warp - kTrSoft, dim = a.c.dim, dim16 = (dim + 15) / 16 * 16;
         const uint8_t *const pool[2] = {a.c.k, a.c.v};
         uint32_t issued = 0, given = 0, n_q = 0;  // tiles started and given to the products, tiles of q
         uint32_t back = 0, done = 0;              // items given back, and whose tiles have all been started
@@ -494,23 +518,46 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
             }
             if constexpr (Q8) {
                 if (given >= S::SLOTS && !wait_warp(sh.ring_empty[slot], given / S::SLOTS - 1)) return;
-#pragma unroll 2
-                for (int i = 0; i < ITER; ++i) {
-                    int row, col;
-                    piece_of(i, &row, &col);
-                    if (col >= dim16) continue;
-                    uint4 x = ld_shared16(raw_s + given % S::RAW * S::RAW_TILE + ((lw * ITER + i) * 32 + lane) * 16);
-                    if (where >= 0) look(x, where, lw * RW + row);
-                    const uint32_t sign = (signs >> row & 1) ? 0x80008000u : 0u;
-                    const uint32_t *w = reinterpret_cast<const uint32_t *>(&x);
-                    uint32_t y[8];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        y[2 * e] = tr_halves(w[e]) ^ sign;
-                        y[2 * e + 1] = tr_halves(w[e] >> 16) ^ sign;
+                // (unseen values' NaN and negative scales are rare: they are mended before and after)
+                const uint32_t from = raw_s + given % S::RAW * S::RAW_TILE + (lw * ITER * 32 + lane) * 16;
+                if (where >= 0 || signs) {
+#pragma unroll 1
+                    for (int i = 0; i < ITER; ++i) {
+                        int row, col;
+                        piece_of(i, &row, &col);
+                        if (col >= dim16) continue;
+                        uint4 x = ld_shared16(from + i * 512);
+                        if (where >= 0) look(x, where, lw * RW + row);
+                        if (signs >> row & 1) {
+                            x.x ^= 0x80808080u;
+                            x.y ^= 0x80808080u;
+                            x.z ^= 0x80808080u;
+                            x.w ^= 0x80808080u;
+                        }
+                        st_shared16(from + i * 512, x);
                     }
-                    st_shared16(tile_at(slot, lw * RW + row, col), make_uint4(y[0], y[1], y[2], y[3]));
-                    st_shared16(tile_at(slot, lw * RW + row, col + 8), make_uint4(y[4], y[5], y[6], y[7]));
+                }
+#pragma unroll
+                for (int i0 = 0; i0 < ITER; i0 += 4) {
+                    uint4 x[4];
+#pragma unroll
+                    for (int i = 0; i < 4 && i0 + i < ITER; ++i) x[i] = ld_shared16(from + (i0 + i) * 512);
+#pragma unroll
+                    for (int i = 0; i < 4 && i0 + i < ITER; ++i) {
+                        int row, col;
+                        piece_of(i0 + i, &row, &col);
+                        if (col >= dim16) continue;
+                        const uint32_t *w = reinterpret_cast<const uint32_t *>(&x[i]);
+                        uint32_t y[8];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            y[2 * e] = tr_halves(w[e]);
+                            y[2 * e + 1] = tr_halves(w[e] >> 16);
+                        }
+                        const uint32_t at = tile_at(slot, lw * RW + row, col);
+                        st_shared16(at, make_uint4(y[0], y[1], y[2], y[3]));
+                        st_shared16(at ^ 16, make_uint4(y[4], y[5], y[6], y[7]));  // (col is a multiple of 16)
+                    }
                 }
             } else if (where >= 0) {
 #pragma unroll 1
@@ -532,31 +579,61 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                 ++back;
             }
         };
-        // gives the tiles that have landed, or waits for all of them
-        auto settle = [&](bool all) {
-            if (all) ptx::cp_async_wait<0>();
-            else ptx::cp_async_wait<S::LAG>();
-            const uint32_t to = all ? issued : issued - S::LAG;
-#pragma unroll 1
-            while (given < to && ok) give();
-        };
-        auto flush = [&] { settle(true); };
+        // Where a row has a power of two of pieces, a lane's are all the same column, and rows eight apart lie alike.
+        constexpr int SPOTS = PR >= 32 ? 8 : 8 * PR / 32 > 0 ? 8 * PR / 32 : 1;
+        const bool plain = a.vec && dim == dim16;
+        const int first_col = lane % PR * (16 / EB);
+        uint32_t spot[SPOTS];
+#pragma unroll
+        for (int i = 0; i < SPOTS; ++i) {
+            const int row = i * (32 / PR) + lane / PR;
+            spot[i] = tile_at(0, lw * RW + row, first_col) - ring_s;
+        }
         // starts a tile of pool w from the rows at `from`
         auto start = [&](int w, int64_t from, int32_t where, uint32_t signs) {
             const uint32_t slot = issued % S::SLOTS;
             if (!Q8 && issued >= S::SLOTS && !wait_warp(sh.ring_empty[slot], issued / S::SLOTS - 1)) return;
+            if (32 % PR == 0 && plain && __all_sync(0xffffffffu, from >= 0 || lane >= RW)) {
+                // every lane the same piece of one row after another: a pointer by shuffle, two additions and a copy
+                const uint8_t *const mine = pool[w] + from * EB;
+                const uint32_t dst = Q8 ? raw_s + issued % S::RAW * S::RAW_TILE + (lw * ITER * 32 + lane) * 16 : ring_s + slot * S::TILE;
 #pragma unroll
-            for (int i = 0; i < ITER; ++i) {
-                int row, col;
-                piece_of(i, &row, &col);
-                const int64_t r = __shfl_sync(0xffffffffu, from, row);
-                if (col >= dim16) continue;
-                const uint32_t dst = Q8 ? raw_s + issued % S::RAW * S::RAW_TILE + ((lw * ITER + i) * 32 + lane) * 16
-                                        : tile_at(slot, lw * RW + row, col);
-                const bool real = r >= 0 && col < dim;
-                const uint8_t *src = pool[w] + (real ? r * EB : 0);
-                if (a.vec) tr_copy16(dst, src + (real ? col * EB : 0), real);
-                else st_shared16(dst, real ? tree_piece<EB>(src, col, dim) : make_uint4(0, 0, 0, 0));
+                for (int i0 = 0; i0 < ITER; i0 += 8) {
+                    const uint8_t *src[8];
+#pragma unroll
+                    for (int i = 0; i < 8 && i0 + i < ITER; ++i)
+                        src[i] = reinterpret_cast<const uint8_t *>(__shfl_sync(
+                            0xffffffffu, reinterpret_cast<uint64_t>(mine), (i0 + i) * (32 / PR) + lane / PR));
+#pragma unroll
+                    for (int i = 0; i < 8 && i0 + i < ITER; ++i)
+                        if (first_col < dim)
+                            ptx::cp_async16(Q8 ? dst + (i0 + i) * 512 : dst + spot[i % SPOTS] + (i0 + i) / SPOTS * SPOTS * (32 / PR) * 128,
+                                            src[i] + first_col * EB);
+                }
+            } else {
+            // the rows' places, eight ahead of their copies
+#pragma unroll
+            for (int i0 = 0; i0 < ITER; i0 += 8) {
+                int64_t place[8];
+#pragma unroll
+                for (int i = 0; i < 8 && i0 + i < ITER; ++i) {
+                    int row, col;
+                    piece_of(i0 + i, &row, &col);
+                    place[i] = __shfl_sync(0xffffffffu, from, row);
+                }
+#pragma unroll
+                for (int i = 0; i < 8 && i0 + i < ITER; ++i) {
+                    int row, col;
+                    piece_of(i0 + i, &row, &col);
+                    if (col >= dim16) continue;
+                    const uint32_t dst = Q8 ? raw_s + issued % S::RAW * S::RAW_TILE + ((lw * ITER + i0 + i) * 32 + lane) * 16
+                                            : tile_at(slot, lw * RW + row, col);
+                    const bool real = place[i] >= 0 && col < dim;
+                    const uint8_t *src = pool[w] + (real ? place[i] * EB : 0);
+                    if (a.vec) tr_copy16(dst, src + (real ? col * EB : 0), real);
+                    else st_shared16(dst, real ? tree_piece<EB>(src, col, dim) : make_uint4(0, 0, 0, 0));
+                }
+            }
             }
             ptx::cp_async_commit();
 #pragma unroll
@@ -566,84 +643,117 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                     flip[i] = signs;
                 }
             ++issued;
-            if (issued - given > S::LAG) settle(false);
         };
         uint32_t step_no = 0;  // steps of all pieces
-        for (uint32_t i = 0; ok; ++i) {
-            if (!done_warp(sh.item_full[i % kTrItems], i / kTrItems)) flush();
-            if (!wait_warp(sh.item_full[i % kTrItems], i / kTrItems)) break;
-            TreeItem &it = sh.item[i % kTrItems];
-            if (it.end) break;
-            const int b = it.b, head = it.head, n = it.n, slot_first = it.begin + it.first * KEYS, steps = it.steps;
-            int entry = 0;
-            int64_t v_off = -1, v_next = -1;   // rows of the values of the step whose keys were started last, and the one before
-            uint32_t signs = 0, signs_next = 0;
-            // a page id a lane, a step ahead
-            auto page_id = [&](int j, int *row) {
-                const int slot = slot_first + j * KEYS + lw * RW + lane;
-                *row = 0;
-                if (lane >= RW || j >= steps || slot >= n) return -1;
-                const int at = static_cast<int>(fast_div(slot, a.c.page_div));
-                *row = slot - at * a.c.page;
-                const int id = a.c.table[b * a.c.table_stride + at];
-                if (id >= 0 && id < a.c.n_pages) return id;
-                note_error(LC_ERR_CACHE_INDEX, kClassTree);
-                return -1;
-            };
-            int row = 0, page = page_id(0, &row);
-            auto load_q = [&] {
-                if (n_q && !done_warp(sh.q_empty, n_q - 1)) {
-                    flush();  // its last keys among them
-                    if (!wait_warp(sh.q_empty, n_q - 1)) return;
-                }
-                // the rows of q: a row a warp at a time, eight on the way
-                constexpr int PQ = NC * 8;
+        uint32_t i = 0;        // pieces taken
+        // the piece: its next tile in the order K0 K1 V0 K2 V1 ..., 2 * steps when all have been started
+        TreeItem *it = nullptr;
+        int b = 0, head = 0, n = 0, slot_first = 0, steps = 0, p = 0, entry = 0;
+        bool q_due = false, end = false;
+        int64_t v_off = -1, v_next = -1;   // rows of the values of the step whose keys were started last, and the one before
+        uint32_t signs = 0, signs_next = 0;
+        int row = 0, page = -1;            // of this lane's slot, a step ahead
+        auto page_id = [&](int j) {
+            const int slot = slot_first + j * KEYS + lw * RW + lane;
+            page = -1;
+            if (lane >= RW || j >= steps || slot >= n) return;
+            const int at = static_cast<int>(fast_div(slot, a.c.page_div));
+            row = slot - at * a.c.page;
+            page = a.c.table[b * a.c.table_stride + at];
+            if (page >= 0 && page < a.c.n_pages) return;
+            page = -1;
+            note_error(LC_ERR_CACHE_INDEX, kClassTree);
+        };
+        // one thing after another -- a piece taken, its q, a tile started -- and then the tiles that have landed are
+        // given on, all but the newest LAG, or all where the next thing is not to be had yet
 #pragma unroll 1
-                for (int r0 = 0; r0 < kTrRows / kTrLoaders; r0 += 8) {
-                    uint4 x[8];
-#pragma unroll
-                    for (int r = 0; r < 8; ++r) {
-                        const int at = it.row0 + lw * (kTrRows / kTrLoaders) + r0 + r;
-                        const int t = static_cast<int>(fast_div(at, a.group_div)), g = at - t * a.group;
-                        x[r] = make_uint4(0, 0, 0, 0);
-                        if (t < it.count && lane * 8 < dim) {
-                            const uint16_t *from = a.q + b * a.qst[0] + t * a.qst[1] + (int64_t(head) * a.group + g) * a.qst[2];
-                            if (a.q_vec) x[r] = *reinterpret_cast<const uint4 *>(from + lane * 8);
-                            else x[r] = tree_piece<2>(reinterpret_cast<const uint8_t *>(from), lane * 8, dim);
+        while (ok && !end) {
+            uint32_t keep = S::LAG;
+            bool q_here = false;
+            if (q_due) {
+                if (n_q && issued != given && !done_warp(sh.q_empty, n_q - 1)) {
+                    keep = 0;  // its last keys among them
+                } else {
+                    if (n_q && !wait_warp(sh.q_empty, n_q - 1)) break;
+                    constexpr int RQ = kTrRows / kTrLoaders, PQ = NC * 8;  // rows of a warp, 16-byte pieces of a row
+                    auto q_row = [&](int r, bool *real) {
+                        const int at = it->row0 + lw * RQ + r, t = static_cast<int>(fast_div(at, a.group_div)), g = at - t * a.group;
+                        *real = t < it->count;
+                        return a.q + b * a.qst[0] + t * a.qst[1] + (int64_t(head) * a.group + g) * a.qst[2];
+                    };
+                    auto q_at = [&](int r, int piece) {
+                        return q_s + piece / 8 * S::QCHUNK + (lw * RQ + r) * 128 + ((piece & 7) ^ (r & 7)) * 16;
+                    };
+                    if constexpr (!Q8) {
+#pragma unroll 4
+                        for (int i = lane; i < RQ * PQ; i += 32) {
+                            const int r = i / PQ, col = i % PQ * 8;
+                            bool real;
+                            const uint16_t *from = q_row(r, &real);
+                            real &= col < dim;
+                            if (a.q_vec) tr_copy16(q_at(r, col / 8), real ? from + col : a.q, real);
+                            else st_shared16(q_at(r, col / 8), real ? tree_piece<2>(reinterpret_cast<const uint8_t *>(from), col, dim)
+                                                                    : make_uint4(0, 0, 0, 0));
                         }
-                    }
+                    } else {
+                        // bfloat16 to float16 of a row whose largest element is between 1 and 2: a row a warp, eight on the way
+#pragma unroll 1
+                        for (int r0 = 0; r0 < RQ; r0 += 8) {
+                            uint4 x[8];
 #pragma unroll
-                    for (int r = 0; r < 8; ++r) {
-                        const int at = lw * (kTrRows / kTrLoaders) + r0 + r;
-                        if constexpr (Q8) {
-                            // bfloat16 to float16 of a row whose largest element is between 1 and 2
-                            uint32_t *w = reinterpret_cast<uint32_t *>(&x[r]);
-                            float f[8], most = 0.f;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                f[2 * e] = __uint_as_float(w[e] << 16);
-                                f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-                                most = fmaxf(most, fmaxf(fabsf(f[2 * e]), fabsf(f[2 * e + 1])));
+                            for (int r = 0; r < 8; ++r) {
+                                bool real;
+                                const uint16_t *from = q_row(r0 + r, &real);
+                                x[r] = make_uint4(0, 0, 0, 0);
+                                if (real && lane * 8 < dim) {
+                                    if (a.q_vec) x[r] = *reinterpret_cast<const uint4 *>(from + lane * 8);
+                                    else x[r] = tree_piece<2>(reinterpret_cast<const uint8_t *>(from), lane * 8, dim);
+                                }
                             }
-                            const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
-                            int ex = static_cast<int>(top >> 23) - 127;
-                            ex = min(max(ex, -126), 126);
-                            const float div = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) w[e] = tr_pack<true>(f[2 * e] * div, f[2 * e + 1] * div);
-                            if (lane == 0) sh.q_scale[i & 1][at] = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+                            for (int r = 0; r < 8; ++r) {
+                                uint32_t *w = reinterpret_cast<uint32_t *>(&x[r]);
+                                uint32_t most = 0;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) most = max(most, max(w[e] << 16 & 0x7fffffffu, w[e] & 0x7fff0000u));
+                                most = __reduce_max_sync(0xffffffffu, most);
+                                const int ex = min(max(static_cast<int>(most >> 23) - 127, -126), 126);
+                                const float div = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    w[e] = tr_pack<true>(__uint_as_float(w[e] << 16) * div, __uint_as_float(w[e] & 0xffff0000u) * div);
+                                if (lane == 0) sh.q_scale[(i - 1) & 1][lw * RQ + r0 + r] = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+                                if (lane < PQ) st_shared16(q_at(r0 + r, lane), x[r]);
+                            }
                         }
-                        if (lane < PQ)
-                            st_shared16(q_s + lane / 8 * S::QCHUNK + at * 128 + ((lane & 7) ^ (at & 7)) * 16, x[r]);
+                    }
+                    if constexpr (!Q8) ptx::cp_async_commit();
+                    ++n_q;
+                    keep = 0;  // and the keys that were started before them
+                    q_due = false;
+                    q_here = true;
+                }
+            } else if (p == 2 * steps) {
+                if (issued != given && !done_warp(sh.item_full[i % kTrItems], i / kTrItems)) {
+                    keep = 0;
+                } else {
+                    if (!wait_warp(sh.item_full[i % kTrItems], i / kTrItems)) break;
+                    it = &sh.item[i % kTrItems];
+                    ++i;
+                    if (it->end) {
+                        end = true;
+                        keep = 0;
+                    } else {
+                        b = it->b;
+                        head = it->head;
+                        n = it->n;
+                        slot_first = it->begin + it->first * KEYS;
+                        steps = it->steps;
+                        p = entry = 0;
+                        page_id(0);
                     }
                 }
-                tc::fence_async_smem();
-                arrive_warp(sh.q_full);
-                ++n_q;
-            };
-            // tiles in their order: K0 K1 V0 K2 V1 ...
-#pragma unroll 1
-            for (int p = 0; p < 2 * steps && ok; ++p) {
+            } else {
                 const bool is_k = p == 0 || (p & 1 && p < 2 * steps - 1);
                 const int j = is_k ? (p + 1) / 2 : p == 2 * steps - 1 ? steps - 1 : p / 2 - 1;
                 int64_t from;
@@ -655,10 +765,10 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                     signs = signs_next;
                     v_next = page >= 0 ? row_offset(a.c.vst, page, head, row) : -1;
                     const int x = step_no % kTrAux;
-                    const uint32_t there = __ballot_sync(0xffffffffu, page >= 0) & ((1u << RW) - 1);
+                    const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
                     if (lane == 0) {
-                        if constexpr (RW == 16) reinterpret_cast<uint16_t *>(sh.there[x])[lw] = static_cast<uint16_t>(there);
-                        else reinterpret_cast<uint8_t *>(sh.there[x])[lw] = static_cast<uint8_t>(there);
+                        if constexpr (RW == 32) sh.there[x][lw] = there;
+                        else reinterpret_cast<uint16_t *>(sh.there[x])[lw] = static_cast<uint16_t>(there);
                     }
                     if constexpr (Q8) {
                         float ks = 0.f, vs = 0.f;
@@ -670,36 +780,49 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                         if (lane < RW) {
                             float lv;
                             asm("lg2.approx.f32 %0, %1;" : "=f"(lv) : "f"(fabsf(vs)));
-                            aux[(x * 2) * KEYS + lw * RW + lane] = ks;
-                            aux[(x * 2 + 1) * KEYS + lw * RW + lane] = lv;
+                            aux[(x * 3) * KEYS + lw * RW + lane] = ks;
+                            aux[(x * 3 + 1) * KEYS + lw * RW + lane] = fabsf(vs);
+                            aux[(x * 3 + 2) * KEYS + lw * RW + lane] = lv;
                         }
                     }
-                    page = page_id(j + 1, &row);
+                    page_id(j + 1);
                     ++step_no;
                 } else {
                     const bool last = j + 1 == steps;
                     from = last ? v_next : v_off;
                     sign = last ? signs_next : signs;
                     const int slot0 = slot_first + j * KEYS;
-                    if (masked(it, slot0) && entry < kTrMasked) {
-                        where = static_cast<int>(i % kTrItems) * kTrMasked + entry;
-                        if (lw == 0 && lane == 0) it.bad_step[entry] = slot0;
+                    if (masked(*it, slot0) && entry < kTrMasked) {
+                        where = static_cast<int>((i - 1) % kTrItems) * kTrMasked + entry;
+                        if (lw == 0 && lane == 0) it->bad_step[entry] = slot0;
                         ++entry;
-                        if (lw == 0 && lane == 0) it.bad_steps = entry;
+                        if (lw == 0 && lane == 0) it->bad_steps = entry;
                     }
                     if (last) {  // before it is started: that may give the item back
-                        if (lane == 0) it.last_tile = issued + 1;  // (every warp the same)
+                        if (lane == 0) it->last_tile = issued + 1;  // (every warp the same)
                         __syncwarp();
                         ++done;
                     }
                 }
                 start(is_k ? 0 : 1, from, where, sign);
-                if (p == 0 && ok) load_q();
+                if (!ok) break;
+                q_due = p == 0;
+                ++p;
+            }
+            if (issued - given > keep || q_here) {
+                if (keep) ptx::cp_async_wait<S::LAG>();
+                else ptx::cp_async_wait<0>();
+#pragma unroll 1
+                while (issued - given > keep && ok) give();
+            }
+            if (q_here && ok) {
+                tc::fence_async_smem();
+                arrive_warp(sh.q_full);
             }
         }
-        if (ok) flush();
         ptx::cp_async_wait<0>();
-    } else if (warp == 4 + kTrLoaders) {
+    } else if (warp == kTrSoft + kTrLoaders) {
+        few_registers();
         // products
         if (lane == 0) {
             const uint32_t qk = tc::instr_desc(M16, KEYS, false, a.negative);
@@ -758,15 +881,23 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
             tc::commit(bar(sh.drain));
             wait(sh.drain, 0);
         }
-    } else if (warp < 4) {
-        // softmax and outputs, a thread a row
-        const int row = warp * 32 + lane;
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(warp) << 21);
-        uint32_t n_s = 0;
+    } else if (warp < kTrSoft) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+        // softmax and outputs: a thread a row and half of a step's slots
+        constexpr int HALF = KEYS / 64;  // 32-slot pieces of a half
+        const int half = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter) << 21);
+        uint32_t n_s = 0, n_pair = 0;
+        // the two warps of 32 rows have both written what the other reads
+        auto meet = [&] {
+            arrive_warp(sh.pair[quarter]);
+            return wait_warp(sh.pair[quarter], n_pair++);
+        };
         for (uint32_t i = 0; ok; ++i) {
             if (!wait_warp(sh.item_full[i % kTrItems], i / kTrItems)) break;
             const TreeItem &it = sh.item[i % kTrItems];
             if (it.end) break;
+            if (!wait_warp(sh.kin_full[i % kTrItems], i / kTrItems)) break;
             const int steps = it.steps, slot_first = it.begin + it.first * KEYS, before = it.n - it.count;
             const int at = it.row0 + row, t = static_cast<int>(fast_div(at, a.group_div)), g = at - t * a.group;
             const bool real = t < it.count;
@@ -783,6 +914,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                 if (d < 32 && d > -64) bits |= static_cast<uint32_t>(d >= 0 ? kin << d : kin >> -d);
                 return bits;
             };
+#pragma unroll 1
             for (int j = 0; j < steps; ++j) {
                 const int buf = n_s & 1, slot0 = slot_first + j * KEYS;
                 const uint32_t s_at = lanes + buf * 128;
@@ -796,61 +928,61 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                     bool part = cut;
 #pragma unroll
                     for (int c = 0; c < KEYS / 32; ++c) part |= sh.there[x_at][c] != 0xffffffffu;
-                    const float *ks = aux + (x_at * 2) * KEYS, *lv = ks + KEYS;
-                    (void)ks;
-                    (void)lv;
-                    // the largest logits
-                    float tops[4], tops_v[4];
+                    const float *const ks = aux + x_at * 3 * KEYS, *const vs = ks + KEYS, *const lv = vs + KEYS;
+                    (void)vs;
+                    const float2 scale = make_float2(scale2, scale2);
+                    // the logits, not scaled by scale2 yet, and the largest (a maximum passes NaN by: the weights will show it)
+                    uint32_t x[HALF][32], bits[HALF];
+                    float tops[2] = {-INFINITY, -INFINITY}, tops_v[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) tops[k] = tops_v[k] = -INFINITY;
-                    auto load = [&](uint32_t (&x)[32], int c) {
-                        tc::ld32(x, s_at + c * 32);
-                        tc::wait_ld(x);
+                    for (int c = 0; c < HALF; ++c) tc::ld32(x[c], s_at + (half * HALF + c) * 32);
+#pragma unroll
+                    for (int c = 0; c < HALF; ++c) {
+                        const int c32 = half * HALF + c;
+                        bits[c] = sh.there[x_at][c32] & (cut ? seen(slot0 + 32 * c32) : 0xffffffffu);
+                    }
+#pragma unroll
+                    for (int c = 0; c < HALF; ++c) tc::wait_ld(x[c]);
+#pragma unroll
+                    for (int c = 0; c < HALF; ++c) {
+                        const int s32 = (half * HALF + c) * 32;
                         if constexpr (Q8) {
 #pragma unroll
                             for (int e = 0; e < 32; e += 4) {
-                                const float4 s = *reinterpret_cast<const float4 *>(ks + c * 32 + e);
-                                x[e] = __float_as_uint(__uint_as_float(x[e]) * (s.x * scale2));
-                                x[e + 1] = __float_as_uint(__uint_as_float(x[e + 1]) * (s.y * scale2));
-                                x[e + 2] = __float_as_uint(__uint_as_float(x[e + 2]) * (s.z * scale2));
-                                x[e + 3] = __float_as_uint(__uint_as_float(x[e + 3]) * (s.w * scale2));
+                                const float4 s = *reinterpret_cast<const float4 *>(ks + s32 + e);
+                                const float2 u = tc::mul2(make_float2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])), make_float2(s.x, s.y));
+                                const float2 v = tc::mul2(make_float2(__uint_as_float(x[c][e + 2]), __uint_as_float(x[c][e + 3])), make_float2(s.z, s.w));
+                                x[c][e] = __float_as_uint(u.x);
+                                x[c][e + 1] = __float_as_uint(u.y);
+                                x[c][e + 2] = __float_as_uint(v.x);
+                                x[c][e + 3] = __float_as_uint(v.y);
                             }
                         }
                         if (part) {
-                            const uint32_t bits = sh.there[x_at][c] & (cut ? seen(slot0 + 32 * c) : 0xffffffffu);
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
-                                if (!(bits & 1u << e)) x[e] = 0xff800000u;
+                                if (!(bits[c] & 1u << e)) x[c][e] = 0xff800000u;
                         }
-                    };
-#pragma unroll 1
-                    for (int c = 0; c < KEYS / 32; ++c) {
-                        uint32_t x[32];
-                        load(x, c);
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
+                            tops[0] = tr_max3(tops[0], __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
+                            tops[1] = tr_max3(tops[1], __uint_as_float(x[c][e + 2]), __uint_as_float(x[c][e + 3]));
                             if constexpr (Q8) {
-                                const float4 s = *reinterpret_cast<const float4 *>(lv + c * 32 + e);
-                                const float sv[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    tops[k] = fmaxf(tops[k], __uint_as_float(x[e + k]));
-                                    // (a slot that is not seen may have any scale)
-                                    const float y = __uint_as_float(x[e + k]) + sv[k];
-                                    tops_v[k] = fmaxf(tops_v[k], part && x[e + k] == 0xff800000u ? -INFINITY : y);
-                                }
-                            } else {
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) tops[k] = fmaxf(tops[k], __uint_as_float(x[e + k]));
+                                const float4 s = *reinterpret_cast<const float4 *>(lv + s32 + e);
+                                const float2 u = tc::fma2(make_float2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])), scale, make_float2(s.x, s.y));
+                                const float2 v = tc::fma2(make_float2(__uint_as_float(x[c][e + 2]), __uint_as_float(x[c][e + 3])), scale, make_float2(s.z, s.w));
+                                tops_v[0] = tr_max3(tops_v[0], u.x, u.y);
+                                tops_v[1] = tr_max3(tops_v[1], v.x, v.y);
                             }
                         }
                     }
-                    float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-                    float top_v = fmaxf(fmaxf(tops_v[0], tops_v[1]), fmaxf(tops_v[2], tops_v[3]));
-                    if constexpr (!Q8) {
-                        top *= scale2;
-                        top_v = top;
-                    }
+                    float top = fmaxf(tops[0], tops[1]), top_v = fmaxf(tops_v[0], tops_v[1]);
+                    const int turn = n_pair & 1;
+                    sh.top[turn][half][row] = top;
+                    if constexpr (Q8) sh.top_v[turn][half][row] = top_v;
+                    if (!meet()) break;
+                    top = fmaxf(top, sh.top[turn][1 - half][row]) * scale2;
+                    top_v = Q8 ? fmaxf(top_v, sh.top_v[turn][1 - half][row]) : top;
                     const bool rise = real && (top_v > mv + kRise || (mv == -INFINITY && top_v > mv));
                     if (Q8 && real && top > m) {
                         l *= tr_exp2(m - top);
@@ -872,7 +1004,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                             if (!wait_warp(sh.o_full[n_s & 1], n_s - 2 >> 1)) break;
                             tc::fence_after();
 #pragma unroll 1
-                            for (int c = 0; c < (a.c.dim + 31) / 32; ++c) {
+                            for (int c = half; c < (a.c.dim + 31) / 32; c += 2) {
                                 uint32_t o[32];
                                 tc::ld32(o, lanes + S::O + c * 32);
                                 tc::wait_ld(o);
@@ -882,34 +1014,42 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                             }
                         }
                     }
-                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                    const float2 scale = make_float2(scale2, scale2), off2 = make_float2(-less, -less);
                     // the weights of 32 slots take the columns of their logits: 16 of leading numbers, 16 of the rests
-#pragma unroll 1
-                    for (int c = 0; c < KEYS / 32; ++c) {
-                        uint32_t x[32], p[16], rest[16];
-                        load(x, c);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    const float2 off = make_float2(-less, -less);
+                    // E4M3: from a slot's weight to what multiplies its codes
+                    const float turn_v = tr_exp2(fminf(less - less_v, 126.f));
+                    const float2 to_v = make_float2(turn_v, turn_v);
+                    (void)to_v;
+#pragma unroll
+                    for (int c = 0; c < HALF; ++c) {
+                        const int s32 = (half * HALF + c) * 32;
+                        uint32_t p[16], rest[16];
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
-                            float2 y = make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                            float2 y = tc::fma2(make_float2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])), scale, off);
+                            y.x = tr_exp2(y.x);
+                            y.y = tr_exp2(y.y);
+                            sum[e >> 1 & 1] = tc::add2(sum[e >> 1 & 1], y);
                             if constexpr (Q8) {
-                                const float2 s = *reinterpret_cast<const float2 *>(lv + c * 32 + e);
-                                float2 z;
-                                z.x = x[e] == 0xff800000u ? 0.f : tr_exp2(y.x + s.x - less_v);
-                                z.y = x[e + 1] == 0xff800000u ? 0.f : tr_exp2(y.y + s.y - less_v);
-                                p[e / 2] = tr_pack<true>(z.x, z.y);
-                                y.x = tr_exp2(y.x - less);
-                                y.y = tr_exp2(y.y - less);
+                                float2 v = tc::mul2(*reinterpret_cast<const float2 *>(vs + s32 + e), to_v);
+                                v.x = tr_finite(v.x);
+                                v.y = tr_finite(v.y);
+                                v = tc::mul2(v, y);
+                                p[e / 2] = tr_pack<true>(v.x, v.y);
                             } else {
-                                y = tc::fma2(y, scale, off2);
-                                y.x = tr_exp2(y.x);
-                                y.y = tr_exp2(y.y);
                                 tr_split<M16>(y.x, y.y, &p[e / 2], &rest[e / 2]);
                             }
-                            sum[e >> 1 & 1] = tc::add2(sum[e >> 1 & 1], y);
                         }
-                        tc::st16(s_at + c * 32, p);
-                        if constexpr (!Q8) tc::st16(s_at + c * 32 + 16, rest);
+                        if constexpr (Q8) {
+                            if (part) {  // a slot that is not seen may have any scale
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    p[e] &= (bits[c] & 1u << 2 * e ? 0xffffu : 0u) | (bits[c] & 2u << 2 * e ? 0xffff0000u : 0u);
+                            }
+                        }
+                        tc::st16(s_at + s32, p);
+                        if constexpr (!Q8) tc::st16(s_at + s32 + 16, rest);
                     }
                     const float2 both = tc::add2(sum[0], sum[1]);
                     l += both.x + both.y;
@@ -923,6 +1063,9 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
             if (!wait_warp(sh.o_full[n_s - 1 & 1], n_s - 1 >> 1)) break;
             if (some) {
                 tc::fence_after();
+                sh.sum[half][row] = l;
+                if (!meet()) break;
+                l = sh.sum[0][row] + sh.sum[1][row];
                 const int hq = it.head * a.group + g;
                 const bool none = l == 0.f;
                 float f = none ? 0.f : 1.f / l;
@@ -930,7 +1073,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                 if (Q8) f *= mv == -INFINITY ? 0.f : exp2f(less_v - less);  // the output was relative to mv
                 uint16_t *out = a.out + it.b * a.ost[0] + t * a.ost[1] + hq * a.ost[2];
 #pragma unroll 1
-                for (int c = 0; c < (a.c.dim + 31) / 32; ++c) {
+                for (int c = half; c < (a.c.dim + 31) / 32; c += 2) {
                     uint32_t o[32];
                     __syncwarp();
                     tc::ld32(o, lanes + S::O + c * 32);
@@ -976,88 +1119,85 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                         }
                     }
                 }
-                if (real && it.part >= 0) {
+                if (half == 0 && real && it.part >= 0) {
                     a.part_ml[int64_t(it.part) * kTrRows + row] = make_float2(m == -INFINITY ? -INFINITY : less, l);
-                } else if (real && a.lse) {
+                } else if (half == 0 && real && a.lse) {
                     a.lse[it.b * a.lst[0] + t * a.lst[1] + hq] =
                         none ? -INFINITY : (less + kSumLift + log2f(l * exp2f(-kSumLift))) * 0.6931471805599453f;
                 }
             }
             arrive_warp(sh.item_empty[i % kTrItems]);
         }
+    } else {
+        few_registers();
     }
     __syncwarp();
     tc::fence_before();
     __syncthreads();
-    if (warp == 4 + kTrLoaders) {
+    if (warp == kTrSoft + kTrLoaders) {
         tc::fence_after();
         tc::dealloc(tmem, 512);
     }
 }
 
-// Joins the parts of the units that were cut, in their order: a block a unit and 32 rows, a warp some columns.
+// Joins the parts of the units that were cut, in their order: a block a unit, 32
+// rows and 32 columns, a warp four columns, a lane a row.
 template <int KV, int NC>
 __global__ void __launch_bounds__(256) k_tree_join(const __grid_constant__ TreeArgs a) {
     constexpr int KEYS = TreeShape<NC, KV == LC_CACHE_E4M3>::KEYS;
-    constexpr float kSumLift = KV == LC_CACHE_F16 ? 12.f : -40.f;
-    __shared__ int64_t all_s, before_s;
+    constexpr float kSumLift = KV == LC_CACHE_F16 ? 8.f : KV == LC_CACHE_E4M3 ? 0.f : -40.f;
+    __shared__ float2 ml[8][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     start_after_prior();
-    const int group = blockIdx.x % 4, unit = blockIdx.x / 4;
+    const int columns = blockIdx.x % (2 * NC), group = blockIdx.x / (2 * NC) % 4, unit = blockIdx.x / (8 * NC);
     const int block = unit % a.most_blocks, head = unit / a.most_blocks % a.c.heads, b = unit / a.most_blocks / a.c.heads;
+    const int2 runs = a.split[unit];  // (nothing to go by where the sequence has no such rows)
     const TreeSeq s = tree_seq<KEYS>(a, b);
     const int row0 = block * kTrRows + group * 32;
-    if (row0 >= s.count * a.group) return;
-    if (warp == 0) {
-        int64_t before;
-        const int64_t all = tree_steps<KEYS>(a, b, &before);
-        if (lane == 0) {
-            all_s = all;
-            before_s = before;
-        }
+    if (row0 >= s.count * a.group || columns * 32 >= a.c.dim || runs.x == runs.y) return;
+    const int row = group * 32 + lane, n = runs.y - runs.x + 1;
+    // the unit's first part is its run's second, the others their runs' first
+    auto slot = [&](int i) { return int64_t(2) * (runs.x + i) + (i == 0); };
+    float top = -INFINITY, l = 0.f;
+    for (int i = warp; i < n; i += 8) {
+        const float2 v = a.part_ml[slot(i) * kTrRows + row];
+        const float t = fmaxf(top, v.x), safe = t == -INFINITY ? 0.f : t;
+        l = l * tr_exp2(top - safe) + v.y * tr_exp2(v.x - safe);
+        top = t;
     }
+    ml[warp][lane] = make_float2(top, l);
     __syncthreads();
-    const int64_t all = all_s, u0 = before_s + (int64_t(head) * s.blocks + block) * s.steps, u1 = u0 + s.steps;
-    const int runs = tree_runs(a, all);
-    // the runs that hold its first and its last step
-    auto run_of = [&](int64_t x) {
-        int r = static_cast<int>(x * runs / all);
-        while (run_begin(all, runs, r + 1) <= x) ++r;
-        while (run_begin(all, runs, r) > x) --r;
-        return r;
-    };
-    const int r0 = run_of(u0), r1 = run_of(u1 - 1);
-    if (r0 == r1) return;
+    top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) top = fmaxf(top, ml[w][lane].x);
+    const float safe = top == -INFINITY ? 0.f : top;
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) l += ml[w][lane].y * tr_exp2(ml[w][lane].x - safe);
+    const int c = columns * 8 + warp;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 *part = reinterpret_cast<const float4 *>(a.part) + int64_t(c) * kTrRows + row;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+        const float w = tr_exp2(a.part_ml[slot(i) * kTrRows + row].x - safe);
+        const float4 z = part[slot(i) * NC * 16 * kTrRows];
+        y.x += z.x * w;
+        y.y += z.y * w;
+        y.z += z.z * w;
+        y.w += z.w * w;
+    }
     const int at = row0 + lane, t = static_cast<int>(fast_div(at, a.group_div)), g = at - t * a.group;
     if (t >= s.count) return;
-    const int row = group * 32 + lane;
-    auto slot = [&](int r) { return int64_t(2 * r + (r == r0)); };
-    float top = -INFINITY, l = 0.f;
-    for (int r = r0; r <= r1; ++r) top = fmaxf(top, a.part_ml[slot(r) * kTrRows + row].x);
-    const float safe = top == -INFINITY ? 0.f : top;
-    for (int r = r0; r <= r1; ++r) {
-        const float2 v = a.part_ml[slot(r) * kTrRows + row];
-        l += v.y * tr_exp2(v.x - safe);
-    }
     const float f = l == 0.f ? 0.f : 1.f / l;
-    uint16_t *out = a.out + b * a.ost[0] + t * a.ost[1] + (int64_t(head) * a.group + g) * a.ost[2];
-    for (int c = warp; c * 4 < a.c.dim; c += 8) {
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int r = r0; r <= r1; ++r) {
-            const float w = tr_exp2(a.part_ml[slot(r) * kTrRows + row].x - safe);
-            const float4 z = reinterpret_cast<const float4 *>(a.part)[(slot(r) * NC * 16 + c) * kTrRows + row];
-            y.x += z.x * w;
-            y.y += z.y * w;
-            y.z += z.z * w;
-            y.w += z.w * w;
-        }
-        const float v[4] = {y.x * f, y.y * f, y.z * f, y.w * f};
-#pragma unroll
+    uint16_t *out = a.out + b * a.ost[0] + t * a.ost[1] + (int64_t(head) * a.group + g) * a.ost[2] + c * 4;
+    const uint32_t lo = tr_pack<KV == LC_CACHE_F16>(y.x * f, y.y * f), hi = tr_pack<KV == LC_CACHE_F16>(y.z * f, y.w * f);
+    if (a.out_vec && c * 4 + 4 <= a.c.dim) {
+        *reinterpret_cast<uint2 *>(out) = make_uint2(lo, hi);
+    } else {
         for (int e = 0; e < 4; ++e)
-            if (c * 4 + e < a.c.dim) out[c * 4 + e] = static_cast<uint16_t>(tr_pack<KV == LC_CACHE_F16>(v[e], 0.f));
+            if (c * 4 + e < a.c.dim) out[e] = static_cast<uint16_t>((e < 2 ? lo : hi) >> (e & 1) * 16);
     }
-    if (warp == 0 && a.lse)
+    if (c == 0 && a.lse)
         a.lse[b * a.lst[0] + t * a.lst[1] + head * a.group + g] =
             l == 0.f ? -INFINITY : (top + kSumLift + log2f(l * exp2f(-kSumLift))) * 0.6931471805599453f;
 }
@@ -1072,10 +1212,11 @@ int launch_tree_shape(const TreeArgs &a, cudaStream_t cs) {
     TreeArgs b = a;
     const int64_t units = int64_t(a.c.n_seqs) * a.c.heads * a.most_blocks;
     const int64_t steps = units * ((int64_t(a.c.cap) + S::KEYS - 1) / S::KEYS);
+    if (steps > 0x7fffffff) return LC_ERR_OVERFLOW;
     b.runs = static_cast<int32_t>(std::min<int64_t>(std::min(sms, kTrMostRuns), (steps + kTrLeast - 1) / kTrLeast));
     const int st = launch_after(fn, b.runs, S::THREADS, S::SMEM, cs, &b);
     if (st) return st;
-    return launch_after(reinterpret_cast<const void *>(&k_tree_join<KV, NC>), static_cast<unsigned>(units * 4), 256, 0, cs, &b);
+    return launch_after(reinterpret_cast<const void *>(&k_tree_join<KV, NC>), static_cast<unsigned>(units * 8 * NC), 256, 0, cs, &b);
 }
 
 template <int KV>
