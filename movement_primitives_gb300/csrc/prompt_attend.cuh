@@ -85,7 +85,7 @@ struct PromptShape {
 struct PromptShared {
     uint64_t ring_full[10], ring_empty[10];
     uint64_t q_full[2], q_empty[2];
-    uint64_t s_full[2], p_full[2];
+    uint64_t s_full[2], p_half[2], p_full[2];  // weights of the first 64 keys, of all
     uint64_t o_full[2];              // of a tile's item; with one tile of every other step
     uint64_t item_full[kPrItems], item_empty[kPrItems];
     uint64_t drain;
@@ -134,7 +134,7 @@ __device__ __forceinline__ PromptSeq prompt_seq(const PromptArgs &a, int b, Prom
     const int r0 = a.starts[b], r1 = a.starts[b + 1], s0 = ks[b], s1 = ks[b + 1];
     const int q0 = min(max(r0, 0), a.n_tokens), q1 = min(max(r1, q0), a.n_tokens);
     const int k0 = min(max(s0, 0), k_most), k1 = min(max(s1, k0), k_most);
-    if (q0 != r0 || q1 != r1 || k0 != s0 || k1 != s1) report_error(LC_ERR_CACHE_INDEX, kClassPrompt);
+    if (q0 != r0 || q1 != r1 || k0 != s0 || k1 != s1) note_error(LC_ERR_CACHE_INDEX, kClassPrompt);
     if (it) {
         it->q0 = q0;
         it->nq = q1 - q0;
@@ -214,6 +214,14 @@ __device__ __forceinline__ void prompt_item(const PromptArgs &a, uint32_t at, Pr
 
 // ---- the kernel ------------------------------------------------------------
 
+// A value that is not finite, 0 for others.
+template <bool F16>
+__device__ __noinline__ float prompt_unusual(uint32_t bits) {
+    constexpr uint32_t kExp = F16 ? 0x7c00u : 0x7f80u;
+    if ((bits & kExp) != kExp) return 0.f;
+    return F16 ? __half2float(__ushort_as_half(bits)) : __uint_as_float(bits << 16);
+}
+
 // Place in the ring, of an item's first slot, of step j's keys or values (in
 // slots of a tile): with two row tiles K0 V0 K1 V1 ..., with one K0 K1 V0 K2 V1 ...
 template <int TILES>
@@ -247,6 +255,7 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
             ptx::mbar_init(bar(sh.q_full[i]), 1);
             ptx::mbar_init(bar(sh.q_empty[i]), 1);
             ptx::mbar_init(bar(sh.s_full[i]), 1);
+            ptx::mbar_init(bar(sh.p_half[i]), 4);
             ptx::mbar_init(bar(sh.p_full[i]), 4);
             ptx::mbar_init(bar(sh.o_full[i]), 1);
         }
@@ -265,9 +274,9 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
 
     bool ok = true;  // no wait of this thread has run out
     auto wait = [&](const uint64_t &b, uint32_t n) {  // for phase n (counted from 0)
-        if (ok && !ptx::mbar_wait_bounded(bar(b), n & 1, a.limit_ns)) {
+        if (ok && !ptx::mbar_wait_step(bar(b), n & 1, a.limit_ns)) {
             ok = false;
-            report_error(LC_ERR_TIMEOUT, kClassPrompt);
+            note_error(LC_ERR_TIMEOUT, kClassPrompt);
         }
         return ok;
     };
@@ -281,12 +290,16 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
         asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar(b)) : "memory");
     };
 
-    // of a block's registers the softmax threads take the larger part (384 x 168 = 256 x 200 + 128 x 104)
+    auto arrive_warp = [&](const uint64_t &b) {
+        __syncwarp();
+        if (lane == 0) arrive(b);
+    };
+    // of a block's registers the softmax threads take the larger part (384 x 168 = 256 x 216 + 128 x 72)
     auto few_registers = [] {
-        if constexpr (TILES == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        if constexpr (TILES == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     };
     if (warp < S::SOFT) {
-        if constexpr (TILES == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        if constexpr (TILES == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         // softmax and outputs: row tile t, a thread a row
         const int t = TILES == 2 ? warp >> 2 : 0, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21);
@@ -336,7 +349,7 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
                     const uint32_t p = p0 + value_place<TILES>(j, it.steps);
                     if (TILES == 2) wait_values(j);
                     bool found = false;
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < NC; ++c) {
                         uint8_t *v = raw + (ring_s - ptx::smem_addr(raw)) +
                                      (p * S::SPT + c / S::CPS) % S::SLOTS * S::SLOT + c % S::CPS * kPrChunk + row * 128;
@@ -388,13 +401,13 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
                         for (int e = 0; e < 32; ++e)
                             if (c * 32 + e < from || c * 32 + e >= to) x[c][e] = 0xff800000u;
                 }
-                float top = -INFINITY;
+                float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
 #pragma unroll
                     for (int e = 0; e < 32; e += 2)
-                        top = pr_max3(top, __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
-                top *= a.scale2;
+                        tops[c] = pr_max3(tops[c], __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
+                const float top = pr_max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]) * a.scale2;
                 const bool rise = real && (top > m + kRise || (m == -INFINITY && top > m));
                 if (__any_sync(0xffffffffu, rise)) {
                     const float f = rise ? pr_exp2(m - top) : 1.f;
@@ -409,6 +422,7 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
                             tc::fence_after();
                         }
                         const uint32_t o_at = lanes + S::O + t * NC * 64;
+#pragma unroll 1
                         for (int c = 0; c < (a.dim + 31) / 32; ++c) {
                             uint32_t o[32];
                             tc::ld32(o, o_at + c * 32);
@@ -433,6 +447,12 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
                         p[e / 2] = pr_pack<F16>(y.x, y.y);
                     }
                     tc::st16(s_at + c * 16, p);
+                    if (c == 1) {
+                        tc::wait_st();
+                        tc::fence_before();
+                        __syncwarp();
+                        if (lane == 0) arrive(sh.p_half[buf]);
+                    }
                 }
                 const float2 both = tc::add2(sum[0], sum[1]);
                 l += both.x + both.y;
@@ -455,6 +475,7 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
             uint32_t bad = 0;
             if (it.steps)
                 for (int w = 0; w < 4; ++w) bad |= sh.bad_any[turn][w];
+#pragma unroll 1
             for (int c = 0; c < (a.dim + 31) / 32; ++c) {
                 uint32_t o[32];
                 __syncwarp();
@@ -466,22 +487,19 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = 0;
                 }
+#pragma unroll 1
                 for (uint32_t left = bad; left; left &= left - 1) {
                     const int n = __ffs(left) - 1, key0 = (it.first + sh.bad_step[turn][n]) * kPrKeys;
+#pragma unroll 1
                     for (int w = 0; w < 4; ++w)
+#pragma unroll 1
                         for (uint32_t keys = sh.bad[turn][n][w]; keys; keys &= keys - 1) {
                             const int key = key0 + w * 32 + __ffs(keys) - 1;
                             if (!real || key < lo || key >= hi) continue;
                             const uint16_t *v = a.v + (it.k0 + key) * a.vst[0] + it.key_head * a.vst[1] + c * 32;
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                if (c * 32 + e >= a.dim) break;
-                                const uint32_t bits = v[e];
-                                constexpr uint32_t kExp = F16 ? 0x7c00u : 0x7f80u;
-                                if ((bits & kExp) != kExp) continue;
-                                const float y = F16 ? __half2float(__ushort_as_half(bits)) : __uint_as_float(bits << 16);
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) + y);
-                            }
+                            for (int e = 0; e < 32; ++e)
+                                if (c * 32 + e < a.dim) o[e] = __float_as_uint(__uint_as_float(o[e]) + prompt_unusual<F16>(v[e]));
                         }
                 }
                 if (real) {
@@ -589,124 +607,148 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
         }
     } else if (warp == S::SOFT) {
         few_registers();
-        // products
-        if (lane == 0) {
-            const uint32_t qk = tc::instr_desc(F16, kPrKeys, false, a.negative);
-            const int k_steps = (a.dim + 15) / 16;
-            uint32_t pos = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
-            for (uint32_t i = 0;; ++i) {
-                if (!wait(sh.item_full[i % kPrItems], i / kPrItems)) break;
-                const PromptItem it = sh.item[i % kPrItems];
-                arrive(sh.item_empty[i % kPrItems]);
-                if (it.end) break;
-                if (!it.steps) continue;
-                const int tiles = TILES == 2 && it.t0 + a.tokens_tile < it.nq ? 2 : 1;
-                auto wait_tile = [&](uint32_t p) {
+        // products, by the whole warp
+        const uint32_t tm = tc::uniform(tmem);
+        const uint32_t q_desc = tc::smem_desc(q_s, 16), k_desc = tc::smem_desc(ring_s, 16);
+        const uint32_t v_desc = tc::smem_desc(ring_s, kPrChunk);
+        const uint32_t qk = tc::instr_desc(F16, kPrKeys, false, a.negative);
+        const int k_steps = (a.dim + 15) / 16;
+        // of the values' columns a full slot, and what is left for the last
+        const uint32_t pv_full = tc::instr_desc(F16, S::CPS * 64, true, false);
+        const uint32_t pv_last = tc::instr_desc(F16, (a.dim - (NC - S::CPS) * 64 + 15) / 16 * 16, true, false);
+        // waits by votes, so that what follows is known to be the warp's
+        auto wait_all = [&](const uint64_t &b, uint32_t n) {
+            if (!ok) return false;
+            uint64_t t0 = 0;
+#pragma unroll 1
+            for (uint32_t polls = 1; !__all_sync(0xffffffffu, ptx::mbar_try_wait(bar(b), n & 1)); ++polls) {
+                if (polls % 64) continue;
+                const uint64_t t = ptx::global_timer_ns();
+                if (__any_sync(0xffffffffu, (t0 && t - t0 > a.limit_ns) || polls > ptx::kMaxPolls)) {
+                    if (lane == 0) note_error(LC_ERR_TIMEOUT, kClassPrompt);
+                    ok = false;
+                    return false;
+                }
+                if (!t0) t0 = t;
+            }
+            tc::fence_after();
+            return true;
+        };
+        // tiles come in the order in which they are used: their first slot and the phase of its barriers
+        uint32_t slot = 0, phase = 0;
+        auto step = [&](uint32_t s, int c) { return s + c < S::SLOTS ? s + c : s + c - S::SLOTS; };
+        auto take = [&]() {  // the next tile's first slot, when it is there
+            const uint32_t s = slot;
 #pragma unroll
-                    for (int c = 0; c < S::SPT; ++c)
-                        wait(sh.ring_full[(p * S::SPT + c) % S::SLOTS], (p * S::SPT + c) / S::SLOTS);
-                    tc::fence_after();
-                };
-                auto free_tile = [&](uint32_t p) {
+            for (int c = 0; c < S::SPT; ++c) {
+                wait_all(sh.ring_full[slot], phase);
+                if (++slot == S::SLOTS) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+            }
+            return s;
+        };
+        auto free_tile = [&](uint32_t s) {
 #pragma unroll
-                    for (int c = 0; c < S::SPT; ++c) tc::commit(bar(sh.ring_empty[(p * S::SPT + c) % S::SLOTS]));
-                };
-                auto chunk_at = [&](uint32_t p, int c) {  // chunk c of the tile at place p
-                    return ring_s + (p * S::SPT + c / S::CPS) % S::SLOTS * S::SLOT + c % S::CPS * kPrChunk;
-                };
-                // S = Q K^T of row tile t into S buffer `to`
-                auto first_product = [&](int t, int to, uint32_t p) {
-                    for (int k = 0; k < k_steps; ++k) {
-                        const uint32_t at = (k & 3) * 32;
-                        tc::mma_ss(tmem + to * 128, tc::smem_desc(q_s + (t * NC + k / 4) * kPrChunk + at, 16),
-                                   tc::smem_desc(chunk_at(p, k / 4) + at, 16), qk, k > 0);
-                    }
-                    tc::commit(bar(sh.s_full[to]));
-                };
-                // O += P V
-                auto second_product = [&](int t, int from, uint32_t p, bool add) {
+            for (int c = 0; c < S::SPT; ++c) tc::commit(bar(sh.ring_empty[0]) + step(s, c) * 8);
+        };
+        // S = Q K^T of row tile t into S buffer `to`
+        auto first_product = [&](int t, int to, uint32_t s) {
 #pragma unroll
-                    for (int c = 0; c < NC; c += S::CPS) {
-                        const int cols = min(a.dim - c * 64, S::CPS * 64);
-                        const uint32_t pv = tc::instr_desc(F16, (cols + 15) / 16 * 16, true, false);
-                        const uint32_t d = tmem + S::O + t * NC * 64 + c * 64;
+            for (int c = 0; c < NC; ++c) {
+                const uint32_t q = q_desc + (t * NC + c) * (kPrChunk / 16);
+                const uint32_t k = k_desc + step(s, c / S::CPS) * (S::SLOT / 16) + c % S::CPS * (kPrChunk / 16);
 #pragma unroll
-                        for (int k = 0; k < kPrKeys / 16; ++k)
-                            tc::mma_ts(d, tmem + from * 128 + k * 8,
-                                       tc::smem_desc(chunk_at(p, c) + k * 2048, kPrChunk), pv, add || k > 0);
-                    }
-                };
-                const uint32_t p0 = pos;
-                pos += 2 * it.steps;
-                if constexpr (TILES == 2) {
-                    wait_tile(p0);
-                    for (int t = 0; t < tiles; ++t) {
-                        wait(sh.q_full[t], n_q[t]++);
-                        tc::fence_after();
+                for (int i = 0; i < 4; ++i)  // 16 columns, 32 bytes, on
+                    if (c * 4 + i < k_steps) tc::mma_ss(tm + to * 128, q + 2 * i, k + 2 * i, qk, c + i > 0);
+            }
+            tc::commit(bar(sh.s_full[0]) + to * 8);
+        };
+        // O += P V; the weights of 64 keys are multiplied while those of the others are made
+        auto second_product = [&](int t, int from, uint32_t n, uint32_t s, bool add) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (!wait_all(h ? sh.p_full[from] : sh.p_half[from], n)) return;
+#pragma unroll
+                for (int c = 0; c < NC; c += S::CPS) {
+                    const uint32_t d = tm + S::O + t * NC * 64 + c * 64, w = tm + from * 128 + h * (kPrKeys / 4);
+                    const uint32_t v = v_desc + step(s, c / S::CPS) * (S::SLOT / 16) + h * (kPrKeys / 2 * 128 / 16);
+#pragma unroll
+                    for (int k = 0; k < kPrKeys / 32; ++k)  // 16 keys, 2048 bytes, on
+                        tc::mma_ts(d, w + k * 8, v + 128 * k, c + S::CPS < NC ? pv_full : pv_last, add || h + k > 0);
+                }
+            }
+        };
+        uint32_t n_q[2] = {0, 0}, n_p[2] = {0, 0};
+        for (uint32_t i = 0;; ++i) {
+            if (!wait_all(sh.item_full[i % kPrItems], i / kPrItems)) break;
+            const PromptItem &it = sh.item[i % kPrItems];
+            const uint32_t end = tc::uniform(it.end), steps = tc::uniform(it.steps);
+            const uint32_t two = tc::uniform(TILES == 2 && it.t0 + a.tokens_tile < it.nq);
+            arrive_warp(sh.item_empty[i % kPrItems]);
+            if (end) break;
+            if (!steps) continue;
+            if constexpr (TILES == 2) {
+                uint32_t k = take(), v;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (t && !two) break;
+                    if (!wait_all(sh.q_full[t], n_q[t]++)) break;
+                    first_product(t, t, k);
+                    if (steps == 1) tc::commit(bar(sh.q_empty[t]));
+                }
+                free_tile(k);
+#pragma unroll 1
+                for (uint32_t j = 0; j < steps && ok; ++j) {
+                    const bool more = j + 1 < steps;
+                    v = take();
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (t && !two) break;
+                        second_product(t, t, n_p[t]++, v, j > 0);
                         if (!ok) break;
-                        first_product(t, t, p0);
-                        if (it.steps == 1) tc::commit(bar(sh.q_empty[t]));
-                    }
-                    free_tile(p0);
-                    for (int j = 0; j < it.steps && ok; ++j) {
-                        const uint32_t pv = p0 + value_place<2>(j, it.steps), pk = p0 + key_place<2>(j + 1);
-                        const bool more = j + 1 < it.steps;
-                        wait_tile(pv);
-                        for (int t = 0; t < tiles; ++t) {
-                            wait(sh.p_full[t], n_p[t]++);
-                            tc::fence_after();
+                        const bool last = t || !two;
+                        if (last) free_tile(v);
+                        if (more) {
+                            if (t == 0) k = take();
                             if (!ok) break;
-                            second_product(t, t, pv, j > 0);
-                            if (t == tiles - 1) free_tile(pv);
-                            if (more) {
-                                if (t == 0) wait_tile(pk);
-                                if (!ok) break;
-                                first_product(t, t, pk);
-                                if (t == tiles - 1) free_tile(pk);
-                                if (j + 2 == it.steps) tc::commit(bar(sh.q_empty[t]));
-                            } else {
-                                tc::commit(bar(sh.o_full[t]));
-                            }
-                        }
-                    }
-                } else {
-                    wait(sh.q_full[0], n_q[0]++);
-                    tc::fence_after();
-                    const uint32_t t0 = n_p[0];  // steps before this item: the S buffers go on in turn
-                    for (int j = 0; j < 2 && j < it.steps && ok; ++j) {
-                        wait_tile(p0 + key_place<1>(j));
-                        if (!ok) break;
-                        first_product(0, (t0 + j) & 1, p0 + key_place<1>(j));
-                        free_tile(p0 + key_place<1>(j));
-                        if (j + 1 == it.steps) tc::commit(bar(sh.q_empty[0]));
-                    }
-                    for (int j = 0; j < it.steps && ok; ++j) {
-                        const int buf = n_p[0] & 1;
-                        const uint32_t pv = p0 + value_place<1>(j, it.steps);
-                        wait_tile(pv);
-                        wait(sh.p_full[buf], n_p[0]++ >> 1);
-                        tc::fence_after();
-                        if (!ok) break;
-                        second_product(0, buf, pv, j > 0);
-                        free_tile(pv);
-                        tc::commit(bar(sh.o_full[buf]));
-                        if (j + 2 < it.steps) {
-                            const uint32_t pk = p0 + key_place<1>(j + 2);
-                            wait_tile(pk);
-                            if (!ok) break;
-                            first_product(0, buf, pk);
-                            free_tile(pk);
-                            if (j + 3 == it.steps) tc::commit(bar(sh.q_empty[0]));
+                            first_product(t, t, k);
+                            if (last) free_tile(k);
+                            if (j + 2 == steps) tc::commit(bar(sh.q_empty[t]));
+                        } else {
+                            tc::commit(bar(sh.o_full[t]));
                         }
                     }
                 }
-                if (!ok) break;
+            } else {
+                wait_all(sh.q_full[0], n_q[0]++);
+                const uint32_t t0 = n_p[0];  // steps before this item: the S buffers go on in turn
+                auto next = [&](uint32_t j) {
+                    const uint32_t k = take();
+                    if (!ok) return;
+                    first_product(0, (t0 + j) & 1, k);
+                    free_tile(k);
+                    if (j + 1 == steps) tc::commit(bar(sh.q_empty[0]));
+                };
+#pragma unroll 1
+                for (uint32_t j = 0; j < 2 && j < steps && ok; ++j) next(j);
+#pragma unroll 1
+                for (uint32_t j = 0; j < steps && ok; ++j) {
+                    const uint32_t buf = n_p[0] & 1, v = take();
+                    second_product(0, buf, n_p[0]++ >> 1, v, j > 0);
+                    if (!ok) break;
+                    free_tile(v);
+                    tc::commit(bar(sh.o_full[0]) + buf * 8);
+                    if (j + 2 < steps) next(j + 2);
+                }
             }
-            // products in flight end before the tensor memory is given back
-            ok = true;
-            tc::commit(bar(sh.drain));
-            wait(sh.drain, 0);
+            if (!ok) break;
         }
+        // products in flight end before the tensor memory is given back
+        ok = true;
+        tc::commit(bar(sh.drain));
+        wait_all(sh.drain, 0);
     } else {
         few_registers();
     }

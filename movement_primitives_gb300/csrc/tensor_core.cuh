@@ -26,33 +26,45 @@ __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::aft
 // Ordinary writes to shared memory become visible to the tensor cores.
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// One arrival on `bar` when all matrix instructions issued by this thread have finished.
-__device__ __forceinline__ void commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
+// The calls below are a whole warp's, converged; one elected lane of it issues the
+// instruction.  Their operands come from uniform registers: values that are the
+// warp's own (uniform() of what was loaded, and what is computed from such values under
+// votes) get there in one step, others take some 100 cycles an instruction to issue.
 
-// d[128, N] (+)= a[128, 16] b[16, N]; a from shared memory or from tensor memory.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+// A value that all lanes hold alike, as the compiler can know it.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_or_sync(0xffffffffu, x); }
+
+// One arrival on `bar` when all matrix instructions issued before have finished.
+__device__ __forceinline__ void commit(uint32_t bar) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
-        : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
         : "memory");
 }
 
 // Operand in shared memory, 128-byte swizzled rows of 64 16-bit elements in
 // groups of 8 rows (1024 bytes).  Rows are the M or N index (K-major) or the K
-// index (MN-major); `across` is the distance of the next 64 elements along MN.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t across) {
-    return static_cast<uint64_t>((addr >> 4) & 0x3fff) | static_cast<uint64_t>(across >> 4) << 16 |
-           static_cast<uint64_t>(1024 >> 4) << 32 | uint64_t(1) << 46 | uint64_t(2) << 61;
+// index (MN-major); `across` is the distance of the next 64 elements along MN.  The
+// low word of the descriptor: bytes / 16 may be added to it.
+__device__ __forceinline__ uint32_t smem_desc(uint32_t addr, uint32_t across) { return addr >> 4 | across >> 4 << 16; }
+constexpr uint32_t kDescHigh = (1024 >> 4) | 1u << 14 | 2u << 29;
+
+// d[128, N] (+)= a[128, 16] b[16, N]; a from shared memory or from tensor memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)), "n"(kDescHigh)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 y;\n\tmov.b64 y, {%2, %5};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)), "n"(kDescHigh)
+        : "memory");
 }
 
 // Instruction descriptor of a 16-bit product with float32 sums: M 128, N, b K-major

@@ -823,64 +823,82 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
         ptx::cp_async_wait<0>();
     } else if (warp == kTrSoft + kTrLoaders) {
         few_registers();
-        // products
-        if (lane == 0) {
-            const uint32_t qk = tc::instr_desc(M16, KEYS, false, a.negative);
-            const uint32_t pv = tc::instr_desc(M16, (a.c.dim + 15) / 16 * 16, true, false);
-            const int k_steps = (a.c.dim + 15) / 16;
-            uint32_t pos = 0, n_q = 0, n_p = 0;
-            for (uint32_t i = 0;; ++i) {
-                if (!wait(sh.item_full[i % kTrItems], i / kTrItems)) break;
-                const int steps = sh.item[i % kTrItems].steps, end = sh.item[i % kTrItems].end;
-                arrive(sh.item_empty[i % kTrItems]);
-                if (end) break;
-                const uint32_t p0 = pos, t0 = n_p;
-                pos += 2 * steps;
-                // places in the ring: K0 K1 V0 K2 V1 ...
-                auto key_place = [&](int j) { return p0 + (j ? 2 * j - 1 : 0); };
-                auto value_place = [&](int j) { return p0 + (j + 1 < steps ? 2 * j + 2 : 2 * j + 1); };
-                auto first_product = [&](int j) {
-                    const uint32_t p = key_place(j), tile = ring_s + p % S::SLOTS * S::TILE;
-                    const int to = (t0 + j) & 1;
-                    wait(sh.ring_full[p % S::SLOTS], p / S::SLOTS);
-                    if (!ok) return;
-                    tc::fence_after();
+        // products, by the whole warp
+        const uint32_t tm = tc::uniform(tmem);
+        const uint32_t q_desc = tc::smem_desc(q_s, 16), k_desc = tc::smem_desc(ring_s, 16), v_desc = tc::smem_desc(ring_s, S::CHUNK);
+        const uint32_t qk = tc::instr_desc(M16, KEYS, false, a.negative);
+        const uint32_t pv = tc::instr_desc(M16, (a.c.dim + 15) / 16 * 16, true, false);
+        const int k_steps = (a.c.dim + 15) / 16;
+        // waits by votes, so that what follows is known to be the warp's
+        auto wait_all = [&](const uint64_t &b, uint32_t n) {
+            if (!ok) return false;
+            uint64_t t0 = 0;
 #pragma unroll 1
-                    for (int k = 0; k < k_steps; ++k)
-                        tc::mma_ss(tmem + to * 128, tc::smem_desc(q_s + k / 4 * S::QCHUNK + (k & 3) * 32, 16),
-                                   tc::smem_desc(tile + k / 4 * S::CHUNK + (k & 3) * 32, 16), qk, k > 0);
-                    tc::commit(bar(sh.s_full[to]));
-                    tc::commit(bar(sh.ring_empty[p % S::SLOTS]));
-                    if (j + 1 == steps) tc::commit(bar(sh.q_empty));
-                };
-                wait(sh.q_full, n_q++);
-                if (!ok) break;
-                tc::fence_after();
-                for (int j = 0; j < 2 && j < steps && ok; ++j) first_product(j);
-                for (int j = 0; j < steps && ok; ++j) {
-                    const int buf = n_p & 1;
-                    const uint32_t p = value_place(j), tile = ring_s + p % S::SLOTS * S::TILE;
-                    wait(sh.ring_full[p % S::SLOTS], p / S::SLOTS);
-                    wait(sh.p_full[buf], n_p++ >> 1);
-                    if (!ok) break;
-                    tc::fence_after();
-#pragma unroll 1
-                    for (int half = 0; half < (Q8 ? 1 : 2); ++half)
-#pragma unroll
-                        for (int k = 0; k < KEYS / 16; ++k)
-                            tc::mma_ts(tmem + S::O, tmem + buf * 128 + k / 2 * 32 + half * 16 + (k & 1) * 8,
-                                       tc::smem_desc(tile + k * 2048, S::CHUNK), pv, j > 0 || half > 0 || k > 0);
-                    tc::commit(bar(sh.ring_empty[p % S::SLOTS]));
-                    tc::commit(bar(sh.o_full[buf]));
-                    if (j + 2 < steps) first_product(j + 2);
+            for (uint32_t polls = 1; !__all_sync(0xffffffffu, ptx::mbar_try_wait(bar(b), n & 1)); ++polls) {
+                if (polls % 64) continue;
+                const uint64_t t = ptx::global_timer_ns();
+                if (__any_sync(0xffffffffu, (t0 && t - t0 > a.limit_ns) || polls > ptx::kMaxPolls)) {
+                    if (lane == 0) note_error(LC_ERR_TIMEOUT, kClassTree);
+                    ok = false;
+                    return false;
                 }
-                if (!ok) break;
+                if (!t0) t0 = t;
             }
-            // products in flight end before the tensor memory is given back
-            ok = true;
-            tc::commit(bar(sh.drain));
-            wait(sh.drain, 0);
+            tc::fence_after();
+            return true;
+        };
+        // tiles come in the order in which they are used, K0 K1 V0 K2 V1 ...
+        uint32_t slot = 0, phase = 0, n_q = 0, n_p = 0;
+        auto take = [&]() {  // the next tile's slot, when it is there
+            const uint32_t s = slot;
+            wait_all(sh.ring_full[slot], phase);
+            if (++slot == S::SLOTS) {
+                slot = 0;
+                phase ^= 1;
+            }
+            return s;
+        };
+        for (uint32_t i = 0;; ++i) {
+            if (!wait_all(sh.item_full[i % kTrItems], i / kTrItems)) break;
+            const uint32_t steps = tc::uniform(sh.item[i % kTrItems].steps), end = tc::uniform(sh.item[i % kTrItems].end);
+            arrive_warp(sh.item_empty[i % kTrItems]);
+            if (end) break;
+            const uint32_t t0 = n_p;  // steps before this piece: the S buffers go on in turn
+            auto first_product = [&](uint32_t j) {
+                const uint32_t s = take(), to = (t0 + j) & 1, keys = k_desc + s * (S::TILE / 16);
+                if (!ok) return;
+#pragma unroll
+                for (int k = 0; k < NC * 4; ++k)  // 16 columns, 32 bytes, on
+                    if (k < k_steps)
+                        tc::mma_ss(tm + to * 128, q_desc + k / 4 * (S::QCHUNK / 16) + (k & 3) * 2,
+                                   keys + k / 4 * (S::CHUNK / 16) + (k & 3) * 2, qk, k > 0);
+                tc::commit(bar(sh.s_full[0]) + to * 8);
+                tc::commit(bar(sh.ring_empty[0]) + s * 8);
+                if (j + 1 == steps) tc::commit(bar(sh.q_empty));
+            };
+            if (!wait_all(sh.q_full, n_q++)) break;
+#pragma unroll 1
+            for (uint32_t j = 0; j < steps + 2 && ok; ++j) {
+                if (j >= 2) {
+                    const uint32_t buf = n_p & 1, s = take(), values = v_desc + s * (S::TILE / 16);
+                    if (!wait_all(sh.p_full[buf], n_p++ >> 1)) break;
+#pragma unroll 1
+                    for (int rest = 0; rest < (Q8 ? 1 : 2); ++rest)
+#pragma unroll
+                        for (int k = 0; k < KEYS / 16; ++k)  // 16 slots, 2048 bytes, on
+                            tc::mma_ts(tm + S::O, tm + buf * 128 + rest * 16 + k / 2 * 32 + (k & 1) * 8, values + 128 * k, pv,
+                                       j > 2 || rest > 0 || k > 0);
+                    tc::commit(bar(sh.ring_empty[0]) + s * 8);
+                    tc::commit(bar(sh.o_full[0]) + buf * 8);
+                }
+                if (j < steps) first_product(j);
+            }
+            if (!ok) break;
         }
+        // products in flight end before the tensor memory is given back
+        ok = true;
+        tc::commit(bar(sh.drain));
+        wait_all(sh.drain, 0);
     } else if (warp < kTrSoft) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
         // softmax and outputs: a thread a row and half of a step's slots
