@@ -388,25 +388,29 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
                 if (!wait_warp(sh.s_full[buf], TILES == 2 ? n_s : n_s >> 1)) break;
                 ++n_s;
                 tc::fence_after();
+                // 32 logits come while the maximum of the 32 before is taken
                 uint32_t x[4][32];
+                float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                const bool cut = key0 < all_lo || key0 + kPrKeys > all_hi;
+                tc::ld32(x[0], s_at);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tc::ld32(x[c], s_at + c * 32);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tc::wait_ld(x[c]);
-                if (key0 < all_lo || key0 + kPrKeys > all_hi) {
-                    const int from = lo - key0, to = hi - key0;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < 4; ++c) {
+                    tc::wait_ld(x[c]);
+                    if (c < 3) tc::ld32(x[c + 1], s_at + c * 32 + 32);
+                    if (cut) {
+                        const int from = lo - key0 - c * 32, to = hi - key0 - c * 32;
+                        const uint32_t bits = (from >= 32 ? 0u : 0xffffffffu << max(from, 0)) &
+                                              (to <= 0 ? 0u : 0xffffffffu >> (32 - min(to, 32)));
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            if (c * 32 + e < from || c * 32 + e >= to) x[c][e] = 0xff800000u;
+                            if (!(bits & 1u << e)) x[c][e] = 0xff800000u;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        tops[0 + 2 * (c & 1)] = pr_max3(tops[0 + 2 * (c & 1)], __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
+                        tops[1 + 2 * (c & 1)] = pr_max3(tops[1 + 2 * (c & 1)], __uint_as_float(x[c][e + 2]), __uint_as_float(x[c][e + 3]));
+                    }
                 }
-                float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2)
-                        tops[c] = pr_max3(tops[c], __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
                 const float top = pr_max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]) * a.scale2;
                 const bool rise = real && (top > m + kRise || (m == -INFINITY && top > m));
                 if (__any_sync(0xffffffffu, rise)) {
@@ -621,15 +625,14 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
             if (!ok) return false;
             uint64_t t0 = 0;
 #pragma unroll 1
-            for (uint32_t polls = 1; !__all_sync(0xffffffffu, ptx::mbar_try_wait(bar(b), n & 1)); ++polls) {
-                if (polls % 64) continue;
+            for (uint32_t polls = 0; !__all_sync(0xffffffffu, ptx::mbar_sleep_wait(bar(b), n & 1)); ++polls) {
                 const uint64_t t = ptx::global_timer_ns();
-                if (__any_sync(0xffffffffu, (t0 && t - t0 > a.limit_ns) || polls > ptx::kMaxPolls)) {
+                if (!t0) t0 = t;
+                if (__any_sync(0xffffffffu, t - t0 > a.limit_ns || polls > ptx::kMaxPolls)) {
                     if (lane == 0) note_error(LC_ERR_TIMEOUT, kClassPrompt);
                     ok = false;
                     return false;
                 }
-                if (!t0) t0 = t;
             }
             tc::fence_after();
             return true;
@@ -667,7 +670,7 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
         };
         // O += P V; the weights of 64 keys are multiplied while those of the others are made
         auto second_product = [&](int t, int from, uint32_t n, uint32_t s, bool add) {
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < 2; ++h) {
                 if (!wait_all(h ? sh.p_full[from] : sh.p_half[from], n)) return;
 #pragma unroll
@@ -680,7 +683,7 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
                 }
             }
         };
-        uint32_t n_q[2] = {0, 0}, n_p[2] = {0, 0};
+        uint32_t n_q0 = 0, n_q1 = 0, n_p0 = 0, n_p1 = 0;
         for (uint32_t i = 0;; ++i) {
             if (!wait_all(sh.item_full[i % kPrItems], i / kPrItems)) break;
             const PromptItem &it = sh.item[i % kPrItems];
@@ -690,57 +693,55 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
             if (end) break;
             if (!steps) continue;
             if constexpr (TILES == 2) {
-                uint32_t k = take(), v;
-#pragma unroll
+                uint32_t k = take();
+#pragma unroll 1
                 for (int t = 0; t < 2; ++t) {
                     if (t && !two) break;
-                    if (!wait_all(sh.q_full[t], n_q[t]++)) break;
+                    if (!wait_all(sh.q_full[t], t ? n_q1++ : n_q0++)) break;
                     first_product(t, t, k);
                     if (steps == 1) tc::commit(bar(sh.q_empty[t]));
                 }
                 free_tile(k);
 #pragma unroll 1
                 for (uint32_t j = 0; j < steps && ok; ++j) {
+                    // what a step needs is there before its weights are waited for, and what it has used is given back when
+                    // all its products are on their way: between the two only products
                     const bool more = j + 1 < steps;
-                    v = take();
-#pragma unroll
+                    const uint32_t v = take();
+                    if (more) k = take();
+#pragma unroll 1
                     for (int t = 0; t < 2; ++t) {
                         if (t && !two) break;
-                        second_product(t, t, n_p[t]++, v, j > 0);
+                        second_product(t, t, t ? n_p1++ : n_p0++, v, j > 0);
                         if (!ok) break;
-                        const bool last = t || !two;
-                        if (last) free_tile(v);
-                        if (more) {
-                            if (t == 0) k = take();
-                            if (!ok) break;
-                            first_product(t, t, k);
-                            if (last) free_tile(k);
-                            if (j + 2 == steps) tc::commit(bar(sh.q_empty[t]));
-                        } else {
-                            tc::commit(bar(sh.o_full[t]));
-                        }
+                        if (more) first_product(t, t, k);
+                        else tc::commit(bar(sh.o_full[0]) + t * 8);
+                        if (j + 2 == steps) tc::commit(bar(sh.q_empty[0]) + t * 8);
                     }
+                    free_tile(v);
+                    if (more) free_tile(k);
                 }
             } else {
-                wait_all(sh.q_full[0], n_q[0]++);
-                const uint32_t t0 = n_p[0];  // steps before this item: the S buffers go on in turn
-                auto next = [&](uint32_t j) {
-                    const uint32_t k = take();
-                    if (!ok) return;
-                    first_product(0, (t0 + j) & 1, k);
-                    free_tile(k);
-                    if (j + 1 == steps) tc::commit(bar(sh.q_empty[0]));
-                };
+                wait_all(sh.q_full[0], n_q0++);
+                const uint32_t t0 = n_p0;  // steps before this item: the S buffers go on in turn
+                uint32_t k = 0;
 #pragma unroll 1
-                for (uint32_t j = 0; j < 2 && j < steps && ok; ++j) next(j);
-#pragma unroll 1
-                for (uint32_t j = 0; j < steps && ok; ++j) {
-                    const uint32_t buf = n_p[0] & 1, v = take();
-                    second_product(0, buf, n_p[0]++ >> 1, v, j > 0);
+                for (uint32_t j = 0; j < steps + 2 && ok; ++j) {
+                    const bool more = j < steps;
+                    uint32_t v = 0;
+                    if (j >= 2) v = take();
+                    if (more) k = take();
                     if (!ok) break;
-                    free_tile(v);
-                    tc::commit(bar(sh.o_full[0]) + buf * 8);
-                    if (j + 2 < steps) next(j + 2);
+                    if (j >= 2) {
+                        const uint32_t buf = n_p0 & 1;
+                        second_product(0, buf, n_p0++ >> 1, v, j > 2);
+                        if (!ok) break;
+                        tc::commit(bar(sh.o_full[0]) + buf * 8);
+                    }
+                    if (more) first_product(0, (t0 + j) & 1, k);
+                    if (j >= 2) free_tile(v);
+                    if (more) free_tile(k);
+                    if (j + 1 == steps) tc::commit(bar(sh.q_empty[0]));
                 }
             }
             if (!ok) break;

@@ -60,18 +60,28 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
     return false;
 }
 
-// The same for waits that one step of a pipeline after another goes through: the
-// timer, whose reading takes longer than most of them, is asked every 64 polls, and
-// the loop is short, as every such wait has a copy of it.
+// The same for waits that one step of a pipeline after another goes through: a poll
+// may sleep up to kPollNs (its polls otherwise take a good part of the issue slots), and
+// the timer is read after such a sleep only.
+constexpr uint32_t kPollNs = 200000;
+__device__ __forceinline__ bool mbar_sleep_wait(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity), "r"(kPollNs)
+        : "memory");
+    return done != 0;
+}
 __device__ __forceinline__ bool mbar_wait_step(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
     uint64_t t0 = 0;
 #pragma unroll 1
-    for (uint32_t polls = 1; !mbar_try_wait(bar, parity); ++polls) {
-        if (polls % 64 == 0) {
-            const uint64_t t = global_timer_ns();
-            if ((t0 && t - t0 > limit_ns) || polls > kMaxPolls) return false;
-            if (!t0) t0 = t;
-        }
+    for (uint32_t polls = 0; !mbar_sleep_wait(bar, parity); ++polls) {
+        const uint64_t t = global_timer_ns();
+        if (!t0) t0 = t;
+        if (t - t0 > limit_ns || polls > kMaxPolls) return false;
     }
     return true;
 }

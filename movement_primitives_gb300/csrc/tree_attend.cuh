@@ -834,15 +834,14 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
             if (!ok) return false;
             uint64_t t0 = 0;
 #pragma unroll 1
-            for (uint32_t polls = 1; !__all_sync(0xffffffffu, ptx::mbar_try_wait(bar(b), n & 1)); ++polls) {
-                if (polls % 64) continue;
+            for (uint32_t polls = 0; !__all_sync(0xffffffffu, ptx::mbar_sleep_wait(bar(b), n & 1)); ++polls) {
                 const uint64_t t = ptx::global_timer_ns();
-                if (__any_sync(0xffffffffu, (t0 && t - t0 > a.limit_ns) || polls > ptx::kMaxPolls)) {
+                if (!t0) t0 = t;
+                if (__any_sync(0xffffffffu, t - t0 > a.limit_ns || polls > ptx::kMaxPolls)) {
                     if (lane == 0) note_error(LC_ERR_TIMEOUT, kClassTree);
                     ok = false;
                     return false;
                 }
-                if (!t0) t0 = t;
             }
             tc::fence_after();
             return true;
@@ -864,23 +863,18 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
             arrive_warp(sh.item_empty[i % kTrItems]);
             if (end) break;
             const uint32_t t0 = n_p;  // steps before this piece: the S buffers go on in turn
-            auto first_product = [&](uint32_t j) {
-                const uint32_t s = take(), to = (t0 + j) & 1, keys = k_desc + s * (S::TILE / 16);
-                if (!ok) return;
-#pragma unroll
-                for (int k = 0; k < NC * 4; ++k)  // 16 columns, 32 bytes, on
-                    if (k < k_steps)
-                        tc::mma_ss(tm + to * 128, q_desc + k / 4 * (S::QCHUNK / 16) + (k & 3) * 2,
-                                   keys + k / 4 * (S::CHUNK / 16) + (k & 3) * 2, qk, k > 0);
-                tc::commit(bar(sh.s_full[0]) + to * 8);
-                tc::commit(bar(sh.ring_empty[0]) + s * 8);
-                if (j + 1 == steps) tc::commit(bar(sh.q_empty));
-            };
             if (!wait_all(sh.q_full, n_q++)) break;
 #pragma unroll 1
             for (uint32_t j = 0; j < steps + 2 && ok; ++j) {
+                // what a step needs is there before its weights are waited for, and what it has used is given back when its
+                // products are on their way
+                const bool more = j < steps;
+                uint32_t sv = 0, sk = 0;
+                if (j >= 2) sv = take();
+                if (more) sk = take();
+                if (!ok) break;
                 if (j >= 2) {
-                    const uint32_t buf = n_p & 1, s = take(), values = v_desc + s * (S::TILE / 16);
+                    const uint32_t buf = n_p & 1, values = v_desc + sv * (S::TILE / 16);
                     if (!wait_all(sh.p_full[buf], n_p++ >> 1)) break;
 #pragma unroll 1
                     for (int rest = 0; rest < (Q8 ? 1 : 2); ++rest)
@@ -888,10 +882,20 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                         for (int k = 0; k < KEYS / 16; ++k)  // 16 slots, 2048 bytes, on
                             tc::mma_ts(tm + S::O, tm + buf * 128 + rest * 16 + k / 2 * 32 + (k & 1) * 8, values + 128 * k, pv,
                                        j > 2 || rest > 0 || k > 0);
-                    tc::commit(bar(sh.ring_empty[0]) + s * 8);
                     tc::commit(bar(sh.o_full[0]) + buf * 8);
                 }
-                if (j < steps) first_product(j);
+                if (more) {
+                    const uint32_t to = (t0 + j) & 1, keys = k_desc + sk * (S::TILE / 16);
+#pragma unroll
+                    for (int k = 0; k < NC * 4; ++k)  // 16 columns, 32 bytes, on
+                        if (k < k_steps)
+                            tc::mma_ss(tm + to * 128, q_desc + k / 4 * (S::QCHUNK / 16) + (k & 3) * 2,
+                                       keys + k / 4 * (S::CHUNK / 16) + (k & 3) * 2, qk, k > 0);
+                    tc::commit(bar(sh.s_full[0]) + to * 8);
+                    tc::commit(bar(sh.ring_empty[0]) + sk * 8);
+                    if (j + 1 == steps) tc::commit(bar(sh.q_empty));
+                }
+                if (j >= 2) tc::commit(bar(sh.ring_empty[0]) + sv * 8);
             }
             if (!ok) break;
         }
