@@ -78,7 +78,7 @@ struct PromptShape {
     static constexpr int SLOTS = (232448 - 2048 - Q) / SLOT < 10 ? (232448 - 2048 - Q) / SLOT : 10;
     static constexpr int SMEM = Q + SLOTS * SLOT + 2048;   // 1024 of them for alignment
     static constexpr int SOFT = 4 * TILES;                 // softmax warps
-    static constexpr int THREADS = 32 * (SOFT + 4);        // products, loads, scheduling, one idle
+    static constexpr int THREADS = 32 * (SOFT + 4);        // products, loads, scheduling, a second tile's products
     static constexpr int O = 256;                          // first output column of tensor memory
 };
 
@@ -88,7 +88,8 @@ struct PromptShared {
     uint64_t s_full[2], p_half[2], p_full[2];  // weights of the first 64 keys, of all
     uint64_t o_full[2];              // of a tile's item; with one tile of every other step
     uint64_t item_full[kPrItems], item_empty[kPrItems];
-    uint64_t drain;
+    uint64_t turn[2];                // of a tile's products, when the other's are on their way
+    uint64_t drain[2];
     PromptItem item[kPrItems];
     uint32_t bad[kPrTurns][kPrMasked][4];   // [item's turn][masked step][rows of 32]: values that are not finite
     int32_t bad_step[kPrTurns][kPrMasked];
@@ -249,7 +250,7 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::SLOTS; ++i) {
             ptx::mbar_init(bar(sh.ring_full[i]), 1);
-            ptx::mbar_init(bar(sh.ring_empty[i]), 1);
+            ptx::mbar_init(bar(sh.ring_empty[i]), TILES);
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(bar(sh.q_full[i]), 1);
@@ -261,9 +262,12 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
         }
         for (int i = 0; i < kPrItems; ++i) {
             ptx::mbar_init(bar(sh.item_full[i]), 1);
-            ptx::mbar_init(bar(sh.item_empty[i]), S::SOFT + 2);
+            ptx::mbar_init(bar(sh.item_empty[i]), S::SOFT + 1 + TILES);
         }
-        ptx::mbar_init(bar(sh.drain), 1);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(bar(sh.turn[i]), 1);
+            ptx::mbar_init(bar(sh.drain[i]), 1);
+        }
         ptx::fence_mbar_init();
     }
     tc::fence_before();
@@ -609,9 +613,12 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
                     if (tiles_q[t]) wait(sh.q_full[t], tiles_q[t] - 1);
             }
         }
-    } else if (warp == S::SOFT) {
+    } else if (warp == S::SOFT || (TILES == 2 && warp == S::SOFT + 3)) {
         few_registers();
-        // products, by the whole warp
+        // products, by the whole warp.  With two row tiles a warp a tile, so that one's waits and bookkeeping pass while
+        // the other's products run; the tiles take turns, else both come to do their softmax at the same time and leave
+        // the tensor cores idle meanwhile (a fifth slower, as is one warp for both).
+        const int t = warp != S::SOFT;
         const uint32_t tm = tc::uniform(tmem);
         const uint32_t q_desc = tc::smem_desc(q_s, 16), k_desc = tc::smem_desc(ring_s, 16);
         const uint32_t v_desc = tc::smem_desc(ring_s, kPrChunk);
@@ -666,13 +673,19 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
                 for (int i = 0; i < 4; ++i)  // 16 columns, 32 bytes, on
                     if (c * 4 + i < k_steps) tc::mma_ss(tm + to * 128, q + 2 * i, k + 2 * i, qk, c + i > 0);
             }
-            tc::commit(bar(sh.s_full[0]) + to * 8);
         };
         // O += P V; the weights of 64 keys are multiplied while those of the others are made
-        auto second_product = [&](int t, int from, uint32_t n, uint32_t s, bool add) {
+        uint32_t n_turn = 0;
+        auto my_turn = [&] { return t == 0 ? n_turn == 0 || wait_all(sh.turn[0], n_turn - 1) : wait_all(sh.turn[1], n_turn); };
+        auto your_turn = [&] {
+            ++n_turn;
+            arrive_warp(sh.turn[1 - t]);
+        };
+        auto second_product = [&](int t, int from, uint32_t n, uint32_t s, bool add, bool turns) {
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
                 if (!wait_all(h ? sh.p_full[from] : sh.p_half[from], n)) return;
+                if (turns && h == 0 && !my_turn()) return;
 #pragma unroll
                 for (int c = 0; c < NC; c += S::CPS) {
                     const uint32_t d = tm + S::O + t * NC * 64 + c * 64, w = tm + from * 128 + h * (kPrKeys / 4);
@@ -683,7 +696,7 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
                 }
             }
         };
-        uint32_t n_q0 = 0, n_q1 = 0, n_p0 = 0, n_p1 = 0;
+        uint32_t n_q = 0, n_p = 0;
         for (uint32_t i = 0;; ++i) {
             if (!wait_all(sh.item_full[i % kPrItems], i / kPrItems)) break;
             const PromptItem &it = sh.item[i % kPrItems];
@@ -694,12 +707,13 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
             if (!steps) continue;
             if constexpr (TILES == 2) {
                 uint32_t k = take();
-#pragma unroll 1
-                for (int t = 0; t < 2; ++t) {
-                    if (t && !two) break;
-                    if (!wait_all(sh.q_full[t], t ? n_q1++ : n_q0++)) break;
+                const bool mine = t == 0 || two;
+                if (mine) {
+                    if (!wait_all(sh.q_full[t], n_q++) || (two && !my_turn())) break;
                     first_product(t, t, k);
-                    if (steps == 1) tc::commit(bar(sh.q_empty[t]));
+                    if (two) your_turn();
+                    tc::commit(bar(sh.s_full[0]) + t * 8);
+                    if (steps == 1) tc::commit(bar(sh.q_empty[0]) + t * 8);
                 }
                 free_tile(k);
 #pragma unroll 1
@@ -709,21 +723,20 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
                     const bool more = j + 1 < steps;
                     const uint32_t v = take();
                     if (more) k = take();
-#pragma unroll 1
-                    for (int t = 0; t < 2; ++t) {
-                        if (t && !two) break;
-                        second_product(t, t, t ? n_p1++ : n_p0++, v, j > 0);
+                    if (mine) {
+                        second_product(t, t, n_p++, v, j > 0, two);
                         if (!ok) break;
                         if (more) first_product(t, t, k);
-                        else tc::commit(bar(sh.o_full[0]) + t * 8);
+                        if (two) your_turn();
+                        tc::commit((more ? bar(sh.s_full[0]) : bar(sh.o_full[0])) + t * 8);
                         if (j + 2 == steps) tc::commit(bar(sh.q_empty[0]) + t * 8);
                     }
                     free_tile(v);
                     if (more) free_tile(k);
                 }
             } else {
-                wait_all(sh.q_full[0], n_q0++);
-                const uint32_t t0 = n_p0;  // steps before this item: the S buffers go on in turn
+                wait_all(sh.q_full[0], n_q++);
+                const uint32_t t0 = n_p;  // steps before this item: the S buffers go on in turn
                 uint32_t k = 0;
 #pragma unroll 1
                 for (uint32_t j = 0; j < steps + 2 && ok; ++j) {
@@ -733,12 +746,15 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
                     if (more) k = take();
                     if (!ok) break;
                     if (j >= 2) {
-                        const uint32_t buf = n_p0 & 1;
-                        second_product(0, buf, n_p0++ >> 1, v, j > 2);
+                        const uint32_t buf = n_p & 1;
+                        second_product(0, buf, n_p++ >> 1, v, j > 2, false);
                         if (!ok) break;
                         tc::commit(bar(sh.o_full[0]) + buf * 8);
                     }
-                    if (more) first_product(0, (t0 + j) & 1, k);
+                    if (more) {
+                        first_product(0, (t0 + j) & 1, k);
+                        tc::commit(bar(sh.s_full[0]) + ((t0 + j) & 1) * 8);
+                    }
                     if (j >= 2) free_tile(v);
                     if (more) free_tile(k);
                     if (j + 1 == steps) tc::commit(bar(sh.q_empty[0]));
@@ -748,8 +764,8 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
         }
         // products in flight end before the tensor memory is given back
         ok = true;
-        tc::commit(bar(sh.drain));
-        wait_all(sh.drain, 0);
+        tc::commit(bar(sh.drain[0]) + t * 8);
+        wait_all(sh.drain[t], 0);
     } else {
         few_registers();
     }
