@@ -19,8 +19,10 @@
 // memory bounds the pass, so the second costs nothing up to about 128 rows, and the output's own
 // rounding is the only one that shows.  E4M3 codes become float16 numbers on their
 // way into shared memory, exactly; the keys' scales multiply the logits, the
-// values' join the weights as 2^(x + log2 |s| - mv) with a maximum mv of that exponent;
-// these weights are one float16 number each.
+// values' the weights, which are one float16 number each, relative to a maximum mv of x
+// + log2 |s|: of a bound of it, the largest x and the largest scale of a step, while
+// scales of a step lie within 2^kNear of one another, and of the maximum itself where
+// they do not.
 //
 // Work.  A (sequence, key head, tile of rows) is a unit; the steps of all units, laid
 // end to end, are cut into equal runs, one a block, found from the lengths on
@@ -47,6 +49,7 @@ constexpr int kTrLoaders = 4;    // warps
 constexpr int kTrSoft = 8;       // warps: two a 32 rows, each half of a step's slots
 constexpr int kTrMostRuns = 160;
 constexpr int kTrLeast = 2;      // steps of a run
+constexpr float kNear = 8.f, kFar = 60.f;  // log2 of scales that are near one another, and of ones that are not too far from 1
 
 struct TreeArgs {
     CacheArgs c;
@@ -161,6 +164,7 @@ struct TreeShared {
     float top[2][2][kTrRows], top_v[2][2][kTrRows];  // [step parity][half of the slots][row]
     float sum[2][kTrRows];
     uint32_t there[kTrAux][4];      // the slots of a step that exist and whose pages do
+    float2 range[kTrAux][kTrLoaders];  // E4M3: largest and least log2 of a step's values' scales, NaN for far ones
     float q_scale[2][kTrRows];      // E4M3: what a row of q was divided by
     TreeItem item[kTrItems];
 };
@@ -175,12 +179,6 @@ __device__ __forceinline__ float tr_max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
-}
-// Infinities as the largest number, NaN as it is.
-__device__ __forceinline__ float tr_finite(float x) {
-    float y;
-    asm("min.NaN.f32 %0, %1, 0f7F7FFFFF;" : "=f"(y) : "f"(x));
-    return y;
 }
 template <bool F16>
 __device__ __forceinline__ uint32_t tr_pack(float lo, float hi) {
@@ -205,10 +203,10 @@ __device__ __forceinline__ void tr_split(float lo, float hi, uint32_t *lead, uin
     }
     *rest = tr_pack<F16>(lo - v.x, hi - v.y);
 }
-__device__ __forceinline__ uint32_t tr_halves(uint32_t codes) {  // two E4M3 codes (the low 16 bits) as float16, exactly
-    uint32_t v;
-    asm("{.reg .b16 c; cvt.u16.u32 c, %1; cvt.rn.f16x2.e4m3x2 %0, c;}" : "=r"(v) : "r"(codes));
-    return v;
+__device__ __forceinline__ void tr_halves(uint32_t codes, uint32_t *lo, uint32_t *hi) {  // four E4M3 codes as float16, exactly
+    asm("{.reg .b16 c, d; mov.b32 {c, d}, %2; cvt.rn.f16x2.e4m3x2 %0, c; cvt.rn.f16x2.e4m3x2 %1, d;}"
+        : "=r"(*lo), "=r"(*hi)
+        : "r"(codes));
 }
 __device__ __forceinline__ void tr_copy16(uint32_t dst, const void *src, bool real) {  // zeros where there is nothing
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
@@ -550,10 +548,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                         const uint32_t *w = reinterpret_cast<const uint32_t *>(&x[i]);
                         uint32_t y[8];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            y[2 * e] = tr_halves(w[e]);
-                            y[2 * e + 1] = tr_halves(w[e] >> 16);
-                        }
+                        for (int e = 0; e < 4; ++e) tr_halves(w[e], &y[2 * e], &y[2 * e + 1]);
                         const uint32_t at = tile_at(slot, lw * RW + row, col);
                         st_shared16(at, make_uint4(y[0], y[1], y[2], y[3]));
                         st_shared16(at ^ 16, make_uint4(y[4], y[5], y[6], y[7]));  // (col is a multiple of 16)
@@ -652,17 +647,31 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
         bool q_due = false, end = false;
         int64_t v_off = -1, v_next = -1;   // rows of the values of the step whose keys were started last, and the one before
         uint32_t signs = 0, signs_next = 0;
-        int row = 0, page = -1;            // of this lane's slot, a step ahead
+        // of this lane's slots: pages two steps ahead, scales one
+        int row = 0, page = -1, row_next = 0, page_next = -1;
+        float ks = 0.f, vs = 0.f;
         auto page_id = [&](int j) {
             const int slot = slot_first + j * KEYS + lw * RW + lane;
-            page = -1;
+            page_next = -1;
             if (lane >= RW || j >= steps || slot >= n) return;
             const int at = static_cast<int>(fast_div(slot, a.c.page_div));
-            row = slot - at * a.c.page;
-            page = a.c.table[b * a.c.table_stride + at];
-            if (page >= 0 && page < a.c.n_pages) return;
-            page = -1;
+            row_next = slot - at * a.c.page;
+            page_next = a.c.table[b * a.c.table_stride + at];
+            if (page_next >= 0 && page_next < a.c.n_pages) return;
+            page_next = -1;
             note_error(LC_ERR_CACHE_INDEX, kClassTree);
+        };
+        auto turn_page = [&](int j) {  // step j's page and scales, and the next one's page asked for
+            page = page_next;
+            row = row_next;
+            if constexpr (Q8) {
+                ks = vs = 0.f;
+                if (page >= 0) {
+                    ks = a.c.ks[row_offset(a.c.kss, page, head, row)];
+                    vs = a.c.vs[row_offset(a.c.vss, page, head, row)];
+                }
+            }
+            page_id(j + 1);
         };
         // one thing after another -- a piece taken, its q, a tile started -- and then the tiles that have landed are
         // given on, all but the newest LAG, or all where the next thing is not to be had yet
@@ -751,6 +760,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                         steps = it->steps;
                         p = entry = 0;
                         page_id(0);
+                        turn_page(0);
                     }
                 }
             } else {
@@ -771,21 +781,26 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                         else reinterpret_cast<uint16_t *>(sh.there[x])[lw] = static_cast<uint16_t>(there);
                     }
                     if constexpr (Q8) {
-                        float ks = 0.f, vs = 0.f;
-                        if (page >= 0) {
-                            ks = a.c.ks[row_offset(a.c.kss, page, head, row)];
-                            vs = a.c.vs[row_offset(a.c.vss, page, head, row)];
-                        }
                         signs_next = __ballot_sync(0xffffffffu, vs < 0.f);
+                        float lv;
+                        asm("lg2.approx.f32 %0, %1;" : "=f"(lv) : "f"(fabsf(vs)));
                         if (lane < RW) {
-                            float lv;
-                            asm("lg2.approx.f32 %0, %1;" : "=f"(lv) : "f"(fabsf(vs)));
                             aux[(x * 3) * KEYS + lw * RW + lane] = ks;
                             aux[(x * 3 + 1) * KEYS + lw * RW + lane] = fabsf(vs);
                             aux[(x * 3 + 2) * KEYS + lw * RW + lane] = lv;
                         }
+                        // a step's largest logarithm, where they are all near one another (else NaN)
+                        const bool counts = page >= 0 && vs != 0.f;
+                        float most = counts ? lv : -INFINITY, least = counts ? lv : INFINITY;
+#pragma unroll
+                        for (int d = 16; d; d >>= 1) {
+                            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+                            least = fminf(least, __shfl_xor_sync(0xffffffffu, least, d));
+                        }
+                        const bool odd = __any_sync(0xffffffffu, counts && !(fabsf(lv) <= kFar));
+                        if (lane == 0) sh.range[x][lw] = odd ? make_float2(NAN, NAN) : make_float2(most, least);
                     }
-                    page_id(j + 1);
+                    turn_page(j + 1);
                     ++step_no;
                 } else {
                     const bool last = j + 1 == steps;
@@ -955,7 +970,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                     const float2 scale = make_float2(scale2, scale2);
                     // the logits, not scaled by scale2 yet, and the largest (a maximum passes NaN by: the weights will show it)
                     uint32_t x[HALF][32], bits[HALF];
-                    float tops[2] = {-INFINITY, -INFINITY}, tops_v[2] = {-INFINITY, -INFINITY};
+                    float tops[2] = {-INFINITY, -INFINITY};
 #pragma unroll
                     for (int c = 0; c < HALF; ++c) tc::ld32(x[c], s_at + (half * HALF + c) * 32);
 #pragma unroll
@@ -989,22 +1004,39 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                         for (int e = 0; e < 32; e += 4) {
                             tops[0] = tr_max3(tops[0], __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
                             tops[1] = tr_max3(tops[1], __uint_as_float(x[c][e + 2]), __uint_as_float(x[c][e + 3]));
-                            if constexpr (Q8) {
-                                const float4 s = *reinterpret_cast<const float4 *>(lv + s32 + e);
-                                const float2 u = tc::fma2(make_float2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])), scale, make_float2(s.x, s.y));
-                                const float2 v = tc::fma2(make_float2(__uint_as_float(x[c][e + 2]), __uint_as_float(x[c][e + 3])), scale, make_float2(s.z, s.w));
-                                tops_v[0] = tr_max3(tops_v[0], u.x, u.y);
-                                tops_v[1] = tr_max3(tops_v[1], v.x, v.y);
-                            }
                         }
                     }
-                    float top = fmaxf(tops[0], tops[1]), top_v = fmaxf(tops_v[0], tops_v[1]);
+                    float top = fmaxf(tops[0], tops[1]), top_v = 0.f;
+                    // E4M3: the largest logarithm of the step's scales; `wide` where they do not lie near one another
+                    float most = -INFINITY;
+                    bool wide = false;
+                    if constexpr (Q8) {
+                        float least = INFINITY;
+#pragma unroll
+                        for (int k = 0; k < kTrLoaders; ++k) {
+                            const float2 r = sh.range[x_at][k];
+                            wide |= !(r.x == r.x);
+                            most = fmaxf(most, r.x);
+                            least = fminf(least, r.y);
+                        }
+                        // (a maximum far from the logits' is one that such scales have left)
+                        wide |= most == -INFINITY || most - least > kNear ||
+                                __any_sync(0xffffffffu, real && mv != -INFINITY && !(fabsf(mv - m) <= kFar + 2 * kNear));
+                        if (wide) {
+                            top_v = -INFINITY;
+#pragma unroll
+                            for (int c = 0; c < HALF; ++c)
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)  // (-infinity where not seen, and no sum with infinity counts)
+                                    top_v = fmaxf(top_v, fmaf(__uint_as_float(x[c][e]), scale2, lv[(half * HALF + c) * 32 + e]));
+                        }
+                    }
                     const int turn = n_pair & 1;
                     sh.top[turn][half][row] = top;
-                    if constexpr (Q8) sh.top_v[turn][half][row] = top_v;
+                    if (Q8 && wide) sh.top_v[turn][half][row] = top_v;
                     if (!meet()) break;
                     top = fmaxf(top, sh.top[turn][1 - half][row]) * scale2;
-                    top_v = Q8 ? fmaxf(top_v, sh.top_v[turn][1 - half][row]) : top;
+                    top_v = !Q8 ? top : wide ? fmaxf(top_v, sh.top_v[turn][1 - half][row]) : top + most;
                     const bool rise = real && (top_v > mv + kRise || (mv == -INFINITY && top_v > mv));
                     if (Q8 && real && top > m) {
                         l *= tr_exp2(m - top);
@@ -1039,28 +1071,43 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                     // the weights of 32 slots take the columns of their logits: 16 of leading numbers, 16 of the rests
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                     const float2 off = make_float2(-less, -less);
-                    // E4M3: from a slot's weight to what multiplies its codes
-                    const float turn_v = tr_exp2(fminf(less - less_v, 126.f));
-                    const float2 to_v = make_float2(turn_v, turn_v);
-                    (void)to_v;
+                    // E4M3: weights relative to mv, for the sum too (its factor follows), but where scales are not near one
+                    // another: there each exponential of its own
+                    const float2 off_v = make_float2(-less_v, -less_v);
+                    (void)off_v;
 #pragma unroll
                     for (int c = 0; c < HALF; ++c) {
                         const int s32 = (half * HALF + c) * 32;
                         uint32_t p[16], rest[16];
+                        if (Q8 && wide) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            float2 y = tc::fma2(make_float2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])), scale, off);
-                            y.x = tr_exp2(y.x);
-                            y.y = tr_exp2(y.y);
-                            sum[e >> 1 & 1] = tc::add2(sum[e >> 1 & 1], y);
-                            if constexpr (Q8) {
-                                float2 v = tc::mul2(*reinterpret_cast<const float2 *>(vs + s32 + e), to_v);
-                                v.x = tr_finite(v.x);
-                                v.y = tr_finite(v.y);
-                                v = tc::mul2(v, y);
-                                p[e / 2] = tr_pack<true>(v.x, v.y);
-                            } else {
-                                tr_split<M16>(y.x, y.y, &p[e / 2], &rest[e / 2]);
+                            for (int e = 0; e < 32; e += 2) {
+                                const float2 z = make_float2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
+                                float2 y = tc::fma2(z, scale, off), v = tc::add2(tc::fma2(z, scale, off_v), *reinterpret_cast<const float2 *>(lv + s32 + e));
+                                y.x = tr_exp2(y.x);
+                                y.y = tr_exp2(y.y);
+                                sum[e >> 1 & 1] = tc::add2(sum[e >> 1 & 1], y);
+                                p[e / 2] = tr_pack<true>(tr_exp2(v.x), tr_exp2(v.y));
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+                                if constexpr (Q8) s = *reinterpret_cast<const float4 *>(vs + s32 + e);
+#pragma unroll
+                                for (int k = 0; k < 4; k += 2) {
+                                    float2 y = tc::fma2(make_float2(__uint_as_float(x[c][e + k]), __uint_as_float(x[c][e + k + 1])), scale,
+                                                        Q8 ? off_v : off);
+                                    y.x = tr_exp2(y.x);
+                                    y.y = tr_exp2(y.y);
+                                    sum[k / 2] = tc::add2(sum[k / 2], y);
+                                    if constexpr (Q8) {
+                                        const float2 v = tc::mul2(y, k ? make_float2(s.z, s.w) : make_float2(s.x, s.y));
+                                        p[(e + k) / 2] = tr_pack<true>(v.x, v.y);
+                                    } else {
+                                        tr_split<M16>(y.x, y.y, &p[(e + k) / 2], &rest[(e + k) / 2]);
+                                    }
+                                }
                             }
                         }
                         if constexpr (Q8) {
@@ -1074,7 +1121,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                         if constexpr (!Q8) tc::st16(s_at + s32 + 16, rest);
                     }
                     const float2 both = tc::add2(sum[0], sum[1]);
-                    l += both.x + both.y;
+                    l += (both.x + both.y) * (Q8 && !wide ? tr_exp2(less_v - less) : 1.f);
                     tc::wait_st();
                     tc::fence_before();
                 }
