@@ -2,6 +2,7 @@
 // entry points (lc_cache_attend_tree; the kernels are tree_attend.cuh).
 #include <cmath>
 
+#include "tensor_map.h"
 #include "tree_attend.cuh"
 
 namespace lc {
@@ -22,6 +23,28 @@ struct TreeSpace {
         end = split + units * 8;
     }
 };
+
+// Pages x heads x slots x head_dim, in boxes of `box` slots of one head (16-bit elements: 64 columns of them).
+bool map_pool(CUtensorMap *m, const lc_paged_cache &c, const void *p, const int64_t *st, int box) {
+    EncodeTiledFn encode = encode_tiled();
+    if (!encode) return false;
+    const bool q8 = c.type == LC_CACHE_E4M3;
+    const int64_t eb = q8 ? 1 : 2;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.head_dim), static_cast<cuuint64_t>(c.page_size),
+                                static_cast<cuuint64_t>(c.n_kv_heads), static_cast<cuuint64_t>(c.n_pages)};
+    const int64_t own = (c.head_dim * eb + 15) / 16 * 16;  // of a mode of one element, which has no stride
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.page_size > 1 ? st[2] * eb : own),
+                                   static_cast<cuuint64_t>(c.n_kv_heads > 1 ? st[1] * eb : own),
+                                   static_cast<cuuint64_t>(c.n_pages > 1 ? st[0] * eb : own)};
+    const cuuint32_t shape[4] = {static_cast<cuuint32_t>(q8 ? c.head_dim : 64), static_cast<cuuint32_t>(box), 1, 1};
+    const cuuint32_t one[4] = {1, 1, 1, 1};
+    const CUtensorMapDataType type = q8                          ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : c.type == LC_CACHE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                              : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    return encode(m, type, 4, const_cast<void *>(p), dims, strides, shape, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  q8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 int most_blocks(int64_t n_drafts, int group) { return static_cast<int>((n_drafts * group + kTrRows - 1) / kTrRows); }
 
@@ -109,6 +132,22 @@ extern "C" int lc_cache_attend_tree(const lc_paged_cache *cache, const lc_cache_
     a.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(q->workspace) + space.ml);
     a.split = reinterpret_cast<int2 *>(static_cast<uint8_t *>(q->workspace) + space.split);
     a.limit_ns = wait_limit_ns();
+    a.piece_div = make_fastdiv(static_cast<uint32_t>(std::max(a.c.dim / 16, 1)));
+    // Tensor copies where rows lie on 16-byte boundaries, pages are whole eights of slots (which the swizzle needs) and
+    // no stride is 0 or past what a tensor map holds: boxes of the largest power of two that divides a page and a step.
+    // Otherwise 16 bytes or an element at a time.
+    a.box = 1;
+    bool boxes = a.vec && cache->page_size % 8 == 0;
+    for (int i = 0; i < 3; ++i)
+        for (const int64_t *pst : {cache->k_stride, cache->v_stride})
+            if (pool[i] > 1 && (pst[i] == 0 || pst[i] >= int64_t(1) << 38)) boxes = false;
+    if (boxes) {
+        const int keys = a.c.dim <= 128 ? 128 : 64;
+        a.box = cache->page_size & -cache->page_size;
+        a.box = std::min(a.box, keys);
+        if (!map_pool(&a.km, *cache, cache->k, cache->k_stride, a.box) || !map_pool(&a.vm, *cache, cache->v, cache->v_stride, a.box))
+            a.box = 1;
+    }
     const auto launch = cache->type == LC_CACHE_BF16 ? launch_tree_bf16 : cache->type == LC_CACHE_F16 ? launch_tree_f16 : launch_tree_e4m3;
     return launch(a, reinterpret_cast<cudaStream_t>(stream));
 }

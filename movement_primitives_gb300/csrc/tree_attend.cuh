@@ -34,6 +34,8 @@
 // them a row's (each half of the slots; they exchange their maxima).
 #pragma once
 
+#include <cuda.h>
+
 #include "cache_common.cuh"
 #include "tensor_core.cuh"
 
@@ -69,7 +71,10 @@ struct TreeArgs {
     int2 *split;            // of a unit: its first and its last run
     float *part;            // [2 runs][dim / 4 rounded up to 16][128 rows][4]
     float2 *part_ml;        // [2 runs][128]
+    int32_t box;            // slots of a tensor copy
+    FastDiv piece_div;      // by the 16-byte pieces of a row of codes
     uint64_t limit_ns;
+    CUtensorMap km, vm;
 };
 
 // A sequence's share.
@@ -87,7 +92,7 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs &a, int b) {
     const int want = a.counts ? a.counts[b] : min(a.drafts, s.n);
     s.count = min(max(want, 0), min(a.drafts, s.n));
     if (s.count != want) note_error(LC_ERR_CACHE_INDEX, kClassTree);
-    s.begin = a.window ? max(s.n - s.count + 1 - a.window, 0) : 0;
+    s.begin = a.window ? max(s.n - s.count + 1 - a.window, 0) / a.box * a.box : 0;
     s.blocks = (s.count * a.group + kTrRows - 1) / kTrRows;
     s.steps = s.count ? (s.n - s.begin + KEYS - 1) / KEYS : 0;
     return s;
@@ -125,7 +130,6 @@ struct TreeItem {
     int32_t first, steps;
     int32_t part;               // where its part goes, -1 for a whole unit
     int32_t end;
-    int32_t bad_steps;
     uint32_t last_tile;
     int32_t bad_step[kTrMasked];
     uint32_t bad[kTrMasked][4];     // values that are not finite, of masked steps
@@ -156,6 +160,7 @@ struct TreeShape {
 struct TreeShared {
     uint64_t ring_full[12], ring_empty[12];
     uint64_t q_full, q_empty;
+    uint64_t raw_full[4], raw_empty[4];
     uint64_t s_full[2], p_full[2], o_full[2];  // of every other step
     uint64_t item_full[kTrItems], item_empty[kTrItems], kin_full[kTrItems];
     uint64_t pair[4];               // of the two warps of 32 rows
@@ -285,6 +290,34 @@ __device__ __forceinline__ void tree_kin(const TreeArgs &a, TreeItem &it) {
     }
 }
 
+// Values that are not finite become 0; whether there was one.
+template <int KV>
+__device__ __forceinline__ bool tree_clean(uint4 &x) {
+    uint32_t *w = reinterpret_cast<uint32_t *>(&x);
+    bool found = false;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if constexpr (KV == LC_CACHE_E4M3) {
+            const uint32_t nan = ((w[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+            if (nan) {
+                found = true;
+                w[e] &= ~(nan | (nan - (nan >> 7)));
+            }
+        } else {
+            constexpr uint32_t kExp = KV == LC_CACHE_F16 ? 0x7c00u : 0x7f80u;
+            if ((w[e] & kExp) == kExp) {
+                found = true;
+                w[e] &= 0xffff0000u;
+            }
+            if ((w[e] & kExp << 16) == kExp << 16) {
+                found = true;
+                w[e] &= 0xffffu;
+            }
+        }
+    }
+    return found;
+}
+
 // The values of a slot, and of an element 0 or what is not finite.
 template <int EB>
 __device__ __noinline__ const uint8_t *tree_value(const TreeArgs &a, int b, int head, int slot) {
@@ -304,12 +337,15 @@ __device__ __noinline__ float tree_unusual(const uint8_t *v, int e) {
     }
 }
 
-template <int KV, int NC>
+// TMA: pages come by tensor copies, a box of a page's slots each, which a warp issues (E4M3 ones go through four more
+// that convert them); else element by element or 16 bytes, by four warps.
+template <int KV, int NC, bool TMA>
 __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1)
     k_tree_attend(const __grid_constant__ TreeArgs a) {
     constexpr bool Q8 = KV == LC_CACHE_E4M3, M16 = KV != LC_CACHE_BF16;  // float16 products
     using S = TreeShape<NC, Q8>;
     constexpr int KEYS = S::KEYS, EB = Q8 ? 1 : 2;
+    constexpr int kIssuer = kTrSoft + kTrLoaders + 2;  // the warp that issues tensor copies
     // weights are up to 2^(kLift + kRise): float16 has few exponents, so small ones are lifted into them; others are
     // lowered, as sums are, so that those of the type's largest values stay in float32
     constexpr float kRise = M16 ? 6.f : 8.f, kLift = M16 ? 8.f : -40.f, kSumLift = Q8 ? 0.f : kLift;
@@ -325,10 +361,14 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
     if (warp == kTrSoft + kTrLoaders) tc::alloc(ptx::smem_addr(&sh.tmem), 512);
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::SLOTS; ++i) {
-            ptx::mbar_init(bar(sh.ring_full[i]), kTrLoaders);
+            ptx::mbar_init(bar(sh.ring_full[i]), TMA && !Q8 ? 1 : kTrLoaders);
             ptx::mbar_init(bar(sh.ring_empty[i]), 1);
         }
-        ptx::mbar_init(bar(sh.q_full), kTrLoaders);
+        ptx::mbar_init(bar(sh.q_full), TMA ? kTrSoft : kTrLoaders);
+        for (int i = 0; i < S::RAW; ++i) {
+            ptx::mbar_init(bar(sh.raw_full[i]), 1);
+            ptx::mbar_init(bar(sh.raw_empty[i]), kTrLoaders);
+        }
         ptx::mbar_init(bar(sh.q_empty), 1);
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(bar(sh.s_full[i]), 1);
@@ -337,7 +377,8 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
         }
         for (int i = 0; i < kTrItems; ++i) {
             ptx::mbar_init(bar(sh.item_full[i]), 1);
-            ptx::mbar_init(bar(sh.item_empty[i]), kTrSoft + kTrLoaders + 1);
+            // the softmax's, the products', and what brings the tiles
+            ptx::mbar_init(bar(sh.item_empty[i]), kTrSoft + 1 + (TMA ? 1 + (Q8 ? kTrLoaders : 0) : kTrLoaders));
             ptx::mbar_init(bar(sh.kin_full[i]), 1);
             ptx::mbar_init(bar(sh.pair[i]), 2);
         }
@@ -441,7 +482,6 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                         it.steps = take;
                         it.part = take == steps ? -1 : 2 * static_cast<int>(blockIdx.x) + (first == 0);
                         it.end = 0;
-                        it.bad_steps = 0;
                     }
                     if (lane < 4 * kTrMasked) it.bad[lane / 4][lane % 4] = 0;
                     __syncwarp();
@@ -451,8 +491,200 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
             at += __shfl_sync(0xffffffffu, upto, 31);
         }
         if (ok) post([&](TreeItem &it) { if (lane == 0) it.end = 1; });
-    } else if (warp >= kTrSoft && warp < kTrSoft + kTrLoaders) {
+    } else if (TMA && warp == kIssuer) {
         few_registers();
+        if constexpr (TMA) {
+            // tensor copies: a lane looks after 4 (2) slots, and issues the box that begins with them
+            constexpr int G = KEYS / 32;
+            uint32_t tiles = 0, step_no = 0;
+            int b = 0, head = 0, n = 0, slot_first = 0, steps = 0;
+            int page = 0, row = 0, page_next = 0, row_next = 0, page_v = 0, row_v = 0;  // (n_pages: nowhere, read as zeros)
+            const int nowhere = static_cast<int>(a.c.n_pages);
+            float ks[G], vs[G];
+            auto page_id = [&](int j) {
+                const int slot = slot_first + j * KEYS + lane * G;
+                page_next = nowhere;
+                row_next = 0;
+                if (j >= steps || slot >= n) return;
+                const int at = static_cast<int>(fast_div(slot, a.c.page_div));
+                row_next = slot - at * a.c.page;
+                page_next = a.c.table[b * a.c.table_stride + at];
+                if (page_next >= 0 && page_next < a.c.n_pages) return;
+                page_next = nowhere;
+                note_error(LC_ERR_CACHE_INDEX, kClassTree);
+            };
+            auto turn_page = [&](int j) {  // step j's page and scales, and the next one's page asked for
+                page = page_next;
+                row = row_next;
+                if constexpr (Q8) {
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        ks[g] = vs[g] = 0.f;
+                        if (page != nowhere && slot_first + j * KEYS + lane * G + g < n) {
+                            ks[g] = a.c.ks[row_offset(a.c.kss, page, head, row + g)];
+                            vs[g] = a.c.vs[row_offset(a.c.vss, page, head, row + g)];
+                        }
+                    }
+                }
+                page_id(j + 1);
+            };
+            const bool leads = lane * G % a.box == 0;
+            const uint32_t tile_bytes = Q8 ? KEYS * a.c.dim : S::TILE;
+            auto issue = [&](const CUtensorMap &map, int at_page, int at_row) {
+                __syncwarp();
+                const uint32_t full = Q8 ? bar(sh.raw_full[0]) + tiles % (S::RAW ? S::RAW : 1) * 8 : bar(sh.ring_full[0]) + tiles % S::SLOTS * 8;
+                if (lane == 0) ptx::mbar_arrive_expect_tx(full, tile_bytes);
+                __syncwarp();
+                if (leads) {
+                    if constexpr (Q8) {
+                        ptx::tma_load_4d(raw_s + tiles % S::RAW * S::RAW_TILE + lane * G * a.c.dim, &map, 0, at_row, head, at_page, full);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < NC; ++c)
+                            ptx::tma_load_4d(ring_s + tiles % S::SLOTS * S::TILE + c * S::CHUNK + lane * G * 128, &map, c * 64,
+                                             at_row, head, at_page, full);
+                    }
+                }
+                __syncwarp();
+                ++tiles;
+            };
+            auto room = [&] {  // for the next tile
+                constexpr uint32_t M = Q8 ? (S::RAW ? S::RAW : 1) : S::SLOTS;
+                return tiles < M || wait_warp(*((Q8 ? sh.raw_empty : sh.ring_empty) + tiles % M), tiles / M - 1);
+            };
+            for (uint32_t i = 0; ok; ++i) {
+                if (!wait_warp(sh.item_full[i % kTrItems], i / kTrItems)) break;
+                const TreeItem &it = sh.item[i % kTrItems];
+                if (it.end) break;
+                b = it.b;
+                head = it.head;
+                n = it.n;
+                slot_first = it.begin + it.first * KEYS;
+                steps = it.steps;
+                arrive_warp(sh.item_empty[i % kTrItems]);
+                page_id(0);
+                turn_page(0);
+#pragma unroll 1
+                for (int p = 0; p < 2 * steps; ++p) {  // K0 K1 V0 K2 V1 ...
+                    if (!room()) break;
+                    const bool is_k = p == 0 || (p & 1 && p < 2 * steps - 1);
+                    if (is_k) {
+                        const int j = (p + 1) / 2, slot0 = slot_first + j * KEYS, x = step_no % kTrAux;
+                        // which slots there are: bits of those before the end whose pages there are
+                        const uint32_t pages = __ballot_sync(0xffffffffu, page != nowhere);
+                        if (lane < KEYS / 32) {
+                            uint32_t bits = 0;
+#pragma unroll
+                            for (int k = 0; k < 32 / G; ++k)
+                                if (pages >> (lane * (32 / G) + k) & 1) bits |= ((1u << G) - 1) << k * G;
+                            const int left = n - slot0 - lane * 32;
+                            sh.there[x][lane] = bits & (left >= 32 ? 0xffffffffu : left <= 0 ? 0u : 0xffffffffu >> (32 - left));
+                        }
+                        if constexpr (Q8) {
+                            float most = -INFINITY, least = INFINITY;
+                            bool odd = false;
+#pragma unroll
+                            for (int g = 0; g < G; ++g) {
+                                float lv;
+                                asm("lg2.approx.f32 %0, %1;" : "=f"(lv) : "f"(fabsf(vs[g])));
+                                aux[(x * 3) * KEYS + lane * G + g] = ks[g];
+                                aux[(x * 3 + 1) * KEYS + lane * G + g] = vs[g];
+                                aux[(x * 3 + 2) * KEYS + lane * G + g] = lv;
+                                if (page != nowhere && vs[g] != 0.f) {
+                                    most = fmaxf(most, lv);
+                                    least = fminf(least, lv);
+                                    odd |= !(fabsf(lv) <= kFar);
+                                }
+                            }
+                            // by quarters of the warp: the largest and the least, NaN where there is a far one
+#pragma unroll
+                            for (int d = 4; d; d >>= 1) {
+                                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+                                least = fminf(least, __shfl_xor_sync(0xffffffffu, least, d));
+                            }
+                            odd = __any_sync(0xffffffffu, odd);
+                            if (lane % 8 == 0) sh.range[x][lane / 8] = odd ? make_float2(NAN, NAN) : make_float2(most, least);
+                        }
+                        const int k_page = page, k_row = row;
+                        if (p == 0) {
+                            page_v = page;
+                            row_v = row;
+                        }
+                        turn_page(j + 1);
+                        ++step_no;
+                        issue(a.km, k_page, k_row);
+                        if (p > 0) {  // the values of the step before follow, then this step's are next
+                            if (!room()) break;
+                            issue(a.vm, page_v, row_v);
+                            page_v = k_page;
+                            row_v = k_row;
+                            ++p;
+                        }
+                    } else {
+                        issue(a.vm, page_v, row_v);
+                    }
+                }
+            }
+            // copies in flight end before the block does
+            ok = true;
+            constexpr uint32_t M = Q8 ? (S::RAW ? S::RAW : 1) : S::SLOTS;
+            for (uint32_t k = tiles > M ? tiles - M : 0; k < tiles; ++k)
+                wait_warp(*((Q8 ? sh.raw_full : sh.ring_full) + k % M), k / M);
+        }
+    } else if (TMA && Q8 && warp >= kTrSoft && warp < kTrSoft + kTrLoaders) {
+        few_registers();
+        if constexpr (TMA && Q8) {
+            // codes to float16: every lane the same pieces of a tile, 16 codes each
+            const int lw = warp - kTrSoft, pieces = KEYS * a.c.dim / 16;
+            uint32_t tiles = 0;
+            for (uint32_t i = 0; ok; ++i) {
+                if (!wait_warp(sh.item_full[i % kTrItems], i / kTrItems)) break;
+                TreeItem &it = sh.item[i % kTrItems];
+                if (it.end) break;
+                const int steps = it.steps, slot_first = it.begin + it.first * KEYS;
+                int entry = 0;
+#pragma unroll 1
+                for (int p = 0; p < 2 * steps; ++p, ++tiles) {
+                    const uint32_t slot = tiles % S::SLOTS, raw = tiles % S::RAW;
+                    if (!wait_warp(sh.raw_full[raw], tiles / S::RAW)) break;
+                    if (tiles >= S::SLOTS && !wait_warp(sh.ring_empty[slot], tiles / S::SLOTS - 1)) break;
+                    int where = -1;
+                    if (p && (!(p & 1) || p == 2 * steps - 1)) {  // values
+                        const int slot0 = slot_first + (p == 2 * steps - 1 ? steps - 1 : p / 2 - 1) * KEYS;
+                        if (masked(it, slot0) && entry < kTrMasked) where = entry++;
+                    }
+                    const uint32_t from = raw_s + raw * S::RAW_TILE, to = ring_s + slot * S::TILE;
+#pragma unroll 1
+                    for (int k0 = lw * 32 + lane; k0 < pieces; k0 += 4 * 32 * kTrLoaders) {
+                        uint4 x[4];
+#pragma unroll
+                        for (int g = 0; g < 4; ++g)
+                            if (k0 + g * 32 * kTrLoaders < pieces) x[g] = ld_shared16(from + (k0 + g * 32 * kTrLoaders) * 16);
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            const int k = k0 + g * 32 * kTrLoaders;
+                            if (k >= pieces) break;
+                            const int row = static_cast<int>(fast_div(k, a.piece_div)), piece = k - row * static_cast<int>(a.piece_div.d);
+                            if (where >= 0 && tree_clean<KV>(x[g])) atomicOr(&it.bad[where][row >> 5], 1u << (row & 31));
+                            const uint32_t *w = reinterpret_cast<const uint32_t *>(&x[g]);
+                            uint32_t y[8];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) tr_halves(w[e], &y[2 * e], &y[2 * e + 1]);
+                            const uint32_t at = to + piece / 4 * S::CHUNK + row * 128 + ((piece & 3) * 2 ^ (row & 7)) * 16;
+                            st_shared16(at, make_uint4(y[0], y[1], y[2], y[3]));
+                            st_shared16(at ^ 16, make_uint4(y[4], y[5], y[6], y[7]));
+                        }
+                    }
+                    tc::fence_async_smem();
+                    arrive_warp(sh.ring_full[slot]);
+                    if (lane == 0) arrive(sh.raw_empty[raw]);
+                }
+                arrive_warp(sh.item_empty[i % kTrItems]);
+            }
+        }
+    } else if (!TMA && warp >= kTrSoft && warp < kTrSoft + kTrLoaders) {
+        few_registers();
+        if constexpr (!TMA) {
         // loads
         constexpr int RW = KEYS / kTrLoaders, PR = S::TILE / KEYS / 16 * EB / 2;  // rows of a warp, 16-byte pieces of a row
         constexpr int ITER = RW * PR / 32;
@@ -460,15 +692,9 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
         const uint8_t *const pool[2] = {a.c.k, a.c.v};
         uint32_t issued = 0, given = 0, n_q = 0;  // tiles started and given to the products, tiles of q
         uint32_t back = 0, done = 0;              // items given back, and whose tiles have all been started
-        // of the tiles under way: values of masked steps (item * kTrMasked + entry, else -1); E4M3 values: the warp's rows
-        // whose scale is negative
-        int32_t note[S::LAG + 1];
-        uint32_t flip[S::LAG + 1];
+        int32_t note[S::LAG + 1];  // of the tiles under way: values of masked steps (item * kTrMasked + entry, else -1)
 #pragma unroll
-        for (int i = 0; i <= S::LAG; ++i) {
-            note[i] = -1;
-            flip[i] = 0;
-        }
+        for (int i = 0; i <= S::LAG; ++i) note[i] = -1;
         auto piece_of = [&](int i, int *row, int *col) {  // i-th piece of this lane: row of the warp, first element
             const int at = i * 32 + lane;
             *row = at / PR;
@@ -479,28 +705,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
         };
         // looks a masked step's values through: what is not finite becomes 0 and is noted
         auto look = [&](uint4 &x, int where, int row) {
-            uint32_t *w = reinterpret_cast<uint32_t *>(&x);
-            bool found = false;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if constexpr (Q8) {
-                    const uint32_t nan = ((w[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-                    if (nan) {
-                        found = true;
-                        w[e] &= ~(nan | (nan - (nan >> 7)));
-                    }
-                } else {
-                    constexpr uint32_t kExp = M16 ? 0x7c00u : 0x7f80u;
-                    if ((w[e] & kExp) == kExp) {
-                        found = true;
-                        w[e] &= 0xffff0000u;
-                    }
-                    if ((w[e] & kExp << 16) == kExp << 16) {
-                        found = true;
-                        w[e] &= 0xffffu;
-                    }
-                }
-            }
+            const bool found = tree_clean<KV>(x);
             if (found) atomicOr(&sh.item[where / kTrMasked].bad[where % kTrMasked][row >> 5], 1u << (row & 31));
             return found;
         };
@@ -508,31 +713,19 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
         auto give = [&]() {
             const uint32_t slot = given % S::SLOTS;
             const int32_t where = note[0];
-            const uint32_t signs = flip[0];
 #pragma unroll
-            for (int i = 0; i < S::LAG; ++i) {
-                note[i] = note[i + 1];
-                flip[i] = flip[i + 1];
-            }
+            for (int i = 0; i < S::LAG; ++i) note[i] = note[i + 1];
             if constexpr (Q8) {
                 if (given >= S::SLOTS && !wait_warp(sh.ring_empty[slot], given / S::SLOTS - 1)) return;
-                // (unseen values' NaN and negative scales are rare: they are mended before and after)
                 const uint32_t from = raw_s + given % S::RAW * S::RAW_TILE + (lw * ITER * 32 + lane) * 16;
-                if (where >= 0 || signs) {
+                if (where >= 0) {
 #pragma unroll 1
                     for (int i = 0; i < ITER; ++i) {
                         int row, col;
                         piece_of(i, &row, &col);
                         if (col >= dim16) continue;
                         uint4 x = ld_shared16(from + i * 512);
-                        if (where >= 0) look(x, where, lw * RW + row);
-                        if (signs >> row & 1) {
-                            x.x ^= 0x80808080u;
-                            x.y ^= 0x80808080u;
-                            x.z ^= 0x80808080u;
-                            x.w ^= 0x80808080u;
-                        }
-                        st_shared16(from + i * 512, x);
+                        if (look(x, where, lw * RW + row)) st_shared16(from + i * 512, x);
                     }
                 }
 #pragma unroll
@@ -585,7 +778,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
             spot[i] = tile_at(0, lw * RW + row, first_col) - ring_s;
         }
         // starts a tile of pool w from the rows at `from`
-        auto start = [&](int w, int64_t from, int32_t where, uint32_t signs) {
+        auto start = [&](int w, int64_t from, int32_t where) {
             const uint32_t slot = issued % S::SLOTS;
             if (!Q8 && issued >= S::SLOTS && !wait_warp(sh.ring_empty[slot], issued / S::SLOTS - 1)) return;
             if (32 % PR == 0 && plain && __all_sync(0xffffffffu, from >= 0 || lane >= RW)) {
@@ -633,10 +826,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
             ptx::cp_async_commit();
 #pragma unroll
             for (int i = 0; i <= S::LAG; ++i)
-                if (issued - given == static_cast<uint32_t>(i)) {
-                    note[i] = where;
-                    flip[i] = signs;
-                }
+                if (issued - given == static_cast<uint32_t>(i)) note[i] = where;
             ++issued;
         };
         uint32_t step_no = 0;  // steps of all pieces
@@ -646,7 +836,6 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
         int b = 0, head = 0, n = 0, slot_first = 0, steps = 0, p = 0, entry = 0;
         bool q_due = false, end = false;
         int64_t v_off = -1, v_next = -1;   // rows of the values of the step whose keys were started last, and the one before
-        uint32_t signs = 0, signs_next = 0;
         // of this lane's slots: pages two steps ahead, scales one
         int row = 0, page = -1, row_next = 0, page_next = -1;
         float ks = 0.f, vs = 0.f;
@@ -768,11 +957,9 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                 const int j = is_k ? (p + 1) / 2 : p == 2 * steps - 1 ? steps - 1 : p / 2 - 1;
                 int64_t from;
                 int32_t where = -1;
-                uint32_t sign = 0;
                 if (is_k) {
                     from = page >= 0 ? row_offset(a.c.kst, page, head, row) : -1;
                     v_off = v_next;
-                    signs = signs_next;
                     v_next = page >= 0 ? row_offset(a.c.vst, page, head, row) : -1;
                     const int x = step_no % kTrAux;
                     const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
@@ -781,12 +968,11 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                         else reinterpret_cast<uint16_t *>(sh.there[x])[lw] = static_cast<uint16_t>(there);
                     }
                     if constexpr (Q8) {
-                        signs_next = __ballot_sync(0xffffffffu, vs < 0.f);
                         float lv;
                         asm("lg2.approx.f32 %0, %1;" : "=f"(lv) : "f"(fabsf(vs)));
                         if (lane < RW) {
                             aux[(x * 3) * KEYS + lw * RW + lane] = ks;
-                            aux[(x * 3 + 1) * KEYS + lw * RW + lane] = fabsf(vs);
+                            aux[(x * 3 + 1) * KEYS + lw * RW + lane] = vs;
                             aux[(x * 3 + 2) * KEYS + lw * RW + lane] = lv;
                         }
                         // a step's largest logarithm, where they are all near one another (else NaN)
@@ -805,13 +991,10 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                 } else {
                     const bool last = j + 1 == steps;
                     from = last ? v_next : v_off;
-                    sign = last ? signs_next : signs;
                     const int slot0 = slot_first + j * KEYS;
                     if (masked(*it, slot0) && entry < kTrMasked) {
                         where = static_cast<int>((i - 1) % kTrItems) * kTrMasked + entry;
-                        if (lw == 0 && lane == 0) it->bad_step[entry] = slot0;
                         ++entry;
-                        if (lw == 0 && lane == 0) it->bad_steps = entry;
                     }
                     if (last) {  // before it is started: that may give the item back
                         if (lane == 0) it->last_tile = issued + 1;  // (every warp the same)
@@ -819,7 +1002,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                         ++done;
                     }
                 }
-                start(is_k ? 0 : 1, from, where, sign);
+                start(is_k ? 0 : 1, from, where);
                 if (!ok) break;
                 q_due = p == 0;
                 ++p;
@@ -836,6 +1019,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
             }
         }
         ptx::cp_async_wait<0>();
+        }
     } else if (warp == kTrSoft + kTrLoaders) {
         few_registers();
         // products, by the whole warp
@@ -908,7 +1092,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                                        keys + k / 4 * (S::CHUNK / 16) + (k & 3) * 2, qk, k > 0);
                     tc::commit(bar(sh.s_full[0]) + to * 8);
                     tc::commit(bar(sh.ring_empty[0]) + sk * 8);
-                    if (j + 1 == steps) tc::commit(bar(sh.q_empty));
+                    if (!TMA && j + 1 == steps) tc::commit(bar(sh.q_empty));
                 }
                 if (j >= 2) tc::commit(bar(sh.ring_empty[0]) + sv * 8);
             }
@@ -924,7 +1108,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
         constexpr int HALF = KEYS / 64;  // 32-slot pieces of a half
         const int half = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter) << 21);
-        uint32_t n_s = 0, n_pair = 0;
+        uint32_t n_s = 0, n_pair = 0, ring = 0;
         // the two warps of 32 rows have both written what the other reads
         auto meet = [&] {
             arrive_warp(sh.pair[quarter]);
@@ -932,10 +1116,64 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
         };
         for (uint32_t i = 0; ok; ++i) {
             if (!wait_warp(sh.item_full[i % kTrItems], i / kTrItems)) break;
-            const TreeItem &it = sh.item[i % kTrItems];
+            TreeItem &it = sh.item[i % kTrItems];
             if (it.end) break;
-            if (!wait_warp(sh.kin_full[i % kTrItems], i / kTrItems)) break;
+            if (!TMA && !wait_warp(sh.kin_full[i % kTrItems], i / kTrItems)) break;
             const int steps = it.steps, slot_first = it.begin + it.first * KEYS, before = it.n - it.count;
+            const uint32_t ring0 = ring;
+            ring += 2 * steps;
+            int n_bad = 0;
+            if constexpr (TMA) {
+                // the rows of q, 16 a warp (the products that read the last ones have ended with that piece)
+                constexpr int RQ = kTrRows / kTrSoft, PQ = NC * 8;
+                auto q_row = [&](int r, bool *there) {
+                    const int at = it.row0 + warp * RQ + r, t = static_cast<int>(fast_div(at, a.group_div)), g = at - t * a.group;
+                    *there = t < it.count;
+                    return a.q + it.b * a.qst[0] + t * a.qst[1] + (int64_t(it.head) * a.group + g) * a.qst[2];
+                };
+                auto q_at = [&](int r, int piece) {
+                    return q_s + piece / 8 * S::QCHUNK + (warp * RQ + r) * 128 + ((piece & 7) ^ (r & 7)) * 16;
+                };
+                auto q_piece = [&](int r, int col) {
+                    bool there;
+                    const uint16_t *from = q_row(r, &there);
+                    if (!there || col >= a.c.dim) return make_uint4(0, 0, 0, 0);
+                    if (a.q_vec) return *reinterpret_cast<const uint4 *>(from + col);
+                    return tree_piece<2>(reinterpret_cast<const uint8_t *>(from), col, a.c.dim);
+                };
+#pragma unroll 1
+                for (int r0 = 0; r0 < RQ; r0 += 8) {
+                    uint4 x[Q8 ? 8 : 2 * NC];
+                    if constexpr (!Q8) {
+#pragma unroll
+                        for (int k = 0; k < 2 * NC; ++k) x[k] = q_piece(r0 + (k * 32 + lane) / PQ, (k * 32 + lane) % PQ * 8);
+#pragma unroll
+                        for (int k = 0; k < 2 * NC; ++k) st_shared16(q_at(r0 + (k * 32 + lane) / PQ, (k * 32 + lane) % PQ), x[k]);
+                    } else {
+                        // bfloat16 to float16 of a row whose largest element is between 1 and 2
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) x[r] = q_piece(r0 + r, lane * 8);
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) {
+                            uint32_t *w = reinterpret_cast<uint32_t *>(&x[r]);
+                            uint32_t most = 0;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) most = max(most, max(w[e] << 16 & 0x7fffffffu, w[e] & 0x7fff0000u));
+                            most = __reduce_max_sync(0xffffffffu, most);
+                            const int ex = min(max(static_cast<int>(most >> 23) - 127, -126), 126);
+                            const float div = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                w[e] = tr_pack<true>(__uint_as_float(w[e] << 16) * div, __uint_as_float(w[e] & 0xffff0000u) * div);
+                            if (lane == 0) sh.q_scale[i & 1][warp * RQ + r0 + r] = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+                            if (lane < PQ) st_shared16(q_at(r0 + r, lane), x[r]);
+                        }
+                    }
+                }
+                tc::fence_async_smem();
+                arrive_warp(sh.q_full);
+                if (!wait_warp(sh.kin_full[i % kTrItems], i / kTrItems)) break;
+            }
             const int at = it.row0 + row, t = static_cast<int>(fast_div(at, a.group_div)), g = at - t * a.group;
             const bool real = t < it.count;
             const bool some = __any_sync(0xffffffffu, real);
@@ -959,6 +1197,31 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                 const int x_at = n_s % kTrAux;
                 ++n_s;
                 if (Q8 && j == 0) scale2 = a.scale2 * sh.q_scale[i & 1][row];
+                if (masked(it, slot0) && n_bad < kTrMasked) {
+                    if constexpr (TMA && !Q8) {
+                        // values that some row does not see are multiplied by weights of 0 there: what is not finite becomes 0,
+                        // and is added at the end where it is seen.  (What their place in the ring held before has been used.)
+                        if (half == 0 && row < KEYS) {
+                            const uint32_t place = ring0 + (j + 1 < steps ? 2 * j + 2 : 2 * j + 1), v_at = ring_s + place % S::SLOTS * S::TILE;
+                            if (!wait_warp(sh.ring_full[place % S::SLOTS], place / S::SLOTS)) break;
+                            bool found = false;
+#pragma unroll 1
+                            for (int c = 0; c < NC * 8; ++c) {
+                                const uint32_t piece = v_at + c / 8 * S::CHUNK + row * 128 + ((c & 7) ^ (row & 7)) * 16;
+                                uint4 v = ld_shared16(piece);
+                                if (tree_clean<KV>(v)) {
+                                    st_shared16(piece, v);
+                                    found = true;
+                                }
+                            }
+                            const uint32_t rows = __ballot_sync(0xffffffffu, found);
+                            if (lane == 0) it.bad[n_bad][quarter] = rows;
+                            tc::fence_async_smem();
+                        }
+                    }
+                    if (lane == 0 && warp == 0) it.bad_step[n_bad] = slot0;
+                    ++n_bad;
+                }
                 if (some) {
                     tc::fence_after();
                     const bool cut = masked(it, slot0);
@@ -1087,7 +1350,8 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                                 y.x = tr_exp2(y.x);
                                 y.y = tr_exp2(y.y);
                                 sum[e >> 1 & 1] = tc::add2(sum[e >> 1 & 1], y);
-                                p[e / 2] = tr_pack<true>(tr_exp2(v.x), tr_exp2(v.y));
+                                const float2 sv = *reinterpret_cast<const float2 *>(vs + s32 + e);
+                                p[e / 2] = tr_pack<true>(copysignf(tr_exp2(v.x), sv.x), copysignf(tr_exp2(v.y), sv.y));
                             }
                         } else {
 #pragma unroll
@@ -1149,7 +1413,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                     tc::wait_ld(o);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = none ? 0u : __float_as_uint(__uint_as_float(o[e]) * f);
-                    for (int n = 0; n < it.bad_steps; ++n)
+                    for (int n = 0; n < n_bad; ++n)
 #pragma unroll 1
                         for (int w = 0; w < 4; ++w)
 #pragma unroll 1
@@ -1275,7 +1539,8 @@ __global__ void __launch_bounds__(256) k_tree_join(const __grid_constant__ TreeA
 template <int KV, int NC>
 int launch_tree_shape(const TreeArgs &a, cudaStream_t cs) {
     using S = TreeShape<NC, KV == LC_CACHE_E4M3>;
-    const void *fn = reinterpret_cast<const void *>(&k_tree_attend<KV, NC>);
+    const void *fn = a.box > 1 ? reinterpret_cast<const void *>(&k_tree_attend<KV, NC, true>)
+                               : reinterpret_cast<const void *>(&k_tree_attend<KV, NC, false>);
     int sms = 0, per_sm = 0;
     if (prepare(fn, S::THREADS, S::SMEM, S::SMEM, &sms, &per_sm) != cudaSuccess) return LC_ERR_CUDA;
     TreeArgs b = a;
