@@ -243,7 +243,8 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
     const uint32_t base = (ptx::smem_addr(raw) + 1023) & ~1023u;
     const uint32_t q_s = base, ring_s = base + S::Q;
     PromptShared &sh = *reinterpret_cast<PromptShared *>(raw + (base - ptx::smem_addr(raw)) + S::Q + S::SLOTS * S::SLOT);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (shuffled, so that the compiler knows a warp's branches on it to be the whole warp's)
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     auto bar = [&](const uint64_t &b) { return ptx::smem_addr(&b); };
 
     if (warp == S::SOFT) tc::alloc(ptx::smem_addr(&sh.tmem), 512);
@@ -276,28 +277,16 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
     const uint32_t tmem = sh.tmem;
     start_after_prior();
 
-    bool ok = true;  // no wait of this thread has run out
-    auto wait = [&](const uint64_t &b, uint32_t n) {  // for phase n (counted from 0)
-        if (ok && !ptx::mbar_wait_step(bar(b), n & 1, a.limit_ns)) {
+    bool ok = true;  // no wait of this warp has run out
+    auto arrive_warp = [&](const uint64_t &b) { tc::arrive(bar(b)); };
+    auto wait_warp = [&](const uint64_t &b, uint32_t n) {  // for phase n (counted from 0)
+        if (ok && !tc::wait(bar(b), n, a.limit_ns)) {
             ok = false;
             note_error(LC_ERR_TIMEOUT, kClassPrompt);
         }
         return ok;
     };
-    // a warp's wait: one lane polls, for the others' polls take turns with what else the shared memory does
-    auto wait_warp = [&](const uint64_t &b, uint32_t n) {
-        if (lane == 0) wait(b, n);
-        ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0);
-        return ok;
-    };
-    auto arrive = [&](const uint64_t &b) {
-        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar(b)) : "memory");
-    };
 
-    auto arrive_warp = [&](const uint64_t &b) {
-        __syncwarp();
-        if (lane == 0) arrive(b);
-    };
     // of a block's registers the softmax threads take the larger part (384 x 168 = 256 x 216 + 128 x 72)
     auto few_registers = [] {
         if constexpr (TILES == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
@@ -312,8 +301,7 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
         for (uint32_t i = 0; ok; ++i) {
             if (!wait_warp(sh.item_full[i % kPrItems], i / kPrItems)) break;
             const PromptItem it = sh.item[i % kPrItems];
-            __syncwarp();
-            if (lane == 0) arrive(sh.item_empty[i % kPrItems]);
+            arrive_warp(sh.item_empty[i % kPrItems]);
             if (it.end) break;
             const uint32_t p0 = pos;
             pos += 2 * it.steps;
@@ -458,16 +446,14 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
                     if (c == 1) {
                         tc::wait_st();
                         tc::fence_before();
-                        __syncwarp();
-                        if (lane == 0) arrive(sh.p_half[buf]);
+                        arrive_warp(sh.p_half[buf]);
                     }
                 }
                 const float2 both = tc::add2(sum[0], sum[1]);
                 l += both.x + both.y;
                 tc::wait_st();
                 tc::fence_before();
-                __syncwarp();
-                if (lane == 0) arrive(sh.p_full[buf]);
+                arrive_warp(sh.p_full[buf]);
             }
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
@@ -546,72 +532,69 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
             prompt_item<TILES>(a, at, &it);
             const int s = i % kPrItems;
             if (i >= kPrItems && !wait_warp(sh.item_empty[s], i / kPrItems - 1)) break;
-            if (lane == 0) {
-                sh.item[s] = it;
-                arrive(sh.item_full[s]);
-            }
-            __syncwarp();
+            if (lane == 0) sh.item[s] = it;
+            arrive_warp(sh.item_full[s]);
             if (it.end) break;
         }
     } else if (warp == S::SOFT + 1) {
         few_registers();
-        // loads
-        if (lane == 0) {
-            uint32_t pos = 0, tiles_q[2] = {0, 0};
-            for (uint32_t i = 0;; ++i) {
-                if (!wait(sh.item_full[i % kPrItems], i / kPrItems)) break;
-                const PromptItem it = sh.item[i % kPrItems];
-                arrive(sh.item_empty[i % kPrItems]);
-                if (it.end) break;
-                if (!it.steps) continue;
-                auto load_q = [&](int t) {
-                    if (it.t0 + t * a.tokens_tile >= it.nq) return;
-                    if (tiles_q[t] && !wait(sh.q_empty[t], tiles_q[t] - 1)) return;
-                    ++tiles_q[t];
-                    ptx::mbar_arrive_expect_tx(bar(sh.q_full[t]), NC * 128 * a.heads_tile * a.tokens_tile);
+        // loads, by the whole warp
+        uint32_t slot = 0, round = 0, tiles_q[2] = {0, 0};  // the next slot of the ring, how often it has been used
+        for (uint32_t i = 0;; ++i) {
+            if (!wait_warp(sh.item_full[i % kPrItems], i / kPrItems)) break;
+            const PromptItem &item = sh.item[i % kPrItems];
+            const uint32_t end = (item.end), steps = (item.steps), key_head = (item.key_head);
+            const int head0 = key_head * a.group + (item.head0);
+            const int q0 = (item.q0 + item.t0), left = (item.nq - item.t0);
+            const int key0 = (item.k0 + item.first * kPrKeys);
+            arrive_warp(sh.item_empty[i % kPrItems]);
+            if (end) break;
+            if (!steps) continue;
+            auto load_q = [&](int t) {
+                if (t * a.tokens_tile >= left) return;
+                if (tiles_q[t] && !wait_warp(sh.q_empty[t], tiles_q[t] - 1)) return;
+                ++tiles_q[t];
+                tc::expect(bar(sh.q_full[t]), NC * 128 * a.heads_tile * a.tokens_tile);
 #pragma unroll
-                    for (int c = 0; c < NC; ++c)
-                        ptx::tma_load_3d(q_s + (t * NC + c) * kPrChunk, &a.qm, c * 64, it.key_head * a.group + it.head0,
-                                         it.q0 + it.t0 + t * a.tokens_tile, bar(sh.q_full[t]));
-                };
-                auto load_tile = [&](const CUtensorMap &m, int j) {
+                for (int c = 0; c < NC; ++c)
+                    tc::load_3d(q_s + (t * NC + c) * kPrChunk, &a.qm, c * 64, head0, q0 + t * a.tokens_tile, bar(sh.q_full[t]));
+            };
+            auto load_tile = [&](const CUtensorMap &m, uint32_t j) {
 #pragma unroll
-                    for (int p = 0; p < S::SPT; ++p, ++pos) {
-                        const uint32_t s = pos % S::SLOTS, n = pos / S::SLOTS;
-                        if (n && !wait(sh.ring_empty[s], n - 1)) return;
-                        if (!ok) return;
-                        ptx::mbar_arrive_expect_tx(bar(sh.ring_full[s]), S::SLOT);
+                for (int p = 0; p < S::SPT; ++p) {
+                    if (!ok || (round && !wait_warp(sh.ring_empty[slot], round - 1))) return;
+                    const uint32_t full = bar(sh.ring_full[0]) + slot * 8;
+                    tc::expect(full, S::SLOT);
 #pragma unroll
-                        for (int c = 0; c < S::CPS; ++c)
-                            ptx::tma_load_3d(ring_s + s * S::SLOT + c * kPrChunk, &m, (p * S::CPS + c) * 64, it.key_head,
-                                             it.k0 + (it.first + j) * kPrKeys, bar(sh.ring_full[s]));
+                    for (int c = 0; c < S::CPS; ++c)
+                        tc::load_3d(ring_s + slot * S::SLOT + c * kPrChunk, &m, (p * S::CPS + c) * 64, key_head,
+                                    key0 + j * kPrKeys, full);
+                    if (++slot == S::SLOTS) {
+                        slot = 0;
+                        ++round;
                     }
-                };
-                load_q(0);
-                load_tile(a.km, 0);
-                if constexpr (TILES == 2) {
-                    load_q(1);
-                    load_tile(a.vm, 0);
-                    for (int j = 1; j < it.steps && ok; ++j) {
-                        load_tile(a.km, j);
-                        load_tile(a.vm, j);
-                    }
-                } else {
-                    for (int j = 1; j < it.steps && ok; ++j) {
-                        load_tile(a.km, j);
-                        load_tile(a.vm, j - 1);
-                    }
-                    load_tile(a.vm, it.steps - 1);
                 }
-                if (!ok) break;
+            };
+            load_q(0);
+            load_tile(a.km, 0);
+            if constexpr (TILES == 2) load_q(1);
+#pragma unroll 1
+            for (uint32_t j = 0; j < steps && ok; ++j) {  // K0 V0 K1 V1 ..., with one tile K0 K1 V0 K2 V1 ...
+                if (j) load_tile(a.km, j);
+                if constexpr (TILES == 2) load_tile(a.vm, j);
+                else if (j) load_tile(a.vm, j - 1);
             }
-            if (!ok) {  // copies in flight end before the block does
-                ok = true;
-                for (uint32_t p = pos > S::SLOTS ? pos - S::SLOTS : 0; p < pos; ++p)
-                    wait(sh.ring_full[p % S::SLOTS], p / S::SLOTS);
-                for (int t = 0; t < TILES; ++t)
-                    if (tiles_q[t]) wait(sh.q_full[t], tiles_q[t] - 1);
+            if constexpr (TILES == 1) load_tile(a.vm, steps - 1);
+            if (!ok) break;
+        }
+        if (!ok) {  // copies in flight end before the block does
+            ok = true;
+            for (uint32_t s = 0; s < S::SLOTS; ++s) {
+                const uint32_t used = round + (s < slot);
+                if (used) wait_warp(sh.ring_full[s], used - 1);
             }
+            for (int t = 0; t < TILES; ++t)
+                if (tiles_q[t]) wait_warp(sh.q_full[t], tiles_q[t] - 1);
         }
     } else if (warp == S::SOFT || (TILES == 2 && warp == S::SOFT + 3)) {
         few_registers();
@@ -619,7 +602,7 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
         // the other's products run; the tiles take turns, else both come to do their softmax at the same time and leave
         // the tensor cores idle meanwhile (a fifth slower, as is one warp for both).
         const int t = warp != S::SOFT;
-        const uint32_t tm = tc::uniform(tmem);
+        const uint32_t tm = (tmem);
         const uint32_t q_desc = tc::smem_desc(q_s, 16), k_desc = tc::smem_desc(ring_s, 16);
         const uint32_t v_desc = tc::smem_desc(ring_s, kPrChunk);
         const uint32_t qk = tc::instr_desc(F16, kPrKeys, false, a.negative);
@@ -627,22 +610,10 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
         // of the values' columns a full slot, and what is left for the last
         const uint32_t pv_full = tc::instr_desc(F16, S::CPS * 64, true, false);
         const uint32_t pv_last = tc::instr_desc(F16, (a.dim - (NC - S::CPS) * 64 + 15) / 16 * 16, true, false);
-        // waits by votes, so that what follows is known to be the warp's
         auto wait_all = [&](const uint64_t &b, uint32_t n) {
-            if (!ok) return false;
-            uint64_t t0 = 0;
-#pragma unroll 1
-            for (uint32_t polls = 0; !__all_sync(0xffffffffu, ptx::mbar_sleep_wait(bar(b), n & 1)); ++polls) {
-                const uint64_t t = ptx::global_timer_ns();
-                if (!t0) t0 = t;
-                if (__any_sync(0xffffffffu, t - t0 > a.limit_ns || polls > ptx::kMaxPolls)) {
-                    if (lane == 0) note_error(LC_ERR_TIMEOUT, kClassPrompt);
-                    ok = false;
-                    return false;
-                }
-            }
+            wait_warp(b, n);
             tc::fence_after();
-            return true;
+            return ok;
         };
         // tiles come in the order in which they are used: their first slot and the phase of its barriers
         uint32_t slot = 0, phase = 0;
@@ -700,8 +671,8 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
         for (uint32_t i = 0;; ++i) {
             if (!wait_all(sh.item_full[i % kPrItems], i / kPrItems)) break;
             const PromptItem &it = sh.item[i % kPrItems];
-            const uint32_t end = tc::uniform(it.end), steps = tc::uniform(it.steps);
-            const uint32_t two = tc::uniform(TILES == 2 && it.t0 + a.tokens_tile < it.nq);
+            const uint32_t end = (it.end), steps = (it.steps);
+            const uint32_t two = (TILES == 2 && it.t0 + a.tokens_tile < it.nq);
             arrive_warp(sh.item_empty[i % kPrItems]);
             if (end) break;
             if (!steps) continue;

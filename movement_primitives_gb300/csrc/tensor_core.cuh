@@ -27,12 +27,30 @@ __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::aft
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // The calls below are a whole warp's, converged; one elected lane of it issues the
-// instruction.  Their operands come from uniform registers: values that are the
-// warp's own (uniform() of what was loaded, and what is computed from such values under
-// votes) get there in one step, others take some 100 cycles an instruction to issue.
+// instruction, by a predicate.  A branch that one lane takes may leave the warp in two
+// parts that go on one after the other and meet at every vote and shuffle, some 250
+// cycles each; so waits are by votes too.
 
-// A value that all lanes hold alike, as the compiler can know it.
-__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_or_sync(0xffffffffu, x); }
+// Waits for the barrier phase n (counted from 0), all lanes alike; false after limit_ns.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t n, uint64_t limit_ns) {
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t polls = 0; !__all_sync(0xffffffffu, ptx::mbar_sleep_wait(bar, n & 1)); ++polls) {
+        const uint64_t t = ptx::global_timer_ns();
+        if (!t0) t0 = t;
+        if (__any_sync(0xffffffffu, t - t0 > limit_ns || polls > ptx::kMaxPolls)) return false;
+    }
+    return true;
+}
+
+// One arrival for what all lanes have done before.
+__device__ __forceinline__ void arrive(uint32_t bar) {
+    __syncwarp();
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar)
+        : "memory");
+}
 
 // One arrival on `bar` when all matrix instructions issued before have finished.
 __device__ __forceinline__ void commit(uint32_t bar) {
@@ -48,6 +66,32 @@ __device__ __forceinline__ void commit(uint32_t bar) {
 // low word of the descriptor: bytes / 16 may be added to it.
 __device__ __forceinline__ uint32_t smem_desc(uint32_t addr, uint32_t across) { return addr >> 4 | across >> 4 << 16; }
 constexpr uint32_t kDescHigh = (1024 >> 4) | 1u << 14 | 2u << 29;
+
+// Tensor copies (see ptx.cuh) and the bytes that they are to bring.
+__device__ __forceinline__ void expect(uint32_t bar, uint32_t bytes) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+        "r"(bytes)
+        : "memory");
+}
+__device__ __forceinline__ void load_3d(uint32_t dst, const void *tmap, int32_t c0, int32_t c1, int32_t c2, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(dst),
+        "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void load_4d(uint32_t dst, const void *tmap, int32_t c0, int32_t c1, int32_t c2, int32_t c3,
+                                        uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];\n\t}" ::"r"(dst),
+        "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        : "memory");
+}
 
 // d[128, N] (+)= a[128, 16] b[16, N]; a from shared memory or from tensor memory.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {

@@ -355,7 +355,8 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
     uint8_t *const after = raw_smem + (base - ptx::smem_addr(raw_smem)) + S::Q + S::SLOTS * S::TILE + S::RAW * S::RAW_TILE;
     TreeShared &sh = *reinterpret_cast<TreeShared *>(after);
     float *const aux = reinterpret_cast<float *>(after + 11264);  // E4M3: [kTrAux][keys' scales, values', log2 of those][KEYS]
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (shuffled, so that the compiler knows a warp's branches on it to be the whole warp's)
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     auto bar = [&](const uint64_t &b) { return ptx::smem_addr(&b); };
 
     if (warp == kTrSoft + kTrLoaders) tc::alloc(ptx::smem_addr(&sh.tmem), 512);
@@ -389,34 +390,18 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
     __syncthreads();
     tc::fence_after();
     const uint32_t tmem = sh.tmem;
-    start_after_prior();
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // (the joining blocks come when this one ends)
 
-    bool ok = true;  // no wait of this thread has run out
-    auto wait = [&](const uint64_t &b, uint32_t n) {  // for phase n (counted from 0)
-        if (ok && !ptx::mbar_wait_step(bar(b), n & 1, a.limit_ns)) {
+    bool ok = true;  // no wait of this warp has run out
+    auto arrive_warp = [&](const uint64_t &b) { tc::arrive(bar(b)); };
+    auto wait_warp = [&](const uint64_t &b, uint32_t n) {  // for phase n (counted from 0)
+        if (ok && !tc::wait(bar(b), n, a.limit_ns)) {
             ok = false;
             note_error(LC_ERR_TIMEOUT, kClassTree);
         }
         return ok;
     };
-    // a warp's wait: one lane polls, for the others' polls take turns with what else the shared memory does
-    auto wait_warp = [&](const uint64_t &b, uint32_t n) {
-        if (lane == 0) wait(b, n);
-        ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0);
-        return ok;
-    };
-    auto done_warp = [&](const uint64_t &b, uint32_t n) {
-        int d = 0;
-        if (lane == 0) d = ptx::mbar_try_wait(bar(b), n & 1);
-        return __shfl_sync(0xffffffffu, d, 0) != 0;
-    };
-    auto arrive = [&](const uint64_t &b) {
-        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar(b)) : "memory");
-    };
-    auto arrive_warp = [&](const uint64_t &b) {
-        __syncwarp();
-        if (lane == 0) arrive(b);
-    };
+    auto done_warp = [&](const uint64_t &b, uint32_t n) { return __all_sync(0xffffffffu, ptx::mbar_try_wait(bar(b), n & 1)) != 0; };
     // whether some row of a piece sees a step in part
     auto masked = [&](const TreeItem &it, int slot0) {
         return slot0 + KEYS > it.n - it.count || (a.window && slot0 < it.n - it.count + kTrDrafts - a.window);
@@ -496,7 +481,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
         if constexpr (TMA) {
             // tensor copies: a lane looks after 4 (2) slots, and issues the box that begins with them
             constexpr int G = KEYS / 32;
-            uint32_t tiles = 0, step_no = 0;
+            uint32_t step_no = 0;
             int b = 0, head = 0, n = 0, slot_first = 0, steps = 0;
             int page = 0, row = 0, page_next = 0, row_next = 0, page_v = 0, row_v = 0;  // (n_pages: nowhere, read as zeros)
             const int nowhere = static_cast<int>(a.c.n_pages);
@@ -528,39 +513,43 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                 }
                 page_id(j + 1);
             };
-            const bool leads = lane * G % a.box == 0;
             const uint32_t tile_bytes = Q8 ? KEYS * a.c.dim : S::TILE;
+            const int boxes = KEYS / a.box, lanes_box = a.box / G;
+            constexpr uint32_t M = Q8 ? (S::RAW ? S::RAW : 1) : S::SLOTS;  // tiles under way at most
+            uint32_t at = 0, round = 0;  // the next tile's place among them, and how often that has been used
             auto issue = [&](const CUtensorMap &map, int at_page, int at_row) {
                 __syncwarp();
-                const uint32_t full = Q8 ? bar(sh.raw_full[0]) + tiles % (S::RAW ? S::RAW : 1) * 8 : bar(sh.ring_full[0]) + tiles % S::SLOTS * 8;
-                if (lane == 0) ptx::mbar_arrive_expect_tx(full, tile_bytes);
-                __syncwarp();
-                if (leads) {
+                const uint32_t full = bar(Q8 ? sh.raw_full[0] : sh.ring_full[0]) + at * 8;
+                tc::expect(full, tile_bytes);
+                const uint32_t dst = Q8 ? raw_s + at * S::RAW_TILE : ring_s + at * S::TILE;
+#pragma unroll 1
+                for (int k = 0; k < boxes; ++k) {
+                    const int pg = __shfl_sync(0xffffffffu, at_page, k * lanes_box);
+                    const int rw = __shfl_sync(0xffffffffu, at_row, k * lanes_box);
                     if constexpr (Q8) {
-                        ptx::tma_load_4d(raw_s + tiles % S::RAW * S::RAW_TILE + lane * G * a.c.dim, &map, 0, at_row, head, at_page, full);
+                        tc::load_4d(dst + k * a.box * a.c.dim, &map, 0, rw, head, pg, full);
                     } else {
 #pragma unroll
-                        for (int c = 0; c < NC; ++c)
-                            ptx::tma_load_4d(ring_s + tiles % S::SLOTS * S::TILE + c * S::CHUNK + lane * G * 128, &map, c * 64,
-                                             at_row, head, at_page, full);
+                        for (int c = 0; c < NC; ++c) tc::load_4d(dst + c * S::CHUNK + k * a.box * 128, &map, c * 64, rw, head, pg, full);
                     }
                 }
-                __syncwarp();
-                ++tiles;
+                if (++at == M) {
+                    at = 0;
+                    ++round;
+                }
             };
             auto room = [&] {  // for the next tile
-                constexpr uint32_t M = Q8 ? (S::RAW ? S::RAW : 1) : S::SLOTS;
-                return tiles < M || wait_warp(*((Q8 ? sh.raw_empty : sh.ring_empty) + tiles % M), tiles / M - 1);
+                return round == 0 || wait_warp(*((Q8 ? sh.raw_empty : sh.ring_empty) + at), round - 1);
             };
             for (uint32_t i = 0; ok; ++i) {
                 if (!wait_warp(sh.item_full[i % kTrItems], i / kTrItems)) break;
                 const TreeItem &it = sh.item[i % kTrItems];
                 if (it.end) break;
-                b = it.b;
-                head = it.head;
-                n = it.n;
-                slot_first = it.begin + it.first * KEYS;
-                steps = it.steps;
+                b = (it.b);
+                head = (it.head);
+                n = (it.n);
+                slot_first = (it.begin + it.first * KEYS);
+                steps = (it.steps);
                 arrive_warp(sh.item_empty[i % kTrItems]);
                 page_id(0);
                 turn_page(0);
@@ -627,9 +616,10 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
             }
             // copies in flight end before the block does
             ok = true;
-            constexpr uint32_t M = Q8 ? (S::RAW ? S::RAW : 1) : S::SLOTS;
-            for (uint32_t k = tiles > M ? tiles - M : 0; k < tiles; ++k)
-                wait_warp(*((Q8 ? sh.raw_full : sh.ring_full) + k % M), k / M);
+            for (uint32_t k = 0; k < M; ++k) {
+                const uint32_t used = round + (k < at);
+                if (used) wait_warp(*((Q8 ? sh.raw_full : sh.ring_full) + k), used - 1);
+            }
         }
     } else if (TMA && Q8 && warp >= kTrSoft && warp < kTrSoft + kTrLoaders) {
         few_registers();
@@ -677,7 +667,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                     }
                     tc::fence_async_smem();
                     arrive_warp(sh.ring_full[slot]);
-                    if (lane == 0) arrive(sh.raw_empty[raw]);
+                    arrive_warp(sh.raw_empty[raw]);
                 }
                 arrive_warp(sh.item_empty[i % kTrItems]);
             }
@@ -1023,27 +1013,15 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
     } else if (warp == kTrSoft + kTrLoaders) {
         few_registers();
         // products, by the whole warp
-        const uint32_t tm = tc::uniform(tmem);
+        const uint32_t tm = (tmem);
         const uint32_t q_desc = tc::smem_desc(q_s, 16), k_desc = tc::smem_desc(ring_s, 16), v_desc = tc::smem_desc(ring_s, S::CHUNK);
         const uint32_t qk = tc::instr_desc(M16, KEYS, false, a.negative);
         const uint32_t pv = tc::instr_desc(M16, (a.c.dim + 15) / 16 * 16, true, false);
         const int k_steps = (a.c.dim + 15) / 16;
-        // waits by votes, so that what follows is known to be the warp's
         auto wait_all = [&](const uint64_t &b, uint32_t n) {
-            if (!ok) return false;
-            uint64_t t0 = 0;
-#pragma unroll 1
-            for (uint32_t polls = 0; !__all_sync(0xffffffffu, ptx::mbar_sleep_wait(bar(b), n & 1)); ++polls) {
-                const uint64_t t = ptx::global_timer_ns();
-                if (!t0) t0 = t;
-                if (__any_sync(0xffffffffu, t - t0 > a.limit_ns || polls > ptx::kMaxPolls)) {
-                    if (lane == 0) note_error(LC_ERR_TIMEOUT, kClassTree);
-                    ok = false;
-                    return false;
-                }
-            }
+            wait_warp(b, n);
             tc::fence_after();
-            return true;
+            return ok;
         };
         // tiles come in the order in which they are used, K0 K1 V0 K2 V1 ...
         uint32_t slot = 0, phase = 0, n_q = 0, n_p = 0;
@@ -1058,7 +1036,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
         };
         for (uint32_t i = 0;; ++i) {
             if (!wait_all(sh.item_full[i % kTrItems], i / kTrItems)) break;
-            const uint32_t steps = tc::uniform(sh.item[i % kTrItems].steps), end = tc::uniform(sh.item[i % kTrItems].end);
+            const uint32_t steps = (sh.item[i % kTrItems].steps), end = (sh.item[i % kTrItems].end);
             arrive_warp(sh.item_empty[i % kTrItems]);
             if (end) break;
             const uint32_t t0 = n_p;  // steps before this piece: the S buffers go on in turn
