@@ -485,30 +485,31 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
             int b = 0, head = 0, n = 0, slot_first = 0, steps = 0;
             int page = 0, row = 0, page_next = 0, row_next = 0, page_v = 0, row_v = 0;  // (n_pages: nowhere, read as zeros)
             const int nowhere = static_cast<int>(a.c.n_pages);
+            bool here_next = false;
             float ks[G], vs[G];
+            const int64_t last_at = int64_t(a.c.n_seqs - 1) * a.c.table_stride + a.c.per - 1;  // of the table
             auto page_id = [&](int j) {
                 const int slot = slot_first + j * KEYS + lane * G;
-                page_next = nowhere;
-                row_next = 0;
-                if (j >= steps || slot >= n) return;
+                const bool here = j < steps && slot < n;
                 const int at = static_cast<int>(fast_div(slot, a.c.page_div));
-                row_next = slot - at * a.c.page;
-                page_next = a.c.table[b * a.c.table_stride + at];
-                if (page_next >= 0 && page_next < a.c.n_pages) return;
-                page_next = nowhere;
-                note_error(LC_ERR_CACHE_INDEX, kClassTree);
+                row_next = here ? slot - at * a.c.page : 0;
+                page_next = a.c.table[here ? b * a.c.table_stride + at : last_at];
+                here_next = here;
             };
             auto turn_page = [&](int j) {  // step j's page and scales, and the next one's page asked for
-                page = page_next;
+                const bool good = page_next >= 0 && page_next < a.c.n_pages;
+                if (__any_sync(0xffffffffu, here_next && !good)) note_error(LC_ERR_CACHE_INDEX, kClassTree);
+                page = here_next && good ? page_next : nowhere;
                 row = row_next;
                 if constexpr (Q8) {
+                    const int from = page != nowhere ? page : 0;
+                    const int64_t k_at = row_offset(a.c.kss, from, head, row), v_at = row_offset(a.c.vss, from, head, row);
 #pragma unroll
                     for (int g = 0; g < G; ++g) {
-                        ks[g] = vs[g] = 0.f;
-                        if (page != nowhere && slot_first + j * KEYS + lane * G + g < n) {
-                            ks[g] = a.c.ks[row_offset(a.c.kss, page, head, row + g)];
-                            vs[g] = a.c.vs[row_offset(a.c.vss, page, head, row + g)];
-                        }
+                        const bool there = page != nowhere && slot_first + j * KEYS + lane * G + g < n;
+                        const float k = a.c.ks[k_at + g * a.c.kss[2]], v = a.c.vs[v_at + g * a.c.vss[2]];
+                        ks[g] = there ? k : 0.f;
+                        vs[g] = there ? v : 0.f;
                     }
                 }
                 page_id(j + 1);
@@ -560,15 +561,13 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                     if (is_k) {
                         const int j = (p + 1) / 2, slot0 = slot_first + j * KEYS, x = step_no % kTrAux;
                         // which slots there are: bits of those before the end whose pages there are
-                        const uint32_t pages = __ballot_sync(0xffffffffu, page != nowhere);
-                        if (lane < KEYS / 32) {
-                            uint32_t bits = 0;
+                        const uint32_t pages = __ballot_sync(0xffffffffu, page != nowhere), word = lane % (KEYS / 32);
+                        uint32_t bits = 0;
 #pragma unroll
-                            for (int k = 0; k < 32 / G; ++k)
-                                if (pages >> (lane * (32 / G) + k) & 1) bits |= ((1u << G) - 1) << k * G;
-                            const int left = n - slot0 - lane * 32;
-                            sh.there[x][lane] = bits & (left >= 32 ? 0xffffffffu : left <= 0 ? 0u : 0xffffffffu >> (32 - left));
-                        }
+                        for (int k = 0; k < 32 / G; ++k) bits |= (pages >> (word * (32 / G) + k) & 1) * (((1u << G) - 1) << k * G);
+                        const int left = min(max(n - slot0 - static_cast<int>(word) * 32, 0), 32);
+                        bits &= left ? 0xffffffffu >> (32 - left) : 0u;
+                        sh.there[x][word] = bits;  // (eight lanes the same)
                         if constexpr (Q8) {
                             float most = -INFINITY, least = INFINITY;
                             bool odd = false;
