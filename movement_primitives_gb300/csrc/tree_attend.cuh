@@ -297,23 +297,16 @@ __device__ __forceinline__ bool tree_clean(uint4 &x) {
     bool found = false;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
+        uint32_t off;  // of the elements that are not finite, all bits
         if constexpr (KV == LC_CACHE_E4M3) {
             const uint32_t nan = ((w[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-            if (nan) {
-                found = true;
-                w[e] &= ~(nan | (nan - (nan >> 7)));
-            }
+            off = nan | (nan - (nan >> 7));
         } else {
             constexpr uint32_t kExp = KV == LC_CACHE_F16 ? 0x7c00u : 0x7f80u;
-            if ((w[e] & kExp) == kExp) {
-                found = true;
-                w[e] &= 0xffff0000u;
-            }
-            if ((w[e] & kExp << 16) == kExp << 16) {
-                found = true;
-                w[e] &= 0xffffu;
-            }
+            off = ((w[e] & kExp) == kExp ? 0xffffu : 0u) | ((w[e] & kExp << 16) == kExp << 16 ? 0xffff0000u : 0u);
         }
+        found |= off != 0;
+        w[e] &= ~off;
     }
     return found;
 }
@@ -643,18 +636,31 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                         if (masked(it, slot0) && entry < kTrMasked) where = entry++;
                     }
                     const uint32_t from = raw_s + raw * S::RAW_TILE, to = ring_s + slot * S::TILE;
+                    if (where >= 0) {
 #pragma unroll 1
-                    for (int k0 = lw * 32 + lane; k0 < pieces; k0 += 4 * 32 * kTrLoaders) {
+                        for (int k = lw * 32 + lane; k < pieces; k += 32 * kTrLoaders) {
+                            uint4 x = ld_shared16(from + k * 16);
+                            if (tree_clean<KV>(x)) {
+                                const int row = static_cast<int>(fast_div(k, a.piece_div));
+                                atomicOr(&it.bad[where][row >> 5], 1u << (row & 31));
+                                st_shared16(from + k * 16, x);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    // (lanes past the last piece convert that one too: no branch parts the warp)
+#pragma unroll 1
+                    for (int k0 = lw * 32 + lane; k0 < pieces + lane; k0 += 4 * 32 * kTrLoaders) {
                         uint4 x[4];
-#pragma unroll
-                        for (int g = 0; g < 4; ++g)
-                            if (k0 + g * 32 * kTrLoaders < pieces) x[g] = ld_shared16(from + (k0 + g * 32 * kTrLoaders) * 16);
+                        int k[4];
 #pragma unroll
                         for (int g = 0; g < 4; ++g) {
-                            const int k = k0 + g * 32 * kTrLoaders;
-                            if (k >= pieces) break;
-                            const int row = static_cast<int>(fast_div(k, a.piece_div)), piece = k - row * static_cast<int>(a.piece_div.d);
-                            if (where >= 0 && tree_clean<KV>(x[g])) atomicOr(&it.bad[where][row >> 5], 1u << (row & 31));
+                            k[g] = min(k0 + g * 32 * kTrLoaders, pieces - 1);
+                            x[g] = ld_shared16(from + k[g] * 16);
+                        }
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            const int row = static_cast<int>(fast_div(k[g], a.piece_div)), piece = k[g] - row * static_cast<int>(a.piece_div.d);
                             const uint32_t *w = reinterpret_cast<const uint32_t *>(&x[g]);
                             uint32_t y[8];
 #pragma unroll
@@ -1183,13 +1189,19 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                             if (!wait_warp(sh.ring_full[place % S::SLOTS], place / S::SLOTS)) break;
                             bool found = false;
 #pragma unroll 1
-                            for (int c = 0; c < NC * 8; ++c) {
-                                const uint32_t piece = v_at + c / 8 * S::CHUNK + row * 128 + ((c & 7) ^ (row & 7)) * 16;
-                                uint4 v = ld_shared16(piece);
-                                if (tree_clean<KV>(v)) {
-                                    st_shared16(piece, v);
-                                    found = true;
+                            for (int c = 0; c < NC; ++c) {
+                                const uint32_t piece = v_at + c * S::CHUNK + row * 128;
+                                uint4 v[8];
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) v[k] = ld_shared16(piece + (k ^ (row & 7)) * 16);
+                                bool bad = false;
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) bad |= tree_clean<KV>(v[k]);
+                                if (bad) {
+#pragma unroll
+                                    for (int k = 0; k < 8; ++k) st_shared16(piece + (k ^ (row & 7)) * 16, v[k]);
                                 }
+                                found |= bad;
                             }
                             const uint32_t rows = __ballot_sync(0xffffffffu, found);
                             if (lane == 0) it.bad[n_bad][quarter] = rows;
