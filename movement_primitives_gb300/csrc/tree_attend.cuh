@@ -100,11 +100,11 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs &a, int b) {
 
 // Steps of all units, by a warp.
 template <int KEYS>
-__device__ __forceinline__ int tree_steps(const TreeArgs &a) {
+__device__ __forceinline__ int tree_steps(const TreeArgs &a, const TreeSeq &first) {  // (of the sequence of this lane's number)
     const int lane = threadIdx.x & 31;
-    int all = 0;
+    int all = first.steps * first.blocks * a.c.heads;
 #pragma unroll 1
-    for (int b = lane; b < a.c.n_seqs; b += 32) {
+    for (int b = lane + 32; b < a.c.n_seqs; b += 32) {
         const TreeSeq s = tree_seq<KEYS>(a, b);
         all += s.steps * s.blocks * a.c.heads;
     }
@@ -330,6 +330,63 @@ __device__ __noinline__ float tree_unusual(const uint8_t *v, int e) {
     }
 }
 
+// The rows of q of a piece into shared memory, RQ a warp from row0 on: float16 copies of bfloat16 rows for E4M3 caches,
+// divided by a power of two so that a row's largest element is between 1 and 2 (`scale`: by which).
+template <int KV, int NC, int RQ>
+__device__ __forceinline__ void tree_query(const TreeArgs &a, const TreeItem &it, int row0, uint32_t q_s, float *scale) {
+    constexpr bool Q8 = KV == LC_CACHE_E4M3;
+    constexpr int PQ = NC * 8, CHUNK = kTrRows * 128;  // 16-byte pieces of a row; bytes of 64 columns
+    const int lane = threadIdx.x & 31;
+    auto q_at = [&](int r, int piece) {
+        return q_s + piece / 8 * CHUNK + (row0 + r) * 128 + ((piece & 7) ^ (r & 7)) * 16;
+    };
+    auto q_piece = [&](int r, int col) {
+        const int at = it.row0 + row0 + r, t = static_cast<int>(fast_div(at, a.group_div)), g = at - t * a.group;
+        const bool real = t < it.count && col < a.c.dim;
+        const uint16_t *from = a.q + (real ? it.b * a.qst[0] + t * a.qst[1] + (int64_t(it.head) * a.group + g) * a.qst[2] + col : 0);
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (a.q_vec) {
+            if (real) x = *reinterpret_cast<const uint4 *>(from);
+        } else if (real) {
+            x = tree_piece<2>(reinterpret_cast<const uint8_t *>(from - col), col, a.c.dim);
+        }
+        return x;
+    };
+    if constexpr (!Q8) {
+#pragma unroll 1
+        for (int r0 = 0; r0 < RQ; r0 += 16) {  // 16 rows on the way at once, 4 NC pieces a lane
+            uint4 x[4 * NC];
+#pragma unroll
+            for (int k = 0; k < 4 * NC; ++k) x[k] = q_piece(r0 + (k * 32 + lane) / PQ, (k * 32 + lane) % PQ * 8);
+#pragma unroll
+            for (int k = 0; k < 4 * NC; ++k) st_shared16(q_at(r0 + (k * 32 + lane) / PQ, (k * 32 + lane) % PQ), x[k]);
+        }
+    } else {
+#pragma unroll 1
+        for (int r0 = 0; r0 < RQ; r0 += 8) {
+            uint4 x[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) x[r] = q_piece(r0 + r, lane * 8);
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                uint32_t *w = reinterpret_cast<uint32_t *>(&x[r]);
+                uint32_t most = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) most = max(most, max(w[e] << 16 & 0x7fffffffu, w[e] & 0x7fff0000u));
+                most = __reduce_max_sync(0xffffffffu, most);
+                const int ex = min(max(static_cast<int>(most >> 23) - 127, -126), 126);
+                const float div = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[e] = tr_pack<true>(__uint_as_float(w[e] << 16) * div, __uint_as_float(w[e] & 0xffff0000u) * div);
+                scale[row0 + r0 + r] = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);  // (by all lanes)
+                if (lane < PQ) st_shared16(q_at(r0 + r, lane), x[r]);
+            }
+        }
+    }
+    tc::fence_async_smem();
+}
+
 // TMA: pages come by tensor copies, a box of a page's slots each, which a warp issues (E4M3 ones go through four more
 // that convert them); else element by element or 16 bytes, by four warps.
 template <int KV, int NC, bool TMA>
@@ -358,7 +415,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
             ptx::mbar_init(bar(sh.ring_full[i]), TMA && !Q8 ? 1 : kTrLoaders);
             ptx::mbar_init(bar(sh.ring_empty[i]), 1);
         }
-        ptx::mbar_init(bar(sh.q_full), TMA ? kTrSoft : kTrLoaders);
+        ptx::mbar_init(bar(sh.q_full), kTrLoaders);
         for (int i = 0; i < S::RAW; ++i) {
             ptx::mbar_init(bar(sh.raw_full[i]), 1);
             ptx::mbar_init(bar(sh.raw_empty[i]), kTrLoaders);
@@ -372,7 +429,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
         for (int i = 0; i < kTrItems; ++i) {
             ptx::mbar_init(bar(sh.item_full[i]), 1);
             // the softmax's, the products', and what brings the tiles
-            ptx::mbar_init(bar(sh.item_empty[i]), kTrSoft + 1 + (TMA ? 1 + (Q8 ? kTrLoaders : 0) : kTrLoaders));
+            ptx::mbar_init(bar(sh.item_empty[i]), kTrSoft + 1 + kTrLoaders + TMA);
             ptx::mbar_init(bar(sh.kin_full[i]), 1);
             ptx::mbar_init(bar(sh.pair[i]), 2);
         }
@@ -383,7 +440,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
     __syncthreads();
     tc::fence_after();
     const uint32_t tmem = sh.tmem;
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // (the joining blocks come when this one ends)
+    start_after_prior();
 
     bool ok = true;  // no wait of this warp has run out
     auto arrive_warp = [&](const uint64_t &b) { tc::arrive(bar(b)); };
@@ -406,7 +463,9 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
         few_registers();
         // scheduling: the pieces of this block's run
         int at = 0, from = 0, to = 0;
-        const TreeRuns runs(a, tree_steps<KEYS>(a));
+        TreeSeq seq0{};
+        if (lane < a.c.n_seqs) seq0 = tree_seq<KEYS>(a, lane);
+        const TreeRuns runs(a, tree_steps<KEYS>(a, seq0));
         if (static_cast<int>(blockIdx.x) < runs.runs) {
             from = runs.begin(blockIdx.x);
             to = runs.begin(blockIdx.x + 1);
@@ -426,8 +485,11 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
         };
 #pragma unroll 1
         for (int b0 = 0; b0 < a.c.n_seqs && from < to && ok; b0 += 32) {
-            TreeSeq s{};
-            if (b0 + lane < a.c.n_seqs) s = tree_seq<KEYS>(a, b0 + lane);
+            TreeSeq s = seq0;
+            if (b0) {
+                s = TreeSeq{};
+                if (b0 + lane < a.c.n_seqs) s = tree_seq<KEYS>(a, b0 + lane);
+            }
             const int w = s.steps * s.blocks * a.c.heads;
             int upto = w;
 #pragma unroll
@@ -613,18 +675,24 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                 if (used) wait_warp(*((Q8 ? sh.raw_full : sh.ring_full) + k), used - 1);
             }
         }
-    } else if (TMA && Q8 && warp >= kTrSoft && warp < kTrSoft + kTrLoaders) {
+    } else if (TMA && warp >= kTrSoft && warp < kTrSoft + kTrLoaders) {
         few_registers();
-        if constexpr (TMA && Q8) {
-            // codes to float16: every lane the same pieces of a tile, 16 codes each
+        if constexpr (TMA) {
+            // the rows of q; E4M3: codes to float16, every lane the same pieces of a tile, 16 codes each
             const int lw = warp - kTrSoft, pieces = KEYS * a.c.dim / 16;
             uint32_t tiles = 0;
+            (void)pieces;
+            (void)tiles;
             for (uint32_t i = 0; ok; ++i) {
                 if (!wait_warp(sh.item_full[i % kTrItems], i / kTrItems)) break;
                 TreeItem &it = sh.item[i % kTrItems];
                 if (it.end) break;
                 const int steps = it.steps, slot_first = it.begin + it.first * KEYS;
                 int entry = 0;
+                if (i && !wait_warp(sh.q_empty, i - 1)) break;
+                tree_query<KV, NC, kTrRows / kTrLoaders>(a, it, lw * (kTrRows / kTrLoaders), q_s, sh.q_scale[i & 1]);
+                arrive_warp(sh.q_full);
+                if constexpr (Q8) {
 #pragma unroll 1
                 for (int p = 0; p < 2 * steps; ++p, ++tiles) {
                     const uint32_t slot = tiles % S::SLOTS, raw = tiles % S::RAW;
@@ -673,6 +741,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                     tc::fence_async_smem();
                     arrive_warp(sh.ring_full[slot]);
                     arrive_warp(sh.raw_empty[raw]);
+                }
                 }
                 arrive_warp(sh.item_empty[i % kTrItems]);
             }
@@ -868,59 +937,8 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                     keep = 0;  // its last keys among them
                 } else {
                     if (n_q && !wait_warp(sh.q_empty, n_q - 1)) break;
-                    constexpr int RQ = kTrRows / kTrLoaders, PQ = NC * 8;  // rows of a warp, 16-byte pieces of a row
-                    auto q_row = [&](int r, bool *real) {
-                        const int at = it->row0 + lw * RQ + r, t = static_cast<int>(fast_div(at, a.group_div)), g = at - t * a.group;
-                        *real = t < it->count;
-                        return a.q + b * a.qst[0] + t * a.qst[1] + (int64_t(head) * a.group + g) * a.qst[2];
-                    };
-                    auto q_at = [&](int r, int piece) {
-                        return q_s + piece / 8 * S::QCHUNK + (lw * RQ + r) * 128 + ((piece & 7) ^ (r & 7)) * 16;
-                    };
-                    if constexpr (!Q8) {
-#pragma unroll 4
-                        for (int i = lane; i < RQ * PQ; i += 32) {
-                            const int r = i / PQ, col = i % PQ * 8;
-                            bool real;
-                            const uint16_t *from = q_row(r, &real);
-                            real &= col < dim;
-                            if (a.q_vec) tr_copy16(q_at(r, col / 8), real ? from + col : a.q, real);
-                            else st_shared16(q_at(r, col / 8), real ? tree_piece<2>(reinterpret_cast<const uint8_t *>(from), col, dim)
-                                                                    : make_uint4(0, 0, 0, 0));
-                        }
-                    } else {
-                        // bfloat16 to float16 of a row whose largest element is between 1 and 2: a row a warp, eight on the way
-#pragma unroll 1
-                        for (int r0 = 0; r0 < RQ; r0 += 8) {
-                            uint4 x[8];
-#pragma unroll
-                            for (int r = 0; r < 8; ++r) {
-                                bool real;
-                                const uint16_t *from = q_row(r0 + r, &real);
-                                x[r] = make_uint4(0, 0, 0, 0);
-                                if (real && lane * 8 < dim) {
-                                    if (a.q_vec) x[r] = *reinterpret_cast<const uint4 *>(from + lane * 8);
-                                    else x[r] = tree_piece<2>(reinterpret_cast<const uint8_t *>(from), lane * 8, dim);
-                                }
-                            }
-#pragma unroll
-                            for (int r = 0; r < 8; ++r) {
-                                uint32_t *w = reinterpret_cast<uint32_t *>(&x[r]);
-                                uint32_t most = 0;
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) most = max(most, max(w[e] << 16 & 0x7fffffffu, w[e] & 0x7fff0000u));
-                                most = __reduce_max_sync(0xffffffffu, most);
-                                const int ex = min(max(static_cast<int>(most >> 23) - 127, -126), 126);
-                                const float div = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    w[e] = tr_pack<true>(__uint_as_float(w[e] << 16) * div, __uint_as_float(w[e] & 0xffff0000u) * div);
-                                if (lane == 0) sh.q_scale[(i - 1) & 1][lw * RQ + r0 + r] = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
-                                if (lane < PQ) st_shared16(q_at(r0 + r, lane), x[r]);
-                            }
-                        }
-                    }
-                    if constexpr (!Q8) ptx::cp_async_commit();
+                    constexpr int RQ = kTrRows / kTrLoaders;
+                    tree_query<KV, NC, RQ>(a, *it, lw * RQ, q_s, sh.q_scale[(i - 1) & 1]);
                     ++n_q;
                     keep = 0;  // and the keys that were started before them
                     q_due = false;
@@ -1075,7 +1093,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                                        keys + k / 4 * (S::CHUNK / 16) + (k & 3) * 2, qk, k > 0);
                     tc::commit(bar(sh.s_full[0]) + to * 8);
                     tc::commit(bar(sh.ring_empty[0]) + sk * 8);
-                    if (!TMA && j + 1 == steps) tc::commit(bar(sh.q_empty));
+                    if (j + 1 == steps) tc::commit(bar(sh.q_empty));
                 }
                 if (j >= 2) tc::commit(bar(sh.ring_empty[0]) + sv * 8);
             }
@@ -1101,62 +1119,11 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
             if (!wait_warp(sh.item_full[i % kTrItems], i / kTrItems)) break;
             TreeItem &it = sh.item[i % kTrItems];
             if (it.end) break;
-            if (!TMA && !wait_warp(sh.kin_full[i % kTrItems], i / kTrItems)) break;
+            if (!wait_warp(sh.kin_full[i % kTrItems], i / kTrItems)) break;
             const int steps = it.steps, slot_first = it.begin + it.first * KEYS, before = it.n - it.count;
             const uint32_t ring0 = ring;
             ring += 2 * steps;
             int n_bad = 0;
-            if constexpr (TMA) {
-                // the rows of q, 16 a warp (the products that read the last ones have ended with that piece)
-                constexpr int RQ = kTrRows / kTrSoft, PQ = NC * 8;
-                auto q_row = [&](int r, bool *there) {
-                    const int at = it.row0 + warp * RQ + r, t = static_cast<int>(fast_div(at, a.group_div)), g = at - t * a.group;
-                    *there = t < it.count;
-                    return a.q + it.b * a.qst[0] + t * a.qst[1] + (int64_t(it.head) * a.group + g) * a.qst[2];
-                };
-                auto q_at = [&](int r, int piece) {
-                    return q_s + piece / 8 * S::QCHUNK + (warp * RQ + r) * 128 + ((piece & 7) ^ (r & 7)) * 16;
-                };
-                auto q_piece = [&](int r, int col) {
-                    bool there;
-                    const uint16_t *from = q_row(r, &there);
-                    if (!there || col >= a.c.dim) return make_uint4(0, 0, 0, 0);
-                    if (a.q_vec) return *reinterpret_cast<const uint4 *>(from + col);
-                    return tree_piece<2>(reinterpret_cast<const uint8_t *>(from), col, a.c.dim);
-                };
-#pragma unroll 1
-                for (int r0 = 0; r0 < RQ; r0 += 8) {
-                    uint4 x[Q8 ? 8 : 2 * NC];
-                    if constexpr (!Q8) {
-#pragma unroll
-                        for (int k = 0; k < 2 * NC; ++k) x[k] = q_piece(r0 + (k * 32 + lane) / PQ, (k * 32 + lane) % PQ * 8);
-#pragma unroll
-                        for (int k = 0; k < 2 * NC; ++k) st_shared16(q_at(r0 + (k * 32 + lane) / PQ, (k * 32 + lane) % PQ), x[k]);
-                    } else {
-                        // bfloat16 to float16 of a row whose largest element is between 1 and 2
-#pragma unroll
-                        for (int r = 0; r < 8; ++r) x[r] = q_piece(r0 + r, lane * 8);
-#pragma unroll
-                        for (int r = 0; r < 8; ++r) {
-                            uint32_t *w = reinterpret_cast<uint32_t *>(&x[r]);
-                            uint32_t most = 0;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) most = max(most, max(w[e] << 16 & 0x7fffffffu, w[e] & 0x7fff0000u));
-                            most = __reduce_max_sync(0xffffffffu, most);
-                            const int ex = min(max(static_cast<int>(most >> 23) - 127, -126), 126);
-                            const float div = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                w[e] = tr_pack<true>(__uint_as_float(w[e] << 16) * div, __uint_as_float(w[e] & 0xffff0000u) * div);
-                            if (lane == 0) sh.q_scale[i & 1][warp * RQ + r0 + r] = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
-                            if (lane < PQ) st_shared16(q_at(r0 + r, lane), x[r]);
-                        }
-                    }
-                }
-                tc::fence_async_smem();
-                arrive_warp(sh.q_full);
-                if (!wait_warp(sh.kin_full[i % kTrItems], i / kTrItems)) break;
-            }
             const int at = it.row0 + row, t = static_cast<int>(fast_div(at, a.group_div)), g = at - t * a.group;
             const bool real = t < it.count;
             const bool some = __any_sync(0xffffffffu, real);
@@ -1394,6 +1361,8 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                 if (it.part >= 0) f = 1.f;
                 if (Q8) f *= mv == -INFINITY ? 0.f : exp2f(less_v - less);  // the output was relative to mv
                 uint16_t *out = a.out + it.b * a.ost[0] + t * a.ost[1] + hq * a.ost[2];
+                uint32_t any_bad = 0;
+                for (int n = 0; n < n_bad; ++n) any_bad |= it.bad[n][0] | it.bad[n][1] | it.bad[n][2] | it.bad[n][3];
 #pragma unroll 1
                 for (int c = half; c < (a.c.dim + 31) / 32; c += 2) {
                     uint32_t o[32];
@@ -1402,6 +1371,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                     tc::wait_ld(o);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = none ? 0u : __float_as_uint(__uint_as_float(o[e]) * f);
+                    if (any_bad)
                     for (int n = 0; n < n_bad; ++n)
 #pragma unroll 1
                         for (int w = 0; w < 4; ++w)
