@@ -236,10 +236,11 @@ int lc_cache_append_packed(const lc_paged_cache *cache, const void *k_new, const
  *   starts       [n_seqs + 1]: where each sequence's tokens begin among the packed ones
  *   slots, positions, seqs   [max_tokens], of every packed token: page * page_size +
  *                row, place in its sequence, sequence; -1 past the last
- * A sequence is not served, keeps the pages that it has and gets no tokens where its
+ * A sequence is not served, keeps the pages that it has (those past lengths + counts
+ * have gone on the stack) and gets no tokens where its
  * pages do not last (those behind it that need pages are not served either), its
- * tokens pass pages_per_seq, or max_tokens ends; that records LC_ERR_CACHE_INDEX,
- * as a negative length or count (taken as 0) does.  All outputs and the stack lie
+ * tokens pass pages_per_seq (then no page goes), or max_tokens ends; that records
+ * LC_ERR_CACHE_INDEX, as a negative length or count (taken as 0) does.  All outputs and the stack lie
  * apart from one another and from what is read.
  * The stack's entries past its top and below free_size may change. */
 typedef struct {

@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kRsThreads) k_cache_reserve(const __grid_const
         const int b = b0 + t;
         int need = 0, c = 0;
         if (b < a.n_seqs) {
-            if (count[b] < 0) want[b] = held[b];
+            if (count[b] < 0) want[b] = min(want[b], held[b]);  // (what it gave back above stays given)
             need = max(want[b] - held[b], 0);
             c = max(count[b], 0);
         }
