@@ -15,9 +15,9 @@
  * struct is read during the call and not retained, launches are asynchronous
  * on `stream`, every function returns an lc_status and launches nothing when
  * it refuses.  The starts live on the device and are read by the kernel: one
- * outside 0 .. n_tokens (n_keys), or below the one before it, is moved there,
- * and LC_ERR_CACHE_INDEX is recorded in the device error word
- * (lc_last_device_error).
+ * outside 0 .. n_tokens (n_keys) is moved there; where one is below the one
+ * before it nothing is computed and out stays as it was.  Both record
+ * LC_ERR_CACHE_INDEX in the device error word (lc_last_device_error).
  */
 #ifndef LAYOUT_COPY_PROMPT_H_
 #define LAYOUT_COPY_PROMPT_H_

@@ -126,6 +126,7 @@ __device__ __forceinline__ float pr_max3(float a, float b, float c) {
 // that come before the sequence's end, the one before it has a level less.
 struct PromptSeq {
     int level, tiles;
+    bool fell;  // it ends before it begins
 };
 
 template <int TILES>
@@ -135,6 +136,7 @@ __device__ __forceinline__ PromptSeq prompt_seq(const PromptArgs &a, int b, Prom
     const int r0 = a.starts[b], r1 = a.starts[b + 1], s0 = ks[b], s1 = ks[b + 1];
     const int q0 = min(max(r0, 0), a.n_tokens), q1 = min(max(r1, q0), a.n_tokens);
     const int k0 = min(max(s0, 0), k_most), k1 = min(max(s1, k0), k_most);
+    const bool fell = min(max(r1, 0), a.n_tokens) < q0 || min(max(s1, 0), k_most) < k0;
     if (q0 != r0 || q1 != r1 || k0 != s0 || k1 != s1) note_error(LC_ERR_CACHE_INDEX, kClassPrompt);
     if (it) {
         it->q0 = q0;
@@ -143,7 +145,7 @@ __device__ __forceinline__ PromptSeq prompt_seq(const PromptArgs &a, int b, Prom
         it->nk = k1 - k0;
     }
     const int per = TILES * a.tokens_tile;
-    return PromptSeq{(max(k1 - k0, 1) - 1) / per, (q1 - q0 + per - 1) / per};
+    return PromptSeq{(max(k1 - k0, 1) - 1) / per, (q1 - q0 + per - 1) / per, fell};
 }
 
 // Tiles of a sequence at level x or above.
@@ -159,15 +161,22 @@ __device__ __forceinline__ void prompt_item(const PromptArgs &a, uint32_t at, Pr
     const int lane = threadIdx.x & 31;
     const uint32_t pair = fast_div(at, a.pair_div);
     const int which = static_cast<int>(at - pair * a.pair_div.d);
-    PromptSeq mine{0, 0};
+    PromptSeq mine{0, 0, false};
     if (lane < a.n_seqs) mine = prompt_seq<TILES>(a, lane, nullptr);
+    bool fell = mine.fell;
     auto total = [&](int x) {
         uint32_t n = lane < a.n_seqs ? prompt_above(a, mine, x) : 0;
-        for (int b = 32 + lane; b < a.n_seqs; b += 32) n += prompt_above(a, prompt_seq<TILES>(a, b, nullptr), x);
+        for (int b = 32 + lane; b < a.n_seqs; b += 32) {
+            const PromptSeq s = prompt_seq<TILES>(a, b, nullptr);
+            fell |= s.fell;
+            n += prompt_above(a, s, x);
+        }
         return __reduce_add_sync(0xffffffffu, n);
     };
     it->end = 1;
-    if (pair >= total(0)) return;
+    // (where starts fall, sequences share rows: there is no answer, and no bound on the tiles)
+    const uint32_t tiles = total(0);
+    if (__any_sync(0xffffffffu, fell) || pair >= tiles) return;
     it->end = 0;
     // the highest level x with more than `pair` tiles at it or above
     int lo = 0, hi = a.n_keys / (TILES * a.tokens_tile) + 1;
@@ -180,7 +189,7 @@ __device__ __forceinline__ void prompt_item(const PromptArgs &a, uint32_t at, Pr
     int tile = 0, seq = 0;
     for (int b0 = 0; b0 < a.n_seqs; b0 += 32) {
         const int b = b0 + lane;
-        PromptSeq s{0, 0};
+        PromptSeq s{0, 0, false};
         if (b < a.n_seqs) s = b0 == 0 ? mine : prompt_seq<TILES>(a, b, nullptr);
         const uint32_t n = b < a.n_seqs ? prompt_above(a, s, lo) - prompt_above(a, s, lo + 1) : 0;
         uint32_t upto = n;
