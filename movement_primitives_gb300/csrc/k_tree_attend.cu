@@ -98,6 +98,8 @@ extern "C" int lc_cache_attend_tree(const lc_paged_cache *cache, const lc_cache_
     a.most_blocks = most_blocks(q->n_drafts, a.group);
     const int64_t heads = int64_t(cache->n_seqs) * cache->n_kv_heads;
     if (heads > 0x3ffffff / a.most_blocks) return LC_ERR_OVERFLOW;  // (32 blocks a unit in the second launch)
+    const int keys = a.c.dim <= 128 ? 128 : 64;
+    if (heads * a.most_blocks > 0x7fffffff / (a.c.cap / keys + 2)) return LC_ERR_OVERFLOW;  // (steps are counted in 32 bits)
     const TreeSpace space(a.c, heads * a.most_blocks);
     if (!q->workspace) return LC_ERR_NULL;
     if (space.end > q->workspace_bytes) return LC_ERR_WORKSPACE;
@@ -142,7 +144,6 @@ extern "C" int lc_cache_attend_tree(const lc_paged_cache *cache, const lc_cache_
         for (const int64_t *pst : {cache->k_stride, cache->v_stride})
             if (pool[i] > 1 && (pst[i] == 0 || pst[i] >= int64_t(1) << 38)) boxes = false;
     if (boxes) {
-        const int keys = a.c.dim <= 128 ? 128 : 64;
         a.box = cache->page_size & -cache->page_size;
         a.box = std::min(a.box, keys);
         if (!map_pool(&a.km, *cache, cache->k, cache->k_stride, a.box) || !map_pool(&a.vm, *cache, cache->v, cache->v_stride, a.box))
