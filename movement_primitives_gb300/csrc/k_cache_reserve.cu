@@ -4,10 +4,16 @@
 // What each sequence has and wants, and the sums over the sequences before it (pages
 // given back, pages taken, tokens), decide where every page and token goes; every
 // block of the cluster works them out for itself, since they are a few numbers a
-// sequence.  Pages given back are written to the stack first, then the cluster
-// meets, then tables and slots are written, each block its share.  A sequence's pages
-// come first in its row, so what it has is found by looking where its length says,
-// and else by a search of 32 places at a time.
+// sequence: one pass of sums where all are served, else one after another.  Pages
+// given back are written to the stack first, then the cluster meets, then tables and slots
+// are written, each block its share.  A sequence's pages come first in its row, so
+// what it has is found by looking where its length says, and else by a search of 32
+// places at a time.
+//
+// What bounds it is the chain of dependent reads (length, row, stack, page), not the
+// bytes: a step of 64 sequences is a block of 256 threads, whose barriers are
+// cheaper than 1024's; many tokens or a table written anew take a cluster, every thread with
+// kRsAtOnce reads on the way.
 #include <cooperative_groups.h>
 
 #include "cache_common.cuh"
@@ -17,8 +23,9 @@ namespace lc {
 namespace cg = cooperative_groups;
 
 constexpr uint32_t kClassReserve = 0xf6;
-constexpr int kRsThreads = 1024;
+constexpr int kRsThreads = 1024, kRsFew = 256;  // few: of a block for up to as many sequences
 constexpr int kRsCluster = 8;
+constexpr int kRsAtOnce = 8;
 
 struct ReserveArgs {
     const int32_t *table, *lengths, *counts, *n_free;
@@ -42,7 +49,7 @@ __device__ __forceinline__ T block_scan(T x, T *warps, T *all) {
     if (lane == 31) warps[warp] = x;
     __syncthreads();
     if (warp == 0) {
-        T w = warps[lane];
+        T w = lane < static_cast<int>(blockDim.x >> 5) ? warps[lane] : T(0);
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const T o = __shfl_up_sync(0xffffffffu, w, d);
@@ -55,80 +62,17 @@ __device__ __forceinline__ T block_scan(T x, T *warps, T *all) {
     return x + (warp ? warps[warp - 1] : T(0));
 }
 
-__global__ void __launch_bounds__(kRsThreads) k_cache_reserve(const __grid_constant__ ReserveArgs a) {
-    extern __shared__ int shared[];
-    __shared__ int warps[32], searches;
-    __shared__ int64_t wide[32];
-    int *const held = shared, *const want = held + a.n_seqs, *const first = want + a.n_seqs;  // pages; pages taken before
-    int *const count = first + a.n_seqs, *const start = count + a.n_seqs;                      // tokens; n_seqs + 1
-    int *const back = start + a.n_seqs + 1;                                                     // pages given back before
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    const int blocks = gridDim.x, block = blockIdx.x;
-    const int cap = a.per * a.page;
+// The same where not all are served: the tokens of those who are (first, start and *pages_taken: theirs).
+__device__ __noinline__ int reserve_in_turn(const ReserveArgs &a, const int *held, int *want, int *first, int *count, int *start,
+                                            int *warps, int64_t *wide, int top, int *pages_taken) {
+    const int t = threadIdx.x, threads = blockDim.x;
     auto error = [&] {
-        if (block == 0) report_error(LC_ERR_CACHE_INDEX, kClassReserve);
+        if (blockIdx.x == 0) report_error(LC_ERR_CACHE_INDEX, kClassReserve);
     };
-    auto pages_of = [&](int tokens) { return static_cast<int>(fast_div(tokens + a.page - 1, a.page_div)); };
-    if (t == 0) searches = 0;
-    start_after_prior();
-    __syncthreads();
-    auto length_of = [&](int b) { return min(max(a.lengths[b], 0), cap); };
-    // what every sequence has: looked for where its length says, searched for where it is not there
-    for (int b = t; b < a.n_seqs; b += kRsThreads) {
-        const int n = a.lengths[b], m = a.counts[b], len = length_of(b);
-        const int32_t *row = a.table + b * a.table_stride;
-        const int guess = pages_of(len);
-        const bool right = (guess == 0 || row[guess - 1] >= 0) && (guess == a.per || row[guess] < 0);
-        held[b] = guess;
-        int c = max(m, 0);
-        if (n != len || m < 0) error();
-        if (c > cap - len) {
-            error();
-            c = -1;  // refused
-        }
-        count[b] = c;
-        if (!right) first[atomicAdd(&searches, 1)] = b;
-    }
-    __syncthreads();
-    for (int i = warp; i < searches; i += kRsThreads / 32) {
-        const int b = first[i];
-        const int32_t *row = a.table + b * a.table_stride;
-        int lo = 0, hi = a.per;  // pages before lo, none from hi on
-        while (lo < hi) {
-            const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-            const int n = __popc(__ballot_sync(0xffffffffu, at < hi && row[at] >= 0));
-            if (n == 0) {
-                hi = lo;
-            } else {
-                const int last = lo + (n - 1) * step;  // a page there
-                hi = min(hi, last + step);
-                lo = last + 1;
-            }
-        }
-        if (lane == 0) held[b] = lo;
-    }
-    __syncthreads();
-    const int free_raw = *a.n_free, n_free = static_cast<int>(min(int64_t(max(free_raw, 0)), a.free_size));
-    if (free_raw != n_free && t == 0) error();
-    // pages given back, in the sequences' order
-    int sum = 0, all;
-    for (int b0 = 0; b0 < a.n_seqs; b0 += kRsThreads) {
-        const int b = b0 + t;
-        int over = 0;
-        if (b < a.n_seqs) {
-            want[b] = count[b] < 0 ? held[b] : pages_of(length_of(b) + count[b]);
-            over = max(held[b] - want[b], 0);
-        }
-        const int upto = block_scan(over, warps, &all);
-        if (b < a.n_seqs) back[b] = sum + upto - over;
-        sum += all;
-        __syncthreads();
-    }
-    const int top = static_cast<int>(min(int64_t(n_free) + sum, a.free_size));
-    if (n_free + int64_t(sum) > a.free_size && t == 0) error();
+    int all;
     // who gets pages: in order, as long as they last, and whoever needs none
     int taken = 0;
-    for (int b0 = 0; b0 < a.n_seqs; b0 += kRsThreads) {
+    for (int b0 = 0; b0 < a.n_seqs; b0 += threads) {
         const int b = b0 + t;
         int need = 0;
         if (b < a.n_seqs && count[b] >= 0) need = max(want[b] - held[b], 0);
@@ -142,7 +86,7 @@ __global__ void __launch_bounds__(kRsThreads) k_cache_reserve(const __grid_const
     }
     // tokens, as far as the packed lists go
     int64_t asked = 0;
-    for (int b0 = 0; b0 < a.n_seqs; b0 += kRsThreads) {
+    for (int b0 = 0; b0 < a.n_seqs; b0 += threads) {
         const int b = b0 + t;
         const int64_t c = b < a.n_seqs ? max(count[b], 0) : 0;
         int64_t most;
@@ -157,7 +101,7 @@ __global__ void __launch_bounds__(kRsThreads) k_cache_reserve(const __grid_const
     // where pages and tokens of those who are served begin
     int tokens = 0;
     taken = 0;
-    for (int b0 = 0; b0 < a.n_seqs; b0 += kRsThreads) {
+    for (int b0 = 0; b0 < a.n_seqs; b0 += threads) {
         const int b = b0 + t;
         int need = 0, c = 0;
         if (b < a.n_seqs) {
@@ -172,14 +116,158 @@ __global__ void __launch_bounds__(kRsThreads) k_cache_reserve(const __grid_const
         if (b < a.n_seqs) start[b] = tokens + upto - c;
         tokens += all;
     }
+    *pages_taken = taken;
+    return tokens;
+}
+
+__global__ void __launch_bounds__(kRsThreads) k_cache_reserve(const __grid_constant__ ReserveArgs a) {
+    extern __shared__ int shared[];
+    __shared__ int warps[32], searches;
+    __shared__ int64_t wide[32];
+    __shared__ int4 sums[2][32];
+    __shared__ uint32_t token_sums[2][32];
+    int *const held = shared, *const want = held + a.n_seqs, *const first = want + a.n_seqs;  // pages; pages taken before
+    int *const count = first + a.n_seqs, *const start = count + a.n_seqs;                      // tokens; n_seqs + 1
+    int *const back = start + a.n_seqs + 1, *const length = back + a.n_seqs;                    // pages given back before
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, threads = blockDim.x;
+    const int blocks = gridDim.x, block = blockIdx.x;
+    const int cap = a.per * a.page;
+    auto error = [&] {
+        if (block == 0) report_error(LC_ERR_CACHE_INDEX, kClassReserve);
+    };
+    auto pages_of = [&](int tokens) { return static_cast<int>(fast_div(tokens + a.page - 1, a.page_div)); };
+    if (t == 0) searches = 0;
+    start_after_prior();
+    const int free_raw = *a.n_free;
+    __syncthreads();
+    // what every sequence has: looked for where its length says, searched for where it is not there
+    for (int b = t; b < a.n_seqs; b += threads) {
+        const int n = a.lengths[b], m = a.counts[b], len = min(max(n, 0), cap);
+        length[b] = len;
+        const int32_t *row = a.table + b * a.table_stride;
+        const int guess = pages_of(len);
+        const bool right = (guess == 0 || row[guess - 1] >= 0) && (guess == a.per || row[guess] < 0);
+        held[b] = guess;
+        int c = max(m, 0);
+        if (n != len || m < 0) error();
+        if (c > cap - len) {
+            error();
+            c = -1;  // refused
+        }
+        count[b] = c;
+        if (!right) first[atomicAdd(&searches, 1)] = b;
+    }
+    __syncthreads();
+    for (int i = warp; i < searches; i += threads / 16) {  // two at a time
+        const int other = min(i + threads / 32, searches - 1), b[2] = {first[i], first[other]};
+        int lo[2] = {0, 0}, hi[2] = {a.per, a.per};  // pages before lo, none from hi on
+        while (lo[0] < hi[0] || lo[1] < hi[1]) {
+            int step[2];
+            bool there[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                step[k] = (hi[k] - lo[k] + 31) / 32;
+                const int at = lo[k] + lane * step[k];
+                there[k] = at < hi[k] && a.table[b[k] * a.table_stride + at] >= 0;
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int n = __popc(__ballot_sync(0xffffffffu, there[k]));
+                if (n == 0) {
+                    hi[k] = lo[k];
+                } else {
+                    const int last = lo[k] + (n - 1) * step[k];  // a page there
+                    hi[k] = min(hi[k], last + step[k]);
+                    lo[k] = last + 1;
+                }
+            }
+        }
+        if (lane < 2) held[b[lane]] = lo[lane];
+    }
+    __syncthreads();
+    const int n_free = static_cast<int>(min(int64_t(max(free_raw, 0)), a.free_size));
+    if (free_raw != n_free && t == 0) error();
+    // pages given back, pages taken and tokens, in the sequences' order, as if all were served
+    int sum = 0, taken = 0;
+    int64_t asked = 0;
+    for (int b0 = 0; b0 < a.n_seqs; b0 += threads) {
+        const int b = b0 + t;
+        // (tokens in 32 bits, which wrap, and their halves' sums, which tell whether they did)
+        const int warps_used = min((a.n_seqs - b0 + 31) / 32, threads / 32);
+        int over = 0, need = 0;
+        uint32_t c = 0;
+        if (b < a.n_seqs) {
+            want[b] = count[b] < 0 ? held[b] : pages_of(length[b] + count[b]);
+            over = max(held[b] - want[b], 0);
+            need = max(want[b] - held[b], 0);
+            c = max(count[b], 0);
+        }
+        int over_upto = over, need_upto = need;
+        uint32_t c_upto = c;
+        if (warp < warps_used) {
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, over_upto, d), n = __shfl_up_sync(0xffffffffu, need_upto, d);
+                const uint32_t m = __shfl_up_sync(0xffffffffu, c_upto, d);
+                if (lane >= d) {
+                    over_upto += o;
+                    need_upto += n;
+                    c_upto += m;
+                }
+            }
+            const uint32_t low = __reduce_add_sync(0xffffffffu, c & 0xffff), high = __reduce_add_sync(0xffffffffu, c >> 16);
+            if (lane == 31) {
+                sums[b0 ? 1 : 0][warp] = make_int4(over_upto, need_upto, static_cast<int>(low), static_cast<int>(high));
+                token_sums[b0 ? 1 : 0][warp] = c_upto;
+            }
+        }
+        __syncthreads();
+        // what the warps before have, and all of them
+        int4 of = make_int4(0, 0, 0, 0);
+        uint32_t tokens_of = 0;
+        if (lane < warps_used) {
+            of = sums[b0 ? 1 : 0][lane];
+            tokens_of = token_sums[b0 ? 1 : 0][lane];
+        }
+        const int over_all = __reduce_add_sync(0xffffffffu, of.x), need_all = __reduce_add_sync(0xffffffffu, of.y);
+        const int64_t c_all = static_cast<int64_t>(__reduce_add_sync(0xffffffffu, static_cast<uint32_t>(of.z))) +
+                              (static_cast<int64_t>(__reduce_add_sync(0xffffffffu, static_cast<uint32_t>(of.w))) << 16);
+        if (warp < warps_used) {
+            const bool earlier = lane < warp;
+            over_upto += __reduce_add_sync(0xffffffffu, earlier ? of.x : 0);
+            need_upto += __reduce_add_sync(0xffffffffu, earlier ? of.y : 0);
+            c_upto += __reduce_add_sync(0xffffffffu, earlier ? tokens_of : 0u);
+        }
+        if (b0) __syncthreads();  // (the second set of sums is used again)
+        if (b < a.n_seqs) {
+            back[b] = sum + over_upto - over;
+            first[b] = taken + need_upto - need;
+            start[b] = static_cast<int>(static_cast<uint32_t>(asked) + c_upto - c);
+        }
+        sum += over_all;
+        taken += need_all;
+        asked += c_all;
+    }
+    const int top = static_cast<int>(min(int64_t(n_free) + sum, a.free_size));
+    if (n_free + int64_t(sum) > a.free_size && t == 0) error();
+    int tokens = static_cast<int>(asked);
+    if (taken > top || asked > a.n_tokens) {
+        tokens = reserve_in_turn(a, held, want, first, count, start, warps, wide, top, &taken);
+    }
     if (t == 0) start[a.n_seqs] = tokens;
     __syncthreads();
     // pages given back
-    for (int b = block * (kRsThreads / 32) + warp; b < a.n_seqs; b += blocks * (kRsThreads / 32)) {
+    for (int b = block * (threads / 32) + warp; b < a.n_seqs; b += blocks * (threads / 32)) {
         const int32_t *row = a.table + b * a.table_stride;
-        for (int j = want[b] + lane; j < held[b]; j += 32) {
-            const int64_t at = int64_t(n_free) + back[b] + j - want[b];
-            if (at < a.free_size) a.free[at] = row[j];
+        for (int j0 = want[b] + lane; j0 < held[b]; j0 += 32 * kRsAtOnce) {
+            int x[kRsAtOnce];
+#pragma unroll
+            for (int i = 0; i < kRsAtOnce; ++i) x[i] = j0 + 32 * i < held[b] ? row[j0 + 32 * i] : -1;
+#pragma unroll
+            for (int i = 0; i < kRsAtOnce; ++i) {
+                const int64_t at = int64_t(n_free) + back[b] + j0 + 32 * i - want[b];
+                if (j0 + 32 * i < held[b] && at < a.free_size) a.free[at] = x[i];
+            }
         }
     }
     if (blocks > 1) {
@@ -191,34 +279,64 @@ __global__ void __launch_bounds__(kRsThreads) k_cache_reserve(const __grid_const
         return j < held[b] ? a.table[b * a.table_stride + j] : a.free[top - 1 - (first[b] + j - held[b])];
     };
     const bool in_place = a.new_table == a.table;
-    for (int b = block * (kRsThreads / 32) + warp; b < a.n_seqs; b += blocks * (kRsThreads / 32)) {
+    for (int b = block * (threads / 32) + warp; b < a.n_seqs; b += blocks * (threads / 32)) {
         int32_t *row = a.new_table + b * a.new_stride;
-        for (int j = (in_place ? min(held[b], want[b]) : 0) + lane; j < (in_place ? max(held[b], want[b]) : a.per); j += 32)
-            row[j] = j < want[b] ? page_at(b, j) : -1;
-        if (lane == 0) a.new_lengths[b] = length_of(b) + max(count[b], 0);
-    }
-    const int stride = blocks * kRsThreads;
-    for (int b = block * kRsThreads + t; b <= a.n_seqs; b += stride) a.starts[b] = start[b];
-    if (block == 0 && t == 0) *a.new_n_free = top - taken;
-    for (int i = block * kRsThreads + t; i < a.n_tokens; i += stride) {
-        int64_t slot = -1;
-        int position = -1, b = -1;
-        if (i < tokens) {
-            int lo = 0, hi = a.n_seqs;  // the last sequence that begins at i or before
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) / 2;
-                if (start[mid] <= i) lo = mid;
-                else hi = mid;
-            }
-            b = lo;
-            position = length_of(b) + i - start[b];
-            const int j = static_cast<int>(fast_div(position, a.page_div));
-            const int page = page_at(b, j);
-            if (page >= 0) slot = int64_t(page) * a.page + (position - j * a.page);
+        const int upto = in_place ? max(held[b], want[b]) : a.per;
+        for (int j0 = (in_place ? min(held[b], want[b]) : 0) + lane; j0 < upto; j0 += 32 * kRsAtOnce) {
+            int x[kRsAtOnce];
+#pragma unroll
+            for (int i = 0; i < kRsAtOnce; ++i) x[i] = j0 + 32 * i < want[b] ? page_at(b, j0 + 32 * i) : -1;
+#pragma unroll
+            for (int i = 0; i < kRsAtOnce; ++i)
+                if (j0 + 32 * i < upto) row[j0 + 32 * i] = x[i];
         }
-        a.slots[i] = slot;
-        a.positions[i] = position;
-        a.seqs[i] = b;
+        if (lane == 0) a.new_lengths[b] = length[b] + max(count[b], 0);
+    }
+    const int stride = blocks * threads;
+    for (int b = block * threads + t; b <= a.n_seqs; b += stride) a.starts[b] = start[b];
+    if (block == 0 && t == 0) *a.new_n_free = top - taken;
+    // a warp 32 x kRsAtOnce tokens in a row
+    for (int64_t at = (int64_t(block) * (threads / 32) + warp) * 32 * kRsAtOnce; at < a.n_tokens; at += int64_t(stride) * kRsAtOnce) {
+        const int i0 = static_cast<int>(at);
+        // the sequences of the first and the last of them, by half a warp each: the last that begins there or before
+        int lo = 0, hi = a.n_seqs;
+        const int64_t edge = lane < 16 ? at : at + 32 * kRsAtOnce - 1;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (start[mid] <= edge) lo = mid;
+            else hi = mid;
+        }
+        const int from = __shfl_sync(0xffffffffu, lo, 0), upto = __shfl_sync(0xffffffffu, lo, 31) + 1;
+        int page[kRsAtOnce], row[kRsAtOnce], position[kRsAtOnce], seq[kRsAtOnce];
+#pragma unroll
+        for (int k = 0; k < kRsAtOnce; ++k) {
+            const int i = i0 + k * 32 + lane;
+            page[k] = position[k] = seq[k] = -1;
+            row[k] = 0;
+            if (at + k * 32 + lane < tokens) {
+                lo = from;
+                hi = upto;
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) / 2;
+                    if (start[mid] <= i) lo = mid;
+                    else hi = mid;
+                }
+                seq[k] = lo;
+                position[k] = length[lo] + i - start[lo];
+                const int j = static_cast<int>(fast_div(position[k], a.page_div));
+                row[k] = position[k] - j * a.page;
+                page[k] = page_at(lo, j);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kRsAtOnce; ++k) {
+            const int64_t i = at + k * 32 + lane;
+            if (i < a.n_tokens) {
+                a.slots[i] = page[k] >= 0 ? int64_t(page[k]) * a.page + row[k] : -1;
+                a.positions[i] = position[k];
+                a.seqs[i] = seq[k];
+            }
+        }
     }
 }
 
@@ -304,11 +422,11 @@ extern "C" int lc_cache_reserve(const lc_cache_reservation *r, lc_stream_t strea
     a.page = r->page_size;
     a.n_tokens = r->max_tokens;
     a.page_div = make_fastdiv(static_cast<uint32_t>(r->page_size));
-    const int smem = (6 * r->n_seqs + 1) * 4;
+    const int smem = (7 * r->n_seqs + 1) * 4;
     int sms = 0, per_sm = 0;
     const void *fn = reinterpret_cast<const void *>(&k_cache_reserve);
     if (prepare(fn, kRsThreads, smem, smem, &sms, &per_sm) != cudaSuccess) return LC_ERR_CUDA;
     const int64_t work = (in_place ? 0 : n * r->pages_per_seq) + r->max_tokens;
-    const int blocks = work > 8 * kRsThreads ? kRsCluster : 1;
-    return launch_after(fn, blocks, kRsThreads, smem, reinterpret_cast<cudaStream_t>(stream), &a, blocks);
+    const int blocks = work > 8 * kRsThreads ? kRsCluster : 1, threads = blocks == 1 && n <= kRsFew ? kRsFew : kRsThreads;
+    return launch_after(fn, blocks, threads, smem, reinterpret_cast<cudaStream_t>(stream), &a, blocks);
 }
