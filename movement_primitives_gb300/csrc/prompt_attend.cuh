@@ -349,23 +349,33 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
                     // becomes 0, and is added at the end where it is seen
                     const uint32_t p = p0 + value_place<TILES>(j, it.steps);
                     if (TILES == 2) wait_values(j);
-                    bool found = false;
+                    constexpr uint32_t kExp = F16 ? 0x7c00u : 0x7f80u;
+                    auto row_at = [&](int c) {
+                        return raw + (ring_s - ptx::smem_addr(raw)) + (p * S::SPT + c / S::CPS) % S::SLOTS * S::SLOT +
+                               c % S::CPS * kPrChunk + row * 128;
+                    };
+                    uint32_t most = 0;  // the row's largest exponents, of even and odd columns
 #pragma unroll 1
                     for (int c = 0; c < NC; ++c) {
-                        uint8_t *v = raw + (ring_s - ptx::smem_addr(raw)) +
-                                     (p * S::SPT + c / S::CPS) % S::SLOTS * S::SLOT + c % S::CPS * kPrChunk + row * 128;
+                        const uint8_t *v = row_at(c);
+                        uint4 x[8];
 #pragma unroll
-                        for (int g = 0; g < 8; ++g) {
-                            uint4 *at = reinterpret_cast<uint4 *>(v + (g ^ (row & 7)) * 16);
-                            uint4 x = *at;
-                            constexpr uint32_t kExp = F16 ? 0x7c00u : 0x7f80u;
-                            uint32_t *w = reinterpret_cast<uint32_t *>(&x);
-                            bool here = false;
+                        for (int g = 0; g < 8; ++g) x[g] = *reinterpret_cast<const uint4 *>(v + (g ^ (row & 7)) * 16);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                here |= (w[e] & kExp) == kExp || (w[e] & kExp << 16) == kExp << 16;
-                            if (here) {
-                                found = true;
+                        for (int g = 0; g < 8; ++g)
+                            most = __vmaxu2(most, __vmaxu2(__vmaxu2(x[g].x & 0x7fff7fffu, x[g].y & 0x7fff7fffu),
+                                                           __vmaxu2(x[g].z & 0x7fff7fffu, x[g].w & 0x7fff7fffu)));
+                    }
+                    const bool found = (most & 0xffffu) >= kExp || most >> 16 >= kExp;
+                    const uint32_t rows = __ballot_sync(0xffffffffu, found);
+                    if (rows) {
+#pragma unroll 1
+                        for (int c = 0; c < NC; ++c)
+#pragma unroll 1
+                            for (int g = 0; g < 8; ++g) {
+                                uint4 *at = reinterpret_cast<uint4 *>(row_at(c) + (g ^ (row & 7)) * 16);
+                                uint4 x = *at;
+                                uint32_t *w = reinterpret_cast<uint32_t *>(&x);
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
                                     if ((w[e] & kExp) == kExp) w[e] &= 0xffff0000u;
@@ -373,16 +383,12 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
                                 }
                                 *at = x;
                             }
-                        }
+                        tc::fence_async_smem();
                     }
-                    const uint32_t rows = __ballot_sync(0xffffffffu, found);
-                    if (lane == 0) {
-                        sh.bad[turn][n_bad][warp & 3] = rows;
-                        sh.bad_step[turn][n_bad] = j;
-                        sh.bad_any[turn][warp & 3] |= rows ? 1u << n_bad : 0u;
-                    }
+                    sh.bad[turn][n_bad][warp & 3] = rows;  // (by every lane)
+                    sh.bad_step[turn][n_bad] = j;
+                    sh.bad_any[turn][warp & 3] |= rows ? 1u << n_bad : 0u;
                     n_bad = min(n_bad + 1, kPrMasked - 1);
-                    tc::fence_async_smem();
                 }
                 const int buf = TILES == 2 ? t : n_s & 1;
                 const uint32_t s_at = lanes + buf * 128;

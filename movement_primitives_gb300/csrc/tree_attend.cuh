@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
     __syncthreads();
     tc::fence_after();
     const uint32_t tmem = sh.tmem;
-    start_after_prior();
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // (joining blocks that come early take what this one needs)
 
     bool ok = true;  // no wait of this warp has run out
     auto arrive_warp = [&](const uint64_t &b) { tc::arrive(bar(b)); };
