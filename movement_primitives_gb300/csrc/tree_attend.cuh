@@ -50,7 +50,6 @@ constexpr int kTrAux = 8;        // steps whose slots' scales and presence are h
 constexpr int kTrLoaders = 4;    // warps
 constexpr int kTrSoft = 8;       // warps: two a 32 rows, each half of a step's slots
 constexpr int kTrMostRuns = 160;
-constexpr int kTrLeast = 2;      // steps of a run
 constexpr float kNear = 8.f, kFar = 60.f;  // log2 of scales that are near one another, and of ones that are not too far from 1
 
 struct TreeArgs {
@@ -66,7 +65,7 @@ struct TreeArgs {
     float scale2;           // |scale| log2 e
     int32_t negative;
     int32_t vec, q_vec, out_vec;  // rows of the pools, of q and of out are whole 16-byte words on 16-byte boundaries
-    int32_t runs;           // blocks of the main kernel
+    int32_t runs, least;    // blocks of the main kernel; steps of a run at least
     int32_t most_blocks;    // tiles of rows a key head at most
     int2 *split;            // of a unit: its first and its last run
     float *part;            // [2 runs][dim / 4 rounded up to 16][128 rows][4]
@@ -115,7 +114,7 @@ __device__ __forceinline__ int tree_steps(const TreeArgs &a, const TreeSeq &firs
 struct TreeRuns {
     int runs, each, more;
     __device__ __forceinline__ TreeRuns(const TreeArgs &a, int all)
-        : runs(min((all + kTrLeast - 1) / kTrLeast, a.runs)), each(all / max(runs, 1)), more(all - each * max(runs, 1)) {}
+        : runs(min((all + a.least - 1) / a.least, a.runs)), each(all / max(runs, 1)), more(all - each * max(runs, 1)) {}
     __device__ __forceinline__ int begin(int r) const { return r * each + min(r, more); }
     __device__ __forceinline__ int of(int step) const {
         const int wide = more * (each + 1);
@@ -1505,8 +1504,11 @@ int launch_tree_shape(const TreeArgs &a, cudaStream_t cs) {
     TreeArgs b = a;
     const int64_t units = int64_t(a.c.n_seqs) * a.c.heads * a.most_blocks;
     const int64_t steps = units * ((int64_t(a.c.cap) + S::KEYS - 1) / S::KEYS);
-    if (steps > 0x7fffffff) return LC_ERR_OVERFLOW;
-    b.runs = static_cast<int32_t>(std::min<int64_t>(std::min(sms, kTrMostRuns), (steps + kTrLeast - 1) / kTrLeast));
+    // Steps of a run: one, so that a few short sequences take as many blocks as there are steps (a sequence of 300 slots, 2
+    // key heads of 64: 10.3 us, 12.8 with two); two past 128 elements a head, whose parts are twice as large and whose joining
+    // is as long as a step (8 windows of 1024, 192 rows of 256: 24.5 us, 26.5 with one).
+    b.least = NC <= 2 ? 1 : 2;
+    b.runs = static_cast<int32_t>(std::min<int64_t>(std::min(sms, kTrMostRuns), (steps + b.least - 1) / b.least));
     const int st = launch_after(fn, b.runs, S::THREADS, S::SMEM, cs, &b);
     if (st) return st;
     return launch_after(reinterpret_cast<const void *>(&k_tree_join<KV, NC>), static_cast<unsigned>(units * 8 * NC), 256, 0, cs, &b);
