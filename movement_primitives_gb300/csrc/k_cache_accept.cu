@@ -7,6 +7,10 @@
 // (pool, head) along the whole path, kAcRows rows read before they are written, and
 // threads need not wait for one another.  Rows that are in their place already are
 // not touched.
+//
+// 192 sequences of up to 64 drafts, 8 heads of 128: 8.1 us for 48 MB, 6.0 TB/s; 4 sequences of 8:
+// 3.0 us, the launch and three dependent reads.  kAcRows rows are on the way a thread:
+// otherwise a path costs a read's latency a draft.
 #include "cache_common.cuh"
 
 namespace lc {

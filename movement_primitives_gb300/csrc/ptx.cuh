@@ -60,9 +60,8 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
     return false;
 }
 
-// The same for waits that one step of a pipeline after another goes through: a poll
-// may sleep up to kPollNs (its polls otherwise take a good part of the issue slots), and
-// the timer is read after such a sleep only.
+// One poll of the waits that a pipeline goes through step after step: it may sleep up to
+// kPollNs, so that waiting warps leave the issue slots to the others.
 constexpr uint32_t kPollNs = 200000;
 __device__ __forceinline__ bool mbar_sleep_wait(uint32_t bar, uint32_t parity) {
     uint32_t done;
@@ -74,16 +73,6 @@ __device__ __forceinline__ bool mbar_sleep_wait(uint32_t bar, uint32_t parity) {
         : "r"(bar), "r"(parity), "r"(kPollNs)
         : "memory");
     return done != 0;
-}
-__device__ __forceinline__ bool mbar_wait_step(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
-    uint64_t t0 = 0;
-#pragma unroll 1
-    for (uint32_t polls = 0; !mbar_sleep_wait(bar, parity); ++polls) {
-        const uint64_t t = global_timer_ns();
-        if (!t0) t0 = t;
-        if (t - t0 > limit_ns || polls > kMaxPolls) return false;
-    }
-    return true;
 }
 
 __device__ __forceinline__ void prefetch_tensormap(const void *tmap) {

@@ -28,10 +28,19 @@
 // end to end, are cut into equal runs, one a block, found from the lengths on
 // the device.  A unit inside one run is finished there; a cut one leaves
 // parts in the workspace, which k_tree_join joins in their order, so results do not
-// depend on timing.  Four warps of a block bring the rows of keys and values in
-// by asynchronous 16-byte copies (a row's place comes from the page table), several
-// tiles ahead; one thread issues the products; eight warps do the softmax, two of
+// depend on timing.  Where pages allow it (launcher) keys and values come by tensor
+// copies, boxes of a page's slots, else four warps bring them in by asynchronous 16-byte
+// copies or an element at a time, several tiles ahead; those warps also bring in the rows of q and turn
+// E4M3 codes into float16.  One warp issues the products; eight do the softmax, two of
 // them a row's (each half of the slots; they exchange their maxima).
+//
+// What bounds it, by GB300 figures of the kernels alone.  16 sequences of up to 4096
+// slots, 8 key heads of 128, 64 rows each, bfloat16 (143 MB): 44 us, 3.3 TB/s, where a steady step runs at
+// the memory's rate; the rest is the scheduler's reads, the first rows, the parts' way through
+// the L2 and the joining (6 us).  12 sequences of up to 32767, 128 rows, E4M3 (443 MB): 218 us, bound by the
+// softmax warps (3400 of 3900 cycles a step): two multiplications by scales more than
+// in bfloat16, beside the conversions.  One of 301 slots: 10.3 us, the chain from the
+// lengths to the join.  By copies of the four warps alone the first took 84 us and the second 678.
 #pragma once
 
 #include <cuda.h>
@@ -693,54 +702,54 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                 arrive_warp(sh.q_full);
                 if constexpr (Q8) {
 #pragma unroll 1
-                for (int p = 0; p < 2 * steps; ++p, ++tiles) {
-                    const uint32_t slot = tiles % S::SLOTS, raw = tiles % S::RAW;
-                    if (!wait_warp(sh.raw_full[raw], tiles / S::RAW)) break;
-                    if (tiles >= S::SLOTS && !wait_warp(sh.ring_empty[slot], tiles / S::SLOTS - 1)) break;
-                    int where = -1;
-                    if (p && (!(p & 1) || p == 2 * steps - 1)) {  // values
-                        const int slot0 = slot_first + (p == 2 * steps - 1 ? steps - 1 : p / 2 - 1) * KEYS;
-                        if (masked(it, slot0) && entry < kTrMasked) where = entry++;
-                    }
-                    const uint32_t from = raw_s + raw * S::RAW_TILE, to = ring_s + slot * S::TILE;
-                    if (where >= 0) {
+                    for (int p = 0; p < 2 * steps; ++p, ++tiles) {
+                        const uint32_t slot = tiles % S::SLOTS, raw = tiles % S::RAW;
+                        if (!wait_warp(sh.raw_full[raw], tiles / S::RAW)) break;
+                        if (tiles >= S::SLOTS && !wait_warp(sh.ring_empty[slot], tiles / S::SLOTS - 1)) break;
+                        int where = -1;
+                        if (p && (!(p & 1) || p == 2 * steps - 1)) {  // values
+                            const int slot0 = slot_first + (p == 2 * steps - 1 ? steps - 1 : p / 2 - 1) * KEYS;
+                            if (masked(it, slot0) && entry < kTrMasked) where = entry++;
+                        }
+                        const uint32_t from = raw_s + raw * S::RAW_TILE, to = ring_s + slot * S::TILE;
+                        if (where >= 0) {
 #pragma unroll 1
-                        for (int k = lw * 32 + lane; k < pieces; k += 32 * kTrLoaders) {
-                            uint4 x = ld_shared16(from + k * 16);
-                            if (tree_clean<KV>(x)) {
-                                const int row = static_cast<int>(fast_div(k, a.piece_div));
-                                atomicOr(&it.bad[where][row >> 5], 1u << (row & 31));
-                                st_shared16(from + k * 16, x);
+                            for (int k = lw * 32 + lane; k < pieces; k += 32 * kTrLoaders) {
+                                uint4 x = ld_shared16(from + k * 16);
+                                if (tree_clean<KV>(x)) {
+                                    const int row = static_cast<int>(fast_div(k, a.piece_div));
+                                    atomicOr(&it.bad[where][row >> 5], 1u << (row & 31));
+                                    st_shared16(from + k * 16, x);
+                                }
+                            }
+                            __syncwarp();
+                        }
+                        // (lanes past the last piece convert that one too: no branch parts the warp)
+#pragma unroll 1
+                        for (int k0 = lw * 32 + lane; k0 < pieces + lane; k0 += 4 * 32 * kTrLoaders) {
+                            uint4 x[4];
+                            int k[4];
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) {
+                                k[g] = min(k0 + g * 32 * kTrLoaders, pieces - 1);
+                                x[g] = ld_shared16(from + k[g] * 16);
+                            }
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) {
+                                const int row = static_cast<int>(fast_div(k[g], a.piece_div)), piece = k[g] - row * static_cast<int>(a.piece_div.d);
+                                const uint32_t *w = reinterpret_cast<const uint32_t *>(&x[g]);
+                                uint32_t y[8];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) tr_halves(w[e], &y[2 * e], &y[2 * e + 1]);
+                                const uint32_t at = to + piece / 4 * S::CHUNK + row * 128 + ((piece & 3) * 2 ^ (row & 7)) * 16;
+                                st_shared16(at, make_uint4(y[0], y[1], y[2], y[3]));
+                                st_shared16(at ^ 16, make_uint4(y[4], y[5], y[6], y[7]));
                             }
                         }
-                        __syncwarp();
+                        tc::fence_async_smem();
+                        arrive_warp(sh.ring_full[slot]);
+                        arrive_warp(sh.raw_empty[raw]);
                     }
-                    // (lanes past the last piece convert that one too: no branch parts the warp)
-#pragma unroll 1
-                    for (int k0 = lw * 32 + lane; k0 < pieces + lane; k0 += 4 * 32 * kTrLoaders) {
-                        uint4 x[4];
-                        int k[4];
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            k[g] = min(k0 + g * 32 * kTrLoaders, pieces - 1);
-                            x[g] = ld_shared16(from + k[g] * 16);
-                        }
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            const int row = static_cast<int>(fast_div(k[g], a.piece_div)), piece = k[g] - row * static_cast<int>(a.piece_div.d);
-                            const uint32_t *w = reinterpret_cast<const uint32_t *>(&x[g]);
-                            uint32_t y[8];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) tr_halves(w[e], &y[2 * e], &y[2 * e + 1]);
-                            const uint32_t at = to + piece / 4 * S::CHUNK + row * 128 + ((piece & 3) * 2 ^ (row & 7)) * 16;
-                            st_shared16(at, make_uint4(y[0], y[1], y[2], y[3]));
-                            st_shared16(at ^ 16, make_uint4(y[4], y[5], y[6], y[7]));
-                        }
-                    }
-                    tc::fence_async_smem();
-                    arrive_warp(sh.ring_full[slot]);
-                    arrive_warp(sh.raw_empty[raw]);
-                }
                 }
                 arrive_warp(sh.item_empty[i % kTrItems]);
             }
@@ -748,289 +757,289 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
     } else if (!TMA && warp >= kTrSoft && warp < kTrSoft + kTrLoaders) {
         few_registers();
         if constexpr (!TMA) {
-        // loads
-        constexpr int RW = KEYS / kTrLoaders, PR = S::TILE / KEYS / 16 * EB / 2;  // rows of a warp, 16-byte pieces of a row
-        constexpr int ITER = RW * PR / 32;
-        const int lw = warp - kTrSoft, dim = a.c.dim, dim16 = (dim + 15) / 16 * 16;
-        const uint8_t *const pool[2] = {a.c.k, a.c.v};
-        uint32_t issued = 0, given = 0, n_q = 0;  // tiles started and given to the products, tiles of q
-        uint32_t back = 0, done = 0;              // items given back, and whose tiles have all been started
-        int32_t note[S::LAG + 1];  // of the tiles under way: values of masked steps (item * kTrMasked + entry, else -1)
+            // loads
+            constexpr int RW = KEYS / kTrLoaders, PR = S::TILE / KEYS / 16 * EB / 2;  // rows of a warp, 16-byte pieces of a row
+            constexpr int ITER = RW * PR / 32;
+            const int lw = warp - kTrSoft, dim = a.c.dim, dim16 = (dim + 15) / 16 * 16;
+            const uint8_t *const pool[2] = {a.c.k, a.c.v};
+            uint32_t issued = 0, given = 0, n_q = 0;  // tiles started and given to the products, tiles of q
+            uint32_t back = 0, done = 0;              // items given back, and whose tiles have all been started
+            int32_t note[S::LAG + 1];  // of the tiles under way: values of masked steps (item * kTrMasked + entry, else -1)
 #pragma unroll
-        for (int i = 0; i <= S::LAG; ++i) note[i] = -1;
-        auto piece_of = [&](int i, int *row, int *col) {  // i-th piece of this lane: row of the warp, first element
-            const int at = i * 32 + lane;
-            *row = at / PR;
-            *col = at % PR * (16 / EB);
-        };
-        auto tile_at = [&](uint32_t slot, int row, int col) {  // where 8 elements go
-            return ring_s + slot * S::TILE + col / 64 * S::CHUNK + row * 128 + ((col / 8 & 7) ^ (row & 7)) * 16;
-        };
-        // looks a masked step's values through: what is not finite becomes 0 and is noted
-        auto look = [&](uint4 &x, int where, int row) {
-            const bool found = tree_clean<KV>(x);
-            if (found) atomicOr(&sh.item[where / kTrMasked].bad[where % kTrMasked][row >> 5], 1u << (row & 31));
-            return found;
-        };
-        // the oldest tile under way has landed: gives it to the products
-        auto give = [&]() {
-            const uint32_t slot = given % S::SLOTS;
-            const int32_t where = note[0];
+            for (int i = 0; i <= S::LAG; ++i) note[i] = -1;
+            auto piece_of = [&](int i, int *row, int *col) {  // i-th piece of this lane: row of the warp, first element
+                const int at = i * 32 + lane;
+                *row = at / PR;
+                *col = at % PR * (16 / EB);
+            };
+            auto tile_at = [&](uint32_t slot, int row, int col) {  // where 8 elements go
+                return ring_s + slot * S::TILE + col / 64 * S::CHUNK + row * 128 + ((col / 8 & 7) ^ (row & 7)) * 16;
+            };
+            // looks a masked step's values through: what is not finite becomes 0 and is noted
+            auto look = [&](uint4 &x, int where, int row) {
+                const bool found = tree_clean<KV>(x);
+                if (found) atomicOr(&sh.item[where / kTrMasked].bad[where % kTrMasked][row >> 5], 1u << (row & 31));
+                return found;
+            };
+            // the oldest tile under way has landed: gives it to the products
+            auto give = [&]() {
+                const uint32_t slot = given % S::SLOTS;
+                const int32_t where = note[0];
 #pragma unroll
-            for (int i = 0; i < S::LAG; ++i) note[i] = note[i + 1];
-            if constexpr (Q8) {
-                if (given >= S::SLOTS && !wait_warp(sh.ring_empty[slot], given / S::SLOTS - 1)) return;
-                const uint32_t from = raw_s + given % S::RAW * S::RAW_TILE + (lw * ITER * 32 + lane) * 16;
-                if (where >= 0) {
+                for (int i = 0; i < S::LAG; ++i) note[i] = note[i + 1];
+                if constexpr (Q8) {
+                    if (given >= S::SLOTS && !wait_warp(sh.ring_empty[slot], given / S::SLOTS - 1)) return;
+                    const uint32_t from = raw_s + given % S::RAW * S::RAW_TILE + (lw * ITER * 32 + lane) * 16;
+                    if (where >= 0) {
+#pragma unroll 1
+                        for (int i = 0; i < ITER; ++i) {
+                            int row, col;
+                            piece_of(i, &row, &col);
+                            if (col >= dim16) continue;
+                            uint4 x = ld_shared16(from + i * 512);
+                            if (look(x, where, lw * RW + row)) st_shared16(from + i * 512, x);
+                        }
+                    }
+#pragma unroll
+                    for (int i0 = 0; i0 < ITER; i0 += 4) {
+                        uint4 x[4];
+#pragma unroll
+                        for (int i = 0; i < 4 && i0 + i < ITER; ++i) x[i] = ld_shared16(from + (i0 + i) * 512);
+#pragma unroll
+                        for (int i = 0; i < 4 && i0 + i < ITER; ++i) {
+                            int row, col;
+                            piece_of(i0 + i, &row, &col);
+                            if (col >= dim16) continue;
+                            const uint32_t *w = reinterpret_cast<const uint32_t *>(&x[i]);
+                            uint32_t y[8];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) tr_halves(w[e], &y[2 * e], &y[2 * e + 1]);
+                            const uint32_t at = tile_at(slot, lw * RW + row, col);
+                            st_shared16(at, make_uint4(y[0], y[1], y[2], y[3]));
+                            st_shared16(at ^ 16, make_uint4(y[4], y[5], y[6], y[7]));  // (col is a multiple of 16)
+                        }
+                    }
+                } else if (where >= 0) {
 #pragma unroll 1
                     for (int i = 0; i < ITER; ++i) {
                         int row, col;
                         piece_of(i, &row, &col);
                         if (col >= dim16) continue;
-                        uint4 x = ld_shared16(from + i * 512);
-                        if (look(x, where, lw * RW + row)) st_shared16(from + i * 512, x);
+                        const uint32_t at = tile_at(slot, lw * RW + row, col);
+                        uint4 x = ld_shared16(at);
+                        if (look(x, where, lw * RW + row)) st_shared16(at, x);
                     }
                 }
+                tc::fence_async_smem();
+                arrive_warp(sh.ring_full[slot]);
+                ++given;
+                // an item is given back when its last values, which may be noted in it, have landed
+                if (back < done && given == sh.item[back % kTrItems].last_tile) {
+                    arrive_warp(sh.item_empty[back % kTrItems]);
+                    ++back;
+                }
+            };
+            // Where a row has a power of two of pieces, a lane's are all the same column, and rows eight apart lie alike.
+            constexpr int SPOTS = PR >= 32 ? 8 : 8 * PR / 32 > 0 ? 8 * PR / 32 : 1;
+            const bool plain = a.vec && dim == dim16;
+            const int first_col = lane % PR * (16 / EB);
+            uint32_t spot[SPOTS];
 #pragma unroll
-                for (int i0 = 0; i0 < ITER; i0 += 4) {
-                    uint4 x[4];
+            for (int i = 0; i < SPOTS; ++i) {
+                const int row = i * (32 / PR) + lane / PR;
+                spot[i] = tile_at(0, lw * RW + row, first_col) - ring_s;
+            }
+            // starts a tile of pool w from the rows at `from`
+            auto start = [&](int w, int64_t from, int32_t where) {
+                const uint32_t slot = issued % S::SLOTS;
+                if (!Q8 && issued >= S::SLOTS && !wait_warp(sh.ring_empty[slot], issued / S::SLOTS - 1)) return;
+                if (32 % PR == 0 && plain && __all_sync(0xffffffffu, from >= 0 || lane >= RW)) {
+                    // every lane the same piece of one row after another: a pointer by shuffle, two additions and a copy
+                    const uint8_t *const mine = pool[w] + from * EB;
+                    const uint32_t dst = Q8 ? raw_s + issued % S::RAW * S::RAW_TILE + (lw * ITER * 32 + lane) * 16 : ring_s + slot * S::TILE;
 #pragma unroll
-                    for (int i = 0; i < 4 && i0 + i < ITER; ++i) x[i] = ld_shared16(from + (i0 + i) * 512);
+                    for (int i0 = 0; i0 < ITER; i0 += 8) {
+                        const uint8_t *src[8];
 #pragma unroll
-                    for (int i = 0; i < 4 && i0 + i < ITER; ++i) {
+                        for (int i = 0; i < 8 && i0 + i < ITER; ++i)
+                            src[i] = reinterpret_cast<const uint8_t *>(__shfl_sync(
+                                0xffffffffu, reinterpret_cast<uint64_t>(mine), (i0 + i) * (32 / PR) + lane / PR));
+#pragma unroll
+                        for (int i = 0; i < 8 && i0 + i < ITER; ++i)
+                            if (first_col < dim)
+                                ptx::cp_async16(Q8 ? dst + (i0 + i) * 512 : dst + spot[i % SPOTS] + (i0 + i) / SPOTS * SPOTS * (32 / PR) * 128,
+                                                src[i] + first_col * EB);
+                    }
+                } else {
+                // the rows' places, eight ahead of their copies
+#pragma unroll
+                for (int i0 = 0; i0 < ITER; i0 += 8) {
+                    int64_t place[8];
+#pragma unroll
+                    for (int i = 0; i < 8 && i0 + i < ITER; ++i) {
+                        int row, col;
+                        piece_of(i0 + i, &row, &col);
+                        place[i] = __shfl_sync(0xffffffffu, from, row);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8 && i0 + i < ITER; ++i) {
                         int row, col;
                         piece_of(i0 + i, &row, &col);
                         if (col >= dim16) continue;
-                        const uint32_t *w = reinterpret_cast<const uint32_t *>(&x[i]);
-                        uint32_t y[8];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) tr_halves(w[e], &y[2 * e], &y[2 * e + 1]);
-                        const uint32_t at = tile_at(slot, lw * RW + row, col);
-                        st_shared16(at, make_uint4(y[0], y[1], y[2], y[3]));
-                        st_shared16(at ^ 16, make_uint4(y[4], y[5], y[6], y[7]));  // (col is a multiple of 16)
+                        const uint32_t dst = Q8 ? raw_s + issued % S::RAW * S::RAW_TILE + ((lw * ITER + i0 + i) * 32 + lane) * 16
+                                                : tile_at(slot, lw * RW + row, col);
+                        const bool real = place[i] >= 0 && col < dim;
+                        const uint8_t *src = pool[w] + (real ? place[i] * EB : 0);
+                        if (a.vec) tr_copy16(dst, src + (real ? col * EB : 0), real);
+                        else st_shared16(dst, real ? tree_piece<EB>(src, col, dim) : make_uint4(0, 0, 0, 0));
                     }
                 }
-            } else if (where >= 0) {
+                }
+                ptx::cp_async_commit();
+#pragma unroll
+                for (int i = 0; i <= S::LAG; ++i)
+                    if (issued - given == static_cast<uint32_t>(i)) note[i] = where;
+                ++issued;
+            };
+            uint32_t step_no = 0;  // steps of all pieces
+            uint32_t i = 0;        // pieces taken
+            // the piece: its next tile in the order K0 K1 V0 K2 V1 ..., 2 * steps when all have been started
+            TreeItem *it = nullptr;
+            int b = 0, head = 0, n = 0, slot_first = 0, steps = 0, p = 0, entry = 0;
+            bool q_due = false, end = false;
+            int64_t v_off = -1, v_next = -1;   // rows of the values of the step whose keys were started last, and the one before
+            // of this lane's slots: pages two steps ahead, scales one
+            int row = 0, page = -1, row_next = 0, page_next = -1;
+            float ks = 0.f, vs = 0.f;
+            auto page_id = [&](int j) {
+                const int slot = slot_first + j * KEYS + lw * RW + lane;
+                page_next = -1;
+                if (lane >= RW || j >= steps || slot >= n) return;
+                const int at = static_cast<int>(fast_div(slot, a.c.page_div));
+                row_next = slot - at * a.c.page;
+                page_next = a.c.table[b * a.c.table_stride + at];
+                if (page_next >= 0 && page_next < a.c.n_pages) return;
+                page_next = -1;
+                note_error(LC_ERR_CACHE_INDEX, kClassTree);
+            };
+            auto turn_page = [&](int j) {  // step j's page and scales, and the next one's page asked for
+                page = page_next;
+                row = row_next;
+                if constexpr (Q8) {
+                    ks = vs = 0.f;
+                    if (page >= 0) {
+                        ks = a.c.ks[row_offset(a.c.kss, page, head, row)];
+                        vs = a.c.vs[row_offset(a.c.vss, page, head, row)];
+                    }
+                }
+                page_id(j + 1);
+            };
+            // one thing after another -- a piece taken, its q, a tile started -- and then the tiles that have landed are
+            // given on, all but the newest LAG, or all where the next thing is not to be had yet
 #pragma unroll 1
-                for (int i = 0; i < ITER; ++i) {
-                    int row, col;
-                    piece_of(i, &row, &col);
-                    if (col >= dim16) continue;
-                    const uint32_t at = tile_at(slot, lw * RW + row, col);
-                    uint4 x = ld_shared16(at);
-                    if (look(x, where, lw * RW + row)) st_shared16(at, x);
-                }
-            }
-            tc::fence_async_smem();
-            arrive_warp(sh.ring_full[slot]);
-            ++given;
-            // an item is given back when its last values, which may be noted in it, have landed
-            if (back < done && given == sh.item[back % kTrItems].last_tile) {
-                arrive_warp(sh.item_empty[back % kTrItems]);
-                ++back;
-            }
-        };
-        // Where a row has a power of two of pieces, a lane's are all the same column, and rows eight apart lie alike.
-        constexpr int SPOTS = PR >= 32 ? 8 : 8 * PR / 32 > 0 ? 8 * PR / 32 : 1;
-        const bool plain = a.vec && dim == dim16;
-        const int first_col = lane % PR * (16 / EB);
-        uint32_t spot[SPOTS];
-#pragma unroll
-        for (int i = 0; i < SPOTS; ++i) {
-            const int row = i * (32 / PR) + lane / PR;
-            spot[i] = tile_at(0, lw * RW + row, first_col) - ring_s;
-        }
-        // starts a tile of pool w from the rows at `from`
-        auto start = [&](int w, int64_t from, int32_t where) {
-            const uint32_t slot = issued % S::SLOTS;
-            if (!Q8 && issued >= S::SLOTS && !wait_warp(sh.ring_empty[slot], issued / S::SLOTS - 1)) return;
-            if (32 % PR == 0 && plain && __all_sync(0xffffffffu, from >= 0 || lane >= RW)) {
-                // every lane the same piece of one row after another: a pointer by shuffle, two additions and a copy
-                const uint8_t *const mine = pool[w] + from * EB;
-                const uint32_t dst = Q8 ? raw_s + issued % S::RAW * S::RAW_TILE + (lw * ITER * 32 + lane) * 16 : ring_s + slot * S::TILE;
-#pragma unroll
-                for (int i0 = 0; i0 < ITER; i0 += 8) {
-                    const uint8_t *src[8];
-#pragma unroll
-                    for (int i = 0; i < 8 && i0 + i < ITER; ++i)
-                        src[i] = reinterpret_cast<const uint8_t *>(__shfl_sync(
-                            0xffffffffu, reinterpret_cast<uint64_t>(mine), (i0 + i) * (32 / PR) + lane / PR));
-#pragma unroll
-                    for (int i = 0; i < 8 && i0 + i < ITER; ++i)
-                        if (first_col < dim)
-                            ptx::cp_async16(Q8 ? dst + (i0 + i) * 512 : dst + spot[i % SPOTS] + (i0 + i) / SPOTS * SPOTS * (32 / PR) * 128,
-                                            src[i] + first_col * EB);
-                }
-            } else {
-            // the rows' places, eight ahead of their copies
-#pragma unroll
-            for (int i0 = 0; i0 < ITER; i0 += 8) {
-                int64_t place[8];
-#pragma unroll
-                for (int i = 0; i < 8 && i0 + i < ITER; ++i) {
-                    int row, col;
-                    piece_of(i0 + i, &row, &col);
-                    place[i] = __shfl_sync(0xffffffffu, from, row);
-                }
-#pragma unroll
-                for (int i = 0; i < 8 && i0 + i < ITER; ++i) {
-                    int row, col;
-                    piece_of(i0 + i, &row, &col);
-                    if (col >= dim16) continue;
-                    const uint32_t dst = Q8 ? raw_s + issued % S::RAW * S::RAW_TILE + ((lw * ITER + i0 + i) * 32 + lane) * 16
-                                            : tile_at(slot, lw * RW + row, col);
-                    const bool real = place[i] >= 0 && col < dim;
-                    const uint8_t *src = pool[w] + (real ? place[i] * EB : 0);
-                    if (a.vec) tr_copy16(dst, src + (real ? col * EB : 0), real);
-                    else st_shared16(dst, real ? tree_piece<EB>(src, col, dim) : make_uint4(0, 0, 0, 0));
-                }
-            }
-            }
-            ptx::cp_async_commit();
-#pragma unroll
-            for (int i = 0; i <= S::LAG; ++i)
-                if (issued - given == static_cast<uint32_t>(i)) note[i] = where;
-            ++issued;
-        };
-        uint32_t step_no = 0;  // steps of all pieces
-        uint32_t i = 0;        // pieces taken
-        // the piece: its next tile in the order K0 K1 V0 K2 V1 ..., 2 * steps when all have been started
-        TreeItem *it = nullptr;
-        int b = 0, head = 0, n = 0, slot_first = 0, steps = 0, p = 0, entry = 0;
-        bool q_due = false, end = false;
-        int64_t v_off = -1, v_next = -1;   // rows of the values of the step whose keys were started last, and the one before
-        // of this lane's slots: pages two steps ahead, scales one
-        int row = 0, page = -1, row_next = 0, page_next = -1;
-        float ks = 0.f, vs = 0.f;
-        auto page_id = [&](int j) {
-            const int slot = slot_first + j * KEYS + lw * RW + lane;
-            page_next = -1;
-            if (lane >= RW || j >= steps || slot >= n) return;
-            const int at = static_cast<int>(fast_div(slot, a.c.page_div));
-            row_next = slot - at * a.c.page;
-            page_next = a.c.table[b * a.c.table_stride + at];
-            if (page_next >= 0 && page_next < a.c.n_pages) return;
-            page_next = -1;
-            note_error(LC_ERR_CACHE_INDEX, kClassTree);
-        };
-        auto turn_page = [&](int j) {  // step j's page and scales, and the next one's page asked for
-            page = page_next;
-            row = row_next;
-            if constexpr (Q8) {
-                ks = vs = 0.f;
-                if (page >= 0) {
-                    ks = a.c.ks[row_offset(a.c.kss, page, head, row)];
-                    vs = a.c.vs[row_offset(a.c.vss, page, head, row)];
-                }
-            }
-            page_id(j + 1);
-        };
-        // one thing after another -- a piece taken, its q, a tile started -- and then the tiles that have landed are
-        // given on, all but the newest LAG, or all where the next thing is not to be had yet
-#pragma unroll 1
-        while (ok && !end) {
-            uint32_t keep = S::LAG;
-            bool q_here = false;
-            if (q_due) {
-                if (n_q && issued != given && !done_warp(sh.q_empty, n_q - 1)) {
-                    keep = 0;  // its last keys among them
-                } else {
-                    if (n_q && !wait_warp(sh.q_empty, n_q - 1)) break;
-                    constexpr int RQ = kTrRows / kTrLoaders;
-                    tree_query<KV, NC, RQ>(a, *it, lw * RQ, q_s, sh.q_scale[(i - 1) & 1]);
-                    ++n_q;
-                    keep = 0;  // and the keys that were started before them
-                    q_due = false;
-                    q_here = true;
-                }
-            } else if (p == 2 * steps) {
-                if (issued != given && !done_warp(sh.item_full[i % kTrItems], i / kTrItems)) {
-                    keep = 0;
-                } else {
-                    if (!wait_warp(sh.item_full[i % kTrItems], i / kTrItems)) break;
-                    it = &sh.item[i % kTrItems];
-                    ++i;
-                    if (it->end) {
-                        end = true;
+            while (ok && !end) {
+                uint32_t keep = S::LAG;
+                bool q_here = false;
+                if (q_due) {
+                    if (n_q && issued != given && !done_warp(sh.q_empty, n_q - 1)) {
+                        keep = 0;  // its last keys among them
+                    } else {
+                        if (n_q && !wait_warp(sh.q_empty, n_q - 1)) break;
+                        constexpr int RQ = kTrRows / kTrLoaders;
+                        tree_query<KV, NC, RQ>(a, *it, lw * RQ, q_s, sh.q_scale[(i - 1) & 1]);
+                        ++n_q;
+                        keep = 0;  // and the keys that were started before them
+                        q_due = false;
+                        q_here = true;
+                    }
+                } else if (p == 2 * steps) {
+                    if (issued != given && !done_warp(sh.item_full[i % kTrItems], i / kTrItems)) {
                         keep = 0;
                     } else {
-                        b = it->b;
-                        head = it->head;
-                        n = it->n;
-                        slot_first = it->begin + it->first * KEYS;
-                        steps = it->steps;
-                        p = entry = 0;
-                        page_id(0);
-                        turn_page(0);
-                    }
-                }
-            } else {
-                const bool is_k = p == 0 || (p & 1 && p < 2 * steps - 1);
-                const int j = is_k ? (p + 1) / 2 : p == 2 * steps - 1 ? steps - 1 : p / 2 - 1;
-                int64_t from;
-                int32_t where = -1;
-                if (is_k) {
-                    from = page >= 0 ? row_offset(a.c.kst, page, head, row) : -1;
-                    v_off = v_next;
-                    v_next = page >= 0 ? row_offset(a.c.vst, page, head, row) : -1;
-                    const int x = step_no % kTrAux;
-                    const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
-                    if (lane == 0) {
-                        if constexpr (RW == 32) sh.there[x][lw] = there;
-                        else reinterpret_cast<uint16_t *>(sh.there[x])[lw] = static_cast<uint16_t>(there);
-                    }
-                    if constexpr (Q8) {
-                        float lv;
-                        asm("lg2.approx.f32 %0, %1;" : "=f"(lv) : "f"(fabsf(vs)));
-                        if (lane < RW) {
-                            aux[(x * 3) * KEYS + lw * RW + lane] = ks;
-                            aux[(x * 3 + 1) * KEYS + lw * RW + lane] = vs;
-                            aux[(x * 3 + 2) * KEYS + lw * RW + lane] = lv;
+                        if (!wait_warp(sh.item_full[i % kTrItems], i / kTrItems)) break;
+                        it = &sh.item[i % kTrItems];
+                        ++i;
+                        if (it->end) {
+                            end = true;
+                            keep = 0;
+                        } else {
+                            b = it->b;
+                            head = it->head;
+                            n = it->n;
+                            slot_first = it->begin + it->first * KEYS;
+                            steps = it->steps;
+                            p = entry = 0;
+                            page_id(0);
+                            turn_page(0);
                         }
-                        // a step's largest logarithm, where they are all near one another (else NaN)
-                        const bool counts = page >= 0 && vs != 0.f;
-                        float most = counts ? lv : -INFINITY, least = counts ? lv : INFINITY;
-#pragma unroll
-                        for (int d = 16; d; d >>= 1) {
-                            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
-                            least = fminf(least, __shfl_xor_sync(0xffffffffu, least, d));
-                        }
-                        const bool odd = __any_sync(0xffffffffu, counts && !(fabsf(lv) <= kFar));
-                        if (lane == 0) sh.range[x][lw] = odd ? make_float2(NAN, NAN) : make_float2(most, least);
                     }
-                    turn_page(j + 1);
-                    ++step_no;
                 } else {
-                    const bool last = j + 1 == steps;
-                    from = last ? v_next : v_off;
-                    const int slot0 = slot_first + j * KEYS;
-                    if (masked(*it, slot0) && entry < kTrMasked) {
-                        where = static_cast<int>((i - 1) % kTrItems) * kTrMasked + entry;
-                        ++entry;
+                    const bool is_k = p == 0 || (p & 1 && p < 2 * steps - 1);
+                    const int j = is_k ? (p + 1) / 2 : p == 2 * steps - 1 ? steps - 1 : p / 2 - 1;
+                    int64_t from;
+                    int32_t where = -1;
+                    if (is_k) {
+                        from = page >= 0 ? row_offset(a.c.kst, page, head, row) : -1;
+                        v_off = v_next;
+                        v_next = page >= 0 ? row_offset(a.c.vst, page, head, row) : -1;
+                        const int x = step_no % kTrAux;
+                        const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
+                        if (lane == 0) {
+                            if constexpr (RW == 32) sh.there[x][lw] = there;
+                            else reinterpret_cast<uint16_t *>(sh.there[x])[lw] = static_cast<uint16_t>(there);
+                        }
+                        if constexpr (Q8) {
+                            float lv;
+                            asm("lg2.approx.f32 %0, %1;" : "=f"(lv) : "f"(fabsf(vs)));
+                            if (lane < RW) {
+                                aux[(x * 3) * KEYS + lw * RW + lane] = ks;
+                                aux[(x * 3 + 1) * KEYS + lw * RW + lane] = vs;
+                                aux[(x * 3 + 2) * KEYS + lw * RW + lane] = lv;
+                            }
+                            // a step's largest logarithm, where they are all near one another (else NaN)
+                            const bool counts = page >= 0 && vs != 0.f;
+                            float most = counts ? lv : -INFINITY, least = counts ? lv : INFINITY;
+#pragma unroll
+                            for (int d = 16; d; d >>= 1) {
+                                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+                                least = fminf(least, __shfl_xor_sync(0xffffffffu, least, d));
+                            }
+                            const bool odd = __any_sync(0xffffffffu, counts && !(fabsf(lv) <= kFar));
+                            if (lane == 0) sh.range[x][lw] = odd ? make_float2(NAN, NAN) : make_float2(most, least);
+                        }
+                        turn_page(j + 1);
+                        ++step_no;
+                    } else {
+                        const bool last = j + 1 == steps;
+                        from = last ? v_next : v_off;
+                        const int slot0 = slot_first + j * KEYS;
+                        if (masked(*it, slot0) && entry < kTrMasked) {
+                            where = static_cast<int>((i - 1) % kTrItems) * kTrMasked + entry;
+                            ++entry;
+                        }
+                        if (last) {  // before it is started: that may give the item back
+                            if (lane == 0) it->last_tile = issued + 1;  // (every warp the same)
+                            __syncwarp();
+                            ++done;
+                        }
                     }
-                    if (last) {  // before it is started: that may give the item back
-                        if (lane == 0) it->last_tile = issued + 1;  // (every warp the same)
-                        __syncwarp();
-                        ++done;
-                    }
+                    start(is_k ? 0 : 1, from, where);
+                    if (!ok) break;
+                    q_due = p == 0;
+                    ++p;
                 }
-                start(is_k ? 0 : 1, from, where);
-                if (!ok) break;
-                q_due = p == 0;
-                ++p;
-            }
-            if (issued - given > keep || q_here) {
-                if (keep) ptx::cp_async_wait<S::LAG>();
-                else ptx::cp_async_wait<0>();
+                if (issued - given > keep || q_here) {
+                    if (keep) ptx::cp_async_wait<S::LAG>();
+                    else ptx::cp_async_wait<0>();
 #pragma unroll 1
-                while (issued - given > keep && ok) give();
+                    while (issued - given > keep && ok) give();
+                }
+                if (q_here && ok) {
+                    tc::fence_async_smem();
+                    arrive_warp(sh.q_full);
+                }
             }
-            if (q_here && ok) {
-                tc::fence_async_smem();
-                arrive_warp(sh.q_full);
-            }
-        }
-        ptx::cp_async_wait<0>();
+            ptx::cp_async_wait<0>();
         }
     } else if (warp == kTrSoft + kTrLoaders) {
         few_registers();
@@ -1370,8 +1379,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                     tc::wait_ld(o);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = none ? 0u : __float_as_uint(__uint_as_float(o[e]) * f);
-                    if (any_bad)
-                    for (int n = 0; n < n_bad; ++n)
+                    for (int n = 0; any_bad && n < n_bad; ++n)
 #pragma unroll 1
                         for (int w = 0; w < 4; ++w)
 #pragma unroll 1
