@@ -45,9 +45,9 @@ constexpr uint32_t kClassPrompt = 0xf3;
 constexpr int kPrRows = 128;   // rows of a tile
 constexpr int kPrKeys = 128;   // keys of a step
 constexpr int kPrChunk = kPrKeys * 128;  // bytes of 64 columns of a tile
-constexpr int kPrItems = 4;    // items that the scheduling warp may be ahead
+constexpr int kPrItems = 3;    // items that the scheduling warp may be ahead
 constexpr int kPrMasked = 6;   // steps of an item whose values are looked through: three at either end of its keys at most
-constexpr int kPrTurns = 3;    // items whose unusual values are held: one tile may be two items ahead of the other
+constexpr int kPrTurns = kPrItems + 1;  // items whose unusual values are held: one tile may be as many ahead of the other
 
 struct PromptArgs {
     const int32_t *starts, *k_starts;
@@ -132,9 +132,11 @@ __device__ __forceinline__ float pr_max3(float a, float b, float c) {
 
 // ---- scheduling ------------------------------------------------------------
 
-// Items are taken from the longest to the shortest.  A sequence's tiles are
+// Up to 32 sequences' items are taken from the longest to the shortest: a sequence's tiles are
 // counted from its last one down: the last one's level is the tiles of keys
-// that come before the sequence's end, the one before it has a level less.
+// that come before the sequence's end, the one before it has a level less.  With more of them
+// a block has many items, and they are taken in the sequences' order, the last tile of each first: to look
+// for the longest of 2000 sequences of 20 tokens took 20 times as long as to compute them.
 struct PromptSeq {
     int level, tiles;
     bool fell;  // it ends before it begins
@@ -166,61 +168,76 @@ __device__ __forceinline__ int prompt_above(const PromptArgs &a, const PromptSeq
     return min(max(s.level - x + 1, 0), s.tiles);
 }
 
-// Item `at` of all, by one warp.
+// Where a block has come to among the sequences: 32 of them, a lane each.
+struct PromptCursor {
+    PromptSeq mine;
+    int b0;
+    uint32_t before;  // tiles of the sequences before them
+    bool fell;        // starts fall somewhere: sequences share rows, so there is no answer, and no bound on the tiles
+};
+
 template <int TILES>
-__device__ __forceinline__ void prompt_item(const PromptArgs &a, uint32_t at, PromptItem *it) {
+__device__ __forceinline__ PromptCursor prompt_begin(const PromptArgs &a) {
     const int lane = threadIdx.x & 31;
-    const uint32_t pair = fast_div(at, a.pair_div);
+    PromptCursor c{{0, 0, false}, 0, 0, false};
+    if (lane < a.n_seqs) c.mine = prompt_seq<TILES>(a, lane, nullptr);
+    bool fell = c.mine.fell;
+#pragma unroll 4
+    for (int b = 32 + lane; b < a.n_seqs; b += 32) fell |= prompt_seq<TILES>(a, b, nullptr).fell;
+    c.fell = __any_sync(0xffffffffu, fell);
+    return c;
+}
+
+// Item `at` of all, by one warp; `at` only rises.
+template <int TILES>
+__device__ __forceinline__ void prompt_item(const PromptArgs &a, uint32_t at, PromptCursor &c, PromptItem *it) {
+    const int lane = threadIdx.x & 31;
+    uint32_t pair = fast_div(at, a.pair_div);
     const int which = static_cast<int>(at - pair * a.pair_div.d);
-    PromptSeq mine{0, 0, false};
-    if (lane < a.n_seqs) mine = prompt_seq<TILES>(a, lane, nullptr);
-    bool fell = mine.fell;
-    auto total = [&](int x) {
-        uint32_t n = lane < a.n_seqs ? prompt_above(a, mine, x) : 0;
-        for (int b = 32 + lane; b < a.n_seqs; b += 32) {
-            const PromptSeq s = prompt_seq<TILES>(a, b, nullptr);
-            fell |= s.fell;
-            n += prompt_above(a, s, x);
-        }
-        return __reduce_add_sync(0xffffffffu, n);
-    };
-    it->end = 1;
-    // (where starts fall, sequences share rows: there is no answer, and no bound on the tiles)
-    const uint32_t tiles = total(0);
-    if (__any_sync(0xffffffffu, fell) || pair >= tiles) return;
-    it->end = 0;
-    // the highest level x with more than `pair` tiles at it or above
-    int lo = 0, hi = a.n_keys / (TILES * a.tokens_tile) + 1;
-    while (hi - lo > 1) {
-        const int mid = lo + (hi - lo) / 2;
-        if (total(mid) > pair) lo = mid;
-        else hi = mid;
-    }
-    uint32_t rest = pair - total(lo + 1);  // of the tiles at level `lo`, in the sequences' order
-    int tile = 0, seq = 0;
-    for (int b0 = 0; b0 < a.n_seqs; b0 += 32) {
-        const int b = b0 + lane;
-        PromptSeq s{0, 0, false};
-        if (b < a.n_seqs) s = b0 == 0 ? mine : prompt_seq<TILES>(a, b, nullptr);
-        const uint32_t n = b < a.n_seqs ? prompt_above(a, s, lo) - prompt_above(a, s, lo + 1) : 0;
-        uint32_t upto = n;
+    auto scan = [&](uint32_t n) {  // over the lanes up to this one
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const uint32_t o = __shfl_up_sync(0xffffffffu, upto, d);
-            if (lane >= d) upto += o;
+            const uint32_t o = __shfl_up_sync(0xffffffffu, n, d);
+            if (lane >= d) n += o;
         }
-        const unsigned hit = __ballot_sync(0xffffffffu, upto > rest);
-        if (hit) {
-            const int src = __ffs(hit) - 1;
-            // tiles of the level begin where those above it, at the sequence's end, leave off
-            const int i = static_cast<int>(rest - (upto - n));
-            const int from = a.causal ? s.tiles - prompt_above(a, s, lo) : 0;
-            tile = __shfl_sync(0xffffffffu, from + i, src);
-            seq = b0 + src;
-            break;
+        return n;
+    };
+    it->end = 1;
+    if (c.fell) return;
+    int tile = 0, seq = 0;
+    if (a.n_seqs <= 32) {
+        auto total = [&](int x) { return __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(prompt_above(a, c.mine, x))); };
+        if (pair >= total(0)) return;
+        // the highest level x with more than `pair` tiles at it or above
+        int lo = 0, hi = a.n_keys / (TILES * a.tokens_tile) + 1;
+        while (hi - lo > 1) {
+            const int mid = lo + (hi - lo) / 2;
+            if (total(mid) > pair) lo = mid;
+            else hi = mid;
         }
-        rest -= __shfl_sync(0xffffffffu, upto, 31);
+        pair -= total(lo + 1);  // of the tiles at level `lo`, in the sequences' order
+        const uint32_t n = prompt_above(a, c.mine, lo) - prompt_above(a, c.mine, lo + 1), upto = scan(n);
+        seq = __ffs(__ballot_sync(0xffffffffu, upto > pair)) - 1;
+        // tiles of the level begin where those above it, at the sequence's end, leave off
+        const int from = a.causal ? c.mine.tiles - prompt_above(a, c.mine, lo) : 0;
+        tile = __shfl_sync(0xffffffffu, from + static_cast<int>(pair - (upto - n)), seq);
+    } else {
+        uint32_t upto;
+        for (;;) {
+            upto = scan(c.mine.tiles);
+            const uint32_t all = __shfl_sync(0xffffffffu, upto, 31);
+            if (pair < c.before + all) break;
+            c.before += all;
+            c.b0 += 32;
+            if (c.b0 >= a.n_seqs) return;
+            c.mine = PromptSeq{0, 0, false};
+            if (c.b0 + lane < a.n_seqs) c.mine = prompt_seq<TILES>(a, c.b0 + lane, nullptr);
+        }
+        const int src = __ffs(__ballot_sync(0xffffffffu, c.before + upto > pair)) - 1;
+        tile = __shfl_sync(0xffffffffu, static_cast<int>(c.before + upto - pair) - 1, src);
+        seq = c.b0 + src;
     }
+    it->end = 0;
     prompt_seq<TILES>(a, seq, it);
     it->key_head = which / a.head_blocks;
     it->head0 = which % a.head_blocks * a.heads_tile;
@@ -305,6 +322,10 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
             note_error(LC_ERR_TIMEOUT, kClassPrompt);
         }
         return ok;
+    };
+
+    auto drained = [&](const uint64_t &b, uint32_t n) {  // what was started ends, however short the limit
+        if (!tc::wait(bar(b), n, max(a.limit_ns, uint64_t(2000000000)))) note_error(LC_ERR_TIMEOUT, kClassPrompt);
     };
 
     // of a block's registers the softmax threads take the larger part (384 x 168 = 256 x 216 + 128 x 72)
@@ -552,10 +573,11 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
     } else if (warp == S::SOFT + 2) {
         few_registers();
         // scheduling: items dealt in turn, every other round backwards, so that none gets the longest of each
+        PromptCursor cursor = prompt_begin<TILES>(a);
         for (uint32_t i = 0; ok; ++i) {
             const uint32_t at = i * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
             PromptItem it{};
-            prompt_item<TILES>(a, at, &it);
+            prompt_item<TILES>(a, at, cursor, &it);
             const int s = i % kPrItems;
             if (i >= kPrItems && !wait_warp(sh.item_empty[s], i / kPrItems - 1)) break;
             if (lane == 0) sh.item[s] = it;
@@ -614,13 +636,12 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
             if (!ok) break;
         }
         if (!ok) {  // copies in flight end before the block does
-            ok = true;
             for (uint32_t s = 0; s < S::SLOTS; ++s) {
                 const uint32_t used = round + (s < slot);
-                if (used) wait_warp(sh.ring_full[s], used - 1);
+                if (used) drained(sh.ring_full[s], used - 1);
             }
             for (int t = 0; t < TILES; ++t)
-                if (tiles_q[t]) wait_warp(sh.q_full[t], tiles_q[t] - 1);
+                if (tiles_q[t]) drained(sh.q_full[t], tiles_q[t] - 1);
         }
     } else if (warp == S::SOFT || (TILES == 2 && warp == S::SOFT + 3)) {
         few_registers();
@@ -760,9 +781,9 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
             if (!ok) break;
         }
         // products in flight end before the tensor memory is given back
-        ok = true;
         tc::commit(bar(sh.drain[0]) + t * 8);
-        wait_all(sh.drain[t], 0);
+        drained(sh.drain[t], 0);
+        tc::fence_after();
     } else {
         few_registers();
     }

@@ -111,7 +111,7 @@ template <int KEYS>
 __device__ __forceinline__ int tree_steps(const TreeArgs &a, const TreeSeq &first) {  // (of the sequence of this lane's number)
     const int lane = threadIdx.x & 31;
     int all = first.steps * first.blocks * a.c.heads;
-#pragma unroll 1
+#pragma unroll 4
     for (int b = lane + 32; b < a.c.n_seqs; b += 32) {
         const TreeSeq s = tree_seq<KEYS>(a, b);
         all += s.steps * s.blocks * a.c.heads;
@@ -459,6 +459,9 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
         }
         return ok;
     };
+    auto drained = [&](const uint64_t &b, uint32_t n) {  // what was started ends, however short the limit
+        if (!tc::wait(bar(b), n, max(a.limit_ns, uint64_t(2000000000)))) note_error(LC_ERR_TIMEOUT, kClassTree);
+    };
     auto done_warp = [&](const uint64_t &b, uint32_t n) { return __all_sync(0xffffffffu, ptx::mbar_try_wait(bar(b), n & 1)) != 0; };
     // whether some row of a piece sees a step in part
     auto masked = [&](const TreeItem &it, int slot0) {
@@ -493,11 +496,9 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
         };
 #pragma unroll 1
         for (int b0 = 0; b0 < a.c.n_seqs && from < to && ok; b0 += 32) {
-            TreeSeq s = seq0;
-            if (b0) {
-                s = TreeSeq{};
-                if (b0 + lane < a.c.n_seqs) s = tree_seq<KEYS>(a, b0 + lane);
-            }
+            const TreeSeq s = seq0;
+            seq0 = TreeSeq{};  // the next 32, read while these are gone through
+            if (b0 + 32 + lane < a.c.n_seqs) seq0 = tree_seq<KEYS>(a, b0 + 32 + lane);
             const int w = s.steps * s.blocks * a.c.heads;
             int upto = w;
 #pragma unroll
@@ -677,10 +678,9 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                 }
             }
             // copies in flight end before the block does
-            ok = true;
             for (uint32_t k = 0; k < M; ++k) {
                 const uint32_t used = round + (k < at);
-                if (used) wait_warp(*((Q8 ? sh.raw_full : sh.ring_full) + k), used - 1);
+                if (used) drained(*((Q8 ? sh.raw_full : sh.ring_full) + k), used - 1);
             }
         }
     } else if (TMA && warp >= kTrSoft && warp < kTrSoft + kTrLoaders) {
@@ -1108,9 +1108,9 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
             if (!ok) break;
         }
         // products in flight end before the tensor memory is given back
-        ok = true;
         tc::commit(bar(sh.drain));
-        wait_all(sh.drain, 0);
+        drained(sh.drain, 0);
+        tc::fence_after();
     } else if (warp < kTrSoft) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
         // softmax and outputs: a thread a row and half of a step's slots
