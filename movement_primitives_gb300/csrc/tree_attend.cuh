@@ -227,6 +227,11 @@ __device__ __forceinline__ void tr_copy16(uint32_t dst, const void *src, bool re
 __device__ __forceinline__ void st_shared16(uint32_t dst, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
+__device__ __forceinline__ void st_global16(void *dst, uint4 v, bool does) {  // by predicate: the warp stays together
+    asm volatile("{.reg .pred p; setp.ne.b32 p, %5, 0; @p st.global.v4.b32 [%0], {%1, %2, %3, %4};}" ::"l"(dst), "r"(v.x), "r"(v.y),
+                 "r"(v.z), "r"(v.w), "r"(static_cast<uint32_t>(does))
+                 : "memory");
+}
 __device__ __forceinline__ uint4 ld_shared16(uint32_t src) {
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(src) : "memory");
@@ -1401,14 +1406,13 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                                     if (c * 16 + e < a.c.dim)
                                         o[e] = __float_as_uint(__uint_as_float(o[e]) + tree_unusual<KV>(v, c * 16 + e));
                             }
-                    if (!real) {
-                    } else if (it.part >= 0) {
+                    if (it.part >= 0) {
                         float4 *to = reinterpret_cast<float4 *>(a.part) + (int64_t(it.part) * NC * 16 + c * 4) * kTrRows + row;
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            to[e * kTrRows] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                                          __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+                            st_global16(to + e * kTrRows, make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]), real);
                     } else {
+                        const bool whole = a.out_vec && c * 16 + 16 <= a.c.dim;
 #pragma unroll
                         for (int e = 0; e < 16; e += 8) {
                             uint32_t y[4];
@@ -1416,12 +1420,13 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                             for (int k = 0; k < 4; ++k)
                                 y[k] = tr_pack<KV == LC_CACHE_F16>(__uint_as_float(o[e + 2 * k]), __uint_as_float(o[e + 2 * k + 1]));
                             uint16_t *to = out + c * 16 + e;
-                            if (a.out_vec && c * 16 + e + 8 <= a.c.dim) {
-                                *reinterpret_cast<uint4 *>(to) = make_uint4(y[0], y[1], y[2], y[3]);
-                            } else {
+                            if (whole) {
+                                st_global16(to, make_uint4(y[0], y[1], y[2], y[3]), real);
+                            } else if (real) {
 #pragma unroll 1
                                 for (int k = 0; k < 8; ++k)
-                                    if (c * 16 + e + k < a.c.dim) to[k] = static_cast<uint16_t>((k < 4 ? k < 2 ? y[0] : y[1] : k < 6 ? y[2] : y[3]) >> (k & 1) * 16);
+                                    if (c * 16 + e + k < a.c.dim)
+                                        to[k] = static_cast<uint16_t>((k < 4 ? k < 2 ? y[0] : y[1] : k < 6 ? y[2] : y[3]) >> (k & 1) * 16);
                             }
                         }
                     }

@@ -242,6 +242,16 @@ def test_many_sequences():
     run([1] * 300, [(i * 5) % 40 for i in range(300)], heads=6, kv=3, dim=96, seed=20)
 
 
+@pytest.mark.parametrize("n", [32, 33, 64, 65, 333])
+@pytest.mark.parametrize("kw", [dict(causal=False), dict(window=70), dict(causal=False, window=9), dict(tail=130, first=7)])
+def test_many_sequences_in_order(n, kw):
+    """Past 32 sequences items come in another order: long and empty ones at either end and between."""
+    nq = [(17 * i) % 61 for i in range(n)]
+    nq[0], nq[-1], nq[n // 2] = 300, 400, 0
+    run(nq, [(13 * i) % 150 for i in range(n)], heads=4, kv=2, dim=64, seed=n, **kw)
+    run(nq, heads=2, kv=1, dim=192, seed=n, **kw)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_strided_arguments(dtype):
     """q, k and v in one buffer; out among other rows; lse among other heads."""
