@@ -35,11 +35,11 @@
 // them a row's (each half of the slots; they exchange their maxima).
 //
 // What bounds it, by GB300 figures of the kernels alone.  16 sequences of up to 4096
-// slots, 8 key heads of 128, 64 rows each, bfloat16 (143 MB): 44 us, 3.3 TB/s, where a steady step runs at
+// slots, 8 key heads of 128, 64 rows each, bfloat16 (143 MB): 43 us, 3.4 TB/s, where a steady step runs at
 // the memory's rate; the rest is the scheduler's reads, the first rows, the parts' way through
 // the L2 and the joining (6 us).  12 sequences of up to 32767, 128 rows, E4M3 (443 MB): 218 us, bound by the
 // softmax warps (3400 of 3900 cycles a step): two multiplications by scales more than
-// in bfloat16, beside the conversions.  One of 301 slots: 10.3 us, the chain from the
+// in bfloat16, beside the conversions.  One of 301 slots: 10 us, the chain from the
 // lengths to the join.  By copies of the four warps alone the first took 84 us and the second 678.
 #pragma once
 
@@ -1527,7 +1527,7 @@ int launch_tree_shape(const TreeArgs &a, cudaStream_t cs) {
     const int64_t steps = units * ((int64_t(a.c.cap) + S::KEYS - 1) / S::KEYS);
     // Steps of a run: one, so that a few short sequences take as many blocks as there are steps (a sequence of 300 slots, 2
     // key heads of 64: 10.3 us, 12.8 with two); two past 128 elements a head, whose parts are twice as large and whose joining
-    // is as long as a step (8 windows of 1024, 192 rows of 256: 24.5 us, 26.5 with one).
+    // is as long as a step (8 windows of 1024, 192 rows of 256: 23 us, 2 more with one).
     b.least = NC <= 2 ? 1 : 2;
     b.runs = static_cast<int32_t>(std::min<int64_t>(std::min(sms, kTrMostRuns), (steps + b.least - 1) / b.least));
     const int st = launch_after(fn, b.runs, S::THREADS, S::SMEM, cs, &b);
