@@ -432,6 +432,31 @@ def test_repeatable_on_any_stream_and_in_graphs():
     no_device_error()
 
 
+def test_calls_at_once():
+    """Prompts, trees and accepted drafts on streams of their own, at the same time, and one after another on each."""
+    g = torch.Generator().manual_seed(22)
+    calls = []
+    for kind, dim in (("bf16", 64), ("e4m3", 128), ("fp16", 256)):
+        s = Setup([700, 33, 1500], heads=2, dim=dim, kind=kind, seed=dim)
+        q, parents = queries(s, 7, 6), trees(3, 7, s.g)
+        calls.append(lambda s=s, q=q, p=parents: lc().cache_attend_tree(s.cache, q, s.lengths, p))
+    for dim in (64, 192):
+        x = torch.randn((500, 8, dim), generator=g).bfloat16().cuda()
+        starts = ints([0, 200, 201, 500])
+        calls.append(lambda x=x, t=starts: lc().prompt_attend(x[:, :4], x[:, 4:6], x[:, 6:], t))
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(4)], [[] for _ in calls]
+    for turn in range(12):
+        for i, c in enumerate(calls):
+            with torch.cuda.stream(streams[(i + turn) % 4]):
+                got[i].append(c())
+    torch.cuda.synchronize()
+    for i, outs in enumerate(got):
+        assert all(torch.equal(want[i], x) for x in outs)
+    no_device_error()
+
+
 def test_a_draft_alone_is_decoding():
     """One draft a sequence sees what the query of cache_attend does."""
     for kind in KINDS:
