@@ -75,6 +75,7 @@ struct TreeArgs {
     int32_t negative;
     int32_t vec, q_vec, out_vec;  // rows of the pools, of q and of out are whole 16-byte words on 16-byte boundaries
     int32_t runs, least;    // blocks of the main kernel; steps of a run at least
+    int32_t whole;          // not 0: units are not cut, nothing is joined
     int32_t most_blocks;    // tiles of rows a key head at most
     int2 *split;            // of a unit: its first and its last run
     float *part;            // [2 runs][dim / 4 rounded up to 16][128 rows][4]
@@ -106,15 +107,16 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs &a, int b) {
     return s;
 }
 
-// Steps of all units, by a warp.
+// Steps of all units (where they stay whole: units), by a warp.
 template <int KEYS>
 __device__ __forceinline__ int tree_steps(const TreeArgs &a, const TreeSeq &first) {  // (of the sequence of this lane's number)
     const int lane = threadIdx.x & 31;
-    int all = first.steps * first.blocks * a.c.heads;
+    auto of = [&](const TreeSeq &s) { return (a.whole ? min(s.steps, 1) : s.steps) * s.blocks * a.c.heads; };
+    int all = of(first);
 #pragma unroll 4
     for (int b = lane + 32; b < a.c.n_seqs; b += 32) {
         const TreeSeq s = tree_seq<KEYS>(a, b);
-        all += s.steps * s.blocks * a.c.heads;
+        all += of(s);
     }
     return __reduce_add_sync(0xffffffffu, all);
 }
@@ -504,7 +506,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
             const TreeSeq s = seq0;
             seq0 = TreeSeq{};  // the next 32, read while these are gone through
             if (b0 + 32 + lane < a.c.n_seqs) seq0 = tree_seq<KEYS>(a, b0 + 32 + lane);
-            const int w = s.steps * s.blocks * a.c.heads;
+            const int w = (a.whole ? min(s.steps, 1) : s.steps) * s.blocks * a.c.heads;
             int upto = w;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -519,9 +521,10 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                 const int n = __shfl_sync(0xffffffffu, s.n, l), count = __shfl_sync(0xffffffffu, s.count, l);
                 const int begin = __shfl_sync(0xffffffffu, s.begin, l);
                 const int in = from - at - __shfl_sync(0xffffffffu, upto - w, l);
-                const int unit = in / steps, first = in - unit * steps, take = min(to - from, steps - first);
+                const int unit = a.whole ? in : in / steps, first = a.whole ? 0 : in - unit * steps;
+                const int take = a.whole ? steps : min(to - from, steps - first);
                 // for the joining: the runs of a unit, from the one that holds its first step
-                if (first == 0 && lane == 0)
+                if (!a.whole && first == 0 && lane == 0)
                     a.split[(int64_t(b0 + l) * a.c.heads + unit / blocks) * a.most_blocks + unit % blocks] =
                         make_int2(blockIdx.x, runs.of(from + steps - 1));
                 post([&](TreeItem &it) {
@@ -540,7 +543,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                     if (lane < 4 * kTrMasked) it.bad[lane / 4][lane % 4] = 0;
                     __syncwarp();
                 });
-                from += take;
+                from += a.whole ? 1 : take;
             }
             at += __shfl_sync(0xffffffffu, upto, 31);
         }
@@ -1528,10 +1531,16 @@ int launch_tree_shape(const TreeArgs &a, cudaStream_t cs) {
     // Steps of a run: one, so that a few short sequences take as many blocks as there are steps (a sequence of 300 slots, 2
     // key heads of 64: 10.3 us, 12.8 with two); two past 128 elements a head, whose parts are twice as large and whose joining
     // is as long as a step (8 windows of 1024, 192 rows of 256: 23 us, 2 more with one).
-    b.least = NC <= 2 ? 1 : 2;
-    b.runs = static_cast<int32_t>(std::min<int64_t>(std::min(sms, kTrMostRuns), (steps + b.least - 1) / b.least));
+    // Units stay whole, and nothing is joined by a second launch, where the table's columns are few steps: up to four
+    // (2 units of 3 steps of 64 elements a head: 9.3 us, cut 9.8, and 3 us less on the host; 128 of 3 steps of 128: 12.0 and 17.7;
+    // of 4 in E4M3 2 units take 17.5 cut 15.3, 128 units 19.2 and 29.1), and up to eight where units take more than half of the
+    // blocks (128 units: 17.7 and 24.9; 2 units of 8 steps 16.6 and 12.5).
+    const int64_t most = (int64_t(a.c.cap) + S::KEYS - 1) / S::KEYS;
+    b.whole = most <= (units <= sms && 2 * units > sms ? 8 : 4);
+    b.least = NC <= 2 || b.whole ? 1 : 2;
+    b.runs = static_cast<int32_t>(std::min<int64_t>(std::min(sms, kTrMostRuns), b.whole ? units : (steps + b.least - 1) / b.least));
     const int st = launch_after(fn, b.runs, S::THREADS, S::SMEM, cs, &b);
-    if (st) return st;
+    if (st || b.whole) return st;
     return launch_after(reinterpret_cast<const void *>(&k_tree_join<KV, NC>), static_cast<unsigned>(units * 8 * NC), 256, 0, cs, &b);
 }
 
