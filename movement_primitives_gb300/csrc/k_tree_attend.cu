@@ -13,14 +13,14 @@ int launch_tree_e4m3(const TreeArgs &a, cudaStream_t cs);
 
 namespace {
 
-// Offsets of the parts' maxima and sums, of the units' runs, and the end.
+// Offsets of the parts' maxima and sums, of the runs' cuts, and the end.
 struct TreeSpace {
     int64_t ml, split, end;
-    TreeSpace(const CacheArgs &c, int64_t units) {
+    explicit TreeSpace(const CacheArgs &c) {
         const int64_t rows = int64_t(2) * kTrMostRuns * kTrRows;
         ml = rows * ((c.dim + 63) / 64 * 64 * 4);
         split = ml + rows * 8;
-        end = split + units * 8;
+        end = split + kTrMostRuns * 16;
     }
 };
 
@@ -58,7 +58,7 @@ extern "C" int64_t lc_cache_attend_tree_workspace(const lc_paged_cache *cache, i
     if (check_cache(cache, false, &c) || n_q_heads < 1 || n_q_heads % c.heads || n_drafts < 0 ||
         n_drafts > LC_CACHE_MAX_DRAFTS)
         return -1;
-    return TreeSpace(c, int64_t(c.n_seqs) * c.heads * most_blocks(n_drafts, n_q_heads / c.heads)).end;
+    return TreeSpace(c).end;
 }
 
 extern "C" int lc_cache_attend_tree(const lc_paged_cache *cache, const lc_cache_tree *q, lc_stream_t stream) {
@@ -97,10 +97,9 @@ extern "C" int lc_cache_attend_tree(const lc_paged_cache *cache, const lc_cache_
     if (int64_t(q->n_drafts) * a.group > 1 << 24) return LC_ERR_OVERFLOW;
     a.most_blocks = most_blocks(q->n_drafts, a.group);
     const int64_t heads = int64_t(cache->n_seqs) * cache->n_kv_heads;
-    if (heads > 0x3ffffff / a.most_blocks) return LC_ERR_OVERFLOW;  // (32 blocks a unit in the second launch)
     const int keys = a.c.dim <= 128 ? 128 : 64;
     if (heads * a.most_blocks > 0x7fffffff / (a.c.cap / keys + 2)) return LC_ERR_OVERFLOW;  // (steps are counted in 32 bits)
-    const TreeSpace space(a.c, heads * a.most_blocks);
+    const TreeSpace space(a.c);
     if (!q->workspace) return LC_ERR_NULL;
     if (space.end > q->workspace_bytes) return LC_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(q->workspace) % 256) return LC_ERR_ALIGN;
@@ -132,7 +131,7 @@ extern "C" int lc_cache_attend_tree(const lc_paged_cache *cache, const lc_cache_
     a.out_vec = rows_aligned(q->out, 3, ext, q->out_stride, 2, 16);
     a.part = static_cast<float *>(q->workspace);
     a.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(q->workspace) + space.ml);
-    a.split = reinterpret_cast<int2 *>(static_cast<uint8_t *>(q->workspace) + space.split);
+    a.split = reinterpret_cast<int4 *>(static_cast<uint8_t *>(q->workspace) + space.split);
     a.limit_ns = wait_limit_ns();
     a.piece_div = make_fastdiv(static_cast<uint32_t>(std::max(a.c.dim / 16, 1)));
     // Tensor copies where rows lie on 16-byte boundaries, pages are whole eights of slots (which the swizzle needs) and

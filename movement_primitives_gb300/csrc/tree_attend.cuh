@@ -77,7 +77,7 @@ struct TreeArgs {
     int32_t runs, least;    // blocks of the main kernel; steps of a run at least
     int32_t whole;          // not 0: units are not cut, nothing is joined
     int32_t most_blocks;    // tiles of rows a key head at most
-    int2 *split;            // of a unit: its first and its last run
+    int4 *split;            // [runs]: the unit that is cut at the run's end (sequence, -1 for none, head, tile), its last run
     float *part;            // [2 runs][dim / 4 rounded up to 16][128 rows][4]
     float2 *part_ml;        // [2 runs][128]
     int32_t box;            // slots of a tensor copy
@@ -481,6 +481,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
         few_registers();
         // scheduling: the pieces of this block's run
         int at = 0, from = 0, to = 0;
+        int4 cut = make_int4(-1, 0, 0, 0);  // for the joining
         TreeSeq seq0{};
         if (lane < a.c.n_seqs) seq0 = tree_seq<KEYS>(a, lane);
         const TreeRuns runs(a, tree_steps<KEYS>(a, seq0));
@@ -523,10 +524,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                 const int in = from - at - __shfl_sync(0xffffffffu, upto - w, l);
                 const int unit = a.whole ? in : in / steps, first = a.whole ? 0 : in - unit * steps;
                 const int take = a.whole ? steps : min(to - from, steps - first);
-                // for the joining: the runs of a unit, from the one that holds its first step
-                if (!a.whole && first == 0 && lane == 0)
-                    a.split[(int64_t(b0 + l) * a.c.heads + unit / blocks) * a.most_blocks + unit % blocks] =
-                        make_int2(blockIdx.x, runs.of(from + steps - 1));
+                if (first == 0 && take < steps) cut = make_int4(b0 + l, unit / blocks, unit % blocks, runs.of(from + steps - 1));
                 post([&](TreeItem &it) {
                     if (lane == 0) {
                         it.b = b0 + l;
@@ -548,6 +546,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
             at += __shfl_sync(0xffffffffu, upto, 31);
         }
         if (ok) post([&](TreeItem &it) { if (lane == 0) it.end = 1; });
+        if (!a.whole) a.split[blockIdx.x] = cut;  // (by every lane)
     } else if (TMA && warp == kIssuer) {
         few_registers();
         if constexpr (TMA) {
@@ -1455,24 +1454,44 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
     }
 }
 
-// Joins the parts of the units that were cut, in their order: a block a unit, 32
+// Joins the parts of the units that were cut, in their order: a block a cut (the end of a run), 32
 // rows and 32 columns, a warp four columns, a lane a row.
 template <int KV, int NC>
 __global__ void __launch_bounds__(256) k_tree_join(const __grid_constant__ TreeArgs a) {
     constexpr int KEYS = TreeShape<NC, KV == LC_CACHE_E4M3>::KEYS;
     constexpr float kSumLift = KV == LC_CACHE_F16 ? 8.f : KV == LC_CACHE_E4M3 ? 0.f : -40.f;
     __shared__ float2 ml[8][32];
+    __shared__ uint32_t cuts_of[8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     start_after_prior();
-    const int columns = blockIdx.x % (2 * NC), group = blockIdx.x / (2 * NC) % 4, unit = blockIdx.x / (8 * NC);
-    const int block = unit % a.most_blocks, head = unit / a.most_blocks % a.c.heads, b = unit / a.most_blocks / a.c.heads;
-    const int2 runs = a.split[unit];  // (nothing to go by where the sequence has no such rows)
+    const int columns = blockIdx.x % (2 * NC), group = blockIdx.x / (2 * NC) % 4;
+    // the block's cut, in the runs' order
+    const uint32_t cuts = __ballot_sync(0xffffffffu, static_cast<int>(threadIdx.x) < a.runs && a.split[threadIdx.x].x >= 0);
+    if (lane == 0) cuts_of[warp] = cuts;
+    __syncthreads();
+    int left = blockIdx.x / (8 * NC), run = 0;
+    uint32_t bits = 0;
+#pragma unroll
+    for (int w = 7; w >= 0; --w) {  // (the words before w have `before` of them)
+        int before = 0;
+#pragma unroll
+        for (int v = 0; v < w; ++v) before += __popc(cuts_of[v]);
+        if (bits == 0 && left >= before) {
+            left -= before;
+            bits = cuts_of[w];
+            run = w * 32;
+            if (left >= __popc(bits)) return;  // fewer cuts than blocks for them
+        }
+    }
+    for (; left; --left) bits &= bits - 1;
+    run += __ffs(bits) - 1;
+    const int4 cut = a.split[run];
+    const int b = cut.x, head = cut.y, row0 = cut.z * kTrRows + group * 32;
     const TreeSeq s = tree_seq<KEYS>(a, b);
-    const int row0 = block * kTrRows + group * 32;
-    if (row0 >= s.count * a.group || columns * 32 >= a.c.dim || runs.x == runs.y) return;
-    const int row = group * 32 + lane, n = runs.y - runs.x + 1;
+    if (row0 >= s.count * a.group || columns * 32 >= a.c.dim) return;
+    const int row = group * 32 + lane, n = cut.w - run + 1;
     // the unit's first part is its run's second, the others their runs' first
-    auto slot = [&](int i) { return int64_t(2) * (runs.x + i) + (i == 0); };
+    auto slot = [&](int i) { return int64_t(2) * (run + i) + (i == 0); };
     float top = -INFINITY, l = 0.f;
     for (int i = warp; i < n; i += 8) {
         const float2 v = a.part_ml[slot(i) * kTrRows + row];
@@ -1541,7 +1560,8 @@ int launch_tree_shape(const TreeArgs &a, cudaStream_t cs) {
     b.runs = static_cast<int32_t>(std::min<int64_t>(std::min(sms, kTrMostRuns), b.whole ? units : (steps + b.least - 1) / b.least));
     const int st = launch_after(fn, b.runs, S::THREADS, S::SMEM, cs, &b);
     if (st || b.whole) return st;
-    return launch_after(reinterpret_cast<const void *>(&k_tree_join<KV, NC>), static_cast<unsigned>(units * 8 * NC), 256, 0, cs, &b);
+    return launch_after(reinterpret_cast<const void *>(&k_tree_join<KV, NC>), static_cast<unsigned>(std::min<int64_t>(b.runs, units) * 8 * NC), 256,
+                        0, cs, &b);
 }
 
 template <int KV>

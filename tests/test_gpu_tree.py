@@ -432,6 +432,17 @@ def test_repeatable_on_any_stream_and_in_graphs():
     no_device_error()
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("per", [8, 16, 32, 33, 64, 120])
+def test_short_sequences_behind_long_tables(kind, per):
+    """Whether units may be cut, and how many blocks join them, goes by the table's columns."""
+    n = [(37 * i) % 120 + 3 for i in range(90)]
+    n[7], n[80] = per * 16, per * 16 - 5
+    run(Setup(n, heads=2, dim=64, per=per, kind=kind, seed=per), 3, 2, [i % 4 if i % 4 else 1 for i in range(90)])
+    run(Setup([per * 16, 5, 70], heads=1, dim=192, per=per, kind=kind, seed=per), 3, 3)
+    run(Setup([per * 16 - 3] * 10, heads=8, dim=128, per=per, kind=kind, seed=per), 3, 2, tree="chain")
+
+
 def test_calls_at_once():
     """Prompts, trees and accepted drafts on streams of their own, at the same time, and one after another on each."""
     g = torch.Generator().manual_seed(22)
