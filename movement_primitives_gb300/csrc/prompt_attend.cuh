@@ -358,6 +358,7 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
             const int all_hi = keys_end(tile0), all_lo = keys_begin(tile_last);
             const int item_hi = keys_end(it.t0);
             const int item_lo = keys_begin(min(it.t0 + TILES * a.tokens_tile, it.nq) - 1);
+            const int first_seen = keys_begin(it.t0), last_seen = keys_end(min(it.t0 + TILES * a.tokens_tile, it.nq) - 1);
             const int turn = i % kPrTurns;
             float m = -INFINITY, less = -kLift, l = 0.f;
             int n_bad = 0;
@@ -399,8 +400,7 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
                                                            __vmaxu2(x[g].z & 0x7fff7fffu, x[g].w & 0x7fff7fffu)));
                     }
                     const bool found = (most & 0xffffu) >= kExp || most >> 16 >= kExp;
-                    const uint32_t rows = __ballot_sync(0xffffffffu, found);
-                    if (rows) {
+                    if (__any_sync(0xffffffffu, found)) {
 #pragma unroll 1
                         for (int c = 0; c < NC; ++c)
 #pragma unroll 1
@@ -417,6 +417,9 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
                             }
                         tc::fence_async_smem();
                     }
+                    // what some row sees is added at the end (not the rows behind the sequence, of whatever they hold)
+                    const int key = key0 + row;
+                    const uint32_t rows = __ballot_sync(0xffffffffu, found && key >= first_seen && key < last_seen);
                     sh.bad[turn][n_bad][warp & 3] = rows;  // (by every lane)
                     sh.bad_step[turn][n_bad] = j;
                     sh.bad_any[turn][warp & 3] |= rows ? 1u << n_bad : 0u;

@@ -713,10 +713,11 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                         const uint32_t slot = tiles % S::SLOTS, raw = tiles % S::RAW;
                         if (!wait_warp(sh.raw_full[raw], tiles / S::RAW)) break;
                         if (tiles >= S::SLOTS && !wait_warp(sh.ring_empty[slot], tiles / S::SLOTS - 1)) break;
-                        int where = -1;
+                        int where = -1, there = 0;  // there: rows that somebody may see
                         if (p && (!(p & 1) || p == 2 * steps - 1)) {  // values
                             const int slot0 = slot_first + (p == 2 * steps - 1 ? steps - 1 : p / 2 - 1) * KEYS;
                             if (masked(it, slot0) && entry < kTrMasked) where = entry++;
+                            there = it.n - slot0;
                         }
                         const uint32_t from = raw_s + raw * S::RAW_TILE, to = ring_s + slot * S::TILE;
                         if (where >= 0) {
@@ -725,7 +726,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                                 uint4 x = ld_shared16(from + k * 16);
                                 if (tree_clean<KV>(x)) {
                                     const int row = static_cast<int>(fast_div(k, a.piece_div));
-                                    atomicOr(&it.bad[where][row >> 5], 1u << (row & 31));
+                                    if (row < there) atomicOr(&it.bad[where][row >> 5], 1u << (row & 31));
                                     st_shared16(from + k * 16, x);
                                 }
                             }
@@ -1182,15 +1183,16 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                                 for (int k = 0; k < 8; ++k)
                                     most = __vmaxu2(most, __vmaxu2(__vmaxu2(v[k].x & 0x7fff7fffu, v[k].y & 0x7fff7fffu),
                                                                    __vmaxu2(v[k].z & 0x7fff7fffu, v[k].w & 0x7fff7fffu)));
-                                const uint32_t rows = __ballot_sync(0xffffffffu, (most & 0xffffu) >= kExp || most >> 16 >= kExp);
-                                if (rows) {
+                                const bool found = (most & 0xffffu) >= kExp || most >> 16 >= kExp;
+                                if (__any_sync(0xffffffffu, found)) {
 #pragma unroll 1
                                     for (int k = 0; k < 8; ++k) {
                                         uint4 x = ld_shared16(piece + k * 16);
                                         tree_clean<KV>(x);
                                         st_shared16(piece + k * 16, x);
                                     }
-                                    atomicOr(&it.bad[n_bad][quarter], rows);
+                                    // (not of slots behind the sequence, which nobody sees)
+                                    atomicOr(&it.bad[n_bad][quarter], __ballot_sync(0xffffffffu, found && slot0 + row < it.n));
                                     tc::fence_async_smem();
                                 }
                             }
