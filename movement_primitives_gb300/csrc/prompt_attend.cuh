@@ -19,9 +19,9 @@
 // What bounds it, by GB300 figures of the kernel alone: a long causal prompt (11585
 // tokens, 32 heads of 128, float16) runs at 1690 TFLOP/s, 87 % of the rate of a large library
 // product: tensor cores and exponentials (16 a cycle and SM) both take a step's 2048 cycles.  24
-// prompts of up to 2048, 32 on 8 heads: 1135 TFLOP/s; of an item's 26 thousand cycles 5 to 9 thousand are
+// prompts of up to 2048, 32 on 8 heads: 1213 TFLOP/s; of an item's 24 thousand cycles 5 to 8 thousand are
 // its first weights, its masked steps and its output.  At 80 elements a head the exponentials
-// are the bound (6 prompts behind 3001 keys, a window of 1024: 53 us).  A short prompt: 6.7 us,
+// are the bound (6 prompts behind 3001 keys, a window of 1024: 47 us).  A short prompt: 6.6 us,
 // the chain of launch, starts, copies, one step and output.
 // Waits are by votes and arrivals by predicates, so that warps stay together: a lane that
 // polls alone parts its warp, and every exchange after it cost 250 cycles (the long prompt: 896

@@ -40,7 +40,7 @@
 // the L2 and the joining (6 us).  12 sequences of up to 32767, 128 rows, E4M3 (443 MB): 218 us, bound by the
 // softmax warps (3400 of 3900 cycles a step): two multiplications by scales more than
 // in bfloat16, beside the conversions.  One of 301 slots: 10 us, the chain from the
-// lengths to the join.  By copies of the four warps alone the first took 84 us and the second 678.
+// lengths to the output.  By copies of the four warps alone the first took 84 us and the second 678.
 #pragma once
 
 #include <cuda.h>
