@@ -91,6 +91,15 @@ struct PromptShape {
     static constexpr int SOFT = 4 * TILES;                 // softmax warps
     static constexpr int THREADS = 32 * (SOFT + 4);        // products, loads, scheduling, a second tile's products
     static constexpr int O = 256;                          // first output column of tensor memory
+    // The softmax waits for a step's values by their phase's parity, so the phase before, of the tile that came SLOTS
+    // places earlier, has to be known to be over.  Logits seen mean that the tiles up to their keys have come, since
+    // the products take tiles in the ring's order.  LATE: how many tiles before the values lies the newest one that
+    // is not known to have come.  With two row tiles that is this step's keys (K V K V: two before).  With one
+    // (K K V K V) the values of the step before were waited for, and it is this step's keys, three before, or where
+    // this step's logits are waited for first the next step's, one before.
+    static constexpr bool LOGITS_FIRST = TILES == 1;
+    static constexpr int LATE = TILES == 2 ? 2 : LOGITS_FIRST ? 1 : 3;
+    static_assert(SLOTS >= (LATE + 1) * SPT, "a values' wait may pass by the phase before");
 };
 
 struct PromptShared {
@@ -373,9 +382,15 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
                 }
             };
             for (int j = 0; j < it.steps; ++j) {
-                const int key0 = (it.first + j) * kPrKeys;
-                // a barrier must not be two phases behind what is waited for: with two tiles what a slot held before was
-                // keys whose product this thread has seen, with one it may be the values before these, so all are waited for
+                const int key0 = (it.first + j) * kPrKeys, buf = TILES == 2 ? t : n_s & 1;
+                auto wait_logits = [&] {
+                    if (!wait_warp(sh.s_full[buf], TILES == 2 ? n_s : n_s >> 1)) return false;
+                    ++n_s;
+                    tc::fence_after();
+                    return true;
+                };
+                // (with one tile in every step, masked or not: the next step's wait counts on it)
+                if (S::LOGITS_FIRST && !wait_logits()) break;
                 if (TILES == 1) wait_values(j);
                 if (t == 0 && (key0 < item_lo || key0 + kPrKeys > item_hi)) {
                     // values that some row does not see are multiplied by weights of 0 there: what is not finite
@@ -425,11 +440,8 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
                     sh.bad_any[turn][warp & 3] |= rows ? 1u << n_bad : 0u;
                     n_bad = min(n_bad + 1, kPrMasked - 1);
                 }
-                const int buf = TILES == 2 ? t : n_s & 1;
+                if (!S::LOGITS_FIRST && !wait_logits()) break;
                 const uint32_t s_at = lanes + buf * 128;
-                if (!wait_warp(sh.s_full[buf], TILES == 2 ? n_s : n_s >> 1)) break;
-                ++n_s;
-                tc::fence_after();
                 // 32 logits come while the maximum of the 32 before is taken
                 uint32_t x[4][32];
                 float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
