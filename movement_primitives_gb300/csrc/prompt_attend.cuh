@@ -650,14 +650,13 @@ __global__ void __launch_bounds__(PromptShape<NC>::THREADS, 1) k_prompt_attend(c
             if constexpr (TILES == 1) load_tile(a.vm, steps - 1);
             if (!ok) break;
         }
-        if (!ok) {  // copies in flight end before the block does
-            for (uint32_t s = 0; s < S::SLOTS; ++s) {
-                const uint32_t used = round + (s < slot);
-                if (used) drained(sh.ring_full[s], used - 1);
-            }
-            for (int t = 0; t < TILES; ++t)
-                if (tiles_q[t]) drained(sh.q_full[t], tiles_q[t] - 1);
+        // copies in flight end before the block does, also where only another warp's wait has run out
+        for (uint32_t s = 0; s < S::SLOTS; ++s) {
+            const uint32_t used = round + (s < slot);
+            if (used) drained(sh.ring_full[s], used - 1);
         }
+        for (int t = 0; t < TILES; ++t)
+            if (tiles_q[t]) drained(sh.q_full[t], tiles_q[t] - 1);
     } else if (warp == S::SOFT || (TILES == 2 && warp == S::SOFT + 3)) {
         few_registers();
         // products, by the whole warp.  With two row tiles a warp a tile, so that one's waits and bookkeeping pass while
