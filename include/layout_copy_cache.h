@@ -192,8 +192,9 @@ typedef struct {
 int64_t lc_cache_attend_tree_workspace(const lc_paged_cache *cache, int32_t n_q_heads, int32_t n_drafts);
 
 /* Errors: as lc_cache_attend; LC_ERR_SHAPE also for n_drafts outside 0 ..
- * LC_CACHE_MAX_DRAFTS.  Waits inside the kernel are bounded (LC_WAIT_TIMEOUT_NS);
- * one that runs out sets LC_ERR_TIMEOUT in the error word. */
+ * LC_CACHE_MAX_DRAFTS.  Waits inside the kernel are bounded (LC_WAIT_TIMEOUT_NS, and up to 0.4
+ * ms more: polls sleep); one that runs out sets LC_ERR_TIMEOUT in the error word, and out and lse
+ * are then not to be used. */
 int lc_cache_attend_tree(const lc_paged_cache *cache, const lc_cache_tree *tree, lc_stream_t stream);
 
 /* Keeps the drafts of a path and lets the others go: the i-th draft of the path

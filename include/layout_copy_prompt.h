@@ -74,7 +74,8 @@ typedef struct {
  * LC_ERR_BAD_STRIDE (negative; 0 for a token or head among several), LC_ERR_ALIGN,
  * LC_ERR_OVERFLOW (2^30 tokens, keys or tiles, offsets past 2^60), LC_ERR_NOT_INJECTIVE (rows of out or lse
  * meet), LC_ERR_OVERLAP, LC_ERR_CUDA.  Waits inside the kernel are bounded
- * (LC_WAIT_TIMEOUT_NS); one that runs out sets LC_ERR_TIMEOUT in the error word. */
+ * (LC_WAIT_TIMEOUT_NS, and up to 0.4 ms more: polls sleep); one that runs out sets LC_ERR_TIMEOUT
+ * in the error word, and out and lse are then not to be used. */
 int lc_prompt_attend(const lc_prompt *prompt, lc_stream_t stream);
 
 #ifdef __cplusplus

@@ -31,7 +31,8 @@ __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.a
 // parts that go on one after the other and meet at every vote and shuffle, some 250
 // cycles each; so waits are by votes too.
 
-// Waits for the barrier phase n (counted from 0), all lanes alike; false after limit_ns.
+// Waits for the barrier phase n (counted from 0), all lanes alike; false after limit_ns and two polls, the one before the
+// timer is read first and the one that the limit falls in.
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t n, uint64_t limit_ns) {
     uint64_t t0 = 0;
 #pragma unroll 1
