@@ -123,6 +123,8 @@ extern "C" int lc_cache_attend_tree(const lc_paged_cache *cache, const lc_cache_
     // a scale of 0 is one too small to tell, so that unseen slots' -infinity stays what it is
     a.scale2 = std::max(std::fabs(q->scale) * 1.4426950408889634f, 0x1p-100f);
     a.negative = q->scale < 0.f;
+    // (nor is it with what a row of q was divided by: a product of 2^-126 or more is never 0)
+    a.q_least = std::max(-126, -126 - std::ilogb(a.scale2));
     const int eb = cache_elem_bytes(cache->type);
     const int64_t pool[3] = {cache->n_pages, cache->n_kv_heads, cache->page_size};
     a.vec = a.c.dim * eb % 16 == 0 && rows_aligned(cache->k, 3, pool, cache->k_stride, eb, 16) &&

@@ -73,6 +73,7 @@ struct TreeArgs {
     FastDiv group_div;
     float scale2;           // |scale| log2 e
     int32_t negative;
+    int32_t q_least;        // E4M3: log2 of what rows of q are divided by at least
     int32_t vec, q_vec, out_vec;  // rows of the pools, of q and of out are whole 16-byte words on 16-byte boundaries
     int32_t runs, least;    // blocks of the main kernel; steps of a run at least
     int32_t whole;          // not 0: units are not cut, nothing is joined
@@ -346,7 +347,7 @@ __device__ __noinline__ float tree_unusual(const uint8_t *v, int e) {
 }
 
 // The rows of q of a piece into shared memory, RQ a warp from row0 on: float16 copies of bfloat16 rows for E4M3 caches,
-// divided by a power of two so that a row's largest element is between 1 and 2 (`scale`: by which; 1 for a row of zeros).
+// divided by a power of two so that a row's largest element is between 1 and 2 (`scale`: by which; rows that are smaller than that, and zeros, by 2^q_least).
 template <int KV, int NC, int RQ>
 __device__ __forceinline__ void tree_query(const TreeArgs &a, const TreeItem &it, int row0, uint32_t q_s, float *scale) {
     constexpr bool Q8 = KV == LC_CACHE_E4M3;
@@ -389,7 +390,7 @@ __device__ __forceinline__ void tree_query(const TreeArgs &a, const TreeItem &it
 #pragma unroll
                 for (int e = 0; e < 4; ++e) most = max(most, max(w[e] << 16 & 0x7fffffffu, w[e] & 0x7fff0000u));
                 most = __reduce_max_sync(0xffffffffu, most);
-                const int ex = most ? min(max(static_cast<int>(most >> 23) - 127, -126), 126) : 0;
+                const int ex = min(max(static_cast<int>(most >> 23) - 127, a.q_least), 126);
                 const float div = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -1162,8 +1163,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
                 if (!wait_warp(sh.s_full[buf], n_s >> 1)) break;
                 const int x_at = n_s % kTrAux;
                 ++n_s;
-                // (never 0, whatever is multiplied: unseen slots' -infinity has to stay what it is)
-                if (Q8 && j == 0) scale2 = fminf(fmaxf(a.scale2 * sh.q_scale[i & 1][row], 0x1p-126f), 0x1p127f);
+                if (Q8 && j == 0) scale2 = a.scale2 * sh.q_scale[i & 1][row];
                 if (masked(it, slot0) && n_bad < kTrMasked) {
                     if constexpr (TMA && !Q8) {
                         // values that some row does not see are multiplied by weights of 0 there: what is not finite becomes 0,
