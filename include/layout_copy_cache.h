@@ -162,7 +162,7 @@ int lc_cache_attend(const lc_paged_cache *cache, const lc_cache_query *query, lc
  *   out        shares no address range with q
  *   window     0, or how many tokens are seen, a draft's own and its nearest ancestors
  *              first, then the newest before the drafts
- *   scale      of the dot products, finite
+ *   scale      of the dot products, finite, and so is its product with log2 e in float32
  *   lse        NULL, or receives log(sum_j exp(scale q . k_j))
  *   workspace  at least lc_cache_attend_tree_workspace(...) bytes, as lc_cache_attend's
  *

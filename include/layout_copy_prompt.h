@@ -37,7 +37,7 @@ extern "C" {
  *   causal     not 0: keys after a query are not seen
  *   window     0, or how many keys are seen of those up to a query's own place
  *              (later ones, where not causal, are all seen)
- *   scale      of the dot products, finite
+ *   scale      of the dot products, finite, and so is its product with log2 e in float32
  *   lse        NULL, or receives log(sum_j exp(scale q . k_j))
  *
  * A query with no key to see gives zeros and the lse -inf.  Rows of out and lse

@@ -91,7 +91,7 @@ constexpr int kJoinRows = kJoinLeast / 32;  // rows of a block of the least widt
 constexpr int kJoinFew = 32;       // parts of a row that one warp joins
 constexpr int kScorePer = 4;       // slots of a thread (4, 8, 16: 43.7, 45.4, 53 us
                                    // of 32 E4M3 sequences with scores)
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 // A run takes at least this many steps: shorter ones leave more parts to join
 // than the further warps save, longer ones leave warps idle.  Of 1, 2, 4, 6, 8

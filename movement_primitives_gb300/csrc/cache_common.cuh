@@ -17,6 +17,8 @@ namespace lc {
 // Kernel classes in the device error word.
 constexpr uint32_t kClassAppend = 0xf0, kClassAttend = 0xf1, kClassEvict = 0xf2;
 
+constexpr float kLog2e = 1.4426950408889634f;
+
 // Kernels are launched to overlap the end of what precedes them on the stream
 // (launch_after): the next one may be set up as soon as every block has come
 // here, and this one touches no memory until all before it has ended and is

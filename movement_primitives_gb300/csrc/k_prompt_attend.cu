@@ -53,7 +53,7 @@ extern "C" int lc_prompt_attend(const lc_prompt *p, lc_stream_t stream) {
     if (p->type != LC_CACHE_BF16 && p->type != LC_CACHE_F16) return LC_ERR_TYPE;
     if (p->n_seqs < 0 || p->n_kv_heads < 1 || p->n_q_heads < 1 || p->n_q_heads % p->n_kv_heads || p->head_dim < 8 ||
         p->head_dim > LC_CACHE_MAX_DIM || p->head_dim % 8 || p->n_tokens < 0 || p->n_keys < 0 || p->window < 0 ||
-        !std::isfinite(p->scale))
+        !std::isfinite(p->scale * kLog2e))
         return LC_ERR_SHAPE;
     if (p->n_tokens > 1 << 30 || p->n_keys > 1 << 30) return LC_ERR_OVERFLOW;
     if (p->n_seqs == 0 || p->n_tokens == 0) return LC_OK;
@@ -120,7 +120,7 @@ extern "C" int lc_prompt_attend(const lc_prompt *p, lc_stream_t stream) {
     if (heads > 0x3fffffff / pairs) return LC_ERR_OVERFLOW;
     a.pair_div = make_fastdiv(static_cast<uint32_t>(heads));
     // a scale of 0 is one too small to tell, so that unseen keys' -infinity stays what it is
-    a.scale2 = std::max(std::fabs(p->scale) * 1.4426950408889634f, 0x1p-100f);
+    a.scale2 = std::max(std::fabs(p->scale) * kLog2e, 0x1p-100f);
     a.negative = p->scale < 0.f;
     a.store = rows_aligned(p->out, 2, qext, p->out_stride, 2, 32) ? 32 : rows_aligned(p->out, 2, qext, p->out_stride, 2, 16) ? 16 : 2;
     a.limit_ns = wait_limit_ns();

@@ -68,7 +68,7 @@ extern "C" int lc_cache_attend_tree(const lc_paged_cache *cache, const lc_cache_
     if (st) return st;
     if (!q) return LC_ERR_NULL;
     if (q->n_q_heads < 1 || q->n_q_heads % cache->n_kv_heads || q->window < 0 || q->n_drafts < 0 ||
-        q->n_drafts > LC_CACHE_MAX_DRAFTS || !std::isfinite(q->scale))
+        q->n_drafts > LC_CACHE_MAX_DRAFTS || !std::isfinite(q->scale * kLog2e))
         return LC_ERR_SHAPE;
     if (q->type != (cache->type == LC_CACHE_E4M3 ? LC_CACHE_BF16 : cache->type)) return LC_ERR_TYPE;
     if (cache->n_seqs == 0 || q->n_drafts == 0) return LC_OK;
@@ -121,7 +121,7 @@ extern "C" int lc_cache_attend_tree(const lc_paged_cache *cache, const lc_cache_
     a.group_div = make_fastdiv(static_cast<uint32_t>(a.group));
     a.window = q->window;
     // a scale of 0 is one too small to tell, so that unseen slots' -infinity stays what it is
-    a.scale2 = std::max(std::fabs(q->scale) * 1.4426950408889634f, 0x1p-100f);
+    a.scale2 = std::max(std::fabs(q->scale) * kLog2e, 0x1p-100f);
     a.negative = q->scale < 0.f;
     // (nor is it with what a row of q was divided by: a product of 2^-126 or more is never 0)
     a.q_least = std::max(-126, -126 - std::ilogb(a.scale2));
