@@ -119,8 +119,8 @@ extern "C" int lc_prompt_attend(const lc_prompt *p, lc_stream_t stream) {
     const int64_t pairs = p->n_tokens / per + p->n_seqs;
     if (heads > 0x3fffffff / pairs) return LC_ERR_OVERFLOW;
     a.pair_div = make_fastdiv(static_cast<uint32_t>(heads));
-    // a scale of 0 is one too small to tell, so that unseen keys' -infinity stays what it is
-    a.scale2 = std::max(std::fabs(p->scale) * kLog2e, 0x1p-100f);
+    // a scale of 0 is the smallest number there is, under which all logits are too small to tell, so that unseen keys' -infinity stays what it is
+    a.scale2 = std::max(std::fabs(p->scale) * kLog2e, 0x1p-149f);
     a.negative = p->scale < 0.f;
     a.store = rows_aligned(p->out, 2, qext, p->out_stride, 2, 32) ? 32 : rows_aligned(p->out, 2, qext, p->out_stride, 2, 16) ? 16 : 2;
     a.limit_ns = wait_limit_ns();

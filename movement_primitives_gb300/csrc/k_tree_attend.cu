@@ -120,8 +120,8 @@ extern "C" int lc_cache_attend_tree(const lc_paged_cache *cache, const lc_cache_
     a.q_heads = q->n_q_heads;
     a.group_div = make_fastdiv(static_cast<uint32_t>(a.group));
     a.window = q->window;
-    // a scale of 0 is one too small to tell, so that unseen slots' -infinity stays what it is
-    a.scale2 = std::max(std::fabs(q->scale) * kLog2e, 0x1p-100f);
+    // a scale of 0 is the smallest number there is, under which all logits are too small to tell, so that unseen slots' -infinity stays what it is
+    a.scale2 = std::max(std::fabs(q->scale) * kLog2e, 0x1p-149f);
     a.negative = q->scale < 0.f;
     // (nor is it with what a row of q was divided by: a product of 2^-126 or more is never 0)
     a.q_least = std::max(-126, -126 - std::ilogb(a.scale2));
