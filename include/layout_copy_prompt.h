@@ -41,8 +41,8 @@ extern "C" {
  *   lse        NULL, or receives log(sum_j exp(scale q . k_j))
  *
  * A query with no key to see gives zeros and the lse -inf.  Rows of out and lse
- * that are no sequence's are left as they were.  out shares no element with q,
- * k or v.  Rows of q, k and v lie on 16-byte boundaries (head_dim and strides
+ * that are no sequence's are left as they were.  out shares no element with q (but for
+ * out = q itself, with its strides), k or v, nor lse with them or out, nor either with the starts.  Rows of q, k and v lie on 16-byte boundaries (head_dim and strides
  * multiples of 8), as the copies of whole tiles need.  There is no backward pass.
  *
  * Logits, maxima and sums are float32; the weights are rounded once to the

@@ -147,6 +147,29 @@ inline bool rows_meet(const void *p, const int64_t *st, const void *q, const int
     return false;
 }
 
+// Rows of a tensor as bytes: what lies between the first and the last byte of each.
+struct Span {
+    const void *p;
+    int64_t rows, pitch, wide;
+};
+// Of `rows` x n x m (runs of `run` elements of eb bytes); n and m 1 where there is no such mode.
+inline Span span_of(const void *p, int64_t rows, int64_t pitch, int64_t run, int64_t eb, int64_t n = 1, int64_t st_n = 0,
+                    int64_t m = 1, int64_t st_m = 0) {
+    return {p, p && n > 0 && m > 0 && run > 0 ? rows : 0, pitch * eb, ((n - 1) * st_n + (m - 1) * st_m + run) * eb};
+}
+
+// Whether two may share a byte: ranges that meet do, but for parts of one buffer whose rows are as far apart in
+// both and lie in other columns.
+inline bool may_meet(const Span &x, const Span &y) {
+    if (x.rows < 1 || y.rows < 1) return false;
+    const int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(x.p)) - static_cast<int64_t>(reinterpret_cast<uintptr_t>(y.p));
+    if (d >= (y.rows - 1) * y.pitch + y.wide || -d >= (x.rows - 1) * x.pitch + x.wide) return false;
+    const int64_t pitch = x.rows > 1 ? x.pitch : y.pitch;
+    if ((y.rows > 1 && y.pitch != pitch) || pitch < x.wide || pitch < y.wide) return true;
+    const int64_t at = ((d % pitch) + pitch) % pitch;  // x's columns from y's
+    return at < y.wide || at + x.wide > pitch;
+}
+
 // Checks a cache descriptor and lays it out for the kernels.  `write`: the
 // operator writes rows, which then have to be apart.
 inline int check_cache(const lc_paged_cache *c, bool write, CacheArgs *a) {

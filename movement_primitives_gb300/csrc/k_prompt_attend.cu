@@ -29,20 +29,6 @@ bool map_rows(CUtensorMap *m, bool f16, const void *p, int64_t tokens, int heads
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Whether rows of tokens x heads at p and at q (2-byte elements) may share any: ranges that meet do, but
-// for parts of one buffer whose tokens are as far apart in both and whose heads lie in other columns.
-bool may_meet(const void *p, const int64_t *st, int64_t heads, const void *q, const int64_t *qst, int64_t q_heads,
-              int64_t tokens, int64_t q_tokens, int64_t dim) {
-    const int64_t wide = (heads - 1) * st[1] + dim, q_wide = (q_heads - 1) * qst[1] + dim;
-    const int64_t d = (static_cast<int64_t>(reinterpret_cast<uintptr_t>(p)) -
-                       static_cast<int64_t>(reinterpret_cast<uintptr_t>(q))) / 2;
-    if (d >= (q_tokens - 1) * qst[0] + q_wide || -d >= (tokens - 1) * st[0] + wide) return false;
-    const int64_t pitch = st[0];
-    if (pitch != qst[0] || pitch < wide || pitch < q_wide) return true;
-    const int64_t at = ((d % pitch) + pitch) % pitch;  // p's columns from q's
-    return at < q_wide || at + wide > pitch;
-}
-
 }  // namespace
 
 }  // namespace lc
@@ -85,12 +71,15 @@ extern "C" int lc_prompt_attend(const lc_prompt *p, lc_stream_t stream) {
     // a row of the queries' own buffer is written when its item has read it
     const bool in_place = p->out == p->q && (qext[0] == 1 || p->q_stride[0] == p->out_stride[0]) &&
                           (qext[1] == 1 || p->q_stride[1] == p->out_stride[1]);
-    if (!in_place && may_meet(p->out, p->out_stride, qext[1], p->q, p->q_stride, qext[1], qext[0], qext[0], dim))
-        return LC_ERR_OVERLAP;
-    if (p->n_keys > 0 &&
-        (may_meet(p->out, p->out_stride, qext[1], p->k, p->k_stride, kext[1], qext[0], kext[0], dim) ||
-         may_meet(p->out, p->out_stride, qext[1], p->v, p->v_stride, kext[1], qext[0], kext[0], dim)))
-        return LC_ERR_OVERLAP;
+    const Span out = span_of(p->out, qext[0], p->out_stride[0], dim, 2, qext[1], p->out_stride[1]);
+    const Span lse = span_of(p->lse, qext[0], p->lse_stride, qext[1], 4);
+    const Span q = span_of(p->q, qext[0], p->q_stride[0], dim, 2, qext[1], p->q_stride[1]);
+    const Span read[] = {span_of(p->k, p->n_keys, p->k_stride[0], dim, 2, kext[1], p->k_stride[1]),
+                         span_of(p->v, p->n_keys, p->v_stride[0], dim, 2, kext[1], p->v_stride[1]),
+                         span_of(p->starts, 1, 0, p->n_seqs + int64_t(1), 4), span_of(p->k_starts, 1, 0, p->n_seqs + int64_t(1), 4)};
+    if ((!in_place && may_meet(out, q)) || may_meet(lse, q) || may_meet(lse, out)) return LC_ERR_OVERLAP;
+    for (const Span &x : read)
+        if (may_meet(out, x) || may_meet(lse, x)) return LC_ERR_OVERLAP;
     PromptArgs a{};
     a.starts = p->starts;
     a.k_starts = p->k_starts;

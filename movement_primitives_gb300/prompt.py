@@ -49,7 +49,7 @@ def prompt_attend(q, k, v, starts, k_starts=None, causal: bool = True, window: i
     after a query are not seen.  ``window``: of the keys up to a query's own
     place only the newest so many are seen (0: all).  ``scale``: of the dot products, 1 /
     sqrt(head_dim) by default.  ``out``: like ``q``, and either ``q`` itself or
-    apart from it, ``k`` and ``v``.  ``lse``: float32 [tokens, q_heads] to receive log sum exp.
+    apart from it, ``k`` and ``v``.  ``lse``: float32 [tokens, q_heads] to receive log sum exp, apart from the others.
     A query with nothing to see gives zeros (lse: -inf); rows that are no sequence's
     are left as they were (in an ``out`` that is made here: undefined).  head_dim is a
     multiple of 8 up to 256 and rows lie on 16-byte boundaries.  The call runs on the current device, which has to be the
