@@ -159,7 +159,9 @@ int lc_cache_attend(const lc_paged_cache *cache, const lc_cache_query *query, lc
  *              length) is clamped, with LC_ERR_CACHE_INDEX
  *   type       of q and out: the cache's own; LC_CACHE_BF16 for an E4M3 cache
  *   *_stride   of sequence, draft, head (lse: of sequence, draft, heads adjacent)
- *   out        shares no address range with q
+ *   out        shares no address range with q; neither out nor lse shares an element with the
+ *              other, q, lengths, counts or parents.  (That they lie apart from the
+ *              cache and the workspace is the caller's to see to.)
  *   window     0, or how many tokens are seen, a draft's own and its nearest ancestors
  *              first, then the newest before the drafts
  *   scale      of the dot products, finite, and so is its product with log2 e in float32

@@ -379,7 +379,7 @@ def cache_attend_tree(cache: PagedCache, q, lengths, parents, counts=None, out=N
     were (in an ``out`` that is made here: undefined).  ``out``: like ``q``, apart from it.  ``scale``: of the dot
     products, 1 / sqrt(head_dim) by default.  ``window``: how many tokens a draft sees,
     itself, its nearest ancestors and then the newest before the drafts (0: all).
-    ``lse``: float32 [seqs, drafts, q_heads] to receive log sum exp.
+    ``lse``: float32 [seqs, drafts, q_heads] to receive log sum exp, apart from the others.
     ``workspace``: at least ``cache.tree_workspace_bytes(q_heads, drafts)`` bytes; calls that may overlap need one each.
     """
     shape = q.shape

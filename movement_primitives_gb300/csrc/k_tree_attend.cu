@@ -93,6 +93,14 @@ extern "C" int lc_cache_attend_tree(const lc_paged_cache *cache, const lc_cache_
     }
     const uintptr_t q0 = reinterpret_cast<uintptr_t>(q->q), o0 = reinterpret_cast<uintptr_t>(q->out);
     if (q0 < o0 + 2 * (o_top + cache->head_dim) && o0 < q0 + 2 * (q_top + cache->head_dim)) return LC_ERR_OVERLAP;
+    const Span out = span_of(q->out, ext[0], q->out_stride[0], cache->head_dim, 2, ext[1], q->out_stride[1], ext[2], q->out_stride[2]);
+    const Span lse = span_of(q->lse, ext[0], q->lse_stride[0], ext[2], 4, ext[1], q->lse_stride[1]);
+    const Span read[] = {span_of(q->lengths, 1, 0, ext[0], 4), span_of(q->counts, 1, 0, ext[0], 4),
+                         span_of(q->parents, ext[0], q->parents_stride, ext[1], 4)};
+    if (may_meet(lse, out) || may_meet(lse, span_of(q->q, ext[0], q->q_stride[0], cache->head_dim, 2, ext[1], q->q_stride[1], ext[2], q->q_stride[2])))
+        return LC_ERR_OVERLAP;
+    for (const Span &x : read)
+        if (may_meet(out, x) || may_meet(lse, x)) return LC_ERR_OVERLAP;
     a.group = q->n_q_heads / cache->n_kv_heads;
     if (int64_t(q->n_drafts) * a.group > 1 << 24) return LC_ERR_OVERFLOW;
     a.most_blocks = most_blocks(q->n_drafts, a.group);

@@ -1,8 +1,8 @@
 """Parts of one buffer as arguments of the prompt and draft operators: apart, they run; where they meet, they are refused."""
 import pytest
 
-from test_gpu_cache import lc, no_device_error
-from test_gpu_tree import ints
+from test_gpu_cache import Setup, lc, no_device_error
+from test_gpu_tree import ints, queries, trees
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -43,4 +43,26 @@ def test_prompt_rows_of_one_buffer():
     refused(lambda: lc().prompt_attend(q, k, v, both[:3], lse=both[2:2 + n * 4].view(torch.float32).view(n, 4)))
     lc().prompt_attend(q, k, v, both[:3], lse=both[3:].view(torch.float32).view(n, 4))
     assert torch.equal(both[3:].view(torch.float32).view(n, 4), want_lse)
+    no_device_error()
+
+
+def test_tree_rows_of_one_buffer():
+    """[q out lse] a sequence: apart as columns.  Ranges of q and out meet all the same, which trees refuse; logs may lie among q's rows."""
+    s = Setup([40, 9], heads=2, dim=64, seed=2)
+    q, parents = queries(s, 3, 4), trees(2, 3, s.g)
+    want_lse = torch.empty((2, 3, 4), device="cuda")
+    want = lc().cache_attend_tree(s.cache, q, s.lengths, parents, lse=want_lse)
+    flat = torch.zeros((2, 3 * 256 + 32), dtype=torch.bfloat16, device="cuda")
+    mine, logs = flat[:, :768].unflatten(1, (3, 4, 64)), flat.view(torch.float32)
+    mine.copy_(q)
+    lse = logs[:, 384:396].unflatten(1, (3, 4))
+    assert torch.equal(lc().cache_attend_tree(s.cache, mine, s.lengths, parents, lse=lse), want) and torch.equal(lse, want_lse)
+    no_device_error()
+    for column in (0, 380, 383):
+        refused(lambda: lc().cache_attend_tree(s.cache, mine, s.lengths, parents, lse=logs[:, column:column + 12].unflatten(1, (3, 4))))
+    refused(lambda: lc().cache_attend_tree(s.cache, q, s.lengths, parents, out=want, lse=want.view(torch.float32).flatten()[8:32].view(2, 3, 4)))
+    lists = torch.zeros(64, dtype=torch.int32, device="cuda")
+    lists[:2] = s.lengths
+    refused(lambda: lc().cache_attend_tree(s.cache, q, lists[:2], parents, lse=lists[1:25].view(torch.float32).view(2, 3, 4)))
+    assert torch.equal(lc().cache_attend_tree(s.cache, q, lists[:2], parents, lse=lists[2:26].view(torch.float32).view(2, 3, 4)), want)
     no_device_error()

@@ -1,7 +1,7 @@
 """Outputs that meet what a call reads or writes beside them, in the prompt and draft operators (no GPU)."""
 import pytest
 
-from test_prompt_host import BASE, M, prompt  # noqa: F401  (M is a fixture)
+from test_prompt_host import BASE, M, prompt, tree  # noqa: F401  (M is a fixture)
 
 
 def test_prompt_refuses_logs_over_anything(M):  # noqa: F811
@@ -21,3 +21,15 @@ def test_prompt_parts_of_one_buffer(M):  # noqa: F811
                 k=BASE + 512, v=BASE + 768, out=BASE + 1024)
     for column in (1532, 1020, 756, 508, 4, 1568 - 4):
         assert prompt(M, lse=BASE + column, **rows) == "LC_ERR_OVERLAP", column
+
+
+def test_tree_refuses_outputs_over_anything(M):  # noqa: F811
+    size, logs = 2 * 3 * 512 * 2, 2 * 3 * 8 * 4
+    for base, n in ((BASE, size), (2 * BASE, size), (3 * BASE, 8), (4 * BASE, 8), (5 * BASE, 24)):
+        for at in (4 - logs, 0, n - 4):
+            assert tree(M, lse=base + at) == "LC_ERR_OVERLAP", (base // BASE, at)
+    for base, n in ((3 * BASE, 8), (4 * BASE, 8), (5 * BASE, 24)):
+        for at in (4 - size, 0, n - 4):
+            assert tree(M, out=base + at) == "LC_ERR_OVERLAP", (base // BASE, at)
+    # a tree for all sequences, its row read by each
+    assert tree(M, parents_stride=0, lse=5 * BASE + 8) == "LC_ERR_OVERLAP"
