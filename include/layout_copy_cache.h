@@ -208,7 +208,7 @@ int lc_cache_attend_tree(const lc_paged_cache *cache, const lc_cache_tree *tree,
  *              sequence ends the path too, and records LC_ERR_CACHE_INDEX
  *   counts     [n_seqs], the drafts a sequence has, or NULL: n_path each, as far as
  *              the length goes; clamped as in lc_cache_attend_tree
- *   new_lengths  [n_seqs], sharing no element with lengths, counts or path
+ *   new_lengths  [n_seqs], sharing no element with lengths, counts, path or the page table
  * The pages that hold the drafts must not be shared with another sequence.
  * Errors: as lc_cache_append. */
 int lc_cache_accept(const lc_paged_cache *cache, const int32_t *lengths, const int32_t *counts, const int32_t *path,

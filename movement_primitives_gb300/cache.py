@@ -433,7 +433,7 @@ def cache_accept(cache: PagedCache, lengths, counts, path, new_lengths=None, str
     The i-th of them moves from slot lengths[b] - counts[b] + path[b, i] to slot
     lengths[b] - counts[b] + i.  ``counts``: int32 [seqs], how many drafts a sequence
     has (None: as many as ``path`` has columns).  ``new_lengths``: an int32 [seqs] tensor to receive lengths -
-    counts + the accepted ones, apart from the inputs.  A path that does not rise, or
+    counts + the accepted ones, apart from the inputs and the page table.  A path that does not rise, or
     leaves the drafts, ends there and sets the device error word.  The pages that hold
     the drafts must not be shared with another sequence.
     """

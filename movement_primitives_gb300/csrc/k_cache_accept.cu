@@ -130,13 +130,15 @@ extern "C" int lc_cache_accept(const lc_paged_cache *cache, const int32_t *lengt
     const int64_t ext[1] = {cache->n_seqs};
     st = check_reach(1, ext, &path_stride, n_path);
     if (st) return st;
-    // blocks read lengths, counts and paths when others have written
+    // blocks read lengths, counts, paths and pages when others have written
     for (const int32_t *in : {lengths, counts})
         if (in && lists_meet(in, new_lengths, cache->n_seqs)) return LC_ERR_OVERLAP;
     if (n_path > 0) {
         const uintptr_t p0 = reinterpret_cast<uintptr_t>(path), l0 = reinterpret_cast<uintptr_t>(new_lengths);
         if (p0 < l0 + 4 * ext[0] && l0 < p0 + 4 * ((ext[0] - 1) * path_stride + n_path)) return LC_ERR_OVERLAP;
     }
+    if (may_meet(span_of(new_lengths, 1, 0, ext[0], 4), span_of(cache->page_table, ext[0], cache->table_stride, cache->pages_per_seq, 4)))
+        return LC_ERR_OVERLAP;
     a.lengths = lengths;
     a.counts = counts;
     a.path = path;

@@ -1,7 +1,7 @@
 """Outputs that meet what a call reads or writes beside them, in the prompt and draft operators (no GPU)."""
 import pytest
 
-from test_prompt_host import BASE, M, prompt, tree  # noqa: F401  (M is a fixture)
+from test_prompt_host import BASE, M, accept, cache, prompt, tree  # noqa: F401  (M is a fixture)
 
 
 def test_prompt_refuses_logs_over_anything(M):  # noqa: F811
@@ -33,3 +33,11 @@ def test_tree_refuses_outputs_over_anything(M):  # noqa: F811
             assert tree(M, out=base + at) == "LC_ERR_OVERLAP", (base // BASE, at)
     # a tree for all sequences, its row read by each
     assert tree(M, parents_stride=0, lse=5 * BASE + 8) == "LC_ERR_OVERLAP"
+
+
+def test_accept_refuses_lengths_over_the_page_table(M):  # noqa: F811
+    for at in (-4, 0, 8, 20):
+        assert accept(M, new=10 * BASE + at) == "LC_ERR_OVERLAP"
+    # in columns of the table's buffer that are not the table's
+    c = cache(M, table_stride=8, n_seqs=1)
+    assert accept(M, c, new=10 * BASE + 8) == "LC_ERR_OVERLAP"
