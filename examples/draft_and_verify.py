@@ -78,13 +78,16 @@ class Server:
         return ((out.flatten(-2) @ self.back) @ self.choose).argmax(-1)
 
     def prompt(self, tokens, counts):
-        """Takes in packed prompts, counts[b] tokens of sequence b."""
+        """Takes in packed prompts, counts[b] tokens of sequence b, which has none yet (a later piece of a prompt would
+        need the keys before it as packed rows, and here they are in pages)."""
+        if torch.any((counts > 0) & (self.lengths > 0)):
+            raise ValueError("prompts are whole: a sequence that has tokens gets no more of them here")
         r = self.reserve(counts, tokens.shape[0])
         q, k, v = self.heads(tokens, r.positions)
         lc.cache_append_packed(self.cache, k, v, r.slots)
         out = lc.prompt_attend(q, k, v, r.starts)
         self.lengths = r.lengths
-        self.next = self.chosen(out[r.starts[1:].long() - 1])
+        self.next = torch.where(counts > 0, self.chosen(out[(r.starts[1:].long() - 1).clamp(min=0)]), self.next)
         return out
 
     def step(self, parents, ranks, guesses):
