@@ -13,9 +13,9 @@
 // What bounds it is the chain of dependent reads (length, row, stack, page), not the
 // bytes: a step of 64 sequences is a block of 256 threads, whose barriers are
 // cheaper than 1024's; many tokens or a table written anew take a cluster, every thread with
-// kRsAtOnce reads on the way (a row of 1024 pages by one read after another a lane: 20.7 us
-// instead of 14.6 for 256 sequences with 65792 tokens; 64 sequences of a token: 6.0 us).  Clusters of 16
-// changed nothing (14.5 and 6.2 us).
+// kRsAtOnce reads on the way (256 sequences with 65792 tokens: 14.4 us, with four reads the same, with two 16.7, with
+// a row of 1024 pages by one read after another a lane 20.7; 64 sequences of a token: 5.8 us).  Clusters of 16
+// changed nothing.
 #include <cooperative_groups.h>
 
 #include "cache_common.cuh"

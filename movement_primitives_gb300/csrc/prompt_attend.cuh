@@ -17,15 +17,18 @@
 // and runs the next tile's first product during the softmax.
 //
 // What bounds it, by GB300 figures of the kernel alone: a long causal prompt (11585
-// tokens, 32 heads of 128, float16) runs at 1690 TFLOP/s, 87 % of the rate of a large library
-// product: tensor cores and exponentials (16 a cycle and SM) both take a step's 2048 cycles.  24
+// tokens, 32 heads of 128, float16) runs at 1690 TFLOP/s (652 us), 87 % of the rate of a large library
+// product: tensor cores and exponentials (16 a cycle and SM) both take a step's 2048 cycles; call after call the
+// power limit leaves 1550.  24
 // prompts of up to 2048, 32 on 8 heads: 1213 TFLOP/s; of an item's 24 thousand cycles 5 to 8 thousand are
-// its first weights, its masked steps and its output.  At 80 elements a head the exponentials
-// are the bound (6 prompts behind 3001 keys, a window of 1024: 47 us).  A short prompt: 6.6 us,
+// its first weights, its masked steps and its output.  Windows at 80 elements a head (6 prompts behind 3001
+// keys, 1024 seen: 48 to 55 us) no one unit bounds: the exponentials would take 23, the rest is items' starts and
+// outputs, three rounds of items where 2.2 would do, and steps in which one of two tiles sees nothing.  Past
+// 128 elements a head: 8192 tokens, 16 heads of 256, 549 us (1000 TFLOP/s).  A short prompt: 6.5 us,
 // the chain of launch, starts, copies, one step and output.
 // Waits are by votes and arrivals by predicates, so that warps stay together: a lane that
-// polls alone parts its warp, and every exchange after it cost 250 cycles (the long prompt: 896
-// us instead of 665).
+// polls alone parts its warp, and every exchange after it cost 250 cycles (the long prompt took 896
+// us, and 665 without).
 //
 // A weight is rounded to the values' 16-bit type for the second product: with
 // independent roundings that adds as much as the output's own rounding does
@@ -145,7 +148,9 @@ __device__ __forceinline__ float pr_max3(float a, float b, float c) {
 // counted from its last one down: the last one's level is the tiles of keys
 // that come before the sequence's end, the one before it has a level less.  With more of them
 // a block has many items, and they are taken in the sequences' order, the last tile of each first: to look
-// for the longest of 2000 sequences of 20 tokens took 16 ms, in order the call takes 0.36 ms (33 of 1000: 258 and 252 us).
+// for the longest of 2000 sequences of 20 tokens took 16 ms, in order the call takes 0.36 ms.  (33 of 1000 tokens each, where
+// the order does not matter: 258 and 252 us.  Ragged ones pay for it where the longest come last: 64 of up to 2048, 32 heads
+// of 128, take 440 us so, 404 to 411 in rising, falling or mixed order.)
 struct PromptSeq {
     int level, tiles;
     bool fell;  // it ends before it begins

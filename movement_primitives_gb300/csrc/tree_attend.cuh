@@ -35,9 +35,9 @@
 // them a row's (each half of the slots; they exchange their maxima).
 //
 // What bounds it, by GB300 figures of the kernels alone.  16 sequences of up to 4096
-// slots, 8 key heads of 128, 64 rows each, bfloat16 (143 MB): 43 us, 3.4 TB/s, where a steady step runs at
+// slots, 8 key heads of 128, 64 rows each, bfloat16 (143 MB): 44 us, 3.3 TB/s, where a steady step runs at
 // the memory's rate; the rest is the scheduler's reads, the first rows, the parts' way through
-// the L2 and the joining (6 us).  12 sequences of up to 32767, 128 rows, E4M3 (443 MB): 218 us, bound by the
+// the L2 and the joining (6 us).  12 sequences of up to 32767, 128 rows, E4M3 (443 MB): 217 us, bound by the
 // softmax warps (3400 of 3900 cycles a step): two multiplications by scales more than
 // in bfloat16, beside the conversions.  One of 301 slots: 10 us, the chain from the
 // lengths to the output.  By copies of the four warps alone the first took 84 us and the second 678.
@@ -1555,7 +1555,7 @@ int launch_tree_shape(const TreeArgs &a, cudaStream_t cs) {
     // is as long as a step (8 windows of 1024, 192 rows of 256: 23 us, 2 more with one).
     // Units stay whole, and nothing is joined by a second launch, where the table's columns are few steps: up to four
     // (2 units of 3 steps of 64 elements a head: 9.3 us, cut 9.8, and 3 us less on the host; 128 of 3 steps of 128: 12.0 and 17.7;
-    // of 4 in E4M3 2 units take 17.5 cut 15.3, 128 units 19.2 and 29.1), and up to eight where units take more than half of the
+    // of 4 in E4M3 2 units take 17.5 cut 15.3, which few units lose by this rule, 128 units 19.2 and 29.1), and up to eight where units take more than half of the
     // blocks (128 units: 17.7 and 24.9; 2 units of 8 steps 16.6 and 12.5).
     const int64_t most = (int64_t(a.c.cap) + S::KEYS - 1) / S::KEYS;
     b.whole = most <= (units <= sms && 2 * units > sms ? 8 : 4);
