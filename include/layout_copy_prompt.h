@@ -49,7 +49,8 @@ extern "C" {
  * values' 16-bit type for the second product (relative to a running maximum, so
  * that each is off by half a step of its own size; float16 weights below 2^-25 of
  * the largest by up to 2^-36 of it), and the output once more.  Exponentials and
- * logarithms are the hardware's approximate ones.  What unseen keys and values
+ * logarithms are the hardware's approximate ones, and lse is off by up to a millionth beside
+ * its logits' roundings.  What unseen keys and values
  * hold never reaches an output; a row that sees a value that is infinite or NaN
  * has no finite number in that column. */
 typedef struct {

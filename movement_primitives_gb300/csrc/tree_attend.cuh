@@ -61,6 +61,9 @@ constexpr int kTrSoft = 8;       // warps: two a 32 rows, each half of a step's 
 constexpr int kTrMostRuns = 160;
 constexpr float kNear = 8.f, kFar = 60.f;  // log2 of scales that are near one another, and of ones that are not too far from 1
 
+template <int KV>
+constexpr float kTrLift = KV == LC_CACHE_BF16 ? -24.f : 8.f;  // log2 of what weights are multiplied by
+
 struct TreeArgs {
     CacheArgs c;
     const uint16_t *q;
@@ -413,8 +416,9 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
     constexpr int KEYS = S::KEYS, EB = Q8 ? 1 : 2;
     constexpr int kIssuer = kTrSoft + kTrLoaders + 2;  // the warp that issues tensor copies
     // weights are up to 2^(kLift + kRise): float16 has few exponents, so small ones are lifted into them; others are
-    // lowered, as sums are, so that those of the type's largest values stay in float32
-    constexpr float kRise = M16 ? 6.f : 8.f, kLift = M16 ? 8.f : -40.f, kSumLift = Q8 ? 0.f : kLift;
+    // lowered, as sums are, so that those of the type's largest values stay in float32 (2^24 of them, 2^16 where the
+    // maximum is 2^kRise behind), and by no more: exponents below 32 lose 2^-20, below 64 2^-19
+    constexpr float kRise = M16 ? 6.f : 8.f, kLift = kTrLift<KV>, kSumLift = Q8 ? 0.f : kLift;
     extern __shared__ uint8_t raw_smem[];
     const uint32_t base = (ptx::smem_addr(raw_smem) + 1023) & ~1023u;
     const uint32_t q_s = base, ring_s = q_s + S::Q, raw_s = ring_s + S::SLOTS * S::TILE;
@@ -1462,7 +1466,7 @@ __global__ void __launch_bounds__(TreeShape<NC, KV == LC_CACHE_E4M3>::THREADS, 1
 template <int KV, int NC>
 __global__ void __launch_bounds__(256) k_tree_join(const __grid_constant__ TreeArgs a) {
     constexpr int KEYS = TreeShape<NC, KV == LC_CACHE_E4M3>::KEYS;
-    constexpr float kSumLift = KV == LC_CACHE_F16 ? 8.f : KV == LC_CACHE_E4M3 ? 0.f : -40.f;
+    constexpr float kSumLift = KV == LC_CACHE_E4M3 ? 0.f : kTrLift<KV>;
     __shared__ float2 ml[8][32];
     __shared__ uint32_t cuts_of[8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
